@@ -7,8 +7,11 @@ is missing, or the GPU is not an sm_103 part, every call raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
+import struct
+import threading
 from typing import Optional
 
 import torch
@@ -18,11 +21,11 @@ from .build import LIB as _LIB_PATH
 GDN_OK = 0
 STATUS_NAMES = {0: "GDN_OK", 1: "GDN_ERR_INVALID_ARGUMENT", 2: "GDN_ERR_UNSUPPORTED",
                 3: "GDN_ERR_ALIAS", 4: "GDN_ERR_CUDA", 5: "GDN_ERR_DEVICE_INPUT"}
-DEVERR_CU_SEQLENS, DEVERR_STATE_INDEX, DEVERR_TIMEOUT = 0x1, 0x2, 0x4
+DEVERR_CU_SEQLENS, DEVERR_STATE_INDEX, DEVERR_TIMEOUT, DEVERR_POSITION = 0x1, 0x2, 0x4, 0x8
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2, torch.int32: 3, torch.int64: 4}
 # symbols include/gdn.h declares; the tests check the library exports all of them
 EXPORTED = ["gdn_init", "gdn_chunk_prefill", "gdn_chunk_prefill_checkpointed", "gdn_chunk_prefill_noalloc",
-            "gdn_decode_step", "gdn_reserve_workspace", "gdn_split_workspace_bytes",
+            "gdn_decode_step", "gdn_qk_norm_rope", "gdn_decay_prefill", "gdn_decay_step", "gdn_reserve_workspace", "gdn_split_workspace_bytes",
             "gdn_get_device_status", "gdn_last_error", "gdn_shutdown", "gdn_testing_force_splits",
             "gdn_testing_wait_limit", "gdn_testing_split_plan"]
 
@@ -72,6 +75,14 @@ def load_library():
         lib.gdn_split_workspace_bytes.restype = ctypes.c_size_t
         lib.gdn_decode_step.argtypes = [P, P, P, P, P, ctypes.c_float, P, P, ctypes.c_int, P, ctypes.c_void_p]
         lib.gdn_decode_step.restype = ctypes.c_int
+        # descriptors by address (see _Descriptors)
+        A, F, I = ctypes.c_void_p, ctypes.c_float, ctypes.c_int
+        lib.gdn_qk_norm_rope.argtypes = [A, A, A, A, F, F, A, A, I, A, A, A]
+        lib.gdn_qk_norm_rope.restype = ctypes.c_int
+        lib.gdn_decay_prefill.argtypes = [A, A, A, A, F, A, A, A, A, I, A, A]
+        lib.gdn_decay_prefill.restype = ctypes.c_int
+        lib.gdn_decay_step.argtypes = [A, A, A, A, F, A, A, A, A]
+        lib.gdn_decay_step.restype = ctypes.c_int
         lib.gdn_get_device_status.argtypes = [ctypes.c_void_p, ctypes.POINTER(ctypes.c_int32)]
         lib.gdn_get_device_status.restype = ctypes.c_int
         lib.gdn_last_error.argtypes = []
@@ -105,6 +116,38 @@ def describe(t: Optional[torch.Tensor]):
         d.shape[i] = t.shape[i]
         d.stride[i] = t.stride(i)
     return d
+
+
+class _Descriptors(threading.local):
+    """Room for one call's gdn_tensor_t descriptors, kept for each thread: ``fill`` writes
+    them and returns their addresses (None for an absent tensor).  The operators whose
+    smallest calls take a few microseconds on the GPU go this way; it costs about 1 us a
+    tensor where ``describe`` costs 5."""
+
+    SIZE = ctypes.sizeof(GdnTensor)
+    ROWS = [struct.Struct("@qii%dq" % n + "%dx" % (8 * (4 - n)) + "%dq" % n + "%dx" % (8 * (4 - n))) for n in range(5)]
+
+    def __init__(self):
+        self.room = ctypes.create_string_buffer(12 * self.SIZE)
+        self.base = ctypes.addressof(self.room)
+
+    def fill(self, *tensors):
+        where = []
+        for i, t in enumerate(tensors):
+            if t is None:
+                where.append(None)
+                continue
+            dtype, n = _DTYPES.get(t.dtype), t.dim()
+            if dtype is None:
+                raise TypeError(f"unsupported dtype {t.dtype}")
+            if n > 4:
+                raise ValueError("at most 4 dims")
+            self.ROWS[n].pack_into(self.room, i * self.SIZE, t.data_ptr(), dtype, n, *t.shape, *t.stride())
+            where.append(self.base + i * self.SIZE)
+        return where
+
+
+_descriptors = _Descriptors()
 
 
 def _ref(d):
@@ -194,6 +237,31 @@ def gdn_decode_step(q, k, v, g, beta, scale: float, state, state_indices, use_qk
     _check(st)
 
 
+def gdn_qk_norm_rope(q, k, q_weight, k_weight, weight_offset: float, eps: float, cos_sin, positions,
+                     interleaved: bool, q_out, k_out, stream=None) -> None:
+    """Norm and rotation of query and key heads; same names and order as the C entry point."""
+    d = _descriptors.fill(q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out)
+    _check(load_library().gdn_qk_norm_rope(d[0], d[1], d[2], d[3], float(weight_offset), float(eps), d[4], d[5],
+                                           int(bool(interleaved)), d[6], d[7], _stream_handle(stream)))
+
+
+def gdn_decay_prefill(q, k, v, g, scale: float, initial_state, state_indices, output_state, cu_seqlens,
+                      batch_invariant: bool, output, stream=None) -> None:
+    """Linear attention with a decay over packed sequences; same names and order as the C
+    entry point."""
+    d = _descriptors.fill(q, k, v, g, initial_state, state_indices, output_state, cu_seqlens, output)
+    _check(load_library().gdn_decay_prefill(d[0], d[1], d[2], d[3], float(scale), d[4], d[5], d[6], d[7],
+                                            int(bool(batch_invariant)), d[8], _stream_handle(stream)))
+
+
+def gdn_decay_step(q, k, v, g, scale: float, state, state_indices, output, stream=None) -> None:
+    """One token per batch row through the same recurrence, ``state`` in place; same names
+    and order as the C entry point."""
+    d = _descriptors.fill(q, k, v, g, state, state_indices, output)
+    _check(load_library().gdn_decay_step(d[0], d[1], d[2], d[3], float(scale), d[4], d[5], d[6],
+                                         _stream_handle(stream)))
+
+
 def gdn_reserve_workspace(nbytes: int, stream=None) -> None:
     """Grow the split-K workspace now (e.g. before capturing a CUDA graph)."""
     _check(load_library().gdn_reserve_workspace(ctypes.c_size_t(int(nbytes)),
@@ -279,6 +347,84 @@ def chunk_gated_delta_rule(q, k, v, g=None, beta=None, scale: Optional[float] = 
                       state_indices, final_state, cu_seqlens, use_qk_l2norm_in_kernel,
                       batch_invariant, output, stream)
     return (output, final_state) if output_final_state else output
+
+
+def _allocating_on(stream):
+    """The context in which a call's results are allocated: the stream they are written on."""
+    if isinstance(stream, torch.cuda.Stream):
+        return torch.cuda.stream(stream)
+    if stream is None or not torch.cuda.is_available():
+        return contextlib.nullcontext()
+    return torch.cuda.stream(torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream())
+
+
+def _empty(shape, like, stream):
+    if stream is None:
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+    with _allocating_on(stream):
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+
+
+def _gate_rows(g, rows: int):
+    """A gate as the library takes it: [rows, H]; [H] is one decay for each head."""
+    return g if g is None or g.dim() != 1 else g.expand(rows, g.shape[0])
+
+
+def qk_norm_rope(q, k=None, cos_sin=None, positions=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+                 weight_offset: float = 0.0, interleaved: bool = False, q_out=None, k_out=None, stream=None):
+    """RMS norm of every query and key head, then the rotation of its first values by the
+    token's position, in one pass (``include/gdn.h``, gdn_qk_norm_rope).
+
+    ``cos_sin`` is ``[places, R]`` f32 (cosines, then sines); without it the heads are only
+    normalised.  Returns ``(q_out, k_out)``, ``k_out`` None without ``k``; pass ``q_out=q,
+    k_out=k`` to work in place.  A result that the call allocates belongs to ``stream``.
+    """
+    if q_out is None:
+        q_out = _empty(q.shape, q, stream)
+    if k is not None and k_out is None:
+        k_out = _empty(k.shape, k, stream)
+    gdn_qk_norm_rope(q, k, q_weight, k_weight, weight_offset, eps, cos_sin, positions, interleaved, q_out, k_out, stream)
+    return q_out, k_out
+
+
+def decay_linear_attention(q, k, v, g=None, scale: Optional[float] = None, initial_state=None,
+                           output_final_state: bool = False, cu_seqlens=None, output=None, output_state=None,
+                           batch_invariant: bool = False, state_indices=None, stream=None):
+    """Linear attention with a decay over packed prompts: ``S_t = g_t S_{t-1} + v_t k_t^T``,
+    ``o_t = scale S_t q_t`` (``include/gdn.h``, gdn_decay_prefill).  Arguments, defaults and
+    results are those of :func:`chunk_gated_delta_rule`; ``g`` is ``[T, H]``, or ``[H]`` for
+    one decay for each head.
+    """
+    if cu_seqlens is None:
+        raise ValueError("cu_seqlens is required")
+    rows, H = q.shape[0], max(q.shape[1], v.shape[1])
+    if output is None:
+        output = _empty((rows, H, q.shape[2]), q, stream)
+    final_state = None
+    if output_final_state:
+        if output_state is None:
+            pooled = state_indices is not None and initial_state is not None
+            slots = initial_state.shape[0] if pooled else cu_seqlens.shape[0] - 1
+            dt = initial_state.dtype if initial_state is not None else torch.float32
+            with _allocating_on(stream):
+                output_state = torch.empty(slots, H, v.shape[2], q.shape[2], dtype=dt, device=q.device)
+        final_state = output_state
+    gdn_decay_prefill(q, k, v, _gate_rows(g, rows), 0.0 if scale is None else float(scale), initial_state,
+                      state_indices, final_state, cu_seqlens, batch_invariant, output, stream)
+    return (output, final_state) if output_final_state else output
+
+
+def decay_linear_step(q, k, v, state, g=None, scale: Optional[float] = None, state_indices=None, output=None,
+                      stream=None):
+    """One token for each batch row through the recurrence of :func:`decay_linear_attention`,
+    ``state`` read and written in place (``include/gdn.h``, gdn_decay_step).  Returns the
+    output ``[B, H, 128]``."""
+    rows = q.shape[0]
+    if output is None:
+        output = _empty((rows, max(q.shape[1], v.shape[1]), q.shape[2]), q, stream)
+    gdn_decay_step(q, k, v, _gate_rows(g, rows), 0.0 if scale is None else float(scale), state, state_indices, output,
+                   stream)
+    return output
 
 
 def run_problem(p, device="cuda", output_state=None, output=None, stream=None):

@@ -16,6 +16,7 @@
 #include <cstring>
 #include <mutex>
 
+#include "decay.h"
 #include "decode.h"
 #include "prefill.h"
 
@@ -596,6 +597,87 @@ gdn_status_t chunk_prefill(const gdn_tensor_t* q, const gdn_tensor_t* k, const g
   return GDN_OK;
 }
 
+// ---- decay linear attention and the q/k norm with rotation
+
+// What the prefill and the step ask of q, k, v, g and the output in common; `rows` names
+// the leading dimension in messages.
+struct DecayShape {
+  int64_t rows, Hqk, Hv, H;
+};
+gdn_status_t check_decay(const gdn_tensor_t* q, const gdn_tensor_t* k, const gdn_tensor_t* v, const gdn_tensor_t* g,
+                         const gdn_tensor_t* output, float scale, DecayShape* s) {
+  gdn_status_t st;
+  if ((st = check_qkv(q, "q")) != GDN_OK) return st;
+  if ((st = check_qkv(k, "k")) != GDN_OK) return st;
+  if ((st = check_qkv(v, "v")) != GDN_OK) return st;
+  if (k->dtype != q->dtype || v->dtype != q->dtype) return fail(GDN_ERR_UNSUPPORTED, "q, k and v must share a dtype");
+  if (k->shape[0] != q->shape[0] || k->shape[1] != q->shape[1])
+    return fail(GDN_ERR_UNSUPPORTED, "q and k must have the same shape (H_q == H_k)");
+  if (v->shape[0] != q->shape[0]) return fail(GDN_ERR_INVALID_ARGUMENT, "v has a different row count than q");
+  const int64_t rows = q->shape[0], Hqk = q->shape[1], Hv = v->shape[1], H = Hqk > Hv ? Hqk : Hv;
+  if (H % Hqk || H % Hv)
+    return fail(GDN_ERR_UNSUPPORTED, "%lld heads must be a multiple of H_qk %lld and H_v %lld", (long long)H,
+                (long long)Hqk, (long long)Hv);
+  if (H > (1 << 20)) return fail(GDN_ERR_UNSUPPORTED, "too many heads");
+  if ((st = check_gate(g, "g", rows, H, true)) != GDN_OK) return st;
+  if ((st = check_qkv(output, "output")) != GDN_OK) return st;
+  if (output->dtype != q->dtype) return fail(GDN_ERR_UNSUPPORTED, "output must have q's dtype");
+  if (output->shape[0] != rows || output->shape[1] != H)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "output must be [%lld, H=%lld, 128]", (long long)rows, (long long)H);
+  if (!std::isfinite(scale)) return fail(GDN_ERR_INVALID_ARGUMENT, "scale must be finite");
+  *s = DecayShape{rows, Hqk, Hv, H};
+  return GDN_OK;
+}
+
+// Whether two [rows, heads, 128] views of 16-bit elements share no element: their byte
+// ranges are apart, or they are slices of the same rows that lie side by side.
+bool rows_apart(const gdn_tensor_t* a, const gdn_tensor_t* b) {
+  if (!overlaps(a, b)) return true;
+  const int64_t S = a->stride[0] * 2;
+  if (b->stride[0] * 2 != S || S <= 0) return false;
+  const int64_t ea = ((a->shape[1] - 1) * a->stride[1] + a->shape[2]) * 2;
+  const int64_t eb = ((b->shape[1] - 1) * b->stride[1] + b->shape[2]) * 2;
+  int64_t d = (int64_t)(reinterpret_cast<uintptr_t>(b->data) - reinterpret_cast<uintptr_t>(a->data)) % S;
+  if (d < 0) d += S;
+  return d >= ea && d + eb <= S;
+}
+bool same_view(const gdn_tensor_t* a, const gdn_tensor_t* b) {
+  if (a->data != b->data) return false;
+  for (int i = 0; i < 2; ++i)
+    if (a->shape[i] > 1 && a->stride[i] != b->stride[i]) return false;
+  return true;
+}
+
+// One of the two head tensors of gdn_qk_norm_rope with its weight and its output.
+gdn_status_t rope_tensor(const gdn_tensor_t* x, const gdn_tensor_t* w, const gdn_tensor_t* y, const char* name,
+                         gdn::RopeTensor* t) {
+  gdn_status_t st;
+  char out_name[16], w_name[16];
+  snprintf(out_name, sizeof(out_name), "%s_out", name);
+  snprintf(w_name, sizeof(w_name), "%s_weight", name);
+  if ((st = check_qkv(x, name)) != GDN_OK) return st;
+  if ((st = check_qkv(y, out_name)) != GDN_OK) return st;
+  if (y->dtype != x->dtype) return fail(GDN_ERR_UNSUPPORTED, "%s must have %s's dtype", out_name, name);
+  if (y->shape[0] != x->shape[0] || y->shape[1] != x->shape[1])
+    return fail(GDN_ERR_INVALID_ARGUMENT, "%s must have %s's shape", out_name, name);
+  if (x->shape[1] > (1 << 20)) return fail(GDN_ERR_UNSUPPORTED, "too many heads");
+  if (y->shape[1] > 1 && y->stride[1] < 128) return fail(GDN_ERR_INVALID_ARGUMENT, "%s heads overlap", out_name);
+  if (w) {
+    if ((st = check_basic(w, w_name, 1)) != GDN_OK) return st;
+    if (w->dtype != GDN_F32 && w->dtype != GDN_BF16 && w->dtype != GDN_F16)
+      return fail(GDN_ERR_UNSUPPORTED, "%s dtype %s is not supported", w_name, dt_name(w->dtype));
+    if (w->shape[0] != 128 || w->stride[0] != 1) return fail(GDN_ERR_INVALID_ARGUMENT, "%s must be 128 contiguous values", w_name);
+    if (reinterpret_cast<uintptr_t>(w->data) % 16) return fail(GDN_ERR_INVALID_ARGUMENT, "%s must be 16-byte aligned", w_name);
+    if (overlaps(y, w)) return fail(GDN_ERR_ALIAS, "%s overlaps %s", out_name, w_name);
+  }
+  if (!same_view(x, y) && !rows_apart(x, y)) return fail(GDN_ERR_ALIAS, "%s overlaps %s without being the same view", out_name, name);
+  t->x = x->data; t->x_st = x->stride[0]; t->x_sh = x->stride[1];
+  t->y = y->data; t->y_st = y->stride[0]; t->y_sh = y->stride[1];
+  t->heads = (int32_t)x->shape[1];
+  if (w) { t->w = w->data; t->w_dtype = w->dtype; }
+  return GDN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -703,6 +785,162 @@ gdn_status_t gdn_decode_step(const gdn_tensor_t* q, const gdn_tensor_t* k, const
   p.in_f16 = q->dtype == GDN_F16 ? 1 : 0;
   cudaError_t e = gdn::launch_decode(p, stream);
   if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "decode launch: %s", cudaGetErrorString(e));
+  return GDN_OK;
+}
+
+gdn_status_t gdn_qk_norm_rope(const gdn_tensor_t* q, const gdn_tensor_t* k, const gdn_tensor_t* q_weight,
+                              const gdn_tensor_t* k_weight, float weight_offset, float eps,
+                              const gdn_tensor_t* cos_sin, const gdn_tensor_t* positions, int interleaved,
+                              const gdn_tensor_t* q_out, const gdn_tensor_t* k_out, cudaStream_t stream) {
+  g_last_error[0] = 0;
+  gdn_status_t st;
+  gdn::RopeParams p;
+  memset(&p, 0, sizeof(p));
+  if ((st = rope_tensor(q, q_weight, q_out, "q", &p.t[0])) != GDN_OK) return st;
+  const int64_t T = q->shape[0];
+  if (k || k_out || k_weight) {
+    if ((st = rope_tensor(k, k_weight, k_out, "k", &p.t[1])) != GDN_OK) return st;
+    if (k->dtype != q->dtype) return fail(GDN_ERR_UNSUPPORTED, "q and k must share a dtype");
+    if (k->shape[0] != T) return fail(GDN_ERR_INVALID_ARGUMENT, "k has a different token count than q");
+    if (!rows_apart(q_out, k) || !rows_apart(k_out, q)) return fail(GDN_ERR_ALIAS, "an output overlaps the other input");
+    if (!rows_apart(q_out, k_out)) return fail(GDN_ERR_ALIAS, "q_out overlaps k_out");
+    if (overlaps(q_out, k_weight) || overlaps(k_out, q_weight)) return fail(GDN_ERR_ALIAS, "an output overlaps a weight");
+  }
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(GDN_ERR_INVALID_ARGUMENT, "eps must be finite and not negative");
+  if (!std::isfinite(weight_offset)) return fail(GDN_ERR_INVALID_ARGUMENT, "weight_offset must be finite");
+  if (cos_sin) {
+    if ((st = check_basic(cos_sin, "cos_sin", 2)) != GDN_OK) return st;
+    if (cos_sin->dtype != GDN_F32) return fail(GDN_ERR_UNSUPPORTED, "cos_sin must be f32, got %s", dt_name(cos_sin->dtype));
+    const int64_t R = cos_sin->shape[1];
+    if (R < 16 || R > 128 || R % 16)
+      return fail(GDN_ERR_UNSUPPORTED, "the rotary size (cos_sin's second dim) must be a multiple of 16 up to 128, got %lld", (long long)R);
+    if (cos_sin->stride[1] != 1 || (cos_sin->shape[0] > 1 && cos_sin->stride[0] % 4) ||
+        reinterpret_cast<uintptr_t>(cos_sin->data) % 16)
+      return fail(GDN_ERR_INVALID_ARGUMENT, "cos_sin rows must be contiguous and 16-byte aligned");
+    if (positions) {
+      if ((st = check_index_vec(positions, "positions", T)) != GDN_OK) return st;
+      p.positions = positions->data;
+      p.pos_dtype = positions->dtype;
+    } else if (cos_sin->shape[0] < T) {
+      return fail(GDN_ERR_INVALID_ARGUMENT, "cos_sin has %lld places for %lld tokens", (long long)cos_sin->shape[0], (long long)T);
+    }
+    for (const gdn_tensor_t* y : {q_out, k_out})
+      if (overlaps(y, cos_sin) || overlaps(y, positions)) return fail(GDN_ERR_ALIAS, "an output overlaps cos_sin or positions");
+    p.cos_sin = static_cast<const float*>(cos_sin->data);
+    p.cs_stride = cos_sin->stride[0];
+    p.places = cos_sin->shape[0];
+    p.rotary = (int32_t)R;
+    p.interleaved = interleaved ? 1 : 0;
+  } else if (positions) {
+    return fail(GDN_ERR_INVALID_ARGUMENT, "positions without cos_sin");
+  }
+  if (T * (p.t[0].heads + p.t[1].heads) >= (int64_t(1) << 34)) return fail(GDN_ERR_UNSUPPORTED, "too many (token, head) rows");
+  int dev = 0;
+  if ((st = current_device(&dev)) != GDN_OK) return st;
+  p.dev_err = g_dev[dev].dev_err;
+  p.T = T;
+  p.in_f16 = q->dtype == GDN_F16 ? 1 : 0;
+  p.eps = eps;
+  p.weight_offset = weight_offset;
+  cudaError_t e = gdn::launch_norm_rope(p, stream);
+  if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "norm and rotation launch: %s", cudaGetErrorString(e));
+  return GDN_OK;
+}
+
+gdn_status_t gdn_decay_prefill(const gdn_tensor_t* q, const gdn_tensor_t* k, const gdn_tensor_t* v,
+                               const gdn_tensor_t* g, float scale, const gdn_tensor_t* initial_state,
+                               const gdn_tensor_t* state_indices, const gdn_tensor_t* output_state,
+                               const gdn_tensor_t* cu_seqlens, int batch_invariant, const gdn_tensor_t* output,
+                               cudaStream_t stream) {
+  g_last_error[0] = 0;
+  gdn_status_t st;
+  DecayShape s;
+  if ((st = check_decay(q, k, v, g, output, scale, &s)) != GDN_OK) return st;
+  if ((st = check_state(initial_state, "initial_state", s.H)) != GDN_OK) return st;
+  if ((st = check_state(output_state, "output_state", s.H)) != GDN_OK) return st;
+  if ((st = check_index_vec(cu_seqlens, "cu_seqlens", -1)) != GDN_OK) return st;
+  const int64_t N = cu_seqlens->shape[0] - 1;
+  if (N < 0) return fail(GDN_ERR_INVALID_ARGUMENT, "cu_seqlens needs at least one entry");
+  if (N * s.H >= (int64_t(1) << 31)) return fail(GDN_ERR_UNSUPPORTED, "too many (sequence, head) units");
+  if (state_indices && (st = check_index_vec(state_indices, "state_indices", N)) != GDN_OK) return st;
+  for (const gdn_tensor_t* x : {initial_state, output_state})
+    if (x && !state_indices && x->shape[0] < N)
+      return fail(GDN_ERR_INVALID_ARGUMENT, "%s has %lld slots for %lld sequences",
+                  x == initial_state ? "initial_state" : "output_state", (long long)x->shape[0], (long long)N);
+  if (overlaps(output_state, initial_state)) return fail(GDN_ERR_ALIAS, "output_state must not overlap initial_state");
+  for (const gdn_tensor_t* in : {q, k, v, g, initial_state, cu_seqlens, state_indices}) {
+    if (overlaps(output, in)) return fail(GDN_ERR_ALIAS, "output overlaps an input");
+    if (overlaps(output_state, in)) return fail(GDN_ERR_ALIAS, "output_state overlaps an input");
+  }
+  if (overlaps(output, output_state)) return fail(GDN_ERR_ALIAS, "output overlaps output_state");
+  int dev = 0;
+  if ((st = current_device(&dev)) != GDN_OK) return st;
+  if (N == 0) return GDN_OK;
+  gdn::DecayPrefillParams p;
+  memset(&p, 0, sizeof(p));
+  p.q = q->data; p.q_st = q->stride[0]; p.q_sh = q->stride[1];
+  p.k = k->data; p.k_st = k->stride[0]; p.k_sh = k->stride[1];
+  p.v = v->data; p.v_st = v->stride[0]; p.v_sh = v->stride[1];
+  if (g) { p.g = g->data; p.g_st = g->stride[0]; p.g_sh = g->stride[1]; p.g_dtype = g->dtype; }
+  if (initial_state) {
+    p.s_in = initial_state->data; p.sin_slot = initial_state->stride[0]; p.sin_head = initial_state->stride[1];
+    p.sin_slots = initial_state->shape[0]; p.sin_dtype = initial_state->dtype;
+  }
+  if (output_state) {
+    p.s_out = output_state->data; p.sout_slot = output_state->stride[0]; p.sout_head = output_state->stride[1];
+    p.sout_slots = output_state->shape[0]; p.sout_dtype = output_state->dtype;
+  }
+  if (state_indices) { p.state_idx = state_indices->data; p.idx_dtype = state_indices->dtype; }
+  p.cu = cu_seqlens->data;
+  p.cu_dtype = cu_seqlens->dtype;
+  p.out = output->data; p.o_st = output->stride[0]; p.o_sh = output->stride[1];
+  p.dev_err = g_dev[dev].dev_err;
+  p.T = s.rows;
+  p.N = (int32_t)N; p.H = (int32_t)s.H; p.H_qk = (int32_t)s.Hqk; p.H_v = (int32_t)s.Hv;
+  p.scale = (scale == 0.0f) ? 1.0f / std::sqrt(128.0f) : scale;
+  p.op_f16 = q->dtype == GDN_F16 ? 1 : 0;
+  cudaError_t e = gdn::launch_decay_prefill(p, stream);
+  if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "decay prefill launch: %s", cudaGetErrorString(e));
+  return GDN_OK;
+}
+
+gdn_status_t gdn_decay_step(const gdn_tensor_t* q, const gdn_tensor_t* k, const gdn_tensor_t* v,
+                            const gdn_tensor_t* g, float scale, const gdn_tensor_t* state,
+                            const gdn_tensor_t* state_indices, const gdn_tensor_t* output, cudaStream_t stream) {
+  g_last_error[0] = 0;
+  gdn_status_t st;
+  DecayShape s;
+  if ((st = check_decay(q, k, v, g, output, scale, &s)) != GDN_OK) return st;
+  const int64_t B = s.rows;
+  if (B * s.H >= (int64_t(1) << 28)) return fail(GDN_ERR_UNSUPPORTED, "too many (row, head) states");
+  if (!state) return fail(GDN_ERR_INVALID_ARGUMENT, "state is required");
+  if ((st = check_state(state, "state", s.H)) != GDN_OK) return st;
+  if (state_indices && (st = check_index_vec(state_indices, "state_indices", B)) != GDN_OK) return st;
+  if (!state_indices && state->shape[0] < B)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "state has %lld slots for %lld rows", (long long)state->shape[0], (long long)B);
+  for (const gdn_tensor_t* in : {q, k, v, g, state_indices}) {
+    if (overlaps(output, in)) return fail(GDN_ERR_ALIAS, "output overlaps an input");
+    if (overlaps(state, in)) return fail(GDN_ERR_ALIAS, "state overlaps an input");
+  }
+  if (overlaps(output, state)) return fail(GDN_ERR_ALIAS, "output overlaps state");
+  int dev = 0;
+  if ((st = current_device(&dev)) != GDN_OK) return st;
+  gdn::DecayStepParams p;
+  memset(&p, 0, sizeof(p));
+  p.q = q->data; p.q_sb = q->stride[0]; p.q_sh = q->stride[1];
+  p.k = k->data; p.k_sb = k->stride[0]; p.k_sh = k->stride[1];
+  p.v = v->data; p.v_sb = v->stride[0]; p.v_sh = v->stride[1];
+  if (g) { p.g = g->data; p.g_sb = g->stride[0]; p.g_sh = g->stride[1]; p.g_dtype = g->dtype; }
+  p.state = state->data; p.st_slot = state->stride[0]; p.st_head = state->stride[1];
+  p.st_slots = state->shape[0]; p.st_dtype = state->dtype;
+  if (state_indices) { p.state_idx = state_indices->data; p.idx_dtype = state_indices->dtype; }
+  p.out = output->data; p.o_sb = output->stride[0]; p.o_sh = output->stride[1];
+  p.dev_err = g_dev[dev].dev_err;
+  p.B = (int32_t)B; p.H = (int32_t)s.H; p.H_qk = (int32_t)s.Hqk; p.H_v = (int32_t)s.Hv;
+  p.scale = (scale == 0.0f) ? 1.0f / std::sqrt(128.0f) : scale;
+  p.in_f16 = q->dtype == GDN_F16 ? 1 : 0;
+  cudaError_t e = gdn::launch_decay_step(p, stream);
+  if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "decay step launch: %s", cudaGetErrorString(e));
   return GDN_OK;
 }
 

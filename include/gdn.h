@@ -74,6 +74,7 @@ typedef struct {
 #define GDN_DEVERR_CU_SEQLENS   0x1  /* some cu_seqlens bound was negative, decreasing or > T */
 #define GDN_DEVERR_STATE_INDEX  0x2  /* some state_indices entry was outside the state pool */
 #define GDN_DEVERR_TIMEOUT      0x4  /* an on-chip wait gave up (the unit's results are invalid) */
+#define GDN_DEVERR_POSITION     0x8  /* some positions entry was outside the cos_sin table */
 
 /*
  * gdn_init: check that `device` is an sm_103 GPU (compute capability 10.3) and
@@ -263,6 +264,68 @@ gdn_status_t gdn_chunk_prefill_noalloc(const gdn_tensor_t* q, const gdn_tensor_t
  */
 gdn_status_t gdn_reserve_workspace(size_t bytes, cudaStream_t stream);
 size_t gdn_split_workspace_bytes(int64_t num_seqs, int64_t num_sab_heads, int splits);
+
+/*
+ * gdn_qk_norm_rope: RMS norm of every query and key head and the rotation of its first R
+ * values by the token's position, in one pass.  For each token and head, x its 128 values:
+ *
+ *     y = x / sqrt(mean(x^2) + eps) * (weight + weight_offset)
+ *     (y_a, y_b) <- (y_a cos - y_b sin, y_a sin + y_b cos)   for the R / 2 pairs (a, b)
+ *
+ * in f32, rounded once.  The 128 - R values behind the rotated ones are only normalised.
+ *
+ *  q              [T, H_q, 128] bf16 or f16 (stride rules of gdn_chunk_prefill's q).
+ *  k              nullable with k_weight and k_out.  [T, H_k, 128], q's dtype.
+ *  q_weight,
+ *  k_weight       nullable (no weight).  [128] f32, bf16 or f16, contiguous, 16-byte aligned.
+ *  weight_offset  added to a weight (1 for weights stored around zero); ignored without one.
+ *  eps            finite, >= 0.
+ *  cos_sin        nullable (norm only).  [places, R] f32, R a multiple of 16 up to 128: the
+ *                 R / 2 cosines, then the R / 2 sines of a place.  Rows contiguous, 16-byte
+ *                 aligned.
+ *  positions      nullable (token t takes place t).  [T] i32 or i64.  A place outside the
+ *                 table sets GDN_DEVERR_POSITION and leaves the token's output rows unwritten.
+ *  interleaved    zero: pair i is (i, i + R / 2); nonzero: (2 i, 2 i + 1).
+ *  q_out, k_out   shapes and dtypes of q and k; each may be the very view it is computed
+ *                 from (in place).  Any other overlap is refused (GDN_ERR_ALIAS); slices of
+ *                 one buffer that lie side by side in each token's row are not an overlap.
+ * Asynchronous on `stream`; no workspace.
+ */
+gdn_status_t gdn_qk_norm_rope(const gdn_tensor_t* q, const gdn_tensor_t* k, const gdn_tensor_t* q_weight,
+                              const gdn_tensor_t* k_weight, float weight_offset, float eps,
+                              const gdn_tensor_t* cos_sin, const gdn_tensor_t* positions,
+                              int interleaved, const gdn_tensor_t* q_out, const gdn_tensor_t* k_out,
+                              cudaStream_t stream);
+
+/*
+ * gdn_decay_prefill: linear attention with a decay over a packed varlen batch, the layer
+ * without the delta update.  For each sequence and head, S the 128 x 128 state (V-major):
+ *
+ *     S_t = g_t S_{t-1} + v_t k_t^T,     o_t = scale S_t q_t
+ *
+ * Arguments, layouts, defaults and errors are those of gdn_chunk_prefill's arguments of the
+ * same names (there is no beta and no norm).  g with a token stride of 0 is one decay for
+ * each head.  An infinity or NaN in a token's q, k or v can reach the other outputs of its
+ * sequence and head, never those of another sequence.  With f16 inputs the state
+ * enters the read-out as scale * S in f16, so values beyond 65504 overflow there.
+ *  batch_invariant  nonzero: never split a sequence, so every output and state bit depends
+ *                   only on that sequence's own inputs.
+ */
+gdn_status_t gdn_decay_prefill(const gdn_tensor_t* q, const gdn_tensor_t* k, const gdn_tensor_t* v,
+                               const gdn_tensor_t* g, float scale, const gdn_tensor_t* initial_state,
+                               const gdn_tensor_t* state_indices, const gdn_tensor_t* output_state,
+                               const gdn_tensor_t* cu_seqlens, int batch_invariant,
+                               const gdn_tensor_t* output, cudaStream_t stream);
+
+/*
+ * gdn_decay_step: one token per batch row through the recurrence of gdn_decay_prefill, each
+ * row's state slot read and written in place.  Arguments and errors are those of
+ * gdn_decode_step's arguments of the same names; output as q's stride rules ([B, H, 128]).
+ */
+gdn_status_t gdn_decay_step(const gdn_tensor_t* q, const gdn_tensor_t* k, const gdn_tensor_t* v,
+                            const gdn_tensor_t* g, float scale, const gdn_tensor_t* state,
+                            const gdn_tensor_t* state_indices, const gdn_tensor_t* output,
+                            cudaStream_t stream);
 
 /*
  * gdn_get_device_status: synchronise `stream`, then return in *device_error the
