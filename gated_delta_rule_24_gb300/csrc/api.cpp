@@ -101,13 +101,13 @@ gdn_status_t ensure_encode() {
   return GDN_OK;
 }
 
-// q/k/v: [T, heads, 128] bf16 read in boxes of (64 dk, 1 head, 64 tokens), 128B swizzle.
-gdn_status_t encode_qkv(CUtensorMap* m, const gdn_tensor_t* t, const char* name) {
+// q/k/v: [T, heads, 128] bf16 read in boxes of (64 dk, 1 head, `rows` tokens), 128B swizzle.
+gdn_status_t encode_qkv(CUtensorMap* m, const gdn_tensor_t* t, const char* name, uint32_t rows = 64) {
   memset(m, 0, sizeof(*m));
   if (t->shape[0] == 0) return GDN_OK;  // no token will ever be loaded
   cuuint64_t dims[3] = {(cuuint64_t)t->shape[2], (cuuint64_t)t->shape[1], (cuuint64_t)t->shape[0]};
   cuuint64_t strides[2] = {(cuuint64_t)t->stride[1] * 2, (cuuint64_t)t->stride[0] * 2};
-  cuuint32_t box[3] = {64, 1, 64};
+  cuuint32_t box[3] = {64, 1, rows};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = g_encode(m, t->dtype == GDN_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, t->data, dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -116,13 +116,13 @@ gdn_status_t encode_qkv(CUtensorMap* m, const gdn_tensor_t* t, const char* name)
   return GDN_OK;
 }
 
-// output: [T, H, 128] bf16 written in boxes of (64 dv, 1 head, 64 tokens), 128B swizzle.
-gdn_status_t encode_out(CUtensorMap* m, const gdn_tensor_t* t) {
+// output: [T, H, 128] bf16 written in boxes of (64 dv, 1 head, `rows` tokens), 128B swizzle.
+gdn_status_t encode_out(CUtensorMap* m, const gdn_tensor_t* t, uint32_t rows = 64) {
   memset(m, 0, sizeof(*m));
   if (t->shape[0] == 0) return GDN_OK;
   cuuint64_t dims[3] = {(cuuint64_t)t->shape[2], (cuuint64_t)t->shape[1], (cuuint64_t)t->shape[0]};
   cuuint64_t strides[2] = {(cuuint64_t)t->stride[1] * 2, (cuuint64_t)t->stride[0] * 2};
-  cuuint32_t box[3] = {64, 1, 64};
+  cuuint32_t box[3] = {64, 1, rows};
   cuuint32_t estr[3] = {1, 1, 1};
   CUresult r = g_encode(m, t->dtype == GDN_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, t->data, dims, strides, box, estr,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
@@ -878,9 +878,10 @@ gdn_status_t gdn_decay_prefill(const gdn_tensor_t* q, const gdn_tensor_t* k, con
   if (N == 0) return GDN_OK;
   gdn::DecayPrefillParams p;
   memset(&p, 0, sizeof(p));
-  p.q = q->data; p.q_st = q->stride[0]; p.q_sh = q->stride[1];
-  p.k = k->data; p.k_st = k->stride[0]; p.k_sh = k->stride[1];
-  p.v = v->data; p.v_st = v->stride[0]; p.v_sh = v->stride[1];
+  if ((st = encode_qkv(&p.tm_q, q, "q", gdn::kDecayChunk)) != GDN_OK) return st;
+  if ((st = encode_qkv(&p.tm_k, k, "k", gdn::kDecayChunk)) != GDN_OK) return st;
+  if ((st = encode_qkv(&p.tm_v, v, "v", gdn::kDecayChunk)) != GDN_OK) return st;
+  if ((st = encode_out(&p.tm_o, output, gdn::kDecayChunk)) != GDN_OK) return st;
   if (g) { p.g = g->data; p.g_st = g->stride[0]; p.g_sh = g->stride[1]; p.g_dtype = g->dtype; }
   if (initial_state) {
     p.s_in = initial_state->data; p.sin_slot = initial_state->stride[0]; p.sin_head = initial_state->stride[1];

@@ -31,13 +31,11 @@ cudaError_t launch_norm_rope(const RopeParams& p, cudaStream_t stream);
 
 // Linear attention with a decay over packed sequences: S <- g S + v k^T, o = scale S q.
 struct DecayPrefillParams {
-  const void* q;  // [T, H_qk, 128], strides in elements
-  int64_t q_st, q_sh;
-  const void* k;
-  int64_t k_st, k_sh;
-  const void* v;  // [T, H_v, 128]
-  int64_t v_st, v_sh;
-  const void* g;  // [T, H] or null; a token stride of 0 is one decay for each head
+  CUtensorMap tm_q;  // [T, H_qk, 128], box (64 values, 1 head, kDecayChunk tokens), 128B swizzle
+  CUtensorMap tm_k;
+  CUtensorMap tm_v;  // [T, H_v, 128]
+  CUtensorMap tm_o;  // output [T, H, 128] (stores)
+  const void* g;     // [T, H] or null, strides in elements; a token stride of 0 is one decay for each head
   int64_t g_st, g_sh;
   const void* s_in;  // [slots, H, 128, 128] or null
   int64_t sin_slot, sin_head, sin_slots;
@@ -54,6 +52,7 @@ struct DecayPrefillParams {
   float scale;
   int32_t op_f16;
 };
+constexpr int kDecayChunk = 128;  // tokens of a chunk
 cudaError_t launch_decay_prefill(const DecayPrefillParams& p, cudaStream_t stream);
 
 // The same recurrence for one token of each batch row, states updated in place.

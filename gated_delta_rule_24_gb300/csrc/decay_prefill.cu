@@ -3,97 +3,722 @@
 //
 //   S_t = g_t S_{t-1} + v_t k_t^T,   o_t = scale S_t q_t.
 //
-// The token recurrence itself: a CTA of 256 threads holds one state in registers, two
-// threads a row with 64 columns each, and takes the tokens one after another from tiles of
-// 16 staged in shared memory.
+// Chunk form, 128 tokens at a time (i, j tokens of the chunk, G = cumsum(log2 g)):
+//
+//   P_ij = scale 2^(G_i - G_j) (q_i . k_j)   for j <= i, else 0
+//   O    = diag(2^G) Q (scale S)^T + P V
+//   S   <- 2^(G_last) S + V_d^T K,           V_d = diag(2^(G_last - G)) V
+//
+// Four products of 128 x 128 x 128 on tcgen05 (the last one two or three times, see
+// below) against 128 KB of q, k, v and o: the bytes bound it once the products of one chunk
+// run without a pause, and that is what the layout is for.
+//
+// One persistent CTA per SM walks (sequence, head) units chunk by chunk.  Roles (16 warps):
+//   warp 0      TMA loads of Q, K, V (two stages) and the unit records;
+//   warp 1      issues every product: Q K^T, Q S^T, V_d^T K, P V of a chunk in this order,
+//               so that P is built while Q S^T and V_d^T K run, and the state is read out
+//               and V_d of the next chunk built while P V and the next Q K^T run;
+//   warp 2      the gates: prefix and suffix sums of log2 g, one chunk ahead;
+//   warp 3      stores of the output tile;
+//   warps 4-7   one thread a token: P (tcgen05.ld, decay, mask, back to TMEM as the A operand
+//               of P V), the 2^G_i of Q S^T in place, and the output tile;
+//   warps 8-15  two threads a value row: the state in registers (f32, 64 values a thread),
+//               its 16-bit copy in shared memory for Q S^T, and V_d.
+// Hand-offs are mbarriers, every wait is bounded and ends early when any role gave up.
+//
+// The state never waits in TMEM: V_d^T K goes to a buffer of its own, and S <- gamma S + it
+// happens in registers, so the chain from chunk to chunk is a read-out, 64 FMAs a thread
+// and a 16-bit copy, next to products that do not depend on it.
+//
+// Precision: P and the copy of scale S are rounded to the 16-bit type of q, k, v (as the
+// output is); everything else that is summed is f32.  V_d would put its rounding straight
+// into the state, so it enters as the sum of 16-bit terms, each the rounding of what is
+// left: two (16 bits bf16, 22 bits f16), or three for bf16 inputs unless the state leaves
+// the call in 16 bits; an f32 state then is as exact as f32 sums are.
+//
+// 2^(G_i - G_j) within blocks of 32 tokens is computed for each pair; between blocks it is
+// the product 2^(G_i - G_e) 2^(G_e - G_j) with e the last token of j's block, both at most
+// 1, so that it costs a row factor and a column factor and cannot overflow.
+//
+// Rows past the end of a sequence hold the next one's tokens (or TMA's zeros).  They are
+// masked where they are a row or a column of P, and zeroed in shared memory where they are
+// summed over (V and K): a zero factor would not do, 0 x NaN is NaN.
 #include <cuda_runtime.h>
+#include <stddef.h>
 
 #include "decay.cuh"
+#include "ptx.cuh"
 
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kTile = 16;  // tokens staged at once
+constexpr int C = kDecayChunk;
+constexpr int D = kHeadDim;
+static_assert(C == 128 && D == 128, "the layouts below are those of 128 x 128 tiles");
 
-template <bool F16>
-__global__ void __launch_bounds__(kThreads) gdn_decay_prefill_kernel(const __grid_constant__ DecayPrefillParams p) {
-  __shared__ __align__(16) float sk[kTile][kHeadDim], sq[kTile][kHeadDim], sv[kTile][kHeadDim];
-  __shared__ float sg[kTile];
-  const int t = threadIdx.x, row = t >> 1, half = t & 1;
-  const int n = blockIdx.x / p.H, h = blockIdx.x % p.H;
-  const int64_t bos = index_at(p.cu, p.cu_dtype, n), eos = index_at(p.cu, p.cu_dtype, n + 1);
-  const int64_t slot = p.state_idx ? index_at(p.state_idx, p.idx_dtype, n) : (int64_t)n;
-  int err = 0;
-  if (bos < 0 || eos < bos || eos > p.T) err |= kDevErrCu;
-  if ((p.s_in && (slot < 0 || slot >= p.sin_slots)) || (p.s_out && (slot < 0 || slot >= p.sout_slots))) err |= kDevErrIdx;
-  if (err) {
-    if (t == 0) atomicOr(p.dev_err, err);
-    return;
+// ------------------------------------------------------------ shared memory (bytes)
+constexpr uint32_t kTile = C * D * 2;       // a 16-bit tile: two 128B-swizzled halves of 64 columns
+constexpr uint32_t kHalf = kTile / 2;
+constexpr uint32_t kStage = 3 * kTile;      // Q (later the output tile), K, V
+constexpr uint32_t kOffS = 2 * kStage;      // 16-bit copy of scale S
+constexpr uint32_t kOffSmall = kOffS + kTile;
+constexpr int kRecs = 4;
+
+struct Rec {       // one unit: a sequence of one head
+  int32_t t0, len, h, nch;  // first token, tokens, head, chunks (-1: no more units)
+  int64_t slot;
+};
+struct Small {
+  float G[2][C];   // inclusive prefix sums of log2 g
+  float d[2][C];   // 2^(sum of the log2 g behind the token), 0 past the end
+  float cf[C];     // 2^(G_e - G_j), e the last token of j's block of 32
+  float gamma[2];  // 2^(G_last)
+  Rec rec[kRecs];
+  uint64_t q_full[2], k_full[2], v_full[2], kv_empty[2], q_empty[2];
+  uint64_t rec_full[kRecs], rec_empty[kRecs];
+  uint64_t gate_full[2], gate_empty[2], cf_empty;
+  uint64_t qk_done, qs_done, ds_done, o_done;  // products that have completed
+  uint64_t p_ready, o_free, o_staged[2];       // warps 4-7
+  uint64_t sb_ready, ds_free, vd_full[2];      // warps 8-15
+  uint64_t vd_empty[2], drain;
+  uint32_t tmem;
+  int32_t abort;
+};
+constexpr uint32_t kSmem = kOffSmall + sizeof(Small);
+static_assert(kSmem <= 227 * 1024, "shared memory budget");
+
+// ------------------------------------------------------------ TMEM (columns)
+constexpr uint32_t kTmAcc = 0;     // Q K^T (128), then P as packed pairs in the first 64
+constexpr uint32_t kTmO = 128;     // Q S^T, then the output
+constexpr uint32_t kTmDs = 256;    // V_d^T K
+constexpr uint32_t kTmVd = 384;    // V_d terms as packed pairs, two slots of 64
+constexpr uint32_t kTmCols = 512;
+
+constexpr int kThreads = 512;
+constexpr int kPoWarps = 4, kKsWarps = 8;
+constexpr int kReaders = 3 + kPoWarps + kKsWarps;  // warps that read a unit's record
+constexpr uint64_t kWaitNs = 200ull * 1000 * 1000;
+
+// Every wait: bounded, and over as soon as another role has given up.
+__device__ __noinline__ bool wait_slow(Small* sm, uint64_t* bar, uint32_t parity) {
+  const uint64_t t0 = global_timer_ns();
+  while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
+    if (*reinterpret_cast<volatile int32_t*>(&sm->abort) || global_timer_ns() - t0 > kWaitNs) return false;
   }
-  const int hq = h / (p.H / p.H_qk), hv = h / (p.H / p.H_v);
-  float s[64];
-#pragma unroll
-  for (int e = 0; e < 64; ++e) {
-    const int c = 4 * (2 * (e >> 2) + half) + (e & 3);  // 16-byte column groups alternate between the two threads
-    s[e] = p.s_in ? real_of(p.s_in, p.sin_dtype, slot * p.sin_slot + (int64_t)h * p.sin_head + row * kHeadDim + c) : 0.f;
+  return true;
+}
+__device__ __forceinline__ bool wait(Small* sm, uint64_t* bar, uint32_t parity) {
+  const bool ok = mbar_try_wait(bar, parity) || wait_slow(sm, bar, parity);
+  return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ void give_up(const DecayPrefillParams& p, Small* sm) {
+  *reinterpret_cast<volatile int32_t*>(&sm->abort) = 1;
+  atomicOr(p.dev_err, kDevErrTimeout);
+}
+// One arrival for the warp, behind everything its lanes have done.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// The next unit's record, for every role but the producer; false when there is none left
+// or a wait gave up (*failed).
+__device__ __forceinline__ bool next_unit(Small* sm, int u, int lane, Rec* r, bool* failed) {
+  const int slot = u % kRecs;
+  if (!wait(sm, &sm->rec_full[slot], (u / kRecs) & 1)) {
+    *failed = true;
+    return false;
   }
-  for (int64_t t0 = bos; t0 < eos; t0 += kTile) {
-    const int len = (int)(eos - t0 < kTile ? eos - t0 : kTile);
-    for (int e = t; e < len * (kHeadDim / 2); e += kThreads) {
-      const int i = e / (kHeadDim / 2), c = 2 * (e % (kHeadDim / 2));
-      const int64_t tok = t0 + i;
-      auto pair = [&](const void* x, int64_t off) {
-        return unpack16<F16>(*reinterpret_cast<const uint32_t*>(reinterpret_cast<const uint16_t*>(x) + off));
+  *r = sm->rec[slot];
+  warp_arrive(&sm->rec_empty[slot], lane);
+  return r->nch >= 0;
+}
+
+// ------------------------------------------------------------ warp 0: loads
+__device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_t* base, Small* sm, int lane) {
+  bool ok = true;
+  int u = 0, ci = 0;  // units and chunks so far
+  const int64_t units = (int64_t)p.N * p.H;
+  int kv_loads = 0, q_loads = 0;
+  auto publish = [&](const Rec& r) {
+    const int slot = u % kRecs;
+    if (u >= kRecs && !wait(sm, &sm->rec_empty[slot], (u / kRecs - 1) & 1)) return false;
+    if (lane == 0) {
+      sm->rec[slot] = r;
+      mbar_arrive(&sm->rec_full[slot]);
+    }
+    ++u;
+    return true;
+  };
+  for (int64_t x = blockIdx.x; x < units && ok; x += gridDim.x) {
+    const int n = (int)(x / p.H), h = (int)(x % p.H);
+    const int64_t bos = index_at(p.cu, p.cu_dtype, n), eos = index_at(p.cu, p.cu_dtype, n + 1);
+    const int64_t slot = p.state_idx ? index_at(p.state_idx, p.idx_dtype, n) : (int64_t)n;
+    int err = 0;
+    if (bos < 0 || eos < bos || eos > p.T) err |= kDevErrCu;
+    if ((p.s_in && (slot < 0 || slot >= p.sin_slots)) || (p.s_out && (slot < 0 || slot >= p.sout_slots)))
+      err |= kDevErrIdx;
+    if (err) {
+      if (lane == 0) atomicOr(p.dev_err, err);
+      continue;
+    }
+    const int len = (int)(eos - bos), nch = (len + C - 1) / C;
+    ok = publish(Rec{(int)bos, len, h, nch, slot});
+    if (!ok) break;
+    if (p.s_in && lane == 0) {
+      const int es = p.sin_dtype == kF32 ? 4 : 2;
+      bulk_prefetch_l2(reinterpret_cast<const char*>(p.s_in) + (slot * p.sin_slot + (int64_t)h * p.sin_head) * es, D * D * es);
+    }
+    const int hq = h / (p.H / p.H_qk), hv = h / (p.H / p.H_v);
+    for (int c = 0; c < nch; ++c, ++ci) {
+      const int s = ci & 1, t0 = (int)bos + c * C;
+      uint8_t* q = base + s * kStage;
+      auto load = [&](uint8_t* dst, const CUtensorMap* tm, uint64_t* bar, int head) {
+        mbar_arrive_expect_tx(bar, kTile);
+        tma_load_3d(dst, tm, bar, 0, head, t0);
+        tma_load_3d(dst + kHalf, tm, bar, 64, head, t0);
       };
-      *reinterpret_cast<float2*>(&sk[i][c]) = pair(p.k, tok * p.k_st + (int64_t)hq * p.k_sh + c);
-      *reinterpret_cast<float2*>(&sq[i][c]) = pair(p.q, tok * p.q_st + (int64_t)hq * p.q_sh + c);
-      *reinterpret_cast<float2*>(&sv[i][c]) = pair(p.v, tok * p.v_st + (int64_t)hv * p.v_sh + c);
-    }
-    if (t < len) sg[t] = p.g ? gate_at(p.g, p.g_dtype, (t0 + t) * p.g_st + (int64_t)h * p.g_sh) : 1.f;
-    __syncthreads();
-    for (int i = 0; i < len; ++i) {
-      const float g = sg[i], v = sv[i][row];
-      float acc = 0.f;
-#pragma unroll
-      for (int j = 0; j < 16; ++j) {
-        const float4 k = *reinterpret_cast<const float4*>(&sk[i][4 * (2 * j + half)]);
-        const float4 q = *reinterpret_cast<const float4*>(&sq[i][4 * (2 * j + half)]);
-        s[4 * j] = fmaf(g, s[4 * j], v * k.x);
-        s[4 * j + 1] = fmaf(g, s[4 * j + 1], v * k.y);
-        s[4 * j + 2] = fmaf(g, s[4 * j + 2], v * k.z);
-        s[4 * j + 3] = fmaf(g, s[4 * j + 3], v * k.w);
-        acc = fmaf(s[4 * j], q.x, acc);
-        acc = fmaf(s[4 * j + 1], q.y, acc);
-        acc = fmaf(s[4 * j + 2], q.z, acc);
-        acc = fmaf(s[4 * j + 3], q.w, acc);
+      ok = ci < 2 || wait(sm, &sm->kv_empty[s], ((ci >> 1) - 1) & 1);
+      if (!ok) break;
+      if (lane == 0) {
+        load(q + kTile, &p.tm_k, &sm->k_full[s], hq);
+        load(q + 2 * kTile, &p.tm_v, &sm->v_full[s], hv);
       }
-      acc += __shfl_xor_sync(0xffffffffu, acc, 1);
-      if (half == 0)
-        reinterpret_cast<uint16_t*>(p.out)[(t0 + i) * p.o_st + (int64_t)h * p.o_sh + row] =
-            (uint16_t)pack16x2<F16>(p.scale * acc, 0.f);
+      ++kv_loads;
+      ok = ci < 2 || wait(sm, &sm->q_empty[s], ((ci >> 1) - 1) & 1);
+      if (!ok) break;
+      if (lane == 0) load(q, &p.tm_q, &sm->q_full[s], hq);
+      ++q_loads;
     }
-    __syncthreads();
   }
-  if (!p.s_out) return;
+  if (ok) ok = publish(Rec{0, 0, 0, -1, 0});
+  if (!ok && lane == 0) give_up(p, sm);
+  // loads that no role waits for any more land before the CTA's shared memory goes away
+  auto landed = [&](uint64_t (&bar)[2], int loads) {
+    for (int s = 0; s < 2; ++s) {
+      const int n = (loads + 1 - s) / 2;  // loads of stage s
+      if (n) mbar_wait(&bar[s], (n - 1) & 1, kWaitNs);
+    }
+  };
+  landed(sm->k_full, kv_loads);
+  landed(sm->v_full, kv_loads);
+  landed(sm->q_full, q_loads);
+}
+
+// ------------------------------------------------------------ warp 1: products
+// V_d terms: a slot holds kSub tokens, kSub / 2 columns a term.
+template <int kTerms>
+__host__ __device__ constexpr int sub_tokens() { return kTerms == 2 ? 64 : 32; }
+
+template <bool F16, int kTerms>
+__device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* base, Small* sm, uint32_t tmem, int lane) {
+  constexpr int kSub = sub_tokens<kTerms>(), kSubs = C / kSub;
+  const uint32_t id_kk = idesc_16_f32(F16, 128, 128, 0, 0, 0);  // both operands K-major
+  const uint32_t id_kmn = idesc_16_f32(F16, 128, 128, 0, 1, 0); // B MN-major (its rows are summed over)
+  const uint64_t d_s = sdesc_sw128(smem_u32(base + kOffS), 16, 1024);
+  bool failed = false;
+  Rec r;
+  int ci = 0, vi = 0;
+  for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
+    for (int c = 0; c < r.nch; ++c, ++ci) {
+      const int s = ci & 1;
+      const uint32_t ph = (ci >> 1) & 1, one = ci & 1;
+      uint8_t* st = base + s * kStage;
+      const uint64_t d_q = sdesc_sw128(smem_u32(st), 16, 1024), d_k = sdesc_sw128(smem_u32(st + kTile), 16, 1024);
+      const uint64_t d_kt = sdesc_sw128(smem_u32(st + kTile), kHalf, 1024);
+      const uint64_t d_vt = sdesc_sw128(smem_u32(st + 2 * kTile), kHalf, 1024);
+      // Q K^T.  P of the chunk before is being read by its P V at the latest, which was
+      // issued before: the products run in order.
+      if (!(wait(sm, &sm->k_full[s], ph) && wait(sm, &sm->q_full[s], ph))) { failed = true; break; }
+      tc_fence_after();
+      if (lane == 0) {
 #pragma unroll
-  for (int e = 0; e < 64; ++e) {
-    const int c = 4 * (2 * (e >> 2) + half) + (e & 3);
-    const int64_t i = slot * p.sout_slot + (int64_t)h * p.sout_head + row * kHeadDim + c;
-    if (p.sout_dtype == kF32) reinterpret_cast<float*>(p.s_out)[i] = s[e];
-    else if (p.sout_dtype == kF16) reinterpret_cast<__half*>(p.s_out)[i] = __float2half_rn(s[e]);
-    else reinterpret_cast<__nv_bfloat16*>(p.s_out)[i] = __float2bfloat16_rn(s[e]);
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t o = ((i >> 2) * kHalf + (i & 3) * 32) / 16;
+          mma_ss(tmem + kTmAcc, d_q + o, d_k + o, id_kk, i > 0);
+        }
+        mma_commit(&sm->qk_done);
+      }
+      __syncwarp();
+      // Q (scale S)^T
+      if (!(wait(sm, &sm->sb_ready, one) && (ci == 0 || wait(sm, &sm->o_free, one ^ 1)))) { failed = true; break; }
+      tc_fence_after();
+      if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          const uint32_t o = ((i >> 2) * kHalf + (i & 3) * 32) / 16;
+          mma_ss(tmem + kTmO, d_q + o, d_s + o, id_kk, i > 0);
+        }
+        mma_commit(&sm->qs_done);
+      }
+      __syncwarp();
+      // V_d^T K
+      if (ci > 0 && !wait(sm, &sm->ds_free, one ^ 1)) { failed = true; break; }
+      for (int b = 0; b < kSubs && !failed; ++b, ++vi) {
+        if (!wait(sm, &sm->vd_full[vi & 1], (vi >> 1) & 1)) { failed = true; break; }
+        tc_fence_after();
+        if (lane == 0) {
+#pragma unroll
+          for (int t = 0; t < kTerms; ++t)
+#pragma unroll
+            for (int i = 0; i < kSub / 16; ++i)
+              mma_ts(tmem + kTmDs, tmem + kTmVd + (vi & 1) * 64 + t * (kSub / 2) + i * 8,
+                     d_kt + (b * (kSub / 16) + i) * 128, id_kmn, b + t + i > 0);
+          mma_commit(&sm->vd_empty[vi & 1]);
+          if (b == kSubs - 1) mma_commit(&sm->ds_done);
+        }
+        __syncwarp();
+      }
+      if (failed) break;
+      // + P V
+      if (!wait(sm, &sm->p_ready, one)) { failed = true; break; }
+      tc_fence_after();
+      if (lane == 0) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mma_ts(tmem + kTmO, tmem + kTmAcc + i * 8, d_vt + i * 128, id_kmn, 1);
+        mma_commit(&sm->o_done);
+        mma_commit(&sm->kv_empty[s]);
+      }
+      __syncwarp();
+    }
+    if (failed) break;
   }
+  if (failed && lane == 0) give_up(p, sm);
+  if (lane == 0) mma_commit(&sm->drain);
+  __syncwarp();
+  mbar_wait(&sm->drain, 0, kWaitNs);  // no product is under way when TMEM is freed
+}
+
+// ------------------------------------------------------------ warp 2: gates
+__device__ __forceinline__ void run_gates(const DecayPrefillParams& p, Small* sm, int lane) {
+  bool failed = false;
+  Rec r;
+  int ci = 0;
+  for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
+    for (int c = 0; c < r.nch; ++c, ++ci) {
+      const int b = ci & 1, left = r.len - c * C;
+      float lg[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int j = 4 * lane + e;
+        lg[e] = 0.f;
+        if (p.g && j < left)
+          lg[e] = log2f(gate_at(p.g, p.g_dtype, ((int64_t)r.t0 + c * C + j) * p.g_st + (int64_t)r.h * p.g_sh));
+      }
+      // prefix and suffix sums: the suffix is summed on its own, since G_last - G_j would
+      // carry the rounding of two large sums into the state
+      float pre[4], suf[4];
+      pre[0] = lg[0]; pre[1] = pre[0] + lg[1]; pre[2] = pre[1] + lg[2]; pre[3] = pre[2] + lg[3];
+      suf[3] = 0.f; suf[2] = lg[3]; suf[1] = suf[2] + lg[2]; suf[0] = suf[1] + lg[1];
+      float up = pre[3], down = pre[3];
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const float a = __shfl_up_sync(0xffffffffu, up, o), z = __shfl_down_sync(0xffffffffu, down, o);
+        if (lane >= o) up += a;
+        if (lane + o < 32) down += z;
+      }
+      float before = __shfl_up_sync(0xffffffffu, up, 1), behind = __shfl_down_sync(0xffffffffu, down, 1);
+      if (lane == 0) before = 0.f;
+      if (lane == 31) behind = 0.f;
+      const float total = __shfl_sync(0xffffffffu, down, 0);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) { pre[e] += before; suf[e] += behind; }
+      const float g_end = __shfl_sync(0xffffffffu, pre[3], lane | 7);  // the last token of the block of 32
+      if (!(ci < 2 || wait(sm, &sm->gate_empty[b], ((ci >> 1) - 1) & 1))) { failed = true; break; }
+      *reinterpret_cast<float4*>(&sm->G[b][4 * lane]) = make_float4(pre[0], pre[1], pre[2], pre[3]);
+      float d[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) d[e] = 4 * lane + e < left ? exp2f(suf[e]) : 0.f;
+      *reinterpret_cast<float4*>(&sm->d[b][4 * lane]) = make_float4(d[0], d[1], d[2], d[3]);
+      if (lane == 0) sm->gamma[b] = exp2f(total);
+      if (!(ci == 0 || wait(sm, &sm->cf_empty, (ci - 1) & 1))) { failed = true; break; }
+      *reinterpret_cast<float4*>(&sm->cf[4 * lane]) = make_float4(
+          exp2_fast(g_end - pre[0]), exp2_fast(g_end - pre[1]), exp2_fast(g_end - pre[2]), exp2_fast(g_end - pre[3]));
+      warp_arrive(&sm->gate_full[b], lane);
+    }
+    if (failed) break;
+  }
+  if (failed && lane == 0) give_up(p, sm);
+}
+
+// ------------------------------------------------------------ warp 3: output stores
+__device__ __forceinline__ void run_store(const DecayPrefillParams& p, uint8_t* base, Small* sm, int lane) {
+  bool failed = false;
+  Rec r;
+  int ci = 0;
+  for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
+    for (int c = 0; c < r.nch; ++c, ++ci) {
+      const int s = ci & 1, t0 = r.t0 + c * C, left = r.len - c * C;
+      if (!wait(sm, &sm->o_staged[s], (ci >> 1) & 1)) { failed = true; break; }
+      uint8_t* tile = base + s * kStage;
+      if (left >= C) {
+        if (lane == 0) {
+          tma_store_3d(&p.tm_o, tile, 0, r.h, t0);
+          tma_store_3d(&p.tm_o, tile + kHalf, 64, r.h, t0);
+          bulk_commit();
+          bulk_wait_read_all();
+        }
+      } else {  // only the sequence's own rows: the next rows belong to another unit
+        char* o = reinterpret_cast<char*>(p.out) + ((int64_t)t0 * p.o_st + (int64_t)r.h * p.o_sh) * 2;
+#pragma unroll 4
+        for (int e = lane; e < left * 16; e += 32) {
+          const int row = e >> 4, ch = e & 15;
+          *reinterpret_cast<uint4*>(o + (int64_t)row * p.o_st * 2 + ch * 16) =
+              *reinterpret_cast<const uint4*>(tile + (ch >> 3) * kHalf + sw128_chunk(row, ch & 7));
+        }
+      }
+      warp_arrive(&sm->q_empty[s], lane);
+    }
+    if (failed) break;
+  }
+  if (failed && lane == 0) give_up(p, sm);
+  if (lane == 0) bulk_wait_read_all();
+}
+
+// ------------------------------------------------------------ warps 4-7: P and the output
+template <bool F16>
+__device__ __forceinline__ void run_po(const DecayPrefillParams& p, uint8_t* base, Small* sm, uint32_t tmem, int warp, int lane) {
+  const int w = warp & 3, row = 32 * w + lane;
+  const uint32_t tr = tmem + ((uint32_t)(32 * w) << 16);
+  bool failed = false;
+  Rec r;
+  int ci = 0;
+  for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
+    for (int c = 0; c < r.nch; ++c, ++ci) {
+      const int b = ci & 1, s = ci & 1;
+      const uint32_t one = ci & 1;
+      if (!(wait(sm, &sm->gate_full[b], (ci >> 1) & 1) && wait(sm, &sm->qk_done, one))) { failed = true; break; }
+      tc_fence_after();
+      const float gi = sm->G[b][row];
+      // P: blocks of 32 columns before this warp's diagonal block by factors, that block pair by pair,
+      // zeros behind it.  The packed pairs go over columns that this thread has read already.
+      for (int jb = 0; jb < 4; ++jb) {
+        uint32_t pk[16];
+        if (jb > w) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) pk[e] = 0u;
+        } else {
+          uint32_t a[32];
+          tmem_ld32(tr + kTmAcc + 32 * jb, a);
+          tmem_ld_wait();
+          if (jb < w) {
+            const float rf = p.scale * exp2_fast(gi - sm->G[b][32 * jb + 31]);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 f = *reinterpret_cast<const float4*>(&sm->cf[32 * jb + 4 * e]);
+              pk[2 * e] = pack16x2<F16>(__uint_as_float(a[4 * e]) * (f.x * rf), __uint_as_float(a[4 * e + 1]) * (f.y * rf));
+              pk[2 * e + 1] = pack16x2<F16>(__uint_as_float(a[4 * e + 2]) * (f.z * rf), __uint_as_float(a[4 * e + 3]) * (f.w * rf));
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 f = *reinterpret_cast<const float4*>(&sm->G[b][32 * jb + 4 * e]);
+              const float x0 = __uint_as_float(a[4 * e]) * (p.scale * exp2_fast(gi - f.x));
+              const float x1 = __uint_as_float(a[4 * e + 1]) * (p.scale * exp2_fast(gi - f.y));
+              const float x2 = __uint_as_float(a[4 * e + 2]) * (p.scale * exp2_fast(gi - f.z));
+              const float x3 = __uint_as_float(a[4 * e + 3]) * (p.scale * exp2_fast(gi - f.w));
+              pk[2 * e] = pack16x2<F16>(4 * e <= lane ? x0 : 0.f, 4 * e + 1 <= lane ? x1 : 0.f);
+              pk[2 * e + 1] = pack16x2<F16>(4 * e + 2 <= lane ? x2 : 0.f, 4 * e + 3 <= lane ? x3 : 0.f);
+            }
+          }
+        }
+        tmem_st16(tr + kTmAcc + 16 * jb, pk);
+      }
+      warp_arrive(&sm->cf_empty, lane);
+      // Q (scale S)^T of the row times 2^G_i
+      if (!wait(sm, &sm->qs_done, one)) { failed = true; break; }
+      tc_fence_after();
+      const float gam = exp2f(gi);
+      for (int q = 0; q < 4; ++q) {
+        uint32_t a[32];
+        tmem_ld32(tr + kTmO + 32 * q, a);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 32; ++e) a[e] = __float_as_uint(gam * __uint_as_float(a[e]));
+        tmem_st32(tr + kTmO + 32 * q, a);
+      }
+      tmem_st_wait();
+      tc_fence_before();
+      warp_arrive(&sm->p_ready, lane);
+      if (lane == 0) mbar_arrive(&sm->gate_empty[b]);
+      // the output tile, into the stage of Q (both products that read Q are complete)
+      if (!wait(sm, &sm->o_done, one)) { failed = true; break; }
+      tc_fence_after();
+      uint8_t* tile = base + s * kStage;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t a[32];
+        tmem_ld32(tr + kTmO + 32 * q, a);
+        tmem_ld_wait();
+        if (q == 3) {
+          tc_fence_before();
+          warp_arrive(&sm->o_free, lane);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float x[8];
+#pragma unroll
+          for (int f = 0; f < 8; ++f) x[f] = __uint_as_float(a[8 * e + f]);
+          *reinterpret_cast<uint4*>(tile + (q >> 1) * kHalf + sw128_chunk(row, 4 * (q & 1) + e)) = pack16x8<F16>(x);
+        }
+      }
+      fence_proxy_async_smem();
+      warp_arrive(&sm->o_staged[s], lane);
+    }
+    if (failed) break;
+  }
+  if (failed && lane == 0) give_up(p, sm);
+}
+
+// ------------------------------------------------------------ warps 8-15: the state
+// 64 values (columns c0 ..) of a state row.
+__device__ __forceinline__ void load_state64(const void* base, int dtype, int64_t off, float (&s)[64]) {
+  if (dtype == kF32) {
+    const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(base) + off);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) StateType<0>::unpack(q[i], reinterpret_cast<float(&)[4]>(s[4 * i]));
+  } else {
+    const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(base) + off);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const uint4 x = q[i];
+      if (dtype == kF16) StateType<2>::unpack(x, reinterpret_cast<float(&)[8]>(s[8 * i]));
+      else StateType<1>::unpack(x, reinterpret_cast<float(&)[8]>(s[8 * i]));
+    }
+  }
+}
+__device__ __forceinline__ void store_state64(void* base, int dtype, int64_t off, const float (&s)[64]) {
+  if (dtype == kF32) {
+    uint4* q = reinterpret_cast<uint4*>(reinterpret_cast<float*>(base) + off);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) q[i] = StateType<0>::pack(reinterpret_cast<const float(&)[4]>(s[4 * i]));
+  } else {
+    uint4* q = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(base) + off);
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      q[i] = dtype == kF16 ? StateType<2>::pack(reinterpret_cast<const float(&)[8]>(s[8 * i]))
+                           : StateType<1>::pack(reinterpret_cast<const float(&)[8]>(s[8 * i]));
+  }
+}
+
+// Zero this warp's share of the rows past the end: of V exactly what the warp reads below (its
+// 32 value columns of its own tokens), of K an eighth of the columns.
+template <int kTerms>
+__device__ __forceinline__ void zero_tails(uint8_t* k, uint8_t* v, int left, int w, int hf, int lane) {
+  constexpr int kSub = sub_tokens<kTerms>();
+  const uint4 z = make_uint4(0, 0, 0, 0);
+  for (int e = lane; e < C * 4; e += 32) {
+    const int row = e >> 2, ch = 4 * w + (e & 3);  // 16-byte chunk of the 128 values
+    if (row >= left && ((row / (kSub / 2)) & 1) == hf)
+      *reinterpret_cast<uint4*>(v + (ch >> 3) * kHalf + sw128_chunk(row, ch & 7)) = z;
+  }
+  for (int e = lane; e < C * 2; e += 32) {
+    const int row = e >> 1, ch = 2 * (4 * hf + w) + (e & 1);
+    if (row >= left) *reinterpret_cast<uint4*>(k + (ch >> 3) * kHalf + sw128_chunk(row, ch & 7)) = z;
+  }
+  fence_proxy_async_smem();
+  __syncwarp();
+}
+
+template <bool F16, int kTerms>
+__device__ __forceinline__ void run_ks(const DecayPrefillParams& p, uint8_t* base, Small* sm, uint32_t tmem, int warp, int lane) {
+  constexpr int kSub = sub_tokens<kTerms>(), kSubs = C / kSub;
+  const int w = warp & 3, hf = (warp >> 2) & 1, row = 32 * w + lane;  // warps 8-11: first halves, 12-15: second
+  const uint32_t tq = tmem + ((uint32_t)(32 * w) << 16);
+  uint8_t* sb = base + kOffS + hf * kHalf;
+  bool failed = false;
+  Rec r;
+  int ci = 0, vi = 0;
+  float s[64];
+  // the 16-bit copy of scale S for the chunk ci, once Q S^T of the chunk before has read the last one
+  auto copy_state = [&](int at) {
+    if (at > 0 && !wait(sm, &sm->qs_done, (at - 1) & 1)) return false;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      float x[8];
+#pragma unroll
+      for (int f = 0; f < 8; ++f) x[f] = p.scale * s[8 * e + f];
+      *reinterpret_cast<uint4*>(sb + sw128_chunk(row, e)) = pack16x8<F16>(x);
+    }
+    fence_proxy_async_smem();
+    warp_arrive(&sm->sb_ready, lane);
+    return true;
+  };
+  for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
+    if (p.s_in) {
+      load_state64(p.s_in, p.sin_dtype, r.slot * p.sin_slot + (int64_t)r.h * p.sin_head + row * D + 64 * hf, s);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 64; ++e) s[e] = 0.f;
+    }
+    if (r.nch > 0 && !copy_state(ci)) { failed = true; break; }
+    for (int c = 0; c < r.nch; ++c, ++ci) {
+      const int b = ci & 1, st = ci & 1, left = r.len - c * C;
+      uint8_t* k = base + st * kStage + kTile;
+      uint8_t* v = k + kTile;
+      if (!(wait(sm, &sm->gate_full[b], (ci >> 1) & 1) && wait(sm, &sm->v_full[st], (ci >> 1) & 1))) { failed = true; break; }
+      if (left < C) {
+        if (!wait(sm, &sm->k_full[st], (ci >> 1) & 1)) { failed = true; break; }
+        zero_tails<kTerms>(k, v, left, w, hf, lane);
+      }
+      // V_d: transposed fragments of V (pairs of tokens, one value each) times d, as kTerms 16-bit terms
+      const uint32_t va = smem_u32(v);
+      const int m = lane >> 3, lr = lane & 7;
+      for (int sub = 0; sub < kSubs; ++sub, ++vi) {
+        if (vi >= 2 && !wait(sm, &sm->vd_empty[vi & 1], ((vi >> 1) - 1) & 1)) { failed = true; break; }
+        tc_fence_after();
+#pragma unroll
+        for (int tt = 0; tt < kSub / 32; ++tt) {
+          const int tok = sub * kSub + hf * (kSub / 2) + 16 * tt;  // 16 tokens from here
+          const float2 d0 = *reinterpret_cast<const float2*>(&sm->d[b][tok + 2 * (lane & 3)]);
+          const float2 d1 = *reinterpret_cast<const float2*>(&sm->d[b][tok + 8 + 2 * (lane & 3)]);
+          const int trow = tok + (m >> 1) * 8 + lr;
+#pragma unroll
+          for (int dd = 0; dd < 2; ++dd) {
+            const int ch = 4 * w + 2 * dd + (m & 1);
+            uint32_t a[4], t[4];
+            ldmatrix_x4_trans(va + (ch >> 3) * kHalf + sw128_chunk(trow, ch & 7), a);
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const float2 f = unpack16<F16>(a[e]);
+              const float2 dj = e < 2 ? d0 : d1;
+              x[2 * e] = f.x * dj.x;
+              x[2 * e + 1] = f.y * dj.y;
+            }
+#pragma unroll
+            for (int term = 0; term < kTerms; ++term) {
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                t[e] = pack16x2<F16>(x[2 * e], x[2 * e + 1]);
+                if (term + 1 < kTerms) {
+                  const float2 f = unpack16<F16>(t[e]);
+                  x[2 * e] -= f.x;
+                  x[2 * e + 1] -= f.y;
+                }
+              }
+              tmem_st16x128_x2(tq + ((uint32_t)(16 * dd) << 16) + kTmVd + (vi & 1) * 64 + term * (kSub / 2) +
+                                   hf * (kSub / 4) + 8 * tt, t);
+            }
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        warp_arrive(&sm->vd_full[vi & 1], lane);
+      }
+      if (failed) break;
+      // S <- gamma S + V_d^T K
+      const float gam = sm->gamma[b];
+      if (!wait(sm, &sm->ds_done, ci & 1)) { failed = true; break; }
+      tc_fence_after();
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        uint32_t a[16];
+        tmem_ld16(tq + kTmDs + 64 * hf + 16 * q, a);
+        tmem_ld_wait();
+        if (q == 3) {
+          tc_fence_before();
+          warp_arrive(&sm->ds_free, lane);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[16 * q + e] = fmaf(gam, s[16 * q + e], __uint_as_float(a[e]));
+      }
+      if (lane == 0) mbar_arrive(&sm->gate_empty[b]);
+      if (c + 1 < r.nch && !copy_state(ci + 1)) { failed = true; break; }
+    }
+    if (failed) break;
+    if (p.s_out) store_state64(p.s_out, p.sout_dtype, r.slot * p.sout_slot + (int64_t)r.h * p.sout_head + row * D + 64 * hf, s);
+  }
+  if (failed && lane == 0) give_up(p, sm);
+}
+
+// ------------------------------------------------------------ the kernel
+template <bool F16, int kTerms>
+__global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __grid_constant__ DecayPrefillParams p) {
+  extern __shared__ __align__(1024) uint8_t base[];
+  Small* sm = reinterpret_cast<Small*>(base + kOffSmall);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    auto init = [](uint64_t* bar, int n, int count) {
+      for (int i = 0; i < n; ++i) mbar_init(bar + i, count);
+    };
+    init(sm->q_full, 2, 1);
+    init(sm->k_full, 2, 1);
+    init(sm->v_full, 2, 1);
+    init(sm->kv_empty, 2, 1);
+    init(sm->q_empty, 2, 1);
+    init(sm->rec_full, kRecs, 1);
+    init(sm->rec_empty, kRecs, kReaders);
+    init(sm->gate_full, 2, 1);
+    init(sm->gate_empty, 2, kPoWarps + kKsWarps);
+    init(&sm->cf_empty, 1, kPoWarps);
+    init(&sm->qk_done, 1, 1);
+    init(&sm->qs_done, 1, 1);
+    init(&sm->ds_done, 1, 1);
+    init(&sm->o_done, 1, 1);
+    init(&sm->p_ready, 1, kPoWarps);
+    init(&sm->o_free, 1, kPoWarps);
+    init(sm->o_staged, 2, kPoWarps);
+    init(&sm->sb_ready, 1, kKsWarps);
+    init(&sm->ds_free, 1, kKsWarps);
+    init(sm->vd_full, 2, kKsWarps);
+    init(sm->vd_empty, 2, 1);
+    init(&sm->drain, 1, 1);
+    sm->abort = 0;
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tm_q);
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_v);
+    tma_prefetch_desc(&p.tm_o);
+  }
+  if (warp == 0) {
+    tmem_alloc(&sm->tmem, kTmCols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = sm->tmem;
+  if (warp == 0) run_producer(p, base, sm, lane);
+  else if (warp == 1) run_mma<F16, kTerms>(p, base, sm, tmem, lane);
+  else if (warp == 2) run_gates(p, sm, lane);
+  else if (warp == 3) run_store(p, base, sm, lane);
+  else if (warp < 8) run_po<F16>(p, base, sm, tmem, warp, lane);
+  else run_ks<F16, kTerms>(p, base, sm, tmem, warp, lane);
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 0) tmem_dealloc(tmem, kTmCols);
+}
+
+template <bool F16, int kTerms>
+cudaError_t launch(const DecayPrefillParams& p, cudaStream_t stream) {
+  static thread_local int device = -1, generation = -1;
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  const int gen = launch_config_generation();
+  if (e == cudaSuccess && (device != dev || generation != gen)) {
+    e = cudaFuncSetAttribute(gdn_decay_prefill_kernel<F16, kTerms>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e == cudaSuccess) { device = dev; generation = gen; }
+  }
+  if (e != cudaSuccess) return e;
+  const int64_t units = (int64_t)p.N * p.H;
+  const int sms = device_sm_count();
+  gdn_decay_prefill_kernel<F16, kTerms><<<(unsigned)(units < sms ? units : sms), kThreads, kSmem, stream>>>(p);
+  return cudaGetLastError();
 }
 
 }  // namespace
 
 cudaError_t launch_decay_prefill(const DecayPrefillParams& p, cudaStream_t stream) {
-  const int64_t units = (int64_t)p.N * p.H;
-  if (units <= 0) return cudaSuccess;
-  if (p.op_f16) gdn_decay_prefill_kernel<true><<<(unsigned)units, kThreads, 0, stream>>>(p);
-  else gdn_decay_prefill_kernel<false><<<(unsigned)units, kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  if ((int64_t)p.N * p.H <= 0) return cudaSuccess;
+  if (p.op_f16) return launch<true, 2>(p, stream);
+  if (p.s_out && p.sout_dtype != kF32) return launch<false, 2>(p, stream);
+  return launch<false, 3>(p, stream);
 }
 
 }  // namespace gdn

@@ -200,6 +200,15 @@ GDN_DEV void tmem_ld16x256_x4(uint32_t taddr, uint32_t (&r)[16]) {
         "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(taddr));
 }
+// Shape 16x128b, two repetitions: the warp writes 16 lanes (from the lane in taddr) x 8
+// columns.  Thread t gives r[2c] = lane (t / 4), column 4c + t % 4, and r[2c + 1] = lane
+// (t / 4 + 8), the same column: with packed 16-bit pairs, the A fragment of an m16n8k16
+// warp product (what ldmatrix returns).
+GDN_DEV void tmem_st16x128_x2(uint32_t taddr, const uint32_t (&r)[4]) {
+  asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1,%2,%3,%4};" ::"r"(taddr), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3])
+               : "memory");
+}
 #undef GDN_R8
 #undef GDN_W8
 GDN_DEV void tmem_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
@@ -263,6 +272,16 @@ GDN_DEV void mma_sync_bf16(float (&d)[4], const uint32_t (&a)[4], const uint32_t
 GDN_DEV void stmatrix_x4_trans(uint32_t saddr, uint32_t r0, uint32_t r1, uint32_t r2, uint32_t r3) {
   asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(saddr), "r"(r0),
                "r"(r1), "r"(r2), "r"(r3)
+               : "memory");
+}
+
+// Four 8 x 8 matrices of 16-bit elements read transposed: thread 8 i + j gives the shared
+// address of row j of matrix i (16 contiguous bytes); register i of thread t receives
+// elements (2 (t % 4), t / 4) and (2 (t % 4) + 1, t / 4) of matrix i (low half first).
+GDN_DEV void ldmatrix_x4_trans(uint32_t saddr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(saddr)
                : "memory");
 }
 
