@@ -27,6 +27,25 @@ __device__ __forceinline__ float gate_at(const void* p, int dtype, int64_t i) {
   return fminf(fmaxf(real_of(p, dtype, i), FLT_MIN), 1.f);
 }
 
+// Two f32 operations in one instruction.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n.reg .b64 x, y;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmul.rn.f32x2 x, x, y;\nmov.b64 {%0, %1}, x;\n}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 r;
+  asm("{\n.reg .b64 x, y, z;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nmov.b64 z, {%6, %7};\n"
+      "fma.rn.f32x2 x, x, y, z;\nmov.b64 {%0, %1}, x;\n}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ float2 pair(float x) { return make_float2(x, x); }
+__device__ __forceinline__ float2 pair_at(const uint32_t* a) { return make_float2(__uint_as_float(a[0]), __uint_as_float(a[1])); }
+
 template <bool F16>
 __device__ __forceinline__ float2 unpack16(uint32_t w) {
   if (F16) return __half22float2(*reinterpret_cast<const __half2*>(&w));
@@ -41,6 +60,8 @@ __device__ __forceinline__ uint32_t pack16x2(float lo, float hi) {
   __nv_bfloat162 h = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<uint32_t*>(&h);
 }
+template <bool F16>
+__device__ __forceinline__ uint32_t pack16x2(float2 x) { return pack16x2<F16>(x.x, x.y); }
 template <bool F16>
 __device__ __forceinline__ void unpack16x8(const uint4& c, float (&x)[8]) {
   const uint32_t w[4] = {c.x, c.y, c.z, c.w};

@@ -6,7 +6,7 @@
 // Chunk form, 128 tokens at a time (i, j tokens of the chunk, G = cumsum(log2 g)):
 //
 //   P_ij = scale 2^(G_i - G_j) (q_i . k_j)   for j <= i, else 0
-//   O    = diag(2^G) Q (scale S)^T + P V
+//   O    = scale diag(2^G) Q S^T + P V
 //   S   <- 2^(G_last) S + V_d^T K,           V_d = diag(2^(G_last - G)) V
 //
 // Four products of 128 x 128 x 128 on tcgen05 (the last one two or three times, see
@@ -30,7 +30,7 @@
 // happens in registers, so the chain from chunk to chunk is a read-out, 64 FMAs a thread
 // and a 16-bit copy, next to products that do not depend on it.
 //
-// Precision: P and the copy of scale S are rounded to the 16-bit type of q, k, v (as the
+// Precision: P and the copy of S are rounded to the 16-bit type of q, k, v (as the
 // output is); everything else that is summed is f32.  V_d would put its rounding straight
 // into the state, so it enters as the sum of 16-bit terms, each the rounding of what is
 // left: two (16 bits bf16, 22 bits f16), or three for bf16 inputs unless the state leaves
@@ -60,7 +60,7 @@ static_assert(C == 128 && D == 128, "the layouts below are those of 128 x 128 ti
 constexpr uint32_t kTile = C * D * 2;       // a 16-bit tile: two 128B-swizzled halves of 64 columns
 constexpr uint32_t kHalf = kTile / 2;
 constexpr uint32_t kStage = 3 * kTile;      // Q (later the output tile), K, V
-constexpr uint32_t kOffS = 2 * kStage;      // 16-bit copy of scale S
+constexpr uint32_t kOffS = 2 * kStage;      // 16-bit copy of S
 constexpr uint32_t kOffSmall = kOffS + kTile;
 constexpr int kRecs = 4;
 
@@ -221,6 +221,7 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
   const uint32_t id_kk = idesc_16_f32(F16, 128, 128, 0, 0, 0);  // both operands K-major
   const uint32_t id_kmn = idesc_16_f32(F16, 128, 128, 0, 1, 0); // B MN-major (its rows are summed over)
   const uint64_t d_s = sdesc_sw128(smem_u32(base + kOffS), 16, 1024);
+  const bool leader = elect_one();
   bool failed = false;
   Rec r;
   int ci = 0, vi = 0;
@@ -236,7 +237,7 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
       // issued before: the products run in order.
       if (!(wait(sm, &sm->k_full[s], ph) && wait(sm, &sm->q_full[s], ph))) { failed = true; break; }
       tc_fence_after();
-      if (lane == 0) {
+      if (leader) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const uint32_t o = ((i >> 2) * kHalf + (i & 3) * 32) / 16;
@@ -245,10 +246,10 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
         mma_commit(&sm->qk_done);
       }
       __syncwarp();
-      // Q (scale S)^T
+      // Q S^T
       if (!(wait(sm, &sm->sb_ready, one) && (ci == 0 || wait(sm, &sm->o_free, one ^ 1)))) { failed = true; break; }
       tc_fence_after();
-      if (lane == 0) {
+      if (leader) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
           const uint32_t o = ((i >> 2) * kHalf + (i & 3) * 32) / 16;
@@ -262,7 +263,7 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
       for (int b = 0; b < kSubs && !failed; ++b, ++vi) {
         if (!wait(sm, &sm->vd_full[vi & 1], (vi >> 1) & 1)) { failed = true; break; }
         tc_fence_after();
-        if (lane == 0) {
+        if (leader) {
 #pragma unroll
           for (int t = 0; t < kTerms; ++t)
 #pragma unroll
@@ -278,7 +279,7 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
       // + P V
       if (!wait(sm, &sm->p_ready, one)) { failed = true; break; }
       tc_fence_after();
-      if (lane == 0) {
+      if (leader) {
 #pragma unroll
         for (int i = 0; i < 8; ++i) mma_ts(tmem + kTmO, tmem + kTmAcc + i * 8, d_vt + i * 128, id_kmn, 1);
         mma_commit(&sm->o_done);
@@ -289,7 +290,7 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
     if (failed) break;
   }
   if (failed && lane == 0) give_up(p, sm);
-  if (lane == 0) mma_commit(&sm->drain);
+  if (leader) mma_commit(&sm->drain);
   __syncwarp();
   mbar_wait(&sm->drain, 0, kWaitNs);  // no product is under way when TMEM is freed
 }
@@ -299,17 +300,28 @@ __device__ __forceinline__ void run_gates(const DecayPrefillParams& p, Small* sm
   bool failed = false;
   Rec r;
   int ci = 0;
+  // this lane's four gates of chunk c (1 past the end): the loads of a dtype go out together,
+  // and a chunk ahead of their use
+  auto load4 = [&](int c, float (&g)[4]) {
+    const int64_t at = ((int64_t)r.t0 + c * C + 4 * lane) * p.g_st + (int64_t)r.h * p.g_sh;
+    const int left = r.len - c * C - 4 * lane;
+    auto each = [&](auto conv) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) g[e] = e < left ? conv(at + e * p.g_st) : 1.f;
+    };
+    if (p.g_dtype == kF32) each([&](int64_t i) { return reinterpret_cast<const float*>(p.g)[i]; });
+    else if (p.g_dtype == kBF16) each([&](int64_t i) { return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p.g)[i]); });
+    else each([&](int64_t i) { return __half2float(reinterpret_cast<const __half*>(p.g)[i]); });
+  };
   for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
+    float ahead[4] = {1.f, 1.f, 1.f, 1.f};
+    if (p.g && r.nch > 0) load4(0, ahead);
     for (int c = 0; c < r.nch; ++c, ++ci) {
       const int b = ci & 1, left = r.len - c * C;
       float lg[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int j = 4 * lane + e;
-        lg[e] = 0.f;
-        if (p.g && j < left)
-          lg[e] = log2f(gate_at(p.g, p.g_dtype, ((int64_t)r.t0 + c * C + j) * p.g_st + (int64_t)r.h * p.g_sh));
-      }
+      for (int e = 0; e < 4; ++e) lg[e] = log2f(fminf(fmaxf(ahead[e], FLT_MIN), 1.f));
+      if (p.g && c + 1 < r.nch) load4(c + 1, ahead);
       // prefix and suffix sums: the suffix is summed on its own, since G_last - G_j would
       // carry the rounding of two large sums into the state
       float pre[4], suf[4];
@@ -397,49 +409,50 @@ __device__ __forceinline__ void run_po(const DecayPrefillParams& p, uint8_t* bas
       const float gi = sm->G[b][row];
       // P: blocks of 32 columns before this warp's diagonal block by factors, that block pair by pair,
       // zeros behind it.  The packed pairs go over columns that this thread has read already.
-      for (int jb = 0; jb < 4; ++jb) {
-        uint32_t pk[16];
-        if (jb > w) {
+      uint32_t a[32], pk[16];
+#pragma unroll 1
+      for (int jb = 0; jb < w; ++jb) {
+        tmem_ld32(tr + kTmAcc + 32 * jb, a);
+        const float2 rf = pair(p.scale * exp2_fast(gi - sm->G[b][32 * jb + 31]));
+        tmem_ld_wait();
 #pragma unroll
-          for (int e = 0; e < 16; ++e) pk[e] = 0u;
-        } else {
-          uint32_t a[32];
-          tmem_ld32(tr + kTmAcc + 32 * jb, a);
-          tmem_ld_wait();
-          if (jb < w) {
-            const float rf = p.scale * exp2_fast(gi - sm->G[b][32 * jb + 31]);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float4 f = *reinterpret_cast<const float4*>(&sm->cf[32 * jb + 4 * e]);
-              pk[2 * e] = pack16x2<F16>(__uint_as_float(a[4 * e]) * (f.x * rf), __uint_as_float(a[4 * e + 1]) * (f.y * rf));
-              pk[2 * e + 1] = pack16x2<F16>(__uint_as_float(a[4 * e + 2]) * (f.z * rf), __uint_as_float(a[4 * e + 3]) * (f.w * rf));
-            }
-          } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const float4 f = *reinterpret_cast<const float4*>(&sm->G[b][32 * jb + 4 * e]);
-              const float x0 = __uint_as_float(a[4 * e]) * (p.scale * exp2_fast(gi - f.x));
-              const float x1 = __uint_as_float(a[4 * e + 1]) * (p.scale * exp2_fast(gi - f.y));
-              const float x2 = __uint_as_float(a[4 * e + 2]) * (p.scale * exp2_fast(gi - f.z));
-              const float x3 = __uint_as_float(a[4 * e + 3]) * (p.scale * exp2_fast(gi - f.w));
-              pk[2 * e] = pack16x2<F16>(4 * e <= lane ? x0 : 0.f, 4 * e + 1 <= lane ? x1 : 0.f);
-              pk[2 * e + 1] = pack16x2<F16>(4 * e + 2 <= lane ? x2 : 0.f, 4 * e + 3 <= lane ? x3 : 0.f);
-            }
-          }
+        for (int e = 0; e < 8; ++e) {
+          const float4 f = *reinterpret_cast<const float4*>(&sm->cf[32 * jb + 4 * e]);
+          pk[2 * e] = pack16x2<F16>(mul2(pair_at(a + 4 * e), mul2(make_float2(f.x, f.y), rf)));
+          pk[2 * e + 1] = pack16x2<F16>(mul2(pair_at(a + 4 * e + 2), mul2(make_float2(f.z, f.w), rf)));
         }
         tmem_st16(tr + kTmAcc + 16 * jb, pk);
       }
+      tmem_ld32(tr + kTmAcc + 32 * w, a);
+      tmem_ld_wait();
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float4 f = *reinterpret_cast<const float4*>(&sm->G[b][32 * w + 4 * e]);
+        const float2 x = mul2(mul2(pair_at(a + 4 * e), pair(p.scale)), make_float2(exp2_fast(gi - f.x), exp2_fast(gi - f.y)));
+        const float2 y = mul2(mul2(pair_at(a + 4 * e + 2), pair(p.scale)), make_float2(exp2_fast(gi - f.z), exp2_fast(gi - f.w)));
+        pk[2 * e] = pack16x2<F16>(4 * e <= lane ? x.x : 0.f, 4 * e + 1 <= lane ? x.y : 0.f);
+        pk[2 * e + 1] = pack16x2<F16>(4 * e + 2 <= lane ? y.x : 0.f, 4 * e + 3 <= lane ? y.y : 0.f);
+      }
+      tmem_st16(tr + kTmAcc + 16 * w, pk);
+#pragma unroll
+      for (int e = 0; e < 16; ++e) pk[e] = 0u;
+#pragma unroll 1
+      for (int jb = w + 1; jb < 4; ++jb) tmem_st16(tr + kTmAcc + 16 * jb, pk);
       warp_arrive(&sm->cf_empty, lane);
-      // Q (scale S)^T of the row times 2^G_i
+      // Q S^T of the row times scale 2^G_i
       if (!wait(sm, &sm->qs_done, one)) { failed = true; break; }
       tc_fence_after();
-      const float gam = exp2f(gi);
+      const float2 gam = pair(p.scale * exp2f(gi));
+#pragma unroll 1
       for (int q = 0; q < 4; ++q) {
-        uint32_t a[32];
         tmem_ld32(tr + kTmO + 32 * q, a);
         tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 32; ++e) a[e] = __float_as_uint(gam * __uint_as_float(a[e]));
+        for (int e = 0; e < 32; e += 2) {
+          const float2 x = mul2(pair_at(a + e), gam);
+          a[e] = __float_as_uint(x.x);
+          a[e + 1] = __float_as_uint(x.y);
+        }
         tmem_st32(tr + kTmO + 32 * q, a);
       }
       tmem_st_wait();
@@ -450,9 +463,8 @@ __device__ __forceinline__ void run_po(const DecayPrefillParams& p, uint8_t* bas
       if (!wait(sm, &sm->o_done, one)) { failed = true; break; }
       tc_fence_after();
       uint8_t* tile = base + s * kStage;
-#pragma unroll
+#pragma unroll 1
       for (int q = 0; q < 4; ++q) {
-        uint32_t a[32];
         tmem_ld32(tr + kTmO + 32 * q, a);
         tmem_ld_wait();
         if (q == 3) {
@@ -460,12 +472,10 @@ __device__ __forceinline__ void run_po(const DecayPrefillParams& p, uint8_t* bas
           warp_arrive(&sm->o_free, lane);
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float x[8];
-#pragma unroll
-          for (int f = 0; f < 8; ++f) x[f] = __uint_as_float(a[8 * e + f]);
-          *reinterpret_cast<uint4*>(tile + (q >> 1) * kHalf + sw128_chunk(row, 4 * (q & 1) + e)) = pack16x8<F16>(x);
-        }
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<uint4*>(tile + (q >> 1) * kHalf + sw128_chunk(row, 4 * (q & 1) + e)) =
+              make_uint4(pack16x2<F16>(pair_at(a + 8 * e)), pack16x2<F16>(pair_at(a + 8 * e + 2)),
+                         pack16x2<F16>(pair_at(a + 8 * e + 4)), pack16x2<F16>(pair_at(a + 8 * e + 6)));
       }
       fence_proxy_async_smem();
       warp_arrive(&sm->o_staged[s], lane);
@@ -476,33 +486,41 @@ __device__ __forceinline__ void run_po(const DecayPrefillParams& p, uint8_t* bas
 }
 
 // ------------------------------------------------------------ warps 8-15: the state
-// 64 values (columns c0 ..) of a state row.
-__device__ __forceinline__ void load_state64(const void* base, int dtype, int64_t off, float (&s)[64]) {
+// 64 values of a state row, as pairs.
+__device__ __forceinline__ void load_state64(const void* base, int dtype, int64_t off, float2 (&s)[32]) {
   if (dtype == kF32) {
-    const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(base) + off);
+    const float4* q = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + off);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) StateType<0>::unpack(q[i], reinterpret_cast<float(&)[4]>(s[4 * i]));
+    for (int i = 0; i < 16; ++i) {
+      const float4 x = q[i];
+      s[2 * i] = make_float2(x.x, x.y);
+      s[2 * i + 1] = make_float2(x.z, x.w);
+    }
   } else {
     const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(base) + off);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const uint4 x = q[i];
-      if (dtype == kF16) StateType<2>::unpack(x, reinterpret_cast<float(&)[8]>(s[8 * i]));
-      else StateType<1>::unpack(x, reinterpret_cast<float(&)[8]>(s[8 * i]));
+      const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int e = 0; e < 4; ++e) s[4 * i + e] = dtype == kF16 ? unpack16<true>(w[e]) : unpack16<false>(w[e]);
     }
   }
 }
-__device__ __forceinline__ void store_state64(void* base, int dtype, int64_t off, const float (&s)[64]) {
+__device__ __forceinline__ void store_state64(void* base, int dtype, int64_t off, const float2 (&s)[32]) {
   if (dtype == kF32) {
-    uint4* q = reinterpret_cast<uint4*>(reinterpret_cast<float*>(base) + off);
+    float4* q = reinterpret_cast<float4*>(reinterpret_cast<float*>(base) + off);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) q[i] = StateType<0>::pack(reinterpret_cast<const float(&)[4]>(s[4 * i]));
+    for (int i = 0; i < 16; ++i) q[i] = make_float4(s[2 * i].x, s[2 * i].y, s[2 * i + 1].x, s[2 * i + 1].y);
   } else {
     uint4* q = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(base) + off);
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-      q[i] = dtype == kF16 ? StateType<2>::pack(reinterpret_cast<const float(&)[8]>(s[8 * i]))
-                           : StateType<1>::pack(reinterpret_cast<const float(&)[8]>(s[8 * i]));
+    for (int i = 0; i < 8; ++i) {
+      uint32_t w[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) w[e] = dtype == kF16 ? pack16x2<true>(s[4 * i + e]) : pack16x2<false>(s[4 * i + e]);
+      q[i] = make_uint4(w[0], w[1], w[2], w[3]);
+    }
   }
 }
 
@@ -533,20 +551,56 @@ __device__ __forceinline__ void run_ks(const DecayPrefillParams& p, uint8_t* bas
   uint8_t* sb = base + kOffS + hf * kHalf;
   bool failed = false;
   Rec r;
-  int ci = 0, vi = 0;
-  float s[64];
-  // the 16-bit copy of scale S for the chunk ci, once Q S^T of the chunk before has read the last one
+  int ci = 0;
+  float2 s[32];
+  // the 16-bit copy of S for chunk `at`, once Q S^T of the chunk before has read the last one
   auto copy_state = [&](int at) {
     if (at > 0 && !wait(sm, &sm->qs_done, (at - 1) & 1)) return false;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      float x[8];
-#pragma unroll
-      for (int f = 0; f < 8; ++f) x[f] = p.scale * s[8 * e + f];
-      *reinterpret_cast<uint4*>(sb + sw128_chunk(row, e)) = pack16x8<F16>(x);
-    }
+    for (int e = 0; e < 8; ++e)
+      *reinterpret_cast<uint4*>(sb + sw128_chunk(row, e)) =
+          make_uint4(pack16x2<F16>(s[4 * e]), pack16x2<F16>(s[4 * e + 1]), pack16x2<F16>(s[4 * e + 2]), pack16x2<F16>(s[4 * e + 3]));
     fence_proxy_async_smem();
     warp_arrive(&sm->sb_ready, lane);
+    return true;
+  };
+  // V_d of tokens [sub * kSub, + kSub) of chunk `at`: transposed fragments of V (pairs of tokens,
+  // one value each) times d, as kTerms 16-bit terms
+  const int m = lane >> 3, lr = lane & 7;
+  auto make_vd = [&](int at, int sub) {
+    const int vi = at * kSubs + sub, slot = vi & 1;
+    if (vi >= 2 && !wait(sm, &sm->vd_empty[slot], ((vi >> 1) - 1) & 1)) return false;
+    tc_fence_after();
+    const uint32_t va = smem_u32(base + (at & 1) * kStage + 2 * kTile);
+    const float* dv = sm->d[at & 1];
+#pragma unroll
+    for (int tt = 0; tt < kSub / 32; ++tt) {
+      const int tok = sub * kSub + hf * (kSub / 2) + 16 * tt;  // 16 tokens from here
+      const float2 d0 = *reinterpret_cast<const float2*>(&dv[tok + 2 * (lane & 3)]);
+      const float2 d1 = *reinterpret_cast<const float2*>(&dv[tok + 8 + 2 * (lane & 3)]);
+      const int trow = tok + (m >> 1) * 8 + lr;
+#pragma unroll
+      for (int dd = 0; dd < 2; ++dd) {
+        const int ch = 4 * w + 2 * dd + (m & 1);
+        uint32_t a[4], t[4];
+        ldmatrix_x4_trans(va + (ch >> 3) * kHalf + sw128_chunk(trow, ch & 7), a);
+        float2 x[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) x[e] = mul2(unpack16<F16>(a[e]), e < 2 ? d0 : d1);
+#pragma unroll
+        for (int term = 0; term < kTerms; ++term) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            t[e] = pack16x2<F16>(x[e]);
+            if (term + 1 < kTerms) x[e] = fma2(unpack16<F16>(t[e]), pair(-1.f), x[e]);
+          }
+          tmem_st16x128_x2(tq + ((uint32_t)(16 * dd) << 16) + kTmVd + slot * 64 + term * (kSub / 2) + hf * (kSub / 4) + 8 * tt, t);
+        }
+      }
+    }
+    tmem_st_wait();
+    tc_fence_before();
+    warp_arrive(&sm->vd_full[slot], lane);
     return true;
   };
   for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
@@ -554,67 +608,32 @@ __device__ __forceinline__ void run_ks(const DecayPrefillParams& p, uint8_t* bas
       load_state64(p.s_in, p.sin_dtype, r.slot * p.sin_slot + (int64_t)r.h * p.sin_head + row * D + 64 * hf, s);
     } else {
 #pragma unroll
-      for (int e = 0; e < 64; ++e) s[e] = 0.f;
+      for (int e = 0; e < 32; ++e) s[e] = pair(0.f);
     }
     if (r.nch > 0 && !copy_state(ci)) { failed = true; break; }
-    for (int c = 0; c < r.nch; ++c, ++ci) {
-      const int b = ci & 1, st = ci & 1, left = r.len - c * C;
-      uint8_t* k = base + st * kStage + kTile;
-      uint8_t* v = k + kTile;
-      if (!(wait(sm, &sm->gate_full[b], (ci >> 1) & 1) && wait(sm, &sm->v_full[st], (ci >> 1) & 1))) { failed = true; break; }
-      if (left < C) {
-        if (!wait(sm, &sm->k_full[st], (ci >> 1) & 1)) { failed = true; break; }
-        zero_tails<kTerms>(k, v, left, w, hf, lane);
-      }
-      // V_d: transposed fragments of V (pairs of tokens, one value each) times d, as kTerms 16-bit terms
-      const uint32_t va = smem_u32(v);
-      const int m = lane >> 3, lr = lane & 7;
-      for (int sub = 0; sub < kSubs; ++sub, ++vi) {
-        if (vi >= 2 && !wait(sm, &sm->vd_empty[vi & 1], ((vi >> 1) - 1) & 1)) { failed = true; break; }
-        tc_fence_after();
-#pragma unroll
-        for (int tt = 0; tt < kSub / 32; ++tt) {
-          const int tok = sub * kSub + hf * (kSub / 2) + 16 * tt;  // 16 tokens from here
-          const float2 d0 = *reinterpret_cast<const float2*>(&sm->d[b][tok + 2 * (lane & 3)]);
-          const float2 d1 = *reinterpret_cast<const float2*>(&sm->d[b][tok + 8 + 2 * (lane & 3)]);
-          const int trow = tok + (m >> 1) * 8 + lr;
-#pragma unroll
-          for (int dd = 0; dd < 2; ++dd) {
-            const int ch = 4 * w + 2 * dd + (m & 1);
-            uint32_t a[4], t[4];
-            ldmatrix_x4_trans(va + (ch >> 3) * kHalf + sw128_chunk(trow, ch & 7), a);
-            float x[8];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              const float2 f = unpack16<F16>(a[e]);
-              const float2 dj = e < 2 ? d0 : d1;
-              x[2 * e] = f.x * dj.x;
-              x[2 * e + 1] = f.y * dj.y;
-            }
-#pragma unroll
-            for (int term = 0; term < kTerms; ++term) {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                t[e] = pack16x2<F16>(x[2 * e], x[2 * e + 1]);
-                if (term + 1 < kTerms) {
-                  const float2 f = unpack16<F16>(t[e]);
-                  x[2 * e] -= f.x;
-                  x[2 * e + 1] -= f.y;
-                }
-              }
-              tmem_st16x128_x2(tq + ((uint32_t)(16 * dd) << 16) + kTmVd + (vi & 1) * 64 + term * (kSub / 2) +
-                                   hf * (kSub / 4) + 8 * tt, t);
-            }
+    // Step j makes V_d part j % kSubs of chunk j / kSubs.  The first part of a chunk is made
+    // before the state of the chunk before is complete: it does not need it.
+#pragma unroll 1
+    for (int j = 0; j <= r.nch * kSubs; ++j) {
+      const int c = j / kSubs, sub = j % kSubs;
+      if (c < r.nch) {
+        if (sub == 0) {
+          const int st = (ci + c) & 1, left = r.len - c * C;
+          const uint32_t ph = ((ci + c) >> 1) & 1;
+          if (!(wait(sm, &sm->gate_full[st], ph) && wait(sm, &sm->v_full[st], ph))) { failed = true; break; }
+          if (left < C) {
+            if (!wait(sm, &sm->k_full[st], ph)) { failed = true; break; }
+            uint8_t* k = base + st * kStage + kTile;
+            zero_tails<kTerms>(k, k + kTile, left, w, hf, lane);
           }
         }
-        tmem_st_wait();
-        tc_fence_before();
-        warp_arrive(&sm->vd_full[vi & 1], lane);
+        if (!make_vd(ci + c, sub)) { failed = true; break; }
       }
-      if (failed) break;
-      // S <- gamma S + V_d^T K
-      const float gam = sm->gamma[b];
-      if (!wait(sm, &sm->ds_done, ci & 1)) { failed = true; break; }
+      if (sub != 0 || c == 0) continue;
+      // S <- gamma S + V_d^T K of chunk c - 1
+      const int at = ci + c - 1;
+      const float2 gam = pair(sm->gamma[at & 1]);
+      if (!wait(sm, &sm->ds_done, at & 1)) { failed = true; break; }
       tc_fence_after();
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -626,12 +645,13 @@ __device__ __forceinline__ void run_ks(const DecayPrefillParams& p, uint8_t* bas
           warp_arrive(&sm->ds_free, lane);
         }
 #pragma unroll
-        for (int e = 0; e < 16; ++e) s[16 * q + e] = fmaf(gam, s[16 * q + e], __uint_as_float(a[e]));
+        for (int e = 0; e < 8; ++e) s[8 * q + e] = fma2(s[8 * q + e], gam, pair_at(a + 2 * e));
       }
-      if (lane == 0) mbar_arrive(&sm->gate_empty[b]);
-      if (c + 1 < r.nch && !copy_state(ci + 1)) { failed = true; break; }
+      if (lane == 0) mbar_arrive(&sm->gate_empty[at & 1]);
+      if (c < r.nch && !copy_state(at + 1)) { failed = true; break; }
     }
     if (failed) break;
+    ci += r.nch;
     if (p.s_out) store_state64(p.s_out, p.sout_dtype, r.slot * p.sout_slot + (int64_t)r.h * p.sout_head + row * D + 64 * hf, s);
   }
   if (failed && lane == 0) give_up(p, sm);

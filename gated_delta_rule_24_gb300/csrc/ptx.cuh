@@ -247,6 +247,14 @@ GDN_DEV void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc, uint32_t 
       "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n}\n" ::"r"(d_tmem),
       "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate));
 }
+// One lane of a converged warp.  A branch on it, unlike one on the lane number, is known
+// to the compiler to leave a single thread, and back-to-back MMAs issue faster behind it
+// (8 of M = N = 128 with A in TMEM: 592 cycles instead of 758).
+GDN_DEV bool elect_one() {
+  uint32_t r;
+  asm volatile("{\n.reg .pred p;\nelect.sync _|p, 0xffffffff;\nselp.u32 %0, 1, 0, p;\n}\n" : "=r"(r));
+  return r != 0;
+}
 // Arrive once on `bar` when every MMA this thread issued before has completed.
 GDN_DEV void mma_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(

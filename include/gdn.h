@@ -307,7 +307,7 @@ gdn_status_t gdn_qk_norm_rope(const gdn_tensor_t* q, const gdn_tensor_t* k, cons
  * same names (there is no beta and no norm).  g with a token stride of 0 is one decay for
  * each head.  An infinity or NaN in a token's q, k or v can reach the other outputs of its
  * sequence and head, never those of another sequence.  With f16 inputs the state
- * enters the read-out as scale * S in f16, so values beyond 65504 overflow there.
+ * enters the read-out in f16, so values beyond 65504 overflow there.
  *  batch_invariant  nonzero: never split a sequence, so every output and state bit depends
  *                   only on that sequence's own inputs.
  */
