@@ -13,16 +13,16 @@
 // below) against 128 KB of q, k, v and o: the bytes bound it once the products of one chunk
 // run without a pause, and that is what the layout is for.
 //
-// One persistent CTA per SM walks (sequence, head) units chunk by chunk.  Roles (16 warps):
+// One persistent CTA per SM walks (sequence, head) units chunk by chunk.  Roles (20 warps):
 //   warp 0      TMA loads of Q, K, V (two stages) and the unit records;
 //   warp 1      issues every product: Q K^T, Q S^T, V_d^T K, P V of a chunk in this order,
 //               so that P is built while Q S^T and V_d^T K run, and the state is read out
 //               and V_d of the next chunk built while P V and the next Q K^T run;
 //   warp 2      the gates: prefix and suffix sums of log2 g, one chunk ahead;
 //   warp 3      stores of the output tile;
-//   warps 4-7   one thread a token: P (tcgen05.ld, decay, mask, back to TMEM as the A operand
+//   warps 4-11  two threads a token: P (tcgen05.ld, decay, mask, back to TMEM as the A operand
 //               of P V), the 2^G_i of Q S^T in place, and the output tile;
-//   warps 8-15  two threads a value row: the state in registers (f32, 64 values a thread),
+//   warps 12-19 two threads a value row: the state in registers (f32, 64 values a thread),
 //               its 16-bit copy in shared memory for Q S^T, and V_d.
 // Hand-offs are mbarriers, every wait is bounded and ends early when any role gave up.
 //
@@ -36,9 +36,11 @@
 // left: two (16 bits bf16, 22 bits f16), or three for bf16 inputs unless the state leaves
 // the call in 16 bits; an f32 state then is as exact as f32 sums are.
 //
-// 2^(G_i - G_j) within blocks of 32 tokens is computed for each pair; between blocks it is
-// the product 2^(G_i - G_e) 2^(G_e - G_j) with e the last token of j's block, both at most
-// 1, so that it costs a row factor and a column factor and cannot overflow.
+// 2^(G_i - G_j) is the product 2^(G_i - G_e) 2^(G_e - G_j) with e the last token of j's block
+// of 16: a row factor for each block and a column factor.  Both are at most 1 where the block
+// ends before i; in i's own block the first is not, and where a block decays by more than
+// 2^-100 (an f32 product could under- or overflow) the pairs near the diagonal are
+// computed one by one.
 //
 // Rows past the end of a sequence hold the next one's tokens (or TMA's zeros).  They are
 // masked where they are a row or a column of P, and zeroed in shared memory where they are
@@ -59,9 +61,10 @@ static_assert(C == 128 && D == 128, "the layouts below are those of 128 x 128 ti
 // ------------------------------------------------------------ shared memory (bytes)
 constexpr uint32_t kTile = C * D * 2;       // a 16-bit tile: two 128B-swizzled halves of 64 columns
 constexpr uint32_t kHalf = kTile / 2;
-constexpr uint32_t kStage = 3 * kTile;      // Q (later the output tile), K, V
-constexpr uint32_t kOffS = 2 * kStage;      // 16-bit copy of S
-constexpr uint32_t kOffSmall = kOffS + kTile;
+constexpr uint32_t kOffKv = kTile;           // after Q: two stages of K, V
+constexpr uint32_t kOffS = kOffKv + 4 * kTile;  // 16-bit copy of S
+constexpr uint32_t kOffO = kOffS + kTile;    // the output tile on its way out
+constexpr uint32_t kOffSmall = kOffO + kTile;
 constexpr int kRecs = 4;
 
 struct Rec {       // one unit: a sequence of one head
@@ -70,17 +73,20 @@ struct Rec {       // one unit: a sequence of one head
 };
 struct Small {
   float G[2][C];   // inclusive prefix sums of log2 g
-  float d[2][C];   // 2^(sum of the log2 g behind the token), 0 past the end
-  float cf[C];     // 2^(G_e - G_j), e the last token of j's block of 32
+  float d[2][C];   // 2^(sum of the log2 g behind the token), 0 past the end; with two V_d terms
+                   // as 16-bit halves, C high ones and C low ones
+  float cf[C];     // 2^(G_e - G_j), e the last token of j's block of 16
+  int32_t mild[2]; // no block of 16 tokens decays by more than 2^-100
   float gamma[2];  // 2^(G_last)
   Rec rec[kRecs];
-  uint64_t q_full[2], k_full[2], v_full[2], kv_empty[2], q_empty[2];
+  uint64_t q_full, q_empty, k_full[2], v_full[2], kv_empty[2];
   uint64_t rec_full[kRecs], rec_empty[kRecs];
   uint64_t gate_full[2], gate_empty[2], cf_empty;
-  uint64_t qk_done, qs_done, ds_done, o_done;  // products that have completed
-  uint64_t p_ready, o_free, o_staged[2];       // warps 4-7
-  uint64_t sb_ready, ds_free, vd_full[2];      // warps 8-15
-  uint64_t vd_empty[2], drain;
+  uint64_t qk_done, qs_done, s_done, o_done;   // products that have completed
+  uint64_t q_ready, acc_read[2], p_ready, o_free, o_staged;  // warps 4-11
+  uint64_t o_stored;                            // warp 3
+  uint64_t s_ready, vd_full[4];                // warps 12-19
+  uint64_t vd_empty[4], drain;
   uint32_t tmem;
   int32_t abort;
 };
@@ -88,28 +94,39 @@ constexpr uint32_t kSmem = kOffSmall + sizeof(Small);
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
 
 // ------------------------------------------------------------ TMEM (columns)
-constexpr uint32_t kTmAcc = 0;     // Q K^T (128), then P as packed pairs in the first 64
+constexpr uint32_t kTmAcc = 0;     // Q K^T (128), then P as packed pairs
 constexpr uint32_t kTmO = 128;     // Q S^T, then the output
-constexpr uint32_t kTmDs = 256;    // V_d^T K
-constexpr uint32_t kTmVd = 384;    // V_d terms as packed pairs, two slots of 64
+constexpr uint32_t kTmS = 256;     // S, f32 (128)
+constexpr uint32_t kTmQ = 384;     // Q as packed pairs (64)
+// P takes 16 columns for a block of 32 tokens: the first two blocks in front, the last two behind, so
+// that the columns between come free as the scores are read, the upper 32 first.
+__device__ __forceinline__ uint32_t p_block_col(int jb) { return kTmAcc + 16 * jb + (jb >= 2 ? 64 : 0); }
+// V_d terms as packed pairs, in four slots of 32: two of their own, two in those columns.
+constexpr uint32_t kTmVd = 448;
+__device__ __forceinline__ uint32_t vd_slot_col(int slot) { return slot < 2 ? kTmVd + 32 * slot : kTmAcc + 64 - 32 * (slot - 2); }
 constexpr uint32_t kTmCols = 512;
 
-constexpr int kThreads = 512;
-constexpr int kPoWarps = 4, kKsWarps = 8;
+constexpr int kThreads = 640;
+constexpr int kPoWarps = 8, kKsWarps = 8;
 constexpr int kReaders = 3 + kPoWarps + kKsWarps;  // warps that read a unit's record
-constexpr uint64_t kWaitNs = 200ull * 1000 * 1000;
+static_assert(kThreads == 32 * (4 + kPoWarps + kKsWarps), "roles");
 
-// Every wait: bounded, and over as soon as another role has given up.
-__device__ __noinline__ bool wait_slow(Small* sm, uint64_t* bar, uint32_t parity) {
-  const uint64_t t0 = global_timer_ns();
-  while (!mbar_try_wait_sleep(bar, parity, 20000u)) {
-    if (*reinterpret_cast<volatile int32_t*>(&sm->abort) || global_timer_ns() - t0 > kWaitNs) return false;
-  }
-  return true;
-}
+// Every wait: bounded (kTries probes of up to 20 us each), and over as soon as another role has
+// given up.
+constexpr int kTries = 50000;
+__device__ __forceinline__ bool probe(uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)); }
 __device__ __forceinline__ bool wait(Small* sm, uint64_t* bar, uint32_t parity) {
-  const bool ok = mbar_try_wait(bar, parity) || wait_slow(sm, bar, parity);
+  if (probe(bar, parity)) return true;
+  bool ok = false;
+#pragma unroll 1
+  for (int i = 0; i < kTries && !ok && !*reinterpret_cast<volatile int32_t*>(&sm->abort); ++i)
+    ok = mbar_try_wait_sleep(bar, parity, 20000u);
   return __all_sync(0xffffffffu, ok);
+}
+// The same for copies and products under way when a CTA ends, whoever gave up.
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
+#pragma unroll 1
+  for (int i = 0; i < kTries && !mbar_try_wait_sleep(bar, parity, 20000u); ++i) {}
 }
 __device__ __forceinline__ void give_up(const DecayPrefillParams& p, Small* sm) {
   *reinterpret_cast<volatile int32_t*>(&sm->abort) = 1;
@@ -177,23 +194,23 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
     const int hq = h / (p.H / p.H_qk), hv = h / (p.H / p.H_v);
     for (int c = 0; c < nch; ++c, ++ci) {
       const int s = ci & 1, t0 = (int)bos + c * C;
-      uint8_t* q = base + s * kStage;
       auto load = [&](uint8_t* dst, const CUtensorMap* tm, uint64_t* bar, int head) {
         mbar_arrive_expect_tx(bar, kTile);
         tma_load_3d(dst, tm, bar, 0, head, t0);
         tma_load_3d(dst + kHalf, tm, bar, 64, head, t0);
       };
+      ok = ci < 1 || wait(sm, &sm->q_empty, (ci - 1) & 1);
+      if (!ok) break;
+      if (lane == 0) load(base, &p.tm_q, &sm->q_full, hq);
+      ++q_loads;
       ok = ci < 2 || wait(sm, &sm->kv_empty[s], ((ci >> 1) - 1) & 1);
       if (!ok) break;
       if (lane == 0) {
-        load(q + kTile, &p.tm_k, &sm->k_full[s], hq);
-        load(q + 2 * kTile, &p.tm_v, &sm->v_full[s], hv);
+        uint8_t* k = base + kOffKv + s * 2 * kTile;
+        load(k, &p.tm_k, &sm->k_full[s], hq);
+        load(k + kTile, &p.tm_v, &sm->v_full[s], hv);
       }
       ++kv_loads;
-      ok = ci < 2 || wait(sm, &sm->q_empty[s], ((ci >> 1) - 1) & 1);
-      if (!ok) break;
-      if (lane == 0) load(q, &p.tm_q, &sm->q_full[s], hq);
-      ++q_loads;
     }
   }
   if (ok) ok = publish(Rec{0, 0, 0, -1, 0});
@@ -202,76 +219,81 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
   auto landed = [&](uint64_t (&bar)[2], int loads) {
     for (int s = 0; s < 2; ++s) {
       const int n = (loads + 1 - s) / 2;  // loads of stage s
-      if (n) mbar_wait(&bar[s], (n - 1) & 1, kWaitNs);
+      if (n) drain(&bar[s], (n - 1) & 1);
     }
   };
   landed(sm->k_full, kv_loads);
   landed(sm->v_full, kv_loads);
-  landed(sm->q_full, q_loads);
+  if (q_loads) drain(&sm->q_full, (q_loads - 1) & 1);
 }
 
 // ------------------------------------------------------------ warp 1: products
-// V_d terms: a slot holds kSub tokens, kSub / 2 columns a term.
+// V_d is made in parts of kSub tokens, kSub / 2 columns a term.  Part b goes to slot b % 2 in the
+// first half of the chunk, 2 + b % 2 in the second: each slot is used kSubs / 4 times a chunk.
 template <int kTerms>
-__host__ __device__ constexpr int sub_tokens() { return kTerms == 2 ? 64 : 32; }
+__host__ __device__ constexpr int sub_tokens() { return kTerms == 2 ? 32 : 16; }
+template <int kTerms>
+__device__ __forceinline__ void vd_place(int ci, int b, int* slot, int* round) {
+  constexpr int kSubs = C / sub_tokens<kTerms>();
+  *slot = (b & 1) + (b >= kSubs / 2 ? 2 : 0);
+  *round = ci * (kSubs / 4) + (b % (kSubs / 2)) / 2;  // uses of the slot before
+}
 
 template <bool F16, int kTerms>
 __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* base, Small* sm, uint32_t tmem, int lane) {
   constexpr int kSub = sub_tokens<kTerms>(), kSubs = C / kSub;
-  const uint32_t id_kk = idesc_16_f32(F16, 128, 128, 0, 0, 0);  // both operands K-major
+  const uint32_t id_kk = idesc_16_f32(F16, 128, 128, 0, 0, 0);  // B K-major
   const uint32_t id_kmn = idesc_16_f32(F16, 128, 128, 0, 1, 0); // B MN-major (its rows are summed over)
+  const uint32_t id_kmn_neg = idesc_16_f32(F16, 128, 128, 0, 1, 1);  // the first of two V_d terms is stored negated
   const uint64_t d_s = sdesc_sw128(smem_u32(base + kOffS), 16, 1024);
   const bool leader = elect_one();
   bool failed = false;
   Rec r;
-  int ci = 0, vi = 0;
+  int ci = 0;
   for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
     for (int c = 0; c < r.nch; ++c, ++ci) {
       const int s = ci & 1;
       const uint32_t ph = (ci >> 1) & 1, one = ci & 1;
-      uint8_t* st = base + s * kStage;
-      const uint64_t d_q = sdesc_sw128(smem_u32(st), 16, 1024), d_k = sdesc_sw128(smem_u32(st + kTile), 16, 1024);
-      const uint64_t d_kt = sdesc_sw128(smem_u32(st + kTile), kHalf, 1024);
-      const uint64_t d_vt = sdesc_sw128(smem_u32(st + 2 * kTile), kHalf, 1024);
+      const uint32_t k = smem_u32(base + kOffKv + s * 2 * kTile);
+      const uint64_t d_k = sdesc_sw128(k, 16, 1024), d_kt = sdesc_sw128(k, kHalf, 1024);
+      const uint64_t d_vt = sdesc_sw128(k + kTile, kHalf, 1024);
       // Q K^T.  P of the chunk before is being read by its P V at the latest, which was
       // issued before: the products run in order.
-      if (!(wait(sm, &sm->k_full[s], ph) && wait(sm, &sm->q_full[s], ph))) { failed = true; break; }
+      if (!(wait(sm, &sm->k_full[s], ph) && wait(sm, &sm->q_ready, one))) { failed = true; break; }
       tc_fence_after();
       if (leader) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t o = ((i >> 2) * kHalf + (i & 3) * 32) / 16;
-          mma_ss(tmem + kTmAcc, d_q + o, d_k + o, id_kk, i > 0);
-        }
+        for (int i = 0; i < 8; ++i)
+          mma_ts(tmem + kTmAcc, tmem + kTmQ + i * 8, d_k + ((i >> 2) * kHalf + (i & 3) * 32) / 16, id_kk, i > 0);
         mma_commit(&sm->qk_done);
       }
       __syncwarp();
       // Q S^T
-      if (!(wait(sm, &sm->sb_ready, one) && (ci == 0 || wait(sm, &sm->o_free, one ^ 1)))) { failed = true; break; }
+      if (!(wait(sm, &sm->s_ready, one) && (ci == 0 || wait(sm, &sm->o_free, one ^ 1)))) { failed = true; break; }
       tc_fence_after();
       if (leader) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          const uint32_t o = ((i >> 2) * kHalf + (i & 3) * 32) / 16;
-          mma_ss(tmem + kTmO, d_q + o, d_s + o, id_kk, i > 0);
-        }
+        for (int i = 0; i < 8; ++i)
+          mma_ts(tmem + kTmO, tmem + kTmQ + i * 8, d_s + ((i >> 2) * kHalf + (i & 3) * 32) / 16, id_kk, i > 0);
         mma_commit(&sm->qs_done);
       }
       __syncwarp();
       // V_d^T K
-      if (ci > 0 && !wait(sm, &sm->ds_free, one ^ 1)) { failed = true; break; }
-      for (int b = 0; b < kSubs && !failed; ++b, ++vi) {
-        if (!wait(sm, &sm->vd_full[vi & 1], (vi >> 1) & 1)) { failed = true; break; }
+#pragma unroll
+      for (int b = 0; b < kSubs; ++b) {
+        int slot, round;
+        vd_place<kTerms>(ci, b, &slot, &round);
+        if (!wait(sm, &sm->vd_full[slot], round & 1)) { failed = true; break; }
         tc_fence_after();
         if (leader) {
 #pragma unroll
           for (int t = 0; t < kTerms; ++t)
 #pragma unroll
             for (int i = 0; i < kSub / 16; ++i)
-              mma_ts(tmem + kTmDs, tmem + kTmVd + (vi & 1) * 64 + t * (kSub / 2) + i * 8,
-                     d_kt + (b * (kSub / 16) + i) * 128, id_kmn, b + t + i > 0);
-          mma_commit(&sm->vd_empty[vi & 1]);
-          if (b == kSubs - 1) mma_commit(&sm->ds_done);
+              mma_ts(tmem + kTmS, tmem + vd_slot_col(slot) + t * (kSub / 2) + i * 8, d_kt + (b * (kSub / 16) + i) * 128,
+                     kTerms == 2 && t == 0 ? id_kmn_neg : id_kmn, 1);
+          mma_commit(&sm->vd_empty[slot]);
+          if (b == kSubs - 1) mma_commit(&sm->s_done);
         }
         __syncwarp();
       }
@@ -281,7 +303,8 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
       tc_fence_after();
       if (leader) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) mma_ts(tmem + kTmO, tmem + kTmAcc + i * 8, d_vt + i * 128, id_kmn, 1);
+        for (int i = 0; i < 8; ++i)
+          mma_ts(tmem + kTmO, tmem + p_block_col(i / 2) + (i & 1) * 8, d_vt + i * 128, id_kmn, 1);
         mma_commit(&sm->o_done);
         mma_commit(&sm->kv_empty[s]);
       }
@@ -292,13 +315,14 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
   if (failed && lane == 0) give_up(p, sm);
   if (leader) mma_commit(&sm->drain);
   __syncwarp();
-  mbar_wait(&sm->drain, 0, kWaitNs);  // no product is under way when TMEM is freed
+  drain(&sm->drain, 0);  // no product is under way when TMEM is freed
 }
 
 // ------------------------------------------------------------ warp 2: gates
+template <bool F16, int kTerms>
 __device__ __forceinline__ void run_gates(const DecayPrefillParams& p, Small* sm, int lane) {
   bool failed = false;
-  Rec r;
+  Rec r{};
   int ci = 0;
   // this lane's four gates of chunk c (1 past the end): the loads of a dtype go out together,
   // and a chunk ahead of their use
@@ -340,14 +364,27 @@ __device__ __forceinline__ void run_gates(const DecayPrefillParams& p, Small* sm
       const float total = __shfl_sync(0xffffffffu, down, 0);
 #pragma unroll
       for (int e = 0; e < 4; ++e) { pre[e] += before; suf[e] += behind; }
-      const float g_end = __shfl_sync(0xffffffffu, pre[3], lane | 7);  // the last token of the block of 32
+      const float g_end = __shfl_sync(0xffffffffu, pre[3], lane | 3);  // the last token of the block of 16
+      const float g_begin = __shfl_sync(0xffffffffu, before, lane & ~3);
+      const bool mild = __all_sync(0xffffffffu, g_begin - g_end <= 100.f);
       if (!(ci < 2 || wait(sm, &sm->gate_empty[b], ((ci >> 1) - 1) & 1))) { failed = true; break; }
       *reinterpret_cast<float4*>(&sm->G[b][4 * lane]) = make_float4(pre[0], pre[1], pre[2], pre[3]);
       float d[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) d[e] = 4 * lane + e < left ? exp2f(suf[e]) : 0.f;
-      *reinterpret_cast<float4*>(&sm->d[b][4 * lane]) = make_float4(d[0], d[1], d[2], d[3]);
-      if (lane == 0) sm->gamma[b] = exp2f(total);
+      if (kTerms == 2) {
+        uint32_t* dh = reinterpret_cast<uint32_t*>(sm->d[b]) + 2 * lane;
+        const uint32_t h0 = pack16x2<F16>(d[0], d[1]), h1 = pack16x2<F16>(d[2], d[3]);
+        const float2 f0 = unpack16<F16>(h0), f1 = unpack16<F16>(h1);
+        *reinterpret_cast<uint2*>(dh) = make_uint2(h0, h1);
+        *reinterpret_cast<uint2*>(dh + C / 2) = make_uint2(pack16x2<F16>(d[0] - f0.x, d[1] - f0.y), pack16x2<F16>(d[2] - f1.x, d[3] - f1.y));
+      } else {
+        *reinterpret_cast<float4*>(&sm->d[b][4 * lane]) = make_float4(d[0], d[1], d[2], d[3]);
+      }
+      if (lane == 0) {
+        sm->gamma[b] = exp2f(total);
+        sm->mild[b] = mild;
+      }
       if (!(ci == 0 || wait(sm, &sm->cf_empty, (ci - 1) & 1))) { failed = true; break; }
       *reinterpret_cast<float4*>(&sm->cf[4 * lane]) = make_float4(
           exp2_fast(g_end - pre[0]), exp2_fast(g_end - pre[1]), exp2_fast(g_end - pre[2]), exp2_fast(g_end - pre[3]));
@@ -365,9 +402,9 @@ __device__ __forceinline__ void run_store(const DecayPrefillParams& p, uint8_t* 
   int ci = 0;
   for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
     for (int c = 0; c < r.nch; ++c, ++ci) {
-      const int s = ci & 1, t0 = r.t0 + c * C, left = r.len - c * C;
-      if (!wait(sm, &sm->o_staged[s], (ci >> 1) & 1)) { failed = true; break; }
-      uint8_t* tile = base + s * kStage;
+      const int t0 = r.t0 + c * C, left = r.len - c * C;
+      if (!wait(sm, &sm->o_staged, ci & 1)) { failed = true; break; }
+      uint8_t* tile = base + kOffO;
       if (left >= C) {
         if (lane == 0) {
           tma_store_3d(&p.tm_o, tile, 0, r.h, t0);
@@ -384,7 +421,7 @@ __device__ __forceinline__ void run_store(const DecayPrefillParams& p, uint8_t* 
               *reinterpret_cast<const uint4*>(tile + (ch >> 3) * kHalf + sw128_chunk(row, ch & 7));
         }
       }
-      warp_arrive(&sm->q_empty[s], lane);
+      warp_arrive(&sm->o_stored, lane);
     }
     if (failed) break;
   }
@@ -392,59 +429,100 @@ __device__ __forceinline__ void run_store(const DecayPrefillParams& p, uint8_t* 
   if (lane == 0) bulk_wait_read_all();
 }
 
-// ------------------------------------------------------------ warps 4-7: P and the output
+// ------------------------------------------------------------ warps 4-11: P and the output
 template <bool F16>
 __device__ __forceinline__ void run_po(const DecayPrefillParams& p, uint8_t* base, Small* sm, uint32_t tmem, int warp, int lane) {
-  const int w = warp & 3, row = 32 * w + lane;
+  const int w = warp & 3, hf = (warp >> 2) - 1, row = 32 * w + lane;  // warps 4-11: columns 0 .. 63, 8-11: 64 .. 127
   const uint32_t tr = tmem + ((uint32_t)(32 * w) << 16);
   bool failed = false;
   Rec r;
-  int ci = 0;
-  for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
-    for (int c = 0; c < r.nch; ++c, ++ci) {
-      const int b = ci & 1, s = ci & 1;
+  int u = 0, left = 0;  // units seen, chunks of the current one that are not begun
+  auto another = [&] {  // whether there is a chunk to begin
+    while (left == 0 && next_unit(sm, u, lane, &r, &failed)) { left = r.nch; ++u; }
+    return left-- > 0;
+  };
+  // Q of chunk `at` from shared memory to TMEM, the A operand of two products.  The products of
+  // the chunk before that read Q there are complete.
+  const uint32_t qa = smem_u32(base);
+  auto copy_q = [&](int at) {
+    if (!wait(sm, &sm->q_full, at & 1)) return false;
+    tc_fence_after();
+    const int rr = 32 * w + ((lane >> 3) & 1) * 8 + (lane & 7);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+      for (int rb = 0; rb < 2; ++rb) {
+        const int i = 4 * hf + j, ch = 2 * i + (lane >> 4);
+        uint32_t a[4];
+        ldmatrix_x4(qa + (ch >> 3) * kHalf + sw128_chunk(rr + 16 * rb, ch & 7), a);
+        tmem_st16x128_x2(tr + ((uint32_t)(16 * rb) << 16) + kTmQ + 8 * i, a);
+      }
+    tmem_st_wait();
+    tc_fence_before();
+    warp_arrive(&sm->q_ready, lane);
+    if (lane == 0) mbar_arrive(&sm->q_empty);
+    return true;
+  };
+  bool more = another();
+  if (more && !copy_q(0)) failed = true;
+  for (int ci = 0; more && !failed; ++ci) {
+    {
+      const int b = ci & 1;
       const uint32_t one = ci & 1;
       if (!(wait(sm, &sm->gate_full[b], (ci >> 1) & 1) && wait(sm, &sm->qk_done, one))) { failed = true; break; }
       tc_fence_after();
       const float gi = sm->G[b][row];
-      // P: blocks of 32 columns before this warp's diagonal block by factors, that block pair by pair,
-      // zeros behind it.  The packed pairs go over columns that this thread has read already.
-      uint32_t a[32], pk[16];
+      const bool mild = sm->mild[b] != 0;
+      // P in blocks of 32 columns: by factors before this warp's diagonal block, pair by pair in it,
+      // zeros behind it.  In the order 0, 1 and 3, 2 each goes over columns that its warp has read.
 #pragma unroll 1
-      for (int jb = 0; jb < w; ++jb) {
-        tmem_ld32(tr + kTmAcc + 32 * jb, a);
-        const float2 rf = pair(p.scale * exp2_fast(gi - sm->G[b][32 * jb + 31]));
-        tmem_ld_wait();
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float4 f = *reinterpret_cast<const float4*>(&sm->cf[32 * jb + 4 * e]);
-          pk[2 * e] = pack16x2<F16>(mul2(pair_at(a + 4 * e), mul2(make_float2(f.x, f.y), rf)));
-          pk[2 * e + 1] = pack16x2<F16>(mul2(pair_at(a + 4 * e + 2), mul2(make_float2(f.z, f.w), rf)));
+      for (int it = 0; it < 2; ++it) {
+        const int jb = hf ? 3 - it : it;
+        uint32_t x[32], pk[16];
+        if (jb <= w) {
+          tmem_ld32(tr + kTmAcc + 32 * jb, x);
+          tmem_ld_wait();
         }
-        tmem_st16(tr + kTmAcc + 16 * jb, pk);
-      }
-      tmem_ld32(tr + kTmAcc + 32 * w, a);
-      tmem_ld_wait();
+        if (jb < w || (jb == w && mild)) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float4 f = *reinterpret_cast<const float4*>(&sm->G[b][32 * w + 4 * e]);
-        const float2 x = mul2(mul2(pair_at(a + 4 * e), pair(p.scale)), make_float2(exp2_fast(gi - f.x), exp2_fast(gi - f.y)));
-        const float2 y = mul2(mul2(pair_at(a + 4 * e + 2), pair(p.scale)), make_float2(exp2_fast(gi - f.z), exp2_fast(gi - f.w)));
-        pk[2 * e] = pack16x2<F16>(4 * e <= lane ? x.x : 0.f, 4 * e + 1 <= lane ? x.y : 0.f);
-        pk[2 * e + 1] = pack16x2<F16>(4 * e + 2 <= lane ? y.x : 0.f, 4 * e + 3 <= lane ? y.y : 0.f);
-      }
-      tmem_st16(tr + kTmAcc + 16 * w, pk);
+          for (int q = 0; q < 2; ++q) {
+            const float2 rf = pair(p.scale * exp2_fast(gi - sm->G[b][32 * jb + 16 * q + 15]));
 #pragma unroll
-      for (int e = 0; e < 16; ++e) pk[e] = 0u;
-#pragma unroll 1
-      for (int jb = w + 1; jb < 4; ++jb) tmem_st16(tr + kTmAcc + 16 * jb, pk);
+            for (int e = 8 * q; e < 8 * q + 8; e += 2) {
+              const float4 f = *reinterpret_cast<const float4*>(&sm->cf[32 * jb + 2 * e]);
+              pk[e] = pack16x2<F16>(mul2(pair_at(x + 2 * e), mul2(make_float2(f.x, f.y), rf)));
+              pk[e + 1] = pack16x2<F16>(mul2(pair_at(x + 2 * e + 2), mul2(make_float2(f.z, f.w), rf)));
+            }
+          }
+          if (jb == w) {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) pk[e] = 2 * e > lane ? 0u : 2 * e == lane ? pk[e] & 0xffffu : pk[e];
+          }
+        } else if (jb == w) {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            const float2 f = *reinterpret_cast<const float2*>(&sm->G[b][32 * jb + 2 * e]);
+            const float2 y = mul2(mul2(pair_at(x + 2 * e), pair(p.scale)), make_float2(exp2_fast(gi - f.x), exp2_fast(gi - f.y)));
+            pk[e] = pack16x2<F16>(2 * e <= lane ? y.x : 0.f, 2 * e + 1 <= lane ? y.y : 0.f);
+          }
+        } else {
+#pragma unroll
+          for (int e = 0; e < 16; ++e) pk[e] = 0u;
+        }
+        tmem_st16(tr + p_block_col(jb), pk);
+        if (it == 1) {
+          tc_fence_before();
+          warp_arrive(&sm->acc_read[1 - hf], lane);
+        }
+      }
       warp_arrive(&sm->cf_empty, lane);
       // Q S^T of the row times scale 2^G_i
       if (!wait(sm, &sm->qs_done, one)) { failed = true; break; }
       tc_fence_after();
       const float2 gam = pair(p.scale * exp2f(gi));
 #pragma unroll 1
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 2 * hf; q < 2 * hf + 2; ++q) {
+        uint32_t a[32];
         tmem_ld32(tr + kTmO + 32 * q, a);
         tmem_ld_wait();
 #pragma unroll
@@ -459,85 +537,105 @@ __device__ __forceinline__ void run_po(const DecayPrefillParams& p, uint8_t* bas
       tc_fence_before();
       warp_arrive(&sm->p_ready, lane);
       if (lane == 0) mbar_arrive(&sm->gate_empty[b]);
-      // the output tile, into the stage of Q (both products that read Q are complete)
-      if (!wait(sm, &sm->o_done, one)) { failed = true; break; }
+      more = another();
+      if (failed || (more && !copy_q(ci + 1))) { failed = true; break; }
+      // the output tile, once the one before has left
+      if (!(wait(sm, &sm->o_done, one) && (ci == 0 || wait(sm, &sm->o_stored, one ^ 1)))) { failed = true; break; }
       tc_fence_after();
-      uint8_t* tile = base + s * kStage;
+      uint8_t* tile = base + kOffO;
 #pragma unroll 1
-      for (int q = 0; q < 4; ++q) {
-        tmem_ld32(tr + kTmO + 32 * q, a);
+      for (int q = 0; q < 2; ++q) {
+        uint32_t a[32];
+        tmem_ld32(tr + kTmO + 64 * hf + 32 * q, a);
         tmem_ld_wait();
-        if (q == 3) {
+        if (q == 1) {
           tc_fence_before();
           warp_arrive(&sm->o_free, lane);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-          *reinterpret_cast<uint4*>(tile + (q >> 1) * kHalf + sw128_chunk(row, 4 * (q & 1) + e)) =
+          *reinterpret_cast<uint4*>(tile + hf * kHalf + sw128_chunk(row, 4 * q + e)) =
               make_uint4(pack16x2<F16>(pair_at(a + 8 * e)), pack16x2<F16>(pair_at(a + 8 * e + 2)),
                          pack16x2<F16>(pair_at(a + 8 * e + 4)), pack16x2<F16>(pair_at(a + 8 * e + 6)));
       }
       fence_proxy_async_smem();
-      warp_arrive(&sm->o_staged[s], lane);
+      warp_arrive(&sm->o_staged, lane);
     }
-    if (failed) break;
   }
   if (failed && lane == 0) give_up(p, sm);
 }
 
-// ------------------------------------------------------------ warps 8-15: the state
-// 64 values of a state row, as pairs.
-__device__ __forceinline__ void load_state64(const void* base, int dtype, int64_t off, float2 (&s)[32]) {
+// ------------------------------------------------------------ warps 12-19: the state
+// 32 values of a state row, as the bits of f32.
+__device__ __forceinline__ void load_state32(const void* base, int dtype, int64_t off, uint32_t (&s)[32]) {
   if (dtype == kF32) {
-    const float4* q = reinterpret_cast<const float4*>(reinterpret_cast<const float*>(base) + off);
+    const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(base) + off);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
-      const float4 x = q[i];
-      s[2 * i] = make_float2(x.x, x.y);
-      s[2 * i + 1] = make_float2(x.z, x.w);
+    for (int i = 0; i < 8; ++i) {
+      const uint4 x = q[i];
+      s[4 * i] = x.x; s[4 * i + 1] = x.y; s[4 * i + 2] = x.z; s[4 * i + 3] = x.w;
     }
   } else {
     const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(base) + off);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
       const uint4 x = q[i];
       const uint32_t w[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[4 * i + e] = dtype == kF16 ? unpack16<true>(w[e]) : unpack16<false>(w[e]);
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = dtype == kF16 ? unpack16<true>(w[e]) : unpack16<false>(w[e]);
+        s[8 * i + 2 * e] = __float_as_uint(f.x);
+        s[8 * i + 2 * e + 1] = __float_as_uint(f.y);
+      }
     }
   }
 }
-__device__ __forceinline__ void store_state64(void* base, int dtype, int64_t off, const float2 (&s)[32]) {
+__device__ __forceinline__ void store_state32(void* base, int dtype, int64_t off, const uint32_t (&s)[32]) {
   if (dtype == kF32) {
-    float4* q = reinterpret_cast<float4*>(reinterpret_cast<float*>(base) + off);
+    uint4* q = reinterpret_cast<uint4*>(reinterpret_cast<float*>(base) + off);
 #pragma unroll
-    for (int i = 0; i < 16; ++i) q[i] = make_float4(s[2 * i].x, s[2 * i].y, s[2 * i + 1].x, s[2 * i + 1].y);
+    for (int i = 0; i < 8; ++i) q[i] = make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
   } else {
     uint4* q = reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(base) + off);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int i = 0; i < 4; ++i) {
       uint32_t w[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) w[e] = dtype == kF16 ? pack16x2<true>(s[4 * i + e]) : pack16x2<false>(s[4 * i + e]);
+      for (int e = 0; e < 4; ++e) {
+        const float2 f = pair_at(s + 8 * i + 2 * e);
+        w[e] = dtype == kF16 ? pack16x2<true>(f) : pack16x2<false>(f);
+      }
       q[i] = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }
 
-// Zero this warp's share of the rows past the end: of V exactly what the warp reads below (its
-// 32 value columns of its own tokens), of K an eighth of the columns.
+// a (d_hi + d_lo) for a pair of 16-bit values as lo - neg: neg is the rounded product of a and
+// -d_hi, lo the exact rest of it (a product of two 16-bit values has no more bits than two of
+// them hold) plus the product of a and d_lo.
+template <bool F16>
+__device__ __forceinline__ void split_product(uint32_t a, uint32_t dh, uint32_t dl, uint32_t* neg, uint32_t* lo) {
+  auto go = [&](auto x, auto h, auto mh, auto l) {
+    const auto n = __hmul2(x, mh);
+    const auto r = __hfma2(x, l, __hfma2(x, h, n));
+    *neg = *reinterpret_cast<const uint32_t*>(&n);
+    *lo = *reinterpret_cast<const uint32_t*>(&r);
+  };
+  uint32_t mh = dh ^ 0x80008000u;
+  if (F16) go(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&dh), *reinterpret_cast<__half2*>(&mh), *reinterpret_cast<__half2*>(&dl));
+  else go(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&dh), *reinterpret_cast<__nv_bfloat162*>(&mh), *reinterpret_cast<__nv_bfloat162*>(&dl));
+}
+
+// Zero this warp's share of the rows past the end, in the tokens of the parts that its half makes:
+// 32 columns of K, and of V exactly what the warp reads below.
 template <int kTerms>
 __device__ __forceinline__ void zero_tails(uint8_t* k, uint8_t* v, int left, int w, int hf, int lane) {
-  constexpr int kSub = sub_tokens<kTerms>();
-  const uint4 z = make_uint4(0, 0, 0, 0);
   for (int e = lane; e < C * 4; e += 32) {
-    const int row = e >> 2, ch = 4 * w + (e & 3);  // 16-byte chunk of the 128 values
-    if (row >= left && ((row / (kSub / 2)) & 1) == hf)
-      *reinterpret_cast<uint4*>(v + (ch >> 3) * kHalf + sw128_chunk(row, ch & 7)) = z;
-  }
-  for (int e = lane; e < C * 2; e += 32) {
-    const int row = e >> 1, ch = 2 * (4 * hf + w) + (e & 1);
-    if (row >= left) *reinterpret_cast<uint4*>(k + (ch >> 3) * kHalf + sw128_chunk(row, ch & 7)) = z;
+    const int row = e >> 2, ch = 4 * w + (e & 3);  // 16-byte chunk of the 128 columns
+    if (row < left || ((row / sub_tokens<kTerms>()) & 1) != hf) continue;
+    const uint32_t at = (ch >> 3) * kHalf + sw128_chunk(row, ch & 7);
+    *reinterpret_cast<uint4*>(k + at) = make_uint4(0, 0, 0, 0);
+    *reinterpret_cast<uint4*>(v + at) = make_uint4(0, 0, 0, 0);
   }
   fence_proxy_async_smem();
   __syncwarp();
@@ -546,55 +644,67 @@ __device__ __forceinline__ void zero_tails(uint8_t* k, uint8_t* v, int left, int
 template <bool F16, int kTerms>
 __device__ __forceinline__ void run_ks(const DecayPrefillParams& p, uint8_t* base, Small* sm, uint32_t tmem, int warp, int lane) {
   constexpr int kSub = sub_tokens<kTerms>(), kSubs = C / kSub;
-  const int w = warp & 3, hf = (warp >> 2) & 1, row = 32 * w + lane;  // warps 8-11: first halves, 12-15: second
+  const int w = warp & 3, hf = (warp >> 2) - 3, row = 32 * w + lane;  // warps 12-15: columns 0 .. 63, 16-19: 64 .. 127
   const uint32_t tq = tmem + ((uint32_t)(32 * w) << 16);
   uint8_t* sb = base + kOffS + hf * kHalf;
   bool failed = false;
-  Rec r;
+  Rec r{};
   int ci = 0;
-  float2 s[32];
-  // the 16-bit copy of S for chunk `at`, once Q S^T of the chunk before has read the last one
-  auto copy_state = [&](int at) {
-    if (at > 0 && !wait(sm, &sm->qs_done, (at - 1) & 1)) return false;
+  auto load_in = [&](int c0, uint32_t (&x)[32]) {
+    if (p.s_in) {
+      load_state32(p.s_in, p.sin_dtype, r.slot * p.sin_slot + (int64_t)r.h * p.sin_head + row * D + c0, x);
+    } else {
 #pragma unroll
-    for (int e = 0; e < 8; ++e)
-      *reinterpret_cast<uint4*>(sb + sw128_chunk(row, e)) =
-          make_uint4(pack16x2<F16>(s[4 * e]), pack16x2<F16>(s[4 * e + 1]), pack16x2<F16>(s[4 * e + 2]), pack16x2<F16>(s[4 * e + 3]));
-    fence_proxy_async_smem();
-    warp_arrive(&sm->sb_ready, lane);
-    return true;
+      for (int e = 0; e < 32; ++e) x[e] = 0u;
+    }
   };
   // V_d of tokens [sub * kSub, + kSub) of chunk `at`: transposed fragments of V (pairs of tokens,
-  // one value each) times d, as kTerms 16-bit terms
+  // one value each) times d, as kTerms 16-bit terms.  The four warps of a half make the parts of
+  // their own slots (sub % 2 == hf).
   const int m = lane >> 3, lr = lane & 7;
   auto make_vd = [&](int at, int sub) {
-    const int vi = at * kSubs + sub, slot = vi & 1;
-    if (vi >= 2 && !wait(sm, &sm->vd_empty[slot], ((vi >> 1) - 1) & 1)) return false;
+    int slot, round;
+    vd_place<kTerms>(at, sub, &slot, &round);
+    if (round > 0 && !wait(sm, &sm->vd_empty[slot], (round - 1) & 1)) return false;
+    if (slot >= 2 && !wait(sm, &sm->acc_read[slot - 2], at & 1)) return false;
     tc_fence_after();
-    const uint32_t va = smem_u32(base + (at & 1) * kStage + 2 * kTile);
+    const uint32_t va = smem_u32(base + kOffKv + ((at & 1) * 2 + 1) * kTile);
     const float* dv = sm->d[at & 1];
 #pragma unroll
-    for (int tt = 0; tt < kSub / 32; ++tt) {
-      const int tok = sub * kSub + hf * (kSub / 2) + 16 * tt;  // 16 tokens from here
-      const float2 d0 = *reinterpret_cast<const float2*>(&dv[tok + 2 * (lane & 3)]);
-      const float2 d1 = *reinterpret_cast<const float2*>(&dv[tok + 8 + 2 * (lane & 3)]);
+    for (int tt = 0; tt < kSub / 16; ++tt) {
+      const int tok = sub * kSub + 16 * tt;  // 16 tokens from here
       const int trow = tok + (m >> 1) * 8 + lr;
+      const int at2 = (tok >> 1) + (lane & 3);  // this lane's first pair of tokens; the second is 4 pairs on
 #pragma unroll
       for (int dd = 0; dd < 2; ++dd) {
         const int ch = 4 * w + 2 * dd + (m & 1);
+        const uint32_t to = tq + ((uint32_t)(16 * dd) << 16) + vd_slot_col(slot) + 8 * tt;
         uint32_t a[4], t[4];
         ldmatrix_x4_trans(va + (ch >> 3) * kHalf + sw128_chunk(trow, ch & 7), a);
-        float2 x[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) x[e] = mul2(unpack16<F16>(a[e]), e < 2 ? d0 : d1);
-#pragma unroll
-        for (int term = 0; term < kTerms; ++term) {
+        if (kTerms == 2) {
+          // three packed 16-bit operations
+          const uint32_t* dh = reinterpret_cast<const uint32_t*>(dv) + at2;
+          uint32_t rest[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            t[e] = pack16x2<F16>(x[e]);
-            if (term + 1 < kTerms) x[e] = fma2(unpack16<F16>(t[e]), pair(-1.f), x[e]);
+            const uint32_t h = dh[2 * (e & 2)], l = dh[C / 2 + 2 * (e & 2)];
+            split_product<F16>(a[e], h, l, &t[e], &rest[e]);
           }
-          tmem_st16x128_x2(tq + ((uint32_t)(16 * dd) << 16) + kTmVd + slot * 64 + term * (kSub / 2) + hf * (kSub / 4) + 8 * tt, t);
+          tmem_st16x128_x2(to, t);
+          tmem_st16x128_x2(to + kSub / 2, rest);
+        } else {
+          float2 x[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) x[e] = mul2(unpack16<F16>(a[e]), reinterpret_cast<const float2*>(dv)[at2 + 2 * (e & 2)]);
+#pragma unroll
+          for (int term = 0; term < kTerms; ++term) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              t[e] = pack16x2<F16>(x[e]);
+              if (term + 1 < kTerms) x[e] = fma2(unpack16<F16>(t[e]), pair(-1.f), x[e]);
+            }
+            tmem_st16x128_x2(to + term * (kSub / 2), t);
+          }
         }
       }
     }
@@ -604,55 +714,67 @@ __device__ __forceinline__ void run_ks(const DecayPrefillParams& p, uint8_t* bas
     return true;
   };
   for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
-    if (p.s_in) {
-      load_state64(p.s_in, p.sin_dtype, r.slot * p.sin_slot + (int64_t)r.h * p.sin_head + row * D + 64 * hf, s);
-    } else {
-#pragma unroll
-      for (int e = 0; e < 32; ++e) s[e] = pair(0.f);
-    }
-    if (r.nch > 0 && !copy_state(ci)) { failed = true; break; }
-    // Step j makes V_d part j % kSubs of chunk j / kSubs.  The first part of a chunk is made
-    // before the state of the chunk before is complete: it does not need it.
-#pragma unroll 1
-    for (int j = 0; j <= r.nch * kSubs; ++j) {
-      const int c = j / kSubs, sub = j % kSubs;
-      if (c < r.nch) {
-        if (sub == 0) {
-          const int st = (ci + c) & 1, left = r.len - c * C;
-          const uint32_t ph = ((ci + c) >> 1) & 1;
-          if (!(wait(sm, &sm->gate_full[st], ph) && wait(sm, &sm->v_full[st], ph))) { failed = true; break; }
-          if (left < C) {
-            if (!wait(sm, &sm->k_full[st], ph)) { failed = true; break; }
-            uint8_t* k = base + st * kStage + kTile;
-            zero_tails<kTerms>(k, k + kTile, left, w, hf, lane);
-          }
-        }
-        if (!make_vd(ci + c, sub)) { failed = true; break; }
-      }
-      if (sub != 0 || c == 0) continue;
-      // S <- gamma S + V_d^T K of chunk c - 1
-      const int at = ci + c - 1;
-      const float2 gam = pair(sm->gamma[at & 1]);
-      if (!wait(sm, &sm->ds_done, at & 1)) { failed = true; break; }
+    for (int c = 0; c < r.nch; ++c, ++ci) {
+      const int st = ci & 1, left = r.len - c * C;
+      const uint32_t ph = (ci >> 1) & 1;
+      // S as the chunk finds it: to 16 bits for Q S^T, times the chunk's decay for V_d^T K
+      if (!(wait(sm, &sm->gate_full[st], ph) && (c == 0 || wait(sm, &sm->s_done, (ci - 1) & 1)))) { failed = true; break; }
       tc_fence_after();
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        uint32_t a[16];
-        tmem_ld16(tq + kTmDs + 64 * hf + 16 * q, a);
-        tmem_ld_wait();
-        if (q == 3) {
-          tc_fence_before();
-          warp_arrive(&sm->ds_free, lane);
+      const float2 gam = pair(sm->gamma[st]);
+#pragma unroll 1
+      for (int q = 0; q < 2; ++q) {
+        uint32_t x[32];
+        if (c == 0) {
+          load_in(64 * hf + 32 * q, x);
+        } else {
+          tmem_ld32(tq + kTmS + 64 * hf + 32 * q, x);
+          tmem_ld_wait();
         }
 #pragma unroll
-        for (int e = 0; e < 8; ++e) s[8 * q + e] = fma2(s[8 * q + e], gam, pair_at(a + 2 * e));
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<uint4*>(sb + sw128_chunk(row, 4 * q + e)) =
+              make_uint4(pack16x2<F16>(pair_at(x + 8 * e)), pack16x2<F16>(pair_at(x + 8 * e + 2)),
+                         pack16x2<F16>(pair_at(x + 8 * e + 4)), pack16x2<F16>(pair_at(x + 8 * e + 6)));
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float2 y = mul2(pair_at(x + e), gam);
+          x[e] = __float_as_uint(y.x);
+          x[e + 1] = __float_as_uint(y.y);
+        }
+        tmem_st32(tq + kTmS + 64 * hf + 32 * q, x);
       }
-      if (lane == 0) mbar_arrive(&sm->gate_empty[at & 1]);
-      if (c < r.nch && !copy_state(at + 1)) { failed = true; break; }
+      fence_proxy_async_smem();
+      tmem_st_wait();
+      tc_fence_before();
+      warp_arrive(&sm->s_ready, lane);
+      if (!wait(sm, &sm->v_full[st], ph)) { failed = true; break; }
+      if (left < C) {
+        if (!wait(sm, &sm->k_full[st], ph)) { failed = true; break; }
+        uint8_t* k = base + kOffKv + st * 2 * kTile;
+        zero_tails<kTerms>(k, k + kTile, left, w, hf, lane);
+      }
+#pragma unroll 1
+      for (int sub = hf; sub < kSubs && !failed; sub += 2) failed = !make_vd(ci, sub);
+      if (failed) break;
+      warp_arrive(&sm->gate_empty[st], lane);
     }
     if (failed) break;
-    ci += r.nch;
-    if (p.s_out) store_state64(p.s_out, p.sout_dtype, r.slot * p.sout_slot + (int64_t)r.h * p.sout_head + row * D + 64 * hf, s);
+    // the state that the sequence leaves (an empty one passes on what it got); the next unit may
+    // overwrite TMEM and the 16-bit copy after that, Q S^T having run before
+    if (r.nch > 0 && !wait(sm, &sm->s_done, (ci - 1) & 1)) { failed = true; break; }
+    if (!p.s_out) continue;
+    tc_fence_after();
+#pragma unroll 1
+    for (int q = 0; q < 2; ++q) {
+      uint32_t x[32];
+      if (r.nch == 0) {
+        load_in(64 * hf + 32 * q, x);
+      } else {
+        tmem_ld32(tq + kTmS + 64 * hf + 32 * q, x);
+        tmem_ld_wait();
+      }
+      store_state32(p.s_out, p.sout_dtype, r.slot * p.sout_slot + (int64_t)r.h * p.sout_head + row * D + 64 * hf + 32 * q, x);
+    }
   }
   if (failed && lane == 0) give_up(p, sm);
 }
@@ -667,11 +789,11 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __
     auto init = [](uint64_t* bar, int n, int count) {
       for (int i = 0; i < n; ++i) mbar_init(bar + i, count);
     };
-    init(sm->q_full, 2, 1);
+    init(&sm->q_full, 1, 1);
+    init(&sm->q_empty, 1, kPoWarps);
     init(sm->k_full, 2, 1);
     init(sm->v_full, 2, 1);
     init(sm->kv_empty, 2, 1);
-    init(sm->q_empty, 2, 1);
     init(sm->rec_full, kRecs, 1);
     init(sm->rec_empty, kRecs, kReaders);
     init(sm->gate_full, 2, 1);
@@ -679,15 +801,17 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __
     init(&sm->cf_empty, 1, kPoWarps);
     init(&sm->qk_done, 1, 1);
     init(&sm->qs_done, 1, 1);
-    init(&sm->ds_done, 1, 1);
+    init(&sm->s_done, 1, 1);
     init(&sm->o_done, 1, 1);
     init(&sm->p_ready, 1, kPoWarps);
     init(&sm->o_free, 1, kPoWarps);
-    init(sm->o_staged, 2, kPoWarps);
-    init(&sm->sb_ready, 1, kKsWarps);
-    init(&sm->ds_free, 1, kKsWarps);
-    init(sm->vd_full, 2, kKsWarps);
-    init(sm->vd_empty, 2, 1);
+    init(&sm->o_staged, 1, kPoWarps);
+    init(&sm->q_ready, 1, kPoWarps);
+    init(sm->acc_read, 2, kPoWarps / 2);
+    init(&sm->o_stored, 1, 1);
+    init(&sm->s_ready, 1, kKsWarps);
+    init(sm->vd_full, 4, kKsWarps / 2);
+    init(sm->vd_empty, 4, 1);
     init(&sm->drain, 1, 1);
     sm->abort = 0;
     fence_mbar_init();
@@ -704,12 +828,16 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = sm->tmem;
-  if (warp == 0) run_producer(p, base, sm, lane);
-  else if (warp == 1) run_mma<F16, kTerms>(p, base, sm, tmem, lane);
-  else if (warp == 2) run_gates(p, sm, lane);
-  else if (warp == 3) run_store(p, base, sm, lane);
-  else if (warp < 8) run_po<F16>(p, base, sm, tmem, warp, lane);
-  else run_ks<F16, kTerms>(p, base, sm, tmem, warp, lane);
+  if (warp < 4) {
+    if (warp == 0) run_producer(p, base, sm, lane);
+    else if (warp == 1) run_mma<F16, kTerms>(p, base, sm, tmem, lane);
+    else if (warp == 2) run_gates<F16, kTerms>(p, sm, lane);
+    else run_store(p, base, sm, lane);
+  } else if (warp < 4 + kPoWarps) {
+    run_po<F16>(p, base, sm, tmem, warp, lane);
+  } else {
+    run_ks<F16, kTerms>(p, base, sm, tmem, warp, lane);
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == 0) tmem_dealloc(tmem, kTmCols);

@@ -283,6 +283,15 @@ GDN_DEV void stmatrix_x4_trans(uint32_t saddr, uint32_t r0, uint32_t r1, uint32_
                : "memory");
 }
 
+// Four 8 x 8 matrices of 16-bit elements: thread 8 i + j gives the shared address of row j of
+// matrix i (16 contiguous bytes); register i of thread t receives elements (t / 4,
+// 2 (t % 4) + {0, 1}) of matrix i (low half first).
+GDN_DEV void ldmatrix_x4(uint32_t saddr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(saddr)
+               : "memory");
+}
 // Four 8 x 8 matrices of 16-bit elements read transposed: thread 8 i + j gives the shared
 // address of row j of matrix i (16 contiguous bytes); register i of thread t receives
 // elements (2 (t % 4), t / 4) and (2 (t % 4) + 1, t / 4) of matrix i (low half first).
