@@ -83,7 +83,7 @@ struct Small {
   uint64_t rec_full[kRecs], rec_empty[kRecs];
   uint64_t gate_full[2], gate_empty[2], cf_empty;
   uint64_t qk_done, qs_done, s_done, o_done;   // products that have completed
-  uint64_t q_ready, acc_read[2], p_ready, o_free, o_staged;  // warps 4-11
+  uint64_t q_ready, p_ready, o_free, o_staged;  // warps 4-11
   uint64_t o_stored;                            // warp 3
   uint64_t s_ready, vd_full[4];                // warps 12-19
   uint64_t vd_empty[4], drain;
@@ -99,11 +99,12 @@ constexpr uint32_t kTmO = 128;     // Q S^T, then the output
 constexpr uint32_t kTmS = 256;     // S, f32 (128)
 constexpr uint32_t kTmQ = 384;     // Q as packed pairs (64)
 // P takes 16 columns for a block of 32 tokens: the first two blocks in front, the last two behind, so
-// that the columns between come free as the scores are read, the upper 32 first.
+// that a block goes over columns that its own warps have read.
 __device__ __forceinline__ uint32_t p_block_col(int jb) { return kTmAcc + 16 * jb + (jb >= 2 ? 64 : 0); }
-// V_d terms as packed pairs, in four slots of 32: two of their own, two in those columns.
+// V_d terms as packed pairs, in four slots of 32: two of their own, two over Q, which is free from
+// Q S^T to the next chunk's copy.
 constexpr uint32_t kTmVd = 448;
-__device__ __forceinline__ uint32_t vd_slot_col(int slot) { return slot < 2 ? kTmVd + 32 * slot : kTmAcc + 64 - 32 * (slot - 2); }
+__device__ __forceinline__ uint32_t vd_slot_col(int slot) { return slot < 2 ? kTmVd + 32 * slot : kTmQ + 32 * (slot - 2); }
 constexpr uint32_t kTmCols = 512;
 
 constexpr int kThreads = 640;
@@ -441,11 +442,11 @@ __device__ __forceinline__ void run_po(const DecayPrefillParams& p, uint8_t* bas
     while (left == 0 && next_unit(sm, u, lane, &r, &failed)) { left = r.nch; ++u; }
     return left-- > 0;
   };
-  // Q of chunk `at` from shared memory to TMEM, the A operand of two products.  The products of
-  // the chunk before that read Q there are complete.
+  // Q of chunk `at` from shared memory to TMEM, the A operand of two products, once V_d^T K of the
+  // chunk before has read the V_d that took its place.
   const uint32_t qa = smem_u32(base);
   auto copy_q = [&](int at) {
-    if (!wait(sm, &sm->q_full, at & 1)) return false;
+    if (!(wait(sm, &sm->q_full, at & 1) && (at == 0 || wait(sm, &sm->s_done, (at - 1) & 1)))) return false;
     tc_fence_after();
     const int rr = 32 * w + ((lane >> 3) & 1) * 8 + (lane & 7);
 #pragma unroll
@@ -510,10 +511,6 @@ __device__ __forceinline__ void run_po(const DecayPrefillParams& p, uint8_t* bas
           for (int e = 0; e < 16; ++e) pk[e] = 0u;
         }
         tmem_st16(tr + p_block_col(jb), pk);
-        if (it == 1) {
-          tc_fence_before();
-          warp_arrive(&sm->acc_read[1 - hf], lane);
-        }
       }
       warp_arrive(&sm->cf_empty, lane);
       // Q S^T of the row times scale 2^G_i
@@ -666,7 +663,7 @@ __device__ __forceinline__ void run_ks(const DecayPrefillParams& p, uint8_t* bas
     int slot, round;
     vd_place<kTerms>(at, sub, &slot, &round);
     if (round > 0 && !wait(sm, &sm->vd_empty[slot], (round - 1) & 1)) return false;
-    if (slot >= 2 && !wait(sm, &sm->acc_read[slot - 2], at & 1)) return false;
+    if (slot >= 2 && !wait(sm, &sm->qs_done, at & 1)) return false;
     tc_fence_after();
     const uint32_t va = smem_u32(base + kOffKv + ((at & 1) * 2 + 1) * kTile);
     const float* dv = sm->d[at & 1];
@@ -807,7 +804,6 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __
     init(&sm->o_free, 1, kPoWarps);
     init(&sm->o_staged, 1, kPoWarps);
     init(&sm->q_ready, 1, kPoWarps);
-    init(sm->acc_read, 2, kPoWarps / 2);
     init(&sm->o_stored, 1, 1);
     init(&sm->s_ready, 1, kKsWarps);
     init(sm->vd_full, 4, kKsWarps / 2);
