@@ -25,7 +25,8 @@ DEVERR_CU_SEQLENS, DEVERR_STATE_INDEX, DEVERR_TIMEOUT, DEVERR_POSITION = 0x1, 0x
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2, torch.int32: 3, torch.int64: 4}
 # symbols include/gdn.h declares; the tests check the library exports all of them
 EXPORTED = ["gdn_init", "gdn_chunk_prefill", "gdn_chunk_prefill_checkpointed", "gdn_chunk_prefill_noalloc",
-            "gdn_decode_step", "gdn_qk_norm_rope", "gdn_decay_prefill", "gdn_decay_step", "gdn_reserve_workspace", "gdn_split_workspace_bytes",
+            "gdn_decode_step", "gdn_qk_norm_rope", "gdn_decay_prefill", "gdn_decay_step",
+            "gdn_decay_workspace_bytes", "gdn_reserve_workspace", "gdn_split_workspace_bytes",
             "gdn_get_device_status", "gdn_last_error", "gdn_shutdown", "gdn_testing_force_splits",
             "gdn_testing_wait_limit", "gdn_testing_split_plan"]
 
@@ -81,6 +82,8 @@ def load_library():
         lib.gdn_qk_norm_rope.restype = ctypes.c_int
         lib.gdn_decay_prefill.argtypes = [A, A, A, A, F, A, A, A, A, I, A, A]
         lib.gdn_decay_prefill.restype = ctypes.c_int
+        lib.gdn_decay_workspace_bytes.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, I]
+        lib.gdn_decay_workspace_bytes.restype = ctypes.c_size_t
         lib.gdn_decay_step.argtypes = [A, A, A, A, F, A, A, A, A]
         lib.gdn_decay_step.restype = ctypes.c_int
         lib.gdn_get_device_status.argtypes = [ctypes.c_void_p, ctypes.POINTER(ctypes.c_int32)]
@@ -252,6 +255,14 @@ def gdn_decay_prefill(q, k, v, g, scale: float, initial_state, state_indices, ou
     d = _descriptors.fill(q, k, v, g, initial_state, state_indices, output_state, cu_seqlens, output)
     _check(load_library().gdn_decay_prefill(d[0], d[1], d[2], d[3], float(scale), d[4], d[5], d[6], d[7],
                                             int(bool(batch_invariant)), d[8], _stream_handle(stream)))
+
+
+def gdn_decay_workspace_bytes(num_seqs: int, num_heads: int, total_tokens: int, num_sms: Optional[int] = None) -> int:
+    """Workspace bytes that a decay prefill of these sizes uses (0 when it does not split its
+    sequences), for :func:`gdn_reserve_workspace`; ``num_sms`` defaults to the current device's."""
+    if num_sms is None:
+        num_sms = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
+    return int(load_library().gdn_decay_workspace_bytes(int(num_seqs), int(num_heads), int(total_tokens), int(num_sms)))
 
 
 def gdn_decay_step(q, k, v, g, scale: float, state, state_indices, output, stream=None) -> None:

@@ -629,6 +629,18 @@ gdn_status_t check_decay(const gdn_tensor_t* q, const gdn_tensor_t* k, const gdn
   return GDN_OK;
 }
 
+// Segments a sequence of a decay prefill, and the workspace that they need: a state and a
+// decay for each segment but the last.
+size_t decay_ws_bytes(int64_t N, int64_t H, int splits) {
+  return splits > 1 ? size_t(N * H) * size_t(splits - 1) * (65536 + sizeof(float)) : 0;
+}
+int decay_plan(int64_t N, int64_t H, int64_t T, int sms) {
+  if (N <= 0) return 1;
+  int P = t_force_splits > 0 ? t_force_splits : gdn::decay_splits(N * H, double(T) / double(N) / gdn::kDecayChunk, sms);
+  while (P > 1 && (N * H * P >= (int64_t(1) << 31) || decay_ws_bytes(N, H, P) > kMaxSplitWorkspace)) --P;
+  return P;
+}
+
 // Whether two [rows, heads, 128] views of 16-bit elements share no element: their byte
 // ranges are apart, or they are slices of the same rows that lie side by side.
 bool rows_apart(const gdn_tensor_t* a, const gdn_tensor_t* b) {
@@ -900,9 +912,22 @@ gdn_status_t gdn_decay_prefill(const gdn_tensor_t* q, const gdn_tensor_t* k, con
   p.N = (int32_t)N; p.H = (int32_t)s.H; p.H_qk = (int32_t)s.Hqk; p.H_v = (int32_t)s.Hv;
   p.scale = (scale == 0.0f) ? 1.0f / std::sqrt(128.0f) : scale;
   p.op_f16 = q->dtype == GDN_F16 ? 1 : 0;
+  p.splits = batch_invariant ? 1 : decay_plan(N, s.H, s.rows, gdn::device_sm_count());
+  std::unique_lock<std::mutex> lk(g_mu, std::defer_lock);
+  if (p.splits > 1) {  // held to the launch, so that no other thread's call replaces the workspace before it
+    lk.lock();
+    if ((st = ensure_workspace(g_dev[dev], decay_ws_bytes(N, s.H, p.splits), stream)) != GDN_OK) return st;
+    p.ws = g_dev[dev].ws;
+    p.ws_decay = p.ws + N * s.H * (p.splits - 1) * 16384;
+  }
   cudaError_t e = gdn::launch_decay_prefill(p, stream);
   if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "decay prefill launch: %s", cudaGetErrorString(e));
   return GDN_OK;
+}
+
+size_t gdn_decay_workspace_bytes(int64_t num_seqs, int64_t num_heads, int64_t total_tokens, int num_sms) {
+  if (num_seqs <= 0 || num_heads <= 0 || total_tokens < 0 || num_sms <= 0) return 0;
+  return decay_ws_bytes(num_seqs, num_heads, decay_plan(num_seqs, num_heads, total_tokens, num_sms));
 }
 
 gdn_status_t gdn_decay_step(const gdn_tensor_t* q, const gdn_tensor_t* k, const gdn_tensor_t* v,

@@ -51,8 +51,16 @@ struct DecayPrefillParams {
   int32_t g_dtype, sin_dtype, sout_dtype, idx_dtype, cu_dtype;
   float scale;
   int32_t op_f16;
+  // Sequences cut into `splits` segments of whole chunks (1: not cut), segment x of a sequence of c
+  // chunks holding chunks [c x / splits, c (x + 1) / splits).  With U = N H and unit nh = n H + h:
+  float* ws;        // [U][splits - 1] states of 128 x 128: the state behind segment x, once joined
+  float* ws_decay;  // [U][splits - 1] decays of whole segments
+  int32_t splits;
 };
 constexpr int kDecayChunk = 128;  // tokens of a chunk
+
+// Segments a sequence for U units on `sms` SMs, `chunks` the mean chunks of a sequence.
+int decay_splits(int64_t units, double chunks, int sms);
 cudaError_t launch_decay_prefill(const DecayPrefillParams& p, cudaStream_t stream);
 
 // The same recurrence for one token of each batch row, states updated in place.

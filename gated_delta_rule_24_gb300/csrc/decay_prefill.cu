@@ -67,10 +67,12 @@ constexpr uint32_t kOffO = kOffS + kTile;    // the output tile on its way out
 constexpr uint32_t kOffSmall = kOffO + kTile;
 constexpr int kRecs = 4;
 
-struct Rec {       // one unit: a sequence of one head
+struct Rec {       // one unit: a sequence, or a segment of one, of one head
   int32_t t0, len, h, nch;  // first token, tokens, head, chunks (-1: no more units)
   int64_t slot;
+  int32_t in, out;  // where the state comes from and goes to: a block of the workspace, or
 };
+constexpr int kPool = -1, kNone = -2;  // the caller's pool (zeros without one), or nowhere (zeros)
 struct Small {
   float G[2][C];   // inclusive prefix sums of log2 g
   float d[2][C];   // 2^(sum of the log2 g behind the token), 0 past the end; with two V_d terms
@@ -109,7 +111,6 @@ constexpr uint32_t kTmCols = 512;
 
 constexpr int kThreads = 640;
 constexpr int kPoWarps = 8, kKsWarps = 8;
-constexpr int kReaders = 3 + kPoWarps + kKsWarps;  // warps that read a unit's record
 static_assert(kThreads == 32 * (4 + kPoWarps + kKsWarps), "roles");
 
 // Every wait: bounded (kTries probes of up to 20 us each), and over as soon as another role has
@@ -158,10 +159,13 @@ __device__ __forceinline__ bool next_unit(Small* sm, int u, int lane, Rec* r, bo
 }
 
 // ------------------------------------------------------------ warp 0: loads
+// kStates, here and below: the launch makes the states that the segments add, no outputs.
+template <bool kStates>
 __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_t* base, Small* sm, int lane) {
   bool ok = true;
   int u = 0, ci = 0;  // units and chunks so far
-  const int64_t units = (int64_t)p.N * p.H;
+  const int segs = kStates ? p.splits - 1 : p.splits;  // segments that this launch walks
+  const int64_t units = (int64_t)p.N * segs * p.H;
   int kv_loads = 0, q_loads = 0;
   auto publish = [&](const Rec& r) {
     const int slot = u % kRecs;
@@ -174,7 +178,8 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
     return true;
   };
   for (int64_t x = blockIdx.x; x < units && ok; x += gridDim.x) {
-    const int n = (int)(x / p.H), h = (int)(x % p.H);
+    // heads of a segment side by side: they share keys and queries, or lines of the gates
+    const int h = (int)(x % p.H), seg = (int)(x / p.H) % segs, n = (int)(x / p.H / segs);
     const int64_t bos = index_at(p.cu, p.cu_dtype, n), eos = index_at(p.cu, p.cu_dtype, n + 1);
     const int64_t slot = p.state_idx ? index_at(p.state_idx, p.idx_dtype, n) : (int64_t)n;
     int err = 0;
@@ -185,25 +190,31 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
       if (lane == 0) atomicOr(p.dev_err, err);
       continue;
     }
-    const int len = (int)(eos - bos), nch = (len + C - 1) / C;
-    ok = publish(Rec{(int)bos, len, h, nch, slot});
+    const int all = (int)((eos - bos + C - 1) / C);  // chunks of the sequence
+    const int c0 = (int)((int64_t)all * seg / p.splits), nch = (int)((int64_t)all * (seg + 1) / p.splits) - c0;
+    const int first = (int)bos + c0 * C, len = nch > 0 ? min((int)eos - first, nch * C) : 0;
+    const int block = (n * p.H + h) * (p.splits - 1) + seg;  // of the state behind this segment
+    const int in = seg == 0 ? kPool : kStates ? kNone : block - 1;
+    ok = publish(Rec{first, len, h, nch, slot, in, kStates ? block : seg == p.splits - 1 ? kPool : kNone});
     if (!ok) break;
-    if (p.s_in && lane == 0) {
+    if (p.s_in && in == kPool && lane == 0) {
       const int es = p.sin_dtype == kF32 ? 4 : 2;
       bulk_prefetch_l2(reinterpret_cast<const char*>(p.s_in) + (slot * p.sin_slot + (int64_t)h * p.sin_head) * es, D * D * es);
     }
     const int hq = h / (p.H / p.H_qk), hv = h / (p.H / p.H_v);
     for (int c = 0; c < nch; ++c, ++ci) {
-      const int s = ci & 1, t0 = (int)bos + c * C;
+      const int s = ci & 1, t0 = first + c * C;
       auto load = [&](uint8_t* dst, const CUtensorMap* tm, uint64_t* bar, int head) {
         mbar_arrive_expect_tx(bar, kTile);
         tma_load_3d(dst, tm, bar, 0, head, t0);
         tma_load_3d(dst + kHalf, tm, bar, 64, head, t0);
       };
-      ok = ci < 1 || wait(sm, &sm->q_empty, (ci - 1) & 1);
-      if (!ok) break;
-      if (lane == 0) load(base, &p.tm_q, &sm->q_full, hq);
-      ++q_loads;
+      if (!kStates) {
+        ok = ci < 1 || wait(sm, &sm->q_empty, (ci - 1) & 1);
+        if (!ok) break;
+        if (lane == 0) load(base, &p.tm_q, &sm->q_full, hq);
+        ++q_loads;
+      }
       ok = ci < 2 || wait(sm, &sm->kv_empty[s], ((ci >> 1) - 1) & 1);
       if (!ok) break;
       if (lane == 0) {
@@ -214,7 +225,7 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
       ++kv_loads;
     }
   }
-  if (ok) ok = publish(Rec{0, 0, 0, -1, 0});
+  if (ok) ok = publish(Rec{0, 0, 0, -1, 0, 0, 0});
   if (!ok && lane == 0) give_up(p, sm);
   // loads that no role waits for any more land before the CTA's shared memory goes away
   auto landed = [&](uint64_t (&bar)[2], int loads) {
@@ -240,7 +251,7 @@ __device__ __forceinline__ void vd_place(int ci, int b, int* slot, int* round) {
   *round = ci * (kSubs / 4) + (b % (kSubs / 2)) / 2;  // uses of the slot before
 }
 
-template <bool F16, int kTerms>
+template <bool F16, int kTerms, bool kStates>
 __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* base, Small* sm, uint32_t tmem, int lane) {
   constexpr int kSub = sub_tokens<kTerms>(), kSubs = C / kSub;
   const uint32_t id_kk = idesc_16_f32(F16, 128, 128, 0, 0, 0);  // B K-major
@@ -258,27 +269,31 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
       const uint32_t k = smem_u32(base + kOffKv + s * 2 * kTile);
       const uint64_t d_k = sdesc_sw128(k, 16, 1024), d_kt = sdesc_sw128(k, kHalf, 1024);
       const uint64_t d_vt = sdesc_sw128(k + kTile, kHalf, 1024);
-      // Q K^T.  P of the chunk before is being read by its P V at the latest, which was
-      // issued before: the products run in order.
-      if (!(wait(sm, &sm->k_full[s], ph) && wait(sm, &sm->q_ready, one))) { failed = true; break; }
-      tc_fence_after();
-      if (leader) {
+      if (kStates) {
+        if (!(wait(sm, &sm->k_full[s], ph) && wait(sm, &sm->s_ready, one))) { failed = true; break; }
+      } else {
+        // Q K^T.  P of the chunk before is being read by its P V at the latest, which was
+        // issued before: the products run in order.
+        if (!(wait(sm, &sm->k_full[s], ph) && wait(sm, &sm->q_ready, one))) { failed = true; break; }
+        tc_fence_after();
+        if (leader) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          mma_ts(tmem + kTmAcc, tmem + kTmQ + i * 8, d_k + ((i >> 2) * kHalf + (i & 3) * 32) / 16, id_kk, i > 0);
-        mma_commit(&sm->qk_done);
-      }
-      __syncwarp();
-      // Q S^T
-      if (!(wait(sm, &sm->s_ready, one) && (ci == 0 || wait(sm, &sm->o_free, one ^ 1)))) { failed = true; break; }
-      tc_fence_after();
-      if (leader) {
+          for (int i = 0; i < 8; ++i)
+            mma_ts(tmem + kTmAcc, tmem + kTmQ + i * 8, d_k + ((i >> 2) * kHalf + (i & 3) * 32) / 16, id_kk, i > 0);
+          mma_commit(&sm->qk_done);
+        }
+        __syncwarp();
+        // Q S^T
+        if (!(wait(sm, &sm->s_ready, one) && (ci == 0 || wait(sm, &sm->o_free, one ^ 1)))) { failed = true; break; }
+        tc_fence_after();
+        if (leader) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          mma_ts(tmem + kTmO, tmem + kTmQ + i * 8, d_s + ((i >> 2) * kHalf + (i & 3) * 32) / 16, id_kk, i > 0);
-        mma_commit(&sm->qs_done);
+          for (int i = 0; i < 8; ++i)
+            mma_ts(tmem + kTmO, tmem + kTmQ + i * 8, d_s + ((i >> 2) * kHalf + (i & 3) * 32) / 16, id_kk, i > 0);
+          mma_commit(&sm->qs_done);
+        }
+        __syncwarp();
       }
-      __syncwarp();
       // V_d^T K
 #pragma unroll
       for (int b = 0; b < kSubs; ++b) {
@@ -295,10 +310,12 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
                      kTerms == 2 && t == 0 ? id_kmn_neg : id_kmn, 1);
           mma_commit(&sm->vd_empty[slot]);
           if (b == kSubs - 1) mma_commit(&sm->s_done);
+          if (kStates && b == kSubs - 1) mma_commit(&sm->kv_empty[s]);
         }
         __syncwarp();
       }
       if (failed) break;
+      if (kStates) continue;
       // + P V
       if (!wait(sm, &sm->p_ready, one)) { failed = true; break; }
       tc_fence_after();
@@ -320,7 +337,7 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
 }
 
 // ------------------------------------------------------------ warp 2: gates
-template <bool F16, int kTerms>
+template <bool F16, int kTerms, bool kStates>
 __device__ __forceinline__ void run_gates(const DecayPrefillParams& p, Small* sm, int lane) {
   bool failed = false;
   Rec r{};
@@ -339,7 +356,7 @@ __device__ __forceinline__ void run_gates(const DecayPrefillParams& p, Small* sm
     else each([&](int64_t i) { return __half2float(reinterpret_cast<const __half*>(p.g)[i]); });
   };
   for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
-    float ahead[4] = {1.f, 1.f, 1.f, 1.f};
+    float ahead[4] = {1.f, 1.f, 1.f, 1.f}, whole = 0.f;
     if (p.g && r.nch > 0) load4(0, ahead);
     for (int c = 0; c < r.nch; ++c, ++ci) {
       const int b = ci & 1, left = r.len - c * C;
@@ -386,12 +403,16 @@ __device__ __forceinline__ void run_gates(const DecayPrefillParams& p, Small* sm
         sm->gamma[b] = exp2f(total);
         sm->mild[b] = mild;
       }
-      if (!(ci == 0 || wait(sm, &sm->cf_empty, (ci - 1) & 1))) { failed = true; break; }
-      *reinterpret_cast<float4*>(&sm->cf[4 * lane]) = make_float4(
-          exp2_fast(g_end - pre[0]), exp2_fast(g_end - pre[1]), exp2_fast(g_end - pre[2]), exp2_fast(g_end - pre[3]));
+      whole += total;
+      if (!kStates) {
+        if (!(ci == 0 || wait(sm, &sm->cf_empty, (ci - 1) & 1))) { failed = true; break; }
+        *reinterpret_cast<float4*>(&sm->cf[4 * lane]) = make_float4(
+            exp2_fast(g_end - pre[0]), exp2_fast(g_end - pre[1]), exp2_fast(g_end - pre[2]), exp2_fast(g_end - pre[3]));
+      }
       warp_arrive(&sm->gate_full[b], lane);
     }
     if (failed) break;
+    if (kStates && lane == 0) p.ws_decay[r.out] = exp2f(whole);
   }
   if (failed && lane == 0) give_up(p, sm);
 }
@@ -638,7 +659,7 @@ __device__ __forceinline__ void zero_tails(uint8_t* k, uint8_t* v, int left, int
   __syncwarp();
 }
 
-template <bool F16, int kTerms>
+template <bool F16, int kTerms, bool kStates>
 __device__ __forceinline__ void run_ks(const DecayPrefillParams& p, uint8_t* base, Small* sm, uint32_t tmem, int warp, int lane) {
   constexpr int kSub = sub_tokens<kTerms>(), kSubs = C / kSub;
   const int w = warp & 3, hf = (warp >> 2) - 3, row = 32 * w + lane;  // warps 12-15: columns 0 .. 63, 16-19: 64 .. 127
@@ -648,7 +669,9 @@ __device__ __forceinline__ void run_ks(const DecayPrefillParams& p, uint8_t* bas
   Rec r{};
   int ci = 0;
   auto load_in = [&](int c0, uint32_t (&x)[32]) {
-    if (p.s_in) {
+    if (r.in >= 0) {
+      load_state32(p.ws, kF32, (int64_t)r.in * (D * D) + row * D + c0, x);
+    } else if (r.in == kPool && p.s_in) {
       load_state32(p.s_in, p.sin_dtype, r.slot * p.sin_slot + (int64_t)r.h * p.sin_head + row * D + c0, x);
     } else {
 #pragma unroll
@@ -663,7 +686,7 @@ __device__ __forceinline__ void run_ks(const DecayPrefillParams& p, uint8_t* bas
     int slot, round;
     vd_place<kTerms>(at, sub, &slot, &round);
     if (round > 0 && !wait(sm, &sm->vd_empty[slot], (round - 1) & 1)) return false;
-    if (slot >= 2 && !wait(sm, &sm->qs_done, at & 1)) return false;
+    if (!kStates && slot >= 2 && !wait(sm, &sm->qs_done, at & 1)) return false;
     tc_fence_after();
     const uint32_t va = smem_u32(base + kOffKv + ((at & 1) * 2 + 1) * kTile);
     const float* dv = sm->d[at & 1];
@@ -728,7 +751,7 @@ __device__ __forceinline__ void run_ks(const DecayPrefillParams& p, uint8_t* bas
           tmem_ld_wait();
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < 4 && !kStates; ++e)
           *reinterpret_cast<uint4*>(sb + sw128_chunk(row, 4 * q + e)) =
               make_uint4(pack16x2<F16>(pair_at(x + 8 * e)), pack16x2<F16>(pair_at(x + 8 * e + 2)),
                          pack16x2<F16>(pair_at(x + 8 * e + 4)), pack16x2<F16>(pair_at(x + 8 * e + 6)));
@@ -740,7 +763,7 @@ __device__ __forceinline__ void run_ks(const DecayPrefillParams& p, uint8_t* bas
         }
         tmem_st32(tq + kTmS + 64 * hf + 32 * q, x);
       }
-      fence_proxy_async_smem();
+      if (!kStates) fence_proxy_async_smem();
       tmem_st_wait();
       tc_fence_before();
       warp_arrive(&sm->s_ready, lane);
@@ -759,7 +782,7 @@ __device__ __forceinline__ void run_ks(const DecayPrefillParams& p, uint8_t* bas
     // the state that the sequence leaves (an empty one passes on what it got); the next unit may
     // overwrite TMEM and the 16-bit copy after that, Q S^T having run before
     if (r.nch > 0 && !wait(sm, &sm->s_done, (ci - 1) & 1)) { failed = true; break; }
-    if (!p.s_out) continue;
+    if (r.out == kNone || (r.out == kPool && !p.s_out)) continue;
     tc_fence_after();
 #pragma unroll 1
     for (int q = 0; q < 2; ++q) {
@@ -770,14 +793,16 @@ __device__ __forceinline__ void run_ks(const DecayPrefillParams& p, uint8_t* bas
         tmem_ld32(tq + kTmS + 64 * hf + 32 * q, x);
         tmem_ld_wait();
       }
-      store_state32(p.s_out, p.sout_dtype, r.slot * p.sout_slot + (int64_t)r.h * p.sout_head + row * D + 64 * hf + 32 * q, x);
+      const int64_t at = row * D + 64 * hf + 32 * q;
+      if (r.out >= 0) store_state32(p.ws, kF32, (int64_t)r.out * (D * D) + at, x);
+      else store_state32(p.s_out, p.sout_dtype, r.slot * p.sout_slot + (int64_t)r.h * p.sout_head + at, x);
     }
   }
   if (failed && lane == 0) give_up(p, sm);
 }
 
 // ------------------------------------------------------------ the kernel
-template <bool F16, int kTerms>
+template <bool F16, int kTerms, bool kStates>
 __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __grid_constant__ DecayPrefillParams p) {
   extern __shared__ __align__(1024) uint8_t base[];
   Small* sm = reinterpret_cast<Small*>(base + kOffSmall);
@@ -792,9 +817,9 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __
     init(sm->v_full, 2, 1);
     init(sm->kv_empty, 2, 1);
     init(sm->rec_full, kRecs, 1);
-    init(sm->rec_empty, kRecs, kReaders);
+    init(sm->rec_empty, kRecs, kStates ? 2 + kKsWarps : 3 + kPoWarps + kKsWarps);
     init(sm->gate_full, 2, 1);
-    init(sm->gate_empty, 2, kPoWarps + kKsWarps);
+    init(sm->gate_empty, 2, kStates ? kKsWarps : kPoWarps + kKsWarps);
     init(&sm->cf_empty, 1, kPoWarps);
     init(&sm->qk_done, 1, 1);
     init(&sm->qs_done, 1, 1);
@@ -825,38 +850,91 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __
   tc_fence_after();
   const uint32_t tmem = sm->tmem;
   if (warp < 4) {
-    if (warp == 0) run_producer(p, base, sm, lane);
-    else if (warp == 1) run_mma<F16, kTerms>(p, base, sm, tmem, lane);
-    else if (warp == 2) run_gates<F16, kTerms>(p, sm, lane);
-    else run_store(p, base, sm, lane);
+    if (warp == 0) run_producer<kStates>(p, base, sm, lane);
+    else if (warp == 1) run_mma<F16, kTerms, kStates>(p, base, sm, tmem, lane);
+    else if (warp == 2) run_gates<F16, kTerms, kStates>(p, sm, lane);
+    else if (!kStates) run_store(p, base, sm, lane);
   } else if (warp < 4 + kPoWarps) {
-    run_po<F16>(p, base, sm, tmem, warp, lane);
+    if (!kStates) run_po<F16>(p, base, sm, tmem, warp, lane);
   } else {
-    run_ks<F16, kTerms>(p, base, sm, tmem, warp, lane);
+    run_ks<F16, kTerms, kStates>(p, base, sm, tmem, warp, lane);
   }
   tc_fence_before();
   __syncthreads();
   if (warp == 0) tmem_dealloc(tmem, kTmCols);
 }
 
-template <bool F16, int kTerms>
-cudaError_t launch(const DecayPrefillParams& p, cudaStream_t stream) {
+// ------------------------------------------------------------ joining segments
+// In f32, the state behind each segment: S <- decay S + what the segment added.  A thread takes
+// four values of one unit through all segments; their loads do not wait for one another.
+constexpr int kJoinThreads = 256;
+__global__ void __launch_bounds__(kJoinThreads) gdn_decay_join_kernel(float* ws, const float* decay, int blocks) {
+  constexpr int kCtas = D * D / 4 / kJoinThreads;  // of a unit
+  const int64_t unit = blockIdx.x / kCtas;
+  float4* s = reinterpret_cast<float4*>(ws + unit * blocks * (D * D)) + (blockIdx.x % kCtas) * kJoinThreads + threadIdx.x;
+  const float* d = decay + unit * blocks;
+  float4 x = *s;
+#pragma unroll 8
+  for (int b = 1; b < blocks; ++b) {
+    const float4 y = s[b * (D * D / 4)];
+    const float g = d[b];
+    x = make_float4(fmaf(g, x.x, y.x), fmaf(g, x.y, y.y), fmaf(g, x.z, y.z), fmaf(g, x.w, y.w));
+    s[b * (D * D / 4)] = x;
+  }
+}
+
+template <bool F16, int kTerms, bool kStates>
+cudaError_t launch_pass(const DecayPrefillParams& p, int sms, cudaStream_t stream) {
   static thread_local int device = -1, generation = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   const int gen = launch_config_generation();
   if (e == cudaSuccess && (device != dev || generation != gen)) {
-    e = cudaFuncSetAttribute(gdn_decay_prefill_kernel<F16, kTerms>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    e = cudaFuncSetAttribute(gdn_decay_prefill_kernel<F16, kTerms, kStates>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e == cudaSuccess) { device = dev; generation = gen; }
   }
   if (e != cudaSuccess) return e;
-  const int64_t units = (int64_t)p.N * p.H;
-  const int sms = device_sm_count();
-  gdn_decay_prefill_kernel<F16, kTerms><<<(unsigned)(units < sms ? units : sms), kThreads, kSmem, stream>>>(p);
+  const int64_t units = (int64_t)p.N * p.H * (kStates ? p.splits - 1 : p.splits);
+  gdn_decay_prefill_kernel<F16, kTerms, kStates><<<(unsigned)(units < sms ? units : sms), kThreads, kSmem, stream>>>(p);
   return cudaGetLastError();
 }
 
+template <bool F16, int kTerms>
+cudaError_t launch(const DecayPrefillParams& p, cudaStream_t stream) {
+  const int sms = device_sm_count();
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  if (p.splits > 1) {
+    cudaError_t e = launch_pass<F16, kTerms, true>(p, sms, stream);
+    if (e != cudaSuccess) return e;
+    if (p.splits > 2) {
+      const int64_t ctas = (int64_t)p.N * p.H * (D * D / 4 / kJoinThreads);
+      gdn_decay_join_kernel<<<(unsigned)ctas, kJoinThreads, 0, stream>>>(p.ws, p.ws_decay, p.splits - 1);
+      e = cudaGetLastError();
+      if (e != cudaSuccess) return e;
+    }
+  }
+  return launch_pass<F16, kTerms, false>(p, sms, stream);
+}
+
 }  // namespace
+
+// Cost in chunks of a whole pass, with U units on a persistent grid of one CTA an SM.  Uncut: the
+// rounds times the chunks.  In P segments: the same for all U P segments, about half of it for the
+// U (P - 1) segments whose states are made first (two of four products, no scores), and two more
+// launches.  A cut has to save a tenth, and leaves two chunks or more to a segment.
+int decay_splits(int64_t units, double chunks, int sms) {
+  constexpr double kStatesCost = 0.5, kLaunches = 4.0;
+  constexpr int kMaxSplits = 32;
+  if (units <= 0 || sms <= 0) return 1;
+  auto rounds = [&](int64_t n) { return double((n + sms - 1) / sms); };
+  double best = 0.9 * rounds(units) * chunks;
+  int P = 1;
+  for (int c = 2; c <= kMaxSplits && chunks >= 2.0 * c; ++c) {
+    const double cost = (kStatesCost * rounds(units * (c - 1)) + rounds(units * c)) * (chunks / c) + kLaunches;
+    if (cost < best) { best = cost; P = c; }
+  }
+  return P;
+}
 
 cudaError_t launch_decay_prefill(const DecayPrefillParams& p, cudaStream_t stream) {
   if ((int64_t)p.N * p.H <= 0) return cudaSuccess;

@@ -309,13 +309,27 @@ gdn_status_t gdn_qk_norm_rope(const gdn_tensor_t* q, const gdn_tensor_t* k, cons
  * sequence and head, never those of another sequence.  With f16 inputs the state
  * enters the read-out in f16, so values beyond 65504 overflow there.
  *  batch_invariant  nonzero: never split a sequence, so every output and state bit depends
- *                   only on that sequence's own inputs.
+ *                   only on that sequence's own inputs.  Zero: where there are too few
+ *                   (sequence, head) units for the SMs, every sequence is cut into segments
+ *                   of whole 128-token chunks (a count that depends on the sizes and the SMs
+ *                   alone) and the call enqueues three kernels: the states that the
+ *                   segments add, their join, and the outputs of all segments.  Results are
+ *                   the same for every run, not the same bits as without.  The
+ *                   states live in the workspace that gdn_chunk_prefill's split calls use,
+ *                   under the same rules (growth, stream capture, one stream at a time);
+ *                   gdn_testing_force_splits forces the count here, too.
+ *
+ * gdn_decay_workspace_bytes: the workspace of such a call of `num_seqs` sequences,
+ * `num_heads` heads and `total_tokens` tokens in all on `num_sms` SMs; 0 when it does not
+ * split.  Pure host arithmetic, for gdn_reserve_workspace.
  */
 gdn_status_t gdn_decay_prefill(const gdn_tensor_t* q, const gdn_tensor_t* k, const gdn_tensor_t* v,
                                const gdn_tensor_t* g, float scale, const gdn_tensor_t* initial_state,
                                const gdn_tensor_t* state_indices, const gdn_tensor_t* output_state,
                                const gdn_tensor_t* cu_seqlens, int batch_invariant,
                                const gdn_tensor_t* output, cudaStream_t stream);
+
+size_t gdn_decay_workspace_bytes(int64_t num_seqs, int64_t num_heads, int64_t total_tokens, int num_sms);
 
 /*
  * gdn_decay_step: one token per batch row through the recurrence of gdn_decay_prefill, each

@@ -185,3 +185,19 @@ def test_wrappers_ask_for_bounds():
     a = prefill_args()
     with pytest.raises(ValueError):
         gdn.decay_linear_attention(a["q"], a["k"], a["v"], a["g"])
+
+
+def test_workspace_bytes_follow_the_plan():
+    """A state and a decay for each segment but the last; nothing where units fill the SMs."""
+    plan = gdn.gdn_decay_workspace_bytes
+    assert plan(0, 4, 100, 152) == 0 and plan(4, 0, 100, 152) == 0 and plan(4, 4, 100, 0) == 0
+    assert plan(512, 16, 512 * 4096, 152) == 0 and plan(1, 1, 256, 152) == 0
+    for args in ((1, 8, 32000, 152), (2, 32, 131072, 152), (1, 1, 1 << 20, 152)):
+        got = plan(*args)
+        blocks, rest = divmod(got, 65536 + 4)
+        assert rest == 0 and blocks % (args[0] * args[1]) == 0 and 1 <= blocks // (args[0] * args[1]) <= 31
+    try:
+        gdn.testing_force_splits(3)
+        assert plan(5, 4, 1000, 152) == 5 * 4 * 2 * (65536 + 4)
+    finally:
+        gdn.testing_force_splits(0)

@@ -280,3 +280,59 @@ def test_offsets_past_32_bits():
     want = gdn.decay_linear_attention(q, k, v, g, cu_seqlens=cu)
     assert torch.equal(gdn.decay_linear_attention(*spread, g, cu_seqlens=cu), want)
     assert math.isfinite(float(want.float().sum()))
+
+
+# ------------------------------------------------------------------------------- sequences cut into segments
+
+
+@pytest.mark.parametrize("splits", [2, 3, 5, 8])
+@pytest.mark.parametrize("dtype,state,init,pool", [(BF, F32, True, None), (BF, BF, True, 7), (HF, F32, False, None)], ids=str)
+def test_segments(force_split, splits, dtype, state, init, pool):
+    """Segments of whole chunks, some of them empty: every output and final state as uncut."""
+    force_split(splits)
+    run_and_check([1100, 0, 1, 129, 384], 2, 4, dtype, "head", state, init, pool, seed=30 + splits)
+
+
+@pytest.mark.parametrize("gate", ["token", "slow", "reset", "none"])
+def test_segments_and_gates(force_split, gate):
+    force_split(4)
+    run_and_check([900, 530], 1, 2, gate=gate, seed=40)
+
+
+def test_segments_skip_bad_sequences(force_split):
+    force_split(3)
+    lengths = [400, 300, 500]
+    q, k, v, g, cu = R.make(lengths, 1, 2, seed=41)
+    s0 = R.states(3, 2, F32, 41)
+    o_ref, s_ref = R.recurrence(q, k, v, g, SCALE, s0, lengths)
+    out, final = torch.zeros(1200, 2, 128, dtype=BF, device="cuda"), torch.zeros_like(s0)
+    gdn.decay_linear_attention(q, k, v, g, initial_state=s0, output_final_state=True, output_state=final, output=out,
+                               cu_seqlens=cu, state_indices=torch.tensor([0, 3, 2], device="cuda"))
+    assert gdn.device_status() == 2
+    R.check(out, o_ref, final, s_ref, lengths, which=(0, 2))
+    assert not bool(out[400:700].any()) and not bool(final[1].any())
+
+
+def test_planned_segments():
+    """Few heads and a long sequence: the library cuts it by itself, the same way every time."""
+    assert gdn.gdn_decay_workspace_bytes(1, 2, 9000) > 0 and gdn.gdn_decay_workspace_bytes(64, 16, 64 * 256) == 0
+    out, st = run_and_check([9000], 1, 2, gate="slow", seed=42)
+    again, st2 = run_and_check([9000], 1, 2, gate="slow", seed=42)
+    assert torch.equal(out, again) and torch.equal(st, st2)
+    whole, _ = run_and_check([9000], 1, 2, gate="slow", seed=42, batch_invariant=True)
+    assert R.rel(out, whole) <= R.OUT[BF]
+
+
+def test_segments_in_a_graph():
+    q, k, v, g, cu = R.make([9000], 2, 2, gate="head", seed=43)
+    need = gdn.gdn_decay_workspace_bytes(1, 2, 9000)
+    gdn.gdn_reserve_workspace(need)
+    out, st = torch.empty(9000, 2, 128, dtype=BF, device="cuda"), torch.empty(1, 2, 128, 128, device="cuda")
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        gdn.decay_linear_attention(q, k, v, g, output_final_state=True, cu_seqlens=cu, output=out, output_state=st)
+    for x in (q, k, v):
+        x.copy_(torch.randn_like(x))
+    graph.replay()
+    o_ref, s_ref = R.recurrence(q, k, v, g, SCALE, None, [9000])
+    R.check(out, o_ref, st, s_ref, [9000])
