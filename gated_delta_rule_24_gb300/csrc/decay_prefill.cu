@@ -13,7 +13,7 @@
 // below) against 128 KB of q, k, v and o: the bytes bound it once the products of one chunk
 // run without a pause, and that is what the layout is for.
 //
-// One persistent CTA per SM walks (sequence, head) units chunk by chunk.  Roles (20 warps):
+// One persistent CTA per SM walks (sequence, head) units chunk by chunk.  Roles (24 warps):
 //   warp 0      TMA loads of Q, K, V (two stages) and the unit records;
 //   warp 1      issues every product: Q K^T, Q S^T, V_d^T K, P V of a chunk in this order,
 //               so that P is built while Q S^T and V_d^T K run, and the state is read out
@@ -22,8 +22,9 @@
 //   warp 3      stores of the output tile;
 //   warps 4-11  two threads a token: P (tcgen05.ld, decay, mask, back to TMEM as the A operand
 //               of P V), the 2^G_i of Q S^T in place, and the output tile;
-//   warps 12-19 two threads a value row: the state in registers (f32, 64 values a thread),
-//               its 16-bit copy in shared memory for Q S^T, and V_d.
+//   warps 12-15 one thread a value row: the state in TMEM, times the chunk's decay, and its
+//               16-bit copy in shared memory for Q S^T;
+//   warps 16-23 V_d, from V in shared memory to TMEM.
 // Hand-offs are mbarriers, every wait is bounded and ends early when any role gave up.
 //
 // The state never waits in TMEM: V_d^T K goes to a buffer of its own, and S <- gamma S + it
@@ -87,7 +88,7 @@ struct Small {
   uint64_t qk_done, qs_done, s_done, o_done;   // products that have completed
   uint64_t q_ready, p_ready, o_free, o_staged;  // warps 4-11
   uint64_t o_stored;                            // warp 3
-  uint64_t s_ready, vd_full[4];                // warps 12-19
+  uint64_t s_ready, vd_full[4];                // warps 12-15, 16-23
   uint64_t vd_empty[4], drain;
   uint32_t tmem;
   int32_t abort;
@@ -109,21 +110,20 @@ constexpr uint32_t kTmVd = 448;
 __device__ __forceinline__ uint32_t vd_slot_col(int slot) { return slot < 2 ? kTmVd + 32 * slot : kTmQ + 32 * (slot - 2); }
 constexpr uint32_t kTmCols = 512;
 
-constexpr int kThreads = 640;
-constexpr int kPoWarps = 8, kKsWarps = 8;
-static_assert(kThreads == 32 * (4 + kPoWarps + kKsWarps), "roles");
-
+constexpr int kPoWarps = 8, kSWarps = 4, kVWarps = 8;
+constexpr int kThreads = 32 * (4 + kPoWarps + kSWarps + kVWarps);
 // Every wait: bounded (kTries probes of up to 20 us each), and over as soon as another role has
-// given up.
+// given up.  Only the first probe is in line: the roles together fill the instruction cache.
 constexpr int kTries = 50000;
-__device__ __forceinline__ bool probe(uint64_t* bar, uint32_t parity) { return __all_sync(0xffffffffu, mbar_try_wait(bar, parity)); }
-__device__ __forceinline__ bool wait(Small* sm, uint64_t* bar, uint32_t parity) {
-  if (probe(bar, parity)) return true;
+__device__ __noinline__ bool wait_slow(const volatile int32_t* abort, uint64_t* bar, uint32_t parity) {
   bool ok = false;
 #pragma unroll 1
-  for (int i = 0; i < kTries && !ok && !*reinterpret_cast<volatile int32_t*>(&sm->abort); ++i)
-    ok = mbar_try_wait_sleep(bar, parity, 20000u);
+  for (int i = 0; i < kTries && !ok && !*abort; ++i) ok = mbar_try_wait_sleep(bar, parity, 20000u);
   return __all_sync(0xffffffffu, ok);
+}
+__device__ __forceinline__ bool wait(Small* sm, uint64_t* bar, uint32_t parity) {
+  if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
+  return wait_slow(&sm->abort, bar, parity);
 }
 // The same for copies and products under way when a CTA ends, whoever gave up.
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
@@ -295,7 +295,7 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
         __syncwarp();
       }
       // V_d^T K
-#pragma unroll
+#pragma unroll 1
       for (int b = 0; b < kSubs; ++b) {
         int slot, round;
         vd_place<kTerms>(ci, b, &slot, &round);
@@ -583,7 +583,7 @@ __device__ __forceinline__ void run_po(const DecayPrefillParams& p, uint8_t* bas
   if (failed && lane == 0) give_up(p, sm);
 }
 
-// ------------------------------------------------------------ warps 12-19: the state
+// ------------------------------------------------------------ warps 12-15: the state
 // 32 values of a state row, as the bits of f32.
 __device__ __forceinline__ void load_state32(const void* base, int dtype, int64_t off, uint32_t (&s)[32]) {
   if (dtype == kF32) {
@@ -659,12 +659,11 @@ __device__ __forceinline__ void zero_tails(uint8_t* k, uint8_t* v, int left, int
   __syncwarp();
 }
 
-template <bool F16, int kTerms, bool kStates>
-__device__ __forceinline__ void run_ks(const DecayPrefillParams& p, uint8_t* base, Small* sm, uint32_t tmem, int warp, int lane) {
-  constexpr int kSub = sub_tokens<kTerms>(), kSubs = C / kSub;
-  const int w = warp & 3, hf = (warp >> 2) - 3, row = 32 * w + lane;  // warps 12-15: columns 0 .. 63, 16-19: 64 .. 127
-  const uint32_t tq = tmem + ((uint32_t)(32 * w) << 16);
-  uint8_t* sb = base + kOffS + hf * kHalf;
+template <bool F16, bool kStates>
+__device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* base, Small* sm, uint32_t tmem, int warp, int lane) {
+  const int w = warp & 3, row = 32 * w + lane;
+  const uint32_t ts = tmem + ((uint32_t)(32 * w) << 16) + kTmS;
+  uint8_t* sb = base + kOffS;
   bool failed = false;
   Rec r{};
   int ci = 0;
@@ -678,81 +677,25 @@ __device__ __forceinline__ void run_ks(const DecayPrefillParams& p, uint8_t* bas
       for (int e = 0; e < 32; ++e) x[e] = 0u;
     }
   };
-  // V_d of tokens [sub * kSub, + kSub) of chunk `at`: transposed fragments of V (pairs of tokens,
-  // one value each) times d, as kTerms 16-bit terms.  The four warps of a half make the parts of
-  // their own slots (sub % 2 == hf).
-  const int m = lane >> 3, lr = lane & 7;
-  auto make_vd = [&](int at, int sub) {
-    int slot, round;
-    vd_place<kTerms>(at, sub, &slot, &round);
-    if (round > 0 && !wait(sm, &sm->vd_empty[slot], (round - 1) & 1)) return false;
-    if (!kStates && slot >= 2 && !wait(sm, &sm->qs_done, at & 1)) return false;
-    tc_fence_after();
-    const uint32_t va = smem_u32(base + kOffKv + ((at & 1) * 2 + 1) * kTile);
-    const float* dv = sm->d[at & 1];
-#pragma unroll
-    for (int tt = 0; tt < kSub / 16; ++tt) {
-      const int tok = sub * kSub + 16 * tt;  // 16 tokens from here
-      const int trow = tok + (m >> 1) * 8 + lr;
-      const int at2 = (tok >> 1) + (lane & 3);  // this lane's first pair of tokens; the second is 4 pairs on
-#pragma unroll
-      for (int dd = 0; dd < 2; ++dd) {
-        const int ch = 4 * w + 2 * dd + (m & 1);
-        const uint32_t to = tq + ((uint32_t)(16 * dd) << 16) + vd_slot_col(slot) + 8 * tt;
-        uint32_t a[4], t[4];
-        ldmatrix_x4_trans(va + (ch >> 3) * kHalf + sw128_chunk(trow, ch & 7), a);
-        if (kTerms == 2) {
-          // three packed 16-bit operations
-          const uint32_t* dh = reinterpret_cast<const uint32_t*>(dv) + at2;
-          uint32_t rest[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint32_t h = dh[2 * (e & 2)], l = dh[C / 2 + 2 * (e & 2)];
-            split_product<F16>(a[e], h, l, &t[e], &rest[e]);
-          }
-          tmem_st16x128_x2(to, t);
-          tmem_st16x128_x2(to + kSub / 2, rest);
-        } else {
-          float2 x[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e) x[e] = mul2(unpack16<F16>(a[e]), reinterpret_cast<const float2*>(dv)[at2 + 2 * (e & 2)]);
-#pragma unroll
-          for (int term = 0; term < kTerms; ++term) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-              t[e] = pack16x2<F16>(x[e]);
-              if (term + 1 < kTerms) x[e] = fma2(unpack16<F16>(t[e]), pair(-1.f), x[e]);
-            }
-            tmem_st16x128_x2(to + term * (kSub / 2), t);
-          }
-        }
-      }
-    }
-    tmem_st_wait();
-    tc_fence_before();
-    warp_arrive(&sm->vd_full[slot], lane);
-    return true;
-  };
   for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
     for (int c = 0; c < r.nch; ++c, ++ci) {
-      const int st = ci & 1, left = r.len - c * C;
-      const uint32_t ph = (ci >> 1) & 1;
+      const int st = ci & 1;
       // S as the chunk finds it: to 16 bits for Q S^T, times the chunk's decay for V_d^T K
-      if (!(wait(sm, &sm->gate_full[st], ph) && (c == 0 || wait(sm, &sm->s_done, (ci - 1) & 1)))) { failed = true; break; }
+      if (!(wait(sm, &sm->gate_full[st], (ci >> 1) & 1) && (c == 0 || wait(sm, &sm->s_done, (ci - 1) & 1)))) { failed = true; break; }
       tc_fence_after();
       const float2 gam = pair(sm->gamma[st]);
 #pragma unroll 1
-      for (int q = 0; q < 2; ++q) {
+      for (int q = 0; q < 4; ++q) {
         uint32_t x[32];
         if (c == 0) {
-          load_in(64 * hf + 32 * q, x);
+          load_in(32 * q, x);
         } else {
-          tmem_ld32(tq + kTmS + 64 * hf + 32 * q, x);
+          tmem_ld32(ts + 32 * q, x);
           tmem_ld_wait();
         }
 #pragma unroll
         for (int e = 0; e < 4 && !kStates; ++e)
-          *reinterpret_cast<uint4*>(sb + sw128_chunk(row, 4 * q + e)) =
+          *reinterpret_cast<uint4*>(sb + (q >> 1) * kHalf + sw128_chunk(row, 4 * (q & 1) + e)) =
               make_uint4(pack16x2<F16>(pair_at(x + 8 * e)), pack16x2<F16>(pair_at(x + 8 * e + 2)),
                          pack16x2<F16>(pair_at(x + 8 * e + 4)), pack16x2<F16>(pair_at(x + 8 * e + 6)));
 #pragma unroll
@@ -761,42 +704,111 @@ __device__ __forceinline__ void run_ks(const DecayPrefillParams& p, uint8_t* bas
           x[e] = __float_as_uint(y.x);
           x[e + 1] = __float_as_uint(y.y);
         }
-        tmem_st32(tq + kTmS + 64 * hf + 32 * q, x);
+        tmem_st32(ts + 32 * q, x);
       }
       if (!kStates) fence_proxy_async_smem();
       tmem_st_wait();
       tc_fence_before();
       warp_arrive(&sm->s_ready, lane);
-      if (!wait(sm, &sm->v_full[st], ph)) { failed = true; break; }
-      if (left < C) {
-        if (!wait(sm, &sm->k_full[st], ph)) { failed = true; break; }
-        uint8_t* k = base + kOffKv + st * 2 * kTile;
-        zero_tails<kTerms>(k, k + kTile, left, w, hf, lane);
-      }
-#pragma unroll 1
-      for (int sub = hf; sub < kSubs && !failed; sub += 2) failed = !make_vd(ci, sub);
-      if (failed) break;
-      warp_arrive(&sm->gate_empty[st], lane);
+      if (lane == 0) mbar_arrive(&sm->gate_empty[st]);
     }
     if (failed) break;
-    // the state that the sequence leaves (an empty one passes on what it got); the next unit may
+    // the state that the unit leaves (an empty one passes on what it got); the next unit may
     // overwrite TMEM and the 16-bit copy after that, Q S^T having run before
     if (r.nch > 0 && !wait(sm, &sm->s_done, (ci - 1) & 1)) { failed = true; break; }
     if (r.out == kNone || (r.out == kPool && !p.s_out)) continue;
     tc_fence_after();
 #pragma unroll 1
-    for (int q = 0; q < 2; ++q) {
+    for (int q = 0; q < 4; ++q) {
       uint32_t x[32];
       if (r.nch == 0) {
-        load_in(64 * hf + 32 * q, x);
+        load_in(32 * q, x);
       } else {
-        tmem_ld32(tq + kTmS + 64 * hf + 32 * q, x);
+        tmem_ld32(ts + 32 * q, x);
         tmem_ld_wait();
       }
-      const int64_t at = row * D + 64 * hf + 32 * q;
+      const int64_t at = row * D + 32 * q;
       if (r.out >= 0) store_state32(p.ws, kF32, (int64_t)r.out * (D * D) + at, x);
       else store_state32(p.s_out, p.sout_dtype, r.slot * p.sout_slot + (int64_t)r.h * p.sout_head + at, x);
     }
+  }
+  if (failed && lane == 0) give_up(p, sm);
+}
+
+// ------------------------------------------------------------ warps 16-23: V_d
+// Transposed fragments of V (pairs of tokens, one value each) times d, as kTerms 16-bit terms.  Each
+// warp makes 32 values of the parts of its half's slots (part % 2 == hf).
+template <bool F16, int kTerms, bool kStates>
+__device__ __forceinline__ void run_v(const DecayPrefillParams& p, uint8_t* base, Small* sm, uint32_t tmem, int warp, int lane) {
+  constexpr int kSub = sub_tokens<kTerms>(), kSubs = C / kSub;
+  const int w = warp & 3, hf = (warp >> 2) & 1;
+  const uint32_t tq = tmem + ((uint32_t)(32 * w) << 16);
+  const int m = lane >> 3, lr = lane & 7;
+  bool failed = false;
+  Rec r;
+  int ci = 0;
+  for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
+    for (int c = 0; c < r.nch; ++c, ++ci) {
+      const int st = ci & 1, left = r.len - c * C;
+      const uint32_t ph = (ci >> 1) & 1;
+      if (!(wait(sm, &sm->gate_full[st], ph) && wait(sm, &sm->v_full[st], ph))) { failed = true; break; }
+      uint8_t* k = base + kOffKv + st * 2 * kTile;
+      if (left < C) {
+        if (!wait(sm, &sm->k_full[st], ph)) { failed = true; break; }
+        zero_tails<kTerms>(k, k + kTile, left, w, hf, lane);
+      }
+      const uint32_t va = smem_u32(k + kTile);
+#pragma unroll 1
+      for (int sub = hf; sub < kSubs; sub += 2) {
+        int slot, round;
+        vd_place<kTerms>(ci, sub, &slot, &round);
+        if (!((round == 0 || wait(sm, &sm->vd_empty[slot], (round - 1) & 1)) &&
+              (kStates || slot < 2 || wait(sm, &sm->qs_done, ci & 1)))) { failed = true; break; }
+        tc_fence_after();
+#pragma unroll
+        for (int tt = 0; tt < kSub / 16; ++tt) {
+          const int tok = sub * kSub + 16 * tt;  // 16 tokens from here
+          const int trow = tok + (m >> 1) * 8 + lr;
+          const int at2 = (tok >> 1) + (lane & 3);  // this lane's first pair of tokens; the second is 4 pairs on
+#pragma unroll
+          for (int dd = 0; dd < 2; ++dd) {
+            const int ch = 4 * w + 2 * dd + (m & 1);
+            const uint32_t to = tq + ((uint32_t)(16 * dd) << 16) + vd_slot_col(slot) + 8 * tt;
+            uint32_t a[4], t[4];
+            ldmatrix_x4_trans(va + (ch >> 3) * kHalf + sw128_chunk(trow, ch & 7), a);
+            if (kTerms == 2) {
+              // three packed 16-bit operations
+              const uint32_t* dh = reinterpret_cast<const uint32_t*>(sm->d[st]) + at2;
+              uint32_t rest[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) split_product<F16>(a[e], dh[2 * (e & 2)], dh[C / 2 + 2 * (e & 2)], &t[e], &rest[e]);
+              tmem_st16x128_x2(to, t);
+              tmem_st16x128_x2(to + kSub / 2, rest);
+            } else {
+              float2 x[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                x[e] = mul2(unpack16<F16>(a[e]), reinterpret_cast<const float2*>(sm->d[st])[at2 + 2 * (e & 2)]);
+#pragma unroll
+              for (int term = 0; term < kTerms; ++term) {
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                  t[e] = pack16x2<F16>(x[e]);
+                  if (term + 1 < kTerms) x[e] = fma2(unpack16<F16>(t[e]), pair(-1.f), x[e]);
+                }
+                tmem_st16x128_x2(to + term * (kSub / 2), t);
+              }
+            }
+          }
+        }
+        tmem_st_wait();
+        tc_fence_before();
+        warp_arrive(&sm->vd_full[slot], lane);
+      }
+      if (failed) break;
+      if (lane == 0) mbar_arrive(&sm->gate_empty[st]);
+    }
+    if (failed) break;
   }
   if (failed && lane == 0) give_up(p, sm);
 }
@@ -817,9 +829,9 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __
     init(sm->v_full, 2, 1);
     init(sm->kv_empty, 2, 1);
     init(sm->rec_full, kRecs, 1);
-    init(sm->rec_empty, kRecs, kStates ? 2 + kKsWarps : 3 + kPoWarps + kKsWarps);
+    init(sm->rec_empty, kRecs, (kStates ? 2 : 3 + kPoWarps) + kSWarps + kVWarps);
     init(sm->gate_full, 2, 1);
-    init(sm->gate_empty, 2, kStates ? kKsWarps : kPoWarps + kKsWarps);
+    init(sm->gate_empty, 2, (kStates ? 0 : kPoWarps) + kSWarps + kVWarps);
     init(&sm->cf_empty, 1, kPoWarps);
     init(&sm->qk_done, 1, 1);
     init(&sm->qs_done, 1, 1);
@@ -830,8 +842,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __
     init(&sm->o_staged, 1, kPoWarps);
     init(&sm->q_ready, 1, kPoWarps);
     init(&sm->o_stored, 1, 1);
-    init(&sm->s_ready, 1, kKsWarps);
-    init(sm->vd_full, 4, kKsWarps / 2);
+    init(&sm->s_ready, 1, kSWarps);
+    init(sm->vd_full, 4, kVWarps / 2);
     init(sm->vd_empty, 4, 1);
     init(&sm->drain, 1, 1);
     sm->abort = 0;
@@ -856,8 +868,10 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __
     else if (!kStates) run_store(p, base, sm, lane);
   } else if (warp < 4 + kPoWarps) {
     if (!kStates) run_po<F16>(p, base, sm, tmem, warp, lane);
+  } else if (warp < 4 + kPoWarps + kSWarps) {
+    run_state<F16, kStates>(p, base, sm, tmem, warp, lane);
   } else {
-    run_ks<F16, kTerms, kStates>(p, base, sm, tmem, warp, lane);
+    run_v<F16, kTerms, kStates>(p, base, sm, tmem, warp, lane);
   }
   tc_fence_before();
   __syncthreads();
