@@ -59,6 +59,21 @@ constexpr int C = kDecayChunk;
 constexpr int D = kHeadDim;
 static_assert(C == 128 && D == 128, "the layouts below are those of 128 x 128 tiles");
 
+// ------------------------------------------------------------ TMEM (columns)
+constexpr uint32_t kTmAcc = 0;     // Q K^T (128), then P as packed pairs
+constexpr uint32_t kTmO = 128;     // Q S^T, then the output
+constexpr uint32_t kTmS = 256;     // S, f32 (128)
+constexpr uint32_t kTmQ = 384;     // Q as packed pairs (64)
+// P takes 16 columns for a block of 32 tokens: the first two blocks in front, the last two behind, so
+// that a block goes over columns that its own warps have read.
+__device__ __forceinline__ uint32_t p_block_col(int jb) { return kTmAcc + 16 * jb + (jb >= 2 ? 64 : 0); }
+// V_d terms as packed pairs, in slots of up to 64 columns: one of its own, one over Q, which is free
+// from Q S^T to the next chunk's copy, and one between the blocks of P.
+constexpr uint32_t kTmVd = 448;
+constexpr int kVdSlots = 3;
+__device__ __forceinline__ uint32_t vd_slot_col(int slot) { return slot == 0 ? kTmVd : slot == 1 ? kTmQ : kTmAcc + 32; }
+constexpr uint32_t kTmCols = 512;
+
 // ------------------------------------------------------------ shared memory (bytes)
 constexpr uint32_t kTile = C * D * 2;       // a 16-bit tile: two 128B-swizzled halves of 64 columns
 constexpr uint32_t kHalf = kTile / 2;
@@ -88,27 +103,13 @@ struct Small {
   uint64_t qk_done, qs_done, s_done, o_done;   // products that have completed
   uint64_t q_ready, p_ready, o_free, o_staged;  // warps 4-11
   uint64_t o_stored;                            // warp 3
-  uint64_t s_ready, vd_full[4];                // warps 12-15, 16-23
-  uint64_t vd_empty[4], drain;
+  uint64_t s_ready, vd_full[kVdSlots];         // warps 12-15, 16-23
+  uint64_t vd_empty[kVdSlots], drain;
   uint32_t tmem;
   int32_t abort;
 };
 constexpr uint32_t kSmem = kOffSmall + sizeof(Small);
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
-
-// ------------------------------------------------------------ TMEM (columns)
-constexpr uint32_t kTmAcc = 0;     // Q K^T (128), then P as packed pairs
-constexpr uint32_t kTmO = 128;     // Q S^T, then the output
-constexpr uint32_t kTmS = 256;     // S, f32 (128)
-constexpr uint32_t kTmQ = 384;     // Q as packed pairs (64)
-// P takes 16 columns for a block of 32 tokens: the first two blocks in front, the last two behind, so
-// that a block goes over columns that its own warps have read.
-__device__ __forceinline__ uint32_t p_block_col(int jb) { return kTmAcc + 16 * jb + (jb >= 2 ? 64 : 0); }
-// V_d terms as packed pairs, in four slots of 32: two of their own, two over Q, which is free from
-// Q S^T to the next chunk's copy.
-constexpr uint32_t kTmVd = 448;
-__device__ __forceinline__ uint32_t vd_slot_col(int slot) { return slot < 2 ? kTmVd + 32 * slot : kTmQ + 32 * (slot - 2); }
-constexpr uint32_t kTmCols = 512;
 
 constexpr int kPoWarps = 8, kSWarps = 4, kVWarps = 8;
 constexpr int kThreads = 32 * (4 + kPoWarps + kSWarps + kVWarps);
@@ -240,15 +241,14 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
 }
 
 // ------------------------------------------------------------ warp 1: products
-// V_d is made in parts of kSub tokens, kSub / 2 columns a term.  Part b goes to slot b % 2 in the
-// first half of the chunk, 2 + b % 2 in the second: each slot is used kSubs / 4 times a chunk.
+// V_d is made in parts of kSub tokens, kSub / 2 columns a term: two of 64 tokens in slots 0 and 1, or,
+// with three terms, four of 32 in slots 0, 1, 0 and 2.
 template <int kTerms>
-__host__ __device__ constexpr int sub_tokens() { return kTerms == 2 ? 32 : 16; }
+__host__ __device__ constexpr int sub_tokens() { return kTerms == 2 ? 64 : 32; }
 template <int kTerms>
-__device__ __forceinline__ void vd_place(int ci, int b, int* slot, int* round) {
-  constexpr int kSubs = C / sub_tokens<kTerms>();
-  *slot = (b & 1) + (b >= kSubs / 2 ? 2 : 0);
-  *round = ci * (kSubs / 4) + (b % (kSubs / 2)) / 2;  // uses of the slot before
+__device__ __forceinline__ void vd_place(int ci, int b, int* slot, int* round) {  // round: uses of the slot before
+  *slot = kTerms == 2 ? b : b == 3 ? 2 : b & 1;
+  *round = kTerms == 3 && *slot == 0 ? 2 * ci + (b >> 1) : ci;
 }
 
 template <bool F16, int kTerms, bool kStates>
@@ -533,6 +533,7 @@ __device__ __forceinline__ void run_po(const DecayPrefillParams& p, uint8_t* bas
         }
         tmem_st16(tr + p_block_col(jb), pk);
       }
+      tc_fence_before();
       warp_arrive(&sm->cf_empty, lane);
       // Q S^T of the row times scale 2^G_i
       if (!wait(sm, &sm->qs_done, one)) { failed = true; break; }
@@ -644,14 +645,12 @@ __device__ __forceinline__ void split_product(uint32_t a, uint32_t dh, uint32_t 
   else go(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&dh), *reinterpret_cast<__nv_bfloat162*>(&mh), *reinterpret_cast<__nv_bfloat162*>(&dl));
 }
 
-// Zero this warp's share of the rows past the end, in the tokens of the parts that its half makes:
-// 32 columns of K, and of V exactly what the warp reads below.
-template <int kTerms>
-__device__ __forceinline__ void zero_tails(uint8_t* k, uint8_t* v, int left, int w, int hf, int lane) {
-  for (int e = lane; e < C * 4; e += 32) {
-    const int row = e >> 2, ch = 4 * w + (e & 3);  // 16-byte chunk of the 128 columns
-    if (row < left || ((row / sub_tokens<kTerms>()) & 1) != hf) continue;
-    const uint32_t at = (ch >> 3) * kHalf + sw128_chunk(row, ch & 7);
+// Zero this warp's share of the rows past the end: 16 columns (two 16-byte chunks from ch0) of K, and of
+// V, exactly what the warp reads below.
+__device__ __forceinline__ void zero_tails(uint8_t* k, uint8_t* v, int left, int ch0, int lane) {
+  for (int e = 2 * left + lane; e < C * 2; e += 32) {
+    const int ch = ch0 + (e & 1);
+    const uint32_t at = (ch >> 3) * kHalf + sw128_chunk(e >> 1, ch & 7);
     *reinterpret_cast<uint4*>(k + at) = make_uint4(0, 0, 0, 0);
     *reinterpret_cast<uint4*>(v + at) = make_uint4(0, 0, 0, 0);
   }
@@ -736,14 +735,15 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
 }
 
 // ------------------------------------------------------------ warps 16-23: V_d
-// Transposed fragments of V (pairs of tokens, one value each) times d, as kTerms 16-bit terms.  Each
-// warp makes 32 values of the parts of its half's slots (part % 2 == hf).
+// Transposed fragments of V (pairs of tokens, one value each) times d, as kTerms 16-bit terms, 16
+// values a warp.
 template <bool F16, int kTerms, bool kStates>
 __device__ __forceinline__ void run_v(const DecayPrefillParams& p, uint8_t* base, Small* sm, uint32_t tmem, int warp, int lane) {
   constexpr int kSub = sub_tokens<kTerms>(), kSubs = C / kSub;
   const int w = warp & 3, hf = (warp >> 2) & 1;
-  const uint32_t tq = tmem + ((uint32_t)(32 * w) << 16);
+  const uint32_t tq = tmem + ((uint32_t)(32 * w + 16 * hf) << 16);
   const int m = lane >> 3, lr = lane & 7;
+  const int ch = 4 * w + 2 * hf + (m & 1);  // this lane's 16-byte chunk of a row of V
   bool failed = false;
   Rec r;
   int ci = 0;
@@ -755,49 +755,45 @@ __device__ __forceinline__ void run_v(const DecayPrefillParams& p, uint8_t* base
       uint8_t* k = base + kOffKv + st * 2 * kTile;
       if (left < C) {
         if (!wait(sm, &sm->k_full[st], ph)) { failed = true; break; }
-        zero_tails<kTerms>(k, k + kTile, left, w, hf, lane);
+        zero_tails(k, k + kTile, left, 4 * w + 2 * hf, lane);
       }
-      const uint32_t va = smem_u32(k + kTile);
+      const uint32_t va = smem_u32(k + kTile) + (ch >> 3) * kHalf;
 #pragma unroll 1
-      for (int sub = hf; sub < kSubs; sub += 2) {
+      for (int sub = 0; sub < kSubs; ++sub) {
         int slot, round;
         vd_place<kTerms>(ci, sub, &slot, &round);
         if (!((round == 0 || wait(sm, &sm->vd_empty[slot], (round - 1) & 1)) &&
-              (kStates || slot < 2 || wait(sm, &sm->qs_done, ci & 1)))) { failed = true; break; }
+              (kStates || slot != 1 || wait(sm, &sm->qs_done, ci & 1)) &&
+              (kStates || slot != 2 || wait(sm, &sm->cf_empty, ci & 1)))) { failed = true; break; }
         tc_fence_after();
 #pragma unroll
         for (int tt = 0; tt < kSub / 16; ++tt) {
           const int tok = sub * kSub + 16 * tt;  // 16 tokens from here
-          const int trow = tok + (m >> 1) * 8 + lr;
           const int at2 = (tok >> 1) + (lane & 3);  // this lane's first pair of tokens; the second is 4 pairs on
+          const uint32_t to = tq + vd_slot_col(slot) + 8 * tt;
+          uint32_t a[4], t[4];
+          ldmatrix_x4_trans(va + sw128_chunk(tok + (m >> 1) * 8 + lr, ch & 7), a);
+          if (kTerms == 2) {
+            // three packed 16-bit operations
+            const uint32_t* dh = reinterpret_cast<const uint32_t*>(sm->d[st]) + at2;
+            uint32_t rest[4];
 #pragma unroll
-          for (int dd = 0; dd < 2; ++dd) {
-            const int ch = 4 * w + 2 * dd + (m & 1);
-            const uint32_t to = tq + ((uint32_t)(16 * dd) << 16) + vd_slot_col(slot) + 8 * tt;
-            uint32_t a[4], t[4];
-            ldmatrix_x4_trans(va + (ch >> 3) * kHalf + sw128_chunk(trow, ch & 7), a);
-            if (kTerms == 2) {
-              // three packed 16-bit operations
-              const uint32_t* dh = reinterpret_cast<const uint32_t*>(sm->d[st]) + at2;
-              uint32_t rest[4];
+            for (int e = 0; e < 4; ++e) split_product<F16>(a[e], dh[2 * (e & 2)], dh[C / 2 + 2 * (e & 2)], &t[e], &rest[e]);
+            tmem_st16x128_x2(to, t);
+            tmem_st16x128_x2(to + kSub / 2, rest);
+          } else {
+            float2 x[4];
 #pragma unroll
-              for (int e = 0; e < 4; ++e) split_product<F16>(a[e], dh[2 * (e & 2)], dh[C / 2 + 2 * (e & 2)], &t[e], &rest[e]);
-              tmem_st16x128_x2(to, t);
-              tmem_st16x128_x2(to + kSub / 2, rest);
-            } else {
-              float2 x[4];
+            for (int e = 0; e < 4; ++e)
+              x[e] = mul2(unpack16<F16>(a[e]), reinterpret_cast<const float2*>(sm->d[st])[at2 + 2 * (e & 2)]);
 #pragma unroll
-              for (int e = 0; e < 4; ++e)
-                x[e] = mul2(unpack16<F16>(a[e]), reinterpret_cast<const float2*>(sm->d[st])[at2 + 2 * (e & 2)]);
+            for (int term = 0; term < kTerms; ++term) {
 #pragma unroll
-              for (int term = 0; term < kTerms; ++term) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                  t[e] = pack16x2<F16>(x[e]);
-                  if (term + 1 < kTerms) x[e] = fma2(unpack16<F16>(t[e]), pair(-1.f), x[e]);
-                }
-                tmem_st16x128_x2(to + term * (kSub / 2), t);
+              for (int e = 0; e < 4; ++e) {
+                t[e] = pack16x2<F16>(x[e]);
+                if (term + 1 < kTerms) x[e] = fma2(unpack16<F16>(t[e]), pair(-1.f), x[e]);
               }
+              tmem_st16x128_x2(to + term * (kSub / 2), t);
             }
           }
         }
@@ -843,8 +839,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __
     init(&sm->q_ready, 1, kPoWarps);
     init(&sm->o_stored, 1, 1);
     init(&sm->s_ready, 1, kSWarps);
-    init(sm->vd_full, 4, kVWarps / 2);
-    init(sm->vd_empty, 4, 1);
+    init(sm->vd_full, kVdSlots, kVWarps);
+    init(sm->vd_empty, kVdSlots, 1);
     init(&sm->drain, 1, 1);
     sm->abort = 0;
     fence_mbar_init();
