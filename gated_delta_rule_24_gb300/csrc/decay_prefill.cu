@@ -68,10 +68,14 @@ constexpr uint32_t kTmQ = 384;     // Q as packed pairs (64)
 // that a block goes over columns that its own warps have read.
 __device__ __forceinline__ uint32_t p_block_col(int jb) { return kTmAcc + 16 * jb + (jb >= 2 ? 64 : 0); }
 // V_d terms as packed pairs, in slots of up to 64 columns: one of its own, one over Q, which is free
-// from Q S^T to the next chunk's copy, and one between the blocks of P.
+// from Q S^T to the next chunk's copy, and one between the blocks of P.  A launch that makes states
+// alone has the columns of the scores and the output for four.
 constexpr uint32_t kTmVd = 448;
-constexpr int kVdSlots = 3;
-__device__ __forceinline__ uint32_t vd_slot_col(int slot) { return slot == 0 ? kTmVd : slot == 1 ? kTmQ : kTmAcc + 32; }
+constexpr int kVdSlots = 4;
+template <bool kStates>
+__device__ __forceinline__ uint32_t vd_slot_col(int slot) {
+  return kStates ? kTmAcc + 64 * slot : slot == 0 ? kTmVd : slot == 1 ? kTmQ : kTmAcc + 32;
+}
 constexpr uint32_t kTmCols = 512;
 
 // ------------------------------------------------------------ shared memory (bytes)
@@ -160,7 +164,9 @@ __device__ __forceinline__ bool next_unit(Small* sm, int u, int lane, Rec* r, bo
 }
 
 // ------------------------------------------------------------ warp 0: loads
-// kStates, here and below: the launch makes the states that the segments add, no outputs.
+// kStates, here and below: the launch makes the states that the segments add, no outputs.  It walks a
+// segment from its last chunk to its first: with decays counted to the end of the segment, V_d^T K
+// of all chunks adds up in TMEM, and no state is read before the end.
 template <bool kStates>
 __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_t* base, Small* sm, int lane) {
   bool ok = true;
@@ -204,7 +210,7 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
     }
     const int hq = h / (p.H / p.H_qk), hv = h / (p.H / p.H_v);
     for (int c = 0; c < nch; ++c, ++ci) {
-      const int s = ci & 1, t0 = first + c * C;
+      const int s = ci & 1, t0 = first + (kStates ? nch - 1 - c : c) * C;
       auto load = [&](uint8_t* dst, const CUtensorMap* tm, uint64_t* bar, int head) {
         mbar_arrive_expect_tx(bar, kTile);
         tma_load_3d(dst, tm, bar, 0, head, t0);
@@ -245,10 +251,11 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
 // with three terms, four of 32 in slots 0, 1, 0 and 2.
 template <int kTerms>
 __host__ __device__ constexpr int sub_tokens() { return kTerms == 2 ? 64 : 32; }
-template <int kTerms>
+// Where only states are made, each part has a slot.
+template <int kTerms, bool kStates>
 __device__ __forceinline__ void vd_place(int ci, int b, int* slot, int* round) {  // round: uses of the slot before
-  *slot = kTerms == 2 ? b : b == 3 ? 2 : b & 1;
-  *round = kTerms == 3 && *slot == 0 ? 2 * ci + (b >> 1) : ci;
+  *slot = kTerms == 2 || kStates ? b : b == 3 ? 2 : b & 1;
+  *round = kTerms == 3 && !kStates && *slot == 0 ? 2 * ci + (b >> 1) : ci;
 }
 
 template <bool F16, int kTerms, bool kStates>
@@ -261,7 +268,7 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
   const bool leader = elect_one();
   bool failed = false;
   Rec r;
-  int ci = 0;
+  int ci = 0, sums = 0;  // chunks so far; units with chunks so far (states)
   for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
     for (int c = 0; c < r.nch; ++c, ++ci) {
       const int s = ci & 1;
@@ -269,8 +276,8 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
       const uint32_t k = smem_u32(base + kOffKv + s * 2 * kTile);
       const uint64_t d_k = sdesc_sw128(k, 16, 1024), d_kt = sdesc_sw128(k, kHalf, 1024);
       const uint64_t d_vt = sdesc_sw128(k + kTile, kHalf, 1024);
-      if (kStates) {
-        if (!(wait(sm, &sm->k_full[s], ph) && wait(sm, &sm->s_ready, one))) { failed = true; break; }
+      if (kStates) {  // the sum of the unit before has been read
+        if (!(wait(sm, &sm->k_full[s], ph) && (c > 0 || sums == 0 || wait(sm, &sm->s_ready, (sums - 1) & 1)))) { failed = true; break; }
       } else {
         // Q K^T.  P of the chunk before is being read by its P V at the latest, which was
         // issued before: the products run in order.
@@ -298,7 +305,7 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
 #pragma unroll 1
       for (int b = 0; b < kSubs; ++b) {
         int slot, round;
-        vd_place<kTerms>(ci, b, &slot, &round);
+        vd_place<kTerms, kStates>(ci, b, &slot, &round);
         if (!wait(sm, &sm->vd_full[slot], round & 1)) { failed = true; break; }
         tc_fence_after();
         if (leader) {
@@ -306,10 +313,10 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
           for (int t = 0; t < kTerms; ++t)
 #pragma unroll
             for (int i = 0; i < kSub / 16; ++i)
-              mma_ts(tmem + kTmS, tmem + vd_slot_col(slot) + t * (kSub / 2) + i * 8, d_kt + (b * (kSub / 16) + i) * 128,
-                     kTerms == 2 && t == 0 ? id_kmn_neg : id_kmn, 1);
+              mma_ts(tmem + kTmS, tmem + vd_slot_col<kStates>(slot) + t * (kSub / 2) + i * 8, d_kt + (b * (kSub / 16) + i) * 128,
+                     kTerms == 2 && t == 0 ? id_kmn_neg : id_kmn, !kStates || c + b + t + i > 0);
           mma_commit(&sm->vd_empty[slot]);
-          if (b == kSubs - 1) mma_commit(&sm->s_done);
+          if (b == kSubs - 1 && (!kStates || c + 1 == r.nch)) mma_commit(&sm->s_done);
           if (kStates && b == kSubs - 1) mma_commit(&sm->kv_empty[s]);
         }
         __syncwarp();
@@ -329,6 +336,7 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
       __syncwarp();
     }
     if (failed) break;
+    sums += r.nch > 0;
   }
   if (failed && lane == 0) give_up(p, sm);
   if (leader) mma_commit(&sm->drain);
@@ -356,14 +364,15 @@ __device__ __forceinline__ void run_gates(const DecayPrefillParams& p, Small* sm
     else each([&](int64_t i) { return __half2float(reinterpret_cast<const __half*>(p.g)[i]); });
   };
   for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
-    float ahead[4] = {1.f, 1.f, 1.f, 1.f}, whole = 0.f;
-    if (p.g && r.nch > 0) load4(0, ahead);
+    float ahead[4] = {1.f, 1.f, 1.f, 1.f}, later = 0.f;  // later: the decay behind this chunk (states)
+    auto chunk_at = [&](int c) { return kStates ? r.nch - 1 - c : c; };
+    if (p.g && r.nch > 0) load4(chunk_at(0), ahead);
     for (int c = 0; c < r.nch; ++c, ++ci) {
-      const int b = ci & 1, left = r.len - c * C;
+      const int b = ci & 1, left = r.len - chunk_at(c) * C;
       float lg[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) lg[e] = log2f(fminf(fmaxf(ahead[e], FLT_MIN), 1.f));
-      if (p.g && c + 1 < r.nch) load4(c + 1, ahead);
+      if (p.g && c + 1 < r.nch) load4(chunk_at(c + 1), ahead);
       // prefix and suffix sums: the suffix is summed on its own, since G_last - G_j would
       // carry the rounding of two large sums into the state
       float pre[4], suf[4];
@@ -379,6 +388,7 @@ __device__ __forceinline__ void run_gates(const DecayPrefillParams& p, Small* sm
       float before = __shfl_up_sync(0xffffffffu, up, 1), behind = __shfl_down_sync(0xffffffffu, down, 1);
       if (lane == 0) before = 0.f;
       if (lane == 31) behind = 0.f;
+      if (kStates) behind += later;
       const float total = __shfl_sync(0xffffffffu, down, 0);
 #pragma unroll
       for (int e = 0; e < 4; ++e) { pre[e] += before; suf[e] += behind; }
@@ -403,7 +413,8 @@ __device__ __forceinline__ void run_gates(const DecayPrefillParams& p, Small* sm
         sm->gamma[b] = exp2f(total);
         sm->mild[b] = mild;
       }
-      whole += total;
+      later += total;
+      if (kStates && c + 1 == r.nch && lane == 0) p.ws_decay[r.out] = exp2f(later);
       if (!kStates) {
         if (!(ci == 0 || wait(sm, &sm->cf_empty, (ci - 1) & 1))) { failed = true; break; }
         *reinterpret_cast<float4*>(&sm->cf[4 * lane]) = make_float4(
@@ -412,7 +423,7 @@ __device__ __forceinline__ void run_gates(const DecayPrefillParams& p, Small* sm
       warp_arrive(&sm->gate_full[b], lane);
     }
     if (failed) break;
-    if (kStates && lane == 0) p.ws_decay[r.out] = exp2f(whole);
+    if (kStates && r.nch == 0 && lane == 0) p.ws_decay[r.out] = 1.f;
   }
   if (failed && lane == 0) give_up(p, sm);
 }
@@ -646,9 +657,11 @@ __device__ __forceinline__ void split_product(uint32_t a, uint32_t dh, uint32_t 
 }
 
 // Zero this warp's share of the rows past the end: 16 columns (two 16-byte chunks from ch0) of K, and of
-// V, exactly what the warp reads below.
-__device__ __forceinline__ void zero_tails(uint8_t* k, uint8_t* v, int left, int ch0, int lane) {
+// V, exactly what the warp reads below.  Of several groups each takes the rows of its own parts.
+template <int kSub, int kGroups>
+__device__ __forceinline__ void zero_tails(uint8_t* k, uint8_t* v, int left, int ch0, int group, int lane) {
   for (int e = 2 * left + lane; e < C * 2; e += 32) {
+    if ((e >> 1) / kSub % kGroups != group) continue;
     const int ch = ch0 + (e & 1);
     const uint32_t at = (ch >> 3) * kHalf + sw128_chunk(e >> 1, ch & 7);
     *reinterpret_cast<uint4*>(k + at) = make_uint4(0, 0, 0, 0);
@@ -677,7 +690,7 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
     }
   };
   for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
-    for (int c = 0; c < r.nch; ++c, ++ci) {
+    for (int c = 0; c < r.nch && !kStates; ++c, ++ci) {
       const int st = ci & 1;
       // S as the chunk finds it: to 16 bits for Q S^T, times the chunk's decay for V_d^T K
       if (!(wait(sm, &sm->gate_full[st], (ci >> 1) & 1) && (c == 0 || wait(sm, &sm->s_done, (ci - 1) & 1)))) { failed = true; break; }
@@ -693,7 +706,7 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
           tmem_ld_wait();
         }
 #pragma unroll
-        for (int e = 0; e < 4 && !kStates; ++e)
+        for (int e = 0; e < 4; ++e)
           *reinterpret_cast<uint4*>(sb + (q >> 1) * kHalf + sw128_chunk(row, 4 * (q & 1) + e)) =
               make_uint4(pack16x2<F16>(pair_at(x + 8 * e)), pack16x2<F16>(pair_at(x + 8 * e + 2)),
                          pack16x2<F16>(pair_at(x + 8 * e + 4)), pack16x2<F16>(pair_at(x + 8 * e + 6)));
@@ -705,7 +718,7 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
         }
         tmem_st32(ts + 32 * q, x);
       }
-      if (!kStates) fence_proxy_async_smem();
+      fence_proxy_async_smem();
       tmem_st_wait();
       tc_fence_before();
       warp_arrive(&sm->s_ready, lane);
@@ -714,9 +727,12 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
     if (failed) break;
     // the state that the unit leaves (an empty one passes on what it got); the next unit may
     // overwrite TMEM and the 16-bit copy after that, Q S^T having run before
+    if (kStates) ci += r.nch > 0;  // sums so far
     if (r.nch > 0 && !wait(sm, &sm->s_done, (ci - 1) & 1)) { failed = true; break; }
     if (r.out == kNone || (r.out == kPool && !p.s_out)) continue;
     tc_fence_after();
+    const bool start = kStates && r.in == kPool && p.s_in && r.nch > 0;
+    const float2 whole = pair(start ? p.ws_decay[r.out] : 0.f);
 #pragma unroll 1
     for (int q = 0; q < 4; ++q) {
       uint32_t x[32];
@@ -726,9 +742,23 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
         tmem_ld32(ts + 32 * q, x);
         tmem_ld_wait();
       }
+      if (start) {  // what the segment added, and the state that it started from
+        uint32_t y[32];
+        load_in(32 * q, y);
+#pragma unroll
+        for (int e = 0; e < 32; e += 2) {
+          const float2 z = fma2(pair_at(y + e), whole, pair_at(x + e));
+          x[e] = __float_as_uint(z.x);
+          x[e + 1] = __float_as_uint(z.y);
+        }
+      }
       const int64_t at = row * D + 32 * q;
       if (r.out >= 0) store_state32(p.ws, kF32, (int64_t)r.out * (D * D) + at, x);
       else store_state32(p.s_out, p.sout_dtype, r.slot * p.sout_slot + (int64_t)r.h * p.sout_head + at, x);
+    }
+    if (kStates && r.nch > 0) {
+      tc_fence_before();
+      warp_arrive(&sm->s_ready, lane);
     }
   }
   if (failed && lane == 0) give_up(p, sm);
@@ -736,11 +766,11 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
 
 // ------------------------------------------------------------ warps 16-23: V_d
 // Transposed fragments of V (pairs of tokens, one value each) times d, as kTerms 16-bit terms, 16
-// values a warp.
+// values a warp.  Where only states are made, the warps of P do the same, every other part.
 template <bool F16, int kTerms, bool kStates>
 __device__ __forceinline__ void run_v(const DecayPrefillParams& p, uint8_t* base, Small* sm, uint32_t tmem, int warp, int lane) {
-  constexpr int kSub = sub_tokens<kTerms>(), kSubs = C / kSub;
-  const int w = warp & 3, hf = (warp >> 2) & 1;
+  constexpr int kSub = sub_tokens<kTerms>(), kSubs = C / kSub, kGroups = kStates ? 2 : 1;
+  const int w = warp & 3, hf = (warp >> 2) & 1, group = kStates && warp < 4 + kPoWarps ? 1 : 0;
   const uint32_t tq = tmem + ((uint32_t)(32 * w + 16 * hf) << 16);
   const int m = lane >> 3, lr = lane & 7;
   const int ch = 4 * w + 2 * hf + (m & 1);  // this lane's 16-byte chunk of a row of V
@@ -749,19 +779,19 @@ __device__ __forceinline__ void run_v(const DecayPrefillParams& p, uint8_t* base
   int ci = 0;
   for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
     for (int c = 0; c < r.nch; ++c, ++ci) {
-      const int st = ci & 1, left = r.len - c * C;
+      const int st = ci & 1, left = r.len - (kStates ? r.nch - 1 - c : c) * C;
       const uint32_t ph = (ci >> 1) & 1;
       if (!(wait(sm, &sm->gate_full[st], ph) && wait(sm, &sm->v_full[st], ph))) { failed = true; break; }
       uint8_t* k = base + kOffKv + st * 2 * kTile;
       if (left < C) {
         if (!wait(sm, &sm->k_full[st], ph)) { failed = true; break; }
-        zero_tails(k, k + kTile, left, 4 * w + 2 * hf, lane);
+        zero_tails<kSub, kGroups>(k, k + kTile, left, 4 * w + 2 * hf, group, lane);
       }
       const uint32_t va = smem_u32(k + kTile) + (ch >> 3) * kHalf;
 #pragma unroll 1
-      for (int sub = 0; sub < kSubs; ++sub) {
+      for (int sub = group; sub < kSubs; sub += kGroups) {
         int slot, round;
-        vd_place<kTerms>(ci, sub, &slot, &round);
+        vd_place<kTerms, kStates>(ci, sub, &slot, &round);
         if (!((round == 0 || wait(sm, &sm->vd_empty[slot], (round - 1) & 1)) &&
               (kStates || slot != 1 || wait(sm, &sm->qs_done, ci & 1)) &&
               (kStates || slot != 2 || wait(sm, &sm->cf_empty, ci & 1)))) { failed = true; break; }
@@ -770,7 +800,7 @@ __device__ __forceinline__ void run_v(const DecayPrefillParams& p, uint8_t* base
         for (int tt = 0; tt < kSub / 16; ++tt) {
           const int tok = sub * kSub + 16 * tt;  // 16 tokens from here
           const int at2 = (tok >> 1) + (lane & 3);  // this lane's first pair of tokens; the second is 4 pairs on
-          const uint32_t to = tq + vd_slot_col(slot) + 8 * tt;
+          const uint32_t to = tq + vd_slot_col<kStates>(slot) + 8 * tt;
           uint32_t a[4], t[4];
           ldmatrix_x4_trans(va + sw128_chunk(tok + (m >> 1) * 8 + lr, ch & 7), a);
           if (kTerms == 2) {
@@ -825,9 +855,9 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __
     init(sm->v_full, 2, 1);
     init(sm->kv_empty, 2, 1);
     init(sm->rec_full, kRecs, 1);
-    init(sm->rec_empty, kRecs, (kStates ? 2 : 3 + kPoWarps) + kSWarps + kVWarps);
+    init(sm->rec_empty, kRecs, (kStates ? 2 : 3) + kPoWarps + kSWarps + kVWarps);
     init(sm->gate_full, 2, 1);
-    init(sm->gate_empty, 2, (kStates ? 0 : kPoWarps) + kSWarps + kVWarps);
+    init(sm->gate_empty, 2, kPoWarps + (kStates ? 0 : kSWarps) + kVWarps);
     init(&sm->cf_empty, 1, kPoWarps);
     init(&sm->qk_done, 1, 1);
     init(&sm->qs_done, 1, 1);
@@ -863,7 +893,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __
     else if (warp == 2) run_gates<F16, kTerms, kStates>(p, sm, lane);
     else if (!kStates) run_store(p, base, sm, lane);
   } else if (warp < 4 + kPoWarps) {
-    if (!kStates) run_po<F16>(p, base, sm, tmem, warp, lane);
+    if (kStates) run_v<F16, kTerms, kStates>(p, base, sm, tmem, warp, lane);
+    else run_po<F16>(p, base, sm, tmem, warp, lane);
   } else if (warp < 4 + kPoWarps + kSWarps) {
     run_state<F16, kStates>(p, base, sm, tmem, warp, lane);
   } else {
