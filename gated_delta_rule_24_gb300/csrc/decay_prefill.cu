@@ -81,7 +81,8 @@ constexpr uint32_t kTmCols = 512;
 // ------------------------------------------------------------ shared memory (bytes)
 constexpr uint32_t kTile = C * D * 2;       // a 16-bit tile: two 128B-swizzled halves of 64 columns
 constexpr uint32_t kHalf = kTile / 2;
-constexpr uint32_t kOffKv = kTile;           // after Q: two stages of K, V
+constexpr uint32_t kOffKv = kTile;           // after Q: two stages of K, V; a launch that makes states
+                                             // alone has a third over what follows
 constexpr uint32_t kOffS = kOffKv + 4 * kTile;  // 16-bit copy of S
 constexpr uint32_t kOffO = kOffS + kTile;    // the output tile on its way out
 constexpr uint32_t kOffSmall = kOffO + kTile;
@@ -101,7 +102,7 @@ struct Small {
   int32_t mild[2]; // no block of 16 tokens decays by more than 2^-100
   float gamma[2];  // 2^(G_last)
   Rec rec[kRecs];
-  uint64_t q_full, q_empty, k_full[2], v_full[2], kv_empty[2];
+  uint64_t q_full, q_empty, k_full[3], v_full[3], kv_empty[3];
   uint64_t rec_full[kRecs], rec_empty[kRecs];
   uint64_t gate_full[2], gate_empty[2], cf_empty;
   uint64_t qk_done, qs_done, s_done, o_done;   // products that have completed
@@ -115,6 +116,8 @@ struct Small {
 constexpr uint32_t kSmem = kOffSmall + sizeof(Small);
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
 
+template <bool kStates>
+__host__ __device__ constexpr int kv_stages() { return kStates ? 3 : 2; }
 constexpr int kPoWarps = 8, kSWarps = 4, kVWarps = 8;
 constexpr int kThreads = 32 * (4 + kPoWarps + kSWarps + kVWarps);
 // Every wait: bounded (kTries probes of up to 20 us each), and over as soon as another role has
@@ -173,6 +176,7 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
   int u = 0, ci = 0;  // units and chunks so far
   const int segs = kStates ? p.splits - 1 : p.splits;  // segments that this launch walks
   const int64_t units = (int64_t)p.N * segs * p.H;
+  constexpr int kKv = kv_stages<kStates>();
   int kv_loads = 0, q_loads = 0;
   auto publish = [&](const Rec& r) {
     const int slot = u % kRecs;
@@ -210,7 +214,7 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
     }
     const int hq = h / (p.H / p.H_qk), hv = h / (p.H / p.H_v);
     for (int c = 0; c < nch; ++c, ++ci) {
-      const int s = ci & 1, t0 = first + (kStates ? nch - 1 - c : c) * C;
+      const int s = ci % kKv, t0 = first + (kStates ? nch - 1 - c : c) * C;
       auto load = [&](uint8_t* dst, const CUtensorMap* tm, uint64_t* bar, int head) {
         mbar_arrive_expect_tx(bar, kTile);
         tma_load_3d(dst, tm, bar, 0, head, t0);
@@ -222,7 +226,7 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
         if (lane == 0) load(base, &p.tm_q, &sm->q_full, hq);
         ++q_loads;
       }
-      ok = ci < 2 || wait(sm, &sm->kv_empty[s], ((ci >> 1) - 1) & 1);
+      ok = ci < kKv || wait(sm, &sm->kv_empty[s], (ci / kKv - 1) & 1);
       if (!ok) break;
       if (lane == 0) {
         uint8_t* k = base + kOffKv + s * 2 * kTile;
@@ -235,9 +239,9 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
   if (ok) ok = publish(Rec{0, 0, 0, -1, 0, 0, 0});
   if (!ok && lane == 0) give_up(p, sm);
   // loads that no role waits for any more land before the CTA's shared memory goes away
-  auto landed = [&](uint64_t (&bar)[2], int loads) {
-    for (int s = 0; s < 2; ++s) {
-      const int n = (loads + 1 - s) / 2;  // loads of stage s
+  auto landed = [&](uint64_t (&bar)[3], int loads) {
+    for (int s = 0; s < kKv; ++s) {
+      const int n = (loads + kKv - 1 - s) / kKv;  // loads of stage s
       if (n) drain(&bar[s], (n - 1) & 1);
     }
   };
@@ -271,8 +275,8 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
   int ci = 0, sums = 0;  // chunks so far; units with chunks so far (states)
   for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
     for (int c = 0; c < r.nch; ++c, ++ci) {
-      const int s = ci & 1;
-      const uint32_t ph = (ci >> 1) & 1, one = ci & 1;
+      const int s = ci % kv_stages<kStates>();
+      const uint32_t ph = (ci / kv_stages<kStates>()) & 1, one = ci & 1;
       const uint32_t k = smem_u32(base + kOffKv + s * 2 * kTile);
       const uint64_t d_k = sdesc_sw128(k, 16, 1024), d_kt = sdesc_sw128(k, kHalf, 1024);
       const uint64_t d_vt = sdesc_sw128(k + kTile, kHalf, 1024);
@@ -780,11 +784,12 @@ __device__ __forceinline__ void run_v(const DecayPrefillParams& p, uint8_t* base
   for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
     for (int c = 0; c < r.nch; ++c, ++ci) {
       const int st = ci & 1, left = r.len - (kStates ? r.nch - 1 - c : c) * C;
-      const uint32_t ph = (ci >> 1) & 1;
-      if (!(wait(sm, &sm->gate_full[st], ph) && wait(sm, &sm->v_full[st], ph))) { failed = true; break; }
-      uint8_t* k = base + kOffKv + st * 2 * kTile;
+      const int kv = ci % kv_stages<kStates>();
+      const uint32_t ph = (ci / kv_stages<kStates>()) & 1;
+      if (!(wait(sm, &sm->gate_full[st], (ci >> 1) & 1) && wait(sm, &sm->v_full[kv], ph))) { failed = true; break; }
+      uint8_t* k = base + kOffKv + kv * 2 * kTile;
       if (left < C) {
-        if (!wait(sm, &sm->k_full[st], ph)) { failed = true; break; }
+        if (!wait(sm, &sm->k_full[kv], ph)) { failed = true; break; }
         zero_tails<kSub, kGroups>(k, k + kTile, left, 4 * w + 2 * hf, group, lane);
       }
       const uint32_t va = smem_u32(k + kTile) + (ch >> 3) * kHalf;
@@ -851,9 +856,9 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __
     };
     init(&sm->q_full, 1, 1);
     init(&sm->q_empty, 1, kPoWarps);
-    init(sm->k_full, 2, 1);
-    init(sm->v_full, 2, 1);
-    init(sm->kv_empty, 2, 1);
+    init(sm->k_full, 3, 1);
+    init(sm->v_full, 3, 1);
+    init(sm->kv_empty, 3, 1);
     init(sm->rec_full, kRecs, 1);
     init(sm->rec_empty, kRecs, (kStates ? 2 : 3) + kPoWarps + kSWarps + kVWarps);
     init(sm->gate_full, 2, 1);
