@@ -128,25 +128,28 @@ class _Descriptors(threading.local):
     tensor where ``describe`` costs 5."""
 
     SIZE = ctypes.sizeof(GdnTensor)
-    ROWS = [struct.Struct("@qii%dq" % n + "%dx" % (8 * (4 - n)) + "%dq" % n + "%dx" % (8 * (4 - n))) for n in range(5)]
+    PACK = [struct.Struct("@qii%dq" % n + "%dx" % (8 * (4 - n)) + "%dq" % n + "%dx" % (8 * (4 - n))).pack_into for n in range(5)]
 
     def __init__(self):
         self.room = ctypes.create_string_buffer(12 * self.SIZE)
         self.base = ctypes.addressof(self.room)
 
     def fill(self, *tensors):
-        where = []
-        for i, t in enumerate(tensors):
+        room, base, size, pack, where, at = self.room, self.base, self.SIZE, self.PACK, [], 0
+        for t in tensors:
             if t is None:
                 where.append(None)
                 continue
-            dtype, n = _DTYPES.get(t.dtype), t.dim()
-            if dtype is None:
-                raise TypeError(f"unsupported dtype {t.dtype}")
+            shape = t.shape
+            n = len(shape)
             if n > 4:
                 raise ValueError("at most 4 dims")
-            self.ROWS[n].pack_into(self.room, i * self.SIZE, t.data_ptr(), dtype, n, *t.shape, *t.stride())
-            where.append(self.base + i * self.SIZE)
+            dtype = _DTYPES.get(t.dtype)
+            if dtype is None:
+                raise TypeError(f"unsupported dtype {t.dtype}")
+            pack[n](room, at, t.data_ptr(), dtype, n, *shape, *t.stride())
+            where.append(base + at)
+            at += size
         return where
 
 
@@ -163,8 +166,14 @@ def _check(status: int):
         raise GdnError(status, msg)
 
 
+# The current stream's handle without making a Stream object of it (3 us), where torch offers it.
+_current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream_handle(stream) -> int:
     if stream is None:
+        if _current_raw_stream is not None:
+            return _current_raw_stream(torch.cuda.current_device())
         stream = torch.cuda.current_stream()
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
