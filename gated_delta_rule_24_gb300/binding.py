@@ -168,12 +168,13 @@ def _check(status: int):
 
 # The current stream's handle without making a Stream object of it (3 us), where torch offers it.
 _current_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _stream_handle(stream) -> int:
     if stream is None:
         if _current_raw_stream is not None:
-            return _current_raw_stream(torch.cuda.current_device())
+            return _current_raw_stream(_current_device())
         stream = torch.cuda.current_stream()
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -252,18 +253,23 @@ def gdn_decode_step(q, k, v, g, beta, scale: float, state, state_indices, use_qk
 def gdn_qk_norm_rope(q, k, q_weight, k_weight, weight_offset: float, eps: float, cos_sin, positions,
                      interleaved: bool, q_out, k_out, stream=None) -> None:
     """Norm and rotation of query and key heads; same names and order as the C entry point."""
-    d = _descriptors.fill(q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out)
-    _check(load_library().gdn_qk_norm_rope(d[0], d[1], d[2], d[3], float(weight_offset), float(eps), d[4], d[5],
-                                           int(bool(interleaved)), d[6], d[7], _stream_handle(stream)))
+    dq, dk, dqw, dkw, dcs, dp, dqo, dko = _descriptors.fill(q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out)
+    status = (_lib or load_library()).gdn_qk_norm_rope(dq, dk, dqw, dkw, weight_offset, eps, dcs, dp, 1 if interleaved else 0,
+                                                       dqo, dko, _stream_handle(stream))
+    if status:
+        _check(status)
 
 
 def gdn_decay_prefill(q, k, v, g, scale: float, initial_state, state_indices, output_state, cu_seqlens,
                       batch_invariant: bool, output, stream=None) -> None:
     """Linear attention with a decay over packed sequences; same names and order as the C
     entry point."""
-    d = _descriptors.fill(q, k, v, g, initial_state, state_indices, output_state, cu_seqlens, output)
-    _check(load_library().gdn_decay_prefill(d[0], d[1], d[2], d[3], float(scale), d[4], d[5], d[6], d[7],
-                                            int(bool(batch_invariant)), d[8], _stream_handle(stream)))
+    dq, dk, dv, dg, ds, di, df, dc, do = _descriptors.fill(q, k, v, g, initial_state, state_indices, output_state,
+                                                           cu_seqlens, output)
+    status = (_lib or load_library()).gdn_decay_prefill(dq, dk, dv, dg, scale, ds, di, df, dc, 1 if batch_invariant else 0, do,
+                                                        _stream_handle(stream))
+    if status:
+        _check(status)
 
 
 def gdn_decay_workspace_bytes(num_seqs: int, num_heads: int, total_tokens: int, num_sms: Optional[int] = None) -> int:
@@ -277,9 +283,10 @@ def gdn_decay_workspace_bytes(num_seqs: int, num_heads: int, total_tokens: int, 
 def gdn_decay_step(q, k, v, g, scale: float, state, state_indices, output, stream=None) -> None:
     """One token per batch row through the same recurrence, ``state`` in place; same names
     and order as the C entry point."""
-    d = _descriptors.fill(q, k, v, g, state, state_indices, output)
-    _check(load_library().gdn_decay_step(d[0], d[1], d[2], d[3], float(scale), d[4], d[5], d[6],
-                                         _stream_handle(stream)))
+    dq, dk, dv, dg, ds, di, do = _descriptors.fill(q, k, v, g, state, state_indices, output)
+    status = (_lib or load_library()).gdn_decay_step(dq, dk, dv, dg, scale, ds, di, do, _stream_handle(stream))
+    if status:
+        _check(status)
 
 
 def gdn_reserve_workspace(nbytes: int, stream=None) -> None:
@@ -380,9 +387,9 @@ def _allocating_on(stream):
 
 def _empty(shape, like, stream):
     if stream is None:
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
+        return like.new_empty(shape)
     with _allocating_on(stream):
-        return torch.empty(shape, dtype=like.dtype, device=like.device)
+        return like.new_empty(shape)
 
 
 def _gate_rows(g, rows: int):
@@ -400,9 +407,9 @@ def qk_norm_rope(q, k=None, cos_sin=None, positions=None, q_weight=None, k_weigh
     k_out=k`` to work in place.  A result that the call allocates belongs to ``stream``.
     """
     if q_out is None:
-        q_out = _empty(q.shape, q, stream)
+        q_out = torch.empty_like(q) if stream is None else _empty(q.shape, q, stream)
     if k is not None and k_out is None:
-        k_out = _empty(k.shape, k, stream)
+        k_out = torch.empty_like(k) if stream is None else _empty(k.shape, k, stream)
     gdn_qk_norm_rope(q, k, q_weight, k_weight, weight_offset, eps, cos_sin, positions, interleaved, q_out, k_out, stream)
     return q_out, k_out
 

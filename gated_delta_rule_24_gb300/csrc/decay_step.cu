@@ -9,7 +9,10 @@
 // nothing else counts (5 flops for 4 to 8 bytes): the step is bound by HBM bandwidth.  A
 // warp takes 16 rows (8 of f32 states): 16 lanes (32) hold one row, 16 bytes of it each, so
 // that every request of the warp is 512 contiguous bytes and each lane keeps its k and q
-// columns in registers; all its loads are issued before the first is used.
+// columns in registers; all its loads are issued before the first is used.  Loads and stores
+// are marked as streaming: a state is not seen again before the whole pool has passed.
+// 1024 rows x 16 heads from a bf16 pool (1.09 GB) take 160 us, 6.8 TB/s (172 us with CTAs of
+// four warps and plain loads and stores, 195 with eight); one row of 32 f32 states 4.5 us.
 #include <cuda_runtime.h>
 
 #include "decay.cuh"
@@ -17,7 +20,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kStepWarps = 4;
+constexpr int kStepWarps = 2;  // of a CTA: it gives its place back the sooner
 constexpr int kStepLoads = 8;  // 16-byte loads a lane has in flight
 
 template <int SDT, bool F16>
@@ -43,7 +46,7 @@ __global__ void __launch_bounds__(32 * kStepWarps) gdn_decay_step_kernel(const _
   uint4 raw[kStepLoads];
 #pragma unroll
   for (int i = 0; i < kStepLoads; ++i)
-    raw[i] = *reinterpret_cast<const uint4*>(s + (int64_t)i * kRowsPerLoad * kHeadDim * ST::kBytes);
+    raw[i] = __ldcs(reinterpret_cast<const uint4*>(s + (int64_t)i * kRowsPerLoad * kHeadDim * ST::kBytes));
   const int hq = h / (p.H / p.H_qk), hv = h / (p.H / p.H_v);
   const char* kp = reinterpret_cast<const char*>(p.k) + (b * p.k_sb + (int64_t)hq * p.k_sh + col) * 2;
   const char* qp = reinterpret_cast<const char*>(p.q) + (b * p.q_sb + (int64_t)hq * p.q_sh + col) * 2;
@@ -71,7 +74,7 @@ __global__ void __launch_bounds__(32 * kStepWarps) gdn_decay_step_kernel(const _
       x[e] = fmaf(g, x[e], v[i] * k[e]);
       acc = fmaf(x[e], q[e], acc);
     }
-    *reinterpret_cast<uint4*>(s + (int64_t)i * kRowsPerLoad * kHeadDim * ST::kBytes) = ST::pack(x);
+    __stcs(reinterpret_cast<uint4*>(s + (int64_t)i * kRowsPerLoad * kHeadDim * ST::kBytes), ST::pack(x));
 #pragma unroll
     for (int d = kLanes / 2; d > 0; d >>= 1) acc += __shfl_xor_sync(0xffffffffu, acc, d);
     if (lane % kLanes == 0) o[i * kRowsPerLoad] = (uint16_t)pack16x2<F16>(p.scale * acc, 0.f);

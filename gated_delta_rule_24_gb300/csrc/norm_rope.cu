@@ -8,9 +8,10 @@
 // HBM bandwidth.  Eight lanes hold a head, two vectors of 8 values each, chosen so that a
 // lane owns both values of each of its pairs: neighbours (2i, 2i + 1) sit in one vector
 // already, and for the halves (i, i + R / 2) lane l < R / 16 takes vectors l and l + R / 16.
-// Either way a rotating lane needs the cosines and sines of pairs 8 l .. 8 l + 7, the same
-// for all heads of a token, and the weights of its 16 values, the same for all tokens: a
-// group of lanes takes a run of heads of one token, with all their loads under way at once.
+// Norm and rotation are then y = r (x P + x' Q) with r the head's norm factor, x' the other
+// value of the pair and P, Q made of the weights, cosines and sines once for a token (P the
+// weight and Q zero where nothing turns).  A group of eight lanes walks some heads of one
+// token with the loads of the next four under way.
 #include <cuda_runtime.h>
 
 #include "decay.cuh"
@@ -18,7 +19,7 @@
 namespace gdn {
 namespace {
 
-constexpr int kRopeThreads = 128;
+constexpr int kRopeThreads = 64;
 constexpr int kRopeLanes = 8;                              // lanes of one head
 constexpr int kRopeGroups = kRopeThreads / kRopeLanes;     // of a CTA
 
@@ -44,23 +45,21 @@ __device__ __forceinline__ void load_weight8(const RopeTensor& t, int at, float 
   for (int e = 0; e < 8; ++e) w[e] += offset;
 }
 
-// kRun heads of one token and tensor for each group of eight lanes; a token's runs side by side.
-template <bool F16, int kRun>
-__global__ void __launch_bounds__(kRopeThreads) gdn_norm_rope_kernel(const __grid_constant__ RopeParams p) {
+// CTAs below q_ctas take q, the others k.  `per` heads a group; a token's groups side by side.
+template <bool F16, bool kInterleaved, int kAhead>
+__global__ void __launch_bounds__(kRopeThreads) gdn_norm_rope_kernel(const __grid_constant__ RopeParams p, unsigned q_ctas,
+                                                                     int per) {
   const int l = threadIdx.x % kRopeLanes;
-  const int q_runs = (p.t[0].heads + kRun - 1) / kRun, runs = q_runs + (p.t[1].heads + kRun - 1) / kRun;
-  const int64_t first = (int64_t)blockIdx.x * kRopeGroups;  // of the CTA's (token, run) units
-  int64_t tok = first / runs;
-  int run = (int)(first - tok * runs) + threadIdx.x / kRopeLanes;
-  if (run >= runs) {
-    tok += run / runs;
-    run %= runs;
-  }
-  const bool is_k = run >= q_runs;
+  const bool is_k = blockIdx.x >= q_ctas;
   const RopeTensor& t = p.t[is_k ? 1 : 0];
-  const int h0 = (is_k ? run - q_runs : run) * kRun;
+  const int parts = (t.heads + per - 1) / per;
+  const int64_t first = (int64_t)(blockIdx.x - (is_k ? q_ctas : 0)) * kRopeGroups;
+  int64_t tok = first / parts;
+  int part = (int)(first - tok * parts) + threadIdx.x / kRopeLanes;
+  tok += part / parts;
+  part %= parts;
   const int rot = p.cos_sin ? p.rotary / 16 : 0;  // lanes that rotate
-  const bool halves = !p.interleaved && l < rot;
+  const bool halves = !kInterleaved && l < rot;
   const int v0 = 8 * (halves ? l : 2 * l), v1 = 8 * (halves ? l + rot : 2 * l + 1);
   bool ok = tok < p.T;
   int64_t place = 0;
@@ -71,72 +70,89 @@ __global__ void __launch_bounds__(kRopeThreads) gdn_norm_rope_kernel(const __gri
       ok = false;
     }
   }
-  uint4 ra[kRun], rb[kRun];
-  const uint16_t* x = reinterpret_cast<const uint16_t*>(t.x) + tok * t.x_st + (int64_t)h0 * t.x_sh;
+  // `n` heads for every group of the warp, so that its lanes stay together; a group without a token or
+  // with fewer heads left loads and stores nothing
+  const int n = min(per, t.heads), own = ok ? min(per, t.heads - part * per) : 0;
+  const int64_t sx = t.x_sh, sy = t.y_sh;
+  const uint16_t* x = reinterpret_cast<const uint16_t*>(t.x) + tok * t.x_st + (int64_t)part * per * sx;
+  uint16_t* y = reinterpret_cast<uint16_t*>(t.y) + tok * t.y_st + (int64_t)part * per * sy;
+  uint4 ra[kAhead], rb[kAhead];
+  auto load = [&](int i, int h) {
+    if (h < own) {
+      ra[i] = __ldcs(reinterpret_cast<const uint4*>(x + h * sx + v0));
+      rb[i] = __ldcs(reinterpret_cast<const uint4*>(x + h * sx + v1));
+    }
+  };
 #pragma unroll
-  for (int i = 0; i < kRun; ++i) {
+  for (int i = 0; i < kAhead; ++i) {
     ra[i] = rb[i] = make_uint4(0, 0, 0, 0);
-    if (ok && h0 + i < t.heads) {
-      ra[i] = __ldcs(reinterpret_cast<const uint4*>(x + i * t.x_sh + v0));
-      rb[i] = __ldcs(reinterpret_cast<const uint4*>(x + i * t.x_sh + v1));
-    }
+    load(i, i);
   }
-  float wa[8], wb[8], c[8], s[8];
-  load_weight8(t, v0, p.weight_offset, wa);
-  load_weight8(t, v1, p.weight_offset, wb);
-  const bool turn = ok && l < rot;
-  if (turn) {
-    load8(p.cos_sin + place * p.cs_stride + 8 * l, c);
-    load8(p.cos_sin + place * p.cs_stride + p.rotary / 2 + 8 * l, s);
-  }
-  uint16_t* y = reinterpret_cast<uint16_t*>(t.y) + tok * t.y_st + (int64_t)h0 * t.y_sh;
+  float2 pa[4], qa[4], pb[4], qb[4];  // P and Q of the two vectors
+  {
+    float wa[8], wb[8], c[8], s[8];
+    load_weight8(t, v0, p.weight_offset, wa);
+    load_weight8(t, v1, p.weight_offset, wb);
 #pragma unroll
-  for (int i = 0; i < kRun; ++i) {
-    float a[8], b[8], ss = 0.f;
-    unpack16x8<F16>(ra[i], a);
-    unpack16x8<F16>(rb[i], b);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) ss += a[e] * a[e] + b[e] * b[e];
-#pragma unroll
-    for (int d = kRopeLanes / 2; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-    const float r = rsqrtf(ss * (1.f / kHeadDim) + p.eps);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      a[e] *= r * wa[e];
-      b[e] *= r * wb[e];
+    for (int e = 0; e < 8; ++e) { c[e] = 1.f; s[e] = 0.f; }
+    if (ok && l < rot) {
+      load8(p.cos_sin + place * p.cs_stride + 8 * l, c);
+      load8(p.cos_sin + place * p.cs_stride + p.rotary / 2 + 8 * l, s);
     }
-    if (turn) {
-      if (p.interleaved) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float x0 = a[2 * e], x1 = a[2 * e + 1], y0 = b[2 * e], y1 = b[2 * e + 1];
-          a[2 * e] = x0 * c[e] - x1 * s[e];
-          a[2 * e + 1] = x0 * s[e] + x1 * c[e];
-          b[2 * e] = y0 * c[4 + e] - y1 * s[4 + e];
-          b[2 * e + 1] = y0 * s[4 + e] + y1 * c[4 + e];
-        }
-      } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float x0 = a[e], x1 = b[e];
-          a[e] = x0 * c[e] - x1 * s[e];
-          b[e] = x0 * s[e] + x1 * c[e];
-        }
+    for (int e = 0; e < 4; ++e) {
+      if (kInterleaved) {  // x' is the pair turned round
+        pa[e] = make_float2(wa[2 * e] * c[e], wa[2 * e + 1] * c[e]);
+        qa[e] = make_float2(-wa[2 * e + 1] * s[e], wa[2 * e] * s[e]);
+        pb[e] = make_float2(wb[2 * e] * c[4 + e], wb[2 * e + 1] * c[4 + e]);
+        qb[e] = make_float2(-wb[2 * e + 1] * s[4 + e], wb[2 * e] * s[4 + e]);
+      } else {  // x' is the other vector's
+        pa[e] = make_float2(wa[2 * e] * c[2 * e], wa[2 * e + 1] * c[2 * e + 1]);
+        qa[e] = make_float2(-wb[2 * e] * s[2 * e], -wb[2 * e + 1] * s[2 * e + 1]);
+        pb[e] = make_float2(wb[2 * e] * c[2 * e], wb[2 * e + 1] * c[2 * e + 1]);
+        qb[e] = make_float2(wa[2 * e] * s[2 * e], wa[2 * e + 1] * s[2 * e + 1]);
       }
     }
-    if (ok && h0 + i < t.heads) {
-      __stcs(reinterpret_cast<uint4*>(y + i * t.y_sh + v0), pack16x8<F16>(a));
-      __stcs(reinterpret_cast<uint4*>(y + i * t.y_sh + v1), pack16x8<F16>(b));
+  }
+#pragma unroll 1
+  for (int h0 = 0; h0 < n; h0 += kAhead) {
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const uint32_t ca[4] = {ra[i].x, ra[i].y, ra[i].z, ra[i].w}, cb[4] = {rb[i].x, rb[i].y, rb[i].z, rb[i].w};
+      float2 a[4], b[4], sum = make_float2(0.f, 0.f);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        a[e] = unpack16<F16>(ca[e]);
+        b[e] = unpack16<F16>(cb[e]);
+        sum = fma2(a[e], a[e], sum);
+        sum = fma2(b[e], b[e], sum);
+      }
+      load(i, h0 + i + kAhead);
+      float ss = sum.x + sum.y;
+#pragma unroll
+      for (int d = kRopeLanes / 2; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
+      const float2 r = pair(rsqrtf(ss * (1.f / kHeadDim) + p.eps));
+      uint32_t ya[4], yb[4];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const float2 ta = kInterleaved ? make_float2(a[e].y, a[e].x) : b[e], tb = kInterleaved ? make_float2(b[e].y, b[e].x) : a[e];
+        ya[e] = pack16x2<F16>(mul2(r, fma2(a[e], pa[e], mul2(ta, qa[e]))));
+        yb[e] = pack16x2<F16>(mul2(r, fma2(b[e], pb[e], mul2(tb, qb[e]))));
+      }
+      if (h0 + i < own) {
+        __stcs(reinterpret_cast<uint4*>(y + (h0 + i) * sy + v0), make_uint4(ya[0], ya[1], ya[2], ya[3]));
+        __stcs(reinterpret_cast<uint4*>(y + (h0 + i) * sy + v1), make_uint4(yb[0], yb[1], yb[2], yb[3]));
+      }
     }
   }
 }
 
-template <int kRun>
-cudaError_t launch(const RopeParams& p, cudaStream_t stream) {
-  const int64_t units = p.T * ((p.t[0].heads + kRun - 1) / kRun + (p.t[1].heads + kRun - 1) / kRun);
-  const unsigned grid = (unsigned)((units + kRopeGroups - 1) / kRopeGroups);
-  if (p.in_f16) gdn_norm_rope_kernel<true, kRun><<<grid, kRopeThreads, 0, stream>>>(p);
-  else gdn_norm_rope_kernel<false, kRun><<<grid, kRopeThreads, 0, stream>>>(p);
+template <bool F16, int kAhead>
+cudaError_t launch(const RopeParams& p, int per, cudaStream_t stream) {
+  auto ctas = [&](int heads) { return (p.T * ((heads + per - 1) / per) + kRopeGroups - 1) / kRopeGroups; };
+  const int64_t q = ctas(p.t[0].heads), k = ctas(p.t[1].heads);
+  if (p.interleaved) gdn_norm_rope_kernel<F16, true, kAhead><<<(unsigned)(q + k), kRopeThreads, 0, stream>>>(p, (unsigned)q, per);
+  else gdn_norm_rope_kernel<F16, false, kAhead><<<(unsigned)(q + k), kRopeThreads, 0, stream>>>(p, (unsigned)q, per);
   return cudaGetLastError();
 }
 
@@ -145,10 +161,18 @@ cudaError_t launch(const RopeParams& p, cudaStream_t stream) {
 cudaError_t launch_norm_rope(const RopeParams& p, cudaStream_t stream) {
   const int64_t rows = p.T * (p.t[0].heads + p.t[1].heads);
   if (rows <= 0) return cudaSuccess;
-  // Runs of four heads where they still fill the SMs several times over; single heads where a
-  // call is all latency.
   const int sms = device_sm_count();
-  return rows >= (int64_t)sms * kRopeGroups * 4 * 8 ? launch<4>(p, stream) : launch<1>(p, stream);
+  if (sms <= 0) return cudaErrorInvalidDevice;
+  // Heads a group, up to 16, so that two rounds of groups are left on all SMs, and the loads of up to
+  // four under way: 65536 tokens x 48 heads take 249 us with 16 heads a group, 290 with 4, 428 with 1
+  // (6.6, 5.7 and 3.8 TB/s); 2000 tokens 14.6 us with 3 and two under way, 16.7 with 1, 27 with the
+  // loop that has four.
+  constexpr int kResident = 80, kRounds = 2;  // groups on an SM
+  const int64_t most = rows / ((int64_t)sms * kResident * kRounds);
+  const int per = (int)(most < 1 ? 1 : most > 16 ? 16 : most);
+  if (per < 2) return p.in_f16 ? launch<true, 1>(p, 1, stream) : launch<false, 1>(p, 1, stream);
+  if (per < 4) return p.in_f16 ? launch<true, 2>(p, per, stream) : launch<false, 2>(p, per, stream);
+  return p.in_f16 ? launch<true, 4>(p, per, stream) : launch<false, 4>(p, per, stream);
 }
 
 }  // namespace gdn
