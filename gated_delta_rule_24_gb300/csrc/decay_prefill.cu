@@ -88,7 +88,7 @@ constexpr uint32_t kOffO = kOffS + kTile;    // the output tile on its way out
 constexpr uint32_t kOffSmall = kOffO + kTile;
 constexpr int kRecs = 4;
 
-struct Rec {       // one unit: a sequence, or a segment of one, of one head
+struct Rec {       // one unit: a sequence, or a segment of one, of one head.  Only units with chunks go round
   int32_t t0, len, h, nch;  // first token, tokens, head, chunks (-1: no more units)
   int64_t slot;
   int32_t in, out;  // where the state comes from and goes to: a block of the workspace, or
@@ -101,6 +101,7 @@ struct Small {
   float cf[C];     // 2^(G_e - G_j), e the last token of j's block of 16
   int32_t mild[2]; // no block of 16 tokens decays by more than 2^-100
   float gamma[2];  // 2^(G_last)
+  int32_t empties; // units without chunks
   Rec rec[kRecs];
   uint64_t q_full, q_empty, k_full[3], v_full[3], kv_empty[3];
   uint64_t rec_full[kRecs], rec_empty[kRecs];
@@ -166,16 +167,42 @@ __device__ __forceinline__ bool next_unit(Small* sm, int u, int lane, Rec* r, bo
   return r->nch >= 0;
 }
 
-// ------------------------------------------------------------ warp 0: loads
+// ------------------------------------------------------------ units
 // kStates, here and below: the launch makes the states that the segments add, no outputs.  It walks a
 // segment from its last chunk to its first: with decays counted to the end of the segment, V_d^T K
 // of all chunks adds up in TMEM, and no state is read before the end.
 template <bool kStates>
+__device__ __forceinline__ int64_t unit_count(const DecayPrefillParams& p) {
+  return (int64_t)p.N * (kStates ? p.splits - 1 : p.splits) * p.H;
+}
+// Unit x of the launch; device error bits instead where its bounds or its slot are bad.
+template <bool kStates>
+__device__ __forceinline__ int unit_at(const DecayPrefillParams& p, int64_t x, Rec* r) {
+  // heads of a segment side by side: they share keys and queries, or lines of the gates
+  const int segs = kStates ? p.splits - 1 : p.splits;
+  const int h = (int)(x % p.H), seg = (int)(x / p.H) % segs, n = (int)(x / p.H / segs);
+  const int64_t bos = index_at(p.cu, p.cu_dtype, n), eos = index_at(p.cu, p.cu_dtype, n + 1);
+  const int64_t slot = p.state_idx ? index_at(p.state_idx, p.idx_dtype, n) : (int64_t)n;
+  int err = 0;
+  if (bos < 0 || eos < bos || eos > p.T) err |= kDevErrCu;
+  if ((p.s_in && (slot < 0 || slot >= p.sin_slots)) || (p.s_out && (slot < 0 || slot >= p.sout_slots))) err |= kDevErrIdx;
+  if (err) return err;
+  const int all = (int)((eos - bos + C - 1) / C);  // chunks of the sequence
+  const int c0 = (int)((int64_t)all * seg / p.splits), nch = (int)((int64_t)all * (seg + 1) / p.splits) - c0;
+  const int first = (int)bos + c0 * C, len = nch > 0 ? min((int)eos - first, nch * C) : 0;
+  const int block = (n * p.H + h) * (p.splits - 1) + seg;  // of the state behind this segment
+  *r = Rec{first, len, h, nch, slot, seg == 0 ? kPool : kStates ? kNone : block - 1,
+           kStates ? block : seg == p.splits - 1 ? kPool : kNone};
+  return 0;
+}
+
+// ------------------------------------------------------------ warp 0: loads
+template <bool kStates>
 __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_t* base, Small* sm, int lane) {
   bool ok = true;
   int u = 0, ci = 0;  // units and chunks so far
-  const int segs = kStates ? p.splits - 1 : p.splits;  // segments that this launch walks
-  const int64_t units = (int64_t)p.N * segs * p.H;
+  const int64_t units = unit_count<kStates>(p);
+  int empties = 0;
   constexpr int kKv = kv_stages<kStates>();
   int kv_loads = 0, q_loads = 0;
   auto publish = [&](const Rec& r) {
@@ -189,28 +216,22 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
     return true;
   };
   for (int64_t x = blockIdx.x; x < units && ok; x += gridDim.x) {
-    // heads of a segment side by side: they share keys and queries, or lines of the gates
-    const int h = (int)(x % p.H), seg = (int)(x / p.H) % segs, n = (int)(x / p.H / segs);
-    const int64_t bos = index_at(p.cu, p.cu_dtype, n), eos = index_at(p.cu, p.cu_dtype, n + 1);
-    const int64_t slot = p.state_idx ? index_at(p.state_idx, p.idx_dtype, n) : (int64_t)n;
-    int err = 0;
-    if (bos < 0 || eos < bos || eos > p.T) err |= kDevErrCu;
-    if ((p.s_in && (slot < 0 || slot >= p.sin_slots)) || (p.s_out && (slot < 0 || slot >= p.sout_slots)))
-      err |= kDevErrIdx;
+    Rec r;
+    const int err = unit_at<kStates>(p, x, &r);
     if (err) {
       if (lane == 0) atomicOr(p.dev_err, err);
       continue;
     }
-    const int all = (int)((eos - bos + C - 1) / C);  // chunks of the sequence
-    const int c0 = (int)((int64_t)all * seg / p.splits), nch = (int)((int64_t)all * (seg + 1) / p.splits) - c0;
-    const int first = (int)bos + c0 * C, len = nch > 0 ? min((int)eos - first, nch * C) : 0;
-    const int block = (n * p.H + h) * (p.splits - 1) + seg;  // of the state behind this segment
-    const int in = seg == 0 ? kPool : kStates ? kNone : block - 1;
-    ok = publish(Rec{first, len, h, nch, slot, in, kStates ? block : seg == p.splits - 1 ? kPool : kNone});
+    if (r.nch == 0) {  // nothing but a state to pass on: warps 12-15 see to these at the end
+      ++empties;
+      continue;
+    }
+    ok = publish(r);
     if (!ok) break;
-    if (p.s_in && in == kPool && lane == 0) {
+    const int h = r.h, nch = r.nch, first = r.t0;
+    if (p.s_in && r.in == kPool && lane == 0) {
       const int es = p.sin_dtype == kF32 ? 4 : 2;
-      bulk_prefetch_l2(reinterpret_cast<const char*>(p.s_in) + (slot * p.sin_slot + (int64_t)h * p.sin_head) * es, D * D * es);
+      bulk_prefetch_l2(reinterpret_cast<const char*>(p.s_in) + (r.slot * p.sin_slot + (int64_t)h * p.sin_head) * es, D * D * es);
     }
     const int hq = h / (p.H / p.H_qk), hv = h / (p.H / p.H_v);
     for (int c = 0; c < nch; ++c, ++ci) {
@@ -236,6 +257,7 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
       ++kv_loads;
     }
   }
+  if (ok && lane == 0) sm->empties = empties;  // ahead of the last record
   if (ok) ok = publish(Rec{0, 0, 0, -1, 0, 0, 0});
   if (!ok && lane == 0) give_up(p, sm);
   // loads that no role waits for any more land before the CTA's shared memory goes away
@@ -340,7 +362,7 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
       __syncwarp();
     }
     if (failed) break;
-    sums += r.nch > 0;
+    ++sums;
   }
   if (failed && lane == 0) give_up(p, sm);
   if (leader) mma_commit(&sm->drain);
@@ -427,7 +449,6 @@ __device__ __forceinline__ void run_gates(const DecayPrefillParams& p, Small* sm
       warp_arrive(&sm->gate_full[b], lane);
     }
     if (failed) break;
-    if (kStates && r.nch == 0 && lane == 0) p.ws_decay[r.out] = 1.f;
   }
   if (failed && lane == 0) give_up(p, sm);
 }
@@ -475,7 +496,7 @@ __device__ __forceinline__ void run_po(const DecayPrefillParams& p, uint8_t* bas
   Rec r;
   int u = 0, left = 0;  // units seen, chunks of the current one that are not begun
   auto another = [&] {  // whether there is a chunk to begin
-    while (left == 0 && next_unit(sm, u, lane, &r, &failed)) { left = r.nch; ++u; }
+    if (left == 0 && next_unit(sm, u, lane, &r, &failed)) { left = r.nch; ++u; }
     return left-- > 0;
   };
   // Q of chunk `at` from shared memory to TMEM, the A operand of two products, once V_d^T K of the
@@ -693,6 +714,11 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
       for (int e = 0; e < 32; ++e) x[e] = 0u;
     }
   };
+  auto store_out = [&](int c0, const uint32_t (&x)[32]) {
+    const int64_t at = row * D + c0;
+    if (r.out >= 0) store_state32(p.ws, kF32, (int64_t)r.out * (D * D) + at, x);
+    else store_state32(p.s_out, p.sout_dtype, r.slot * p.sout_slot + (int64_t)r.h * p.sout_head + at, x);
+  };
   for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
     for (int c = 0; c < r.nch && !kStates; ++c, ++ci) {
       const int st = ci & 1;
@@ -729,23 +755,19 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
       if (lane == 0) mbar_arrive(&sm->gate_empty[st]);
     }
     if (failed) break;
-    // the state that the unit leaves (an empty one passes on what it got); the next unit may
-    // overwrite TMEM and the 16-bit copy after that, Q S^T having run before
-    if (kStates) ci += r.nch > 0;  // sums so far
-    if (r.nch > 0 && !wait(sm, &sm->s_done, (ci - 1) & 1)) { failed = true; break; }
+    // the state that the unit leaves; the next unit may overwrite TMEM and the 16-bit copy after
+    // that, Q S^T having run before
+    if (kStates) ++ci;  // sums so far
+    if (!wait(sm, &sm->s_done, (ci - 1) & 1)) { failed = true; break; }
     if (r.out == kNone || (r.out == kPool && !p.s_out)) continue;
     tc_fence_after();
-    const bool start = kStates && r.in == kPool && p.s_in && r.nch > 0;
+    const bool start = kStates && r.in == kPool && p.s_in;
     const float2 whole = pair(start ? p.ws_decay[r.out] : 0.f);
 #pragma unroll 1
     for (int q = 0; q < 4; ++q) {
       uint32_t x[32];
-      if (r.nch == 0) {
-        load_in(32 * q, x);
-      } else {
-        tmem_ld32(ts + 32 * q, x);
-        tmem_ld_wait();
-      }
+      tmem_ld32(ts + 32 * q, x);
+      tmem_ld_wait();
       if (start) {  // what the segment added, and the state that it started from
         uint32_t y[32];
         load_in(32 * q, y);
@@ -756,16 +778,39 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
           x[e + 1] = __float_as_uint(z.y);
         }
       }
-      const int64_t at = row * D + 32 * q;
-      if (r.out >= 0) store_state32(p.ws, kF32, (int64_t)r.out * (D * D) + at, x);
-      else store_state32(p.s_out, p.sout_dtype, r.slot * p.sout_slot + (int64_t)r.h * p.sout_head + at, x);
+      store_out(32 * q, x);
     }
-    if (kStates && r.nch > 0) {
+    if (kStates) {
       tc_fence_before();
       warp_arrive(&sm->s_ready, lane);
     }
   }
-  if (failed && lane == 0) give_up(p, sm);
+  if (failed) {
+    if (lane == 0) give_up(p, sm);
+    return;
+  }
+  // units without chunks pass on what they got: 32 units looked at together, a lane each
+  const int64_t units = sm->empties ? unit_count<kStates>(p) : 0;
+  for (int64_t x0 = blockIdx.x; x0 < units; x0 += 32 * (int64_t)gridDim.x) {
+    const int64_t x = x0 + (int64_t)lane * gridDim.x;
+    Rec mine{};
+    bool empty = x < units && unit_at<kStates>(p, x, &mine) == 0 && mine.nch == 0;
+    for (unsigned left = __ballot_sync(0xffffffffu, empty); left; left &= left - 1) {
+      const int from = __ffs(left) - 1;
+      r.h = __shfl_sync(0xffffffffu, mine.h, from);
+      r.in = __shfl_sync(0xffffffffu, mine.in, from);
+      r.out = __shfl_sync(0xffffffffu, mine.out, from);
+      r.slot = __shfl_sync(0xffffffffu, mine.slot, from);
+      if (kStates && w == 0 && lane == 0) p.ws_decay[r.out] = 1.f;
+      if (r.out == kNone || (r.out == kPool && !p.s_out)) continue;
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        uint32_t y[32];
+        load_in(32 * q, y);
+        store_out(32 * q, y);
+      }
+    }
+  }
 }
 
 // ------------------------------------------------------------ warps 16-23: V_d

@@ -3,10 +3,14 @@
 Bounds (relative L2 of each (sequence, head) on its own, fixed before the first run):
 
 * 16-bit outputs: three independent roundings to the 16-bit type reach an output (the
-  decayed scores, the state as it is read, the output itself), each at most half a unit:
-  sqrt(3) 2^-9 = 3.4e-3 for bf16, held to 2^-8; sqrt(3) 2^-12 = 4.2e-4 for f16, held to 2^-11.
-* 16-bit states: the state's own rounding, at most 2^-9 (bf16) or 2^-12 (f16), plus the
-  f32 error below: held to 2.1e-3 and 2.7e-4.
+  decayed scores, the state as it is read, the output itself).  A rounding is off by 0.42
+  of the unit roundoff in the root mean square, 1.7e-3 for bf16 and 2.1e-4 for f16, so that
+  the three are at most sqrt(3) times that, 2.9e-3 and 3.6e-4: held to 2^-8 and 2^-11.  It
+  takes some hundred independent roundings for that; the few scores of a sequence of one or
+  two tokens can be off by a whole roundoff, 2^-8, on their own, and such sequences are
+  judged together where there are many of them.
+* 16-bit states: the state's own rounding, 1.7e-3 (bf16) or 2.1e-4 (f16), plus the f32 error
+  below: held to 2.1e-3 and 2.7e-4.
 * f32 states: sums of up to some thousand f32 products and decays exp(sum log g), whose
   exponent is known to about 2^-23 of its size (at most 100 where the decay counts): 1e-5.
 """

@@ -336,3 +336,19 @@ def test_segments_in_a_graph():
     graph.replay()
     o_ref, s_ref = R.recurrence(q, k, v, g, SCALE, None, [9000])
     R.check(out, o_ref, st, s_ref, [9000])
+
+
+@pytest.mark.parametrize("splits", [1, 2])
+def test_long_runs_of_empty_sequences(force_split, splits):
+    """Rounds of empty sequences between others, as every CTA of a persistent grid meets them."""
+    force_split(splits)
+    lengths = [2] * 200 + [0] * 2000 + [130, 1] * 100
+    q, k, v, g, cu = R.make(lengths, 1, 1, seed=50)
+    s0 = R.states(len(lengths), 1, F32, 50)
+    out, st = gdn.decay_linear_attention(q, k, v, g, initial_state=s0, output_final_state=True, cu_seqlens=cu)
+    o_ref, s_ref = R.recurrence(q, k, v, g, SCALE, s0, lengths)
+    assert gdn.device_status() == 0
+    assert R.rel(out, o_ref) <= R.OUT[BF]
+    assert max(R.rel(a, b) for a, b in zip(st, s_ref)) <= R.STATE[F32]
+    empty = torch.tensor([n == 0 for n in lengths], device="cuda")
+    assert torch.equal(st[empty], s0[empty])
