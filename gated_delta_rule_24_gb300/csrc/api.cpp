@@ -898,10 +898,12 @@ gdn_status_t gdn_decay_prefill(const gdn_tensor_t* q, const gdn_tensor_t* k, con
   if (initial_state) {
     p.s_in = initial_state->data; p.sin_slot = initial_state->stride[0]; p.sin_head = initial_state->stride[1];
     p.sin_slots = initial_state->shape[0]; p.sin_dtype = initial_state->dtype;
+    p.sin_tma = initial_state->dtype == q->dtype && encode_state_pool(&p.tm_sin, initial_state) ? 1 : 0;
   }
   if (output_state) {
     p.s_out = output_state->data; p.sout_slot = output_state->stride[0]; p.sout_head = output_state->stride[1];
     p.sout_slots = output_state->shape[0]; p.sout_dtype = output_state->dtype;
+    p.sout_tma = encode_state_pool(&p.tm_sout, output_state) ? 1 : 0;
   }
   if (state_indices) { p.state_idx = state_indices->data; p.idx_dtype = state_indices->dtype; }
   p.cu = cu_seqlens->data;

@@ -86,7 +86,7 @@ constexpr uint32_t kOffKv = kTile;           // after Q: two stages of K, V; a l
 constexpr uint32_t kOffS = kOffKv + 4 * kTile;  // 16-bit copy of S
 constexpr uint32_t kOffO = kOffS + kTile;    // the output tile on its way out
 constexpr uint32_t kOffSmall = kOffO + kTile;
-constexpr int kRecs = 4;
+constexpr int kRecs = 3;
 
 struct Rec {       // one unit: a sequence, or a segment of one, of one head.  Only units with chunks go round
   int32_t t0, len, h, nch;  // first token, tokens, head, chunks (-1: no more units)
@@ -108,7 +108,8 @@ struct Small {
   uint64_t gate_full[2], gate_empty[2], cf_empty;
   uint64_t qk_done, qs_done, s_done, o_done;   // products that have completed
   uint64_t q_ready, p_ready, o_free, o_staged;  // warps 4-11
-  uint64_t o_stored;                            // warp 3
+  uint64_t o_stored, f_stored;                  // warp 3
+  uint64_t f_staged, si_full;                   // warps 12-15; an incoming state by TMA
   uint64_t s_ready, vd_full[kVdSlots];         // warps 12-15, 16-23
   uint64_t vd_empty[kVdSlots], drain;
   uint32_t tmem;
@@ -196,6 +197,11 @@ __device__ __forceinline__ int unit_at(const DecayPrefillParams& p, int64_t x, R
   return 0;
 }
 
+// Whether a unit's state comes by TMA, straight into the place of its 16-bit copy, and whether the
+// one that it leaves goes by TMA, from that place.
+__device__ __forceinline__ bool state_in_tma(const DecayPrefillParams& p, const Rec& r) { return p.sin_tma && r.in == kPool; }
+__device__ __forceinline__ bool state_out_tma(const DecayPrefillParams& p, const Rec& r) { return p.sout_tma && r.out == kPool; }
+
 // ------------------------------------------------------------ warp 0: loads
 template <bool kStates>
 __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_t* base, Small* sm, int lane) {
@@ -204,7 +210,7 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
   const int64_t units = unit_count<kStates>(p);
   int empties = 0;
   constexpr int kKv = kv_stages<kStates>();
-  int kv_loads = 0, q_loads = 0;
+  int kv_loads = 0, q_loads = 0, s_loads = 0, outs = 0;  // outs: states by TMA of the units so far
   auto publish = [&](const Rec& r) {
     const int slot = u % kRecs;
     if (u >= kRecs && !wait(sm, &sm->rec_empty[slot], (u / kRecs - 1) & 1)) return false;
@@ -255,7 +261,20 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
         load(k + kTile, &p.tm_v, &sm->v_full[s], hv);
       }
       ++kv_loads;
+      if (!kStates && c == 0 && state_in_tma(p, r)) {
+        // what was in its place has been read: by Q S^T, by warps 12-15, and by the state's own way out
+        ok = (ci == 0 || (wait(sm, &sm->qs_done, (ci - 1) & 1) && wait(sm, &sm->s_ready, (ci - 1) & 1))) &&
+             (outs == 0 || wait(sm, &sm->f_stored, (outs - 1) & 1));
+        if (!ok) break;
+        if (lane == 0) {
+          mbar_arrive_expect_tx(&sm->si_full, kTile);
+          tma_load_4d(base + kOffS, &p.tm_sin, &sm->si_full, 0, 0, h, (int)r.slot);
+          tma_load_4d(base + kOffS + kHalf, &p.tm_sin, &sm->si_full, 64, 0, h, (int)r.slot);
+        }
+        ++s_loads;
+      }
     }
+    outs += !kStates && state_out_tma(p, r);
   }
   if (ok && lane == 0) sm->empties = empties;  // ahead of the last record
   if (ok) ok = publish(Rec{0, 0, 0, -1, 0, 0, 0});
@@ -270,6 +289,7 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
   landed(sm->k_full, kv_loads);
   landed(sm->v_full, kv_loads);
   if (q_loads) drain(&sm->q_full, (q_loads - 1) & 1);
+  if (s_loads) drain(&sm->si_full, (s_loads - 1) & 1);
 }
 
 // ------------------------------------------------------------ warp 1: products
@@ -294,7 +314,7 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
   const bool leader = elect_one();
   bool failed = false;
   Rec r;
-  int ci = 0, sums = 0;  // chunks so far; units with chunks so far (states)
+  int ci = 0, sums = 0, ins = 0;  // chunks so far; units (states); states by TMA
   for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
     for (int c = 0; c < r.nch; ++c, ++ci) {
       const int s = ci % kv_stages<kStates>();
@@ -317,7 +337,9 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
         }
         __syncwarp();
         // Q S^T
-        if (!(wait(sm, &sm->s_ready, one) && (ci == 0 || wait(sm, &sm->o_free, one ^ 1)))) { failed = true; break; }
+        const bool direct = c == 0 && state_in_tma(p, r);  // the copy that is read came by TMA
+        if (!((direct ? wait(sm, &sm->si_full, ins & 1) : wait(sm, &sm->s_ready, one)) &&
+              (ci == 0 || wait(sm, &sm->o_free, one ^ 1)))) { failed = true; break; }
         tc_fence_after();
         if (leader) {
 #pragma unroll
@@ -326,6 +348,10 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
           mma_commit(&sm->qs_done);
         }
         __syncwarp();
+        if (direct) {
+          ++ins;
+          if (!wait(sm, &sm->s_ready, one)) { failed = true; break; }
+        }
       }
       // V_d^T K
 #pragma unroll 1
@@ -457,10 +483,20 @@ __device__ __forceinline__ void run_gates(const DecayPrefillParams& p, Small* sm
 __device__ __forceinline__ void run_store(const DecayPrefillParams& p, uint8_t* base, Small* sm, int lane) {
   bool failed = false;
   Rec r;
-  int ci = 0;
+  int ci = 0, outs = 0;  // tiles and states that have gone out
   for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
     for (int c = 0; c < r.nch; ++c, ++ci) {
       const int t0 = r.t0 + c * C, left = r.len - c * C;
+      if (c + 1 == r.nch && state_out_tma(p, r)) {  // ready before the last tile is
+        if (!wait(sm, &sm->f_staged, outs++ & 1)) { failed = true; break; }
+        if (lane == 0) {
+          tma_store_4d(&p.tm_sout, base + kOffS, 0, 0, r.h, (int)r.slot);
+          tma_store_4d(&p.tm_sout, base + kOffS + kHalf, 64, 0, r.h, (int)r.slot);
+          bulk_commit();
+          bulk_wait_read_all();
+        }
+        warp_arrive(&sm->f_stored, lane);
+      }
       if (!wait(sm, &sm->o_staged, ci & 1)) { failed = true; break; }
       uint8_t* tile = base + kOffO;
       if (left >= C) {
@@ -471,13 +507,12 @@ __device__ __forceinline__ void run_store(const DecayPrefillParams& p, uint8_t* 
           bulk_wait_read_all();
         }
       } else {  // only the sequence's own rows: the next rows belong to another unit
-        char* o = reinterpret_cast<char*>(p.out) + ((int64_t)t0 * p.o_st + (int64_t)r.h * p.o_sh) * 2;
+        const int ch = lane & 15;
+        const uint8_t* from = tile + (ch >> 3) * kHalf;
+        char* o = reinterpret_cast<char*>(p.out) + ((int64_t)(t0 + (lane >> 4)) * p.o_st + (int64_t)r.h * p.o_sh) * 2 + ch * 16;
 #pragma unroll 4
-        for (int e = lane; e < left * 16; e += 32) {
-          const int row = e >> 4, ch = e & 15;
-          *reinterpret_cast<uint4*>(o + (int64_t)row * p.o_st * 2 + ch * 16) =
-              *reinterpret_cast<const uint4*>(tile + (ch >> 3) * kHalf + sw128_chunk(row, ch & 7));
-        }
+        for (int row = lane >> 4; row < left; row += 2, o += p.o_st * 4)
+          *reinterpret_cast<uint4*>(o) = *reinterpret_cast<const uint4*>(from + sw128_chunk(row, ch & 7));
       }
       warp_arrive(&sm->o_stored, lane);
     }
@@ -703,7 +738,7 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
   uint8_t* sb = base + kOffS;
   bool failed = false;
   Rec r{};
-  int ci = 0;
+  int ci = 0, ins = 0, outs = 0;  // chunks; states by TMA that came and went
   auto load_in = [&](int c0, uint32_t (&x)[32]) {
     if (r.in >= 0) {
       load_state32(p.ws, kF32, (int64_t)r.in * (D * D) + row * D + c0, x);
@@ -726,17 +761,34 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
       if (!(wait(sm, &sm->gate_full[st], (ci >> 1) & 1) && (c == 0 || wait(sm, &sm->s_done, (ci - 1) & 1)))) { failed = true; break; }
       tc_fence_after();
       const float2 gam = pair(sm->gamma[st]);
+      const bool direct = c == 0 && state_in_tma(p, r);  // the copy came by TMA
+      if (c == 0 && !(direct ? wait(sm, &sm->si_full, ins++ & 1) : outs == 0 || wait(sm, &sm->f_stored, (outs - 1) & 1))) {
+        failed = true;
+        break;
+      }
 #pragma unroll 1
       for (int q = 0; q < 4; ++q) {
         uint32_t x[32];
-        if (c == 0) {
+        if (direct) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint4 z = *reinterpret_cast<const uint4*>(sb + (q >> 1) * kHalf + sw128_chunk(row, 4 * (q & 1) + e));
+            const uint32_t zw[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const float2 f = unpack16<F16>(zw[i]);
+              x[8 * e + 2 * i] = __float_as_uint(f.x);
+              x[8 * e + 2 * i + 1] = __float_as_uint(f.y);
+            }
+          }
+        } else if (c == 0) {
           load_in(32 * q, x);
         } else {
           tmem_ld32(ts + 32 * q, x);
           tmem_ld_wait();
         }
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
+        for (int e = 0; e < 4 && !direct; ++e)
           *reinterpret_cast<uint4*>(sb + (q >> 1) * kHalf + sw128_chunk(row, 4 * (q & 1) + e)) =
               make_uint4(pack16x2<F16>(pair_at(x + 8 * e)), pack16x2<F16>(pair_at(x + 8 * e + 2)),
                          pack16x2<F16>(pair_at(x + 8 * e + 4)), pack16x2<F16>(pair_at(x + 8 * e + 6)));
@@ -761,6 +813,28 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
     if (!wait(sm, &sm->s_done, (ci - 1) & 1)) { failed = true; break; }
     if (r.out == kNone || (r.out == kPool && !p.s_out)) continue;
     tc_fence_after();
+    if (!kStates && state_out_tma(p, r)) {
+      ++outs;
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        uint32_t x[32];
+        tmem_ld32(ts + 32 * q, x);
+        tmem_ld_wait();
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          uint32_t y[4];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 f = pair_at(x + 8 * e + 2 * i);
+            y[i] = p.sout_dtype == kF16 ? pack16x2<true>(f) : pack16x2<false>(f);
+          }
+          *reinterpret_cast<uint4*>(sb + (q >> 1) * kHalf + sw128_chunk(row, 4 * (q & 1) + e)) = make_uint4(y[0], y[1], y[2], y[3]);
+        }
+      }
+      fence_proxy_async_smem();
+      warp_arrive(&sm->f_staged, lane);
+      continue;
+    }
     const bool start = kStates && r.in == kPool && p.s_in;
     const float2 whole = pair(start ? p.ws_decay[r.out] : 0.f);
 #pragma unroll 1
@@ -918,6 +992,9 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __
     init(&sm->o_staged, 1, kPoWarps);
     init(&sm->q_ready, 1, kPoWarps);
     init(&sm->o_stored, 1, 1);
+    init(&sm->f_stored, 1, 1);
+    init(&sm->f_staged, 1, kSWarps);
+    init(&sm->si_full, 1, 1);
     init(&sm->s_ready, 1, kSWarps);
     init(sm->vd_full, kVdSlots, kVWarps);
     init(sm->vd_empty, kVdSlots, 1);
