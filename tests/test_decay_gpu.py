@@ -352,3 +352,16 @@ def test_long_runs_of_empty_sequences(force_split, splits):
     assert max(R.rel(a, b) for a, b in zip(st, s_ref)) <= R.STATE[F32]
     empty = torch.tensor([n == 0 for n in lengths], device="cuda")
     assert torch.equal(st[empty], s0[empty])
+
+
+def test_example_layer():
+    """The example's prompts and steps agree with one long prompt to what their 16-bit states and
+    outputs allow: each step rounds the state to bf16 (1.7e-3), eight of them and the roundings on
+    either side (2.9e-3 each) are within 1e-2 together."""
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "decay_layer.py")
+    spec = importlib.util.spec_from_file_location("decay_layer", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    assert module.main() <= 1e-2
