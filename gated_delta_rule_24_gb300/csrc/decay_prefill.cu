@@ -541,7 +541,7 @@ __device__ __forceinline__ void run_po(const DecayPrefillParams& p, uint8_t* bas
     if (!(wait(sm, &sm->q_full, at & 1) && (at == 0 || wait(sm, &sm->s_done, (at - 1) & 1)))) return false;
     tc_fence_after();
     const int rr = 32 * w + ((lane >> 3) & 1) * 8 + (lane & 7);
-#pragma unroll
+#pragma unroll 2
     for (int j = 0; j < 4; ++j)
 #pragma unroll
       for (int rb = 0; rb < 2; ++rb) {
@@ -566,43 +566,41 @@ __device__ __forceinline__ void run_po(const DecayPrefillParams& p, uint8_t* bas
       tc_fence_after();
       const float gi = sm->G[b][row];
       const bool mild = sm->mild[b] != 0;
-      // P in blocks of 32 columns: by factors before this warp's diagonal block, pair by pair in it,
-      // zeros behind it.  In the order 0, 1 and 3, 2 each goes over columns that its warp has read.
+      // P in blocks of 16 columns, by factors up to this warp's diagonal ones and zeros behind them, in the
+      // order 0 .. 3 and 7 .. 4 so that each goes over columns that its warp has read.  Rolled up: the
+      // roles together fill the instruction cache.
 #pragma unroll 1
-      for (int it = 0; it < 2; ++it) {
-        const int jb = hf ? 3 - it : it;
-        uint32_t x[32], pk[16];
-        if (jb <= w) {
-          tmem_ld32(tr + kTmAcc + 32 * jb, x);
+      for (int it = 0; it < 4; ++it) {
+        const int jb = hf ? 7 - it : it, j0 = 16 * jb;
+        uint32_t pk[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) pk[e] = 0u;
+        if (jb <= 2 * w + 1) {
+          uint32_t x[16];
+          tmem_ld16(tr + kTmAcc + j0, x);
+          const float2 rf = pair(p.scale * exp2_fast(gi - sm->G[b][j0 + 15]));
           tmem_ld_wait();
-        }
-        if (jb < w || (jb == w && mild)) {
+          if (mild || jb < 2 * w) {
 #pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const float2 rf = pair(p.scale * exp2_fast(gi - sm->G[b][32 * jb + 16 * q + 15]));
-#pragma unroll
-            for (int e = 8 * q; e < 8 * q + 8; e += 2) {
-              const float4 f = *reinterpret_cast<const float4*>(&sm->cf[32 * jb + 2 * e]);
+            for (int e = 0; e < 8; e += 2) {
+              const float4 f = *reinterpret_cast<const float4*>(&sm->cf[j0 + 2 * e]);
               pk[e] = pack16x2<F16>(mul2(pair_at(x + 2 * e), mul2(make_float2(f.x, f.y), rf)));
               pk[e + 1] = pack16x2<F16>(mul2(pair_at(x + 2 * e + 2), mul2(make_float2(f.z, f.w), rf)));
             }
-          }
-          if (jb == w) {
+          } else {  // pair by pair
 #pragma unroll
-            for (int e = 0; e < 16; ++e) pk[e] = 2 * e > lane ? 0u : 2 * e == lane ? pk[e] & 0xffffu : pk[e];
+            for (int e = 0; e < 8; ++e) {
+              const float2 f = *reinterpret_cast<const float2*>(&sm->G[b][j0 + 2 * e]);
+              pk[e] = pack16x2<F16>(mul2(mul2(pair_at(x + 2 * e), pair(p.scale)), make_float2(exp2_fast(gi - f.x), exp2_fast(gi - f.y))));
+            }
           }
-        } else if (jb == w) {
+          if (jb >= 2 * w) {  // pairs behind the diagonal, whose factor may be infinite, go
+            const int d = row - j0;
 #pragma unroll
-          for (int e = 0; e < 16; ++e) {
-            const float2 f = *reinterpret_cast<const float2*>(&sm->G[b][32 * jb + 2 * e]);
-            const float2 y = mul2(mul2(pair_at(x + 2 * e), pair(p.scale)), make_float2(exp2_fast(gi - f.x), exp2_fast(gi - f.y)));
-            pk[e] = pack16x2<F16>(2 * e <= lane ? y.x : 0.f, 2 * e + 1 <= lane ? y.y : 0.f);
+            for (int e = 0; e < 8; ++e) pk[e] = 2 * e > d ? 0u : 2 * e == d ? pk[e] & 0xffffu : pk[e];
           }
-        } else {
-#pragma unroll
-          for (int e = 0; e < 16; ++e) pk[e] = 0u;
         }
-        tmem_st16(tr + p_block_col(jb), pk);
+        tmem_st8(tr + p_block_col(jb / 2) + 8 * (jb & 1), pk);
       }
       tc_fence_before();
       warp_arrive(&sm->cf_empty, lane);
@@ -920,7 +918,7 @@ __device__ __forceinline__ void run_v(const DecayPrefillParams& p, uint8_t* base
               (kStates || slot != 1 || wait(sm, &sm->qs_done, ci & 1)) &&
               (kStates || slot != 2 || wait(sm, &sm->cf_empty, ci & 1)))) { failed = true; break; }
         tc_fence_after();
-#pragma unroll
+#pragma unroll 2
         for (int tt = 0; tt < kSub / 16; ++tt) {
           const int tok = sub * kSub + 16 * tt;  // 16 tokens from here
           const int at2 = (tok >> 1) + (lane & 3);  // this lane's first pair of tokens; the second is 4 pairs on
