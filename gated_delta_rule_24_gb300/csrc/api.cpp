@@ -148,6 +148,20 @@ bool encode_state_pool(CUtensorMap* m, const gdn_tensor_t* t) {
   return r == CUDA_SUCCESS;
 }
 
+// A pool of f32 states [slots, heads, 128, 128] by tiles of 32 columns.
+bool encode_f32_states(CUtensorMap* m, void* data, int64_t heads, int64_t slots, int64_t head_stride, int64_t slot_stride) {
+  cuuint64_t dims[4] = {128, 128, (cuuint64_t)heads, (cuuint64_t)slots};
+  cuuint64_t strides[3] = {512, (cuuint64_t)head_stride * 4, (cuuint64_t)slot_stride * 4};
+  cuuint32_t box[4] = {32, 128, 1, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  return g_encode(m, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, data, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                  CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_NONE, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool encode_decay_state(CUtensorMap* m, const gdn_tensor_t* t) {
+  if (t->dtype != GDN_F32) return encode_state_pool(m, t);
+  return encode_f32_states(m, t->data, t->shape[1], t->shape[0], t->stride[1], t->stride[0]);
+}
+
 gdn_status_t check_qkv(const gdn_tensor_t* t, const char* name) {
   gdn_status_t st = check_basic(t, name, 3);
   if (st != GDN_OK) return st;
@@ -898,12 +912,12 @@ gdn_status_t gdn_decay_prefill(const gdn_tensor_t* q, const gdn_tensor_t* k, con
   if (initial_state) {
     p.s_in = initial_state->data; p.sin_slot = initial_state->stride[0]; p.sin_head = initial_state->stride[1];
     p.sin_slots = initial_state->shape[0]; p.sin_dtype = initial_state->dtype;
-    p.sin_tma = initial_state->dtype == q->dtype && encode_state_pool(&p.tm_sin, initial_state) ? 1 : 0;
+    p.sin_tma = (initial_state->dtype == q->dtype || initial_state->dtype == GDN_F32) && encode_decay_state(&p.tm_sin, initial_state);
   }
   if (output_state) {
     p.s_out = output_state->data; p.sout_slot = output_state->stride[0]; p.sout_head = output_state->stride[1];
     p.sout_slots = output_state->shape[0]; p.sout_dtype = output_state->dtype;
-    p.sout_tma = encode_state_pool(&p.tm_sout, output_state) ? 1 : 0;
+    p.sout_tma = encode_decay_state(&p.tm_sout, output_state);
   }
   if (state_indices) { p.state_idx = state_indices->data; p.idx_dtype = state_indices->dtype; }
   p.cu = cu_seqlens->data;
@@ -921,6 +935,8 @@ gdn_status_t gdn_decay_prefill(const gdn_tensor_t* q, const gdn_tensor_t* k, con
     if ((st = ensure_workspace(g_dev[dev], decay_ws_bytes(N, s.H, p.splits), stream)) != GDN_OK) return st;
     p.ws = g_dev[dev].ws;
     p.ws_decay = p.ws + N * s.H * (p.splits - 1) * 16384;
+    if (!encode_f32_states(&p.tm_ws, p.ws, 1, N * s.H * (p.splits - 1), 16384, 16384))
+      return fail(GDN_ERR_CUDA, "decay prefill: no tensor map for the workspace");
   }
   cudaError_t e = gdn::launch_decay_prefill(p, stream);
   if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "decay prefill launch: %s", cudaGetErrorString(e));

@@ -35,8 +35,9 @@ struct DecayPrefillParams {
   CUtensorMap tm_k;
   CUtensorMap tm_v;  // [T, H_v, 128]
   CUtensorMap tm_o;  // output [T, H, 128] (stores)
-  CUtensorMap tm_sin;   // 16-bit state pools [slots, H, 128, 128], box (64 columns, 128 rows, 1, 1), 128B
+  CUtensorMap tm_sin;   // state pools [slots, H, 128, 128], box (128 bytes of columns, 128 rows, 1, 1), 128B
   CUtensorMap tm_sout;  // swizzle; valid where sin_tma, sout_tma say so
+  CUtensorMap tm_ws;    // the states of the workspace, as a pool of one head
   const void* g;     // [T, H] or null, strides in elements; a token stride of 0 is one decay for each head
   int64_t g_st, g_sh;
   const void* s_in;  // [slots, H, 128, 128] or null
@@ -53,7 +54,7 @@ struct DecayPrefillParams {
   int32_t g_dtype, sin_dtype, sout_dtype, idx_dtype, cu_dtype;
   float scale;
   int32_t op_f16;
-  int32_t sin_tma, sout_tma;  // incoming states by TMA (of q's dtype only), outgoing ones by TMA
+  int32_t sin_tma, sout_tma;  // incoming states by TMA (f32 or of q's dtype), outgoing ones by TMA
   // Sequences cut into `splits` segments of whole chunks (1: not cut), segment x of a sequence of c
   // chunks holding chunks [c x / splits, c (x + 1) / splits).  With U = N H and unit nh = n H + h:
   float* ws;        // [U][splits - 1] states of 128 x 128: the state behind segment x, once joined

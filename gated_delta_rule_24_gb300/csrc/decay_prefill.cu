@@ -109,7 +109,8 @@ struct Small {
   uint64_t qk_done, qs_done, s_done, o_done;   // products that have completed
   uint64_t q_ready, p_ready, o_free, o_staged;  // warps 4-11
   uint64_t o_stored, f_stored;                  // warp 3
-  uint64_t f_staged, si_full;                   // warps 12-15; an incoming state by TMA
+  uint64_t f_staged, si_full;                   // warps 12-15; an incoming 16-bit state
+  uint64_t sf_full, sf_empty;                   // an incoming f32 state
   uint64_t s_ready, vd_full[kVdSlots];         // warps 12-15, 16-23
   uint64_t vd_empty[kVdSlots], drain;
   uint32_t tmem;
@@ -122,6 +123,16 @@ template <bool kStates>
 __host__ __device__ constexpr int kv_stages() { return kStates ? 3 : 2; }
 constexpr int kPoWarps = 8, kSWarps = 4, kVWarps = 8;
 constexpr int kThreads = 32 * (4 + kPoWarps + kSWarps + kVWarps);
+// The stages of K and V as a role goes through them, with the phase of each.
+template <bool kStates>
+struct Ring {
+  int s = 0;
+  uint32_t phases = 0;
+  __device__ __forceinline__ uint32_t phase() const { return phases >> s & 1; }
+  __device__ __forceinline__ void pass() { s = s + 1 == kv_stages<kStates>() ? 0 : s + 1; }  // over an f32 state
+  __device__ __forceinline__ void next() { phases ^= 1u << s; pass(); }                      // over a chunk
+};
+
 // Every wait: bounded (kTries probes of up to 20 us each), and over as soon as another role has
 // given up.  Only the first probe is in line: the roles together fill the instruction cache.
 constexpr int kTries = 50000;
@@ -197,20 +208,42 @@ __device__ __forceinline__ int unit_at(const DecayPrefillParams& p, int64_t x, R
   return 0;
 }
 
-// Whether a unit's state comes by TMA, straight into the place of its 16-bit copy, and whether the
-// one that it leaves goes by TMA, from that place.
-__device__ __forceinline__ bool state_in_tma(const DecayPrefillParams& p, const Rec& r) { return p.sin_tma && r.in == kPool; }
+// Whether a unit's state comes by TMA, in 16 bits straight into the place of its 16-bit copy or in f32
+// into a stage of K and V (as those behind segments do), and whether the one that it leaves goes by
+// TMA, from the place of the copy: f32 in two halves of 64 columns.
+// kWide: a launch that meets f32 states; the others keep the instructions for them out of the cache.
+template <bool kWide>
+__device__ __forceinline__ bool state_in_tma(const DecayPrefillParams& p, const Rec& r) {
+  return p.sin_tma && r.in == kPool && !(kWide && p.sin_dtype == kF32);
+}
+template <bool kWide>
+__device__ __forceinline__ bool state_in_ring(const DecayPrefillParams& p, const Rec& r) {
+  if (!kWide) return false;
+  return r.in >= 0 || (p.sin_tma && r.in == kPool && p.sin_dtype == kF32);
+}
 __device__ __forceinline__ bool state_out_tma(const DecayPrefillParams& p, const Rec& r) { return p.sout_tma && r.out == kPool; }
+template <bool kWide>
+__device__ __forceinline__ int state_out_parts(const DecayPrefillParams& p) { return kWide && p.sout_dtype == kF32 ? 2 : 1; }
 
 // ------------------------------------------------------------ warp 0: loads
-template <bool kStates>
+template <bool kStates, bool kWide>
 __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_t* base, Small* sm, int lane) {
   bool ok = true;
   int u = 0, ci = 0;  // units and chunks so far
+  Ring<kStates> ring;
+  uint32_t chunks_in = 0;  // bit s: a chunk has been in stage s
+  int f32_stage = -1;      // the stage that holds an f32 state
   const int64_t units = unit_count<kStates>(p);
   int empties = 0;
-  constexpr int kKv = kv_stages<kStates>();
-  int kv_loads = 0, q_loads = 0, s_loads = 0, outs = 0;  // outs: states by TMA of the units so far
+  int q_loads = 0, s_loads = 0, sf_loads = 0, outs = 0;  // outs: parts of states by TMA of the units so far
+  auto stage_free = [&] {
+    const int s = ring.s;
+    if (s == f32_stage) {
+      f32_stage = -1;
+      return wait(sm, &sm->sf_empty, (sf_loads - 1) & 1);
+    }
+    return !(chunks_in >> s & 1) || wait(sm, &sm->kv_empty[s], ring.phase() ^ 1);
+  };
   auto publish = [&](const Rec& r) {
     const int slot = u % kRecs;
     if (u >= kRecs && !wait(sm, &sm->rec_empty[slot], (u / kRecs - 1) & 1)) return false;
@@ -235,13 +268,26 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
     ok = publish(r);
     if (!ok) break;
     const int h = r.h, nch = r.nch, first = r.t0;
-    if (p.s_in && r.in == kPool && lane == 0) {
+    if (!kStates && state_in_ring<kWide>(p, r)) {
+      ok = stage_free();
+      if (!ok) break;
+      if (lane == 0) {
+        uint8_t* dst = base + kOffKv + ring.s * 2 * kTile;
+        mbar_arrive_expect_tx(&sm->sf_full, 2 * kTile);
+        for (int q = 0; q < 4; ++q)
+          if (r.in >= 0) tma_load_4d(dst + q * kHalf, &p.tm_ws, &sm->sf_full, 32 * q, 0, 0, r.in);
+          else tma_load_4d(dst + q * kHalf, &p.tm_sin, &sm->sf_full, 32 * q, 0, r.h, (int)r.slot);
+      }
+      ++sf_loads;
+      f32_stage = ring.s;
+      ring.pass();
+    } else if (p.s_in && r.in == kPool && lane == 0) {
       const int es = p.sin_dtype == kF32 ? 4 : 2;
       bulk_prefetch_l2(reinterpret_cast<const char*>(p.s_in) + (r.slot * p.sin_slot + (int64_t)h * p.sin_head) * es, D * D * es);
     }
     const int hq = h / (p.H / p.H_qk), hv = h / (p.H / p.H_v);
     for (int c = 0; c < nch; ++c, ++ci) {
-      const int s = ci % kKv, t0 = first + (kStates ? nch - 1 - c : c) * C;
+      const int s = ring.s, t0 = first + (kStates ? nch - 1 - c : c) * C;
       auto load = [&](uint8_t* dst, const CUtensorMap* tm, uint64_t* bar, int head) {
         mbar_arrive_expect_tx(bar, kTile);
         tma_load_3d(dst, tm, bar, 0, head, t0);
@@ -253,15 +299,16 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
         if (lane == 0) load(base, &p.tm_q, &sm->q_full, hq);
         ++q_loads;
       }
-      ok = ci < kKv || wait(sm, &sm->kv_empty[s], (ci / kKv - 1) & 1);
+      ok = stage_free();
       if (!ok) break;
+      chunks_in |= 1u << s;
       if (lane == 0) {
         uint8_t* k = base + kOffKv + s * 2 * kTile;
         load(k, &p.tm_k, &sm->k_full[s], hq);
         load(k + kTile, &p.tm_v, &sm->v_full[s], hv);
       }
-      ++kv_loads;
-      if (!kStates && c == 0 && state_in_tma(p, r)) {
+      ring.next();
+      if (!kStates && c == 0 && state_in_tma<kWide>(p, r)) {
         // what was in its place has been read: by Q S^T, by warps 12-15, and by the state's own way out
         ok = (ci == 0 || (wait(sm, &sm->qs_done, (ci - 1) & 1) && wait(sm, &sm->s_ready, (ci - 1) & 1))) &&
              (outs == 0 || wait(sm, &sm->f_stored, (outs - 1) & 1));
@@ -274,22 +321,20 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
         ++s_loads;
       }
     }
-    outs += !kStates && state_out_tma(p, r);
+    if (!kStates && state_out_tma(p, r)) outs += state_out_parts<kWide>(p);
   }
   if (ok && lane == 0) sm->empties = empties;  // ahead of the last record
   if (ok) ok = publish(Rec{0, 0, 0, -1, 0, 0, 0});
   if (!ok && lane == 0) give_up(p, sm);
   // loads that no role waits for any more land before the CTA's shared memory goes away
-  auto landed = [&](uint64_t (&bar)[3], int loads) {
-    for (int s = 0; s < kKv; ++s) {
-      const int n = (loads + kKv - 1 - s) / kKv;  // loads of stage s
-      if (n) drain(&bar[s], (n - 1) & 1);
-    }
-  };
-  landed(sm->k_full, kv_loads);
-  landed(sm->v_full, kv_loads);
+  for (int s = 0; s < kv_stages<kStates>(); ++s) {
+    if (!(chunks_in >> s & 1)) continue;
+    drain(&sm->k_full[s], (ring.phases >> s & 1) ^ 1);
+    drain(&sm->v_full[s], (ring.phases >> s & 1) ^ 1);
+  }
   if (q_loads) drain(&sm->q_full, (q_loads - 1) & 1);
   if (s_loads) drain(&sm->si_full, (s_loads - 1) & 1);
+  if (sf_loads) drain(&sm->sf_full, (sf_loads - 1) & 1);
 }
 
 // ------------------------------------------------------------ warp 1: products
@@ -304,7 +349,7 @@ __device__ __forceinline__ void vd_place(int ci, int b, int* slot, int* round) {
   *round = kTerms == 3 && !kStates && *slot == 0 ? 2 * ci + (b >> 1) : ci;
 }
 
-template <bool F16, int kTerms, bool kStates>
+template <bool F16, int kTerms, bool kStates, bool kWide>
 __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* base, Small* sm, uint32_t tmem, int lane) {
   constexpr int kSub = sub_tokens<kTerms>(), kSubs = C / kSub;
   const uint32_t id_kk = idesc_16_f32(F16, 128, 128, 0, 0, 0);  // B K-major
@@ -314,11 +359,13 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
   const bool leader = elect_one();
   bool failed = false;
   Rec r;
-  int ci = 0, sums = 0, ins = 0;  // chunks so far; units (states); states by TMA
+  int ci = 0, sums = 0, ins = 0;  // chunks so far; units (states); 16-bit states by TMA
+  Ring<kStates> ring;
   for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
-    for (int c = 0; c < r.nch; ++c, ++ci) {
-      const int s = ci % kv_stages<kStates>();
-      const uint32_t ph = (ci / kv_stages<kStates>()) & 1, one = ci & 1;
+    if (!kStates && state_in_ring<kWide>(p, r)) ring.pass();
+    for (int c = 0; c < r.nch; ++c, ++ci, ring.next()) {
+      const int s = ring.s;
+      const uint32_t ph = ring.phase(), one = ci & 1;
       const uint32_t k = smem_u32(base + kOffKv + s * 2 * kTile);
       const uint64_t d_k = sdesc_sw128(k, 16, 1024), d_kt = sdesc_sw128(k, kHalf, 1024);
       const uint64_t d_vt = sdesc_sw128(k + kTile, kHalf, 1024);
@@ -337,7 +384,7 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
         }
         __syncwarp();
         // Q S^T
-        const bool direct = c == 0 && state_in_tma(p, r);  // the copy that is read came by TMA
+        const bool direct = c == 0 && state_in_tma<kWide>(p, r);  // the copy that is read came by TMA
         if (!((direct ? wait(sm, &sm->si_full, ins & 1) : wait(sm, &sm->s_ready, one)) &&
               (ci == 0 || wait(sm, &sm->o_free, one ^ 1)))) { failed = true; break; }
         tc_fence_after();
@@ -480,6 +527,7 @@ __device__ __forceinline__ void run_gates(const DecayPrefillParams& p, Small* sm
 }
 
 // ------------------------------------------------------------ warp 3: output stores
+template <bool kWide>
 __device__ __forceinline__ void run_store(const DecayPrefillParams& p, uint8_t* base, Small* sm, int lane) {
   bool failed = false;
   Rec r;
@@ -488,14 +536,18 @@ __device__ __forceinline__ void run_store(const DecayPrefillParams& p, uint8_t* 
     for (int c = 0; c < r.nch; ++c, ++ci) {
       const int t0 = r.t0 + c * C, left = r.len - c * C;
       if (c + 1 == r.nch && state_out_tma(p, r)) {  // ready before the last tile is
-        if (!wait(sm, &sm->f_staged, outs++ & 1)) { failed = true; break; }
-        if (lane == 0) {
-          tma_store_4d(&p.tm_sout, base + kOffS, 0, 0, r.h, (int)r.slot);
-          tma_store_4d(&p.tm_sout, base + kOffS + kHalf, 64, 0, r.h, (int)r.slot);
-          bulk_commit();
-          bulk_wait_read_all();
+        const int parts = state_out_parts<kWide>(p), cols = 64 / parts;
+        for (int x = 0; x < parts && !failed; ++x) {
+          if (!wait(sm, &sm->f_staged, outs++ & 1)) { failed = true; break; }
+          if (lane == 0) {
+            tma_store_4d(&p.tm_sout, base + kOffS, 64 * x, 0, r.h, (int)r.slot);
+            tma_store_4d(&p.tm_sout, base + kOffS + kHalf, 64 * x + cols, 0, r.h, (int)r.slot);
+            bulk_commit();
+            bulk_wait_read_all();
+          }
+          warp_arrive(&sm->f_stored, lane);
         }
-        warp_arrive(&sm->f_stored, lane);
+        if (failed) break;
       }
       if (!wait(sm, &sm->o_staged, ci & 1)) { failed = true; break; }
       uint8_t* tile = base + kOffO;
@@ -655,8 +707,9 @@ __device__ __forceinline__ void run_po(const DecayPrefillParams& p, uint8_t* bas
 
 // ------------------------------------------------------------ warps 12-15: the state
 // 32 values of a state row, as the bits of f32.
+template <bool kWide>
 __device__ __forceinline__ void load_state32(const void* base, int dtype, int64_t off, uint32_t (&s)[32]) {
-  if (dtype == kF32) {
+  if (kWide && dtype == kF32) {
     const uint4* q = reinterpret_cast<const uint4*>(reinterpret_cast<const float*>(base) + off);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
@@ -678,8 +731,9 @@ __device__ __forceinline__ void load_state32(const void* base, int dtype, int64_
     }
   }
 }
+template <bool kWide>
 __device__ __forceinline__ void store_state32(void* base, int dtype, int64_t off, const uint32_t (&s)[32]) {
-  if (dtype == kF32) {
+  if (kWide && dtype == kF32) {
     uint4* q = reinterpret_cast<uint4*>(reinterpret_cast<float*>(base) + off);
 #pragma unroll
     for (int i = 0; i < 8; ++i) q[i] = make_uint4(s[4 * i], s[4 * i + 1], s[4 * i + 2], s[4 * i + 3]);
@@ -729,19 +783,20 @@ __device__ __forceinline__ void zero_tails(uint8_t* k, uint8_t* v, int left, int
   __syncwarp();
 }
 
-template <bool F16, bool kStates>
+template <bool F16, bool kStates, bool kWide>
 __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* base, Small* sm, uint32_t tmem, int warp, int lane) {
   const int w = warp & 3, row = 32 * w + lane;
   const uint32_t ts = tmem + ((uint32_t)(32 * w) << 16) + kTmS;
   uint8_t* sb = base + kOffS;
   bool failed = false;
   Rec r{};
-  int ci = 0, ins = 0, outs = 0;  // chunks; states by TMA that came and went
+  int ci = 0, ins = 0, fins = 0, outs = 0;  // chunks; 16-bit and f32 states by TMA that came, parts that went
+  int entries = 0;                          // of the stages of K and V
   auto load_in = [&](int c0, uint32_t (&x)[32]) {
-    if (r.in >= 0) {
-      load_state32(p.ws, kF32, (int64_t)r.in * (D * D) + row * D + c0, x);
+    if (kWide && r.in >= 0) {
+      load_state32<kWide>(p.ws, kF32, (int64_t)r.in * (D * D) + row * D + c0, x);
     } else if (r.in == kPool && p.s_in) {
-      load_state32(p.s_in, p.sin_dtype, r.slot * p.sin_slot + (int64_t)r.h * p.sin_head + row * D + c0, x);
+      load_state32<kWide>(p.s_in, p.sin_dtype, r.slot * p.sin_slot + (int64_t)r.h * p.sin_head + row * D + c0, x);
     } else {
 #pragma unroll
       for (int e = 0; e < 32; ++e) x[e] = 0u;
@@ -749,25 +804,38 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
   };
   auto store_out = [&](int c0, const uint32_t (&x)[32]) {
     const int64_t at = row * D + c0;
-    if (r.out >= 0) store_state32(p.ws, kF32, (int64_t)r.out * (D * D) + at, x);
-    else store_state32(p.s_out, p.sout_dtype, r.slot * p.sout_slot + (int64_t)r.h * p.sout_head + at, x);
+    if (kWide && r.out >= 0) store_state32<kWide>(p.ws, kF32, (int64_t)r.out * (D * D) + at, x);
+    else store_state32<kWide>(p.s_out, p.sout_dtype, r.slot * p.sout_slot + (int64_t)r.h * p.sout_head + at, x);
   };
   for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
+    const bool ring = !kStates && state_in_ring<kWide>(p, r);
+    const uint8_t* from = base + kOffKv + (entries & 1) * 2 * kTile;
+    entries += r.nch + ring;
     for (int c = 0; c < r.nch && !kStates; ++c, ++ci) {
       const int st = ci & 1;
       // S as the chunk finds it: to 16 bits for Q S^T, times the chunk's decay for V_d^T K
       if (!(wait(sm, &sm->gate_full[st], (ci >> 1) & 1) && (c == 0 || wait(sm, &sm->s_done, (ci - 1) & 1)))) { failed = true; break; }
       tc_fence_after();
       const float2 gam = pair(sm->gamma[st]);
-      const bool direct = c == 0 && state_in_tma(p, r);  // the copy came by TMA
+      const bool direct = c == 0 && state_in_tma<kWide>(p, r);  // the copy came by TMA
       if (c == 0 && !(direct ? wait(sm, &sm->si_full, ins++ & 1) : outs == 0 || wait(sm, &sm->f_stored, (outs - 1) & 1))) {
         failed = true;
         break;
       }
+      if (c == 0 && ring && !wait(sm, &sm->sf_full, fins++ & 1)) { failed = true; break; }
 #pragma unroll 1
       for (int q = 0; q < 4; ++q) {
         uint32_t x[32];
-        if (direct) {
+        if (c > 0) {
+          tmem_ld32(ts + 32 * q, x);
+          tmem_ld_wait();
+        } else if (ring) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint4 z = *reinterpret_cast<const uint4*>(from + q * kHalf + sw128_chunk(row, e));
+            x[4 * e] = z.x; x[4 * e + 1] = z.y; x[4 * e + 2] = z.z; x[4 * e + 3] = z.w;
+          }
+        } else if (direct) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const uint4 z = *reinterpret_cast<const uint4*>(sb + (q >> 1) * kHalf + sw128_chunk(row, 4 * (q & 1) + e));
@@ -779,11 +847,8 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
               x[8 * e + 2 * i + 1] = __float_as_uint(f.y);
             }
           }
-        } else if (c == 0) {
-          load_in(32 * q, x);
         } else {
-          tmem_ld32(ts + 32 * q, x);
-          tmem_ld_wait();
+          load_in(32 * q, x);
         }
 #pragma unroll
         for (int e = 0; e < 4 && !direct; ++e)
@@ -803,6 +868,7 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
       tc_fence_before();
       warp_arrive(&sm->s_ready, lane);
       if (lane == 0) mbar_arrive(&sm->gate_empty[st]);
+      if (c == 0 && ring && lane == 0) mbar_arrive(&sm->sf_empty);
     }
     if (failed) break;
     // the state that the unit leaves; the next unit may overwrite TMEM and the 16-bit copy after
@@ -811,6 +877,26 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
     if (!wait(sm, &sm->s_done, (ci - 1) & 1)) { failed = true; break; }
     if (r.out == kNone || (r.out == kPool && !p.s_out)) continue;
     tc_fence_after();
+    if (!kStates && kWide && state_out_tma(p, r) && p.sout_dtype == kF32) {
+#pragma unroll 1
+      for (int q = 0; q < 4; ++q) {
+        uint32_t x[32];
+        tmem_ld32(ts + 32 * q, x);
+        tmem_ld_wait();
+        if (q == 2 && !wait(sm, &sm->f_stored, (outs - 1) & 1)) { failed = true; break; }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          *reinterpret_cast<uint4*>(sb + (q & 1) * kHalf + sw128_chunk(row, e)) =
+              make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
+        if (q & 1) {
+          ++outs;
+          fence_proxy_async_smem();
+          warp_arrive(&sm->f_staged, lane);
+        }
+      }
+      if (failed) break;
+      continue;
+    }
     if (!kStates && state_out_tma(p, r)) {
       ++outs;
 #pragma unroll 1
@@ -888,7 +974,7 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
 // ------------------------------------------------------------ warps 16-23: V_d
 // Transposed fragments of V (pairs of tokens, one value each) times d, as kTerms 16-bit terms, 16
 // values a warp.  Where only states are made, the warps of P do the same, every other part.
-template <bool F16, int kTerms, bool kStates>
+template <bool F16, int kTerms, bool kStates, bool kWide>
 __device__ __forceinline__ void run_v(const DecayPrefillParams& p, uint8_t* base, Small* sm, uint32_t tmem, int warp, int lane) {
   constexpr int kSub = sub_tokens<kTerms>(), kSubs = C / kSub, kGroups = kStates ? 2 : 1;
   const int w = warp & 3, hf = (warp >> 2) & 1, group = kStates && warp < 4 + kPoWarps ? 1 : 0;
@@ -898,11 +984,13 @@ __device__ __forceinline__ void run_v(const DecayPrefillParams& p, uint8_t* base
   bool failed = false;
   Rec r;
   int ci = 0;
+  Ring<kStates> ring;
   for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
-    for (int c = 0; c < r.nch; ++c, ++ci) {
+    if (!kStates && state_in_ring<kWide>(p, r)) ring.pass();
+    for (int c = 0; c < r.nch; ++c, ++ci, ring.next()) {
       const int st = ci & 1, left = r.len - (kStates ? r.nch - 1 - c : c) * C;
-      const int kv = ci % kv_stages<kStates>();
-      const uint32_t ph = (ci / kv_stages<kStates>()) & 1;
+      const int kv = ring.s;
+      const uint32_t ph = ring.phase();
       if (!(wait(sm, &sm->gate_full[st], (ci >> 1) & 1) && wait(sm, &sm->v_full[kv], ph))) { failed = true; break; }
       uint8_t* k = base + kOffKv + kv * 2 * kTile;
       if (left < C) {
@@ -962,7 +1050,7 @@ __device__ __forceinline__ void run_v(const DecayPrefillParams& p, uint8_t* base
 }
 
 // ------------------------------------------------------------ the kernel
-template <bool F16, int kTerms, bool kStates>
+template <bool F16, int kTerms, bool kStates, bool kWide>
 __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __grid_constant__ DecayPrefillParams p) {
   extern __shared__ __align__(1024) uint8_t base[];
   Small* sm = reinterpret_cast<Small*>(base + kOffSmall);
@@ -993,6 +1081,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __
     init(&sm->f_stored, 1, 1);
     init(&sm->f_staged, 1, kSWarps);
     init(&sm->si_full, 1, 1);
+    init(&sm->sf_full, 1, 1);
+    init(&sm->sf_empty, 1, kSWarps);
     init(&sm->s_ready, 1, kSWarps);
     init(sm->vd_full, kVdSlots, kVWarps);
     init(sm->vd_empty, kVdSlots, 1);
@@ -1013,17 +1103,17 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __
   tc_fence_after();
   const uint32_t tmem = sm->tmem;
   if (warp < 4) {
-    if (warp == 0) run_producer<kStates>(p, base, sm, lane);
-    else if (warp == 1) run_mma<F16, kTerms, kStates>(p, base, sm, tmem, lane);
+    if (warp == 0) run_producer<kStates, kWide>(p, base, sm, lane);
+    else if (warp == 1) run_mma<F16, kTerms, kStates, kWide>(p, base, sm, tmem, lane);
     else if (warp == 2) run_gates<F16, kTerms, kStates>(p, sm, lane);
-    else if (!kStates) run_store(p, base, sm, lane);
+    else if (!kStates) run_store<kWide>(p, base, sm, lane);
   } else if (warp < 4 + kPoWarps) {
-    if (kStates) run_v<F16, kTerms, kStates>(p, base, sm, tmem, warp, lane);
+    if (kStates) run_v<F16, kTerms, kStates, kWide>(p, base, sm, tmem, warp, lane);
     else run_po<F16>(p, base, sm, tmem, warp, lane);
   } else if (warp < 4 + kPoWarps + kSWarps) {
-    run_state<F16, kStates>(p, base, sm, tmem, warp, lane);
+    run_state<F16, kStates, kWide>(p, base, sm, tmem, warp, lane);
   } else {
-    run_v<F16, kTerms, kStates>(p, base, sm, tmem, warp, lane);
+    run_v<F16, kTerms, kStates, kWide>(p, base, sm, tmem, warp, lane);
   }
   tc_fence_before();
   __syncthreads();
@@ -1049,19 +1139,19 @@ __global__ void __launch_bounds__(kJoinThreads) gdn_decay_join_kernel(float* ws,
   }
 }
 
-template <bool F16, int kTerms, bool kStates>
+template <bool F16, int kTerms, bool kStates, bool kWide>
 cudaError_t launch_pass(const DecayPrefillParams& p, int sms, cudaStream_t stream) {
   static thread_local int device = -1, generation = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   const int gen = launch_config_generation();
   if (e == cudaSuccess && (device != dev || generation != gen)) {
-    e = cudaFuncSetAttribute(gdn_decay_prefill_kernel<F16, kTerms, kStates>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    e = cudaFuncSetAttribute(gdn_decay_prefill_kernel<F16, kTerms, kStates, kWide>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e == cudaSuccess) { device = dev; generation = gen; }
   }
   if (e != cudaSuccess) return e;
   const int64_t units = (int64_t)p.N * p.H * (kStates ? p.splits - 1 : p.splits);
-  gdn_decay_prefill_kernel<F16, kTerms, kStates><<<(unsigned)(units < sms ? units : sms), kThreads, kSmem, stream>>>(p);
+  gdn_decay_prefill_kernel<F16, kTerms, kStates, kWide><<<(unsigned)(units < sms ? units : sms), kThreads, kSmem, stream>>>(p);
   return cudaGetLastError();
 }
 
@@ -1070,7 +1160,7 @@ cudaError_t launch(const DecayPrefillParams& p, cudaStream_t stream) {
   const int sms = device_sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
   if (p.splits > 1) {
-    cudaError_t e = launch_pass<F16, kTerms, true>(p, sms, stream);
+    cudaError_t e = launch_pass<F16, kTerms, true, true>(p, sms, stream);
     if (e != cudaSuccess) return e;
     if (p.splits > 2) {
       const int64_t ctas = (int64_t)p.N * p.H * (D * D / 4 / kJoinThreads);
@@ -1079,7 +1169,8 @@ cudaError_t launch(const DecayPrefillParams& p, cudaStream_t stream) {
       if (e != cudaSuccess) return e;
     }
   }
-  return launch_pass<F16, kTerms, false>(p, sms, stream);
+  const bool wide = p.splits > 1 || (p.s_in && p.sin_dtype == kF32) || (p.s_out && p.sout_dtype == kF32);
+  return wide ? launch_pass<F16, kTerms, false, true>(p, sms, stream) : launch_pass<F16, kTerms, false, false>(p, sms, stream);
 }
 
 }  // namespace
