@@ -49,6 +49,8 @@
 #include <cuda_runtime.h>
 #include <stddef.h>
 
+#include <cmath>
+
 #include "decay.cuh"
 #include "ptx.cuh"
 
@@ -1122,20 +1124,40 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __
 
 // ------------------------------------------------------------ joining segments
 // In f32, the state behind each segment: S <- decay S + what the segment added.  A thread takes
-// four values of one unit through all segments; their loads do not wait for one another.
-constexpr int kJoinThreads = 256;
-__global__ void __launch_bounds__(kJoinThreads) gdn_decay_join_kernel(float* ws, const float* decay, int blocks) {
+// four values of one unit through all segments, and loads those of the next few segments while it
+// works on the last few.
+constexpr int kJoinThreads = 256, kJoinAhead = 8;
+__global__ void __launch_bounds__(kJoinThreads) gdn_decay_join_kernel(float* __restrict__ ws, const float* __restrict__ decay, int blocks) {
   constexpr int kCtas = D * D / 4 / kJoinThreads;  // of a unit
   const int64_t unit = blockIdx.x / kCtas;
   float4* s = reinterpret_cast<float4*>(ws + unit * blocks * (D * D)) + (blockIdx.x % kCtas) * kJoinThreads + threadIdx.x;
   const float* d = decay + unit * blocks;
-  float4 x = *s;
-#pragma unroll 8
-  for (int b = 1; b < blocks; ++b) {
-    const float4 y = s[b * (D * D / 4)];
-    const float g = d[b];
-    x = make_float4(fmaf(g, x.x, y.x), fmaf(g, x.y, y.y), fmaf(g, x.z, y.z), fmaf(g, x.w, y.w));
-    s[b * (D * D / 4)] = x;
+  float4 next[kJoinAhead];
+  float g_next[kJoinAhead];
+  auto load = [&](int b0) {
+#pragma unroll
+    for (int i = 0; i < kJoinAhead; ++i) {
+      next[i] = b0 + i < blocks ? s[(b0 + i) * (D * D / 4)] : make_float4(0.f, 0.f, 0.f, 0.f);
+      g_next[i] = b0 + i < blocks ? d[b0 + i] : 0.f;
+    }
+  };
+  float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+  load(0);
+  for (int b0 = 0; b0 < blocks; b0 += kJoinAhead) {
+    float4 y[kJoinAhead];
+    float g[kJoinAhead];
+#pragma unroll
+    for (int i = 0; i < kJoinAhead; ++i) { y[i] = next[i]; g[i] = g_next[i]; }
+    load(b0 + kJoinAhead);
+#pragma unroll
+    for (int i = 0; i < kJoinAhead; ++i) {
+      if (b0 + i == 0) {
+        x = y[0];  // already what is behind the first segment
+      } else if (b0 + i < blocks) {
+        x = make_float4(fmaf(g[i], x.x, y[i].x), fmaf(g[i], x.y, y[i].y), fmaf(g[i], x.z, y[i].z), fmaf(g[i], x.w, y[i].w));
+        s[(b0 + i) * (D * D / 4)] = x;
+      }
+    }
   }
 }
 
@@ -1175,19 +1197,25 @@ cudaError_t launch(const DecayPrefillParams& p, cudaStream_t stream) {
 
 }  // namespace
 
-// Cost in chunks of a whole pass, with U units on a persistent grid of one CTA an SM.  Uncut: the
-// rounds times the chunks.  In P segments: the same for all U P segments, about half of it for the
-// U (P - 1) segments whose states are made first (two of four products, no scores), and two more
-// launches.  A cut has to save a tenth, and leaves two chunks or more to a segment.
+// Time in chunks of the main pass, with U units on a persistent grid of one CTA an SM: rounds times
+// the chunks of a unit and what a unit costs besides.  Cut into P segments, U P units go through the
+// main pass and U (P - 1) through the pass that makes states (no scores, no output, two of four
+// products), and the join walks P - 1 states.  A cut has to save a twentieth, and leaves two chunks
+// or more to a segment.  The constants are a fit to measured times of 12 shapes from 4 x 2000 to
+// 32 x 131072 (heads x tokens of a sequence), each uncut and in 2 to 152 segments; the P that it
+// picks is the fastest one measured in each (32000 tokens on 8 heads: 575 us uncut, 78 in 19
+// segments, 114 in 22; 2 x 65536 on 32 heads: 1457 uncut, 990 in 7, 1250 in 3; 16 x 4096 on 32: 316
+// uncut, 400 in 2).
 int decay_splits(int64_t units, double chunks, int sms) {
-  constexpr double kStatesCost = 0.5, kLaunches = 4.0;
-  constexpr int kMaxSplits = 32;
+  constexpr double kUnit = 2.5, kStatesChunk = 0.35, kStatesUnit = 0.75, kLaunches = 3.0, kJoin = 0.06;
   if (units <= 0 || sms <= 0) return 1;
   auto rounds = [&](int64_t n) { return double((n + sms - 1) / sms); };
-  double best = 0.9 * rounds(units) * chunks;
+  double best = 0.95 * rounds(units) * (std::ceil(chunks) + kUnit);
   int P = 1;
-  for (int c = 2; c <= kMaxSplits && chunks >= 2.0 * c; ++c) {
-    const double cost = (kStatesCost * rounds(units * (c - 1)) + rounds(units * c)) * (chunks / c) + kLaunches;
+  for (int c = 2; c <= sms && chunks >= 2.0 * c; ++c) {
+    const double each = std::ceil(chunks / c);
+    const double cost = rounds(units * c) * (each + kUnit) + rounds(units * (c - 1)) * (kStatesChunk * each + kStatesUnit) +
+                        kLaunches + kJoin * (c - 1);
     if (cost < best) { best = cost; P = c; }
   }
   return P;
