@@ -92,7 +92,7 @@ constexpr int kRecs = 3;
 
 struct Rec {       // one unit: a sequence, or a segment of one, of one head.  Only units with chunks go round
   int32_t t0, len, h, nch;  // first token, tokens, head, chunks (-1: no more units)
-  int64_t slot;
+  int32_t slot;     // in the pools (2^31 slots would be 64 TB)
   int32_t in, out;  // where the state comes from and goes to: a block of the workspace, or
 };
 constexpr int kPool = -1, kNone = -2;  // the caller's pool (zeros without one), or nowhere (zeros)
@@ -110,7 +110,7 @@ struct Small {
   uint64_t gate_full[2], gate_empty[2], cf_empty;
   uint64_t qk_done, qs_done, s_done, o_done;   // products that have completed
   uint64_t q_ready, p_ready, o_free, o_staged;  // warps 4-11
-  uint64_t o_stored, f_stored;                  // warp 3
+  uint64_t o_stored, f_half, f_stored;          // warp 3
   uint64_t f_staged, si_full;                   // warps 12-15; an incoming 16-bit state
   uint64_t sf_full, sf_empty;                   // an incoming f32 state
   uint64_t s_ready, vd_full[kVdSlots];         // warps 12-15, 16-23
@@ -205,7 +205,7 @@ __device__ __forceinline__ int unit_at(const DecayPrefillParams& p, int64_t x, R
   const int c0 = (int)((int64_t)all * seg / p.splits), nch = (int)((int64_t)all * (seg + 1) / p.splits) - c0;
   const int first = (int)bos + c0 * C, len = nch > 0 ? min((int)eos - first, nch * C) : 0;
   const int block = (n * p.H + h) * (p.splits - 1) + seg;  // of the state behind this segment
-  *r = Rec{first, len, h, nch, slot, seg == 0 ? kPool : kStates ? kNone : block - 1,
+  *r = Rec{first, len, h, nch, (int)slot, seg == 0 ? kPool : kStates ? kNone : block - 1,
            kStates ? block : seg == p.splits - 1 ? kPool : kNone};
   return 0;
 }
@@ -237,7 +237,7 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
   int f32_stage = -1;      // the stage that holds an f32 state
   const int64_t units = unit_count<kStates>(p);
   int empties = 0;
-  int q_loads = 0, s_loads = 0, sf_loads = 0, outs = 0;  // outs: parts of states by TMA of the units so far
+  int q_loads = 0, s_loads = 0, sf_loads = 0, outs = 0;  // outs: states that the units so far leave by TMA
   auto stage_free = [&] {
     const int s = ring.s;
     if (s == f32_stage) {
@@ -278,14 +278,14 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
         mbar_arrive_expect_tx(&sm->sf_full, 2 * kTile);
         for (int q = 0; q < 4; ++q)
           if (r.in >= 0) tma_load_4d(dst + q * kHalf, &p.tm_ws, &sm->sf_full, 32 * q, 0, 0, r.in);
-          else tma_load_4d(dst + q * kHalf, &p.tm_sin, &sm->sf_full, 32 * q, 0, r.h, (int)r.slot);
+          else tma_load_4d(dst + q * kHalf, &p.tm_sin, &sm->sf_full, 32 * q, 0, r.h, r.slot);
       }
       ++sf_loads;
       f32_stage = ring.s;
       ring.pass();
     } else if (p.s_in && r.in == kPool && lane == 0) {
       const int es = p.sin_dtype == kF32 ? 4 : 2;
-      bulk_prefetch_l2(reinterpret_cast<const char*>(p.s_in) + (r.slot * p.sin_slot + (int64_t)h * p.sin_head) * es, D * D * es);
+      bulk_prefetch_l2(reinterpret_cast<const char*>(p.s_in) + ((int64_t)r.slot * p.sin_slot + (int64_t)h * p.sin_head) * es, D * D * es);
     }
     const int hq = h / (p.H / p.H_qk), hv = h / (p.H / p.H_v);
     for (int c = 0; c < nch; ++c, ++ci) {
@@ -317,13 +317,13 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
         if (!ok) break;
         if (lane == 0) {
           mbar_arrive_expect_tx(&sm->si_full, kTile);
-          tma_load_4d(base + kOffS, &p.tm_sin, &sm->si_full, 0, 0, h, (int)r.slot);
-          tma_load_4d(base + kOffS + kHalf, &p.tm_sin, &sm->si_full, 64, 0, h, (int)r.slot);
+          tma_load_4d(base + kOffS, &p.tm_sin, &sm->si_full, 0, 0, h, r.slot);
+          tma_load_4d(base + kOffS + kHalf, &p.tm_sin, &sm->si_full, 64, 0, h, r.slot);
         }
         ++s_loads;
       }
     }
-    if (!kStates && state_out_tma(p, r)) outs += state_out_parts<kWide>(p);
+    if (!kStates && state_out_tma(p, r)) ++outs;
   }
   if (ok && lane == 0) sm->empties = empties;  // ahead of the last record
   if (ok) ok = publish(Rec{0, 0, 0, -1, 0, 0, 0});
@@ -533,7 +533,7 @@ template <bool kWide>
 __device__ __forceinline__ void run_store(const DecayPrefillParams& p, uint8_t* base, Small* sm, int lane) {
   bool failed = false;
   Rec r;
-  int ci = 0, outs = 0;  // tiles and states that have gone out
+  int ci = 0, outs = 0;  // tiles and parts of states that have gone out
   for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
     for (int c = 0; c < r.nch; ++c, ++ci) {
       const int t0 = r.t0 + c * C, left = r.len - c * C;
@@ -542,12 +542,12 @@ __device__ __forceinline__ void run_store(const DecayPrefillParams& p, uint8_t* 
         for (int x = 0; x < parts && !failed; ++x) {
           if (!wait(sm, &sm->f_staged, outs++ & 1)) { failed = true; break; }
           if (lane == 0) {
-            tma_store_4d(&p.tm_sout, base + kOffS, 64 * x, 0, r.h, (int)r.slot);
-            tma_store_4d(&p.tm_sout, base + kOffS + kHalf, 64 * x + cols, 0, r.h, (int)r.slot);
+            tma_store_4d(&p.tm_sout, base + kOffS, 64 * x, 0, r.h, r.slot);
+            tma_store_4d(&p.tm_sout, base + kOffS + kHalf, 64 * x + cols, 0, r.h, r.slot);
             bulk_commit();
             bulk_wait_read_all();
           }
-          warp_arrive(&sm->f_stored, lane);
+          warp_arrive(x + 1 < parts ? &sm->f_half : &sm->f_stored, lane);
         }
         if (failed) break;
       }
@@ -792,13 +792,13 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
   uint8_t* sb = base + kOffS;
   bool failed = false;
   Rec r{};
-  int ci = 0, ins = 0, fins = 0, outs = 0;  // chunks; 16-bit and f32 states by TMA that came, parts that went
+  int ci = 0, ins = 0, fins = 0, outs = 0;  // chunks; 16-bit and f32 states by TMA that came, states that went
   int entries = 0;                          // of the stages of K and V
   auto load_in = [&](int c0, uint32_t (&x)[32]) {
     if (kWide && r.in >= 0) {
       load_state32<kWide>(p.ws, kF32, (int64_t)r.in * (D * D) + row * D + c0, x);
     } else if (r.in == kPool && p.s_in) {
-      load_state32<kWide>(p.s_in, p.sin_dtype, r.slot * p.sin_slot + (int64_t)r.h * p.sin_head + row * D + c0, x);
+      load_state32<kWide>(p.s_in, p.sin_dtype, (int64_t)r.slot * p.sin_slot + (int64_t)r.h * p.sin_head + row * D + c0, x);
     } else {
 #pragma unroll
       for (int e = 0; e < 32; ++e) x[e] = 0u;
@@ -807,7 +807,7 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
   auto store_out = [&](int c0, const uint32_t (&x)[32]) {
     const int64_t at = row * D + c0;
     if (kWide && r.out >= 0) store_state32<kWide>(p.ws, kF32, (int64_t)r.out * (D * D) + at, x);
-    else store_state32<kWide>(p.s_out, p.sout_dtype, r.slot * p.sout_slot + (int64_t)r.h * p.sout_head + at, x);
+    else store_state32<kWide>(p.s_out, p.sout_dtype, (int64_t)r.slot * p.sout_slot + (int64_t)r.h * p.sout_head + at, x);
   };
   for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
     const bool ring = !kStates && state_in_ring<kWide>(p, r);
@@ -885,18 +885,18 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
         uint32_t x[32];
         tmem_ld32(ts + 32 * q, x);
         tmem_ld_wait();
-        if (q == 2 && !wait(sm, &sm->f_stored, (outs - 1) & 1)) { failed = true; break; }
+        if (q == 2 && !wait(sm, &sm->f_half, outs & 1)) { failed = true; break; }
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           *reinterpret_cast<uint4*>(sb + (q & 1) * kHalf + sw128_chunk(row, e)) =
               make_uint4(x[4 * e], x[4 * e + 1], x[4 * e + 2], x[4 * e + 3]);
         if (q & 1) {
-          ++outs;
           fence_proxy_async_smem();
           warp_arrive(&sm->f_staged, lane);
         }
       }
       if (failed) break;
+      ++outs;
       continue;
     }
     if (!kStates && state_out_tma(p, r)) {
@@ -1080,6 +1080,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __
     init(&sm->o_staged, 1, kPoWarps);
     init(&sm->q_ready, 1, kPoWarps);
     init(&sm->o_stored, 1, 1);
+    init(&sm->f_half, 1, 1);
     init(&sm->f_stored, 1, 1);
     init(&sm->f_staged, 1, kSWarps);
     init(&sm->si_full, 1, 1);

@@ -354,6 +354,42 @@ def test_long_runs_of_empty_sequences(force_split, splits):
     assert torch.equal(st[empty], s0[empty])
 
 
+@pytest.mark.parametrize("dtype,into,state", [(BF, F32, F32), (BF, BF, BF), (BF, BF, F32), (HF, F32, HF), (HF, None, BF)], ids=str)
+@pytest.mark.parametrize("splits", [1, 2])
+def test_more_units_than_sms(force_split, splits, dtype, into, state):
+    """More (sequence, head) units than SMs, of very different lengths, some of them empty, states of every pair of types."""
+    force_split(splits)
+    lengths = [0, 900, 3, 640, 0, 0, 129, 512] * 3 + [2300, 0]
+    q, k, v, g, cu = R.make(lengths, 4, 8, dtype, "token", 51)
+    N, slots = len(lengths), len(lengths) + 4
+    idx = torch.randperm(slots, generator=torch.Generator().manual_seed(51))[:N].cuda()
+    s0 = None if into is None else R.states(slots, 8, into, 51)
+    final = torch.full((slots, 8, 128, 128), 7.0, dtype=state, device="cuda")
+    out, _ = gdn.decay_linear_attention(q, k, v, g, initial_state=s0, output_final_state=True, output_state=final,
+                                        cu_seqlens=cu, state_indices=idx)
+    assert gdn.device_status() == 0
+    o_ref, s_ref = R.recurrence(q, k, v, g, SCALE, None if s0 is None else s0[idx], lengths)
+    R.check(out, o_ref, final[idx], s_ref, lengths)
+    rest = sorted(set(range(slots)) - set(idx.tolist()))
+    assert bool((final[rest] == 7.0).all())
+
+
+def test_more_units_than_sms_skip_bad_sequences():
+    lengths = [300, 700] * 20
+    q, k, v, g, cu = R.make(lengths, 2, 8, seed=52)
+    s0 = R.states(40, 8, F32, 52)
+    idx = torch.arange(40, device="cuda")
+    idx[7], idx[33] = 40, -1
+    out, final = torch.zeros(20000, 8, 128, dtype=BF, device="cuda"), torch.zeros_like(s0)
+    gdn.decay_linear_attention(q, k, v, g, initial_state=s0, output_final_state=True, output_state=final, output=out,
+                               cu_seqlens=cu, state_indices=idx)
+    assert gdn.device_status() == 2
+    o_ref, s_ref = R.recurrence(q, k, v, g, SCALE, s0, lengths)
+    R.check(out, o_ref, final, s_ref, lengths, which=[n for n in range(40) if n not in (7, 33)])
+    for n in (7, 33):
+        assert not bool(out[cu[n]:cu[n + 1]].any()) and not bool(final[n].any())
+
+
 def test_example_layer():
     """The example's prompts and steps agree with one long prompt to what their 16-bit states and
     outputs allow: each step rounds the state to bf16 (1.7e-3), eight of them and the roundings on
