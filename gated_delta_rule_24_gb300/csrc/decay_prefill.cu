@@ -91,7 +91,7 @@ constexpr uint32_t kOffSmall = kOffO + kTile;
 constexpr int kRecs = 3;
 
 struct Rec {       // one unit: a sequence, or a segment of one, of one head.  Only units with chunks go round
-  int32_t t0, len, h, nch;  // first token, tokens, head, chunks (-1: no more units)
+  int32_t t0, len, h, nch;  // first token, tokens, head, chunks (-1: no more units; h counts those without chunks)
   int32_t slot;     // in the pools (2^31 slots would be 64 TB)
   int32_t in, out;  // where the state comes from and goes to: a block of the workspace, or
 };
@@ -103,10 +103,10 @@ struct Small {
   float cf[C];     // 2^(G_e - G_j), e the last token of j's block of 16
   int32_t mild[2]; // no block of 16 tokens decays by more than 2^-100
   float gamma[2];  // 2^(G_last)
-  int32_t empties; // units without chunks
+  alignas(16) uint32_t claim[4];  // the answer to a claim of another unit
   Rec rec[kRecs];
   uint64_t q_full, q_empty, k_full[3], v_full[3], kv_empty[3];
-  uint64_t rec_full[kRecs], rec_empty[kRecs];
+  uint64_t rec_full[kRecs], rec_empty[kRecs], claim_full;
   uint64_t gate_full[2], gate_empty[2], cf_empty;
   uint64_t qk_done, qs_done, s_done, o_done;   // products that have completed
   uint64_t q_ready, p_ready, o_free, o_staged;  // warps 4-11
@@ -227,6 +227,49 @@ __device__ __forceinline__ bool state_out_tma(const DecayPrefillParams& p, const
 template <bool kWide>
 __device__ __forceinline__ int state_out_parts(const DecayPrefillParams& p) { return kWide && p.sout_dtype == kF32 ? 2 : 1; }
 
+// The state of a unit without chunks from where it comes to where it goes, by one warp.
+template <bool kStates>
+__device__ __forceinline__ void pass_on(const DecayPrefillParams& p, int h, int64_t slot, int in, int out, int lane) {
+  if (kStates && lane == 0) p.ws_decay[out] = 1.f;
+  if (out == kNone || (out == kPool && !p.s_out)) return;
+  const bool pool = in == kPool && p.s_in;
+  const int from_dtype = pool ? p.sin_dtype : kF32, to_dtype = out >= 0 ? kF32 : p.sout_dtype;
+  const char* from = pool ? reinterpret_cast<const char*>(p.s_in) + (slot * p.sin_slot + (int64_t)h * p.sin_head) * (from_dtype == kF32 ? 4 : 2)
+                          : in >= 0 ? reinterpret_cast<const char*>(p.ws + (int64_t)in * (D * D)) : nullptr;
+  char* to = out >= 0 ? reinterpret_cast<char*>(p.ws + (int64_t)out * (D * D))
+                        : reinterpret_cast<char*>(p.s_out) + (slot * p.sout_slot + (int64_t)h * p.sout_head) * (to_dtype == kF32 ? 4 : 2);
+  constexpr int kBatch = 4;
+#pragma unroll 1
+  for (int e0 = 4 * lane; e0 < D * D; e0 += 128 * kBatch) {
+    float2 x[kBatch][2];
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int e = e0 + 128 * i;
+      x[i][0] = x[i][1] = make_float2(0.f, 0.f);
+      if (!from) continue;
+      if (from_dtype == kF32) {
+        const float4 f = reinterpret_cast<const float4*>(from)[e / 4];
+        x[i][0] = make_float2(f.x, f.y);
+        x[i][1] = make_float2(f.z, f.w);
+      } else {
+        const uint2 f = reinterpret_cast<const uint2*>(from)[e / 4];
+        x[i][0] = from_dtype == kF16 ? unpack16<true>(f.x) : unpack16<false>(f.x);
+        x[i][1] = from_dtype == kF16 ? unpack16<true>(f.y) : unpack16<false>(f.y);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int e = e0 + 128 * i;
+      if (to_dtype == kF32)
+        reinterpret_cast<float4*>(to)[e / 4] = make_float4(x[i][0].x, x[i][0].y, x[i][1].x, x[i][1].y);
+      else if (to_dtype == kF16)
+        reinterpret_cast<uint2*>(to)[e / 4] = make_uint2(pack16x2<true>(x[i][0]), pack16x2<true>(x[i][1]));
+      else
+        reinterpret_cast<uint2*>(to)[e / 4] = make_uint2(pack16x2<false>(x[i][0]), pack16x2<false>(x[i][1]));
+    }
+  }
+}
+
 // ------------------------------------------------------------ warp 0: loads
 template <bool kStates, bool kWide>
 __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_t* base, Small* sm, int lane) {
@@ -256,15 +299,40 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
     ++u;
     return true;
   };
-  for (int64_t x = blockIdx.x; x < units && ok; x += gridDim.x) {
+  // The first unit is that of the CTA's place in the grid.  Then, with a grid of one CTA an SM, every
+  // gridDim.x-th one; or, with a CTA for each unit, those of CTAs that have not been launched, taken over
+  // one at a time when the last chunk of the one before is loaded.
+  int64_t x = blockIdx.x;
+  int claims = 0;
+  auto claim = [&] {
+    if (!p.claim_units) return;
+    __syncwarp();
+    if (lane == 0) {
+      fence_proxy_async_smem();
+      mbar_arrive_expect_tx(&sm->claim_full, 16);
+      clc_ask(sm->claim, &sm->claim_full);
+    }
+    ++claims;
+  };
+  auto another = [&] {
+    if (!p.claim_units) return (x += gridDim.x) < units;
+    uint32_t to = 0;
+    ok = wait(sm, &sm->claim_full, (claims - 1) & 1);
+    const bool any = ok && clc_answer(sm->claim, &to);
+    x = to;
+    return any;
+  };
+  for (bool more = true; more; more = ok && another()) {
     Rec r;
     const int err = unit_at<kStates>(p, x, &r);
+    if (err || r.nch == 0) claim();
     if (err) {
       if (lane == 0) atomicOr(p.dev_err, err);
       continue;
     }
-    if (r.nch == 0) {  // nothing but a state to pass on: warps 12-15 see to these at the end
-      ++empties;
+    if (r.nch == 0) {  // nothing but a state to pass on: warps 12-15 see to these at the end, if they can find them
+      if (p.claim_units) pass_on<kStates>(p, r.h, r.slot, r.in, r.out, lane);
+      else ++empties;
       continue;
     }
     ok = publish(r);
@@ -289,6 +357,7 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
     }
     const int hq = h / (p.H / p.H_qk), hv = h / (p.H / p.H_v);
     for (int c = 0; c < nch; ++c, ++ci) {
+      if (c + 1 == nch) claim();
       const int s = ring.s, t0 = first + (kStates ? nch - 1 - c : c) * C;
       auto load = [&](uint8_t* dst, const CUtensorMap* tm, uint64_t* bar, int head) {
         mbar_arrive_expect_tx(bar, kTile);
@@ -325,8 +394,7 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
     }
     if (!kStates && state_out_tma(p, r)) ++outs;
   }
-  if (ok && lane == 0) sm->empties = empties;  // ahead of the last record
-  if (ok) ok = publish(Rec{0, 0, 0, -1, 0, 0, 0});
+  if (ok) ok = publish(Rec{0, 0, empties, -1, 0, 0, 0});
   if (!ok && lane == 0) give_up(p, sm);
   // loads that no role waits for any more land before the CTA's shared memory goes away
   for (int s = 0; s < kv_stages<kStates>(); ++s) {
@@ -334,6 +402,7 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
     drain(&sm->k_full[s], (ring.phases >> s & 1) ^ 1);
     drain(&sm->v_full[s], (ring.phases >> s & 1) ^ 1);
   }
+  if (claims) drain(&sm->claim_full, (claims - 1) & 1);
   if (q_loads) drain(&sm->q_full, (q_loads - 1) & 1);
   if (s_loads) drain(&sm->si_full, (s_loads - 1) & 1);
   if (sf_loads) drain(&sm->sf_full, (sf_loads - 1) & 1);
@@ -950,7 +1019,7 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
     return;
   }
   // units without chunks pass on what they got: 32 units looked at together, a lane each
-  const int64_t units = sm->empties ? unit_count<kStates>(p) : 0;
+  const int64_t units = r.h > 0 ? unit_count<kStates>(p) : 0;
   for (int64_t x0 = blockIdx.x; x0 < units; x0 += 32 * (int64_t)gridDim.x) {
     const int64_t x = x0 + (int64_t)lane * gridDim.x;
     Rec mine{};
@@ -1070,6 +1139,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __
     init(sm->rec_empty, kRecs, (kStates ? 2 : 3) + kPoWarps + kSWarps + kVWarps);
     init(sm->gate_full, 2, 1);
     init(sm->gate_empty, 2, kPoWarps + (kStates ? 0 : kSWarps) + kVWarps);
+    init(&sm->claim_full, 1, 1);
     init(&sm->cf_empty, 1, kPoWarps);
     init(&sm->qk_done, 1, 1);
     init(&sm->qs_done, 1, 1);
@@ -1162,6 +1232,15 @@ __global__ void __launch_bounds__(kJoinThreads) gdn_decay_join_kernel(float* __r
   }
 }
 
+// Whether CTAs take units over instead of walking them in equal steps.  That evens out sequences of
+// different lengths, but each claim delays what follows by about a microsecond: it pays where an SM
+// has few units, or long ones.  Us in equal steps and by claims, lengths drawn evenly up to twice the mean: 93
+// sequences of 1198 tokens on 2 heads 113 / 78, 64 x 2000 on 16 348 / 313, 300 x 1000 on 16 870 / 806, 400 x 600
+// on 8 347 / 348, 200 x 136 on 16 137 / 145, 1000 x 300 on 16 948 / 1042.
+bool claims_pay(int64_t units, double chunks, int sms) {
+  return units > sms && chunks >= (units <= 8 * (int64_t)sms ? 2.0 : 6.0);
+}
+
 template <bool F16, int kTerms, bool kStates, bool kWide>
 cudaError_t launch_pass(const DecayPrefillParams& p, int sms, cudaStream_t stream) {
   static thread_local int device = -1, generation = -1;
@@ -1174,7 +1253,10 @@ cudaError_t launch_pass(const DecayPrefillParams& p, int sms, cudaStream_t strea
   }
   if (e != cudaSuccess) return e;
   const int64_t units = (int64_t)p.N * p.H * (kStates ? p.splits - 1 : p.splits);
-  gdn_decay_prefill_kernel<F16, kTerms, kStates, kWide><<<(unsigned)(units < sms ? units : sms), kThreads, kSmem, stream>>>(p);
+  DecayPrefillParams q = p;
+  q.claim_units = claims_pay(units, double(p.T) / double(p.N) / p.splits / C, sms);
+  const int64_t grid = q.claim_units || units < sms ? units : sms;
+  gdn_decay_prefill_kernel<F16, kTerms, kStates, kWide><<<(unsigned)grid, kThreads, kSmem, stream>>>(q);
   return cudaGetLastError();
 }
 

@@ -121,6 +121,27 @@ GDN_DEV void tma_load_4d(void* dst, const void* tmap, uint64_t* bar, int c0, int
       "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
       : "memory");
 }
+// Takes over a CTA of this grid that has not been launched yet, if there is one: 16 bytes of response
+// to shared memory.  Not to be asked again after a "none".
+GDN_DEV void clc_ask(void* response, uint64_t* bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+                   smem_u32(response)),
+               "r"(smem_u32(bar))
+               : "memory");
+}
+// The response: whether there was one, and its blockIdx.x.
+GDN_DEV bool clc_answer(const void* response, uint32_t* ctaid) {
+  uint32_t ok, x;
+  asm volatile(
+      "{\n.reg .pred p;\n.reg .b128 r;\nld.shared.b128 r, [%2];\n"
+      "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\nselp.u32 %0, 1, 0, p;\nmov.u32 %1, 0;\n"
+      "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, r;\n}\n"
+      : "=r"(ok), "=r"(x)
+      : "r"(smem_u32(response))
+      : "memory");
+  *ctaid = x;
+  return ok != 0;
+}
 // 4-D tiled store from shared memory (bulk-group completion).
 GDN_DEV void tma_store_4d(const void* tmap, const void* src, int c0, int c1, int c2, int c3) {
   asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(tmap),
