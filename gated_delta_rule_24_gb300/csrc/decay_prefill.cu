@@ -9,33 +9,51 @@
 //   O    = scale diag(2^G) Q S^T + P V
 //   S   <- 2^(G_last) S + V_d^T K,           V_d = diag(2^(G_last - G)) V
 //
-// Four products of 128 x 128 x 128 on tcgen05 (the last one two or three times, see
-// below) against 128 KB of q, k, v and o: the bytes bound it once the products of one chunk
-// run without a pause, and that is what the layout is for.
+// Four products of 128 x 128 x 128 on tcgen05 (the last one two or three times, see below) against
+// 128 KB of q, k, v and o.  At 6.8 TB/s an SM of 152 gets its 128 KB in 2.9 us, and the products
+// take 1.6 us (two terms; 592 cycles a product with its A operand in TMEM, 853 with A in shared memory,
+// so that all four have A there): the bytes bound it where every SM is busy and heads share nothing,
+// and otherwise the chain of roles that a chunk goes through does.
 //
-// One persistent CTA per SM walks (sequence, head) units chunk by chunk.  Roles (24 warps):
-//   warp 0      TMA loads of Q, K, V (two stages) and the unit records;
-//   warp 1      issues every product: Q K^T, Q S^T, V_d^T K, P V of a chunk in this order,
-//               so that P is built while Q S^T and V_d^T K run, and the state is read out
-//               and V_d of the next chunk built while P V and the next Q K^T run;
+// A CTA an SM walks (sequence, head) units chunk by chunk.  Roles (24 warps; 80 registers a thread):
+//   warp 0      unit records, TMA loads of Q, K, V (K and V in two stages) and of states;
+//   warp 1      issues the products of a chunk: Q K^T, Q S^T, V_d^T K, P V.  P is built while Q S^T
+//               and V_d^T K run; the state is read and V_d of the next chunk made while P V and the next
+//               Q K^T run;
 //   warp 2      the gates: prefix and suffix sums of log2 g, one chunk ahead;
-//   warp 3      stores of the output tile;
-//   warps 4-11  two threads a token: P (tcgen05.ld, decay, mask, back to TMEM as the A operand
-//               of P V), the 2^G_i of Q S^T in place, and the output tile;
-//   warps 12-15 one thread a value row: the state in TMEM, times the chunk's decay, and its
-//               16-bit copy in shared memory for Q S^T;
-//   warps 16-23 V_d, from V in shared memory to TMEM.
-// Hand-offs are mbarriers, every wait is bounded and ends early when any role gave up.
+//   warp 3      stores of output tiles (TMA, or rows where a sequence ends inside) and of states;
+//   warps 4-11  two threads a token: Q from shared memory to TMEM, P (scores times decay, masked, back to
+//               TMEM), Q S^T times scale 2^G_i in place, and the output tile;
+//   warps 12-15 one thread a value row: before a chunk's V_d^T K adds to it, the state in TMEM goes times
+//               the chunk's decay, and as a 16-bit copy to shared memory for Q S^T;
+//   warps 16-23 V_d: transposed fragments of V times d, to TMEM.
+// Hand-offs are mbarriers, every wait is bounded and ends early when any role gave up.  With all
+// roles resident the instruction cache is short: loops are rolled up where that measured faster
+// (P in rolled blocks of 16 columns: 16 x 4096 tokens on 32 heads 341 -> 322 us), and launches that
+// meet no f32 state are compiled without the code for them (1024 short prompts 680 -> 640 us).
 //
-// The state never waits in TMEM: V_d^T K goes to a buffer of its own, and S <- gamma S + it
-// happens in registers, so the chain from chunk to chunk is a read-out, 64 FMAs a thread
-// and a 16-bit copy, next to products that do not depend on it.
+// TMEM is full: the scores (then P), the output, the state (128 columns each), Q and V_d (64
+// each).  Further parts of V_d go where Q was, once Q S^T has read it, and between the blocks of P.
 //
-// Precision: P and the copy of S are rounded to the 16-bit type of q, k, v (as the
-// output is); everything else that is summed is f32.  V_d would put its rounding straight
-// into the state, so it enters as the sum of 16-bit terms, each the rounding of what is
-// left: two (16 bits bf16, 22 bits f16), or three for bf16 inputs unless the state leaves
-// the call in 16 bits; an f32 state then is as exact as f32 sums are.
+// Too few units for the SMs: sequences are cut into segments (decay_splits).  One launch makes the
+// states that the segments add (K and V alone, sums in TMEM), the join chains them in f32, and the main
+// launch runs all segments from those.
+//
+// Measured (bf16 unless stated; time of the launches, share of 6.8 TB/s in the bytes that have to move):
+//   12800 tokens, 152 heads, none shared:  294 us, 6.6 TB/s (98 %, at the power limit)
+//   16 x 4096, 16 q/k and 32 v heads, bf16 states: 316 us (77 %): 512 units are 3.4 rounds of 152
+//   2 x 65536, 16 and 32 heads, f32 states: 981 us (49 %); 7 segments, K and V read twice, three terms
+//   32000 tokens, 8 heads, f16: 80 us (48 %); 31 us states, 7 join, 41 outputs
+//   1024 prompts of 136 on average, 8 and 16 heads, bf16 states: 650 us (64 %); 1.6 chunks a unit
+//   one chunk of a unit alone: 2.3 us with two terms, 2.8 with three
+// Tensor pipe 54 % busy, issue slots 53 %, 60 % of DRAM (8 x 4096, 16 and 32 heads): a chunk takes
+// 4300 cycles at 2960 of products, the rest is hand-offs of 300 to 450 cycles between roles.
+//
+// Precision: P and the copy of S are rounded to the 16-bit type of q, k, v (as the output is);
+// everything else that is summed is f32.  V_d would put its rounding straight into the state, so
+// it enters as the sum of 16-bit terms, each the rounding of what is left: two (16 bits bf16, 22
+// bits f16), or three for bf16 inputs whose state stays in f32, which then is as exact as f32 sums
+// are.  The third term costs 0.5 us a chunk where SMs are not kept busy by bytes.
 //
 // 2^(G_i - G_j) is the product 2^(G_i - G_e) 2^(G_e - G_j) with e the last token of j's block
 // of 16: a row factor for each block and a column factor.  Both are at most 1 where the block
@@ -1286,7 +1304,7 @@ cudaError_t launch(const DecayPrefillParams& p, cudaStream_t stream) {
 // products), and the join walks P - 1 states.  A cut has to save a twentieth, and leaves two chunks
 // or more to a segment.  The constants are a fit to measured times of 12 shapes from 4 x 2000 to
 // 32 x 131072 (heads x tokens of a sequence), each uncut and in 2 to 152 segments; the P that it
-// picks is the fastest one measured in each (32000 tokens on 8 heads: 575 us uncut, 78 in 19
+// picks is the fastest one measured in each (32000 tokens on 8 heads: 575 us uncut, 78 in 18
 // segments, 114 in 22; 2 x 65536 on 32 heads: 1457 uncut, 990 in 7, 1250 in 3; 16 x 4096 on 32: 316
 // uncut, 400 in 2).
 int decay_splits(int64_t units, double chunks, int sms) {
