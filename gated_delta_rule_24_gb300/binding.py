@@ -1,4 +1,4 @@
-"""Thin ctypes binding of the C ABI in ``include/gdn.h``.
+"""Thin binding of the C ABI in ``include/gdn.h``, by ctypes and (three operators) a small extension.
 
 Only argument marshalling happens here: torch tensors are described to the
 library (pointer, dtype, shape, strides) and every step of the computation runs
@@ -9,14 +9,14 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
-import struct
-import threading
 from typing import Optional
 
 import torch
 
-from .build import LIB as _LIB_PATH
+from .build import LIB as _LIB_PATH, PYCALL as _PYCALL_PATH
 
 GDN_OK = 0
 STATUS_NAMES = {0: "GDN_OK", 1: "GDN_ERR_INVALID_ARGUMENT", 2: "GDN_ERR_UNSUPPORTED",
@@ -76,16 +76,9 @@ def load_library():
         lib.gdn_split_workspace_bytes.restype = ctypes.c_size_t
         lib.gdn_decode_step.argtypes = [P, P, P, P, P, ctypes.c_float, P, P, ctypes.c_int, P, ctypes.c_void_p]
         lib.gdn_decode_step.restype = ctypes.c_int
-        # descriptors by address (see _Descriptors)
-        A, F, I = ctypes.c_void_p, ctypes.c_float, ctypes.c_int
-        lib.gdn_qk_norm_rope.argtypes = [A, A, A, A, F, F, A, A, I, A, A, A]
-        lib.gdn_qk_norm_rope.restype = ctypes.c_int
-        lib.gdn_decay_prefill.argtypes = [A, A, A, A, F, A, A, A, A, I, A, A]
-        lib.gdn_decay_prefill.restype = ctypes.c_int
-        lib.gdn_decay_workspace_bytes.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, I]
+        lib.gdn_decay_workspace_bytes.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
+                                                  ctypes.c_int]
         lib.gdn_decay_workspace_bytes.restype = ctypes.c_size_t
-        lib.gdn_decay_step.argtypes = [A, A, A, A, F, A, A, A, A]
-        lib.gdn_decay_step.restype = ctypes.c_int
         lib.gdn_get_device_status.argtypes = [ctypes.c_void_p, ctypes.POINTER(ctypes.c_int32)]
         lib.gdn_get_device_status.restype = ctypes.c_int
         lib.gdn_last_error.argtypes = []
@@ -99,6 +92,7 @@ def load_library():
         lib.gdn_testing_split_plan.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int,
                                                ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64]
         lib.gdn_testing_split_plan.restype = ctypes.c_int
+        _calls.load(lib)
         _lib = lib
     return _lib
 
@@ -121,39 +115,29 @@ def describe(t: Optional[torch.Tensor]):
     return d
 
 
-class _Descriptors(threading.local):
-    """Room for one call's gdn_tensor_t descriptors, kept for each thread: ``fill`` writes
-    them and returns their addresses (None for an absent tensor).  The operators whose
-    smallest calls take a few microseconds on the GPU go this way; it costs about 1 us a
-    tensor where ``describe`` costs 5."""
+class _PyCall:
+    """The extension ``csrc/pycall.c``, for the operators whose smallest calls take a few
+    microseconds on the GPU: ``qk_norm_rope``, ``decay_prefill`` and ``decay_step`` with the
+    arguments of the C functions, tensors described on the way, and ``fill``, the addresses of
+    descriptors alone.  Loaded with the library, at the first use."""
 
-    SIZE = ctypes.sizeof(GdnTensor)
-    PACK = [struct.Struct("@qii%dq" % n + "%dx" % (8 * (4 - n)) + "%dq" % n + "%dx" % (8 * (4 - n))).pack_into for n in range(5)]
+    def load(self, lib):
+        loader = importlib.machinery.ExtensionFileLoader("gdn_pycall", _PYCALL_PATH)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("gdn_pycall", _PYCALL_PATH, loader=loader))
+        loader.exec_module(module)
+        module.bind(_DTYPES, *(ctypes.cast(getattr(lib, "gdn_" + name), ctypes.c_void_p).value
+                               for name in ("qk_norm_rope", "decay_prefill", "decay_step")))
+        for name in ("qk_norm_rope", "decay_prefill", "decay_step", "fill"):
+            setattr(self, name, getattr(module, name))
 
-    def __init__(self):
-        self.room = ctypes.create_string_buffer(12 * self.SIZE)
-        self.base = ctypes.addressof(self.room)
-
-    def fill(self, *tensors):
-        room, base, size, pack, where, at = self.room, self.base, self.SIZE, self.PACK, [], 0
-        for t in tensors:
-            if t is None:
-                where.append(None)
-                continue
-            shape = t.shape
-            n = len(shape)
-            if n > 4:
-                raise ValueError("at most 4 dims")
-            dtype = _DTYPES.get(t.dtype)
-            if dtype is None:
-                raise TypeError(f"unsupported dtype {t.dtype}")
-            pack[n](room, at, t.data_ptr(), dtype, n, *shape, *t.stride())
-            where.append(base + at)
-            at += size
-        return where
+    def __getattr__(self, name):
+        if name not in ("qk_norm_rope", "decay_prefill", "decay_step", "fill"):
+            raise AttributeError(name)
+        load_library()
+        return self.__dict__[name]
 
 
-_descriptors = _Descriptors()
+_calls = _descriptors = _PyCall()
 
 
 def _ref(d):
@@ -253,9 +237,8 @@ def gdn_decode_step(q, k, v, g, beta, scale: float, state, state_indices, use_qk
 def gdn_qk_norm_rope(q, k, q_weight, k_weight, weight_offset: float, eps: float, cos_sin, positions,
                      interleaved: bool, q_out, k_out, stream=None) -> None:
     """Norm and rotation of query and key heads; same names and order as the C entry point."""
-    dq, dk, dqw, dkw, dcs, dp, dqo, dko = _descriptors.fill(q, k, q_weight, k_weight, cos_sin, positions, q_out, k_out)
-    status = (_lib or load_library()).gdn_qk_norm_rope(dq, dk, dqw, dkw, weight_offset, eps, dcs, dp, 1 if interleaved else 0,
-                                                       dqo, dko, _stream_handle(stream))
+    status = _calls.qk_norm_rope(q, k, q_weight, k_weight, weight_offset, eps, cos_sin, positions, interleaved, q_out, k_out,
+                                 _stream_handle(stream))
     if status:
         _check(status)
 
@@ -264,10 +247,8 @@ def gdn_decay_prefill(q, k, v, g, scale: float, initial_state, state_indices, ou
                       batch_invariant: bool, output, stream=None) -> None:
     """Linear attention with a decay over packed sequences; same names and order as the C
     entry point."""
-    dq, dk, dv, dg, ds, di, df, dc, do = _descriptors.fill(q, k, v, g, initial_state, state_indices, output_state,
-                                                           cu_seqlens, output)
-    status = (_lib or load_library()).gdn_decay_prefill(dq, dk, dv, dg, scale, ds, di, df, dc, 1 if batch_invariant else 0, do,
-                                                        _stream_handle(stream))
+    status = _calls.decay_prefill(q, k, v, g, scale, initial_state, state_indices, output_state, cu_seqlens, batch_invariant,
+                                  output, _stream_handle(stream))
     if status:
         _check(status)
 
@@ -283,8 +264,7 @@ def gdn_decay_workspace_bytes(num_seqs: int, num_heads: int, total_tokens: int, 
 def gdn_decay_step(q, k, v, g, scale: float, state, state_indices, output, stream=None) -> None:
     """One token per batch row through the same recurrence, ``state`` in place; same names
     and order as the C entry point."""
-    dq, dk, dv, dg, ds, di, do = _descriptors.fill(q, k, v, g, state, state_indices, output)
-    status = (_lib or load_library()).gdn_decay_step(dq, dk, dv, dg, scale, ds, di, do, _stream_handle(stream))
+    status = _calls.decay_step(q, k, v, g, scale, state, state_indices, output, _stream_handle(stream))
     if status:
         _check(status)
 

@@ -1,7 +1,8 @@
-"""Build the sm_103a C-ABI library ``_build/libgdn_gb300.so`` in the package tree.
+"""Build the sm_103a C-ABI library ``_build/libgdn_gb300.so`` in the package tree, and the
+binding's extension ``_build/gdn_pycall.so`` beside it.
 
 Each translation unit is compiled by nvcc in parallel, then linked; a rebuild
-happens only when a source or header is newer than the library.
+happens only when a source or header is newer than the library or the extension.
 """
 from __future__ import annotations
 
@@ -9,6 +10,7 @@ import concurrent.futures as cf
 import os
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -16,6 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libgdn_gb300.so")
+PYCALL = os.path.join(BUILD, "gdn_pycall.so")
+PYCALL_SOURCE = os.path.join(CSRC, "pycall.c")
 SOURCES = ["prefill.cu", "decode.cu", "decay_prefill.cu", "decay_step.cu", "norm_rope.cu", "api.cpp"]
 HEADERS = [os.path.join(CSRC, f) for f in ("prefill.h", "decode.h", "decay.h", "decay.cuh", "ptx.cuh")] + [os.path.join(INCLUDE, "gdn.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
@@ -29,11 +33,21 @@ def _nvcc() -> str:
 
 
 def _stale() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(PYCALL):
         return True
-    t = os.path.getmtime(LIB)
-    deps = [os.path.join(CSRC, s) for s in SOURCES] + HEADERS
+    t = min(os.path.getmtime(LIB), os.path.getmtime(PYCALL))
+    deps = [os.path.join(CSRC, s) for s in SOURCES] + HEADERS + [PYCALL_SOURCE]
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _build_pycall() -> None:
+    cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
+    tmp = PYCALL + f".tmp{os.getpid()}"
+    r = subprocess.run(["gcc", "-O2", "-std=c11", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
+                        "-I", os.path.join(cuda, "include"), PYCALL_SOURCE, "-o", tmp], capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"gcc failed on {PYCALL_SOURCE}:\n{r.stdout}\n{r.stderr}")
+    os.replace(tmp, PYCALL)
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -55,8 +69,10 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES)) as ex:
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        extension = ex.submit(_build_pycall)
         objs = list(ex.map(compile_one, SOURCES))
+        extension.result()
     tmp = LIB + f".tmp{os.getpid()}"
     r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"], capture_output=True, text=True)
     if r.returncode != 0:
