@@ -118,7 +118,8 @@ def describe(t: Optional[torch.Tensor]):
 class _PyCall:
     """The extension ``csrc/pycall.c``, for the operators whose smallest calls take a few
     microseconds on the GPU: ``qk_norm_rope``, ``decay_prefill`` and ``decay_step`` with the
-    arguments of the C functions, tensors described on the way, and ``fill``, the addresses of
+    arguments of the C functions (the last two also with whether the gate may be ``[H]``, one decay
+    for each head), tensors described on the way, and ``fill``, the addresses of
     descriptors alone.  Loaded with the library, at the first use."""
 
     def load(self, lib):
@@ -248,7 +249,7 @@ def gdn_decay_prefill(q, k, v, g, scale: float, initial_state, state_indices, ou
     """Linear attention with a decay over packed sequences; same names and order as the C
     entry point."""
     status = _calls.decay_prefill(q, k, v, g, scale, initial_state, state_indices, output_state, cu_seqlens, batch_invariant,
-                                  output, _stream_handle(stream))
+                                  output, _stream_handle(stream), False)
     if status:
         _check(status)
 
@@ -264,7 +265,7 @@ def gdn_decay_workspace_bytes(num_seqs: int, num_heads: int, total_tokens: int, 
 def gdn_decay_step(q, k, v, g, scale: float, state, state_indices, output, stream=None) -> None:
     """One token per batch row through the same recurrence, ``state`` in place; same names
     and order as the C entry point."""
-    status = _calls.decay_step(q, k, v, g, scale, state, state_indices, output, _stream_handle(stream))
+    status = _calls.decay_step(q, k, v, g, scale, state, state_indices, output, _stream_handle(stream), False)
     if status:
         _check(status)
 
@@ -365,6 +366,9 @@ def _allocating_on(stream):
     return torch.cuda.stream(torch.cuda.ExternalStream(int(stream)) if int(stream) else torch.cuda.default_stream())
 
 
+_no_context = contextlib.nullcontext()
+
+
 def _empty(shape, like, stream):
     if stream is None:
         return like.new_empty(shape)
@@ -372,9 +376,11 @@ def _empty(shape, like, stream):
         return like.new_empty(shape)
 
 
-def _gate_rows(g, rows: int):
-    """A gate as the library takes it: [rows, H]; [H] is one decay for each head."""
-    return g if g is None or g.dim() != 1 else g.expand(rows, g.shape[0])
+def _output_like(q, v, stream):
+    """An output of max(H_qk, H_v) heads: the shape of v, or of q (empty_like takes half of new_empty's time)."""
+    like = v if v.shape[1] >= q.shape[1] else q
+    with _allocating_on(stream) if stream is not None else _no_context:
+        return torch.empty_like(like, memory_format=torch.contiguous_format)
 
 
 def qk_norm_rope(q, k=None, cos_sin=None, positions=None, q_weight=None, k_weight=None, eps: float = 1e-6,
@@ -404,33 +410,36 @@ def decay_linear_attention(q, k, v, g=None, scale: Optional[float] = None, initi
     """
     if cu_seqlens is None:
         raise ValueError("cu_seqlens is required")
-    rows, H = q.shape[0], max(q.shape[1], v.shape[1])
     if output is None:
-        output = _empty((rows, H, q.shape[2]), q, stream)
+        output = _output_like(q, v, stream)
     final_state = None
     if output_final_state:
         if output_state is None:
+            H = max(q.shape[1], v.shape[1])
             pooled = state_indices is not None and initial_state is not None
             slots = initial_state.shape[0] if pooled else cu_seqlens.shape[0] - 1
             dt = initial_state.dtype if initial_state is not None else torch.float32
             with _allocating_on(stream):
                 output_state = torch.empty(slots, H, v.shape[2], q.shape[2], dtype=dt, device=q.device)
         final_state = output_state
-    gdn_decay_prefill(q, k, v, _gate_rows(g, rows), 0.0 if scale is None else float(scale), initial_state,
-                      state_indices, final_state, cu_seqlens, batch_invariant, output, stream)
+    status = _calls.decay_prefill(q, k, v, g, 0.0 if scale is None else scale, initial_state, state_indices, final_state,
+                                  cu_seqlens, batch_invariant, output, _stream_handle(stream), True)
+    if status:
+        _check(status)
     return (output, final_state) if output_final_state else output
 
 
 def decay_linear_step(q, k, v, state, g=None, scale: Optional[float] = None, state_indices=None, output=None,
                       stream=None):
     """One token for each batch row through the recurrence of :func:`decay_linear_attention`,
-    ``state`` read and written in place (``include/gdn.h``, gdn_decay_step).  Returns the
-    output ``[B, H, 128]``."""
-    rows = q.shape[0]
+    ``state`` read and written in place (``include/gdn.h``, gdn_decay_step); ``g`` is ``[B, H]``
+    or ``[H]``.  Returns the output ``[B, H, 128]``."""
     if output is None:
-        output = _empty((rows, max(q.shape[1], v.shape[1]), q.shape[2]), q, stream)
-    gdn_decay_step(q, k, v, _gate_rows(g, rows), 0.0 if scale is None else float(scale), state, state_indices, output,
-                   stream)
+        output = _output_like(q, v, stream)
+    status = _calls.decay_step(q, k, v, g, 0.0 if scale is None else scale, state, state_indices, output,
+                               _stream_handle(stream), True)
+    if status:
+        _check(status)
     return output
 
 

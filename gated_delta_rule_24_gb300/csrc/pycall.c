@@ -76,13 +76,24 @@ static int describe_all(descriptors* d, PyObject* const* t, int first, int n) {
   }
   return 0;
 }
+// A gate of one dimension is one decay for each head: the rows of q with a stride of 0.
+static void gate_rows(descriptors* d) {
+  if (!d->at[0] || !d->at[3] || d->at[3]->ndim != 1) return;
+  gdn_tensor_t* g = &d->room[3];
+  g->ndim = 2;
+  g->shape[1] = g->shape[0];
+  g->stride[1] = g->stride[0];
+  g->shape[0] = d->at[0]->shape[0];
+  g->stride[0] = 0;
+}
 static int wants(Py_ssize_t n, Py_ssize_t want, const void* fn) {
   if (n != want) PyErr_Format(PyExc_TypeError, "%zd arguments are wanted, got %zd", want, n);
   else if (!fn) PyErr_SetString(PyExc_RuntimeError, "the library is not bound");
   return n == want && fn ? 0 : -1;
 }
 
-// The arguments of the three are those of the C functions, in their order.
+// The arguments of the three are those of the C functions, in their order; then, for the last two, whether
+// a gate may be [H].
 static PyObject* qk_norm_rope(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   descriptors d;
   if (wants(n, 12, f_rope) || describe_all(&d, a, 0, 4) || describe_all(&d, a + 6, 4, 2) || describe_all(&d, a + 9, 6, 2)) return NULL;
@@ -99,7 +110,8 @@ static PyObject* qk_norm_rope(PyObject* self, PyObject* const* a, Py_ssize_t n) 
 
 static PyObject* decay_prefill(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   descriptors d;
-  if (wants(n, 12, f_prefill) || describe_all(&d, a, 0, 4) || describe_all(&d, a + 5, 4, 4) || describe_all(&d, a + 10, 8, 1)) return NULL;
+  if (wants(n, 13, f_prefill) || describe_all(&d, a, 0, 4) || describe_all(&d, a + 5, 4, 4) || describe_all(&d, a + 10, 8, 1)) return NULL;
+  if (a[12] == Py_True) gate_rows(&d);
   const float scale = (float)PyFloat_AsDouble(a[4]);
   const int invariant = PyObject_IsTrue(a[9]);
   cudaStream_t stream = (cudaStream_t)PyLong_AsVoidPtr(a[11]);
@@ -113,7 +125,8 @@ static PyObject* decay_prefill(PyObject* self, PyObject* const* a, Py_ssize_t n)
 
 static PyObject* decay_step(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   descriptors d;
-  if (wants(n, 9, f_step) || describe_all(&d, a, 0, 4) || describe_all(&d, a + 5, 4, 3)) return NULL;
+  if (wants(n, 10, f_step) || describe_all(&d, a, 0, 4) || describe_all(&d, a + 5, 4, 3)) return NULL;
+  if (a[9] == Py_True) gate_rows(&d);
   const float scale = (float)PyFloat_AsDouble(a[4]);
   cudaStream_t stream = (cudaStream_t)PyLong_AsVoidPtr(a[8]);
   if (PyErr_Occurred()) return NULL;
