@@ -60,7 +60,6 @@ struct DecayPrefillParams {
   float* ws;        // [U][splits - 1] states of 128 x 128: the state behind segment x, once joined
   float* ws_decay;  // [U][splits - 1] decays of whole segments
   int32_t splits;
-  int32_t claim_units;  // a CTA for each unit, which running ones take over (set by the launch)
 };
 constexpr int kDecayChunk = 128;  // tokens of a chunk
 

@@ -30,7 +30,8 @@
 // Hand-offs are mbarriers, every wait is bounded and ends early when any role gave up.  With all
 // roles resident the instruction cache is short: loops are rolled up where that measured faster
 // (P in rolled blocks of 16 columns: 16 x 4096 tokens on 32 heads 341 -> 322 us), and launches that
-// meet no f32 state are compiled without the code for them (1024 short prompts 680 -> 640 us).
+// meet no f32 state, or whose CTAs take no units over, are compiled without the code for that (1024
+// short prompts 680 -> 640 us, 650 -> 638).
 //
 // TMEM is full: the scores (then P), the output, the state (128 columns each), Q and V_d (64
 // each).  Further parts of V_d go where Q was, once Q S^T has read it, and between the blocks of P.
@@ -44,7 +45,7 @@
 //   16 x 4096, 16 q/k and 32 v heads, bf16 states: 316 us (77 %): 512 units are 3.4 rounds of 152
 //   2 x 65536, 16 and 32 heads, f32 states: 981 us (49 %); 7 segments, K and V read twice, three terms
 //   32000 tokens, 8 heads, f16: 80 us (48 %); 31 us states, 7 join, 41 outputs
-//   1024 prompts of 136 on average, 8 and 16 heads, bf16 states: 650 us (64 %); 1.6 chunks a unit
+//   1024 prompts of 136 on average, 8 and 16 heads, bf16 states: 638 us (65 %); 1.6 chunks a unit
 //   one chunk of a unit alone: 2.3 us with two terms, 2.8 with three
 // Tensor pipe 54 % busy, issue slots 53 %, 60 % of DRAM (8 x 4096, 16 and 32 heads): a chunk takes
 // 4300 cycles at 2960 of products, the rest is hand-offs of 300 to 450 cycles between roles.
@@ -289,7 +290,7 @@ __device__ __forceinline__ void pass_on(const DecayPrefillParams& p, int h, int6
 }
 
 // ------------------------------------------------------------ warp 0: loads
-template <bool kStates, bool kWide>
+template <bool kStates, bool kWide, bool kClaim>
 __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_t* base, Small* sm, int lane) {
   bool ok = true;
   int u = 0, ci = 0;  // units and chunks so far
@@ -323,7 +324,7 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
   int64_t x = blockIdx.x;
   int claims = 0;
   auto claim = [&] {
-    if (!p.claim_units) return;
+    if (!kClaim) return;
     __syncwarp();
     if (lane == 0) {
       fence_proxy_async_smem();
@@ -333,7 +334,7 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
     ++claims;
   };
   auto another = [&] {
-    if (!p.claim_units) return (x += gridDim.x) < units;
+    if (!kClaim) return (x += gridDim.x) < units;
     uint32_t to = 0;
     ok = wait(sm, &sm->claim_full, (claims - 1) & 1);
     const bool any = ok && clc_answer(sm->claim, &to);
@@ -349,7 +350,7 @@ __device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_
       continue;
     }
     if (r.nch == 0) {  // nothing but a state to pass on: warps 12-15 see to these at the end, if they can find them
-      if (p.claim_units) pass_on<kStates>(p, r.h, r.slot, r.in, r.out, lane);
+      if (kClaim) pass_on<kStates>(p, r.h, r.slot, r.in, r.out, lane);
       else ++empties;
       continue;
     }
@@ -1139,7 +1140,7 @@ __device__ __forceinline__ void run_v(const DecayPrefillParams& p, uint8_t* base
 }
 
 // ------------------------------------------------------------ the kernel
-template <bool F16, int kTerms, bool kStates, bool kWide>
+template <bool F16, int kTerms, bool kStates, bool kWide, bool kClaim>
 __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __grid_constant__ DecayPrefillParams p) {
   extern __shared__ __align__(1024) uint8_t base[];
   Small* sm = reinterpret_cast<Small*>(base + kOffSmall);
@@ -1194,7 +1195,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __
   tc_fence_after();
   const uint32_t tmem = sm->tmem;
   if (warp < 4) {
-    if (warp == 0) run_producer<kStates, kWide>(p, base, sm, lane);
+    if (warp == 0) run_producer<kStates, kWide, kClaim>(p, base, sm, lane);
     else if (warp == 1) run_mma<F16, kTerms, kStates, kWide>(p, base, sm, tmem, lane);
     else if (warp == 2) run_gates<F16, kTerms, kStates>(p, sm, lane);
     else if (!kStates) run_store<kWide>(p, base, sm, lane);
@@ -1259,23 +1260,29 @@ bool claims_pay(int64_t units, double chunks, int sms) {
   return units > sms && chunks >= (units <= 8 * (int64_t)sms ? 2.0 : 6.0);
 }
 
-template <bool F16, int kTerms, bool kStates, bool kWide>
-cudaError_t launch_pass(const DecayPrefillParams& p, int sms, cudaStream_t stream) {
+template <bool F16, int kTerms, bool kStates, bool kWide, bool kClaim>
+cudaError_t launch_walk(const DecayPrefillParams& p, int sms, cudaStream_t stream) {
   static thread_local int device = -1, generation = -1;
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   const int gen = launch_config_generation();
   if (e == cudaSuccess && (device != dev || generation != gen)) {
-    e = cudaFuncSetAttribute(gdn_decay_prefill_kernel<F16, kTerms, kStates, kWide>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    e = cudaFuncSetAttribute(gdn_decay_prefill_kernel<F16, kTerms, kStates, kWide, kClaim>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
     if (e == cudaSuccess) { device = dev; generation = gen; }
   }
   if (e != cudaSuccess) return e;
   const int64_t units = (int64_t)p.N * p.H * (kStates ? p.splits - 1 : p.splits);
-  DecayPrefillParams q = p;
-  q.claim_units = claims_pay(units, double(p.T) / double(p.N) / p.splits / C, sms);
-  const int64_t grid = q.claim_units || units < sms ? units : sms;
-  gdn_decay_prefill_kernel<F16, kTerms, kStates, kWide><<<(unsigned)grid, kThreads, kSmem, stream>>>(q);
+  const int64_t grid = kClaim || units < sms ? units : sms;
+  gdn_decay_prefill_kernel<F16, kTerms, kStates, kWide, kClaim><<<(unsigned)grid, kThreads, kSmem, stream>>>(p);
   return cudaGetLastError();
+}
+
+template <bool F16, int kTerms, bool kStates, bool kWide>
+cudaError_t launch_pass(const DecayPrefillParams& p, int sms, cudaStream_t stream) {
+  const int64_t units = (int64_t)p.N * p.H * (kStates ? p.splits - 1 : p.splits);
+  return claims_pay(units, double(p.T) / double(p.N) / p.splits / C, sms)
+             ? launch_walk<F16, kTerms, kStates, kWide, true>(p, sms, stream)
+             : launch_walk<F16, kTerms, kStates, kWide, false>(p, sms, stream);
 }
 
 template <bool F16, int kTerms>

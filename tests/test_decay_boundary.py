@@ -201,3 +201,17 @@ def test_workspace_bytes_follow_the_plan():
         assert plan(5, 4, 1000, 152) == 5 * 4 * 2 * (65536 + 4)
     finally:
         gdn.testing_force_splits(0)
+
+
+def test_calls_refuse_what_is_no_tensor():
+    a = dict(step_args(), stream=0)
+    with pytest.raises(AttributeError):
+        gdn.gdn_decay_step(**dict(a, q=[1.0]))
+    with pytest.raises(TypeError):
+        gdn.gdn_decay_step(**dict(a, scale="1"))
+    with pytest.raises(TypeError):
+        gdn.gdn_decay_step(**dict(a, state=torch.zeros(3, 4, 128, 128, dtype=torch.int8)))
+    with pytest.raises(ValueError):
+        gdn.gdn_decay_step(**dict(a, k=torch.zeros(1, 1, 1, 1, 1)))
+    with pytest.raises(RuntimeError):  # GdnError: host tensors, or no GPU at all
+        gdn.decay_linear_step(a["q"], a["k"], a["v"], a["state"], torch.ones(a["v"].shape[1]), stream=0)
