@@ -42,9 +42,9 @@
 //
 // Measured (bf16 unless stated; time of the launches, share of 6.8 TB/s in the bytes that have to move):
 //   12800 tokens, 152 heads, none shared:  294 us, 6.6 TB/s (98 %, at the power limit)
-//   16 x 4096, 16 q/k and 32 v heads, bf16 states: 316 us (77 %): 512 units are 3.4 rounds of 152
-//   2 x 65536, 16 and 32 heads, f32 states: 981 us (49 %); 7 segments, K and V read twice, three terms
-//   32000 tokens, 8 heads, f16: 80 us (48 %); 31 us states, 7 join, 41 outputs
+//   16 x 4096, 16 q/k and 32 v heads, bf16 states: 314 us (77 %): 512 units are 3.4 rounds of 152
+//   2 x 65536, 16 and 32 heads, f32 states: 976 us (49 %); 7 segments, K and V read twice, three terms
+//   32000 tokens, 8 heads, f16: 78 us (49 %); 31 us states, 7 join, 41 outputs
 //   1024 prompts of 136 on average, 8 and 16 heads, bf16 states: 638 us (65 %); 1.6 chunks a unit
 //   one chunk of a unit alone: 2.3 us with two terms, 2.8 with three
 // Tensor pipe 54 % busy, issue slots 53 %, 60 % of DRAM (8 x 4096, 16 and 32 heads): a chunk takes

@@ -1,6 +1,7 @@
 // The Python side of the operators whose smallest calls take a few microseconds on the GPU:
-// reads the tensors' descriptors and calls the C entry point, which is bound by address.  For one token's
-// norm and rotation (eight tensors) that takes 3 us where ctypes and struct take 8.
+// reads the tensors' descriptors and calls the C entry point, which is bound by address.  One token's norm
+// and rotation (eight tensors, outputs given) then takes the host 5.6 us, launch included, where it took
+// 10.7 with ctypes and struct.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 #include <string.h>
