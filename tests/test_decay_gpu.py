@@ -374,6 +374,20 @@ def test_more_units_than_sms(force_split, splits, dtype, into, state):
     assert bool((final[rest] == 7.0).all())
 
 
+@pytest.mark.parametrize("dtype,state", [(BF, F32), (HF, HF)], ids=str)
+def test_segments_of_more_units_than_sms(force_split, dtype, state):
+    """As above, cut in two: segments without chunks among the states that are made first, too."""
+    force_split(2)
+    lengths = [0, 1900, 3, 1640, 0, 0, 129, 1512] * 3 + [2300, 0]
+    q, k, v, g, cu = R.make(lengths, 8, 8, dtype, "slow", 53)
+    s0 = R.states(len(lengths), 8, state, 53)
+    final = torch.full_like(s0, 7.0)
+    out, _ = gdn.decay_linear_attention(q, k, v, g, initial_state=s0, output_final_state=True, output_state=final, cu_seqlens=cu)
+    assert gdn.device_status() == 0
+    o_ref, s_ref = R.recurrence(q, k, v, g, SCALE, s0, lengths)
+    R.check(out, o_ref, final, s_ref, lengths)
+
+
 def test_more_units_than_sms_skip_bad_sequences():
     lengths = [300, 700] * 20
     q, k, v, g, cu = R.make(lengths, 2, 8, seed=52)
