@@ -906,13 +906,7 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
       // S as the chunk finds it: to 16 bits for Q S^T, times the chunk's decay for V_d^T K
       if (!(wait(sm, &sm->gate_full[st], (ci >> 1) & 1) && (c == 0 || wait(sm, &sm->s_done, (ci - 1) & 1)))) { failed = true; break; }
       tc_fence_after();
-      // The tensor cores' sums are cut off towards zero: each product of 16 tokens that is added to the state
-      // costs half a unit in its last place on average, 4 kTerms units a chunk and 2/3 of that times 2^-23
-      // of the value.  An f32 state that decays gets it back with the decay: one that holds some 2000
-      // tokens is off by 2.5e-6 instead of 8.8e-6.  Without a decay it stays as it is (8.6e-6
-      // after 16000 tokens, 2.4e-5 after 60000), so that tokens of zeros leave the state alone.
-      const float decay = sm->gamma[st];
-      const float2 gam = pair(kWide && decay < 1.f ? fmaf(decay, kTerms * 0x1.555556p-22f, decay) : decay);
+      const float2 gam = pair(sm->gamma[st]);
       const bool direct = c == 0 && state_in_tma<kWide>(p, r);  // the copy came by TMA
       if (c == 0 && !(direct ? wait(sm, &sm->si_full, ins++ & 1) : outs == 0 || wait(sm, &sm->f_stored, (outs - 1) & 1))) {
         failed = true;

@@ -1,0 +1,64 @@
+"""What f32 states of the decay prefill hold after many tokens, against sums in 64 bits."""
+import pytest
+import torch
+
+import gated_delta_rule_24_gb300 as gdn
+from tests import decay_ref as R
+
+pytestmark = pytest.mark.gpu
+BF, HF, F32 = torch.bfloat16, torch.float16, torch.float32
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from gated_delta_rule_24_gb300 import build
+    build.build()
+    gdn.gdn_init(0)
+    yield
+    assert gdn.device_status() == 0
+
+
+def summed(k, v, g, state=None):
+    """The state behind one sequence, [H, 128, 128] in 64 bits: every token's product times the decays behind it."""
+    T, H = v.shape[:2]
+    logs = torch.zeros(T, H, dtype=torch.float64, device=v.device) if g is None else g.double().expand(T, H).log()
+    behind = logs.flip(0).cumsum(0).flip(0) - logs
+    s = torch.einsum("thr,thc->hrc", v.double() * behind.exp()[..., None], k.double())
+    return s if state is None else s + logs.sum(0).exp()[:, None, None] * state.double()
+
+
+def final_state(q, k, v, g, state=None, **kw):
+    cu = torch.tensor([0, q.shape[0]], dtype=torch.int32, device="cuda")
+    _, s = gdn.decay_linear_attention(q, k, v, g, initial_state=state, output_final_state=True, cu_seqlens=cu, **kw)
+    assert s.dtype == F32
+    return s
+
+
+# A state that tokens of zeros pass over is multiplied by one decay a chunk: 2^x, with an error of up to two units in
+# the last place, and the rounding of the product, half of one.  A unit is at most 2^-23 of the value.
+UNITS = 3 * 2.0 ** -23
+DECAYS = (1 - 2.0 ** -24, 1 - 1e-6, 0.99999, 0.9999)
+
+
+@pytest.mark.parametrize("invariant", [True, False], ids=["uncut", "planned"])
+@pytest.mark.parametrize("zeros", ["keys", "values"])
+def test_tokens_of_zeros_only_decay(zeros, invariant):
+    T, g = 64000, torch.tensor(DECAYS, device="cuda")
+    q, k, v, _, _ = R.make([T], len(DECAYS), len(DECAYS), gate="none", seed=60)
+    (k if zeros == "keys" else v)[1:] = 0
+    got, want = final_state(q, k, v, g, batch_invariant=invariant)[0], summed(k, v, g)
+    for h in range(len(DECAYS)):
+        assert R.rel(got[h], want[h]) <= T / 128 * UNITS, (DECAYS[h], R.rel(got[h], want[h]))
+
+
+def test_short_calls_of_zeros_only_decay():
+    calls, g = 400, torch.tensor(DECAYS, device="cuda")
+    q, k, v, _, _ = R.make([3], len(DECAYS), len(DECAYS), gate="none", seed=61)
+    s0 = R.states(1, len(DECAYS), F32, 61)
+    for n in (1, 3):
+        s = s0
+        for _ in range(calls):
+            s = final_state(q[:n], torch.zeros_like(k[:n]), v[:n], g, s)
+        want = s0.double() * (g.double() ** (n * calls))[:, None, None]
+        for h in range(len(DECAYS)):
+            assert R.rel(s[0, h], want[0, h]) <= calls * UNITS, (n, DECAYS[h], R.rel(s[0, h], want[0, h]))
