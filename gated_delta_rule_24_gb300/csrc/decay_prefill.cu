@@ -25,7 +25,8 @@
 //   warps 4-11  two threads a token: Q from shared memory to TMEM, P (scores times decay, masked, back to
 //               TMEM), Q S^T times scale 2^G_i in place, and the output tile;
 //   warps 12-15 one thread a value row: before a chunk's V_d^T K adds to it, the state in TMEM goes times
-//               the chunk's decay, and as a 16-bit copy to shared memory for Q S^T;
+//               the chunk's decay, and as a 16-bit copy to shared memory for Q S^T; f32 states stay in
+//               these warps' registers, and take from TMEM what each chunk adds;
 //   warps 16-23 V_d: transposed fragments of V times d, to TMEM.
 // Hand-offs are mbarriers, every wait is bounded and ends early when any role gave up.  With all
 // roles resident the instruction cache is short: loops are rolled up where that measured faster
@@ -69,6 +70,7 @@
 #include <stddef.h>
 
 #include <cmath>
+#include <type_traits>
 
 #include "decay.cuh"
 #include "ptx.cuh"
@@ -98,6 +100,16 @@ __device__ __forceinline__ uint32_t vd_slot_col(int slot) {
   return kStates ? kTmAcc + 64 * slot : slot == 0 ? kTmVd : slot == 1 ? kTmQ : kTmAcc + 32;
 }
 constexpr uint32_t kTmCols = 512;
+// kWide (a launch that meets f32 states): TMEM holds what one chunk adds, and the state itself is in the registers
+// of warps 12-15, where each chunk is added to it in f32.  The tensor cores cut their sums off towards zero: with
+// the state in TMEM each product of 16 tokens cost it half a unit in the last place, 1.8e-5 of a state of 16000 tokens
+// and 7e-5 after 60000; now 5e-7, which is what the sum over a chunk costs.  Where only states are made there is
+// room for two chunks.  8 prompts of up to 2000 tokens 55.6 -> 57.4 us, 32000 tokens of f16 85 -> 90, 2 x 65536
+// 1048 -> 1085, one of 256 tokens 14.4 -> 16.4.
+template <bool kWide>
+__host__ __device__ constexpr bool apart() { return kWide; }
+template <bool kStates>
+__device__ __forceinline__ uint32_t sum_col(int ci) { return kStates ? kTmS + 128 * (ci & 1) : kTmS; }
 
 // ------------------------------------------------------------ shared memory (bytes)
 constexpr uint32_t kTile = C * D * 2;       // a 16-bit tile: two 128B-swizzled halves of 64 columns
@@ -116,18 +128,22 @@ struct Rec {       // one unit: a sequence, or a segment of one, of one head.  O
 };
 constexpr int kPool = -1, kNone = -2;  // the caller's pool (zeros without one), or nowhere (zeros)
 struct Small {
+  static constexpr bool kInline = false;  // of slow waits
   float G[2][C];   // inclusive prefix sums of log2 g
   float d[2][C];   // 2^(sum of the log2 g behind the token), 0 past the end; with two V_d terms
                    // as 16-bit halves, C high ones and C low ones
   float cf[C];     // 2^(G_e - G_j), e the last token of j's block of 16
   int32_t mild[2]; // no block of 16 tokens decays by more than 2^-100
-  float gamma[2];  // 2^(G_last)
+  float gamma[2];  // 2^(G_last); where the state is kept apart and the decay is slow, 2^(G_last) - 1 with the sign bit set
   alignas(16) uint32_t claim[4];  // the answer to a claim of another unit
   Rec rec[kRecs];
   uint64_t q_full, q_empty, k_full[3], v_full[3], kv_empty[3];
   uint64_t rec_full[kRecs], rec_empty[kRecs], claim_full;
   uint64_t gate_full[2], gate_empty[2], cf_empty;
-  uint64_t qk_done, qs_done, s_done, o_done;   // products that have completed
+  union {
+    struct { uint64_t qk_done, qs_done, s_done, o_done; };  // products that have completed
+    struct { uint64_t sum_done[2], sum_free[2]; };          // where only states are made: what a chunk adds
+  };
   uint64_t q_ready, p_ready, o_free, o_staged;  // warps 4-11
   uint64_t o_stored, f_half, f_stored;          // warp 3
   uint64_t f_staged, si_full;                   // warps 12-15; an incoming 16-bit state
@@ -137,6 +153,9 @@ struct Small {
   uint32_t tmem;
   int32_t abort;
 };
+struct SmallInline : Small { static constexpr bool kInline = true; };
+template <bool kWide>
+using SmallOf = std::conditional_t<apart<kWide>(), SmallInline, Small>;
 constexpr uint32_t kSmem = kOffSmall + sizeof(Small);
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
 
@@ -144,6 +163,10 @@ template <bool kStates>
 __host__ __device__ constexpr int kv_stages() { return kStates ? 3 : 2; }
 constexpr int kPoWarps = 8, kSWarps = 4, kVWarps = 8;
 constexpr int kThreads = 32 * (4 + kPoWarps + kSWarps + kVWarps);
+// Registers a thread: what a launch has, and how a launch that keeps the state apart shares them out among its
+// groups of four warps.  200 to 216 for the state are the fewest without spills; 176 to 216 measured within 2 %.
+constexpr int kRegs = 80, kRegsOne = 56, kRegsPo = 56, kRegsState = 216, kRegsV = 48;
+static_assert(4 * kRegsOne + kPoWarps * kRegsPo + kSWarps * kRegsState + kVWarps * kRegsV <= kThreads / 32 * kRegs, "registers of a launch");
 // The stages of K and V as a role goes through them, with the phase of each.
 template <bool kStates>
 struct Ring {
@@ -154,16 +177,25 @@ struct Ring {
   __device__ __forceinline__ void next() { phases ^= 1u << s; pass(); }                      // over a chunk
 };
 
-// Every wait: bounded (kTries probes of up to 20 us each), and over as soon as another role has
-// given up.  Only the first probe is in line: the roles together fill the instruction cache.
-constexpr int kTries = 50000;
+// Every wait: bounded (kTries probes of 4 us each, or kTriesInline of 1.5 us; 0.2 s), and over as soon as another
+// role has given up.  Only the first probe is in line: the roles together fill the instruction cache.  Where the
+// groups of warps share registers out among them there can be no call, and a single loop in line is the smallest.
+constexpr int kTries = 50000, kTriesInline = 150000;
 __device__ __noinline__ bool wait_slow(const volatile int32_t* abort, uint64_t* bar, uint32_t parity) {
   bool ok = false;
 #pragma unroll 1
   for (int i = 0; i < kTries && !ok && !*abort; ++i) ok = mbar_try_wait_sleep(bar, parity, 20000u);
   return __all_sync(0xffffffffu, ok);
 }
-__device__ __forceinline__ bool wait(Small* sm, uint64_t* bar, uint32_t parity) {
+template <class Sm>
+__device__ __forceinline__ bool wait(Sm* sm, uint64_t* bar, uint32_t parity) {
+  if (Sm::kInline) {
+    int left = kTriesInline;
+#pragma unroll 1
+    while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+      if (--left == 0 || *reinterpret_cast<const volatile int32_t*>(&sm->abort)) return false;
+    return true;
+  }
   if (__all_sync(0xffffffffu, mbar_try_wait(bar, parity))) return true;
   return wait_slow(&sm->abort, bar, parity);
 }
@@ -189,7 +221,8 @@ __device__ __forceinline__ float exp2_fast(float x) {
 
 // The next unit's record, for every role but the producer; false when there is none left
 // or a wait gave up (*failed).
-__device__ __forceinline__ bool next_unit(Small* sm, int u, int lane, Rec* r, bool* failed) {
+template <class Sm>
+__device__ __forceinline__ bool next_unit(Sm* sm, int u, int lane, Rec* r, bool* failed) {
   const int slot = u % kRecs;
   if (!wait(sm, &sm->rec_full[slot], (u / kRecs) & 1)) {
     *failed = true;
@@ -291,7 +324,7 @@ __device__ __forceinline__ void pass_on(const DecayPrefillParams& p, int h, int6
 
 // ------------------------------------------------------------ warp 0: loads
 template <bool kStates, bool kWide, bool kClaim>
-__device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_t* base, Small* sm, int lane) {
+__device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_t* base, SmallOf<kWide>* sm, int lane) {
   bool ok = true;
   int u = 0, ci = 0;  // units and chunks so far
   Ring<kStates> ring;
@@ -440,7 +473,7 @@ __device__ __forceinline__ void vd_place(int ci, int b, int* slot, int* round) {
 }
 
 template <bool F16, int kTerms, bool kStates, bool kWide>
-__device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* base, Small* sm, uint32_t tmem, int lane) {
+__device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* base, SmallOf<kWide>* sm, uint32_t tmem, int lane) {
   constexpr int kSub = sub_tokens<kTerms>(), kSubs = C / kSub;
   const uint32_t id_kk = idesc_16_f32(F16, 128, 128, 0, 0, 0);  // B K-major
   const uint32_t id_kmn = idesc_16_f32(F16, 128, 128, 0, 1, 0); // B MN-major (its rows are summed over)
@@ -449,7 +482,7 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
   const bool leader = elect_one();
   bool failed = false;
   Rec r;
-  int ci = 0, sums = 0, ins = 0;  // chunks so far; units (states); 16-bit states by TMA
+  int ci = 0, ins = 0;  // chunks so far; 16-bit states by TMA
   Ring<kStates> ring;
   for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
     if (!kStates && state_in_ring<kWide>(p, r)) ring.pass();
@@ -459,8 +492,8 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
       const uint32_t k = smem_u32(base + kOffKv + s * 2 * kTile);
       const uint64_t d_k = sdesc_sw128(k, 16, 1024), d_kt = sdesc_sw128(k, kHalf, 1024);
       const uint64_t d_vt = sdesc_sw128(k + kTile, kHalf, 1024);
-      if (kStates) {  // the sum of the unit before has been read
-        if (!(wait(sm, &sm->k_full[s], ph) && (c > 0 || sums == 0 || wait(sm, &sm->s_ready, (sums - 1) & 1)))) { failed = true; break; }
+      if (kStates) {  // what the chunk before the last added has been read
+        if (!(wait(sm, &sm->k_full[s], ph) && (ci < 2 || wait(sm, &sm->sum_free[one], ((ci >> 1) - 1) & 1)))) { failed = true; break; }
       } else {
         // Q K^T.  P of the chunk before is being read by its P V at the latest, which was
         // issued before: the products run in order.
@@ -502,10 +535,10 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
           for (int t = 0; t < kTerms; ++t)
 #pragma unroll
             for (int i = 0; i < kSub / 16; ++i)
-              mma_ts(tmem + kTmS, tmem + vd_slot_col<kStates>(slot) + t * (kSub / 2) + i * 8, d_kt + (b * (kSub / 16) + i) * 128,
-                     kTerms == 2 && t == 0 ? id_kmn_neg : id_kmn, !kStates || c + b + t + i > 0);
+              mma_ts(tmem + sum_col<kStates>(ci), tmem + vd_slot_col<kStates>(slot) + t * (kSub / 2) + i * 8, d_kt + (b * (kSub / 16) + i) * 128,
+                     kTerms == 2 && t == 0 ? id_kmn_neg : id_kmn, !apart<kWide>() || b + t + i > 0);
           mma_commit(&sm->vd_empty[slot]);
-          if (b == kSubs - 1 && (!kStates || c + 1 == r.nch)) mma_commit(&sm->s_done);
+          if (b == kSubs - 1) mma_commit(kStates ? &sm->sum_done[one] : &sm->s_done);
           if (kStates && b == kSubs - 1) mma_commit(&sm->kv_empty[s]);
         }
         __syncwarp();
@@ -525,7 +558,6 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
       __syncwarp();
     }
     if (failed) break;
-    ++sums;
   }
   if (failed && lane == 0) give_up(p, sm);
   if (leader) mma_commit(&sm->drain);
@@ -534,8 +566,8 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
 }
 
 // ------------------------------------------------------------ warp 2: gates
-template <bool F16, int kTerms, bool kStates>
-__device__ __forceinline__ void run_gates(const DecayPrefillParams& p, Small* sm, int lane) {
+template <bool F16, int kTerms, bool kStates, bool kWide>
+__device__ __forceinline__ void run_gates(const DecayPrefillParams& p, SmallOf<kWide>* sm, int lane) {
   bool failed = false;
   Rec r{};
   int ci = 0;
@@ -599,7 +631,10 @@ __device__ __forceinline__ void run_gates(const DecayPrefillParams& p, Small* sm
         *reinterpret_cast<float4*>(&sm->d[b][4 * lane]) = make_float4(d[0], d[1], d[2], d[3]);
       }
       if (lane == 0) {
-        sm->gamma[b] = exp2f(total);
+        // b S + a S with a = 2^(G_last) - 1 knows a decay near 1 far better than 2^(G_last) S, whose error is the same
+        // one in every chunk of equal gates
+        const bool slow = apart<kWide>() && total > -1.f;
+        sm->gamma[b] = slow ? copysignf(expm1f(total * 0.693147180559945f), -1.f) : exp2f(total);
         sm->mild[b] = mild;
       }
       later += total;
@@ -618,7 +653,7 @@ __device__ __forceinline__ void run_gates(const DecayPrefillParams& p, Small* sm
 
 // ------------------------------------------------------------ warp 3: output stores
 template <bool kWide>
-__device__ __forceinline__ void run_store(const DecayPrefillParams& p, uint8_t* base, Small* sm, int lane) {
+__device__ __forceinline__ void run_store(const DecayPrefillParams& p, uint8_t* base, SmallOf<kWide>* sm, int lane) {
   bool failed = false;
   Rec r;
   int ci = 0, outs = 0;  // tiles and parts of states that have gone out
@@ -665,8 +700,8 @@ __device__ __forceinline__ void run_store(const DecayPrefillParams& p, uint8_t* 
 }
 
 // ------------------------------------------------------------ warps 4-11: P and the output
-template <bool F16>
-__device__ __forceinline__ void run_po(const DecayPrefillParams& p, uint8_t* base, Small* sm, uint32_t tmem, int warp, int lane) {
+template <bool F16, bool kWide>
+__device__ __forceinline__ void run_po(const DecayPrefillParams& p, uint8_t* base, SmallOf<kWide>* sm, uint32_t tmem, int warp, int lane) {
   const int w = warp & 3, hf = (warp >> 2) - 1, row = 32 * w + lane;  // warps 4-11: columns 0 .. 63, 8-11: 64 .. 127
   const uint32_t tr = tmem + ((uint32_t)(32 * w) << 16);
   bool failed = false;
@@ -874,7 +909,7 @@ __device__ __forceinline__ void zero_tails(uint8_t* k, uint8_t* v, int left, int
 }
 
 template <bool F16, int kTerms, bool kStates, bool kWide>
-__device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* base, Small* sm, uint32_t tmem, int warp, int lane) {
+__device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* base, SmallOf<kWide>* sm, uint32_t tmem, int warp, int lane) {
   const int w = warp & 3, row = 32 * w + lane;
   const uint32_t ts = tmem + ((uint32_t)(32 * w) << 16) + kTmS;
   uint8_t* sb = base + kOffS;
@@ -897,10 +932,55 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
     if (kWide && r.out >= 0) store_state32<kWide>(p.ws, kF32, (int64_t)r.out * (D * D) + at, x);
     else store_state32<kWide>(p.s_out, p.sout_dtype, (int64_t)r.slot * p.sout_slot + (int64_t)r.h * p.sout_head + at, x);
   };
+  // S <- b S + (a S + what the chunk before added, from TMEM); with `copy`, also in 16 bits to where Q S^T reads it
+  float2 S[apart<kWide>() ? D / 2 : 1];
+  float sa = 0.f, keep = 0.f;  // a and b
+  auto add_chunk = [&](uint32_t from, bool copy) {
+    const float2 a2 = pair(sa), b2 = pair(keep);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      uint32_t x[32];
+      tmem_ld32(from + 32 * q, x);
+      tmem_ld_wait();
+#pragma unroll
+      for (int e = 0; e < 16; ++e) S[16 * q + e] = fma2(b2, S[16 * q + e], fma2(a2, S[16 * q + e], pair_at(x + 2 * e)));
+      if (copy) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          *reinterpret_cast<uint4*>(sb + (q >> 1) * kHalf + sw128_chunk(row, 4 * (q & 1) + e)) =
+              make_uint4(pack16x2<F16>(S[16 * q + 4 * e]), pack16x2<F16>(S[16 * q + 4 * e + 1]),
+                         pack16x2<F16>(S[16 * q + 4 * e + 2]), pack16x2<F16>(S[16 * q + 4 * e + 3]));
+      }
+    }
+  };
+  auto zero = [&] {
+#pragma unroll
+    for (int e = 0; e < D / 2; ++e) S[e] = make_float2(0.f, 0.f);
+  };
+  auto put_back = [&](uint32_t to) {  // S to TMEM, from where loops that are rolled up store it
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      uint32_t x[8];
+#pragma unroll
+      for (int e = 0; e < 4; ++e) { x[2 * e] = __float_as_uint(S[4 * q + e].x); x[2 * e + 1] = __float_as_uint(S[4 * q + e].y); }
+      tmem_st8(to + 8 * q, x);
+    }
+    tmem_st_wait();
+  };
   for (int u = 0; next_unit(sm, u, lane, &r, &failed); ++u) {
     const bool ring = !kStates && state_in_ring<kWide>(p, r);
     const uint8_t* from = base + kOffKv + (entries & 1) * 2 * kTile;
     entries += r.nch + ring;
+    for (int c = 0; c < r.nch && kStates; ++c, ++ci) {
+      if (!wait(sm, &sm->sum_done[ci & 1], (ci >> 1) & 1)) { failed = true; break; }
+      tc_fence_after();
+      if (c == 0) zero();
+      keep = 1.f;
+      add_chunk(ts + (sum_col<kStates>(ci) - kTmS), false);
+      if (c + 1 == r.nch) continue;
+      tc_fence_before();
+      warp_arrive(&sm->sum_free[ci & 1], lane);
+    }
     for (int c = 0; c < r.nch && !kStates; ++c, ++ci) {
       const int st = ci & 1;
       // S as the chunk finds it: to 16 bits for Q S^T, times the chunk's decay for V_d^T K
@@ -913,45 +993,61 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
         break;
       }
       if (c == 0 && ring && !wait(sm, &sm->sf_full, fins++ & 1)) { failed = true; break; }
+      auto through = [&] {
 #pragma unroll 1
-      for (int q = 0; q < 4; ++q) {
-        uint32_t x[32];
-        if (c > 0) {
-          tmem_ld32(ts + 32 * q, x);
-          tmem_ld_wait();
-        } else if (ring) {
+        for (int q = 0; q < 4; ++q) {
+          uint32_t x[32];
+          if (c > 0) {
+            tmem_ld32(ts + 32 * q, x);
+            tmem_ld_wait();
+          } else if (ring) {
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint4 z = *reinterpret_cast<const uint4*>(from + q * kHalf + sw128_chunk(row, e));
-            x[4 * e] = z.x; x[4 * e + 1] = z.y; x[4 * e + 2] = z.z; x[4 * e + 3] = z.w;
+            for (int e = 0; e < 8; ++e) {
+              const uint4 z = *reinterpret_cast<const uint4*>(from + q * kHalf + sw128_chunk(row, e));
+              x[4 * e] = z.x; x[4 * e + 1] = z.y; x[4 * e + 2] = z.z; x[4 * e + 3] = z.w;
+            }
+          } else if (direct) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const uint4 z = *reinterpret_cast<const uint4*>(sb + (q >> 1) * kHalf + sw128_chunk(row, 4 * (q & 1) + e));
+              const uint32_t zw[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const float2 f = unpack16<F16>(zw[i]);
+                x[8 * e + 2 * i] = __float_as_uint(f.x);
+                x[8 * e + 2 * i + 1] = __float_as_uint(f.y);
+              }
+            }
+          } else {
+            load_in(32 * q, x);
           }
-        } else if (direct) {
+          if (!apart<kWide>()) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const uint4 z = *reinterpret_cast<const uint4*>(sb + (q >> 1) * kHalf + sw128_chunk(row, 4 * (q & 1) + e));
-            const uint32_t zw[4] = {z.x, z.y, z.z, z.w};
+            for (int e = 0; e < 4 && !direct; ++e)
+              *reinterpret_cast<uint4*>(sb + (q >> 1) * kHalf + sw128_chunk(row, 4 * (q & 1) + e)) =
+                  make_uint4(pack16x2<F16>(pair_at(x + 8 * e)), pack16x2<F16>(pair_at(x + 8 * e + 2)),
+                             pack16x2<F16>(pair_at(x + 8 * e + 4)), pack16x2<F16>(pair_at(x + 8 * e + 6)));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const float2 f = unpack16<F16>(zw[i]);
-              x[8 * e + 2 * i] = __float_as_uint(f.x);
-              x[8 * e + 2 * i + 1] = __float_as_uint(f.y);
+            for (int e = 0; e < 32; e += 2) {
+              const float2 y = mul2(pair_at(x + e), gam);
+              x[e] = __float_as_uint(y.x);
+              x[e + 1] = __float_as_uint(y.y);
             }
           }
-        } else {
-          load_in(32 * q, x);
+          tmem_st32(ts + 32 * q, x);
         }
-#pragma unroll
-        for (int e = 0; e < 4 && !direct; ++e)
-          *reinterpret_cast<uint4*>(sb + (q >> 1) * kHalf + sw128_chunk(row, 4 * (q & 1) + e)) =
-              make_uint4(pack16x2<F16>(pair_at(x + 8 * e)), pack16x2<F16>(pair_at(x + 8 * e + 2)),
-                         pack16x2<F16>(pair_at(x + 8 * e + 4)), pack16x2<F16>(pair_at(x + 8 * e + 6)));
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) {
-          const float2 y = mul2(pair_at(x + e), gam);
-          x[e] = __float_as_uint(y.x);
-          x[e + 1] = __float_as_uint(y.y);
+      };
+      if (!apart<kWide>()) {
+        through();
+      } else {
+        if (c == 0) {  // to TMEM as it is: it is what is added to zero
+          through();
+          tmem_st_wait();
+          zero();
         }
-        tmem_st32(ts + 32 * q, x);
+        add_chunk(ts, !direct);
+        sa = sm->gamma[st];
+        keep = __float_as_int(sa) < 0 ? 1.f : 0.f;
       }
       fence_proxy_async_smem();
       tmem_st_wait();
@@ -963,10 +1059,14 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
     if (failed) break;
     // the state that the unit leaves; the next unit may overwrite TMEM and the 16-bit copy after
     // that, Q S^T having run before
-    if (kStates) ++ci;  // sums so far
-    if (!wait(sm, &sm->s_done, (ci - 1) & 1)) { failed = true; break; }
+    if (!kStates && !wait(sm, &sm->s_done, (ci - 1) & 1)) { failed = true; break; }
     if (r.out == kNone || (r.out == kPool && !p.s_out)) continue;
     tc_fence_after();
+    const uint32_t last = ts + (sum_col<kStates>(ci - 1) - kTmS);
+    if (apart<kWide>()) {
+      if (!kStates) add_chunk(last, false);
+      put_back(last);
+    }
     if (!kStates && kWide && state_out_tma(p, r) && p.sout_dtype == kF32) {
 #pragma unroll 1
       for (int q = 0; q < 4; ++q) {
@@ -1014,7 +1114,7 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
 #pragma unroll 1
     for (int q = 0; q < 4; ++q) {
       uint32_t x[32];
-      tmem_ld32(ts + 32 * q, x);
+      tmem_ld32(last + 32 * q, x);
       tmem_ld_wait();
       if (start) {  // what the segment added, and the state that it started from
         uint32_t y[32];
@@ -1030,7 +1130,7 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
     }
     if (kStates) {
       tc_fence_before();
-      warp_arrive(&sm->s_ready, lane);
+      warp_arrive(&sm->sum_free[(ci - 1) & 1], lane);
     }
   }
   if (failed) {
@@ -1065,7 +1165,7 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
 // Transposed fragments of V (pairs of tokens, one value each) times d, as kTerms 16-bit terms, 16
 // values a warp.  Where only states are made, the warps of P do the same, every other part.
 template <bool F16, int kTerms, bool kStates, bool kWide>
-__device__ __forceinline__ void run_v(const DecayPrefillParams& p, uint8_t* base, Small* sm, uint32_t tmem, int warp, int lane) {
+__device__ __forceinline__ void run_v(const DecayPrefillParams& p, uint8_t* base, SmallOf<kWide>* sm, uint32_t tmem, int warp, int lane) {
   constexpr int kSub = sub_tokens<kTerms>(), kSubs = C / kSub, kGroups = kStates ? 2 : 1;
   const int w = warp & 3, hf = (warp >> 2) & 1, group = kStates && warp < 4 + kPoWarps ? 1 : 0;
   const uint32_t tq = tmem + ((uint32_t)(32 * w + 16 * hf) << 16);
@@ -1143,7 +1243,7 @@ __device__ __forceinline__ void run_v(const DecayPrefillParams& p, uint8_t* base
 template <bool F16, int kTerms, bool kStates, bool kWide, bool kClaim>
 __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __grid_constant__ DecayPrefillParams p) {
   extern __shared__ __align__(1024) uint8_t base[];
-  Small* sm = reinterpret_cast<Small*>(base + kOffSmall);
+  SmallOf<kWide>* sm = reinterpret_cast<SmallOf<kWide>*>(base + kOffSmall);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     auto init = [](uint64_t* bar, int n, int count) {
@@ -1160,10 +1260,15 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __
     init(sm->gate_empty, 2, kPoWarps + (kStates ? 0 : kSWarps) + kVWarps);
     init(&sm->claim_full, 1, 1);
     init(&sm->cf_empty, 1, kPoWarps);
-    init(&sm->qk_done, 1, 1);
-    init(&sm->qs_done, 1, 1);
-    init(&sm->s_done, 1, 1);
-    init(&sm->o_done, 1, 1);
+    if (kStates) {
+      init(sm->sum_done, 2, 1);
+      init(sm->sum_free, 2, kSWarps);
+    } else {
+      init(&sm->qk_done, 1, 1);
+      init(&sm->qs_done, 1, 1);
+      init(&sm->s_done, 1, 1);
+      init(&sm->o_done, 1, 1);
+    }
     init(&sm->p_ready, 1, kPoWarps);
     init(&sm->o_free, 1, kPoWarps);
     init(&sm->o_staged, 1, kPoWarps);
@@ -1195,16 +1300,20 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __
   tc_fence_after();
   const uint32_t tmem = sm->tmem;
   if (warp < 4) {
+    if (apart<kWide>()) reg_dec<kRegsOne>();
     if (warp == 0) run_producer<kStates, kWide, kClaim>(p, base, sm, lane);
     else if (warp == 1) run_mma<F16, kTerms, kStates, kWide>(p, base, sm, tmem, lane);
-    else if (warp == 2) run_gates<F16, kTerms, kStates>(p, sm, lane);
+    else if (warp == 2) run_gates<F16, kTerms, kStates, kWide>(p, sm, lane);
     else if (!kStates) run_store<kWide>(p, base, sm, lane);
   } else if (warp < 4 + kPoWarps) {
+    if (apart<kWide>()) reg_dec<kRegsPo>();
     if (kStates) run_v<F16, kTerms, kStates, kWide>(p, base, sm, tmem, warp, lane);
-    else run_po<F16>(p, base, sm, tmem, warp, lane);
+    else run_po<F16, kWide>(p, base, sm, tmem, warp, lane);
   } else if (warp < 4 + kPoWarps + kSWarps) {
+    if (apart<kWide>()) reg_inc<kRegsState>();
     run_state<F16, kTerms, kStates, kWide>(p, base, sm, tmem, warp, lane);
   } else {
+    if (apart<kWide>()) reg_dec<kRegsV>();
     run_v<F16, kTerms, kStates, kWide>(p, base, sm, tmem, warp, lane);
   }
   tc_fence_before();
@@ -1268,6 +1377,10 @@ cudaError_t launch_walk(const DecayPrefillParams& p, int sms, cudaStream_t strea
   const int gen = launch_config_generation();
   if (e == cudaSuccess && (device != dev || generation != gen)) {
     e = cudaFuncSetAttribute(gdn_decay_prefill_kernel<F16, kTerms, kStates, kWide, kClaim>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    cudaFuncAttributes have{};
+    if (e == cudaSuccess) e = cudaFuncGetAttributes(&have, gdn_decay_prefill_kernel<F16, kTerms, kStates, kWide, kClaim>);
+    // the shares of the groups of warps are those of kRegs: with fewer, the group that asks for more would wait for ever
+    if (e == cudaSuccess && apart<kWide>() && have.numRegs <= kRegs - 8) e = cudaErrorLaunchOutOfResources;
     if (e == cudaSuccess) { device = dev; generation = gen; }
   }
   if (e != cudaSuccess) return e;
@@ -1299,8 +1412,11 @@ cudaError_t launch(const DecayPrefillParams& p, cudaStream_t stream) {
       if (e != cudaSuccess) return e;
     }
   }
-  const bool wide = p.splits > 1 || (p.s_in && p.sin_dtype == kF32) || (p.s_out && p.sout_dtype == kF32);
-  return wide ? launch_pass<F16, kTerms, false, true>(p, sms, stream) : launch_pass<F16, kTerms, false, false>(p, sms, stream);
+  if constexpr (kTerms == 2) {
+    const bool wide = p.splits > 1 || (p.s_in && p.sin_dtype == kF32) || (p.s_out && p.sout_dtype == kF32);
+    if (!wide) return launch_pass<F16, kTerms, false, false>(p, sms, stream);
+  }
+  return launch_pass<F16, kTerms, false, true>(p, sms, stream);
 }
 
 }  // namespace

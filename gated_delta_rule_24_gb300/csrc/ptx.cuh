@@ -323,6 +323,14 @@ GDN_DEV void ldmatrix_x4_trans(uint32_t saddr, uint32_t (&r)[4]) {
                : "memory");
 }
 
+// ---------------------------------------------------------------- registers
+// The calling group of four warps gives registers back, or waits for some: `N` a thread.  The groups' shares
+// must add up to no more than the launch has.
+template <int N>
+GDN_DEV void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N>
+GDN_DEV void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+
 // ---------------------------------------------------------------- 128-byte swizzle addressing
 // Byte offset of the 16-byte chunk `chunk` (0..7) of row `row` in a 128-byte-swizzled
 // K-major block whose rows are 128 B (64 bf16); the block must be 1024-B aligned.

@@ -62,3 +62,47 @@ def test_short_calls_of_zeros_only_decay():
         want = s0.double() * (g.double() ** (n * calls))[:, None, None]
         for h in range(len(DECAYS)):
             assert R.rel(s[0, h], want[0, h]) <= calls * UNITS, (n, DECAYS[h], R.rel(s[0, h], want[0, h]))
+
+
+# From here on the bound is that of f32 sums, whatever the number of tokens or calls (tests/decay_ref.py).
+
+
+def each_head(got, want, what):
+    for h in range(want.shape[0]):
+        assert R.rel(got[h], want[h]) <= R.STATE[F32], (what, h, R.rel(got[h], want[h]))
+
+
+@pytest.mark.parametrize("T,invariant", [(16000, True), (60000, True), (60000, False)], ids=["16000", "60000", "60000_planned"])
+@pytest.mark.parametrize("gate", ["none", 1e-5, 5e-4, "slow", "token"])
+@pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "f16"])
+def test_long_sums(dtype, gate, T, invariant):
+    """A number: one decay of exp(-gate) for all tokens."""
+    q, k, v, g, _ = R.make([T], 2, 2, dtype, gate if isinstance(gate, str) else "none", seed=62)
+    if not isinstance(gate, str):
+        g = torch.exp(torch.full((2,), -gate, device="cuda"))
+    s0 = R.states(1, 2, F32, 62)
+    each_head(final_state(q, k, v, g, s0, batch_invariant=invariant)[0], summed(k, v, g, s0[0]), (gate, T))
+
+
+@pytest.mark.parametrize("n", [1, 4, 8, 128])
+@pytest.mark.parametrize("gate", [0.0, 5e-4, "slow"])
+@pytest.mark.parametrize("dtype", [BF, HF], ids=["bf16", "f16"])
+def test_short_calls(dtype, gate, n):
+    """4096 tokens, n a call, into one state."""
+    T = 4096
+    q, k, v, g, _ = R.make([T], 2, 2, dtype, gate if isinstance(gate, str) else "none", seed=63)
+    if not isinstance(gate, str):
+        g = torch.exp(torch.full((T, 2), -gate, device="cuda"))
+    s = None
+    for t in range(0, T, n):
+        s = final_state(q[t:t + n], k[t:t + n], v[t:t + n], g[t:t + n], s)
+    each_head(s[0], summed(k, v, g), (gate, n))
+
+
+@pytest.mark.parametrize("invariant", [True, False], ids=["uncut", "planned"])
+def test_sparse_keys(invariant):
+    """One token in 700 has a key; between them nothing but decays."""
+    T, g = 64000, torch.tensor(DECAYS, device="cuda")
+    q, k, v, _, _ = R.make([T], len(DECAYS), len(DECAYS), gate="none", seed=64)
+    k[torch.arange(T, device="cuda") % 700 != 5] = 0
+    each_head(final_state(q, k, v, g, batch_invariant=invariant)[0], summed(k, v, g), "sparse")
