@@ -38,7 +38,7 @@
 // each).  Further parts of V_d go where Q was, once Q S^T has read it, and between the blocks of P.
 //
 // Too few units for the SMs: sequences are cut into segments (decay_splits).  One launch makes the
-// states that the segments add (K and V alone, sums in TMEM), the join chains them in f32, and the main
+// states that the segments add (K and V alone), the join chains them in f32, and the main
 // launch runs all segments from those.
 //
 // Measured (bf16 unless stated; time of the launches, share of 6.8 TB/s in the bytes that have to move):
@@ -54,7 +54,7 @@
 // Precision: P and the copy of S are rounded to the 16-bit type of q, k, v (as the output is);
 // everything else that is summed is f32.  V_d would put its rounding straight into the state, so
 // it enters as the sum of 16-bit terms, each the rounding of what is left: two (16 bits bf16, 22
-// bits f16), or three for bf16 inputs whose state stays in f32, which then is as exact as f32 sums
+// bits f16, where v_scale keeps them in f16's range), or three for bf16 inputs whose state stays in f32, which then is as exact as f32 sums
 // are.  The third term costs 0.5 us a chunk where SMs are not kept busy by bytes.
 //
 // 2^(G_i - G_j) is the product 2^(G_i - G_e) 2^(G_e - G_j) with e the last token of j's block
@@ -69,8 +69,8 @@
 #include <cuda_runtime.h>
 #include <stddef.h>
 
+#include <algorithm>
 #include <cmath>
-#include <type_traits>
 
 #include "decay.cuh"
 #include "ptx.cuh"
@@ -94,7 +94,8 @@ __device__ __forceinline__ uint32_t p_block_col(int jb) { return kTmAcc + 16 * j
 // from Q S^T to the next chunk's copy, and one between the blocks of P.  A launch that makes states
 // alone has the columns of the scores and the output for four.
 constexpr uint32_t kTmVd = 448;
-constexpr int kVdSlots = 4;
+template <bool kStates>
+__host__ __device__ constexpr int vd_slots() { return kStates ? 4 : 3; }
 template <bool kStates>
 __device__ __forceinline__ uint32_t vd_slot_col(int slot) {
   return kStates ? kTmAcc + 64 * slot : slot == 0 ? kTmVd : slot == 1 ? kTmQ : kTmAcc + 32;
@@ -120,6 +121,11 @@ constexpr uint32_t kOffS = kOffKv + 4 * kTile;  // 16-bit copy of S
 constexpr uint32_t kOffO = kOffS + kTile;    // the output tile on its way out
 constexpr uint32_t kOffSmall = kOffO + kTile;
 constexpr int kRecs = 3;
+constexpr int kPoWarps = 8, kSWarps = 4, kVWarps = 8;
+// f16 and a state that is kept apart: V_d is multiplied by powers of two (v_scale), the decays d by 2^kDExp
+template <bool F16, bool kWide>
+__host__ __device__ constexpr bool lifted() { return F16 && apart<kWide>(); }
+constexpr int kDExp = 13;
 
 struct Rec {       // one unit: a sequence, or a segment of one, of one head.  Only units with chunks go round
   int32_t t0, len, h, nch;  // first token, tokens, head, chunks (-1: no more units; h counts those without chunks)
@@ -127,17 +133,21 @@ struct Rec {       // one unit: a sequence, or a segment of one, of one head.  O
   int32_t in, out;  // where the state comes from and goes to: a block of the workspace, or
 };
 constexpr int kPool = -1, kNone = -2;  // the caller's pool (zeros without one), or nowhere (zeros)
+template <bool kStates>
+__host__ __device__ constexpr int kv_stages() { return kStates ? 3 : 2; }
+template <bool kStates, bool kInline_>
 struct Small {
-  static constexpr bool kInline = false;  // of slow waits
+  static constexpr bool kInline = kInline_;  // slow waits
   float G[2][C];   // inclusive prefix sums of log2 g
   float d[2][C];   // 2^(sum of the log2 g behind the token), 0 past the end; with two V_d terms
                    // as 16-bit halves, C high ones and C low ones
-  float cf[C];     // 2^(G_e - G_j), e the last token of j's block of 16
+  float cf[kStates ? 4 : C];  // 2^(G_e - G_j), e the last token of j's block of 16
   int32_t mild[2]; // no block of 16 tokens decays by more than 2^-100
   float gamma[2];  // 2^(G_last); where the state is kept apart and the decay is slow, 2^(G_last) - 1 with the sign bit set
   alignas(16) uint32_t claim[4];  // the answer to a claim of another unit
+  int8_t v_exp[4][kVWarps];  // what the 16 values of each warp of V_d add is 2^v_exp times too large (the last four chunks)
   Rec rec[kRecs];
-  uint64_t q_full, q_empty, k_full[3], v_full[3], kv_empty[3];
+  uint64_t q_full, q_empty, k_full[kv_stages<kStates>()], v_full[kv_stages<kStates>()], kv_empty[kv_stages<kStates>()];
   uint64_t rec_full[kRecs], rec_empty[kRecs], claim_full;
   uint64_t gate_full[2], gate_empty[2], cf_empty;
   union {
@@ -148,20 +158,14 @@ struct Small {
   uint64_t o_stored, f_half, f_stored;          // warp 3
   uint64_t f_staged, si_full;                   // warps 12-15; an incoming 16-bit state
   uint64_t sf_full, sf_empty;                   // an incoming f32 state
-  uint64_t s_ready, vd_full[kVdSlots];         // warps 12-15, 16-23
-  uint64_t vd_empty[kVdSlots], drain;
+  uint64_t s_ready, vd_full[vd_slots<kStates>()];  // warps 12-15, 16-23
+  uint64_t vd_empty[vd_slots<kStates>()], drain;
   uint32_t tmem;
   int32_t abort;
 };
-struct SmallInline : Small { static constexpr bool kInline = true; };
-template <bool kWide>
-using SmallOf = std::conditional_t<apart<kWide>(), SmallInline, Small>;
-constexpr uint32_t kSmem = kOffSmall + sizeof(Small);
+constexpr uint32_t kSmem = kOffSmall + std::max({sizeof(Small<false, false>), sizeof(Small<false, true>), sizeof(Small<true, true>)});
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
 
-template <bool kStates>
-__host__ __device__ constexpr int kv_stages() { return kStates ? 3 : 2; }
-constexpr int kPoWarps = 8, kSWarps = 4, kVWarps = 8;
 constexpr int kThreads = 32 * (4 + kPoWarps + kSWarps + kVWarps);
 // Registers a thread: what a launch has, and how a launch that keeps the state apart shares them out among its
 // groups of four warps.  200 to 216 for the state are the fewest without spills; 176 to 216 measured within 2 %.
@@ -204,7 +208,8 @@ __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
 #pragma unroll 1
   for (int i = 0; i < kTries && !mbar_try_wait_sleep(bar, parity, 20000u); ++i) {}
 }
-__device__ __forceinline__ void give_up(const DecayPrefillParams& p, Small* sm) {
+template <class Sm>
+__device__ __forceinline__ void give_up(const DecayPrefillParams& p, Sm* sm) {
   *reinterpret_cast<volatile int32_t*>(&sm->abort) = 1;
   atomicOr(p.dev_err, kDevErrTimeout);
 }
@@ -236,7 +241,7 @@ __device__ __forceinline__ bool next_unit(Sm* sm, int u, int lane, Rec* r, bool*
 // ------------------------------------------------------------ units
 // kStates, here and below: the launch makes the states that the segments add, no outputs.  It walks a
 // segment from its last chunk to its first: with decays counted to the end of the segment, V_d^T K
-// of all chunks adds up in TMEM, and no state is read before the end.
+// of all chunks just adds up.
 template <bool kStates>
 __device__ __forceinline__ int64_t unit_count(const DecayPrefillParams& p) {
   return (int64_t)p.N * (kStates ? p.splits - 1 : p.splits) * p.H;
@@ -323,8 +328,8 @@ __device__ __forceinline__ void pass_on(const DecayPrefillParams& p, int h, int6
 }
 
 // ------------------------------------------------------------ warp 0: loads
-template <bool kStates, bool kWide, bool kClaim>
-__device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_t* base, SmallOf<kWide>* sm, int lane) {
+template <bool kStates, bool kWide, bool kClaim, class Sm>
+__device__ __forceinline__ void run_producer(const DecayPrefillParams& p, uint8_t* base, Sm* sm, int lane) {
   bool ok = true;
   int u = 0, ci = 0;  // units and chunks so far
   Ring<kStates> ring;
@@ -472,8 +477,8 @@ __device__ __forceinline__ void vd_place(int ci, int b, int* slot, int* round) {
   *round = kTerms == 3 && !kStates && *slot == 0 ? 2 * ci + (b >> 1) : ci;
 }
 
-template <bool F16, int kTerms, bool kStates, bool kWide>
-__device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* base, SmallOf<kWide>* sm, uint32_t tmem, int lane) {
+template <bool F16, int kTerms, bool kStates, bool kWide, class Sm>
+__device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* base, Sm* sm, uint32_t tmem, int lane) {
   constexpr int kSub = sub_tokens<kTerms>(), kSubs = C / kSub;
   const uint32_t id_kk = idesc_16_f32(F16, 128, 128, 0, 0, 0);  // B K-major
   const uint32_t id_kmn = idesc_16_f32(F16, 128, 128, 0, 1, 0); // B MN-major (its rows are summed over)
@@ -566,8 +571,8 @@ __device__ __forceinline__ void run_mma(const DecayPrefillParams& p, uint8_t* ba
 }
 
 // ------------------------------------------------------------ warp 2: gates
-template <bool F16, int kTerms, bool kStates, bool kWide>
-__device__ __forceinline__ void run_gates(const DecayPrefillParams& p, SmallOf<kWide>* sm, int lane) {
+template <bool F16, int kTerms, bool kStates, bool kWide, class Sm>
+__device__ __forceinline__ void run_gates(const DecayPrefillParams& p, Sm* sm, int lane) {
   bool failed = false;
   Rec r{};
   int ci = 0;
@@ -620,7 +625,7 @@ __device__ __forceinline__ void run_gates(const DecayPrefillParams& p, SmallOf<k
       *reinterpret_cast<float4*>(&sm->G[b][4 * lane]) = make_float4(pre[0], pre[1], pre[2], pre[3]);
       float d[4];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) d[e] = 4 * lane + e < left ? exp2f(suf[e]) : 0.f;
+      for (int e = 0; e < 4; ++e) d[e] = 4 * lane + e < left ? exp2f(suf[e]) * (lifted<F16, kWide>() ? float(1 << kDExp) : 1.f) : 0.f;
       if (kTerms == 2) {
         uint32_t* dh = reinterpret_cast<uint32_t*>(sm->d[b]) + 2 * lane;
         const uint32_t h0 = pack16x2<F16>(d[0], d[1]), h1 = pack16x2<F16>(d[2], d[3]);
@@ -652,8 +657,8 @@ __device__ __forceinline__ void run_gates(const DecayPrefillParams& p, SmallOf<k
 }
 
 // ------------------------------------------------------------ warp 3: output stores
-template <bool kWide>
-__device__ __forceinline__ void run_store(const DecayPrefillParams& p, uint8_t* base, SmallOf<kWide>* sm, int lane) {
+template <bool kWide, class Sm>
+__device__ __forceinline__ void run_store(const DecayPrefillParams& p, uint8_t* base, Sm* sm, int lane) {
   bool failed = false;
   Rec r;
   int ci = 0, outs = 0;  // tiles and parts of states that have gone out
@@ -700,8 +705,8 @@ __device__ __forceinline__ void run_store(const DecayPrefillParams& p, uint8_t* 
 }
 
 // ------------------------------------------------------------ warps 4-11: P and the output
-template <bool F16, bool kWide>
-__device__ __forceinline__ void run_po(const DecayPrefillParams& p, uint8_t* base, SmallOf<kWide>* sm, uint32_t tmem, int warp, int lane) {
+template <bool F16, bool kWide, class Sm>
+__device__ __forceinline__ void run_po(const DecayPrefillParams& p, uint8_t* base, Sm* sm, uint32_t tmem, int warp, int lane) {
   const int w = warp & 3, hf = (warp >> 2) - 1, row = 32 * w + lane;  // warps 4-11: columns 0 .. 63, 8-11: 64 .. 127
   const uint32_t tr = tmem + ((uint32_t)(32 * w) << 16);
   bool failed = false;
@@ -878,8 +883,8 @@ __device__ __forceinline__ void store_state32(void* base, int dtype, int64_t off
 }
 
 // a (d_hi + d_lo) for a pair of 16-bit values as lo - neg: neg is the rounded product of a and
-// -d_hi, lo the exact rest of it (a product of two 16-bit values has no more bits than two of
-// them hold) plus the product of a and d_lo.
+// -d_hi, lo the rest of it (exact where f16 reaches down to it: a product of two 16-bit values has no more
+// bits than two of them hold) plus the product of a and d_lo.
 template <bool F16>
 __device__ __forceinline__ void split_product(uint32_t a, uint32_t dh, uint32_t dl, uint32_t* neg, uint32_t* lo) {
   auto go = [&](auto x, auto h, auto mh, auto l) {
@@ -891,6 +896,25 @@ __device__ __forceinline__ void split_product(uint32_t a, uint32_t dh, uint32_t 
   uint32_t mh = dh ^ 0x80008000u;
   if (F16) go(*reinterpret_cast<__half2*>(&a), *reinterpret_cast<__half2*>(&dh), *reinterpret_cast<__half2*>(&mh), *reinterpret_cast<__half2*>(&dl));
   else go(*reinterpret_cast<__nv_bfloat162*>(&a), *reinterpret_cast<__nv_bfloat162*>(&dh), *reinterpret_cast<__nv_bfloat162*>(&mh), *reinterpret_cast<__nv_bfloat162*>(&dl));
+}
+
+// f16 does not reach far down: two terms hold 22 bits of products near 1, but of 1e-3 only 15.  So V_d of the 16 values
+// of a warp goes times the power of two that brings the largest value to 2 .. 4 (and d to 2^kDExp), and warps 12-15 take
+// it back when they add the chunk: an error of 2^-22 of the product, or 2^-39 of the largest value.  Values are
+// made larger and never smaller, d the other way round, so that neither loses bits.  Values of 1e-3: 8e-5 -> 2e-7 of
+// an f32 state; 32000 tokens of 8 heads 89 -> 93 us,
+// 16 x 4096 of 32 heads 348 -> 382.  (An f16 state does without: it has no more bits there than the two terms.)
+__device__ __forceinline__ int v_scale(uint32_t va, int m, int lr, int ch) {  // log2
+  __half2 most = __half2half2(__ushort_as_half(0));
+#pragma unroll 2
+  for (int tok = 0; tok < C; tok += 16) {
+    uint32_t a[4];
+    ldmatrix_x4_trans(va + sw128_chunk(tok + (m >> 1) * 8 + lr, ch & 7), a);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) most = __hmax2(most, __habs2(*reinterpret_cast<const __half2*>(&a[e])));
+  }
+  const int e = (int)(__reduce_max_sync(0xffffffffu, (uint32_t)__half_as_ushort(__hmax(__low2half(most), __high2half(most)))) >> 10);
+  return max(min(16 - e, 15), -14);
 }
 
 // Zero this warp's share of the rows past the end: 16 columns (two 16-byte chunks from ch0) of K, and of
@@ -908,8 +932,8 @@ __device__ __forceinline__ void zero_tails(uint8_t* k, uint8_t* v, int left, int
   __syncwarp();
 }
 
-template <bool F16, int kTerms, bool kStates, bool kWide>
-__device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* base, SmallOf<kWide>* sm, uint32_t tmem, int warp, int lane) {
+template <bool F16, int kTerms, bool kStates, bool kWide, class Sm>
+__device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* base, Sm* sm, uint32_t tmem, int warp, int lane) {
   const int w = warp & 3, row = 32 * w + lane;
   const uint32_t ts = tmem + ((uint32_t)(32 * w) << 16) + kTmS;
   uint8_t* sb = base + kOffS;
@@ -935,15 +959,16 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
   // S <- b S + (a S + what the chunk before added, from TMEM); with `copy`, also in 16 bits to where Q S^T reads it
   float2 S[apart<kWide>() ? D / 2 : 1];
   float sa = 0.f, keep = 0.f;  // a and b
-  auto add_chunk = [&](uint32_t from, bool copy) {
-    const float2 a2 = pair(sa), b2 = pair(keep);
+  auto add_chunk = [&](uint32_t from, int v_exp, bool copy) {
+    const float2 a2 = pair(sa), b2 = pair(keep), f2 = pair(__int_as_float((127 - v_exp) << 23));
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       uint32_t x[32];
       tmem_ld32(from + 32 * q, x);
       tmem_ld_wait();
 #pragma unroll
-      for (int e = 0; e < 16; ++e) S[16 * q + e] = fma2(b2, S[16 * q + e], fma2(a2, S[16 * q + e], pair_at(x + 2 * e)));
+      for (int e = 0; e < 16; ++e)
+        S[16 * q + e] = fma2(b2, S[16 * q + e], fma2(a2, S[16 * q + e], lifted<F16, kWide>() ? mul2(f2, pair_at(x + 2 * e)) : pair_at(x + 2 * e)));
       if (copy) {
 #pragma unroll
         for (int e = 0; e < 4; ++e)
@@ -953,6 +978,7 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
       }
     }
   };
+  auto v_exp = [&](int chunk) { return lifted<F16, kWide>() ? (int)sm->v_exp[chunk & 3][2 * w + (lane >> 4)] : 0; };
   auto zero = [&] {
 #pragma unroll
     for (int e = 0; e < D / 2; ++e) S[e] = make_float2(0.f, 0.f);
@@ -976,7 +1002,7 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
       tc_fence_after();
       if (c == 0) zero();
       keep = 1.f;
-      add_chunk(ts + (sum_col<kStates>(ci) - kTmS), false);
+      add_chunk(ts + (sum_col<kStates>(ci) - kTmS), v_exp(ci), false);
       if (c + 1 == r.nch) continue;
       tc_fence_before();
       warp_arrive(&sm->sum_free[ci & 1], lane);
@@ -1045,7 +1071,7 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
           tmem_st_wait();
           zero();
         }
-        add_chunk(ts, !direct);
+        add_chunk(ts, c == 0 ? 0 : v_exp(ci - 1), !direct);
         sa = sm->gamma[st];
         keep = __float_as_int(sa) < 0 ? 1.f : 0.f;
       }
@@ -1064,7 +1090,7 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
     tc_fence_after();
     const uint32_t last = ts + (sum_col<kStates>(ci - 1) - kTmS);
     if (apart<kWide>()) {
-      if (!kStates) add_chunk(last, false);
+      if (!kStates) add_chunk(last, v_exp(ci - 1), false);
       put_back(last);
     }
     if (!kStates && kWide && state_out_tma(p, r) && p.sout_dtype == kF32) {
@@ -1164,9 +1190,10 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
 // ------------------------------------------------------------ warps 16-23: V_d
 // Transposed fragments of V (pairs of tokens, one value each) times d, as kTerms 16-bit terms, 16
 // values a warp.  Where only states are made, the warps of P do the same, every other part.
-template <bool F16, int kTerms, bool kStates, bool kWide>
-__device__ __forceinline__ void run_v(const DecayPrefillParams& p, uint8_t* base, SmallOf<kWide>* sm, uint32_t tmem, int warp, int lane) {
+template <bool F16, int kTerms, bool kStates, bool kWide, class Sm>
+__device__ __forceinline__ void run_v(const DecayPrefillParams& p, uint8_t* base, Sm* sm, uint32_t tmem, int warp, int lane) {
   constexpr int kSub = sub_tokens<kTerms>(), kSubs = C / kSub, kGroups = kStates ? 2 : 1;
+  constexpr bool kLifted = lifted<F16, kWide>();
   const int w = warp & 3, hf = (warp >> 2) & 1, group = kStates && warp < 4 + kPoWarps ? 1 : 0;
   const uint32_t tq = tmem + ((uint32_t)(32 * w + 16 * hf) << 16);
   const int m = lane >> 3, lr = lane & 7;
@@ -1185,9 +1212,15 @@ __device__ __forceinline__ void run_v(const DecayPrefillParams& p, uint8_t* base
       uint8_t* k = base + kOffKv + kv * 2 * kTile;
       if (left < C) {
         if (!wait(sm, &sm->k_full[kv], ph)) { failed = true; break; }
-        zero_tails<kSub, kGroups>(k, k + kTile, left, 4 * w + 2 * hf, group, lane);
+        zero_tails<kSub, kLifted ? 1 : kGroups>(k, k + kTile, left, 4 * w + 2 * hf, kLifted ? 0 : group, lane);
       }
       const uint32_t va = smem_u32(k + kTile) + (ch >> 3) * kHalf;
+      const int up = kLifted ? v_scale(va, m, lr, ch) : 0;
+      const __half2 scale = __half2half2(__ushort_as_half((unsigned short)((up + 15) << 10)));
+      auto scaled = [&](uint32_t x) {
+        const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&x), scale);
+        return *reinterpret_cast<const uint32_t*>(&y);
+      };
 #pragma unroll 1
       for (int sub = group; sub < kSubs; sub += kGroups) {
         int slot, round;
@@ -1196,6 +1229,8 @@ __device__ __forceinline__ void run_v(const DecayPrefillParams& p, uint8_t* base
               (kStates || slot != 1 || wait(sm, &sm->qs_done, ci & 1)) &&
               (kStates || slot != 2 || wait(sm, &sm->cf_empty, ci & 1)))) { failed = true; break; }
         tc_fence_after();
+        // behind a wait for a product that added this chunk's predecessor, so that what was here has been read
+        if (kLifted && sub == 0 && lane == 0) sm->v_exp[ci & 3][2 * w + hf] = (int8_t)(up + kDExp);
 #pragma unroll 2
         for (int tt = 0; tt < kSub / 16; ++tt) {
           const int tok = sub * kSub + 16 * tt;  // 16 tokens from here
@@ -1206,9 +1241,18 @@ __device__ __forceinline__ void run_v(const DecayPrefillParams& p, uint8_t* base
           if (kTerms == 2) {
             // three packed 16-bit operations
             const uint32_t* dh = reinterpret_cast<const uint32_t*>(sm->d[st]) + at2;
-            uint32_t rest[4];
+            uint32_t rest[4], h[2] = {dh[0], dh[4]}, l[2] = {dh[C / 2], dh[C / 2 + 4]};
+            if (kLifted) {
+              if (up > 0) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) split_product<F16>(a[e], dh[2 * (e & 2)], dh[C / 2 + 2 * (e & 2)], &t[e], &rest[e]);
+                for (int e = 0; e < 4; ++e) a[e] = scaled(a[e]);
+              } else if (up < 0) {
+#pragma unroll
+                for (int e = 0; e < 2; ++e) { h[e] = scaled(h[e]); l[e] = scaled(l[e]); }
+              }
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) split_product<F16>(a[e], h[e >> 1], l[e >> 1], &t[e], &rest[e]);
             tmem_st16x128_x2(to, t);
             tmem_st16x128_x2(to + kSub / 2, rest);
           } else {
@@ -1243,7 +1287,8 @@ __device__ __forceinline__ void run_v(const DecayPrefillParams& p, uint8_t* base
 template <bool F16, int kTerms, bool kStates, bool kWide, bool kClaim>
 __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __grid_constant__ DecayPrefillParams p) {
   extern __shared__ __align__(1024) uint8_t base[];
-  SmallOf<kWide>* sm = reinterpret_cast<SmallOf<kWide>*>(base + kOffSmall);
+  using Sm = Small<kStates, apart<kWide>()>;
+  Sm* sm = reinterpret_cast<Sm*>(base + kOffSmall);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     auto init = [](uint64_t* bar, int n, int count) {
@@ -1251,9 +1296,9 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __
     };
     init(&sm->q_full, 1, 1);
     init(&sm->q_empty, 1, kPoWarps);
-    init(sm->k_full, 3, 1);
-    init(sm->v_full, 3, 1);
-    init(sm->kv_empty, 3, 1);
+    init(sm->k_full, kv_stages<kStates>(), 1);
+    init(sm->v_full, kv_stages<kStates>(), 1);
+    init(sm->kv_empty, kv_stages<kStates>(), 1);
     init(sm->rec_full, kRecs, 1);
     init(sm->rec_empty, kRecs, (kStates ? 2 : 3) + kPoWarps + kSWarps + kVWarps);
     init(sm->gate_full, 2, 1);
@@ -1281,8 +1326,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __
     init(&sm->sf_full, 1, 1);
     init(&sm->sf_empty, 1, kSWarps);
     init(&sm->s_ready, 1, kSWarps);
-    init(sm->vd_full, kVdSlots, kVWarps);
-    init(sm->vd_empty, kVdSlots, 1);
+    init(sm->vd_full, vd_slots<kStates>(), kVWarps);
+    init(sm->vd_empty, vd_slots<kStates>(), 1);
     init(&sm->drain, 1, 1);
     sm->abort = 0;
     fence_mbar_init();
@@ -1412,8 +1457,9 @@ cudaError_t launch(const DecayPrefillParams& p, cudaStream_t stream) {
       if (e != cudaSuccess) return e;
     }
   }
-  if constexpr (kTerms == 2) {
-    const bool wide = p.splits > 1 || (p.s_in && p.sin_dtype == kF32) || (p.s_out && p.sout_dtype == kF32);
+  if constexpr (kTerms == 2) {  // three terms are for a state that stays in f32, whether it is asked for or not
+    // f16 inputs: a bf16 state takes the way of f32 ones, as it holds more of small values than f16 does
+    const bool wide = p.splits > 1 || (p.s_in && p.sin_dtype == kF32) || (p.s_out && (p.sout_dtype == kF32 || (F16 && p.sout_dtype == kBF16)));
     if (!wide) return launch_pass<F16, kTerms, false, false>(p, sms, stream);
   }
   return launch_pass<F16, kTerms, false, true>(p, sms, stream);

@@ -106,3 +106,33 @@ def test_sparse_keys(invariant):
     q, k, v, _, _ = R.make([T], len(DECAYS), len(DECAYS), gate="none", seed=64)
     k[torch.arange(T, device="cuda") % 700 != 5] = 0
     each_head(final_state(q, k, v, g, batch_invariant=invariant)[0], summed(k, v, g), "sparse")
+
+
+@pytest.mark.parametrize("T,splits", [(5, 1), (700, 1), (3000, 1), (3000, 4)])
+@pytest.mark.parametrize("std", [1e4, 1e-2, 1e-3, 1e-4, 1e-6])
+def test_f16_values_of_any_size(force_split, std, T, splits):
+    """f16 values far from 1, next to the smallest (2^-24) and the largest there are, also where the last tokens of
+    a chunk are zeros and only decayed ones count, and with a first row of heads that is a thousand times larger."""
+    force_split(splits)
+    for gate in ("token", "slow", "none"):
+        q, k, v, g, _ = R.make([T], 2, 2, HF, gate, seed=65)
+        v = (v.float() * std).clamp(-6e4, 6e4).to(HF)
+        each_head(final_state(q, k, v, g)[0], summed(k, v, g), (gate, "all"))
+        v[:, 1, ::16] = (v[:, 1, ::16].float() * 1e3).clamp(-6e4, 6e4).to(HF)
+        got, want = final_state(q, k, v, g)[0], summed(k, v, g)
+        each_head(got, want, (gate, "rows"))
+        small = torch.arange(128, device="cuda") % 16 != 0
+        assert R.rel(got[1, small], want[1, small]) <= R.STATE[F32], (gate, R.rel(got[1, small], want[1, small]))
+        v[torch.arange(T, device="cuda") % 128 > 118] = 0
+        each_head(final_state(q, k, v, g)[0], summed(k, v, g), (gate, "zeros"))
+
+
+@pytest.mark.parametrize("state,std", [(HF, 3.0), (HF, 1e-2), (BF, 3.0), (BF, 1e-2), (BF, 1e-5)], ids=str)
+def test_f16_values_into_16_bit_states(state, std):
+    q, k, v, g, cu = R.make([700], 2, 2, HF, "token", seed=66)
+    v = (v.float() * std).to(HF)
+    final = torch.empty(1, 2, 128, 128, dtype=state, device="cuda")
+    gdn.decay_linear_attention(q, k, v, g, output_final_state=True, cu_seqlens=cu, output_state=final)
+    want = summed(k, v, g)
+    for h in range(2):
+        assert R.rel(final[0, h], want[h]) <= R.STATE[state], (h, R.rel(final[0, h], want[h]))
