@@ -405,6 +405,19 @@ gdn_status_t ensure_workspace(DeviceState& d, size_t bytes, cudaStream_t stream)
   return GDN_OK;
 }
 
+// The current device, its context bound to the calling thread: a thread that has made no call of the runtime
+// that needs a context has none, and the tensor maps' encoder, a call of the driver, would fail there.
+gdn_status_t bind_device(int* dev) {
+  static thread_local int bound = -1, generation = -1;
+  cudaError_t e = cudaGetDevice(dev);
+  const int gen = gdn::launch_config_generation();
+  if (e == cudaSuccess && (bound != *dev || generation != gen)) {
+    e = cudaSetDevice(*dev);
+    if (e == cudaSuccess) { bound = *dev; generation = gen; }
+  }
+  return e == cudaSuccess ? GDN_OK : fail(GDN_ERR_CUDA, "the current device: %s", cudaGetErrorString(e));
+}
+
 // Set-up of the allocation-free entry point on the current device: the device
 // checks, the tensor-map encoder and the address of the static scratch, once.
 struct NoAllocState {
@@ -414,17 +427,16 @@ struct NoAllocState {
 NoAllocState g_na[kMaxDevices];
 
 gdn_status_t noalloc_device(int* dev) {
-  cudaError_t e = cudaGetDevice(dev);
-  if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
+  gdn_status_t st = bind_device(dev);
+  if (st != GDN_OK) return st;
   if (*dev < 0 || *dev >= kMaxDevices) return fail(GDN_ERR_INVALID_ARGUMENT, "device %d out of range", *dev);
   std::lock_guard<std::mutex> lk(g_mu);
   NoAllocState& d = g_na[*dev];
   if (d.ready) return GDN_OK;
-  gdn_status_t st = check_device(*dev);
-  if (st != GDN_OK) return st;
+  if ((st = check_device(*dev)) != GDN_OK) return st;
   if ((st = ensure_encode()) != GDN_OK) return st;
   void* base = nullptr;
-  e = gdn::noalloc_scratch(&base);
+  cudaError_t e = gdn::noalloc_scratch(&base);
   if (e != cudaSuccess || !base)
     return fail(GDN_ERR_CUDA, "static scratch address (cudaGetSymbolAddress): %s", cudaGetErrorString(e));
   d.scratch = static_cast<uint8_t*>(base);
@@ -433,9 +445,8 @@ gdn_status_t noalloc_device(int* dev) {
 }
 
 gdn_status_t current_device(int* dev) {
-  cudaError_t e = cudaGetDevice(dev);
-  if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "cudaGetDevice: %s", cudaGetErrorString(e));
-  return init_device(*dev);
+  const gdn_status_t st = bind_device(dev);
+  return st == GDN_OK ? init_device(*dev) : st;
 }
 
 // Both prefill entry points.  `noalloc` selects the static scratch (and
