@@ -407,6 +407,10 @@ def decay_linear_attention(q, k, v, g=None, scale: Optional[float] = None, initi
     ``o_t = scale S_t q_t`` (``include/gdn.h``, gdn_decay_prefill).  Arguments, defaults and
     results are those of :func:`chunk_gated_delta_rule`; ``g`` is ``[T, H]``, or ``[H]`` for
     one decay for each head.
+
+    Without ``batch_invariant`` few long sequences are cut into segments, whose states are in a
+    workspace of the device.  Such calls run one after the other even on different streams; replays of a graph
+    that holds one must not run concurrently with others.
     """
     if cu_seqlens is None:
         raise ValueError("cu_seqlens is required")

@@ -15,6 +15,7 @@
 #include <cstdio>
 #include <cstring>
 #include <mutex>
+#include <vector>
 
 #include "decay.h"
 #include "decode.h"
@@ -38,6 +39,10 @@ struct DeviceState {
   int32_t* dev_err = nullptr;  // device error word
   float* ws = nullptr;         // split-K workspace (grow-only, stream-ordered allocation)
   size_t ws_bytes = 0;
+  cudaEvent_t ws_done = nullptr;  // behind the last work that was given the workspace (ws_used)
+  bool ws_used = false;
+  bool ws_in_graph = false;       // a captured call holds its address: it is kept, not freed, when a larger one takes over
+  std::vector<void*> ws_kept;
 };
 DeviceState g_dev[kMaxDevices];
 std::mutex g_mu;
@@ -379,31 +384,64 @@ SplitPlan choose_splits(int64_t N, int64_t H, int64_t T, int sms) {
   return pl;
 }
 
-gdn_status_t ensure_workspace(DeviceState& d, size_t bytes, cudaStream_t stream) {
-  if (bytes <= d.ws_bytes) return GDN_OK;
-  // An allocation made while the stream is being captured would belong to the graph
-  // (valid only while it runs), not to this library: the caller has to reserve first.
-  cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
-  cudaError_t ce = cudaStreamIsCapturing(stream, &cap);
-  if (ce != cudaSuccess) return fail(GDN_ERR_CUDA, "cudaStreamIsCapturing: %s", cudaGetErrorString(ce));
-  if (cap != cudaStreamCaptureStatusNone)
-    return fail(GDN_ERR_UNSUPPORTED,
-                "split-K needs %zu B of workspace but %zu B are reserved and the stream is being "
-                "captured: call gdn_reserve_workspace before the capture",
-                bytes, d.ws_bytes);
-  if (d.ws) {
-    cudaError_t e = cudaFreeAsync(d.ws, stream);
-    d.ws = nullptr;
-    d.ws_bytes = 0;
-    if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "split-K workspace release: %s", cudaGetErrorString(e));
+// The workspace for one call, from `take` to the end of the scope that enqueues its kernels: no other thread gets
+// it meanwhile, and the next call's work, on whatever stream, comes behind this one's.  A stream that is being
+// captured neither waits nor is waited for (an event of one side means nothing on the other).
+class Workspace {
+ public:
+  gdn_status_t take(DeviceState& d, size_t bytes, cudaStream_t stream, bool* grown = nullptr) {
+    lock_ = std::unique_lock<std::mutex>(g_mu);
+    cudaStreamCaptureStatus cap = cudaStreamCaptureStatusNone;
+    cudaError_t e = cudaStreamIsCapturing(stream, &cap);
+    if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "cudaStreamIsCapturing: %s", cudaGetErrorString(e));
+    const bool capturing = cap != cudaStreamCaptureStatusNone;
+    // An allocation made while the stream is being captured would belong to the graph
+    // (valid only while it runs), not to this library: the caller has to reserve first.
+    if (bytes > d.ws_bytes && capturing)
+      return fail(GDN_ERR_UNSUPPORTED,
+                  "split-K needs %zu B of workspace but %zu B are reserved and the stream is being "
+                  "captured: call gdn_reserve_workspace before the capture",
+                  bytes, d.ws_bytes);
+    if (capturing) {
+      d.ws_in_graph = true;
+      return GDN_OK;
+    }
+    if (!d.ws_done) e = cudaEventCreateWithFlags(&d.ws_done, cudaEventDisableTiming);
+    if (e == cudaSuccess && d.ws_used) e = cudaStreamWaitEvent(stream, d.ws_done, 0);
+    if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "split-K workspace order: %s", cudaGetErrorString(e));
+    d_ = &d;
+    stream_ = stream;
+    if (bytes <= d.ws_bytes) return GDN_OK;
+    if (d.ws) {
+      if (d.ws_in_graph) d.ws_kept.push_back(d.ws);
+      else e = cudaFreeAsync(d.ws, stream);
+      d.ws = nullptr;
+      d.ws_bytes = 0;
+      d.ws_in_graph = false;
+      if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "split-K workspace release: %s", cudaGetErrorString(e));
+    }
+    void* ptr = nullptr;
+    e = cudaMallocAsync(&ptr, bytes, stream);
+    if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "split-K workspace (%zu B): %s", bytes, cudaGetErrorString(e));
+    d.ws = static_cast<float*>(ptr);
+    d.ws_bytes = bytes;
+    if (grown) *grown = true;
+    return GDN_OK;
   }
-  void* ptr = nullptr;
-  cudaError_t e = cudaMallocAsync(&ptr, bytes, stream);
-  if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "split-K workspace (%zu B): %s", bytes, cudaGetErrorString(e));
-  d.ws = static_cast<float*>(ptr);
-  d.ws_bytes = bytes;
-  return GDN_OK;
-}
+  Workspace() = default;
+  Workspace(const Workspace&) = delete;
+  Workspace& operator=(const Workspace&) = delete;
+  ~Workspace() {
+    // without the event the next call on another stream would not wait: better that this one has ended
+    if (d_ && cudaEventRecord(d_->ws_done, stream_) != cudaSuccess) cudaStreamSynchronize(stream_);
+    if (d_) d_->ws_used = true;
+  }
+
+ private:
+  std::unique_lock<std::mutex> lock_;
+  DeviceState* d_ = nullptr;
+  cudaStream_t stream_ = nullptr;
+};
 
 // The current device, its context bound to the calling thread: a thread that has made no call of the runtime
 // that needs a context has none, and the tensor maps' encoder, a call of the driver, would fail there.
@@ -592,6 +630,7 @@ gdn_status_t chunk_prefill(const gdn_tensor_t* q, const gdn_tensor_t* k, const g
     return GDN_OK;
   }
   // split-K: pass 1 (segment 0 + middle-segment maps), fix-up, pass 2 (segments 1..P-1)
+  Workspace workspace;
   const size_t ws_bytes = size_t(N * H) * size_t(gdn::split_ws_blocks(P)) * 65536;
   if (noalloc) {
     if (ws_bytes > gdn::kNoAllocWorkspaceBytes)
@@ -601,8 +640,7 @@ gdn_status_t chunk_prefill(const gdn_tensor_t* q, const gdn_tensor_t* k, const g
                   P, ws_bytes, gdn::kNoAllocWorkspaceBytes);
     p.ws = reinterpret_cast<float*>(g_na[dev].scratch + gdn::kNoAllocHeaderBytes);
   } else {
-    std::lock_guard<std::mutex> lk(g_mu);
-    if ((st = ensure_workspace(g_dev[dev], ws_bytes, stream)) != GDN_OK) return st;
+    if ((st = workspace.take(g_dev[dev], ws_bytes, stream)) != GDN_OK) return st;
     p.ws = g_dev[dev].ws;
   }
   p.splits = P;
@@ -940,10 +978,9 @@ gdn_status_t gdn_decay_prefill(const gdn_tensor_t* q, const gdn_tensor_t* k, con
   p.scale = (scale == 0.0f) ? 1.0f / std::sqrt(128.0f) : scale;
   p.op_f16 = q->dtype == GDN_F16 ? 1 : 0;
   p.splits = batch_invariant ? 1 : decay_plan(N, s.H, s.rows, gdn::device_sm_count());
-  std::unique_lock<std::mutex> lk(g_mu, std::defer_lock);
-  if (p.splits > 1) {  // held to the launch, so that no other thread's call replaces the workspace before it
-    lk.lock();
-    if ((st = ensure_workspace(g_dev[dev], decay_ws_bytes(N, s.H, p.splits), stream)) != GDN_OK) return st;
+  Workspace workspace;
+  if (p.splits > 1) {
+    if ((st = workspace.take(g_dev[dev], decay_ws_bytes(N, s.H, p.splits), stream)) != GDN_OK) return st;
     p.ws = g_dev[dev].ws;
     p.ws_decay = p.ws + N * s.H * (p.splits - 1) * 16384;
     if (!encode_f32_states(&p.tm_ws, p.ws, 1, N * s.H * (p.splits - 1), 16384, 16384))
@@ -1004,8 +1041,12 @@ gdn_status_t gdn_reserve_workspace(size_t bytes, cudaStream_t stream) {
   int dev = 0;
   gdn_status_t st = current_device(&dev);
   if (st != GDN_OK) return st;
-  std::lock_guard<std::mutex> lk(g_mu);
-  return ensure_workspace(g_dev[dev], bytes, stream);
+  Workspace workspace;
+  bool grown = false;
+  if ((st = workspace.take(g_dev[dev], bytes, stream, &grown)) != GDN_OK) return st;
+  // replays of a graph that is captured next do not wait for the event, so the new block has to be there
+  cudaError_t e = grown ? cudaStreamSynchronize(stream) : cudaSuccess;
+  return e == cudaSuccess ? GDN_OK : fail(GDN_ERR_CUDA, "split-K workspace: %s", cudaGetErrorString(e));
 }
 
 size_t gdn_split_workspace_bytes(int64_t num_seqs, int64_t num_sab_heads, int splits) {
@@ -1085,10 +1126,12 @@ void gdn_shutdown(void) {
   int prev = -1;
   cudaGetDevice(&prev);
   for (int d = 0; d < kMaxDevices; ++d) {
-    if (g_dev[d].dev_err || g_dev[d].ws) {
+    if (g_dev[d].dev_err || g_dev[d].ws || g_dev[d].ws_done || !g_dev[d].ws_kept.empty()) {
       cudaSetDevice(d);
       if (g_dev[d].dev_err) cudaFree(g_dev[d].dev_err);
       if (g_dev[d].ws) cudaFree(g_dev[d].ws);
+      for (void* kept : g_dev[d].ws_kept) cudaFree(kept);
+      if (g_dev[d].ws_done) cudaEventDestroy(g_dev[d].ws_done);
     }
     g_dev[d] = DeviceState();
     g_na[d] = NoAllocState();  // the static scratch's address is looked up again (it lives as long as the context)

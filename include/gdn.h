@@ -136,11 +136,15 @@ gdn_status_t gdn_init(int device);
  *                 batch but not bit-identical across batchings.  The maps live in a
  *                 library-owned workspace of N * H * (3P - 5) * 64 KiB per device,
  *                 grown with cudaMallocAsync on `stream` (the old one released with
- *                 cudaFreeAsync) and freed by gdn_shutdown(); split calls on two
- *                 streams of one device must not run concurrently.  While `stream`
+ *                 cudaFreeAsync) and freed by gdn_shutdown().  It is one per device:
+ *                 the work of a split call comes behind that of the split call before
+ *                 it, on whatever stream that was (an event).  While `stream`
  *                 is being captured into a CUDA graph the workspace is not grown:
  *                 the call fails with GDN_ERR_UNSUPPORTED unless
- *                 gdn_reserve_workspace made it large enough beforehand.
+ *                 gdn_reserve_workspace made it large enough beforehand.  Replays of
+ *                 such a graph are not ordered by the library: they must not run
+ *                 concurrently with other split calls or replays.  A block that a
+ *                 captured call uses stays allocated until gdn_shutdown().
  *                 gdn_testing_force_splits forces P, for tests.
  *  output         [T, H, 128] in q's dtype, innermost contiguous, written in place.  Must
  *                 not overlap q, k, v or the states (GDN_ERR_ALIAS).
@@ -250,7 +254,7 @@ gdn_status_t gdn_chunk_prefill_noalloc(const gdn_tensor_t* q, const gdn_tensor_t
  *
  * gdn_reserve_workspace: grow the current device's split-K workspace to at least
  * `bytes` now, with cudaMallocAsync on `stream` (the previous block released with
- * cudaFreeAsync on the same stream), so that later gdn_chunk_prefill calls with
+ * cudaFreeAsync on the same stream), and wait for that, so that later gdn_chunk_prefill calls with
  * batch_invariant = 0 allocate nothing -- for instance while a CUDA graph is being
  * captured, when the library refuses to grow it (GDN_ERR_UNSUPPORTED).  The workspace
  * is owned by the library, never shrinks, and is freed by gdn_shutdown.  Returns
@@ -316,7 +320,7 @@ gdn_status_t gdn_qk_norm_rope(const gdn_tensor_t* q, const gdn_tensor_t* k, cons
  *                   segments add, their join, and the outputs of all segments.  Results are
  *                   the same for every run, not the same bits as without.  The
  *                   states live in the workspace that gdn_chunk_prefill's split calls use,
- *                   under the same rules (growth, stream capture, one stream at a time);
+ *                   under the same rules (growth, order among streams, stream capture);
  *                   gdn_testing_force_splits forces the count here, too.
  *
  * gdn_decay_workspace_bytes: the workspace of such a call of `num_seqs` sequences,
