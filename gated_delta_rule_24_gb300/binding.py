@@ -1,4 +1,4 @@
-"""Thin binding of the C ABI in ``include/gdn.h``, by ctypes and (three operators) a small extension.
+"""Thin binding of the C ABI in ``include/gdn.h``, by ctypes and (three operators, where it is there) a small extension.
 
 Only argument marshalling happens here: torch tensors are described to the
 library (pointer, dtype, shape, strides) and every step of the computation runs
@@ -76,6 +76,12 @@ def load_library():
         lib.gdn_split_workspace_bytes.restype = ctypes.c_size_t
         lib.gdn_decode_step.argtypes = [P, P, P, P, P, ctypes.c_float, P, P, ctypes.c_int, P, ctypes.c_void_p]
         lib.gdn_decode_step.restype = ctypes.c_int
+        lib.gdn_qk_norm_rope.argtypes = [P, P, P, P, ctypes.c_float, ctypes.c_float, P, P, ctypes.c_int, P, P, ctypes.c_void_p]
+        lib.gdn_qk_norm_rope.restype = ctypes.c_int
+        lib.gdn_decay_prefill.argtypes = [P, P, P, P, ctypes.c_float, P, P, P, P, ctypes.c_int, P, ctypes.c_void_p]
+        lib.gdn_decay_prefill.restype = ctypes.c_int
+        lib.gdn_decay_step.argtypes = [P, P, P, P, ctypes.c_float, P, P, P, ctypes.c_void_p]
+        lib.gdn_decay_step.restype = ctypes.c_int
         lib.gdn_decay_workspace_bytes.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64,
                                                   ctypes.c_int]
         lib.gdn_decay_workspace_bytes.restype = ctypes.c_size_t
@@ -92,7 +98,6 @@ def load_library():
         lib.gdn_testing_split_plan.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_int64, ctypes.c_int,
                                                ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int64]
         lib.gdn_testing_split_plan.restype = ctypes.c_int
-        _calls.load(lib)
         _lib = lib
     return _lib
 
@@ -116,26 +121,57 @@ def describe(t: Optional[torch.Tensor]):
 
 
 class _PyCall:
-    """The extension ``csrc/pycall.c``, for the operators whose smallest calls take a few
-    microseconds on the GPU: ``qk_norm_rope``, ``decay_prefill`` and ``decay_step`` with the
-    arguments of the C functions (the last two also with whether the gate may be ``[H]``, one decay
-    for each head), tensors described on the way, and ``fill``, the addresses of
-    descriptors alone.  Loaded with the library, at the first use."""
-
-    def load(self, lib):
-        loader = importlib.machinery.ExtensionFileLoader("gdn_pycall", _PYCALL_PATH)
-        module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("gdn_pycall", _PYCALL_PATH, loader=loader))
-        loader.exec_module(module)
-        module.bind(_DTYPES, *(ctypes.cast(getattr(lib, "gdn_" + name), ctypes.c_void_p).value
-                               for name in ("qk_norm_rope", "decay_prefill", "decay_step")))
-        for name in ("qk_norm_rope", "decay_prefill", "decay_step", "fill"):
-            setattr(self, name, getattr(module, name))
+    """The operators whose smallest calls take a few microseconds on the GPU: ``qk_norm_rope``,
+    ``decay_prefill`` and ``decay_step`` with the arguments of the C functions (the last two also with
+    whether the gate may be ``[H]``, one decay for each head), tensors described on the way.  At the
+    first use they are taken from the extension ``csrc/pycall.c``, with ``fill``, the addresses of
+    descriptors alone; where it was not built or does not load, they go by ctypes as all others do."""
 
     def __getattr__(self, name):
         if name not in ("qk_norm_rope", "decay_prefill", "decay_step", "fill"):
             raise AttributeError(name)
-        load_library()
+        lib = load_library()
+        try:
+            loader = importlib.machinery.ExtensionFileLoader("gdn_pycall", _PYCALL_PATH)
+            module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("gdn_pycall", _PYCALL_PATH, loader=loader))
+            loader.exec_module(module)
+            module.bind(_DTYPES, *(ctypes.cast(getattr(lib, "gdn_" + name), ctypes.c_void_p).value
+                                   for name in ("qk_norm_rope", "decay_prefill", "decay_step")))
+        except (ImportError, OSError):
+            module = _ByCtypes(lib)
+        for each in ("qk_norm_rope", "decay_prefill", "decay_step", "fill"):
+            setattr(self, each, getattr(module, each))
         return self.__dict__[name]
+
+
+class _ByCtypes:
+    def __init__(self, lib):
+        self._lib = lib
+
+    def fill(self, *tensors):
+        raise RuntimeError(f"{_PYCALL_PATH} was not built")
+
+    def qk_norm_rope(self, q, k, q_weight, k_weight, weight_offset, eps, cos_sin, positions, interleaved, q_out, k_out, stream):
+        return self._lib.gdn_qk_norm_rope(*_described(q, k, q_weight, k_weight), weight_offset + 0.0, eps + 0.0,
+                                          *_described(cos_sin, positions), bool(interleaved), *_described(q_out, k_out), stream)
+
+    def decay_prefill(self, q, k, v, g, scale, initial_state, state_indices, output_state, cu_seqlens, batch_invariant, output,
+                      stream, head_gate):
+        return self._lib.gdn_decay_prefill(*_described(q, k, v, _gate_rows(q, g, head_gate)), scale + 0.0,
+                                           *_described(initial_state, state_indices, output_state, cu_seqlens),
+                                           bool(batch_invariant), *_described(output), stream)
+
+    def decay_step(self, q, k, v, g, scale, state, state_indices, output, stream, head_gate):
+        return self._lib.gdn_decay_step(*_described(q, k, v, _gate_rows(q, g, head_gate)), scale + 0.0,
+                                        *_described(state, state_indices, output), stream)
+
+
+def _described(*tensors):
+    return [_ref(describe(t)) for t in tensors]
+
+
+def _gate_rows(q, g, head_gate):
+    return g.expand(q.shape[0], -1) if head_gate and q is not None and g is not None and g.dim() == 1 else g
 
 
 _calls = _descriptors = _PyCall()

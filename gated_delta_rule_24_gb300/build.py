@@ -2,7 +2,9 @@
 binding's extension ``_build/gdn_pycall.so`` beside it.
 
 Each translation unit is compiled by nvcc in parallel, then linked; a rebuild
-happens only when a source or header is newer than the library or the extension.
+happens only when a source or header is newer than what is made of it.  The extension makes calls
+lighter for the host and nothing else: where it cannot be built (no Python headers), the binding does
+without.
 """
 from __future__ import annotations
 
@@ -11,6 +13,7 @@ import os
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -32,30 +35,42 @@ def _nvcc() -> str:
     return cand if os.path.exists(cand) else "nvcc"
 
 
-def _stale() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(PYCALL):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(PYCALL))
-    deps = [os.path.join(CSRC, s) for s in SOURCES] + HEADERS + [PYCALL_SOURCE]
-    return any(os.path.getmtime(d) > t for d in deps)
+def _stale(made, deps) -> bool:
+    return not os.path.exists(made) or any(os.path.getmtime(d) > os.path.getmtime(made) for d in deps)
 
 
 def _build_pycall() -> None:
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     tmp = PYCALL + f".tmp{os.getpid()}"
-    r = subprocess.run(["gcc", "-O2", "-std=c11", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
-                        "-I", os.path.join(cuda, "include"), PYCALL_SOURCE, "-o", tmp], capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"gcc failed on {PYCALL_SOURCE}:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, PYCALL)
+    try:
+        r = subprocess.run(["gcc", "-O2", "-std=c11", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
+                            "-I", os.path.join(cuda, "include"), PYCALL_SOURCE, "-o", tmp], capture_output=True, text=True)
+        failed = r.returncode and f"gcc failed on {PYCALL_SOURCE}:\n{r.stdout}\n{r.stderr}"
+    except OSError as e:
+        failed = str(e)
+    if not failed:
+        os.replace(tmp, PYCALL)
+        return
+    if os.path.exists(PYCALL):  # of an older source
+        os.remove(PYCALL)
+    warnings.warn(f"calls of the decay operators will take the host longer: no {PYCALL}: {failed}")
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
-    if not force and not _stale():
-        return LIB
     os.makedirs(BUILD, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
+        extension = None
+        if force or _stale(PYCALL, [PYCALL_SOURCE, os.path.join(INCLUDE, "gdn.h")]):
+            extension = ex.submit(_build_pycall)
+        if force or _stale(LIB, [os.path.join(CSRC, s) for s in SOURCES] + HEADERS):
+            _build_lib(ex, verbose)
+        if extension:
+            extension.result()
+    return LIB
+
+
+def _build_lib(ex: cf.Executor, verbose: bool) -> None:
     nvcc = _nvcc()
-    objs = []
 
     def compile_one(src):
         obj = os.path.join(BUILD, os.path.splitext(src)[0] + ".o")
@@ -69,16 +84,12 @@ def build(force: bool = False, verbose: bool = False) -> str:
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    with cf.ThreadPoolExecutor(max_workers=len(SOURCES) + 1) as ex:
-        extension = ex.submit(_build_pycall)
-        objs = list(ex.map(compile_one, SOURCES))
-        extension.result()
+    objs = list(ex.map(compile_one, SOURCES))
     tmp = LIB + f".tmp{os.getpid()}"
     r = subprocess.run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lcudart"], capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"nvcc link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":
