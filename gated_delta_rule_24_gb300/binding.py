@@ -135,7 +135,7 @@ class _PyCall:
             loader = importlib.machinery.ExtensionFileLoader("gdn_pycall", _PYCALL_PATH)
             module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("gdn_pycall", _PYCALL_PATH, loader=loader))
             loader.exec_module(module)
-            module.bind(_DTYPES, *(ctypes.cast(getattr(lib, "gdn_" + name), ctypes.c_void_p).value
+            module.bind(_DTYPES, _on_host if torch.cuda.is_available() else None, *(ctypes.cast(getattr(lib, "gdn_" + name), ctypes.c_void_p).value
                                    for name in ("qk_norm_rope", "decay_prefill", "decay_step")))
         except (ImportError, OSError):
             module = _ByCtypes(lib)
@@ -166,8 +166,20 @@ class _ByCtypes:
                                         *_described(state, state_indices, output), stream)
 
 
+def _on_host(t):
+    """Kernels run after the call has returned, so host memory that they were given could be gone by then;
+    pinned tensors are the caller's to keep."""
+    if not t.is_pinned():
+        raise GdnError(1, "a tensor is on the host")
+
+
 def _described(*tensors):
-    return [_ref(describe(t)) for t in tensors]
+    described = [_ref(describe(t)) for t in tensors]
+    if torch.cuda.is_available():
+        for t in tensors:
+            if t is not None and not t.is_cuda:
+                _on_host(t)
+    return described
 
 
 def _gate_rows(q, g, head_gate):

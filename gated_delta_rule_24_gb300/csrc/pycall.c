@@ -19,8 +19,9 @@ typedef gdn_status_t (*step_fn)(const gdn_tensor_t*, const gdn_tensor_t*, const 
 static rope_fn f_rope;
 static prefill_fn f_prefill;
 static step_fn f_step;
-static PyObject *n_shape, *n_stride, *n_dtype, *n_data_ptr;
+static PyObject *n_shape, *n_stride, *n_dtype, *n_data_ptr, *n_is_cuda;
 static PyObject* dtypes;  // {torch dtype: its code}
+static PyObject* on_host; // called with a tensor that is not the GPU's: raises where that is an error (or None: never asked)
 
 #define MOST 12
 typedef struct {
@@ -70,10 +71,22 @@ static int describe(PyObject* t, gdn_tensor_t* d) {
   return PyErr_Occurred() ? -1 : 0;
 }
 
+// 0 where the GPU may read the tensor; -1 with an exception set.
+static int check_place(PyObject* t) {
+  if (on_host == Py_None) return 0;
+  PyObject* x = PyObject_GetAttr(t, n_is_cuda);
+  if (!x) return -1;
+  Py_DECREF(x);
+  if (x == Py_True) return 0;
+  x = PyObject_CallOneArg(on_host, t);
+  Py_XDECREF(x);
+  return x ? 0 : -1;
+}
+
 static int describe_all(descriptors* d, PyObject* const* t, int first, int n) {
   for (int i = first; i < first + n; ++i) {
     d->at[i] = t[i - first] == Py_None ? NULL : &d->room[i];
-    if (d->at[i] && describe(t[i - first], &d->room[i])) return -1;
+    if (d->at[i] && (describe(t[i - first], &d->room[i]) || check_place(t[i - first]))) return -1;
   }
   return 0;
 }
@@ -142,7 +155,10 @@ static PyObject* decay_step(PyObject* self, PyObject* const* a, Py_ssize_t n) {
 static PyObject* fill(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   static _Thread_local descriptors d;
   if (n > MOST) return PyErr_Format(PyExc_ValueError, "at most %d tensors", MOST);
-  if (describe_all(&d, a, 0, (int)n)) return NULL;
+  for (Py_ssize_t i = 0; i < n; ++i) {
+    d.at[i] = a[i] == Py_None ? NULL : &d.room[i];
+    if (d.at[i] && describe(a[i], &d.room[i])) return NULL;
+  }
   PyObject* out = PyList_New(n);
   for (Py_ssize_t i = 0; out && i < n; ++i) {
     PyObject* x = d.at[i] ? PyLong_FromVoidPtr((void*)d.at[i]) : Py_NewRef(Py_None);
@@ -152,14 +168,15 @@ static PyObject* fill(PyObject* self, PyObject* const* a, Py_ssize_t n) {
   return out;
 }
 
-// bind({dtype: code}, gdn_qk_norm_rope, gdn_decay_prefill, gdn_decay_step): the functions by address.
+// bind({dtype: code}, on_host, gdn_qk_norm_rope, gdn_decay_prefill, gdn_decay_step): the functions by address.
 static PyObject* bind(PyObject* self, PyObject* args) {
-  PyObject *d, *a, *b, *c;
-  if (!PyArg_ParseTuple(args, "O!OOO", &PyDict_Type, &d, &a, &b, &c)) return NULL;
+  PyObject *d, *host, *a, *b, *c;
+  if (!PyArg_ParseTuple(args, "O!OOOO", &PyDict_Type, &d, &host, &a, &b, &c)) return NULL;
   f_rope = (rope_fn)PyLong_AsVoidPtr(a);
   f_prefill = (prefill_fn)PyLong_AsVoidPtr(b);
   f_step = (step_fn)PyLong_AsVoidPtr(c);
   Py_XSETREF(dtypes, Py_NewRef(d));
+  Py_XSETREF(on_host, Py_NewRef(host));
   if (PyErr_Occurred()) return NULL;
   Py_RETURN_NONE;
 }
@@ -176,7 +193,9 @@ PyMODINIT_FUNC PyInit_gdn_pycall(void) {
   n_stride = PyUnicode_InternFromString("stride");
   n_dtype = PyUnicode_InternFromString("dtype");
   n_data_ptr = PyUnicode_InternFromString("data_ptr");
+  n_is_cuda = PyUnicode_InternFromString("is_cuda");
   dtypes = PyDict_New();
-  if (!n_shape || !n_stride || !n_dtype || !n_data_ptr || !dtypes) return NULL;
+  on_host = Py_NewRef(Py_None);
+  if (!n_shape || !n_stride || !n_dtype || !n_data_ptr || !n_is_cuda || !dtypes) return NULL;
   return PyModule_Create(&module);
 }
