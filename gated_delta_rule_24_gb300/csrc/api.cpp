@@ -977,6 +977,8 @@ gdn_status_t gdn_decay_prefill(const gdn_tensor_t* q, const gdn_tensor_t* k, con
   p.N = (int32_t)N; p.H = (int32_t)s.H; p.H_qk = (int32_t)s.Hqk; p.H_v = (int32_t)s.Hv;
   p.scale = (scale == 0.0f) ? 1.0f / std::sqrt(128.0f) : scale;
   p.op_f16 = q->dtype == GDN_F16 ? 1 : 0;
+  p.wait_ns = t_wait_ns;
+  p.hold_gates = t_hold_local_ready;
   p.splits = batch_invariant ? 1 : decay_plan(N, s.H, s.rows, gdn::device_sm_count());
   Workspace workspace;
   if (p.splits > 1) {

@@ -60,6 +60,9 @@ struct DecayPrefillParams {
   float* ws;        // [U][splits - 1] states of 128 x 128: the state behind segment x, once joined
   float* ws_decay;  // [U][splits - 1] decays of whole segments
   int32_t splits;
+  // Testing aids: the bound of every wait in ns (0: 0.2 s), and a first hand-off of every CTA, that of the gates, withheld.
+  int32_t hold_gates;
+  uint64_t wait_ns;
 };
 constexpr int kDecayChunk = 128;  // tokens of a chunk
 

@@ -161,7 +161,7 @@ struct Small {
   uint64_t s_ready, vd_full[vd_slots<kStates>()];  // warps 12-15, 16-23
   uint64_t vd_empty[vd_slots<kStates>()], drain;
   uint32_t tmem;
-  int32_t abort;
+  int32_t abort, tries;  // side by side: wait_slow takes the address of the first
 };
 constexpr uint32_t kSmem = kOffSmall + std::max({sizeof(Small<false, false>), sizeof(Small<false, true>), sizeof(Small<true, true>)});
 static_assert(kSmem <= 227 * 1024, "shared memory budget");
@@ -181,20 +181,20 @@ struct Ring {
   __device__ __forceinline__ void next() { phases ^= 1u << s; pass(); }                      // over a chunk
 };
 
-// Every wait: bounded (kTries probes of 4 us each, or kTriesInline of 1.5 us; 0.2 s), and over as soon as another
+// Every wait: bounded (0.2 s in probes of kProbeNs, or kProbeInlineNs), and over as soon as another
 // role has given up.  Only the first probe is in line: the roles together fill the instruction cache.  Where the
 // groups of warps share registers out among them there can be no call, and a single loop in line is the smallest.
-constexpr int kTries = 50000, kTriesInline = 150000;
+constexpr uint64_t kWaitNs = 200000000, kProbeNs = 4000, kProbeInlineNs = 1400;
 __device__ __noinline__ bool wait_slow(const volatile int32_t* abort, uint64_t* bar, uint32_t parity) {
   bool ok = false;
 #pragma unroll 1
-  for (int i = 0; i < kTries && !ok && !*abort; ++i) ok = mbar_try_wait_sleep(bar, parity, 20000u);
+  for (int left = abort[1]; left > 0 && !ok && !*abort; --left) ok = mbar_try_wait_sleep(bar, parity, 20000u);
   return __all_sync(0xffffffffu, ok);
 }
 template <class Sm>
 __device__ __forceinline__ bool wait(Sm* sm, uint64_t* bar, uint32_t parity) {
   if (Sm::kInline) {
-    int left = kTriesInline;
+    int left = sm->tries;
 #pragma unroll 1
     while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
       if (--left == 0 || *reinterpret_cast<const volatile int32_t*>(&sm->abort)) return false;
@@ -206,7 +206,7 @@ __device__ __forceinline__ bool wait(Sm* sm, uint64_t* bar, uint32_t parity) {
 // The same for copies and products under way when a CTA ends, whoever gave up.
 __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
 #pragma unroll 1
-  for (int i = 0; i < kTries && !mbar_try_wait_sleep(bar, parity, 20000u); ++i) {}
+  for (uint64_t ns = 0; ns < kWaitNs && !mbar_try_wait_sleep(bar, parity, 20000u); ns += kProbeNs) {}
 }
 template <class Sm>
 __device__ __forceinline__ void give_up(const DecayPrefillParams& p, Sm* sm) {
@@ -649,7 +649,7 @@ __device__ __forceinline__ void run_gates(const DecayPrefillParams& p, Sm* sm, i
         *reinterpret_cast<float4*>(&sm->cf[4 * lane]) = make_float4(
             exp2_fast(g_end - pre[0]), exp2_fast(g_end - pre[1]), exp2_fast(g_end - pre[2]), exp2_fast(g_end - pre[3]));
       }
-      warp_arrive(&sm->gate_full[b], lane);
+      if (ci > 0 || !p.hold_gates) warp_arrive(&sm->gate_full[b], lane);
     }
     if (failed) break;
   }
@@ -1330,6 +1330,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __
     init(sm->vd_empty, vd_slots<kStates>(), 1);
     init(&sm->drain, 1, 1);
     sm->abort = 0;
+    sm->tries = (int32_t)max(uint64_t(1), min(p.wait_ns ? p.wait_ns : kWaitNs, kWaitNs) / (Sm::kInline ? kProbeInlineNs : kProbeNs));
     fence_mbar_init();
     tma_prefetch_desc(&p.tm_q);
     tma_prefetch_desc(&p.tm_k);
@@ -1361,6 +1362,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __
     if (apart<kWide>()) reg_dec<kRegsV>();
     run_v<F16, kTerms, kStates, kWide>(p, base, sm, tmem, warp, lane);
   }
+  tmem_st_wait();  // of a role that has given up
   tc_fence_before();
   __syncthreads();
   if (warp == 0) tmem_dealloc(tmem, kTmCols);

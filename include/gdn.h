@@ -384,11 +384,12 @@ void gdn_shutdown(void);
  * split-K layout can be exercised; 0 restores the planner.  GDN_ERR_INVALID_ARGUMENT
  * outside 0..8.
  *
- * gdn_testing_wait_limit: bound every on-chip hand-off wait of the prefill kernel by
- * `limit_ns` nanoseconds instead of the default 200 ms (0 restores the default; values
+ * gdn_testing_wait_limit: bound every on-chip hand-off wait of the prefill kernels by
+ * `limit_ns` nanoseconds (200 ms at most in the decay prefill) instead of the default 200 ms (0 restores the default; values
  * from 1 to 999 are refused with GDN_ERR_INVALID_ARGUMENT).  With
  * `withhold_local_ready` nonzero, the chunk-local group of every CTA withholds its
- * first "operands ready" hand-off, so that the wait for it runs out: the call then
+ * first "operands ready" hand-off, and in the decay prefill that of the first chunk's
+ * gates, so that the wait for it runs out: the call then
  * returns normally, its results are invalid, and the device error word gets
  * GDN_DEVERR_TIMEOUT.  The waits that drain in-flight copies and MMAs before the CTA
  * exits keep the full bound either way.
