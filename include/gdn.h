@@ -310,8 +310,11 @@ gdn_status_t gdn_qk_norm_rope(const gdn_tensor_t* q, const gdn_tensor_t* k, cons
  * Arguments, layouts, defaults and errors are those of gdn_chunk_prefill's arguments of the
  * same names (there is no beta and no norm).  g with a token stride of 0 is one decay for
  * each head.  An infinity or NaN in a token's q, k or v can reach the other outputs of its
- * sequence and head, never those of another sequence.  With f16 inputs the state
- * enters the read-out in f16, so values beyond 65504 overflow there.
+ * sequence and head, never those of another sequence (one in an f32 initial state may come
+ * out as NaN).  With f16 inputs the scores (scale and decay included) and the state enter the
+ * outputs in f16: beyond 65504 they overflow, and the outputs are infinite or NaN where the formula
+ * has finite ones; below 6e-5 they are off by up to 3e-8, so that outputs made of such alone keep less
+ * than f16's 11 bits.  The states that are written know neither limit, but what enters one of f16 is off by up to 3e-8, too.
  *  batch_invariant  nonzero: never split a sequence, so every output and state bit depends
  *                   only on that sequence's own inputs.  Zero: where there are too few
  *                   (sequence, head) units for the SMs, every sequence is cut into segments
