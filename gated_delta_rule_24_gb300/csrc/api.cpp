@@ -682,6 +682,7 @@ gdn_status_t check_decay(const gdn_tensor_t* q, const gdn_tensor_t* k, const gdn
     return fail(GDN_ERR_UNSUPPORTED, "%lld heads must be a multiple of H_qk %lld and H_v %lld", (long long)H,
                 (long long)Hqk, (long long)Hv);
   if (H > (1 << 20)) return fail(GDN_ERR_UNSUPPORTED, "too many heads");
+  if (rows >= (int64_t(1) << 31) - gdn::kDecayChunk) return fail(GDN_ERR_UNSUPPORTED, "too many rows");  // whole chunks of them are int32
   if ((st = check_gate(g, "g", rows, H, true)) != GDN_OK) return st;
   if ((st = check_qkv(output, "output")) != GDN_OK) return st;
   if (output->dtype != q->dtype) return fail(GDN_ERR_UNSUPPORTED, "output must have q's dtype");
