@@ -649,7 +649,7 @@ __device__ __forceinline__ void run_gates(const DecayPrefillParams& p, Sm* sm, i
         *reinterpret_cast<float4*>(&sm->cf[4 * lane]) = make_float4(
             exp2_fast(g_end - pre[0]), exp2_fast(g_end - pre[1]), exp2_fast(g_end - pre[2]), exp2_fast(g_end - pre[3]));
       }
-      if (ci > 0 || !p.hold_gates) warp_arrive(&sm->gate_full[b], lane);
+      warp_arrive(&sm->gate_full[b], lane);
     }
     if (failed) break;
   }
@@ -959,6 +959,13 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
   // S <- b S + (a S + what the chunk before added, from TMEM); with `copy`, also in 16 bits to where Q S^T reads it
   float2 S[apart<kWide>() ? D / 2 : 1];
   float sa = 0.f, keep = 0.f;  // a and b
+  auto put_copy = [&](int q) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      *reinterpret_cast<uint4*>(sb + (q >> 1) * kHalf + sw128_chunk(row, 4 * (q & 1) + e)) =
+          make_uint4(pack16x2<F16>(S[16 * q + 4 * e]), pack16x2<F16>(S[16 * q + 4 * e + 1]),
+                     pack16x2<F16>(S[16 * q + 4 * e + 2]), pack16x2<F16>(S[16 * q + 4 * e + 3]));
+  };
   auto add_chunk = [&](uint32_t from, int v_exp, bool copy) {
     const float2 a2 = pair(sa), b2 = pair(keep), f2 = pair(__int_as_float((127 - v_exp) << 23));
 #pragma unroll
@@ -969,13 +976,7 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
 #pragma unroll
       for (int e = 0; e < 16; ++e)
         S[16 * q + e] = fma2(b2, S[16 * q + e], fma2(a2, S[16 * q + e], lifted<F16, kWide>() ? mul2(f2, pair_at(x + 2 * e)) : pair_at(x + 2 * e)));
-      if (copy) {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          *reinterpret_cast<uint4*>(sb + (q >> 1) * kHalf + sw128_chunk(row, 4 * (q & 1) + e)) =
-              make_uint4(pack16x2<F16>(S[16 * q + 4 * e]), pack16x2<F16>(S[16 * q + 4 * e + 1]),
-                         pack16x2<F16>(S[16 * q + 4 * e + 2]), pack16x2<F16>(S[16 * q + 4 * e + 3]));
-      }
+      if (copy) put_copy(q);
     }
   };
   auto v_exp = [&](int chunk) { return lifted<F16, kWide>() ? (int)sm->v_exp[chunk & 3][2 * w + (lane >> 4)] : 0; };
@@ -1026,12 +1027,6 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
           if (c > 0) {
             tmem_ld32(ts + 32 * q, x);
             tmem_ld_wait();
-          } else if (ring) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              const uint4 z = *reinterpret_cast<const uint4*>(from + q * kHalf + sw128_chunk(row, e));
-              x[4 * e] = z.x; x[4 * e + 1] = z.y; x[4 * e + 2] = z.z; x[4 * e + 3] = z.w;
-            }
           } else if (direct) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
@@ -1066,12 +1061,25 @@ __device__ __forceinline__ void run_state(const DecayPrefillParams& p, uint8_t* 
       if (!apart<kWide>()) {
         through();
       } else {
-        if (c == 0) {  // to TMEM as it is: it is what is added to zero
-          through();
-          tmem_st_wait();
-          zero();
+        if (c == 0 && ring) {  // an f32 state out of a stage of K and V
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+              const float4 z = *reinterpret_cast<const float4*>(from + q * kHalf + sw128_chunk(row, e));
+              S[16 * q + 2 * e] = make_float2(z.x, z.y);
+              S[16 * q + 2 * e + 1] = make_float2(z.z, z.w);
+            }
+            put_copy(q);
+          }
+        } else {
+          if (c == 0) {  // another, or none, to TMEM as it is: it is what is added to zero
+            through();
+            tmem_st_wait();
+            zero();
+          }
+          add_chunk(ts, c == 0 ? 0 : v_exp(ci - 1), !direct);
         }
-        add_chunk(ts, c == 0 ? 0 : v_exp(ci - 1), !direct);
         sa = sm->gamma[st];
         keep = __float_as_int(sa) < 0 ? 1.f : 0.f;
       }
@@ -1301,7 +1309,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_decay_prefill_kernel(const __
     init(sm->kv_empty, kv_stages<kStates>(), 1);
     init(sm->rec_full, kRecs, 1);
     init(sm->rec_empty, kRecs, (kStates ? 2 : 3) + kPoWarps + kSWarps + kVWarps);
-    init(sm->gate_full, 2, 1);
+    init(sm->gate_full, 2, p.hold_gates ? 2 : 1);  // held: one arrival of two never comes
     init(sm->gate_empty, 2, kPoWarps + (kStates ? 0 : kSWarps) + kVWarps);
     init(&sm->claim_full, 1, 1);
     init(&sm->cf_empty, 1, kPoWarps);
