@@ -41,20 +41,22 @@
 // states that the segments add (K and V alone), the join chains them in f32, and the main
 // launch runs all segments from those.
 //
-// Measured (bf16 unless stated; time of the launches, share of 6.8 TB/s in the bytes that have to move):
-//   12800 tokens, 152 heads, none shared:  294 us, 6.6 TB/s (98 %, at the power limit)
-//   16 x 4096, 16 q/k and 32 v heads, bf16 states: 314 us (77 %): 512 units are 3.4 rounds of 152
-//   2 x 65536, 16 and 32 heads, f32 states: 976 us (49 %); 7 segments, K and V read twice, three terms
-//   32000 tokens, 8 heads, f16: 78 us (49 %); 31 us states, 7 join, 41 outputs
-//   1024 prompts of 136 on average, 8 and 16 heads, bf16 states: 638 us (65 %); 1.6 chunks a unit
-//   one chunk of a unit alone: 2.3 us with two terms, 2.8 with three
+// Measured (bf16 unless stated; time of the launches in short bursts, share of 6.8 TB/s in the bytes that have to
+// move; back to back for seconds the power limit adds 2 to 5 % to the first four):
+//   12800 tokens, 152 heads, none shared:  294 us, 6.6 TB/s (98 %); 333 with f32 states
+//   16 x 4096, 16 q/k and 32 v heads, bf16 states: 314 us (77 %): 512 units are 3.4 rounds of 152; f32 states 407
+//   2 x 65536, 16 and 32 heads, f32 states: 1055 us (45 %); 7 segments, K and V read twice, three terms
+//   32000 tokens, 8 heads, f16: 85 to 93 us (45 to 42 %); 31 us states, 7 join, the rest outputs
+//   1024 prompts of 136 on average, 8 and 16 heads, bf16 states: 637 us (65 %); 1.6 chunks a unit; f32 states 857
+//   one chunk of a unit alone: 2.2 us with two terms (f16 and f32 states 2.5), 2.8 with three
 // Tensor pipe 54 % busy, issue slots 53 %, 60 % of DRAM (8 x 4096, 16 and 32 heads): a chunk takes
 // 4300 cycles at 2960 of products, the rest is hand-offs of 300 to 450 cycles between roles.
 //
 // Precision: P and the copy of S are rounded to the 16-bit type of q, k, v (as the output is);
-// everything else that is summed is f32.  V_d would put its rounding straight into the state, so
-// it enters as the sum of 16-bit terms, each the rounding of what is left: two (16 bits bf16, 22
-// bits f16, where v_scale keeps them in f16's range), or three for bf16 inputs whose state stays in f32, which then is as exact as f32 sums
+// everything else that is summed is f32 (by the tensor cores towards zero: see apart).  V_d would
+// put its rounding straight into the state, so it enters as the sum of 16-bit terms, each the
+// rounding of what is left: two (16 bits bf16, 22 bits f16, where v_scale keeps them in f16's
+// range), or three for bf16 inputs whose state stays in f32, which then is as exact as f32 sums
 // are.  The third term costs 0.5 us a chunk where SMs are not kept busy by bytes.
 //
 // 2^(G_i - G_j) is the product 2^(G_i - G_e) 2^(G_e - G_j) with e the last token of j's block
@@ -103,10 +105,10 @@ __device__ __forceinline__ uint32_t vd_slot_col(int slot) {
 constexpr uint32_t kTmCols = 512;
 // kWide (a launch that meets f32 states): TMEM holds what one chunk adds, and the state itself is in the registers
 // of warps 12-15, where each chunk is added to it in f32.  The tensor cores cut their sums off towards zero: with
-// the state in TMEM each product of 16 tokens cost it half a unit in the last place, 1.8e-5 of a state of 16000 tokens
-// and 7e-5 after 60000; now 5e-7, which is what the sum over a chunk costs.  Where only states are made there is
-// room for two chunks.  8 prompts of up to 2000 tokens 55.6 -> 57.4 us, 32000 tokens of f16 85 -> 90, 2 x 65536
-// 1048 -> 1085, one of 256 tokens 14.4 -> 16.4.
+// the state in TMEM each product of 16 tokens costs it half a unit in the last place, 1.8e-5 of a state of 16000 tokens
+// and 7e-5 after 60000, which 16-bit states do not show; like this 5e-7, which is what the sum over a chunk costs.
+// Where only states are made there is room for two chunks.  With the state in TMEM: 16 x 4096 with f32 states
+// 385 us instead of 407, 2 x 65536 970 instead of 1055, 1024 short prompts 821 instead of 857, 256 tokens 12.7 instead of 13.0.
 template <bool kWide>
 __host__ __device__ constexpr bool apart() { return kWide; }
 template <bool kStates>
@@ -168,7 +170,8 @@ static_assert(kSmem <= 227 * 1024, "shared memory budget");
 
 constexpr int kThreads = 32 * (4 + kPoWarps + kSWarps + kVWarps);
 // Registers a thread: what a launch has, and how a launch that keeps the state apart shares them out among its
-// groups of four warps.  200 to 216 for the state are the fewest without spills; 176 to 216 measured within 2 %.
+// groups of four warps.  The state needs 216 to stay without spills: with 200 the long cases take 1 to 2 % more,
+// 1024 short prompts with f32 states 10 %.
 constexpr int kRegs = 80, kRegsOne = 56, kRegsPo = 56, kRegsState = 216, kRegsV = 48;
 static_assert(4 * kRegsOne + kPoWarps * kRegsPo + kSWarps * kRegsState + kVWarps * kRegsV <= kThreads / 32 * kRegs, "registers of a launch");
 // The stages of K and V as a role goes through them, with the phase of each.
@@ -902,8 +905,8 @@ __device__ __forceinline__ void split_product(uint32_t a, uint32_t dh, uint32_t 
 // of a warp goes times the power of two that brings the largest value to 2 .. 4 (and d to 2^kDExp), and warps 12-15 take
 // it back when they add the chunk: an error of 2^-22 of the product, or 2^-39 of the largest value.  Values are
 // made larger and never smaller, d the other way round, so that neither loses bits.  Values of 1e-3: 8e-5 -> 2e-7 of
-// an f32 state; 32000 tokens of 8 heads 89 -> 93 us,
-// 16 x 4096 of 32 heads 348 -> 382.  (An f16 state does without: it has no more bits there than the two terms.)
+// an f32 state; 16 x 4096 of 32 heads 348 -> 386 us, 32000
+// tokens of 8 heads 3 % more.  (An f16 state does without: it has no more bits there than the two terms.)
 __device__ __forceinline__ int v_scale(uint32_t va, int m, int lr, int ch) {  // log2
   __half2 most = __half2half2(__ushort_as_half(0));
 #pragma unroll 2

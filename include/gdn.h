@@ -318,8 +318,9 @@ gdn_status_t gdn_qk_norm_rope(const gdn_tensor_t* q, const gdn_tensor_t* k, cons
  *  batch_invariant  nonzero: never split a sequence, so every output and state bit depends
  *                   only on that sequence's own inputs.  Zero: where there are too few
  *                   (sequence, head) units for the SMs, every sequence is cut into segments
- *                   of whole 128-token chunks (a count that depends on the sizes and the SMs
- *                   alone, at most one for each SM) and the call enqueues three kernels: the states that the
+ *                   of whole 128-token chunks (one count for all, which follows from the units,
+ *                   the mean length and the SMs, at most one for each SM: a long sequence among
+ *                   many short ones may stay whole) and the call enqueues three kernels: the states that the
  *                   segments add, their join, and the outputs of all segments.  Results are
  *                   the same for every run, not the same bits as without.  The
  *                   states live in the workspace that gdn_chunk_prefill's split calls use,
