@@ -1,4 +1,4 @@
-"""Thin binding of the C ABI in ``include/gdn.h``, by ctypes and (three operators, where it is there) a small extension.
+"""Thin binding of the C ABI in ``include/gdn.h``, by ctypes and (some operators, where it is there) a small extension.
 
 Only argument marshalling happens here: torch tensors are described to the
 library (pointer, dtype, shape, strides) and every step of the computation runs
@@ -22,10 +22,12 @@ GDN_OK = 0
 STATUS_NAMES = {0: "GDN_OK", 1: "GDN_ERR_INVALID_ARGUMENT", 2: "GDN_ERR_UNSUPPORTED",
                 3: "GDN_ERR_ALIAS", 4: "GDN_ERR_CUDA", 5: "GDN_ERR_DEVICE_INPUT"}
 DEVERR_CU_SEQLENS, DEVERR_STATE_INDEX, DEVERR_TIMEOUT, DEVERR_POSITION = 0x1, 0x2, 0x4, 0x8
+DEVERR_SLOT, DEVERR_PAGE, DEVERR_LENGTH = 0x10, 0x20, 0x40
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2, torch.int32: 3, torch.int64: 4}
 # symbols include/gdn.h declares; the tests check the library exports all of them
 EXPORTED = ["gdn_init", "gdn_chunk_prefill", "gdn_chunk_prefill_checkpointed", "gdn_chunk_prefill_noalloc",
-            "gdn_decode_step", "gdn_qk_norm_rope", "gdn_decay_prefill", "gdn_decay_step",
+            "gdn_decode_step", "gdn_qk_norm_rope", "gdn_qk_norm_rope_axes", "gdn_norm_rope_append",
+            "gdn_paged_attention_step", "gdn_paged_attention_workspace_bytes", "gdn_decay_prefill", "gdn_decay_step",
             "gdn_decay_workspace_bytes", "gdn_reserve_workspace", "gdn_split_workspace_bytes",
             "gdn_get_device_status", "gdn_last_error", "gdn_shutdown", "gdn_testing_force_splits",
             "gdn_testing_wait_limit", "gdn_testing_split_plan"]
@@ -78,6 +80,17 @@ def load_library():
         lib.gdn_decode_step.restype = ctypes.c_int
         lib.gdn_qk_norm_rope.argtypes = [P, P, P, P, ctypes.c_float, ctypes.c_float, P, P, ctypes.c_int, P, P, ctypes.c_void_p]
         lib.gdn_qk_norm_rope.restype = ctypes.c_int
+        I = ctypes.POINTER(ctypes.c_int32)
+        lib.gdn_qk_norm_rope_axes.argtypes = [P, P, P, P, ctypes.c_float, ctypes.c_float, P, P, I, ctypes.c_int, ctypes.c_int, P, P,
+                                              ctypes.c_void_p]
+        lib.gdn_qk_norm_rope_axes.restype = ctypes.c_int
+        lib.gdn_norm_rope_append.argtypes = [P, P, P, P, P, ctypes.c_float, ctypes.c_float, ctypes.c_int, P, P, I, ctypes.c_int,
+                                             ctypes.c_int, P, P, P, P, ctypes.c_void_p]
+        lib.gdn_norm_rope_append.restype = ctypes.c_int
+        lib.gdn_paged_attention_step.argtypes = [P, P, P, P, P, ctypes.c_float, P, ctypes.c_int64, P, P, ctypes.c_void_p]
+        lib.gdn_paged_attention_step.restype = ctypes.c_int
+        lib.gdn_paged_attention_workspace_bytes.argtypes = [ctypes.c_int64] * 5 + [ctypes.c_int]
+        lib.gdn_paged_attention_workspace_bytes.restype = ctypes.c_size_t
         lib.gdn_decay_prefill.argtypes = [P, P, P, P, ctypes.c_float, P, P, P, P, ctypes.c_int, P, ctypes.c_void_p]
         lib.gdn_decay_prefill.restype = ctypes.c_int
         lib.gdn_decay_step.argtypes = [P, P, P, P, ctypes.c_float, P, P, P, ctypes.c_void_p]
@@ -121,25 +134,28 @@ def describe(t: Optional[torch.Tensor]):
 
 
 class _PyCall:
-    """The operators whose smallest calls take a few microseconds on the GPU: ``qk_norm_rope``,
-    ``decay_prefill`` and ``decay_step`` with the arguments of the C functions (the last two also with
-    whether the gate may be ``[H]``, one decay for each head), tensors described on the way.  At the
+    """The operators whose smallest calls take a few microseconds on the GPU, with the arguments of the C
+    functions (``decay_prefill`` and ``decay_step`` also with whether the gate may be ``[H]``, one decay for
+    each head; ``pair_axes`` without its length), tensors described on the way.  At the
     first use they are taken from the extension ``csrc/pycall.c``, with ``fill``, the addresses of
     descriptors alone; where it was not built or does not load, they go by ctypes as all others do."""
 
+    _names = ("qk_norm_rope", "decay_prefill", "decay_step", "qk_norm_rope_axes", "norm_rope_append", "paged_attention_step")
+
     def __getattr__(self, name):
-        if name not in ("qk_norm_rope", "decay_prefill", "decay_step", "fill"):
+        if name not in self._names and name != "fill":
             raise AttributeError(name)
         lib = load_library()
         try:
             loader = importlib.machinery.ExtensionFileLoader("gdn_pycall", _PYCALL_PATH)
             module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("gdn_pycall", _PYCALL_PATH, loader=loader))
             loader.exec_module(module)
-            module.bind(_DTYPES, _on_host if torch.cuda.is_available() else None, *(ctypes.cast(getattr(lib, "gdn_" + name), ctypes.c_void_p).value
-                                   for name in ("qk_norm_rope", "decay_prefill", "decay_step")))
+            module.bind(_DTYPES, _on_host if torch.cuda.is_available() else None,
+                        *(ctypes.cast(getattr(lib, "gdn_" + each), ctypes.c_void_p).value
+                          for each in self._names))
         except (ImportError, OSError):
             module = _ByCtypes(lib)
-        for each in ("qk_norm_rope", "decay_prefill", "decay_step", "fill"):
+        for each in (*self._names, "fill"):
             setattr(self, each, getattr(module, each))
         return self.__dict__[name]
 
@@ -164,6 +180,31 @@ class _ByCtypes:
     def decay_step(self, q, k, v, g, scale, state, state_indices, output, stream, head_gate):
         return self._lib.gdn_decay_step(*_described(q, k, v, _gate_rows(q, g, head_gate)), scale + 0.0,
                                         *_described(state, state_indices, output), stream)
+
+    def qk_norm_rope_axes(self, q, k, q_weight, k_weight, weight_offset, eps, cos_sin, positions, pair_axes, interleaved, q_out, k_out,
+                          stream):
+        return self._lib.gdn_qk_norm_rope_axes(*_described(q, k, q_weight, k_weight), weight_offset + 0.0, eps + 0.0,
+                                               *_described(cos_sin, positions), *_axes(pair_axes), bool(interleaved),
+                                               *_described(q_out, k_out), stream)
+
+    def norm_rope_append(self, q, k, v, q_weight, k_weight, weight_offset, eps, norm, cos_sin, positions, pair_axes, interleaved,
+                         slots, q_out, k_cache, v_cache, stream):
+        return self._lib.gdn_norm_rope_append(*_described(q, k, v, q_weight, k_weight), weight_offset + 0.0, eps + 0.0, bool(norm),
+                                              *_described(cos_sin, positions), *_axes(pair_axes), bool(interleaved),
+                                              *_described(slots, q_out, k_cache, v_cache), stream)
+
+    def paged_attention_step(self, q, k_cache, v_cache, page_table, lengths, scale, prefix_pages, prefix_length, output, lse, stream):
+        return self._lib.gdn_paged_attention_step(*_described(q, k_cache, v_cache, page_table, lengths), scale + 0.0,
+                                                  *_described(prefix_pages), prefix_length, *_described(output, lse), stream)
+
+
+def _axes(pair_axes):
+    if pair_axes is None:
+        return None, 0
+    pair_axes = list(pair_axes)
+    if len(pair_axes) > 64:
+        raise ValueError("at most 64 pair_axes")
+    return (ctypes.c_int32 * max(1, len(pair_axes)))(*(x if -1 <= x <= 127 else -1 for x in pair_axes)), len(pair_axes)
 
 
 def _on_host(t):
@@ -290,6 +331,47 @@ def gdn_qk_norm_rope(q, k, q_weight, k_weight, weight_offset: float, eps: float,
                                  _stream_handle(stream))
     if status:
         _check(status)
+
+
+def gdn_qk_norm_rope_axes(q, k, q_weight, k_weight, weight_offset: float, eps: float, cos_sin, positions, pair_axes,
+                          interleaved: bool, q_out, k_out, stream=None) -> None:
+    """The same for positions on several axes; names and order of the C entry point, ``pair_axes`` a sequence of
+    integers (its length is the C function's ``num_pairs``)."""
+    if pair_axes is None:
+        raise ValueError("pair_axes is required")
+    status = _calls.qk_norm_rope_axes(q, k, q_weight, k_weight, weight_offset, eps, cos_sin, positions, pair_axes, interleaved,
+                                      q_out, k_out, _stream_handle(stream))
+    if status:
+        _check(status)
+
+
+def gdn_norm_rope_append(q, k, v, q_weight, k_weight, weight_offset: float, eps: float, norm: bool, cos_sin, positions, pair_axes,
+                         interleaved: bool, slots, q_out, k_cache, v_cache, stream=None) -> None:
+    """Norm and rotation with the write of keys and values to a paged cache; names and order of the C entry point,
+    ``pair_axes`` a sequence of integers or None."""
+    status = _calls.norm_rope_append(q, k, v, q_weight, k_weight, weight_offset, eps, norm, cos_sin, positions, pair_axes, interleaved,
+                                     slots, q_out, k_cache, v_cache, _stream_handle(stream))
+    if status:
+        _check(status)
+
+
+def gdn_paged_attention_step(q, k_cache, v_cache, page_table, lengths, scale: float, prefix_pages, prefix_length: int, output,
+                             lse, stream=None) -> None:
+    """Attention of new tokens over a paged cache and a shared prefix; names and order of the C entry point."""
+    status = _calls.paged_attention_step(q, k_cache, v_cache, page_table, lengths, scale, prefix_pages, prefix_length, output, lse,
+                                         _stream_handle(stream))
+    if status:
+        _check(status)
+
+
+def gdn_paged_attention_workspace_bytes(num_seqs: int, tokens: int, num_q_heads: int, num_k_heads: int, prefix_length: int = 0,
+                                        num_sms: Optional[int] = None) -> int:
+    """Workspace bytes that an attention step of these sizes uses, for :func:`gdn_reserve_workspace`; ``num_sms``
+    defaults to the current device's."""
+    if num_sms is None:
+        num_sms = torch.cuda.get_device_properties(torch.cuda.current_device()).multi_processor_count
+    return int(load_library().gdn_paged_attention_workspace_bytes(int(num_seqs), int(tokens), int(num_q_heads), int(num_k_heads),
+                                                                  int(prefix_length), int(num_sms)))
 
 
 def gdn_decay_prefill(q, k, v, g, scale: float, initial_state, state_indices, output_state, cu_seqlens,
@@ -432,20 +514,70 @@ def _output_like(q, v, stream):
 
 
 def qk_norm_rope(q, k=None, cos_sin=None, positions=None, q_weight=None, k_weight=None, eps: float = 1e-6,
-                 weight_offset: float = 0.0, interleaved: bool = False, q_out=None, k_out=None, stream=None):
+                 weight_offset: float = 0.0, interleaved: bool = False, q_out=None, k_out=None, stream=None, pair_axes=None):
     """RMS norm of every query and key head, then the rotation of its first values by the
     token's position, in one pass (``include/gdn.h``, gdn_qk_norm_rope).
 
     ``cos_sin`` is ``[places, R]`` f32 (cosines, then sines); without it the heads are only
     normalised.  Returns ``(q_out, k_out)``, ``k_out`` None without ``k``; pass ``q_out=q,
     k_out=k`` to work in place.  A result that the call allocates belongs to ``stream``.
+
+    With ``pair_axes``, the axis of each of the R / 2 pairs, ``positions`` is ``[axes, T]``, a place on each of up
+    to four axes (gdn_qk_norm_rope_axes).
     """
     if q_out is None:
         q_out = torch.empty_like(q) if stream is None else _empty(q.shape, q, stream)
     if k is not None and k_out is None:
         k_out = torch.empty_like(k) if stream is None else _empty(k.shape, k, stream)
-    gdn_qk_norm_rope(q, k, q_weight, k_weight, weight_offset, eps, cos_sin, positions, interleaved, q_out, k_out, stream)
+    if pair_axes is not None:
+        gdn_qk_norm_rope_axes(q, k, q_weight, k_weight, weight_offset, eps, cos_sin, positions, pair_axes, interleaved, q_out, k_out,
+                              stream)
+    else:
+        gdn_qk_norm_rope(q, k, q_weight, k_weight, weight_offset, eps, cos_sin, positions, interleaved, q_out, k_out, stream)
     return q_out, k_out
+
+
+def norm_rope_append(q, k, v, k_cache, v_cache, slots, cos_sin=None, positions=None, q_weight=None, k_weight=None,
+                     eps: float = 1e-6, weight_offset: float = 0.0, norm: bool = True, interleaved: bool = False, pair_axes=None,
+                     q_out=None, stream=None):
+    """What :func:`qk_norm_rope` does with queries and keys (``norm`` False: the rotation alone), with the keys and
+    the values written to their ``slots`` (page * page_size + place; negative: nowhere) of a paged cache
+    ``[pages, page_size, H_k, 128]`` in the same pass (``include/gdn.h``, gdn_norm_rope_append).
+
+    Returns ``q_out``; pass ``q_out=q`` to work in place.  A result that the call allocates belongs to ``stream``.
+    """
+    if q_out is None:
+        q_out = torch.empty_like(q) if stream is None else _empty(q.shape, q, stream)
+    status = _calls.norm_rope_append(q, k, v, q_weight, k_weight, weight_offset, eps, norm, cos_sin, positions, pair_axes, interleaved,
+                                     slots, q_out, k_cache, v_cache, _stream_handle(stream))
+    if status:
+        _check(status)
+    return q_out
+
+
+def paged_attention_step(q, k_cache, v_cache, page_table, lengths, scale: Optional[float] = None, prefix_pages=None,
+                         prefix_length: int = 0, output=None, return_lse: bool = False, lse=None, stream=None):
+    """Softmax attention of each sequence's newest tokens (``q`` ``[N * tokens, H_q, 128]``, 1 to 16 tokens) over its
+    pages of a cache ``[pages, page_size, H_k, 128]`` and over a prefix that all sequences share, read once for the
+    batch (``include/gdn.h``, gdn_paged_attention_step).
+
+    ``lengths`` counts a sequence's own keys, those of the new tokens included, which are in the cache already
+    (:func:`norm_rope_append`).  Returns the output ``[N * tokens, H_q, 128]``, with ``return_lse`` also the logarithms
+    of the softmax' sums ``[N * tokens, H_q]`` in f32.  Partial results are in a workspace of the device.
+    Such calls run one after the other even on different streams; replays of a graph that holds one must not run
+    concurrently with others.
+    """
+    if output is None or (return_lse and lse is None):
+        with _allocating_on(stream) if stream is not None else _no_context:
+            if output is None:
+                output = torch.empty_like(q, memory_format=torch.contiguous_format)
+            if return_lse and lse is None:
+                lse = q.new_empty(q.shape[:2], dtype=torch.float32)
+    status = _calls.paged_attention_step(q, k_cache, v_cache, page_table, lengths, 0.0 if scale is None else scale, prefix_pages,
+                                         prefix_length, output, lse, _stream_handle(stream))
+    if status:
+        _check(status)
+    return (output, lse) if return_lse else output
 
 
 def decay_linear_attention(q, k, v, g=None, scale: Optional[float] = None, initial_state=None,

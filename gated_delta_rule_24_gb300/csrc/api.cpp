@@ -17,6 +17,7 @@
 #include <mutex>
 #include <vector>
 
+#include "attention.h"
 #include "decay.h"
 #include "decode.h"
 #include "prefill.h"
@@ -724,20 +725,22 @@ bool same_view(const gdn_tensor_t* a, const gdn_tensor_t* b) {
   return true;
 }
 
-// One of the two head tensors of gdn_qk_norm_rope with its weight and its output.
+// One of the head tensors of the norm and rotation with its weight and its output (none where it goes to a cache).
 gdn_status_t rope_tensor(const gdn_tensor_t* x, const gdn_tensor_t* w, const gdn_tensor_t* y, const char* name,
-                         gdn::RopeTensor* t) {
+                         gdn::RopeTensor* t, bool to_cache = false) {
   gdn_status_t st;
   char out_name[16], w_name[16];
   snprintf(out_name, sizeof(out_name), "%s_out", name);
   snprintf(w_name, sizeof(w_name), "%s_weight", name);
   if ((st = check_qkv(x, name)) != GDN_OK) return st;
-  if ((st = check_qkv(y, out_name)) != GDN_OK) return st;
-  if (y->dtype != x->dtype) return fail(GDN_ERR_UNSUPPORTED, "%s must have %s's dtype", out_name, name);
-  if (y->shape[0] != x->shape[0] || y->shape[1] != x->shape[1])
-    return fail(GDN_ERR_INVALID_ARGUMENT, "%s must have %s's shape", out_name, name);
+  if (!to_cache) {
+    if ((st = check_qkv(y, out_name)) != GDN_OK) return st;
+    if (y->dtype != x->dtype) return fail(GDN_ERR_UNSUPPORTED, "%s must have %s's dtype", out_name, name);
+    if (y->shape[0] != x->shape[0] || y->shape[1] != x->shape[1])
+      return fail(GDN_ERR_INVALID_ARGUMENT, "%s must have %s's shape", out_name, name);
+  }
   if (x->shape[1] > (1 << 20)) return fail(GDN_ERR_UNSUPPORTED, "too many heads");
-  if (y->shape[1] > 1 && y->stride[1] < 128) return fail(GDN_ERR_INVALID_ARGUMENT, "%s heads overlap", out_name);
+  if (y && y->shape[1] > 1 && y->stride[1] < 128) return fail(GDN_ERR_INVALID_ARGUMENT, "%s heads overlap", out_name);
   if (w) {
     if ((st = check_basic(w, w_name, 1)) != GDN_OK) return st;
     if (w->dtype != GDN_F32 && w->dtype != GDN_BF16 && w->dtype != GDN_F16)
@@ -746,11 +749,157 @@ gdn_status_t rope_tensor(const gdn_tensor_t* x, const gdn_tensor_t* w, const gdn
     if (reinterpret_cast<uintptr_t>(w->data) % 16) return fail(GDN_ERR_INVALID_ARGUMENT, "%s must be 16-byte aligned", w_name);
     if (overlaps(y, w)) return fail(GDN_ERR_ALIAS, "%s overlaps %s", out_name, w_name);
   }
-  if (!same_view(x, y) && !rows_apart(x, y)) return fail(GDN_ERR_ALIAS, "%s overlaps %s without being the same view", out_name, name);
+  if (y && !same_view(x, y) && !rows_apart(x, y)) return fail(GDN_ERR_ALIAS, "%s overlaps %s without being the same view", out_name, name);
   t->x = x->data; t->x_st = x->stride[0]; t->x_sh = x->stride[1];
-  t->y = y->data; t->y_st = y->stride[0]; t->y_sh = y->stride[1];
+  if (y) { t->y = y->data; t->y_st = y->stride[0]; t->y_sh = y->stride[1]; }
   t->heads = (int32_t)x->shape[1];
   if (w) { t->w = w->data; t->w_dtype = w->dtype; }
+  return GDN_OK;
+}
+
+// The cosines and sines and the positions of T tokens: [T], or [axes, T] where every pair has its axis.
+gdn_status_t rope_places(const gdn_tensor_t* cos_sin, const gdn_tensor_t* positions, const int32_t* pair_axes, int num_pairs,
+                         int interleaved, int64_t T, gdn::RopeParams* p) {
+  gdn_status_t st;
+  if (!cos_sin) {
+    if (positions) return fail(GDN_ERR_INVALID_ARGUMENT, "positions without cos_sin");
+    if (pair_axes) return fail(GDN_ERR_INVALID_ARGUMENT, "pair_axes without cos_sin");
+    return GDN_OK;
+  }
+  if ((st = check_basic(cos_sin, "cos_sin", 2)) != GDN_OK) return st;
+  if (cos_sin->dtype != GDN_F32) return fail(GDN_ERR_UNSUPPORTED, "cos_sin must be f32, got %s", dt_name(cos_sin->dtype));
+  const int64_t R = cos_sin->shape[1];
+  if (R < 16 || R > 128 || R % 16)
+    return fail(GDN_ERR_UNSUPPORTED, "the rotary size (cos_sin's second dim) must be a multiple of 16 up to 128, got %lld", (long long)R);
+  if (cos_sin->stride[1] != 1 || (cos_sin->shape[0] > 1 && cos_sin->stride[0] % 4) ||
+      reinterpret_cast<uintptr_t>(cos_sin->data) % 16)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "cos_sin rows must be contiguous and 16-byte aligned");
+  if (pair_axes) {
+    if (!positions) return fail(GDN_ERR_INVALID_ARGUMENT, "pair_axes without positions");
+    if ((st = check_basic(positions, "positions", 2)) != GDN_OK) return st;
+    if (positions->dtype != GDN_I32 && positions->dtype != GDN_I64) return fail(GDN_ERR_UNSUPPORTED, "positions must be i32 or i64");
+    const int64_t A = positions->shape[0];
+    if (A < 1 || A > 4) return fail(GDN_ERR_UNSUPPORTED, "positions must have 1 to 4 axes, got %lld", (long long)A);
+    if (positions->shape[1] != T) return fail(GDN_ERR_INVALID_ARGUMENT, "positions must be [axes, T=%lld]", (long long)T);
+    if (T > 1 && positions->stride[1] != 1) return fail(GDN_ERR_INVALID_ARGUMENT, "each axis' positions must be contiguous");
+    if (num_pairs != R / 2) return fail(GDN_ERR_INVALID_ARGUMENT, "pair_axes must have %lld entries, got %d", (long long)(R / 2), num_pairs);
+    for (int i = 0; i < num_pairs; ++i) {
+      if (pair_axes[i] < 0 || pair_axes[i] >= A)
+        return fail(GDN_ERR_INVALID_ARGUMENT, "pair_axes[%d] = %d is no axis of %lld", i, pair_axes[i], (long long)A);
+      p->pair_axes[i / 16] |= (uint32_t)pair_axes[i] << (2 * (i % 16));
+    }
+    p->axes = (int32_t)A;
+    p->pos_axis = positions->stride[0];
+  } else if (num_pairs) {
+    return fail(GDN_ERR_INVALID_ARGUMENT, "num_pairs without pair_axes");
+  } else if (positions) {
+    if ((st = check_index_vec(positions, "positions", T)) != GDN_OK) return st;
+  } else if (cos_sin->shape[0] < T) {
+    return fail(GDN_ERR_INVALID_ARGUMENT, "cos_sin has %lld places for %lld tokens", (long long)cos_sin->shape[0], (long long)T);
+  }
+  if (positions) {
+    p->positions = positions->data;
+    p->pos_dtype = positions->dtype;
+  }
+  p->cos_sin = static_cast<const float*>(cos_sin->data);
+  p->cs_stride = cos_sin->stride[0];
+  p->places = cos_sin->shape[0];
+  p->rotary = (int32_t)R;
+  p->interleaved = interleaved ? 1 : 0;
+  return GDN_OK;
+}
+
+// gdn_qk_norm_rope and, with pair_axes, gdn_qk_norm_rope_axes.
+gdn_status_t norm_rope(const gdn_tensor_t* q, const gdn_tensor_t* k, const gdn_tensor_t* q_weight, const gdn_tensor_t* k_weight,
+                       float weight_offset, float eps, const gdn_tensor_t* cos_sin, const gdn_tensor_t* positions,
+                       const int32_t* pair_axes, int num_pairs, int interleaved, const gdn_tensor_t* q_out,
+                       const gdn_tensor_t* k_out, cudaStream_t stream) {
+  gdn_status_t st;
+  gdn::RopeParams p;
+  memset(&p, 0, sizeof(p));
+  if ((st = rope_tensor(q, q_weight, q_out, "q", &p.t[0])) != GDN_OK) return st;
+  const int64_t T = q->shape[0];
+  if (k || k_out || k_weight) {
+    if ((st = rope_tensor(k, k_weight, k_out, "k", &p.t[1])) != GDN_OK) return st;
+    if (k->dtype != q->dtype) return fail(GDN_ERR_UNSUPPORTED, "q and k must share a dtype");
+    if (k->shape[0] != T) return fail(GDN_ERR_INVALID_ARGUMENT, "k has a different token count than q");
+    if (!rows_apart(q_out, k) || !rows_apart(k_out, q)) return fail(GDN_ERR_ALIAS, "an output overlaps the other input");
+    if (!rows_apart(q_out, k_out)) return fail(GDN_ERR_ALIAS, "q_out overlaps k_out");
+    if (overlaps(q_out, k_weight) || overlaps(k_out, q_weight)) return fail(GDN_ERR_ALIAS, "an output overlaps a weight");
+  }
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(GDN_ERR_INVALID_ARGUMENT, "eps must be finite and not negative");
+  if (!std::isfinite(weight_offset)) return fail(GDN_ERR_INVALID_ARGUMENT, "weight_offset must be finite");
+  if ((st = rope_places(cos_sin, positions, pair_axes, num_pairs, interleaved, T, &p)) != GDN_OK) return st;
+  for (const gdn_tensor_t* y : {q_out, k_out})
+    if (overlaps(y, cos_sin) || overlaps(y, positions)) return fail(GDN_ERR_ALIAS, "an output overlaps cos_sin or positions");
+  if (T * (p.t[0].heads + p.t[1].heads) >= (int64_t(1) << 34)) return fail(GDN_ERR_UNSUPPORTED, "too many (token, head) rows");
+  int dev = 0;
+  if ((st = current_device(&dev)) != GDN_OK) return st;
+  p.dev_err = g_dev[dev].dev_err;
+  p.T = T;
+  p.in_f16 = q->dtype == GDN_F16 ? 1 : 0;
+  p.eps = eps;
+  p.weight_offset = weight_offset;
+  p.norm = 1;
+  p.general = pair_axes ? 1 : 0;
+  cudaError_t e = gdn::launch_norm_rope(p, stream);
+  if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "norm and rotation launch: %s", cudaGetErrorString(e));
+  return GDN_OK;
+}
+
+// A paged cache [pages, page_size, heads, 128]: rows of 128 at 16-byte steps, no two in one place.
+gdn_status_t check_cache(const gdn_tensor_t* t, const char* name, int32_t dtype) {
+  gdn_status_t st = check_basic(t, name, 4);
+  if (st != GDN_OK) return st;
+  if (t->dtype != dtype) return fail(GDN_ERR_UNSUPPORTED, "%s must have q's dtype", name);
+  if (t->shape[3] != 128) return fail(GDN_ERR_UNSUPPORTED, "%s head_dim must be 128, got %lld", name, (long long)t->shape[3]);
+  if (t->shape[1] < 1 || t->shape[2] < 1) return fail(GDN_ERR_INVALID_ARGUMENT, "%s needs at least one place and one head in a page", name);
+  if (t->shape[0] >= (int64_t(1) << 31) || t->shape[1] >= (int64_t(1) << 24) || t->shape[2] > (1 << 20))
+    return fail(GDN_ERR_UNSUPPORTED, "%s has too many pages, places or heads", name);
+  if (t->stride[3] != 1) return fail(GDN_ERR_INVALID_ARGUMENT, "%s innermost dim must be contiguous", name);
+  if (reinterpret_cast<uintptr_t>(t->data) % 16) return fail(GDN_ERR_INVALID_ARGUMENT, "%s must be 16-byte aligned", name);
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int a, int b) { return t->stride[a] < t->stride[b]; });
+  int64_t extent = 128;
+  for (int d : order) {
+    if (t->shape[d] <= 1) continue;
+    if (t->stride[d] % 8) return fail(GDN_ERR_INVALID_ARGUMENT, "%s strides must be multiples of 8 elements", name);
+    if (t->stride[d] < extent) return fail(GDN_ERR_INVALID_ARGUMENT, "%s has two places in one", name);
+    extent += (t->shape[d] - 1) * t->stride[d];
+  }
+  return GDN_OK;
+}
+
+// Whether a row of one cache can lie over a row of the other, of the same shape and strides, `by` elements on.
+bool rows_meet(const gdn_tensor_t* a, int64_t by, const int* order, int left) {
+  if (left == 0) return by > -128 && by < 128;
+  const int d = order[left - 1];
+  if (a->shape[d] <= 1) return rows_meet(a, by, order, left - 1);
+  const int64_t S = a->stride[d], down = by >= 0 ? by / S : -((-by + S - 1) / S);
+  for (int64_t steps : {down, down + 1})  // more steps leave more than what the smaller strides span
+    if (steps < a->shape[d] && -steps < a->shape[d] && rows_meet(a, by - steps * S, order, left - 1)) return true;
+  return false;
+}
+// Whether two caches that passed check_cache share no element: apart in memory, or woven into one buffer.
+bool caches_apart(const gdn_tensor_t* a, const gdn_tensor_t* b) {
+  if (!overlaps(a, b)) return true;
+  for (int d = 0; d < 3; ++d)
+    if (a->shape[d] > 1 && a->stride[d] != b->stride[d]) return false;
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + 3, [&](int x, int y) { return a->stride[x] < a->stride[y]; });
+  const int64_t bytes = (int64_t)(reinterpret_cast<uintptr_t>(b->data) - reinterpret_cast<uintptr_t>(a->data));
+  return !rows_meet(a, bytes / 2, order, 3);
+}
+
+// Both caches of an operator whose keys have `heads` heads (0: any).
+gdn_status_t check_caches(const gdn_tensor_t* k_cache, const gdn_tensor_t* v_cache, int32_t dtype, int64_t heads) {
+  gdn_status_t st;
+  if ((st = check_cache(k_cache, "k_cache", dtype)) != GDN_OK) return st;
+  if ((st = check_cache(v_cache, "v_cache", dtype)) != GDN_OK) return st;
+  for (int d = 0; d < 3; ++d)
+    if (k_cache->shape[d] != v_cache->shape[d]) return fail(GDN_ERR_INVALID_ARGUMENT, "k_cache and v_cache must have one shape");
+  if (heads && k_cache->shape[2] != heads)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "the caches have %lld heads for %lld", (long long)k_cache->shape[2], (long long)heads);
   return GDN_OK;
 }
 
@@ -869,58 +1018,158 @@ gdn_status_t gdn_qk_norm_rope(const gdn_tensor_t* q, const gdn_tensor_t* k, cons
                               const gdn_tensor_t* cos_sin, const gdn_tensor_t* positions, int interleaved,
                               const gdn_tensor_t* q_out, const gdn_tensor_t* k_out, cudaStream_t stream) {
   g_last_error[0] = 0;
+  return norm_rope(q, k, q_weight, k_weight, weight_offset, eps, cos_sin, positions, nullptr, 0, interleaved, q_out, k_out, stream);
+}
+
+gdn_status_t gdn_qk_norm_rope_axes(const gdn_tensor_t* q, const gdn_tensor_t* k, const gdn_tensor_t* q_weight,
+                                   const gdn_tensor_t* k_weight, float weight_offset, float eps,
+                                   const gdn_tensor_t* cos_sin, const gdn_tensor_t* positions, const int32_t* pair_axes,
+                                   int num_pairs, int interleaved, const gdn_tensor_t* q_out, const gdn_tensor_t* k_out,
+                                   cudaStream_t stream) {
+  g_last_error[0] = 0;
+  if (!cos_sin || !positions || !pair_axes) return fail(GDN_ERR_INVALID_ARGUMENT, "cos_sin, positions and pair_axes are required");
+  return norm_rope(q, k, q_weight, k_weight, weight_offset, eps, cos_sin, positions, pair_axes, num_pairs, interleaved, q_out, k_out,
+                   stream);
+}
+
+gdn_status_t gdn_norm_rope_append(const gdn_tensor_t* q, const gdn_tensor_t* k, const gdn_tensor_t* v,
+                                  const gdn_tensor_t* q_weight, const gdn_tensor_t* k_weight, float weight_offset, float eps,
+                                  int norm, const gdn_tensor_t* cos_sin, const gdn_tensor_t* positions, const int32_t* pair_axes,
+                                  int num_pairs, int interleaved, const gdn_tensor_t* slots, const gdn_tensor_t* q_out,
+                                  const gdn_tensor_t* k_cache, const gdn_tensor_t* v_cache, cudaStream_t stream) {
+  g_last_error[0] = 0;
   gdn_status_t st;
   gdn::RopeParams p;
   memset(&p, 0, sizeof(p));
   if ((st = rope_tensor(q, q_weight, q_out, "q", &p.t[0])) != GDN_OK) return st;
+  if ((st = rope_tensor(k, k_weight, nullptr, "k", &p.t[1], true)) != GDN_OK) return st;
+  if ((st = rope_tensor(v, nullptr, nullptr, "v", &p.t[2], true)) != GDN_OK) return st;
+  if (k->dtype != q->dtype || v->dtype != q->dtype) return fail(GDN_ERR_UNSUPPORTED, "q, k and v must share a dtype");
   const int64_t T = q->shape[0];
-  if (k || k_out || k_weight) {
-    if ((st = rope_tensor(k, k_weight, k_out, "k", &p.t[1])) != GDN_OK) return st;
-    if (k->dtype != q->dtype) return fail(GDN_ERR_UNSUPPORTED, "q and k must share a dtype");
-    if (k->shape[0] != T) return fail(GDN_ERR_INVALID_ARGUMENT, "k has a different token count than q");
-    if (!rows_apart(q_out, k) || !rows_apart(k_out, q)) return fail(GDN_ERR_ALIAS, "an output overlaps the other input");
-    if (!rows_apart(q_out, k_out)) return fail(GDN_ERR_ALIAS, "q_out overlaps k_out");
-    if (overlaps(q_out, k_weight) || overlaps(k_out, q_weight)) return fail(GDN_ERR_ALIAS, "an output overlaps a weight");
-  }
+  if (k->shape[0] != T || v->shape[0] != T) return fail(GDN_ERR_INVALID_ARGUMENT, "q, k and v must have the same token count");
+  if (v->shape[1] != k->shape[1]) return fail(GDN_ERR_INVALID_ARGUMENT, "k and v must have the same heads");
+  if ((st = check_caches(k_cache, v_cache, q->dtype, k->shape[1])) != GDN_OK) return st;
+  if ((st = check_index_vec(slots, "slots", T)) != GDN_OK) return st;
+  if (!norm && (q_weight || k_weight)) return fail(GDN_ERR_INVALID_ARGUMENT, "weights without the norm");
   if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(GDN_ERR_INVALID_ARGUMENT, "eps must be finite and not negative");
   if (!std::isfinite(weight_offset)) return fail(GDN_ERR_INVALID_ARGUMENT, "weight_offset must be finite");
-  if (cos_sin) {
-    if ((st = check_basic(cos_sin, "cos_sin", 2)) != GDN_OK) return st;
-    if (cos_sin->dtype != GDN_F32) return fail(GDN_ERR_UNSUPPORTED, "cos_sin must be f32, got %s", dt_name(cos_sin->dtype));
-    const int64_t R = cos_sin->shape[1];
-    if (R < 16 || R > 128 || R % 16)
-      return fail(GDN_ERR_UNSUPPORTED, "the rotary size (cos_sin's second dim) must be a multiple of 16 up to 128, got %lld", (long long)R);
-    if (cos_sin->stride[1] != 1 || (cos_sin->shape[0] > 1 && cos_sin->stride[0] % 4) ||
-        reinterpret_cast<uintptr_t>(cos_sin->data) % 16)
-      return fail(GDN_ERR_INVALID_ARGUMENT, "cos_sin rows must be contiguous and 16-byte aligned");
-    if (positions) {
-      if ((st = check_index_vec(positions, "positions", T)) != GDN_OK) return st;
-      p.positions = positions->data;
-      p.pos_dtype = positions->dtype;
-    } else if (cos_sin->shape[0] < T) {
-      return fail(GDN_ERR_INVALID_ARGUMENT, "cos_sin has %lld places for %lld tokens", (long long)cos_sin->shape[0], (long long)T);
-    }
-    for (const gdn_tensor_t* y : {q_out, k_out})
-      if (overlaps(y, cos_sin) || overlaps(y, positions)) return fail(GDN_ERR_ALIAS, "an output overlaps cos_sin or positions");
-    p.cos_sin = static_cast<const float*>(cos_sin->data);
-    p.cs_stride = cos_sin->stride[0];
-    p.places = cos_sin->shape[0];
-    p.rotary = (int32_t)R;
-    p.interleaved = interleaved ? 1 : 0;
-  } else if (positions) {
-    return fail(GDN_ERR_INVALID_ARGUMENT, "positions without cos_sin");
+  if ((st = rope_places(cos_sin, positions, pair_axes, num_pairs, interleaved, T, &p)) != GDN_OK) return st;
+  if (!rows_apart(q_out, k) || !rows_apart(q_out, v)) return fail(GDN_ERR_ALIAS, "q_out overlaps k or v");
+  for (const gdn_tensor_t* in : {k_weight, cos_sin, positions, slots})
+    if (overlaps(q_out, in)) return fail(GDN_ERR_ALIAS, "q_out overlaps an input");
+  for (const gdn_tensor_t* y : {k_cache, v_cache}) {
+    for (const gdn_tensor_t* in : {q, k, v, q_weight, k_weight, cos_sin, positions, slots, q_out})
+      if (overlaps(y, in)) return fail(GDN_ERR_ALIAS, "a cache overlaps another argument");
   }
-  if (T * (p.t[0].heads + p.t[1].heads) >= (int64_t(1) << 34)) return fail(GDN_ERR_UNSUPPORTED, "too many (token, head) rows");
+  if (!caches_apart(k_cache, v_cache)) return fail(GDN_ERR_ALIAS, "k_cache overlaps v_cache");
+  if (T * (p.t[0].heads + 2 * (int64_t)p.t[1].heads) >= (int64_t(1) << 34))
+    return fail(GDN_ERR_UNSUPPORTED, "too many (token, head) rows");
   int dev = 0;
   if ((st = current_device(&dev)) != GDN_OK) return st;
+  for (int i = 1; i < 3; ++i) {
+    const gdn_tensor_t* y = i == 1 ? k_cache : v_cache;
+    p.t[i].y = y->data; p.t[i].y_sp = y->stride[0]; p.t[i].y_st = y->stride[1]; p.t[i].y_sh = y->stride[2];
+  }
+  p.slots = slots->data;
+  p.slot_dtype = slots->dtype;
+  p.page_size = k_cache->shape[1];
+  p.cache_slots = k_cache->shape[0] * p.page_size;
+  p.page_shift = -1;
+  for (int i = 0; i < 24; ++i)
+    if (p.page_size == int64_t(1) << i) p.page_shift = i;
   p.dev_err = g_dev[dev].dev_err;
   p.T = T;
   p.in_f16 = q->dtype == GDN_F16 ? 1 : 0;
   p.eps = eps;
   p.weight_offset = weight_offset;
+  p.norm = norm ? 1 : 0;
+  p.general = 1;
   cudaError_t e = gdn::launch_norm_rope(p, stream);
-  if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "norm and rotation launch: %s", cudaGetErrorString(e));
+  if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "norm, rotation and append launch: %s", cudaGetErrorString(e));
   return GDN_OK;
+}
+
+gdn_status_t gdn_paged_attention_step(const gdn_tensor_t* q, const gdn_tensor_t* k_cache, const gdn_tensor_t* v_cache,
+                                      const gdn_tensor_t* page_table, const gdn_tensor_t* lengths, float scale,
+                                      const gdn_tensor_t* prefix_pages, int64_t prefix_length, const gdn_tensor_t* output,
+                                      const gdn_tensor_t* lse, cudaStream_t stream) {
+  g_last_error[0] = 0;
+  gdn_status_t st;
+  if ((st = check_qkv(q, "q")) != GDN_OK) return st;
+  if ((st = check_caches(k_cache, v_cache, q->dtype, 0)) != GDN_OK) return st;
+  const int64_t T = q->shape[0], Hq = q->shape[1], Hk = k_cache->shape[2], page_size = k_cache->shape[1];
+  if (Hq % Hk) return fail(GDN_ERR_UNSUPPORTED, "%lld query heads must be a multiple of %lld key heads", (long long)Hq, (long long)Hk);
+  if (Hq > (1 << 20)) return fail(GDN_ERR_UNSUPPORTED, "too many heads");
+  if (page_size % 8) return fail(GDN_ERR_UNSUPPORTED, "page_size must be a multiple of 8, got %lld", (long long)page_size);
+  if ((st = check_index_vec(lengths, "lengths", -1)) != GDN_OK) return st;
+  const int64_t N = lengths->shape[0];
+  if (N ? T % N != 0 : T != 0)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "%lld rows of q are not the same number for each of %lld sequences", (long long)T, (long long)N);
+  const int64_t tokens = N ? T / N : 0;
+  if (N && (tokens < 1 || tokens > 16)) return fail(GDN_ERR_UNSUPPORTED, "1 to 16 tokens a sequence, got %lld", (long long)tokens);
+  if (T * Hq >= (int64_t(1) << 28)) return fail(GDN_ERR_UNSUPPORTED, "too many (row, head) pairs");
+  if ((st = check_basic(page_table, "page_table", 2)) != GDN_OK) return st;
+  if (page_table->dtype != GDN_I32 && page_table->dtype != GDN_I64) return fail(GDN_ERR_UNSUPPORTED, "page_table must be i32 or i64");
+  if (page_table->shape[0] != N) return fail(GDN_ERR_INVALID_ARGUMENT, "page_table must have %lld rows", (long long)N);
+  if (page_table->shape[1] > 1 && page_table->stride[1] != 1) return fail(GDN_ERR_INVALID_ARGUMENT, "page_table rows must be contiguous");
+  constexpr int64_t kMostKeys = (int64_t(1) << 31) - (1 << 25);  // the tiles behind a length are int32, too
+  if (page_table->shape[1] > kMostKeys / page_size) return fail(GDN_ERR_UNSUPPORTED, "page_table holds too many keys of a sequence");
+  if (prefix_length < 0) return fail(GDN_ERR_INVALID_ARGUMENT, "prefix_length must not be negative");
+  if (prefix_length > kMostKeys) return fail(GDN_ERR_UNSUPPORTED, "prefix_length is too large");
+  if (prefix_pages) {
+    if ((st = check_index_vec(prefix_pages, "prefix_pages", -1)) != GDN_OK) return st;
+  } else if (prefix_length) {
+    return fail(GDN_ERR_INVALID_ARGUMENT, "prefix_length without prefix_pages");
+  }
+  if (prefix_length && prefix_pages->shape[0] < (prefix_length + page_size - 1) / page_size)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "%lld prefix_pages hold fewer than %lld keys", (long long)prefix_pages->shape[0],
+                (long long)prefix_length);
+  if (!std::isfinite(scale)) return fail(GDN_ERR_INVALID_ARGUMENT, "scale must be finite");
+  if ((st = check_qkv(output, "output")) != GDN_OK) return st;
+  if (output->dtype != q->dtype) return fail(GDN_ERR_UNSUPPORTED, "output must have q's dtype");
+  if (output->shape[0] != T || output->shape[1] != Hq)
+    return fail(GDN_ERR_INVALID_ARGUMENT, "output must be [T=%lld, H_q=%lld, 128]", (long long)T, (long long)Hq);
+  if (Hq > 1 && output->stride[1] < 128) return fail(GDN_ERR_INVALID_ARGUMENT, "output heads overlap");
+  if (T > 1 && output->stride[0] < 128) return fail(GDN_ERR_INVALID_ARGUMENT, "output rows overlap");
+  if (lse) {
+    if ((st = check_basic(lse, "lse", 2)) != GDN_OK) return st;
+    if (lse->dtype != GDN_F32) return fail(GDN_ERR_UNSUPPORTED, "lse must be f32, got %s", dt_name(lse->dtype));
+    if (lse->shape[0] != T || lse->shape[1] != Hq)
+      return fail(GDN_ERR_INVALID_ARGUMENT, "lse must be [T=%lld, H_q=%lld]", (long long)T, (long long)Hq);
+    if ((Hq > 1 && lse->stride[1] != 1) || (T > 1 && lse->stride[0] < Hq))
+      return fail(GDN_ERR_INVALID_ARGUMENT, "lse rows must be contiguous");
+  }
+  for (const gdn_tensor_t* y : {output, lse})
+    for (const gdn_tensor_t* in : {q, k_cache, v_cache, page_table, lengths, prefix_pages})
+      if (overlaps(y, in)) return fail(GDN_ERR_ALIAS, "an output overlaps an input");
+  if (overlaps(output, lse)) return fail(GDN_ERR_ALIAS, "output overlaps lse");
+  int dev = 0;
+  if ((st = current_device(&dev)) != GDN_OK) return st;
+  if (T == 0) return GDN_OK;
+  gdn::AttentionParams p;
+  memset(&p, 0, sizeof(p));
+  p.q = q->data; p.q_st = q->stride[0]; p.q_sh = q->stride[1];
+  p.k = k_cache->data; p.k_sp = k_cache->stride[0]; p.k_st = k_cache->stride[1]; p.k_sh = k_cache->stride[2];
+  p.v = v_cache->data; p.v_sp = v_cache->stride[0]; p.v_st = v_cache->stride[1]; p.v_sh = v_cache->stride[2];
+  p.table = page_table->data; p.table_st = page_table->stride[0]; p.table_dtype = page_table->dtype;
+  p.max_pages = (int32_t)page_table->shape[1];
+  p.lengths = lengths->data; p.len_dtype = lengths->dtype;
+  if (prefix_length) { p.prefix_pages = prefix_pages->data; p.prefix_dtype = prefix_pages->dtype; p.prefix = (int32_t)prefix_length; }
+  p.out = output->data; p.o_st = output->stride[0]; p.o_sh = output->stride[1];
+  if (lse) { p.lse = static_cast<float*>(lse->data); p.lse_st = lse->stride[0]; }
+  p.dev_err = g_dev[dev].dev_err;
+  p.pages = k_cache->shape[0];
+  p.N = (int32_t)N; p.tokens = (int32_t)tokens; p.H_q = (int32_t)Hq; p.H_k = (int32_t)Hk; p.page_size = (int32_t)page_size;
+  p.scale = (scale == 0.0f) ? 1.0f / std::sqrt(128.0f) : scale;
+  p.op_f16 = q->dtype == GDN_F16 ? 1 : 0;
+  cudaError_t e = gdn::launch_attention(p, stream);
+  if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "paged attention launch: %s", cudaGetErrorString(e));
+  return GDN_OK;
+}
+
+size_t gdn_paged_attention_workspace_bytes(int64_t num_seqs, int64_t tokens, int64_t num_q_heads, int64_t num_k_heads,
+                                           int64_t prefix_length, int num_sms) {
+  return 0;
 }
 
 gdn_status_t gdn_decay_prefill(const gdn_tensor_t* q, const gdn_tensor_t* k, const gdn_tensor_t* v,

@@ -11,7 +11,8 @@
 
 namespace gdn {
 
-constexpr int32_t kDevErrCu = 0x1, kDevErrIdx = 0x2, kDevErrTimeout = 0x4, kDevErrPosition = 0x8;
+constexpr int32_t kDevErrCu = 0x1, kDevErrIdx = 0x2, kDevErrTimeout = 0x4, kDevErrPosition = 0x8, kDevErrSlot = 0x10,
+                  kDevErrPage = 0x20, kDevErrLength = 0x40;
 
 __device__ __forceinline__ int64_t index_at(const void* p, int dtype, int64_t i) {
   return dtype == kI64 ? reinterpret_cast<const int64_t*>(p)[i] : (int64_t) reinterpret_cast<const int32_t*>(p)[i];

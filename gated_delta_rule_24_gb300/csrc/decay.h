@@ -14,11 +14,12 @@ struct RopeTensor {
   int64_t x_st, x_sh;
   void* y;
   int64_t y_st, y_sh;
+  int64_t y_sp;   // of a paged cache: from page to page (y_st is then from place to place in a page)
   const void* w;  // [128] or null
   int32_t heads, w_dtype;
 };
 struct RopeParams {
-  RopeTensor t[2];        // q, then k (heads = 0: absent)
+  RopeTensor t[3];        // q, then k (heads = 0: absent), then v of an append
   const float* cos_sin;   // [places, rotary] f32 (cosines, then sines) or null
   int64_t cs_stride, places;
   const void* positions;  // [T] or null (token t takes place t)
@@ -26,6 +27,17 @@ struct RopeParams {
   int64_t T;
   int32_t pos_dtype, rotary, interleaved, in_f16;
   float eps, weight_offset;
+  // The rest is for positions on several axes and for appends (`general`).
+  int32_t general;
+  int32_t norm;            // zero: values are only turned
+  int32_t axes;            // positions are [axes, T], rows pos_axis apart; 0: one position a token
+  int64_t pos_axis;
+  uint32_t pair_axes[4];   // two bits for each pair: its axis
+  const void* slots;       // [T] or null: where k and v of a token go in their caches
+  int64_t cache_slots;     // pages * page_size
+  int64_t page_size;
+  int32_t page_shift;      // page_size is 1 << page_shift, or -1
+  int32_t slot_dtype;
 };
 cudaError_t launch_norm_rope(const RopeParams& p, cudaStream_t stream);
 

@@ -12,6 +12,12 @@
 // value of the pair and P, Q made of the weights, cosines and sines once for a token (P the
 // weight and Q zero where nothing turns).  A group of eight lanes walks some heads of one
 // token with the loads of the next four under way.
+//
+// The general kernel takes positions on several axes as well (each pair has its axis, and a
+// lane collects the cosines and sines of its eight pairs from the places of the axes they
+// turn by) and appends: turned keys and untouched values go to a token's place in paged caches.
+// Its norm can be left out; values that do not turn are then exactly what they were, whatever
+// stands beside them.
 #include <cuda_runtime.h>
 
 #include "decay.cuh"
@@ -45,15 +51,33 @@ __device__ __forceinline__ void load_weight8(const RopeTensor& t, int at, float 
   for (int e = 0; e < 8; ++e) w[e] += offset;
 }
 
-// CTAs below q_ctas take q, the others k.  `per` heads a group; a token's groups side by side.
-template <bool F16, bool kInterleaved, int kAhead>
+// Cosines and sines of the eight pairs from 8 l on, each from the place of its axis.
+__device__ __forceinline__ void load_axes8(const RopeParams& p, const int64_t (&place)[4], int l, float (&c)[8], float (&s)[8]) {
+  const uint32_t mine = p.pair_axes[l >> 1] >> (16 * (l & 1));
+#pragma unroll
+  for (int a = 0; a < 4; ++a) {
+    const uint32_t other = mine ^ (0x5555u * a), not_a = (other | other >> 1) & 0x5555u;
+    if (a < p.axes && not_a != 0x5555u) {
+      const float* row = p.cos_sin + place[a] * p.cs_stride + 8 * l;
+      float ca[8], sa[8];
+      load8(row, ca);
+      load8(row + p.rotary / 2, sa);
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (!(not_a >> (2 * e) & 1u)) { c[e] = ca[e]; s[e] = sa[e]; }
+    }
+  }
+}
+
+// CTAs below q_ctas take q, those below qk_ctas k, the others v.  `per` heads a group; a token's groups side by side.
+template <bool F16, bool kInterleaved, int kAhead, bool kGeneral>
 __global__ void __launch_bounds__(kRopeThreads) gdn_norm_rope_kernel(const __grid_constant__ RopeParams p, unsigned q_ctas,
-                                                                     int per) {
+                                                                     unsigned qk_ctas, int per) {
   const int l = threadIdx.x % kRopeLanes;
-  const bool is_k = blockIdx.x >= q_ctas;
-  const RopeTensor& t = p.t[is_k ? 1 : 0];
+  const bool is_k = blockIdx.x >= q_ctas, is_v = kGeneral && blockIdx.x >= qk_ctas;
+  const RopeTensor& t = p.t[is_v ? 2 : is_k ? 1 : 0];
   const int parts = (t.heads + per - 1) / per;
-  const int64_t first = (int64_t)(blockIdx.x - (is_k ? q_ctas : 0)) * kRopeGroups;
+  const int64_t first = (int64_t)(blockIdx.x - (is_v ? qk_ctas : is_k ? q_ctas : 0)) * kRopeGroups;
   int64_t tok = first / parts;
   int part = (int)(first - tok * parts) + threadIdx.x / kRopeLanes;
   tok += part / parts;
@@ -62,8 +86,16 @@ __global__ void __launch_bounds__(kRopeThreads) gdn_norm_rope_kernel(const __gri
   const bool halves = !kInterleaved && l < rot;
   const int v0 = 8 * (halves ? l : 2 * l), v1 = 8 * (halves ? l + rot : 2 * l + 1);
   bool ok = tok < p.T;
-  int64_t place = 0;
-  if (ok && p.cos_sin) {
+  const int own_in = kGeneral && ok ? min(per, t.heads - part * per) : 0;
+  int64_t place = 0, places[4] = {0, 0, 0, 0}, slot = 0;
+  if (kGeneral && ok && p.cos_sin) {  // every axis has to be on the table
+    const int axes = p.axes ? p.axes : 1;
+#pragma unroll
+    for (int a = 0; a < 4; ++a)
+      if (a < axes) places[a] = p.positions ? index_at(p.positions, p.pos_dtype, a * p.pos_axis + tok) : tok;
+  }
+  if (kGeneral && ok && is_k && p.slots) slot = index_at(p.slots, p.slot_dtype, tok);
+  if (!kGeneral && ok && p.cos_sin) {
     place = p.positions ? index_at(p.positions, p.pos_dtype, tok) : tok;
     if (place < 0 || place >= p.places) {
       if (l == 0) atomicOr(p.dev_err, kDevErrPosition);
@@ -72,13 +104,13 @@ __global__ void __launch_bounds__(kRopeThreads) gdn_norm_rope_kernel(const __gri
   }
   // `n` heads for every group of the warp, so that its lanes stay together; a group without a token or
   // with fewer heads left loads and stores nothing
-  const int n = min(per, t.heads), own = ok ? min(per, t.heads - part * per) : 0;
+  const int n = min(per, t.heads);
+  int own = ok ? min(per, t.heads - part * per) : 0;
   const int64_t sx = t.x_sh, sy = t.y_sh;
   const uint16_t* x = reinterpret_cast<const uint16_t*>(t.x) + tok * t.x_st + (int64_t)part * per * sx;
-  uint16_t* y = reinterpret_cast<uint16_t*>(t.y) + tok * t.y_st + (int64_t)part * per * sy;
   uint4 ra[kAhead], rb[kAhead];
   auto load = [&](int i, int h) {
-    if (h < own) {
+    if (h < (kGeneral ? own_in : own)) {
       ra[i] = __ldcs(reinterpret_cast<const uint4*>(x + h * sx + v0));
       rb[i] = __ldcs(reinterpret_cast<const uint4*>(x + h * sx + v1));
     }
@@ -88,6 +120,22 @@ __global__ void __launch_bounds__(kRopeThreads) gdn_norm_rope_kernel(const __gri
     ra[i] = rb[i] = make_uint4(0, 0, 0, 0);
     load(i, i);
   }
+  int64_t row = tok * t.y_st;
+  if (kGeneral) {  // places and the slot are looked at once the loads are on their way
+    const int axes = p.cos_sin ? (p.axes ? p.axes : 1) : 0;
+#pragma unroll
+    for (int a = 0; a < 4; ++a) ok = ok && (a >= axes || (places[a] >= 0 && places[a] < p.places));
+    if (!ok && tok < p.T && l == 0) atomicOr(p.dev_err, kDevErrPosition);
+    if (!ok) own = 0;
+    place = places[0];
+    if (is_k && p.slots) {
+      if (slot >= p.cache_slots && tok < p.T && l == 0) atomicOr(p.dev_err, kDevErrSlot);
+      if (slot < 0 || slot >= p.cache_slots) own = 0;
+      const int64_t page = p.page_shift >= 0 ? slot >> p.page_shift : slot / p.page_size;
+      row = page * t.y_sp + (slot - page * p.page_size) * t.y_st;
+    }
+  }
+  uint16_t* y = reinterpret_cast<uint16_t*>(t.y) + row + (int64_t)part * per * sy;
   float2 pa[4], qa[4], pb[4], qb[4];  // P and Q of the two vectors
   {
     float wa[8], wb[8], c[8], s[8];
@@ -95,7 +143,9 @@ __global__ void __launch_bounds__(kRopeThreads) gdn_norm_rope_kernel(const __gri
     load_weight8(t, v1, p.weight_offset, wb);
 #pragma unroll
     for (int e = 0; e < 8; ++e) { c[e] = 1.f; s[e] = 0.f; }
-    if (ok && l < rot) {
+    if (kGeneral && ok && l < rot && p.axes && !is_v) {
+      load_axes8(p, places, l, c, s);
+    } else if (ok && l < rot && !is_v) {
       load8(p.cos_sin + place * p.cs_stride + 8 * l, c);
       load8(p.cos_sin + place * p.cs_stride + p.rotary / 2 + 8 * l, s);
     }
@@ -131,13 +181,18 @@ __global__ void __launch_bounds__(kRopeThreads) gdn_norm_rope_kernel(const __gri
       float ss = sum.x + sum.y;
 #pragma unroll
       for (int d = kRopeLanes / 2; d > 0; d >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, d);
-      const float2 r = pair(rsqrtf(ss * (1.f / kHeadDim) + p.eps));
+      const float2 r = pair(kGeneral && !p.norm ? 1.f : rsqrtf(ss * (1.f / kHeadDim) + p.eps));
       uint32_t ya[4], yb[4];
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const float2 ta = kInterleaved ? make_float2(a[e].y, a[e].x) : b[e], tb = kInterleaved ? make_float2(b[e].y, b[e].x) : a[e];
+        float2 ta = kInterleaved ? make_float2(a[e].y, a[e].x) : b[e], tb = kInterleaved ? make_float2(b[e].y, b[e].x) : a[e];
+        if (kGeneral && l >= rot) ta = tb = pair(0.f);  // an infinity beside a value that does not turn stays out of it
         ya[e] = pack16x2<F16>(mul2(r, fma2(a[e], pa[e], mul2(ta, qa[e]))));
         yb[e] = pack16x2<F16>(mul2(r, fma2(b[e], pb[e], mul2(tb, qb[e]))));
+      }
+      if (kGeneral && is_v) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) { ya[e] = ca[e]; yb[e] = cb[e]; }
       }
       if (h0 + i < own) {
         __stcs(reinterpret_cast<uint4*>(y + (h0 + i) * sy + v0), make_uint4(ya[0], ya[1], ya[2], ya[3]));
@@ -147,19 +202,25 @@ __global__ void __launch_bounds__(kRopeThreads) gdn_norm_rope_kernel(const __gri
   }
 }
 
-template <bool F16, int kAhead>
+template <bool F16, int kAhead, bool kGeneral>
 cudaError_t launch(const RopeParams& p, int per, cudaStream_t stream) {
   auto ctas = [&](int heads) { return (p.T * ((heads + per - 1) / per) + kRopeGroups - 1) / kRopeGroups; };
-  const int64_t q = ctas(p.t[0].heads), k = ctas(p.t[1].heads);
-  if (p.interleaved) gdn_norm_rope_kernel<F16, true, kAhead><<<(unsigned)(q + k), kRopeThreads, 0, stream>>>(p, (unsigned)q, per);
-  else gdn_norm_rope_kernel<F16, false, kAhead><<<(unsigned)(q + k), kRopeThreads, 0, stream>>>(p, (unsigned)q, per);
+  const int64_t q = ctas(p.t[0].heads), qk = q + ctas(p.t[1].heads);
+  const unsigned grid = (unsigned)(qk + ctas(p.t[2].heads));
+  if (p.interleaved) gdn_norm_rope_kernel<F16, true, kAhead, kGeneral><<<grid, kRopeThreads, 0, stream>>>(p, (unsigned)q, (unsigned)qk, per);
+  else gdn_norm_rope_kernel<F16, false, kAhead, kGeneral><<<grid, kRopeThreads, 0, stream>>>(p, (unsigned)q, (unsigned)qk, per);
   return cudaGetLastError();
+}
+template <int kAhead>
+cudaError_t launch(const RopeParams& p, int per, cudaStream_t stream) {
+  if (p.general) return p.in_f16 ? launch<true, kAhead, true>(p, per, stream) : launch<false, kAhead, true>(p, per, stream);
+  return p.in_f16 ? launch<true, kAhead, false>(p, per, stream) : launch<false, kAhead, false>(p, per, stream);
 }
 
 }  // namespace
 
 cudaError_t launch_norm_rope(const RopeParams& p, cudaStream_t stream) {
-  const int64_t rows = p.T * (p.t[0].heads + p.t[1].heads);
+  const int64_t rows = p.T * (p.t[0].heads + p.t[1].heads + p.t[2].heads);
   if (rows <= 0) return cudaSuccess;
   const int sms = device_sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
@@ -170,9 +231,9 @@ cudaError_t launch_norm_rope(const RopeParams& p, cudaStream_t stream) {
   constexpr int kResident = 80, kRounds = 2;  // groups on an SM
   const int64_t most = rows / ((int64_t)sms * kResident * kRounds);
   const int per = (int)(most < 1 ? 1 : most > 16 ? 16 : most);
-  if (per < 2) return p.in_f16 ? launch<true, 1>(p, 1, stream) : launch<false, 1>(p, 1, stream);
-  if (per < 4) return p.in_f16 ? launch<true, 2>(p, per, stream) : launch<false, 2>(p, per, stream);
-  return p.in_f16 ? launch<true, 4>(p, per, stream) : launch<false, 4>(p, per, stream);
+  if (per < 2) return launch<1>(p, 1, stream);
+  if (per < 4) return launch<2>(p, per, stream);
+  return launch<4>(p, per, stream);
 }
 
 }  // namespace gdn

@@ -75,6 +75,9 @@ typedef struct {
 #define GDN_DEVERR_STATE_INDEX  0x2  /* some state_indices entry was outside the state pool */
 #define GDN_DEVERR_TIMEOUT      0x4  /* an on-chip wait gave up (the unit's results are invalid) */
 #define GDN_DEVERR_POSITION     0x8  /* some positions entry was outside the cos_sin table */
+#define GDN_DEVERR_SLOT         0x10 /* some slots entry was behind the end of the cache */
+#define GDN_DEVERR_PAGE         0x20 /* some page index was outside the cache */
+#define GDN_DEVERR_LENGTH       0x40 /* some lengths entry was negative or more than its pages hold */
 
 /*
  * gdn_init: check that `device` is an sm_103 GPU (compute capability 10.3) and
@@ -300,6 +303,100 @@ gdn_status_t gdn_qk_norm_rope(const gdn_tensor_t* q, const gdn_tensor_t* k, cons
                               const gdn_tensor_t* cos_sin, const gdn_tensor_t* positions,
                               int interleaved, const gdn_tensor_t* q_out, const gdn_tensor_t* k_out,
                               cudaStream_t stream);
+
+/*
+ * gdn_qk_norm_rope_axes: gdn_qk_norm_rope for tokens that have a position on each of several
+ * axes (time, height and width of a patch, say): every pair turns by the place of one of them.
+ * Arguments, layouts, defaults and errors are those of gdn_qk_norm_rope, but
+ *  cos_sin        required.
+ *  positions      required.  [A, T] i32 or i64, A from 1 to 4, each row contiguous.  Every
+ *                 position of a token has to be on the table, or its output rows are left unwritten.
+ *  pair_axes      required, in HOST memory, read during the call: num_pairs = R / 2 entries, the axis (0 to A - 1) that
+ *                 turns pair i.
+ */
+gdn_status_t gdn_qk_norm_rope_axes(const gdn_tensor_t* q, const gdn_tensor_t* k, const gdn_tensor_t* q_weight,
+                                   const gdn_tensor_t* k_weight, float weight_offset, float eps,
+                                   const gdn_tensor_t* cos_sin, const gdn_tensor_t* positions,
+                                   const int32_t* pair_axes, int num_pairs, int interleaved,
+                                   const gdn_tensor_t* q_out, const gdn_tensor_t* k_out, cudaStream_t stream);
+
+/*
+ * gdn_norm_rope_append: what a softmax-attention layer does with its new tokens before it attends
+ * (gdn_paged_attention_step): norm and rotation of query and key heads, in one pass with the
+ * write of keys and values to their places in a paged cache.
+ *
+ *  q              [T, H_q, 128], k, v [T, H_k, 128], of one dtype (rules of gdn_qk_norm_rope).
+ *  norm           zero: no norm, the values are only turned (and those that do not turn are
+ *                 what they were, bit for bit unless NaN); q_weight and k_weight then have to be NULL.
+ *  q_weight, k_weight, weight_offset, eps, cos_sin, interleaved
+ *                 as in gdn_qk_norm_rope.
+ *  positions,
+ *  pair_axes,
+ *  num_pairs      positions [T] with pair_axes NULL and num_pairs 0, as in gdn_qk_norm_rope, or both as
+ *                 in gdn_qk_norm_rope_axes.
+ *  slots          [T] i32 or i64: token t's key and value go to place slots[t] % page_size of
+ *                 page slots[t] / page_size.  A negative one leaves the caches alone (a padded
+ *                 row of a batch); one behind the last page does, too, and sets GDN_DEVERR_SLOT.
+ *                 Slots must be unique (caller precondition: duplicates race).
+ *  q_out          as in gdn_qk_norm_rope: q itself, or apart from every other argument.
+ *  k_cache,
+ *  v_cache        [pages, page_size, H_k, 128] of q's dtype, innermost contiguous, 16-byte
+ *                 aligned, the other strides multiples of 8 elements in any order (heads of a page
+ *                 one behind the other, both caches in one buffer); written in place.  Neither
+ *                 overlaps another argument.
+ * A token with a position outside the table sets GDN_DEVERR_POSITION; its row of q_out and its
+ * places in the caches are left unwritten.  Asynchronous on `stream`; no workspace.
+ */
+gdn_status_t gdn_norm_rope_append(const gdn_tensor_t* q, const gdn_tensor_t* k, const gdn_tensor_t* v,
+                                  const gdn_tensor_t* q_weight, const gdn_tensor_t* k_weight, float weight_offset,
+                                  float eps, int norm, const gdn_tensor_t* cos_sin, const gdn_tensor_t* positions,
+                                  const int32_t* pair_axes, int num_pairs, int interleaved,
+                                  const gdn_tensor_t* slots, const gdn_tensor_t* q_out, const gdn_tensor_t* k_cache,
+                                  const gdn_tensor_t* v_cache, cudaStream_t stream);
+
+/*
+ * gdn_paged_attention_step: softmax attention of each sequence's newest tokens over its pages of
+ * a cache and over a prefix that all sequences share, whose keys and values are read once for the
+ * batch.  Sequence n has `tokens` = T / N new tokens, rows n * tokens and up; row i of them, query
+ * head h and key head h / (H_q / H_k) give
+ *
+ *     s_j = scale q . k_j,     out = sum_j exp(s_j) v_j / sum_j exp(s_j),     lse = log sum_j exp(s_j)
+ *
+ * over all keys j of the prefix and the first lengths[n] - tokens + i + 1 keys of the sequence's own
+ * pages (the new tokens' keys are there already).  A row without any key gives zeros and an lse
+ * of -infinity.
+ *
+ *  q              [T, H_q, 128] bf16 or f16 (stride rules of gdn_chunk_prefill's q), T = N * tokens,
+ *                 tokens from 1 to 16.
+ *  k_cache,
+ *  v_cache        [pages, page_size, H_k, 128] of q's dtype, laid out as in gdn_norm_rope_append;
+ *                 H_q a multiple of H_k; page_size a multiple of 8.  What is in places that no
+ *                 key stands in (behind a length, in pages that no sequence has) is never used.
+ *  page_table     [N, max_pages] i32 or i64, rows contiguous: page p of sequence n holds its
+ *                 keys p * page_size and up.  Entries behind a length are not read.
+ *  lengths        [N] i32 or i64: keys in a sequence's own pages; 0 where it has none.  A negative
+ *                 one, or one above max_pages * page_size, sets GDN_DEVERR_LENGTH; a page index outside
+ *                 the cache sets GDN_DEVERR_PAGE.  Either leaves the sequence's rows unwritten.
+ *  scale          0 means 1/sqrt(128).  Must be finite.
+ *  prefix_pages   nullable without a prefix.  [n] i32 or i64, n * page_size >= prefix_length.  An
+ *                 index outside the cache sets GDN_DEVERR_PAGE and leaves all rows unwritten.
+ *  prefix_length  keys of the prefix, 0 or more, not a multiple of anything.
+ *  output         [T, H_q, 128] of q's dtype, stride rules of q.  Overlaps no other argument.
+ *  lse            nullable.  [T, H_q] f32, rows contiguous: natural logarithms.
+ *
+ * Work is cut into equal shares for the SMs, so results are the same for every run of the same
+ * batch, not the same bits in another batch.  Their partial results live in the workspace
+ * that gdn_chunk_prefill's split calls use, under the same rules (growth, order among streams,
+ * stream capture).  gdn_paged_attention_workspace_bytes: how much of it a call takes on `num_sms`
+ * SMs; pure host arithmetic, for gdn_reserve_workspace.
+ */
+gdn_status_t gdn_paged_attention_step(const gdn_tensor_t* q, const gdn_tensor_t* k_cache, const gdn_tensor_t* v_cache,
+                                      const gdn_tensor_t* page_table, const gdn_tensor_t* lengths, float scale,
+                                      const gdn_tensor_t* prefix_pages, int64_t prefix_length,
+                                      const gdn_tensor_t* output, const gdn_tensor_t* lse, cudaStream_t stream);
+
+size_t gdn_paged_attention_workspace_bytes(int64_t num_seqs, int64_t tokens, int64_t num_q_heads, int64_t num_k_heads,
+                                           int64_t prefix_length, int num_sms);
 
 /*
  * gdn_decay_prefill: linear attention with a decay over a packed varlen batch, the layer
