@@ -891,6 +891,23 @@ bool caches_apart(const gdn_tensor_t* a, const gdn_tensor_t* b) {
   return !rows_meet(a, bytes / 2, order, 3);
 }
 
+// A paged cache in boxes of (64 values, 1 head, `rows` places, 1 page), 128B swizzle.
+gdn_status_t encode_cache(CUtensorMap* m, const gdn_tensor_t* t, const char* name, uint32_t rows) {
+  memset(m, 0, sizeof(*m));
+  if (t->shape[0] == 0) return GDN_OK;  // no page will ever be loaded
+  cuuint64_t dims[4] = {128, (cuuint64_t)t->shape[2], (cuuint64_t)t->shape[1], (cuuint64_t)t->shape[0]};
+  cuuint64_t strides[3];
+  for (int d = 0; d < 3; ++d)  // that of a single head, place or page can be anything
+    strides[d] = t->shape[2 - d] > 1 ? (cuuint64_t)t->stride[2 - d] * 2 : 256;
+  cuuint32_t box[4] = {64, 1, rows, 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = g_encode(m, t->dtype == GDN_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, t->data, dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS) return fail(GDN_ERR_INVALID_ARGUMENT, "TMA descriptor for %s rejected (CUresult %d)", name, (int)r);
+  return GDN_OK;
+}
+
 // Both caches of an operator whose keys have `heads` heads (0: any).
 gdn_status_t check_caches(const gdn_tensor_t* k_cache, const gdn_tensor_t* v_cache, int32_t dtype, int64_t heads) {
   gdn_status_t st;
@@ -1114,6 +1131,8 @@ gdn_status_t gdn_paged_attention_step(const gdn_tensor_t* q, const gdn_tensor_t*
   if (page_table->shape[1] > 1 && page_table->stride[1] != 1) return fail(GDN_ERR_INVALID_ARGUMENT, "page_table rows must be contiguous");
   constexpr int64_t kMostKeys = (int64_t(1) << 31) - (1 << 25);  // the tiles behind a length are int32, too
   if (page_table->shape[1] > kMostKeys / page_size) return fail(GDN_ERR_UNSUPPORTED, "page_table holds too many keys of a sequence");
+  if (N * Hq * tokens * (page_table->shape[1] * page_size / 64 + 1) >= (int64_t(1) << 38))
+    return fail(GDN_ERR_UNSUPPORTED, "page_table holds too many keys");
   if (prefix_length < 0) return fail(GDN_ERR_INVALID_ARGUMENT, "prefix_length must not be negative");
   if (prefix_length > kMostKeys) return fail(GDN_ERR_UNSUPPORTED, "prefix_length is too large");
   if (prefix_pages) {
@@ -1149,8 +1168,9 @@ gdn_status_t gdn_paged_attention_step(const gdn_tensor_t* q, const gdn_tensor_t*
   gdn::AttentionParams p;
   memset(&p, 0, sizeof(p));
   p.q = q->data; p.q_st = q->stride[0]; p.q_sh = q->stride[1];
-  p.k = k_cache->data; p.k_sp = k_cache->stride[0]; p.k_st = k_cache->stride[1]; p.k_sh = k_cache->stride[2];
-  p.v = v_cache->data; p.v_sp = v_cache->stride[0]; p.v_st = v_cache->stride[1]; p.v_sh = v_cache->stride[2];
+  p.box_rows = page_size % 16 ? 8 : 16;
+  if ((st = encode_cache(&p.tm_k, k_cache, "k_cache", p.box_rows)) != GDN_OK) return st;
+  if ((st = encode_cache(&p.tm_v, v_cache, "v_cache", p.box_rows)) != GDN_OK) return st;
   p.table = page_table->data; p.table_st = page_table->stride[0]; p.table_dtype = page_table->dtype;
   p.max_pages = (int32_t)page_table->shape[1];
   p.lengths = lengths->data; p.len_dtype = lengths->dtype;
@@ -1162,6 +1182,12 @@ gdn_status_t gdn_paged_attention_step(const gdn_tensor_t* q, const gdn_tensor_t*
   p.N = (int32_t)N; p.tokens = (int32_t)tokens; p.H_q = (int32_t)Hq; p.H_k = (int32_t)Hk; p.page_size = (int32_t)page_size;
   p.scale = (scale == 0.0f) ? 1.0f / std::sqrt(128.0f) : scale;
   p.op_f16 = q->dtype == GDN_F16 ? 1 : 0;
+  p.wait_ns = t_wait_ns;
+  p.hold_copies = t_hold_local_ready;
+  const int sms = gdn::device_sm_count();
+  Workspace workspace;
+  if ((st = workspace.take(g_dev[dev], gdn::plan_attention(&p, sms, nullptr), stream)) != GDN_OK) return st;
+  gdn::plan_attention(&p, sms, g_dev[dev].ws);
   cudaError_t e = gdn::launch_attention(p, stream);
   if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "paged attention launch: %s", cudaGetErrorString(e));
   return GDN_OK;
@@ -1169,7 +1195,13 @@ gdn_status_t gdn_paged_attention_step(const gdn_tensor_t* q, const gdn_tensor_t*
 
 size_t gdn_paged_attention_workspace_bytes(int64_t num_seqs, int64_t tokens, int64_t num_q_heads, int64_t num_k_heads,
                                            int64_t prefix_length, int num_sms) {
-  return 0;
+  if (num_seqs <= 0 || tokens <= 0 || num_q_heads <= 0 || num_k_heads <= 0 || num_sms <= 0) return 0;
+  if (tokens > 16 || num_q_heads > (1 << 20) || num_k_heads > num_q_heads || num_seqs >= (int64_t(1) << 28) / num_q_heads / tokens) return 0;
+  gdn::AttentionParams p;
+  memset(&p, 0, sizeof(p));
+  p.N = (int32_t)num_seqs; p.tokens = (int32_t)tokens; p.H_q = (int32_t)num_q_heads; p.H_k = (int32_t)num_k_heads;
+  p.prefix = prefix_length > 0 ? 1 : 0;
+  return gdn::plan_attention(&p, num_sms, nullptr);
 }
 
 gdn_status_t gdn_decay_prefill(const gdn_tensor_t* q, const gdn_tensor_t* k, const gdn_tensor_t* v,

@@ -1,18 +1,17 @@
 // Internal interface between the C-ABI host code (api.cpp) and the kernels of the attention over a
 // paged cache (attention.cu).  Not part of the public ABI.
 #pragma once
+#include <cuda.h>
 #include <cuda_runtime_api.h>
 #include <stdint.h>
 
 namespace gdn {
 
 struct AttentionParams {
+  CUtensorMap tm_k;  // [pages, page_size, H_k, 128], box (64 values, 1 head, box_rows places, 1 page), 128B swizzle
+  CUtensorMap tm_v;
   const void* q;  // [N * tokens, H_q, 128], strides in elements
   int64_t q_st, q_sh;
-  const void* k;  // [pages, page_size, H_k, 128]
-  int64_t k_sp, k_st, k_sh;
-  const void* v;
-  int64_t v_sp, v_st, v_sh;
   const void* table;  // [N, max_pages]
   int64_t table_st;
   const void* lengths;  // [N]
@@ -23,11 +22,26 @@ struct AttentionParams {
   int64_t lse_st;
   int32_t* dev_err;
   int64_t pages;
-  int32_t N, tokens, H_q, H_k, page_size, max_pages, prefix;
+  int32_t N, tokens, H_q, H_k, group, page_size, max_pages, prefix;
+  int32_t box_rows;  // places of a box: 16, or 8 where a page is not a multiple of 16
   int32_t table_dtype, len_dtype, prefix_dtype;
   float scale;
   int32_t op_f16;
+  // Workers, units and where their partial results go (attention.cu says what these are).
+  int32_t workers;
+  int32_t blocks, block_rows;  // row blocks of a (sequence, key head) and the rows of one
+  int32_t prefix_blocks;       // row blocks of a key head for the prefix
+  float* part_o;               // [slots][block_rows][128]
+  float* part_ml;              // [slots][block_rows][2]: base, sum
+  int32_t* first_worker;       // [units], then
+  int32_t* last_worker;        // [units]
+  // Testing aids: the bound of every wait in ns (0: 0.2 s), and the first copy of every warp withheld.
+  int32_t hold_copies;
+  uint64_t wait_ns;
 };
+
+// Fills in what follows from the sizes (and the workspace, where it is given); returns the workspace's bytes.
+size_t plan_attention(AttentionParams* p, int sms, void* workspace);
 cudaError_t launch_attention(const AttentionParams& p, cudaStream_t stream);
 
 }  // namespace gdn
