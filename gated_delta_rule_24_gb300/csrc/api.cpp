@@ -1178,6 +1178,12 @@ gdn_status_t gdn_paged_attention_step(const gdn_tensor_t* q, const gdn_tensor_t*
   p.out = output->data; p.o_st = output->stride[0]; p.o_sh = output->stride[1];
   if (lse) { p.lse = static_cast<float*>(lse->data); p.lse_st = lse->stride[0]; }
   p.dev_err = g_dev[dev].dev_err;
+  p.prefix_box = 8;
+  while (p.prefix_box < gdn::kPrefixKeys && page_size % (2 * p.prefix_box) == 0) p.prefix_box *= 2;
+  if (prefix_length) {
+    if ((st = encode_cache(&p.tm_pk, k_cache, "k_cache", p.prefix_box)) != GDN_OK) return st;
+    if ((st = encode_cache(&p.tm_pv, v_cache, "v_cache", p.prefix_box)) != GDN_OK) return st;
+  }
   p.pages = k_cache->shape[0];
   p.N = (int32_t)N; p.tokens = (int32_t)tokens; p.H_q = (int32_t)Hq; p.H_k = (int32_t)Hk; p.page_size = (int32_t)page_size;
   p.scale = (scale == 0.0f) ? 1.0f / std::sqrt(128.0f) : scale;

@@ -38,7 +38,7 @@ constexpr int kSmemBytes = kRingBytes + kJoinBytes + kWarps * kRows * 8 + kWarps
 constexpr int kResident = 2;                   // workers on an SM
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRoom = 8.f;                   // how far (powers of two) scores may exceed the base before it moves
-constexpr float kBad = -1.f;                   // as a sum: the unit met a bad page
+constexpr float kBad = kAttentionBad;
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;
@@ -513,25 +513,36 @@ __global__ void __launch_bounds__(kThreads) gdn_attention_join_kernel(const __gr
     own = p.last_worker[unit] - first + 1;
   }
   if (own == 1 && !p.prefix) return;  // it is in the output
-  int prefix_first = 0, shared = 0;
-  const int pr = n * p.tokens * p.group + r, prefix_unit = p.N * subs + hk * p.prefix_blocks + pr / kRows;
-  if (p.prefix) {
+  // the prefix' parts of the row, of this kind's workers or of those of the prefix kernel
+  int prefix_first = 0, shared = 0, prefix_unit = 0;
+  const int pr = n * p.tokens * p.group + r;
+  const bool many = p.prefix_units > 0;
+  if (many) {
+    prefix_unit = hk * p.prefix_units + pr / kPrefixRows;
+    const int64_t tiles = (p.prefix + kPrefixKeys - 1) / kPrefixKeys, total = tiles * p.H_k * p.prefix_units, at = prefix_unit * tiles;
+    prefix_first = (int)(((at + 1) * p.prefix_workers - 1) / total);   // the worker whose share holds tile `at`
+    shared = (int)(((at + tiles) * p.prefix_workers - 1) / total) - prefix_first + 1;
+  } else if (p.prefix) {
+    prefix_unit = p.N * subs + hk * p.prefix_blocks + pr / kRows;
     prefix_first = p.first_worker[prefix_unit];
     shared = p.last_worker[prefix_unit] - prefix_first + 1;
   }
   float top = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   // parts of no worker: the kernel before this one gave up, and said so
-  bool bad = first < 0 || own < 0 || first + own > p.workers || prefix_first < 0 || shared < 0 || prefix_first + shared > p.workers;
+  bool bad = first < 0 || own < 0 || first + own > p.workers || prefix_first < 0 || shared < 0 ||
+             prefix_first + shared > (many ? p.prefix_workers : p.workers);
   if (bad) own = shared = 0;
 #pragma unroll 4
   for (int i = warp; i < own + shared; i += kWarps) {
     const bool of_prefix = i >= own;
     const int j = of_prefix ? i - own : i, parts = of_prefix ? shared : own, w = (of_prefix ? prefix_first : first) + j;
-    const int64_t slot = parts == 1 ? 2 * (int64_t)p.workers + (of_prefix ? prefix_unit : unit) : 2 * w + (j == 0 ? 1 : 0);
-    const int64_t at = slot * p.block_rows + (of_prefix ? pr % kRows : row);
-    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
-    const float4 x = *reinterpret_cast<const float4*>(p.part_o + at * kHeadDim + 4 * lane);
+    const bool of_many = of_prefix && many;
+    const int workers = of_many ? p.prefix_workers : p.workers;
+    const int64_t slot = parts == 1 ? 2 * (int64_t)workers + (of_prefix ? prefix_unit : unit) : 2 * w + (j == 0 ? 1 : 0);
+    const int64_t at = of_many ? slot * kPrefixRows + pr % kPrefixRows : slot * p.block_rows + (of_prefix ? pr % kRows : row);
+    const float2 ml = *reinterpret_cast<const float2*>((of_many ? p.prefix_ml : p.part_ml) + 2 * at);
+    const float4 x = *reinterpret_cast<const float4*>((of_many ? p.prefix_o : p.part_o) + at * kHeadDim + 4 * lane);
     bad |= ml.y == kBad;
     const float now = fmaxf(top, ml.x), from_base = now == -INFINITY ? 0.f : now;
     const float keep = exp2_fast(top - from_base), f = exp2_fast(ml.x - from_base);
@@ -575,6 +586,7 @@ cudaError_t launch(const AttentionParams& p, cudaStream_t stream) {
   const int64_t subs = (int64_t)p.H_k * p.blocks;
   const int64_t most = ((int64_t)p.max_pages * p.page_size + kTile - 1) / kTile * p.N * subs +
                        ((int64_t)p.prefix + kTile - 1) / kTile * p.H_k * p.prefix_blocks;
+  if (p.prefix_units > 0 && (e = launch_attention_prefix(p, stream)) != cudaSuccess) return e;
   if (most) gdn_attention_kernel<F16><<<(unsigned)std::min<int64_t>(p.workers, most), kThreads, kSmemBytes, stream>>>(p);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
@@ -587,20 +599,34 @@ cudaError_t launch(const AttentionParams& p, cudaStream_t stream) {
 size_t plan_attention(AttentionParams* p, int sms, void* workspace) {
   p->group = p->H_q / p->H_k;
   const int64_t rows = (int64_t)p->tokens * p->group, all = p->N * rows;
+  const bool many = p->prefix && all > kRows;
   p->workers = kResident * sms;
   p->blocks = (int32_t)((rows + kRows - 1) / kRows);
-  p->prefix_blocks = p->prefix ? (int32_t)((all + kRows - 1) / kRows) : 0;
-  p->block_rows = (int32_t)std::min<int64_t>(kRows, p->prefix ? all : rows);
+  p->prefix_blocks = p->prefix && !many ? 1 : 0;
+  p->block_rows = (int32_t)std::min<int64_t>(kRows, p->prefix_blocks ? all : rows);
+  p->prefix_units = many ? (int32_t)((all + kPrefixRows - 1) / kPrefixRows) : 0;
+  const int64_t many_units = (int64_t)p->H_k * p->prefix_units;
+  p->prefix_workers = many ? (int32_t)std::min<int64_t>(sms, many_units * (((int64_t)p->prefix + kPrefixKeys - 1) / kPrefixKeys)) : 0;
   const int64_t units = (int64_t)p->N * p->H_k * p->blocks + (int64_t)p->H_k * p->prefix_blocks;
-  const int64_t slots = 2 * (int64_t)p->workers + (p->prefix ? units : 0);
-  const size_t o = (size_t)(slots * p->block_rows) * kHeadDim * 4, ml = ((size_t)(slots * p->block_rows) * 8 + 15) / 16 * 16;
+  const int64_t slots = (2 * (int64_t)p->workers + (p->prefix ? units : 0)) * p->block_rows;
+  const int64_t many_slots = many ? (2 * (int64_t)sms + many_units) * kPrefixRows : 0;
+  size_t end = 0;
+  auto take = [&](size_t bytes) {
+    char* at = static_cast<char*>(workspace) + end;
+    end += (bytes + 255) / 256 * 256;
+    return at;
+  };
+  float* part_o = reinterpret_cast<float*>(take((size_t)slots * kHeadDim * 4));
+  float* prefix_o = reinterpret_cast<float*>(take((size_t)many_slots * kHeadDim * 4));
+  float* part_ml = reinterpret_cast<float*>(take((size_t)slots * 8));
+  float* prefix_ml = reinterpret_cast<float*>(take((size_t)many_slots * 8));
+  int32_t* first_worker = reinterpret_cast<int32_t*>(take((size_t)units * 8));
   if (workspace) {
-    p->part_o = static_cast<float*>(workspace);
-    p->part_ml = reinterpret_cast<float*>(static_cast<char*>(workspace) + o);
-    p->first_worker = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + o + ml);
-    p->last_worker = p->first_worker + units;
+    p->part_o = part_o; p->part_ml = part_ml;
+    p->prefix_o = prefix_o; p->prefix_ml = prefix_ml;
+    p->first_worker = first_worker; p->last_worker = first_worker + units;
   }
-  return o + ml + (size_t)units * 8;
+  return end;
 }
 
 cudaError_t launch_attention(const AttentionParams& p, cudaStream_t stream) {

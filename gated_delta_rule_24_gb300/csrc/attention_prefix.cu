@@ -1,0 +1,422 @@
+// Softmax attention of many rows over the prefix that they share, for sm_103a: the part of the paged
+// attention (attention.cu) that reads keys and values once for the whole batch.
+//
+//   s_j = scale q . k_j,   (base, sum_j 2^(s_j log2(e) - base), sum_j 2^(s_j log2(e) - base) v_j)
+//
+// All rows of a key head (sequences x tokens x its query heads) see all keys, so there is nothing to mask but what lies
+// behind the prefix in its last tile.  Every key costs 4 x 128 flops a row against 512 bytes: from some
+// 300 rows on the tensor cores bound it.  A CTA takes 256 rows as two tiles of 128, A and B, against
+// 128 keys at a time:
+//
+//   S = Q K^T (tcgen05, both operands in shared memory, S in TMEM),
+//   P = 2^(S - base) by one thread a row, 16-bit, to TMEM in S's place,
+//   O += P V (tcgen05, P from TMEM, O in TMEM),
+//
+// and while four warps make A's weights, the tensor cores are at B's products, and the other way round.  A
+// base moves only when a score exceeds it by 2^8, so that O is seldom read back to be scaled: the weights
+// grow to 2^8 at most, which changes no rounding.  When S of a tile is there, all products issued before it
+// are done, so a row's thread may scale O then without a hand-off of its own.
+//
+// Units are (key head, 256 rows), a unit's tiles of 128 keys come one behind the other, and all units'
+// tiles are cut into equal shares for the SMs; the parts are joined by attention.cu's second kernel.
+#include <cuda_runtime.h>
+
+#include "attention.h"
+#include "decay.cuh"
+#include "ptx.cuh"
+
+namespace gdn {
+namespace {
+
+constexpr int kThreads = 384;                 // two groups of four warps for the weights, one with the copies and the products
+constexpr int kHalf = 16384;                  // 128 rows of 64 values
+constexpr int kTileBytes = 2 * kHalf;
+constexpr int kStages = 2;                    // of keys, and of values
+constexpr int kQ = 0, kK = 2 * kTileBytes, kV = kK + kStages * kTileBytes, kBars = kV + kStages * kTileBytes;
+constexpr int kSmemBytes = kBars + 256;
+constexpr uint32_t kS = 0, kO = 256;          // TMEM columns: S of A and B (and P over it), O of A and B
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kRoom = 8.f;
+constexpr uint64_t kWaitNs = 200000000ull;
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 r;
+  asm("{\n.reg .b64 x, y;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nadd.rn.f32x2 x, x, y;\nmov.b64 {%0, %1}, x;\n}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+
+// Waits for this thread's loads from TMEM, and keeps what uses these registers behind the wait.
+__device__ __forceinline__ void loaded(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]),
+                 "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]), "+r"(r[16]), "+r"(r[17]),
+                 "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]), "+r"(r[23]), "+r"(r[24]), "+r"(r[25]),
+                 "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]), "+r"(r[30]), "+r"(r[31])::"memory");
+}
+
+struct Bars {
+  uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], done;
+  uint32_t tmem, bad;
+};
+
+// The shares: steps (tiles of keys) of this CTA, and the pieces of units that they make.
+struct Share {
+  int64_t at, end;
+  int tiles;
+  __device__ __forceinline__ explicit Share(const AttentionParams& p) {
+    tiles = (p.prefix + kPrefixKeys - 1) / kPrefixKeys;
+    const int64_t total = (int64_t)p.H_k * p.prefix_units * tiles;
+    at = total * blockIdx.x / gridDim.x;
+    end = total * (blockIdx.x + 1) / gridDim.x;
+  }
+  int unit, t0, n;  // the piece: tiles t0 .. t0 + n - 1 of the unit
+  __device__ __forceinline__ bool next() {
+    if (at >= end) return false;
+    unit = (int)(at / tiles);
+    t0 = (int)(at % tiles);
+    n = (int)min((int64_t)(tiles - t0), end - at);
+    at += n;
+    return true;
+  }
+};
+
+template <bool F16>
+__global__ void __launch_bounds__(kThreads, 1) gdn_attention_prefix_kernel(const __grid_constant__ AttentionParams p) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Bars& bar = *reinterpret_cast<Bars*>(smem + kBars);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = warp >> 2;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&bar.k_full[i], 1);
+      mbar_init(&bar.k_empty[i], 1);
+      mbar_init(&bar.v_full[i], 1);
+      mbar_init(&bar.v_empty[i], 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bar.q_full[i], 128);
+      mbar_init(&bar.s_full[i], 1);
+      mbar_init(&bar.p_full[i], 128);
+      mbar_init(&bar.o_full[i], 1);
+    }
+    mbar_init(&bar.done, 1);
+    fence_mbar_init();
+    bar.bad = smem_u32(smem) & 1023 ? 1 : 0;  // the swizzled tiles have to be where their bits say
+    if (bar.bad) atomicOr(p.dev_err, kDevErrTimeout);
+  }
+  if (warp == 9) {
+    tmem_alloc(&bar.tmem, 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = bar.tmem;
+  const uint64_t limit = p.wait_ns ? p.wait_ns : kWaitNs;
+  const int rows_all = p.N * p.tokens * p.group;
+  Share share(p);
+
+  if (group == 2) {
+    if (warp == 8) {  // copies
+      const int box = p.prefix_box, boxes = kPrefixKeys / box;
+      bool dead = false;
+      int step = 0, issued[2] = {0, 0};
+      auto page_of = [&](int t) -> int64_t {
+        const int key = t * kPrefixKeys + lane * box;
+        if (lane >= boxes || key >= p.prefix) return -2;
+        const int64_t page = index_at(p.prefix_pages, p.prefix_dtype, key / p.page_size);
+        return page < 0 || page >= p.pages ? -1 : page;
+      };
+      while (!dead && share.next()) {
+        const int head = share.unit / p.prefix_units;
+        int64_t page = page_of(share.t0);
+        for (int i = 0; i < share.n && !dead; ++i, ++step) {
+          const int t = share.t0 + i, st = step % kStages;
+          const int64_t ahead = i + 1 < share.n ? page_of(t + 1) : -2;
+          const unsigned some = __ballot_sync(0xffffffffu, page >= 0);
+          if (__any_sync(0xffffffffu, page == -1) && lane == 0) {
+            atomicOr(p.dev_err, kDevErrPage);
+            atomicOr(&bar.bad, 1u);
+          }
+          const uint32_t bytes = __popc(some) * box * 256;
+          const int row = (t * kPrefixKeys + lane * box) % p.page_size;
+          for (int kv = 0; kv < 2; ++kv) {
+            uint64_t* full = kv ? &bar.v_full[st] : &bar.k_full[st];
+            dead = dead || !__all_sync(0xffffffffu, mbar_wait(kv ? &bar.v_empty[st] : &bar.k_empty[st], (step / kStages + 1) & 1, limit));
+            if (dead) break;
+            if (lane == 0) mbar_arrive_expect_tx(full, bytes);
+            __syncwarp();
+            ++issued[kv];
+            if (page >= 0 && !(p.hold_copies && step == 0)) {
+              uint8_t* at = smem + (kv ? kV : kK) + st * kTileBytes + lane * box * 128;
+              for (int half = 0; half < 2; ++half)
+                tma_load_4d(at + half * kHalf, kv ? &p.tm_pv : &p.tm_pk, full, 64 * half, head, row, (int)page);
+            }
+            __syncwarp();
+          }
+          page = ahead;
+        }
+      }
+      if (dead && lane == 0) atomicOr(p.dev_err, kDevErrTimeout);
+      // every copy ends before the memory is another's
+      for (int kv = 0; kv < 2; ++kv)
+        for (int i = max(0, issued[kv] - kStages); i < issued[kv]; ++i)
+          if (!(p.hold_copies && i == 0)) mbar_wait(kv ? &bar.v_full[i % kStages] : &bar.k_full[i % kStages], (i / kStages) & 1, kWaitNs);
+    } else if (warp == 9) {  // products
+      const bool one = elect_one();
+      bool dead = false;
+      uint32_t step = 0, steps[2] = {0, 0}, pieces[2] = {0, 0};
+      const uint32_t sdesc_rows = 1024;
+      constexpr uint32_t id_s = idesc_16_f32(F16, 128, 128, 0, 0, 0), id_o = idesc_16_f32(F16, 128, 128, 0, 1, 0);
+      const uint32_t q_at = smem_u32(smem + kQ), k_at = smem_u32(smem + kK), v_at = smem_u32(smem + kV);
+      auto wait = [&](uint64_t* b, uint32_t parity) {
+        if (!dead && !__all_sync(0xffffffffu, mbar_wait(b, parity & 1, limit))) dead = true;
+        tc_fence_after();
+      };
+      auto scores = [&](int x, uint32_t st) {
+        if (one && !dead) {
+          const uint32_t a = q_at + x * kTileBytes, b = k_at + st * kTileBytes;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk) {
+            const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
+            mma_ss(tmem + kS + 128 * x, sdesc_sw128(a + off, 16, sdesc_rows), sdesc_sw128(b + off, 16, sdesc_rows), id_s, kk > 0);
+          }
+          mma_commit(&bar.s_full[x]);
+        }
+        __syncwarp();
+      };
+      auto values = [&](int x, uint32_t st, bool more) {
+        if (one && !dead) {
+          const uint32_t b = v_at + st * kTileBytes;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            mma_ts(tmem + kO + 128 * x, tmem + kS + 128 * x + 8 * kk, sdesc_sw128(b + kk * 2048, kHalf, 1024), id_o, more || kk > 0);
+        }
+        __syncwarp();
+      };
+      auto commit = [&](uint64_t* b) {
+        if (one && !dead) mma_commit(b);
+        __syncwarp();
+      };
+      while (!dead && share.next()) {
+        const int both = rows_all - share.unit % p.prefix_units * kPrefixRows > 128 ? 2 : 1;
+        for (int x = 0; x < both; ++x) {
+          wait(&bar.q_full[x], pieces[x]++);
+          if (x == 0) wait(&bar.k_full[step % kStages], step / kStages);
+          scores(x, step % kStages);
+        }
+        commit(&bar.k_empty[step % kStages]);
+        for (int i = 0; i < share.n && !dead; ++i, ++step) {
+          const uint32_t st = step % kStages, ahead = step + 1;
+          for (int x = 0; x < both; ++x) {
+            wait(&bar.p_full[x], steps[x]++);
+            if (x == 0) wait(&bar.v_full[st], step / kStages);
+            values(x, st, i > 0);
+            if (x + 1 == both) commit(&bar.v_empty[st]);
+            if (i + 1 < share.n) {
+              if (x == 0) wait(&bar.k_full[ahead % kStages], ahead / kStages);
+              scores(x, ahead % kStages);
+              if (x + 1 == both) commit(&bar.k_empty[ahead % kStages]);
+            } else {
+              commit(&bar.o_full[x]);
+            }
+          }
+        }
+      }
+      if (dead && lane == 0) atomicOr(p.dev_err, kDevErrTimeout);
+      // nothing is on its way to or from TMEM any more
+      if (one) mma_commit(&bar.done);
+      __syncwarp();
+      mbar_wait(&bar.done, 0, kWaitNs);
+    }
+  } else {
+    const int x = group, i128 = tid & 127;  // tile A or B, the thread's row of it
+    const uint32_t lanes = (uint32_t)(warp & 3) << 21;
+    const uint32_t s_at = tmem + kS + 128 * x + lanes, o_at = tmem + kO + 128 * x + lanes;
+    const float c = fabsf(p.scale) * kLog2e;
+    const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
+    constexpr float kBias = F16 ? 6.f : 0.f;
+    bool dead = false;
+    uint32_t steps = 0, pieces = 0, at_step = 0;
+    auto wait = [&](uint64_t* b, uint32_t parity) {
+      if (!dead && !__all_sync(0xffffffffu, mbar_wait(b, parity & 1, limit))) {
+        dead = true;
+        if (lane == 0) atomicOr(p.dev_err, kDevErrTimeout);
+      }
+    };
+    while (share.next()) {
+      const int unit_row = share.unit % p.prefix_units * kPrefixRows;
+      if (rows_all - unit_row <= 128 * x) {  // no rows for B
+        at_step += share.n;
+        continue;
+      }
+      const int r = unit_row + 128 * x + i128, head = share.unit / p.prefix_units * p.group;
+      // the rows of Q, one by half a warp each time
+#pragma unroll 4
+      for (int j = 0; j < 16; ++j) {
+        const int rr = (warp & 3) * 32 + 2 * j + (lane >> 4), chunk = lane & 15, row = unit_row + 128 * x + rr;
+        uint4 v = make_uint4(0, 0, 0, 0);
+        if (row < rows_all) {
+          v = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.q) + (int64_t)(row / p.group) * p.q_st +
+                                              (int64_t)(head + row % p.group) * p.q_sh + 8 * chunk);
+          v.x ^= flip; v.y ^= flip; v.z ^= flip; v.w ^= flip;
+        }
+        *reinterpret_cast<uint4*>(smem + kQ + x * kTileBytes + (chunk >> 3) * kHalf + sw128_chunk(rr, chunk & 7)) = v;
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&bar.q_full[x]);
+      float base = -INFINITY;
+      float2 sum = make_float2(0.f, 0.f);
+#pragma unroll 1
+      for (int i = 0; i < share.n; ++i, ++at_step) {
+        wait(&bar.s_full[x], steps++);
+        if (dead) continue;
+        tc_fence_after();
+        // A row's scores pass twice, the second time as its weights are made: half of them stay in registers, P lies
+        // over what was read, never over what is still to be.
+        const int valid = p.prefix - (share.t0 + i) * kPrefixKeys;
+        float top[4];
+        uint32_t s0[32], s1[32], s2[32];
+        auto largest = [&](int h, uint32_t (&s)[32]) {
+          if (valid < kPrefixKeys) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (32 * h + e >= valid) s[e] = 0xff800000u;
+          }
+          float y[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) y[e] = __uint_as_float(s[e]);
+#pragma unroll
+          for (int e = 4; e < 32; ++e) y[e & 3] = fmaxf(y[e & 3], __uint_as_float(s[e]));
+          top[h] = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+        };
+        tmem_ld32(s_at + 64, s0);
+        tmem_ld32(s_at + 96, s1);
+        loaded(s0);
+        loaded(s1);
+        largest(2, s0);
+        largest(3, s1);
+        tmem_ld32(s_at, s0);
+        tmem_ld32(s_at + 32, s1);
+        loaded(s0);
+        loaded(s1);
+        largest(0, s0);
+        largest(1, s1);
+        if (valid < kPrefixKeys && x == 0) {  // values of no key have a weight of zero, but must not be infinite either
+          wait(&bar.v_full[at_step % kStages], at_step / kStages);
+          uint8_t* v = smem + kV + (at_step % kStages) * kTileBytes;
+          for (int e = i128; e < (kPrefixKeys - valid) * 16; e += 128)
+            *reinterpret_cast<uint4*>(v + (e & 8 ? kHalf : 0) + (valid + e / 16) * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          if (dead) continue;
+        }
+        const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
+        if (__any_sync(0xffffffffu, high > base + (kRoom + kBias))) {
+          const float now = fmaxf(base, high - kBias);
+          const float keep = now == -INFINITY || now == base ? 1.f : exp2_fast(base - now);
+          base = now;
+          sum = mul2(sum, pair(keep));
+          if (i > 0) {
+#pragma unroll 1
+            for (int h = 0; h < 4; ++h) {
+              uint32_t o[32];
+              tmem_ld32(o_at + 32 * h, o);
+              loaded(o);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * keep);
+              tmem_st32(o_at + 32 * h, o);
+            }
+          }
+        }
+        const float2 minus = pair(base == -INFINITY ? 0.f : -base), cc = pair(c);
+        auto weights = [&](int h, uint32_t (&s)[32], bool masked) {
+          if (masked) {
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (32 * h + e >= valid) s[e] = 0xff800000u;
+          }
+          uint32_t w[16];
+#pragma unroll
+          for (int e = 0; e < 16; ++e) {
+            float2 y = fma2(pair_at(&s[2 * e]), cc, minus);
+            y.x = exp2_fast(y.x);
+            y.y = exp2_fast(y.y);
+            sum = add2(sum, y);
+            w[e] = pack16x2<F16>(y);
+          }
+          tmem_st16(s_at + 16 * h, w);
+        };
+        tmem_ld32(s_at + 64, s2);
+        weights(0, s0, false);
+        loaded(s2);
+        tmem_ld32(s_at + 96, s0);
+        weights(1, s1, false);
+        weights(2, s2, valid < kPrefixKeys);
+        loaded(s0);
+        weights(3, s0, valid < kPrefixKeys);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&bar.p_full[x]);
+      }
+      wait(&bar.o_full[x], pieces++);
+      tc_fence_after();
+      const bool whole = share.t0 == 0 && share.n == share.tiles;
+      const int64_t slot = whole ? 2 * (int64_t)gridDim.x + share.unit : 2 * (int64_t)blockIdx.x + (share.t0 == 0 ? 1 : 0);
+      const int64_t at = slot * kPrefixRows + 128 * x + i128;
+      const bool write = r < rows_all;
+      if (!dead) {
+#pragma unroll 1
+        for (int h = 0; h < 4; ++h) {
+          uint32_t o[32];
+          tmem_ld32(o_at + 32 * h, o);
+          loaded(o);
+          if (write) {
+            uint4* y = reinterpret_cast<uint4*>(p.prefix_o + at * kHeadDim + 32 * h);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) y[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+          }
+        }
+      }
+      if (write) {
+        const bool bad = dead || *reinterpret_cast<volatile uint32_t*>(&bar.bad);
+        *reinterpret_cast<float2*>(p.prefix_ml + 2 * at) = make_float2(base, bad ? kAttentionBad : sum.x + sum.y);
+      }
+      tc_fence_before();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 9) tmem_dealloc(tmem, 512);
+}
+
+template <bool F16>
+cudaError_t launch(const AttentionParams& p, cudaStream_t stream) {
+  static thread_local int generation = -1, device = -1;  // the attribute is one of a device
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (generation != launch_config_generation() || device != dev) {
+    e = cudaFuncSetAttribute(gdn_attention_prefix_kernel<F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
+    if (e != cudaSuccess) return e;
+    generation = launch_config_generation();
+    device = dev;
+  }
+  gdn_attention_prefix_kernel<F16><<<(unsigned)p.prefix_workers, kThreads, kSmemBytes, stream>>>(p);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_attention_prefix(const AttentionParams& p, cudaStream_t stream) {
+  return p.op_f16 ? launch<true>(p, stream) : launch<false>(p, stream);
+}
+
+}  // namespace gdn
