@@ -1168,7 +1168,10 @@ gdn_status_t gdn_paged_attention_step(const gdn_tensor_t* q, const gdn_tensor_t*
   gdn::AttentionParams p;
   memset(&p, 0, sizeof(p));
   p.q = q->data; p.q_st = q->stride[0]; p.q_sh = q->stride[1];
-  p.box_rows = page_size % 16 ? 8 : 16;
+  // boxes: the largest power of two that a page is a multiple of, up to the kernels' tiles
+  p.prefix_box = 8;
+  while (p.prefix_box < gdn::kPrefixKeys && page_size % (2 * p.prefix_box) == 0) p.prefix_box *= 2;
+  p.box_rows = std::min(p.prefix_box, gdn::kOwnKeys);
   if ((st = encode_cache(&p.tm_k, k_cache, "k_cache", p.box_rows)) != GDN_OK) return st;
   if ((st = encode_cache(&p.tm_v, v_cache, "v_cache", p.box_rows)) != GDN_OK) return st;
   p.table = page_table->data; p.table_st = page_table->stride[0]; p.table_dtype = page_table->dtype;
@@ -1178,8 +1181,6 @@ gdn_status_t gdn_paged_attention_step(const gdn_tensor_t* q, const gdn_tensor_t*
   p.out = output->data; p.o_st = output->stride[0]; p.o_sh = output->stride[1];
   if (lse) { p.lse = static_cast<float*>(lse->data); p.lse_st = lse->stride[0]; }
   p.dev_err = g_dev[dev].dev_err;
-  p.prefix_box = 8;
-  while (p.prefix_box < gdn::kPrefixKeys && page_size % (2 * p.prefix_box) == 0) p.prefix_box *= 2;
   if (prefix_length) {
     if ((st = encode_cache(&p.tm_pk, k_cache, "k_cache", p.prefix_box)) != GDN_OK) return st;
     if ((st = encode_cache(&p.tm_pv, v_cache, "v_cache", p.prefix_box)) != GDN_OK) return st;

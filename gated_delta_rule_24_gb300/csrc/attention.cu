@@ -11,10 +11,11 @@
 // a second kernel joins those.
 //
 // Each key and value is read once for up to 16 rows, 2 x 16 flops a byte at most: the kernel is bound by
-// HBM bandwidth as long as copies are always under way.  Each of a worker's four warps takes 16 of a tile's
-// keys on its own: a ring of tensor copies (box_rows places of a page each) that it issues and waits for
-// itself, scores and sums by warp products with the keys as the narrow side, weights passed on in
-// registers.  The warps meet at the end of a unit only.
+// HBM bandwidth as long as copies are always under way.  A warp of its own looks up pages and issues the tensor
+// copies (boxes of up to 64 places of a page) into a ring of three tiles, over the ends of units; with a unit's first
+// tile come its queries.  Four warps take 16 of a tile's keys each: scores and sums by warp products
+// with the keys as the narrow side, weights passed on in registers.  They meet at the end of a unit only, over the
+// memory of its last tile.
 #include <cuda_runtime.h>
 
 #include <algorithm>
@@ -26,17 +27,26 @@
 namespace gdn {
 namespace {
 
-constexpr int kWarps = 4, kThreads = 32 * kWarps;
+constexpr int kWarps = 4;                      // that compute; one more copies
+constexpr int kThreads = 32 * kWarps + 32;
 constexpr int kWarpKeys = 16, kTile = kWarps * kWarpKeys;
+static_assert(kTile == kOwnKeys, "boxes fit a tile");
 constexpr int kRows = 16;                      // rows of a unit
 constexpr int kStages = 3;
-constexpr int kHalfBytes = kWarpKeys * 128;    // 64 of a row's 128 values
-constexpr int kStageBytes = 4 * kHalfBytes;    // keys, then values
-constexpr int kRingBytes = kWarps * kStages * kStageBytes;
-constexpr int kJoinBytes = kWarps * kRows * 64 * 4;   // half the columns of every warp's sums
-constexpr int kSmemBytes = kRingBytes + kJoinBytes + kWarps * kRows * 8 + kWarps * kStages * 8 + 64;
+constexpr int kHalfBytes = kTile * 128;        // 64 of a row's 128 values
+constexpr int kTileBytes = 4 * kHalfBytes;     // keys, then values
+constexpr int kQueryBytes = kRows * 256;
+static_assert(kWarps * kRows * kHeadDim * 4 == kTileBytes, "the warps' sums lie over a tile");
+struct Bars {
+  float2 ml[kWarps][kRows];
+  uint64_t full[kStages], empty[kStages];
+  int64_t found[kWarps + 1];                   // the walk's start
+  uint32_t bad[kStages];                       // a page of the stage's tile is none
+};
+constexpr int kSmemBytes = kStages * (kTileBytes + kQueryBytes) + sizeof(Bars);
 constexpr int kResident = 2;                   // workers on an SM
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr uint64_t kWaitNs = 200000000ull;
 constexpr float kRoom = 8.f;                   // how far (powers of two) scores may exceed the base before it moves
 constexpr float kBad = kAttentionBad;
 
@@ -56,6 +66,12 @@ __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uin
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+
+// Kernels of a call are launched one behind the other without a gap: each lets the next start when it has started
+// itself (go_ahead), and waits for the end of the one before it (grid_wait) before it reads what that has written, and before it
+// ends.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void go_ahead() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Keys of sequence n in its own pages, or -1 where its length is none.
 __device__ __forceinline__ int length_of(const AttentionParams& p, int n) {
@@ -105,45 +121,129 @@ struct Walk {
   }
 };
 
-struct Smem {
-  uint8_t* ring;   // [warp][stage]
-  float* join;     // [warp][16][64], columns by eights turned by the row
-  float2* ml;      // [warp][16]
-  uint64_t* full;  // [warp][stage]
-  int64_t* found;  // the walk's start
+// 16 bytes to shared memory, zeros where there is nothing to copy.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool some) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(some ? 16 : 0) : "memory");
+}
+// Arrives (as one of those that the barrier counts) once this thread's copies so far are there.
+__device__ __forceinline__ void arrive_copied(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// The rows of a unit.
+struct Unit {
+  int tok0, head0, r0, rows;
+  __device__ __forceinline__ Unit(const AttentionParams& p, const Walk& w) {
+    const bool own = w.n < p.N;
+    const int blocks = own ? p.blocks : p.prefix_blocks, head = w.sub / blocks;
+    head0 = head * p.group;
+    r0 = (w.sub - head * blocks) * kRows;
+    tok0 = own ? w.n * p.tokens : 0;
+    rows = min(kRows, (own ? p.tokens : p.N * p.tokens) * p.group - r0);
+  }
 };
+
+// The copying warp.
+__device__ __forceinline__ void copy_tiles(const AttentionParams& p, uint8_t* smem, Bars& bar, Walk walk, int count, uint64_t limit) {
+  const int lane = threadIdx.x & 31, boxes = kTile / p.box_rows;
+  const auto page_of = [&](const Walk& w) -> int64_t {  // of the lane's box: -2 behind the length, -1 outside the cache
+    const int key = w.t * kTile + lane * p.box_rows;
+    if (lane >= boxes || key >= w.length) return -2;
+    const int64_t page = w.n < p.N ? index_at(p.table, p.table_dtype, w.n * p.table_st + key / p.page_size)
+                                   : index_at(p.prefix_pages, p.prefix_dtype, key / p.page_size);
+    return page < 0 || page >= p.pages ? -1 : page;
+  };
+  int64_t page = page_of(walk);
+  int issued = 0;
+  for (int k = 0; k < count; ++k) {
+    const int stage = k % kStages;
+    Walk ahead = walk;
+    int64_t page_ahead = -2;
+    if (k + 1 < count) {
+      ahead.next(p, lane);
+      page_ahead = page_of(ahead);
+    }
+    if (!__all_sync(0xffffffffu, mbar_wait(&bar.empty[stage], (k / kStages + 1) & 1, limit))) {
+      if (lane == 0) atomicOr(p.dev_err, kDevErrTimeout);
+      break;
+    }
+    ++issued;
+    const bool bad = __any_sync(0xffffffffu, page == -1), held = p.hold_copies && k == 0;
+    const unsigned some = __ballot_sync(0xffffffffu, page >= 0);
+    uint8_t* tile = smem + stage * kTileBytes;
+    uint64_t* full = &bar.full[stage];
+    if (lane == 0) {
+      bar.bad[stage] = bad;
+      if (bad) atomicOr(p.dev_err, kDevErrPage);
+      mbar_arrive_expect_tx(full, __popc(some) * p.box_rows * 512);
+    }
+    __syncwarp();
+    if (page >= 0 && !held) {
+      const int row = (walk.t * kTile + lane * p.box_rows) % p.page_size, head = walk.sub / (walk.n < p.N ? p.blocks : p.prefix_blocks);
+      uint8_t* at = tile + lane * p.box_rows * 128;
+      for (int half = 0; half < 2; ++half) {
+        tma_load_4d(at + half * kHalfBytes, &p.tm_k, full, 64 * half, head, row, (int)page);
+        tma_load_4d(at + (2 + half) * kHalfBytes, &p.tm_v, full, 64 * half, head, row, (int)page);
+      }
+    }
+    if (k == 0 || walk.t == 0) {  // the queries: half a warp a row
+      const Unit u(p, walk);
+      const uint32_t to = smem_u32(smem + kStages * kTileBytes + stage * kQueryBytes);
+      const int chunk = lane & 15;
+#pragma unroll
+      for (int j = 0; j < kRows / 2; ++j) {
+        const int i = 2 * j + (lane >> 4), r = u.r0 + i;
+        const bool some_row = i < u.rows;
+        const uint16_t* from = reinterpret_cast<const uint16_t*>(p.q);
+        if (some_row) from += (int64_t)(u.tok0 + r / p.group) * p.q_st + (int64_t)(u.head0 + r % p.group) * p.q_sh + 8 * chunk;
+        copy16(to + i * 256 + ((chunk ^ (i & 7)) << 4), from, some_row);
+      }
+      arrive_copied(full);
+    } else {
+      mbar_arrive(full);
+    }
+    walk = ahead;
+    page = page_ahead;
+  }
+  // every copy ends before the memory is another's
+  for (int k = max(0, issued - kStages); k < issued; ++k)
+    if (!(p.hold_copies && k == 0)) mbar_wait(&bar.full[k % kStages], (k / kStages) & 1, kWaitNs);
+}
 
 template <bool F16>
 __global__ void __launch_bounds__(kThreads, kResident) gdn_attention_kernel(const __grid_constant__ AttentionParams p) {
-  extern __shared__ __align__(1024) uint8_t raw[];
-  Smem s;
-  s.ring = raw;
-  if (smem_u32(raw) & 1023) {  // where the swizzled tiles have to be; two workers would not fit an SM with room to spare for it
+  extern __shared__ __align__(1024) uint8_t smem[];
+  Bars& bar = *reinterpret_cast<Bars*>(smem + kStages * (kTileBytes + kQueryBytes));
+  if (smem_u32(smem) & 1023) {  // where the swizzled tiles have to be; two workers would not fit an SM with room to spare for it
     if (threadIdx.x == 0) atomicOr(p.dev_err, kDevErrTimeout);
+    grid_wait();
     return;
   }
-  s.join = reinterpret_cast<float*>(s.ring + kRingBytes);
-  s.ml = reinterpret_cast<float2*>(s.ring + kRingBytes + kJoinBytes);
-  s.full = reinterpret_cast<uint64_t*>(s.ml + kWarps * kRows);
-  s.found = reinterpret_cast<int64_t*>(s.full + kWarps * kStages);
+  go_ahead();
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint64_t* full = s.full + warp * kStages;
-  if (lane == 0) {
-    for (int i = 0; i < kStages; ++i) mbar_init(&full[i], 1);
-    fence_mbar_init();
-  }
-  // Each thread counts the tiles of N / 128 sequences in a row, then the threads' sums are joined.
-  const int subs = p.H_k * p.blocks, each = (p.N + kThreads - 1) / kThreads;
-  const int64_t prefix_tiles = (int64_t)tiles_of(p.prefix) * p.H_k * p.prefix_blocks;
-  int64_t before = 0, total, sharers;
-  {
-    int64_t mine = 0;
-    bool bad = false;
-    for (int i = 0, n = tid * each; i < each && n < p.N; ++i, ++n) {
-      const int length = length_of(p, n);
-      bad |= length < 0;
-      mine += tiles_of(length);
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&bar.full[i], 33);     // the copying warp's lanes, and one of them for the tensor copies
+      mbar_init(&bar.empty[i], kWarps);
     }
+    fence_mbar_init();
+    tma_prefetch_desc(&p.tm_k);
+    tma_prefetch_desc(&p.tm_v);
+  }
+  // Each thread of the first four warps counts the tiles of N / 128 sequences in a row, then the threads' sums are joined.
+  constexpr int kCounting = 32 * kWarps;
+  const int subs = p.H_k * p.blocks, each = (p.N + kCounting - 1) / kCounting;
+  const int64_t prefix_tiles = (int64_t)tiles_of(p.prefix) * p.H_k * p.prefix_blocks;
+  int64_t total, sharers;
+  {
+    int64_t mine = 0, before = 0;
+    bool bad = false;
+    if (warp < kWarps)
+      for (int i = 0, n = tid * each; i < each && n < p.N; ++i, ++n) {
+        const int length = length_of(p, n);
+        bad |= length < 0;
+        mine += tiles_of(length);
+      }
     if (bad && blockIdx.x == 0) atomicOr(p.dev_err, kDevErrLength);
     int64_t upto = mine;
 #pragma unroll
@@ -151,29 +251,32 @@ __global__ void __launch_bounds__(kThreads, kResident) gdn_attention_kernel(cons
       const int64_t x = __shfl_up_sync(0xffffffffu, upto, d);
       if (lane >= d) upto += x;
     }
-    if (lane == 31) s.found[warp] = upto;
+    if (lane == 31) bar.found[warp] = upto;
     __syncthreads();
     int64_t all = 0;
     for (int w = 0; w < kWarps; ++w) {
-      if (w < warp) before += s.found[w];
-      all += s.found[w];
+      if (w < warp) before += bar.found[w];
+      all += bar.found[w];
     }
     before += upto - mine;
     total = all * subs + prefix_tiles;
     __syncthreads();
     // no more workers than tiles: one without any between two parts of a unit would leave a gap
     sharers = total < gridDim.x ? total : (int64_t)gridDim.x;
-    if (blockIdx.x >= sharers) return;
+    if (blockIdx.x >= sharers) {
+      grid_wait();
+      return;
+    }
     const int64_t a = total * blockIdx.x / sharers;
-    if (before * subs <= a && a < (before + mine) * subs) {  // the share begins in one of these
+    if (warp < kWarps && before * subs <= a && a < (before + mine) * subs) {  // the share begins in one of these
       int64_t at = before;
       for (int i = 0, n = tid * each; i < each && n < p.N; ++i, ++n) {
         const int tiles = tiles_of(length_of(p, n));
         if (a < (at + tiles) * subs) {
           const int64_t in = a - at * subs;
-          s.found[0] = n;
-          s.found[1] = in / tiles;
-          s.found[2] = in % tiles;
+          bar.found[0] = n;
+          bar.found[1] = in / tiles;
+          bar.found[2] = in % tiles;
           break;
         }
         at += tiles;
@@ -181,128 +284,67 @@ __global__ void __launch_bounds__(kThreads, kResident) gdn_attention_kernel(cons
     }
     if (tid == 0 && a >= all * subs && prefix_tiles) {
       const int64_t in = a - all * subs, tiles = tiles_of(p.prefix);
-      s.found[0] = p.N;
-      s.found[1] = in / tiles;
-      s.found[2] = in % tiles;
+      bar.found[0] = p.N;
+      bar.found[1] = in / tiles;
+      bar.found[2] = in % tiles;
     }
     __syncthreads();
   }
   const int count = (int)(total * (blockIdx.x + 1) / sharers - total * blockIdx.x / sharers);  // at least one
-  Walk take, load;
-  take.n = (int)s.found[0];
-  take.sub = (int)s.found[1];
-  take.t = (int)s.found[2];
+  Walk take;
+  take.n = (int)bar.found[0];
+  take.sub = (int)bar.found[1];
+  take.t = (int)bar.found[2];
   take.hold(p, lane);
   take.enter(p, lane);
-  load = take;
+  const uint64_t limit = p.wait_ns ? p.wait_ns : kWaitNs;
+  if (warp == kWarps) {
+    copy_tiles(p, smem, bar, take, count, limit);
+    return;
+  }
 
-  const uint64_t limit = p.wait_ns ? p.wait_ns : 200000000ull;
-  uint8_t* ring = s.ring + warp * kStages * kStageBytes;
-  int dead_at = count;      // the tile whose wait ran out: from there on no more copies, no more waits
-  bool dead = false;
-  uint32_t bad_stage = 0;   // stages whose tile has a bad page
-  const int boxes = kWarpKeys / p.box_rows;
-  int64_t held_pages = -1;
-  int held_n = -1, held_box = 0;   // lane i holds the page of the warp's box held_box + i of sequence held_n
-  auto issue = [&](int k) {
-    const int stage = k % kStages;
-    const int box0 = load.t * boxes;
-    if (load.n != held_n || box0 < held_box || box0 + boxes > held_box + 32) {
-      held_n = load.n;
-      held_box = box0;
-      const int box = box0 + lane, key = box / boxes * kTile + warp * kWarpKeys + box % boxes * p.box_rows;
-      held_pages = -1;
-      if (key < load.length) {
-        held_pages = load.n < p.N ? index_at(p.table, p.table_dtype, load.n * p.table_st + key / p.page_size)
-                                  : index_at(p.prefix_pages, p.prefix_dtype, key / p.page_size);
-      }
-    }
-    const int head = load.sub / (load.n < p.N ? p.blocks : p.prefix_blocks);
-    uint8_t* at = ring + stage * kStageBytes;
-    int copies = 0;
-    bool bad = false;
-    int64_t page[2];
-    int row[2];
-    for (int i = 0; i < boxes; ++i) {
-      const int key = load.t * kTile + warp * kWarpKeys + i * p.box_rows;
-      page[i] = __shfl_sync(0xffffffffu, held_pages, box0 - held_box + i);
-      row[i] = key % p.page_size;
-      if (key < load.length) {
-        if (page[i] < 0 || page[i] >= p.pages) { bad = true; page[i] = -1; }
-        else ++copies;
-      } else {
-        page[i] = -1;
-      }
-    }
-    if (bad) {
-      bad_stage |= 1u << stage;
-      if (lane == 0) atomicOr(p.dev_err, kDevErrPage);
-    }
-    if (lane == 0) {
-      mbar_arrive_expect_tx(&full[stage], copies * 4 * p.box_rows * 128);
-      if (!(p.hold_copies && k == 0)) {
-        for (int i = 0; i < boxes; ++i) {
-          if (page[i] < 0) continue;
-          for (int half = 0; half < 2; ++half) {
-            tma_load_4d(at + half * kHalfBytes + i * 1024, &p.tm_k, &full[stage], 64 * half, head, row[i], (int)page[i]);
-            tma_load_4d(at + (2 + half) * kHalfBytes + i * 1024, &p.tm_v, &full[stage], 64 * half, head, row[i], (int)page[i]);
-          }
-        }
-      }
-    }
-    load.next(p, lane);
-  };
-  for (int k = 0; k < min(count, kStages); ++k) issue(k);
-
+  // All four warps walk the same units whatever happens on the way, so that they meet at the same ends.
   const float c = fabsf(p.scale) * kLog2e;
   const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
   constexpr float kBias = F16 ? 6.f : 0.f;  // f16 weights are kept 2^6 above their normal range's end for longer
+  const int mi = lane >> 3, mj = lane & 7;
   uint32_t q[8][4];
   float base[2], sum[2], o[16][4];
-  bool starts = false, unit_bad = false;
-  int rows = 0, tok0 = 0, r0 = 0, head0 = 0;
+  bool starts = false, unit_bad = false, dead = false;
 #pragma unroll 1
   for (int k = 0; k < count; ++k) {
     const int stage = k % kStages;
-    if (k == 0 || take.t == 0) {  // a unit
+    uint8_t* tile = smem + stage * kTileBytes;
+    if (!dead && !__all_sync(0xffffffffu, mbar_wait(&bar.full[stage], (k / kStages) & 1, limit))) {
+      dead = true;
+      if (lane == 0) atomicOr(p.dev_err, kDevErrTimeout);
+    }
+    const Unit u(p, take);
+    const bool own = take.n < p.N;
+    if (k == 0 || take.t == 0) {
       starts = take.t == 0;
       unit_bad = false;
-      const bool own = take.n < p.N;
-      const int blocks = own ? p.blocks : p.prefix_blocks;
-      head0 = take.sub / blocks * p.group;
-      r0 = take.sub % blocks * kRows;
-      tok0 = own ? take.n * p.tokens : 0;
-      rows = (own ? p.tokens : p.N * p.tokens) * p.group;
-      rows = min(kRows, rows - r0);
+      const uint32_t at = smem_u32(smem + kStages * kTileBytes + stage * kQueryBytes) + ((mi & 1) * 8 + mj) * 256;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-        const int i = lane / 4 + 8 * half, r = r0 + i;
-        const uint16_t* row = reinterpret_cast<const uint16_t*>(p.q) + (int64_t)(tok0 + r / p.group) * p.q_st +
-                              (int64_t)(head0 + r % p.group) * p.q_sh + 2 * (lane & 3);
+      for (int kk = 0; kk < 8; ++kk) {
+        ldmatrix_x4(at + (((2 * kk + (mi >> 1)) ^ mj) << 4), q[kk]);
 #pragma unroll
-        for (int kk = 0; kk < 8; ++kk) {
-          q[kk][half] = i < rows ? *reinterpret_cast<const uint32_t*>(row + 16 * kk) ^ flip : 0u;
-          q[kk][half + 2] = i < rows ? *reinterpret_cast<const uint32_t*>(row + 16 * kk + 8) ^ flip : 0u;
-        }
-        base[half] = -INFINITY;
-        sum[half] = 0.f;
+        for (int e = 0; e < 4; ++e) q[kk][e] ^= flip;
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        base[i] = -INFINITY;
+        sum[i] = 0.f;
       }
 #pragma unroll
       for (int i = 0; i < 16; ++i)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
     }
-    if (!dead && !__all_sync(0xffffffffu, mbar_wait(&full[stage], (k / kStages) & 1, limit))) {
-      dead = true;
-      dead_at = k;
-      if (lane == 0) atomicOr(p.dev_err, kDevErrTimeout);
-    }
-    unit_bad |= dead || (bad_stage >> stage & 1u);
-    bad_stage &= ~(1u << stage);
+    unit_bad |= dead || bar.bad[stage];
     const int key0 = take.t * kTile + warp * kWarpKeys, valid = min(kWarpKeys, take.length - key0);
     if (valid > 0 && !unit_bad) {
-      const uint32_t kb = smem_u32(ring + stage * kStageBytes), vb = kb + 2 * kHalfBytes;
-      const int mi = lane >> 3, mj = lane & 7;
+      const uint32_t kb = smem_u32(tile) + warp * kWarpKeys * 128, vb = kb + 2 * kHalfBytes;
       float acc[2][2][4] = {};  // [even and odd steps][keys]
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
@@ -313,7 +355,6 @@ __global__ void __launch_bounds__(kThreads, kResident) gdn_attention_kernel(cons
         mma16<F16>(acc[kk & 1][1], q[kk], b[2], b[3]);
       }
       float w[2][4];
-      const bool own = take.n < p.N;
       const int tail = own && p.tokens > 1 ? max(0, take.length - p.tokens + 1) : take.length;  // keys from here on are not for all rows
       float top[2] = {-INFINITY, -INFINITY};
 #pragma unroll
@@ -325,7 +366,7 @@ __global__ void __launch_bounds__(kThreads, kResident) gdn_attention_kernel(cons
         for (int h = 0; h < 2; ++h)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            const int key = key0 + 8 * h + 2 * (lane & 3) + (e & 1), r = r0 + lane / 4 + 8 * (e >> 1);
+            const int key = key0 + 8 * h + 2 * (lane & 3) + (e & 1), r = u.r0 + lane / 4 + 8 * (e >> 1);
             const int seen = own ? take.length - p.tokens + 1 + r / p.group : take.length;
             if (key >= min(seen, take.length)) w[h][e] = -INFINITY;
           }
@@ -375,7 +416,7 @@ __global__ void __launch_bounds__(kThreads, kResident) gdn_attention_kernel(cons
           for (int i = 0; i < 2; ++i) {
             const float x0 = j < 8 ? w[0][2 * i] : w[1][2 * i], x1 = j < 8 ? w[0][2 * i + 1] : w[1][2 * i + 1];
             pj[i] = __shfl_sync(0xffffffffu, j & 1 ? x1 : x0, from);
-            const int r = r0 + lane / 4 + 8 * i;
+            const int r = u.r0 + lane / 4 + 8 * i;
             if (key0 + j >= take.length - p.tokens + 1 + r / p.group) pj[i] = -1.f;  // not seen
           }
 #pragma unroll
@@ -416,16 +457,25 @@ __global__ void __launch_bounds__(kThreads, kResident) gdn_attention_kernel(cons
         mma16<F16>(o[nt + 1], a, b[2], b[3]);
       }
     }
-    __syncwarp();
-    if (k + kStages < count && !dead) issue(k + kStages);
     const bool ends = take.t + 1 == take.tiles;
-    if (ends || k + 1 == count) {  // the warps' parts of the unit come together, half the columns at a time
+    if (ends || k + 1 == count) {  // the warps' parts of the unit come together, over the tile
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 1);
         sum[i] += __shfl_xor_sync(0xffffffffu, sum[i], 2);
-        if ((lane & 3) == 0) s.ml[warp * kRows + lane / 4 + 8 * i] = make_float2(base[i], unit_bad ? kBad : sum[i]);
+        if ((lane & 3) == 0) bar.ml[warp][lane / 4 + 8 * i] = make_float2(base[i], unit_bad ? kBad : sum[i]);
       }
+      float* join = reinterpret_cast<float*>(tile);   // [warp][16][128], columns by eights turned by the row
+      named_sync(1, 32 * kWarps);
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 16; ++j) {
+          const int at = lane / 4 + 8 * i;
+          *reinterpret_cast<float2*>(join + (warp * kRows + at) * kHeadDim + ((j ^ (at & 7)) * 8 + 2 * (lane & 3))) =
+              make_float2(o[j][2 * i], o[j][2 * i + 1]);
+        }
+      named_sync(1, 32 * kWarps);
       const int unit = take.n * subs + take.sub, worker = (int)blockIdx.x;
       const bool whole = starts && ends;
       if (tid == 0) {
@@ -433,24 +483,17 @@ __global__ void __launch_bounds__(kThreads, kResident) gdn_attention_kernel(cons
         if (ends) p.last_worker[unit] = worker;
       }
       const int64_t slot = whole ? 2 * p.workers + (int64_t)unit : 2 * worker + (starts ? 1 : 0);
-      const int row = tid / 8, cg = tid % 8, r = r0 + row;
+      const int cg = tid & 15;
 #pragma unroll
-      for (int half = 0; half < 2; ++half) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const int at = lane / 4 + 8 * i;
-            *reinterpret_cast<float2*>(s.join + (warp * kRows + at) * 64 + ((j ^ (at & 7)) * 8 + 2 * (lane & 3))) =
-                make_float2(o[8 * half + j][2 * i], o[8 * half + j][2 * i + 1]);
-          }
-        __syncthreads();
+      for (int i = 0; i < 2; ++i) {
+        const int row = tid / 16 + 8 * i, r = u.r0 + row;
+        if (row >= u.rows) break;
         float2 ml[kWarps];
         float top = -INFINITY, l = 0.f, x[8] = {};
         bool bad = false;
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
-          ml[w] = s.ml[w * kRows + row];
+          ml[w] = bar.ml[w][row];
           top = fmaxf(top, ml[w].x);
           bad |= ml[w].y == kBad;
         }
@@ -458,61 +501,59 @@ __global__ void __launch_bounds__(kThreads, kResident) gdn_attention_kernel(cons
 #pragma unroll
         for (int w = 0; w < kWarps; ++w) {
           const float f = exp2_fast(ml[w].x - from_base);
-          const float4* y = reinterpret_cast<const float4*>(s.join + (w * kRows + row) * 64 + (cg ^ (row & 7)) * 8);
+          const float4* y = reinterpret_cast<const float4*>(join + (w * kRows + row) * kHeadDim + (cg ^ (row & 7)) * 8);
           const float4 y0 = y[0], y1 = y[1];
           l = fmaf(f, ml[w].y, l);
           x[0] = fmaf(f, y0.x, x[0]); x[1] = fmaf(f, y0.y, x[1]); x[2] = fmaf(f, y0.z, x[2]); x[3] = fmaf(f, y0.w, x[3]);
           x[4] = fmaf(f, y1.x, x[4]); x[5] = fmaf(f, y1.y, x[5]); x[6] = fmaf(f, y1.z, x[6]); x[7] = fmaf(f, y1.w, x[7]);
         }
-        if (row < rows) {
-          if (whole && !p.prefix) {
-            if (!bad) {
-              const float inv = top == -INFINITY && l == 0.f ? 0.f : 1.f / l;
+        if (whole && !p.prefix) {
+          if (!bad) {
+            const float inv = top == -INFINITY && l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
-              for (int e = 0; e < 8; ++e) x[e] *= inv;
-              const int64_t token = tok0 + r / p.group;
-              const int head = head0 + r % p.group;
-              *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + token * p.o_st + head * p.o_sh + 64 * half + 8 * cg) = pack16x8<F16>(x);
-              if (p.lse && half == 0 && cg == 0)
-                p.lse[token * p.lse_st + head] = top == -INFINITY && l == 0.f ? -INFINITY : (from_base + log2f(l)) * kLn2;
-            }
-          } else {
-            float4* y = reinterpret_cast<float4*>(p.part_o + (slot * p.block_rows + row) * kHeadDim + 64 * half + 8 * cg);
-            y[0] = make_float4(x[0], x[1], x[2], x[3]);
-            y[1] = make_float4(x[4], x[5], x[6], x[7]);
-            if (half == 0 && cg == 0)
-              *reinterpret_cast<float2*>(p.part_ml + (slot * p.block_rows + row) * 2) = make_float2(top, bad ? kBad : l);
+            for (int e = 0; e < 8; ++e) x[e] *= inv;
+            const int64_t token = u.tok0 + r / p.group;
+            const int head = u.head0 + r % p.group;
+            *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + token * p.o_st + head * p.o_sh + 8 * cg) = pack16x8<F16>(x);
+            if (p.lse && cg == 0)
+              p.lse[token * p.lse_st + head] = top == -INFINITY && l == 0.f ? -INFINITY : (from_base + log2f(l)) * kLn2;
           }
+        } else {
+          float4* y = reinterpret_cast<float4*>(p.part_o + (slot * p.block_rows + row) * kHeadDim + 8 * cg);
+          y[0] = make_float4(x[0], x[1], x[2], x[3]);
+          y[1] = make_float4(x[4], x[5], x[6], x[7]);
+          if (cg == 0) *reinterpret_cast<float2*>(p.part_ml + (slot * p.block_rows + row) * 2) = make_float2(top, bad ? kBad : l);
         }
-        __syncthreads();
       }
+      fence_proxy_async_smem();
+      named_sync(1, 32 * kWarps);   // the sums before the next unit's, too
     }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar.empty[stage]);
     if (k + 1 < count) take.next(p, lane);
   }
-  // Copies that are still on their way after a wait ran out end before the memory is another's.
-  for (int k = dead_at; k < min(count, dead_at + kStages); ++k)
-    if (!(p.hold_copies && k == 0)) mbar_wait(&full[k % kStages], (k / kStages) & 1, 200000000ull);
+  grid_wait();
 }
 
-// The parts of the units that were cut, and those of the prefix: one CTA for each row, its warps taking
-// turns at the parts, lanes four columns each.
-template <bool F16>
-__global__ void __launch_bounds__(kThreads) gdn_attention_join_kernel(const __grid_constant__ AttentionParams p) {
-  __shared__ float s_o[kWarps][kHeadDim];
-  __shared__ float2 s_ml[kWarps];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  const int unit = (int)(blockIdx.x / (unsigned)p.block_rows), row = (int)(blockIdx.x % (unsigned)p.block_rows);
-  const int subs = p.H_k * p.blocks, n = unit / subs, hk = unit % subs / p.blocks;
-  const int r = unit % p.blocks * kRows + row;
+// The parts of the units that were cut, and those of the prefix: `kPer` warps for each row take turns at its
+// parts, four on their way at a time, lanes four columns each.
+template <bool F16, int kPer>
+__global__ void __launch_bounds__(kPer > 4 ? 32 * kPer : 128) gdn_attention_join_kernel(const __grid_constant__ AttentionParams p) {
+  constexpr int kRowsHere = kPer >= 4 ? 1 : 4 / kPer;
+  __shared__ float s_o[kPer][kHeadDim];
+  __shared__ float2 s_ml[kPer];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5 & (kPer - 1);
+  const int64_t id = (int64_t)blockIdx.x * kRowsHere + (kPer >= 4 ? 0 : threadIdx.x >> 5);
+  grid_wait();
+  if (id >= (int64_t)p.N * p.H_k * p.blocks * p.block_rows) return;
+  const int unit = (int)(id / p.block_rows), row = (int)(id - (int64_t)unit * p.block_rows);
+  const int subs = p.H_k * p.blocks, n = unit / subs, sub = unit - n * subs, hk = sub / p.blocks;
+  const int r = (sub - hk * p.blocks) * kRows + row;
   if (r >= p.tokens * p.group) return;
   const int length = length_of(p, n);
-  if (length < 0) return;
-  int first = 0, own = 0;  // the sequence's own parts: of worker `first` and those behind it, or one of a whole unit
-  if (length > 0) {
-    first = p.first_worker[unit];
-    own = p.last_worker[unit] - first + 1;
-  }
-  if (own == 1 && !p.prefix) return;  // it is in the output
+  // the sequence's own parts: of worker `first` and those behind it, or one of a whole unit
+  int first = p.first_worker[unit], own = p.last_worker[unit] - first + 1;
+  if (length <= 0) first = own = 0;
   // the prefix' parts of the row, of this kind's workers or of those of the prefix kernel
   int prefix_first = 0, shared = 0, prefix_unit = 0;
   const int pr = n * p.tokens * p.group + r;
@@ -527,48 +568,92 @@ __global__ void __launch_bounds__(kThreads) gdn_attention_join_kernel(const __gr
     prefix_first = p.first_worker[prefix_unit];
     shared = p.last_worker[prefix_unit] - prefix_first + 1;
   }
-  float top = -INFINITY, l = 0.f;
-  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (length < 0 || (own == 1 && !p.prefix)) return;  // none, or it is in the output
   // parts of no worker: the kernel before this one gave up, and said so
   bool bad = first < 0 || own < 0 || first + own > p.workers || prefix_first < 0 || shared < 0 ||
              prefix_first + shared > (many ? p.prefix_workers : p.workers);
   if (bad) own = shared = 0;
-#pragma unroll 4
-  for (int i = warp; i < own + shared; i += kWarps) {
-    const bool of_prefix = i >= own;
-    const int j = of_prefix ? i - own : i, parts = of_prefix ? shared : own, w = (of_prefix ? prefix_first : first) + j;
-    const bool of_many = of_prefix && many;
-    const int workers = of_many ? p.prefix_workers : p.workers;
-    const int64_t slot = parts == 1 ? 2 * (int64_t)workers + (of_prefix ? prefix_unit : unit) : 2 * w + (j == 0 ? 1 : 0);
-    const int64_t at = of_many ? slot * kPrefixRows + pr % kPrefixRows : slot * p.block_rows + (of_prefix ? pr % kRows : row);
-    const float2 ml = *reinterpret_cast<const float2*>((of_many ? p.prefix_ml : p.part_ml) + 2 * at);
-    const float4 x = *reinterpret_cast<const float4*>((of_many ? p.prefix_o : p.part_o) + at * kHeadDim + 4 * lane);
-    bad |= ml.y == kBad;
-    const float now = fmaxf(top, ml.x), from_base = now == -INFINITY ? 0.f : now;
-    const float keep = exp2_fast(top - from_base), f = exp2_fast(ml.x - from_base);
+  float top = -INFINITY, l = 0.f;
+  float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int i0 = warp; i0 < own + shared; i0 += 4 * kPer) {
+    float2 ml[4];
+    float4 x[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int i = i0 + e * kPer;
+      const bool of_prefix = i >= own, of_many = of_prefix && many;
+      const int j = of_prefix ? i - own : i, parts = of_prefix ? shared : own, w = (of_prefix ? prefix_first : first) + j;
+      const int workers = of_many ? p.prefix_workers : p.workers;
+      const int64_t slot = parts == 1 ? 2 * (int64_t)workers + (of_prefix ? prefix_unit : unit) : 2 * w + (j == 0 ? 1 : 0);
+      const int64_t at = of_many ? slot * kPrefixRows + pr % kPrefixRows : slot * p.block_rows + (of_prefix ? pr % kRows : row);
+      ml[e] = make_float2(-INFINITY, 0.f);
+      x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (i < own + shared) {
+        ml[e] = *reinterpret_cast<const float2*>((of_many ? p.prefix_ml : p.part_ml) + 2 * at);
+        x[e] = *reinterpret_cast<const float4*>((of_many ? p.prefix_o : p.part_o) + at * kHeadDim + 4 * lane);
+      }
+    }
+    float now = top;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      now = fmaxf(now, ml[e].x);
+      bad |= ml[e].y == kBad;
+    }
+    const float from_base = now == -INFINITY ? 0.f : now, keep = exp2_fast(top - from_base);
     top = now;
-    l = l * keep + f * ml.y;
-    o = make_float4(o.x * keep + f * x.x, o.y * keep + f * x.y, o.z * keep + f * x.z, o.w * keep + f * x.w);
-  }
-  reinterpret_cast<float4*>(s_o[warp])[lane] = o;
-  if (lane == 0) s_ml[warp] = make_float2(top, l);
-  if (__syncthreads_or(bad)) return;
-  float total = 0.f, x = 0.f;
-  top = -INFINITY;
+    l *= keep;
+    o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
 #pragma unroll
-  for (int w = 0; w < kWarps; ++w) top = fmaxf(top, s_ml[w].x);
+    for (int e = 0; e < 4; ++e) {
+      const float f = exp2_fast(ml[e].x - from_base);
+      l = fmaf(f, ml[e].y, l);
+      o = make_float4(fmaf(f, x[e].x, o.x), fmaf(f, x[e].y, o.y), fmaf(f, x[e].z, o.z), fmaf(f, x[e].w, o.w));
+    }
+  }
+  if constexpr (kPer > 1) {
+    reinterpret_cast<float4*>(s_o[warp])[lane] = o;
+    if (lane == 0) s_ml[warp] = make_float2(top, l);
+    bad = __syncthreads_or(bad);
+    if (warp > 0) return;
+    top = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kPer; ++w) top = fmaxf(top, s_ml[w].x);
+    const float from_base = top == -INFINITY ? 0.f : top;
+    l = 0.f;
+    o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int w = 0; w < kPer; ++w) {
+      const float f = exp2_fast(s_ml[w].x - from_base);
+      const float4 x = reinterpret_cast<const float4*>(s_o[w])[lane];
+      l = fmaf(f, s_ml[w].y, l);
+      o = make_float4(fmaf(f, x.x, o.x), fmaf(f, x.y, o.y), fmaf(f, x.z, o.z), fmaf(f, x.w, o.w));
+    }
+  }
+  if (bad) return;
   const float from_base = top == -INFINITY ? 0.f : top;
-#pragma unroll
-  for (int w = 0; w < kWarps; ++w) {
-    const float f = exp2_fast(s_ml[w].x - from_base);
-    total += f * s_ml[w].y;
-    x += f * s_o[w][threadIdx.x];
-  }
-  const bool none = top == -INFINITY && total == 0.f;
+  const bool none = top == -INFINITY && l == 0.f;
+  const float inv = none ? 0.f : 1.f / l;
   const int64_t token = n * (int64_t)p.tokens + r / p.group;
   const int head = hk * p.group + r % p.group;
-  reinterpret_cast<uint16_t*>(p.out)[token * p.o_st + head * p.o_sh + threadIdx.x] = (uint16_t)pack16x2<F16>(none ? 0.f : x / total, 0.f);
-  if (p.lse && threadIdx.x == 0) p.lse[token * p.lse_st + head] = none ? -INFINITY : (from_base + log2f(total)) * kLn2;
+  *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + token * p.o_st + head * p.o_sh + 4 * lane) =
+      make_uint2(pack16x2<F16>(o.x * inv, o.y * inv), pack16x2<F16>(o.z * inv, o.w * inv));
+  if (p.lse && lane == 0) p.lse[token * p.lse_st + head] = none ? -INFINITY : (from_base + log2f(l)) * kLn2;
+}
+
+// A kernel that may start before the one in front of it has ended (it waits for it itself).
+template <typename Kernel>
+cudaError_t launch_behind(Kernel kernel, int64_t grid, int threads, int smem, bool behind, const AttentionParams& p, cudaStream_t stream) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)grid);
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = stream;
+  cudaLaunchAttribute a;
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &a;
+  c.numAttrs = behind ? 1 : 0;
+  return cudaLaunchKernelEx(&c, kernel, p);
 }
 
 template <bool F16>
@@ -583,15 +668,22 @@ cudaError_t launch(const AttentionParams& p, cudaStream_t stream) {
     generation = launch_config_generation();
     device = dev;
   }
-  const int64_t subs = (int64_t)p.H_k * p.blocks;
-  const int64_t most = ((int64_t)p.max_pages * p.page_size + kTile - 1) / kTile * p.N * subs +
+  const int64_t subs = (int64_t)p.H_k * p.blocks, own_units = p.N * subs;
+  const int64_t most = ((int64_t)p.max_pages * p.page_size + kTile - 1) / kTile * own_units +
                        ((int64_t)p.prefix + kTile - 1) / kTile * p.H_k * p.prefix_blocks;
-  if (p.prefix_units > 0 && (e = launch_attention_prefix(p, stream)) != cudaSuccess) return e;
-  if (most) gdn_attention_kernel<F16><<<(unsigned)std::min<int64_t>(p.workers, most), kThreads, kSmemBytes, stream>>>(p);
-  e = cudaGetLastError();
-  if (e != cudaSuccess) return e;
-  gdn_attention_join_kernel<F16><<<(unsigned)(p.N * subs * p.block_rows), kThreads, 0, stream>>>(p);
-  return cudaGetLastError();
+  const bool many = p.prefix_units > 0;
+  if (many && (e = launch_attention_prefix(p, stream)) != cudaSuccess) return e;
+  if (most) {
+    e = launch_behind(gdn_attention_kernel<F16>, std::min<int64_t>(p.workers, most), kThreads, kSmemBytes, many, p, stream);
+    if (e != cudaSuccess) return e;
+  }
+  // Warps a row by the parts that a row has about: 16 rows of 152 parts each take 5 us with sixteen, 26 with four.
+  int64_t parts = 1 + p.workers / (own_units + p.H_k * p.prefix_blocks);
+  if (many) parts += 1 + p.prefix_workers / ((int64_t)p.H_k * p.prefix_units);
+  const int64_t rows = own_units * p.block_rows;
+  if (parts <= 8) return launch_behind(gdn_attention_join_kernel<F16, 1>, (rows + 3) / 4, 128, 0, true, p, stream);
+  if (parts <= 32) return launch_behind(gdn_attention_join_kernel<F16, 4>, rows, 128, 0, true, p, stream);
+  return launch_behind(gdn_attention_join_kernel<F16, 16>, rows, 512, 0, true, p, stream);
 }
 
 }  // namespace

@@ -7,6 +7,7 @@
 
 namespace gdn {
 
+constexpr int kOwnKeys = 64;                         // keys of a tile of attention.cu
 constexpr int kPrefixKeys = 128, kPrefixRows = 256;  // tiles of attention_prefix.cu
 constexpr float kAttentionBad = -1.f;                // as a part's sum: it met a bad page, or gave up
 
@@ -26,7 +27,7 @@ struct AttentionParams {
   int32_t* dev_err;
   int64_t pages;
   int32_t N, tokens, H_q, H_k, group, page_size, max_pages, prefix;
-  int32_t box_rows;  // places of a box: 16, or 8 where a page is not a multiple of 16
+  int32_t box_rows;  // places of a box
   int32_t table_dtype, len_dtype, prefix_dtype;
   float scale;
   int32_t op_f16;

@@ -92,6 +92,7 @@ template <bool F16>
 __global__ void __launch_bounds__(kThreads, 1) gdn_attention_prefix_kernel(const __grid_constant__ AttentionParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
   Bars& bar = *reinterpret_cast<Bars*>(smem + kBars);
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // what comes next does not wait for this kernel to begin with
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = warp >> 2;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
