@@ -558,11 +558,13 @@ __global__ void __launch_bounds__(kPer > 4 ? 32 * kPer : 128) gdn_attention_join
   int prefix_first = 0, shared = 0, prefix_unit = 0;
   const int pr = n * p.tokens * p.group + r;
   const bool many = p.prefix_units > 0;
+  int turns = 1;  // sums of the row that a worker of the prefix kernel has
   if (many) {
     prefix_unit = hk * p.prefix_units + pr / kPrefixRows;
     const int64_t tiles = (p.prefix + kPrefixKeys - 1) / kPrefixKeys, total = tiles * p.H_k * p.prefix_units, at = prefix_unit * tiles;
     prefix_first = (int)(((at + 1) * p.prefix_workers - 1) / total);   // the worker whose share holds tile `at`
     shared = (int)(((at + tiles) * p.prefix_workers - 1) / total) - prefix_first + 1;
+    turns = p.N * p.tokens * p.group - pr / kPrefixRows * kPrefixRows <= 128 ? 2 : 1;
   } else if (p.prefix) {
     prefix_unit = p.N * subs + hk * p.prefix_blocks + pr / kRows;
     prefix_first = p.first_worker[prefix_unit];
@@ -573,24 +575,29 @@ __global__ void __launch_bounds__(kPer > 4 ? 32 * kPer : 128) gdn_attention_join
   bool bad = first < 0 || own < 0 || first + own > p.workers || prefix_first < 0 || shared < 0 ||
              prefix_first + shared > (many ? p.prefix_workers : p.workers);
   if (bad) own = shared = 0;
+  const int parts_all = own + shared * turns;
   float top = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = warp; i0 < own + shared; i0 += 4 * kPer) {
+  for (int i0 = warp; i0 < parts_all; i0 += 4 * kPer) {
     float2 ml[4];
     float4 x[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int i = i0 + e * kPer;
       const bool of_prefix = i >= own, of_many = of_prefix && many;
-      const int j = of_prefix ? i - own : i, parts = of_prefix ? shared : own, w = (of_prefix ? prefix_first : first) + j;
+      const int j2 = of_prefix ? i - own : i, j = of_prefix && turns == 2 ? j2 >> 1 : j2, turn = of_prefix && turns == 2 ? j2 & 1 : 0;
+      const int parts = of_prefix ? shared : own, w = (of_prefix ? prefix_first : first) + j;
       const int workers = of_many ? p.prefix_workers : p.workers;
       const int64_t slot = parts == 1 ? 2 * (int64_t)workers + (of_prefix ? prefix_unit : unit) : 2 * w + (j == 0 ? 1 : 0);
-      const int64_t at = of_many ? slot * kPrefixRows + pr % kPrefixRows : slot * p.block_rows + (of_prefix ? pr % kRows : row);
+      const int64_t at = of_many ? slot * kPrefixRows + pr % kPrefixRows + 128 * turn : slot * p.block_rows + (of_prefix ? pr % kRows : row);
       ml[e] = make_float2(-INFINITY, 0.f);
       x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i < own + shared) {
+      if (i < parts_all) {
         ml[e] = *reinterpret_cast<const float2*>((of_many ? p.prefix_ml : p.part_ml) + 2 * at);
-        x[e] = *reinterpret_cast<const float4*>((of_many ? p.prefix_o : p.part_o) + at * kHeadDim + 4 * lane);
+        const float* y = of_many ? p.prefix_o + (slot * kHeadDim + lane / 2 * 8) * kPrefixRows + (pr % kPrefixRows + 128 * turn) * 8 + (lane & 1) * 4
+                                 : p.part_o + at * kHeadDim + 4 * lane;
+        x[e] = *reinterpret_cast<const float4*>(y);
+        if (ml[e].y == 0.f) x[e] = make_float4(0.f, 0.f, 0.f, 0.f);  // no key: nothing was written
       }
     }
     float now = top;

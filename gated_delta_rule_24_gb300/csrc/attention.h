@@ -43,7 +43,7 @@ struct AttentionParams {
   CUtensorMap tm_pk;  // as tm_k, boxes of prefix_box places
   CUtensorMap tm_pv;
   int32_t prefix_box, prefix_units, prefix_workers;
-  float* prefix_o;   // [slots][kPrefixRows][128]
+  float* prefix_o;   // [slots][16][kPrefixRows][8]: columns by eights
   float* prefix_ml;  // [slots][kPrefixRows][2]
   // Testing aids: the bound of every wait in ns (0: 0.2 s), and the first copy of every warp withheld.
   int32_t hold_copies;

@@ -13,9 +13,12 @@
 //   O += P V (tcgen05, P from TMEM, O in TMEM),
 //
 // and while four warps make A's weights, the tensor cores are at B's products, and the other way round.  A
+// (P comes in two halves, and the first goes into the product while the second is made.)  A
 // base moves only when a score exceeds it by 2^8, so that O is seldom read back to be scaled: the weights
 // grow to 2^8 at most, which changes no rounding.  When S of a tile is there, all products issued before it
 // are done, so a row's thread may scale O then without a hand-off of its own.
+//
+// Where a unit has no more than 128 rows, A and B are the same rows and take every other tile of keys, each with sums of its own.
 //
 // Units are (key head, 256 rows), a unit's tiles of 128 keys come one behind the other, and all units'
 // tiles are cut into equal shares for the SMs; the parts are joined by attention.cu's second kernel.
@@ -63,7 +66,7 @@ __device__ __forceinline__ void loaded(uint32_t (&r)[32]) {
 
 struct Bars {
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], done;
+  uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], done;
   uint32_t tmem, bad;
 };
 
@@ -104,7 +107,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_attention_prefix_kernel(const
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bar.q_full[i], 128);
       mbar_init(&bar.s_full[i], 1);
-      mbar_init(&bar.p_full[i], 128);
+      for (int h = 0; h < 2; ++h) mbar_init(&bar.p_full[i][h], 128);
       mbar_init(&bar.o_full[i], 1);
     }
     mbar_init(&bar.done, 1);
@@ -123,6 +126,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_attention_prefix_kernel(const
   const uint64_t limit = p.wait_ns ? p.wait_ns : kWaitNs;
   const int rows_all = p.N * p.tokens * p.group;
   Share share(p);
+  const auto turns = [&] { return rows_all - share.unit % p.prefix_units * kPrefixRows <= 128; };  // A and B take turns at the tiles
 
   if (group == 2) {
     if (warp == 8) {  // copies
@@ -174,57 +178,84 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_attention_prefix_kernel(const
       const bool one = elect_one();
       bool dead = false;
       uint32_t step = 0, steps[2] = {0, 0}, pieces[2] = {0, 0};
-      const uint32_t sdesc_rows = 1024;
-      constexpr uint32_t id_s = idesc_16_f32(F16, 128, 128, 0, 0, 0), id_o = idesc_16_f32(F16, 128, 128, 0, 1, 0);
+      const uint32_t id_s = p.scale < 0.f ? idesc_16_f32(F16, 128, 128, 0, 0, 1) : idesc_16_f32(F16, 128, 128, 0, 0, 0);
+      constexpr uint32_t id_o = idesc_16_f32(F16, 128, 128, 0, 1, 0);
       const uint32_t q_at = smem_u32(smem + kQ), k_at = smem_u32(smem + kK), v_at = smem_u32(smem + kV);
       auto wait = [&](uint64_t* b, uint32_t parity) {
         if (!dead && !__all_sync(0xffffffffu, mbar_wait(b, parity & 1, limit))) dead = true;
         tc_fence_after();
       };
-      auto scores = [&](int x, uint32_t st) {
+      auto commit = [&](uint64_t* b) {
+        if (one && !dead) mma_commit(b);
+        __syncwarp();
+      };
+      auto scores = [&](int x, int rows, uint32_t st) {  // S of A or B, with the rows of tile `rows`
         if (one && !dead) {
-          const uint32_t a = q_at + x * kTileBytes, b = k_at + st * kTileBytes;
+          const uint32_t a = q_at + rows * kTileBytes, b = k_at + st * kTileBytes;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-            mma_ss(tmem + kS + 128 * x, sdesc_sw128(a + off, 16, sdesc_rows), sdesc_sw128(b + off, 16, sdesc_rows), id_s, kk > 0);
+            mma_ss(tmem + kS + 128 * x, sdesc_sw128(a + off, 16, 1024), sdesc_sw128(b + off, 16, 1024), id_s, kk > 0);
           }
           mma_commit(&bar.s_full[x]);
         }
         __syncwarp();
       };
-      auto values = [&](int x, uint32_t st, bool more) {
-        if (one && !dead) {
-          const uint32_t b = v_at + st * kTileBytes;
+      auto values = [&](int x, uint32_t at, bool more) {  // O of A or B, of the values of step `at`
+        const uint32_t st = at % kStages, b = v_at + st * kTileBytes;
+        for (int h = 0; h < 2; ++h) {
+          wait(&bar.p_full[x][h], steps[x]);
+          if (h == 0) wait(&bar.v_full[st], at / kStages);
+          if (one && !dead) {
 #pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            mma_ts(tmem + kO + 128 * x, tmem + kS + 128 * x + 8 * kk, sdesc_sw128(b + kk * 2048, kHalf, 1024), id_o, more || kk > 0);
+            for (int k4 = 0; k4 < 4; ++k4) {
+              const int kk = 4 * h + k4;
+              mma_ts(tmem + kO + 128 * x, tmem + kS + 128 * x + 8 * kk, sdesc_sw128(b + kk * 2048, kHalf, 1024), id_o, more || kk > 0);
+            }
+          }
+          __syncwarp();
         }
-        __syncwarp();
-      };
-      auto commit = [&](uint64_t* b) {
-        if (one && !dead) mma_commit(b);
-        __syncwarp();
+        ++steps[x];
       };
       while (!dead && share.next()) {
-        const int both = rows_all - share.unit % p.prefix_units * kPrefixRows > 128 ? 2 : 1;
-        for (int x = 0; x < both; ++x) {
+        const uint32_t n = share.n;
+        if (turns()) {
+          wait(&bar.q_full[0], pieces[0]++);
+          for (uint32_t i = 0; i < min(n, 2u); ++i) {
+            wait(&bar.k_full[(step + i) % kStages], (step + i) / kStages);
+            scores(i, 0, (step + i) % kStages);
+            commit(&bar.k_empty[(step + i) % kStages]);
+          }
+          for (uint32_t i = 0; i < n && !dead; ++i) {
+            const uint32_t x = i & 1, at = step + i, ahead = at + 2;
+            values(x, at, i > 1);
+            commit(&bar.v_empty[at % kStages]);
+            if (i + 2 < n) {
+              wait(&bar.k_full[ahead % kStages], ahead / kStages);
+              scores(x, 0, ahead % kStages);
+              commit(&bar.k_empty[ahead % kStages]);
+            } else {
+              commit(&bar.o_full[x]);
+            }
+          }
+          step += n;
+          continue;
+        }
+        for (int x = 0; x < 2; ++x) {
           wait(&bar.q_full[x], pieces[x]++);
           if (x == 0) wait(&bar.k_full[step % kStages], step / kStages);
-          scores(x, step % kStages);
+          scores(x, x, step % kStages);
         }
         commit(&bar.k_empty[step % kStages]);
-        for (int i = 0; i < share.n && !dead; ++i, ++step) {
-          const uint32_t st = step % kStages, ahead = step + 1;
-          for (int x = 0; x < both; ++x) {
-            wait(&bar.p_full[x], steps[x]++);
-            if (x == 0) wait(&bar.v_full[st], step / kStages);
-            values(x, st, i > 0);
-            if (x + 1 == both) commit(&bar.v_empty[st]);
-            if (i + 1 < share.n) {
+        for (uint32_t i = 0; i < n && !dead; ++i, ++step) {
+          const uint32_t ahead = step + 1;
+          for (int x = 0; x < 2; ++x) {
+            values(x, step, i > 0);
+            if (x == 1) commit(&bar.v_empty[step % kStages]);
+            if (i + 1 < n) {
               if (x == 0) wait(&bar.k_full[ahead % kStages], ahead / kStages);
-              scores(x, ahead % kStages);
-              if (x + 1 == both) commit(&bar.k_empty[ahead % kStages]);
+              scores(x, x, ahead % kStages);
+              if (x == 1) commit(&bar.k_empty[ahead % kStages]);
             } else {
               commit(&bar.o_full[x]);
             }
@@ -242,41 +273,37 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_attention_prefix_kernel(const
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t s_at = tmem + kS + 128 * x + lanes, o_at = tmem + kO + 128 * x + lanes;
     const float c = fabsf(p.scale) * kLog2e;
-    const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
     constexpr float kBias = F16 ? 6.f : 0.f;
     bool dead = false;
-    uint32_t steps = 0, pieces = 0, at_step = 0;
+    uint32_t steps = 0, pieces = 0, first = 0;   // `first`: the piece's first step
     auto wait = [&](uint64_t* b, uint32_t parity) {
       if (!dead && !__all_sync(0xffffffffu, mbar_wait(b, parity & 1, limit))) {
         dead = true;
         if (lane == 0) atomicOr(p.dev_err, kDevErrTimeout);
       }
     };
-    while (share.next()) {
-      const int unit_row = share.unit % p.prefix_units * kPrefixRows;
-      if (rows_all - unit_row <= 128 * x) {  // no rows for B
-        at_step += share.n;
-        continue;
-      }
-      const int r = unit_row + 128 * x + i128, head = share.unit / p.prefix_units * p.group;
-      // the rows of Q, one by half a warp each time
+    for (; share.next(); first += share.n) {
+      const bool turn = turns();
+      const int unit_row = share.unit % p.prefix_units * kPrefixRows, row0 = unit_row + (turn ? 0 : 128 * x), r = row0 + i128;
+      if (!turn || x == 0) {  // the rows of Q, half a warp a row, all on their way at once
+        const int head = share.unit / p.prefix_units * p.group, chunk = lane & 15;
+        const uint16_t* q = reinterpret_cast<const uint16_t*>(p.q) + 8 * chunk;
+        const uint32_t to = smem_u32(smem + kQ + x * kTileBytes + (chunk >> 3) * kHalf);
 #pragma unroll 4
-      for (int j = 0; j < 16; ++j) {
-        const int rr = (warp & 3) * 32 + 2 * j + (lane >> 4), chunk = lane & 15, row = unit_row + 128 * x + rr;
-        uint4 v = make_uint4(0, 0, 0, 0);
-        if (row < rows_all) {
-          v = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(p.q) + (int64_t)(row / p.group) * p.q_st +
-                                              (int64_t)(head + row % p.group) * p.q_sh + 8 * chunk);
-          v.x ^= flip; v.y ^= flip; v.z ^= flip; v.w ^= flip;
+        for (int j = 0; j < 16; ++j) {
+          const int rr = (warp & 3) * 32 + 2 * j + (lane >> 4), row = row0 + rr, token = row / p.group;
+          const bool some = row < rows_all;
+          const uint16_t* from = some ? q + (int64_t)token * p.q_st + (int64_t)(head + row - token * p.group) * p.q_sh : q;
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + sw128_chunk(rr, chunk & 7)), "l"(from), "r"(some ? 16 : 0) : "memory");
         }
-        *reinterpret_cast<uint4*>(smem + kQ + x * kTileBytes + (chunk >> 3) * kHalf + sw128_chunk(rr, chunk & 7)) = v;
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        fence_proxy_async_smem();
+        mbar_arrive(&bar.q_full[x]);
       }
-      fence_proxy_async_smem();
-      mbar_arrive(&bar.q_full[x]);
       float base = -INFINITY;
       float2 sum = make_float2(0.f, 0.f);
 #pragma unroll 1
-      for (int i = 0; i < share.n; ++i, ++at_step) {
+      for (int i = turn ? x : 0; i < share.n; i += turn ? 2 : 1) {
         wait(&bar.s_full[x], steps++);
         if (dead) continue;
         tc_fence_after();
@@ -310,9 +337,10 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_attention_prefix_kernel(const
         loaded(s1);
         largest(0, s0);
         largest(1, s1);
-        if (valid < kPrefixKeys && x == 0) {  // values of no key have a weight of zero, but must not be infinite either
-          wait(&bar.v_full[at_step % kStages], at_step / kStages);
-          uint8_t* v = smem + kV + (at_step % kStages) * kTileBytes;
+        if (valid < kPrefixKeys && (x == 0 || turn)) {  // values of no key have a weight of zero, but must not be infinite either
+          const uint32_t at = first + i;
+          wait(&bar.v_full[at % kStages], at / kStages);
+          uint8_t* v = smem + kV + (at % kStages) * kTileBytes;
           for (int e = i128; e < (kPrefixKeys - valid) * 16; e += 128)
             *reinterpret_cast<uint4*>(v + (e & 8 ? kHalf : 0) + (valid + e / 16) * 128 + (e & 7) * 16) = make_uint4(0, 0, 0, 0);
           fence_proxy_async_smem();
@@ -324,7 +352,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_attention_prefix_kernel(const
           const float keep = now == -INFINITY || now == base ? 1.f : exp2_fast(base - now);
           base = now;
           sum = mul2(sum, pair(keep));
-          if (i > 0) {
+          if (i > (turn ? 1 : 0)) {
 #pragma unroll 1
             for (int h = 0; h < 4; ++h) {
               uint32_t o[32];
@@ -359,35 +387,41 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_attention_prefix_kernel(const
         loaded(s2);
         tmem_ld32(s_at + 96, s0);
         weights(1, s1, false);
+        tmem_st_wait();
+        tc_fence_before();
+        mbar_arrive(&bar.p_full[x][0]);
         weights(2, s2, valid < kPrefixKeys);
         loaded(s0);
         weights(3, s0, valid < kPrefixKeys);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(&bar.p_full[x]);
+        mbar_arrive(&bar.p_full[x][1]);
       }
-      wait(&bar.o_full[x], pieces++);
+      const bool some = !turn || x < share.n;  // tiles for this group
+      if (some) wait(&bar.o_full[x], pieces++);
       tc_fence_after();
-      const bool whole = share.t0 == 0 && share.n == share.tiles;
+      const bool whole = share.t0 == 0 && share.n == share.tiles, write = r < rows_all;
       const int64_t slot = whole ? 2 * (int64_t)gridDim.x + share.unit : 2 * (int64_t)blockIdx.x + (share.t0 == 0 ? 1 : 0);
-      const int64_t at = slot * kPrefixRows + 128 * x + i128;
-      const bool write = r < rows_all;
-      if (!dead) {
+      const int row = 128 * x + i128;
+      if (some && !dead) {
+        float* y = p.prefix_o + slot * kPrefixRows * kHeadDim + row * 8;   // by eights of columns: a warp writes 1 KB in a row
 #pragma unroll 1
         for (int h = 0; h < 4; ++h) {
           uint32_t o[32];
           tmem_ld32(o_at + 32 * h, o);
           loaded(o);
           if (write) {
-            uint4* y = reinterpret_cast<uint4*>(p.prefix_o + at * kHeadDim + 32 * h);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) y[e] = make_uint4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+            for (int e = 0; e < 32; e += 8)
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(y + (4 * h + e / 8) * kPrefixRows * 8),
+                           "r"(o[e]), "r"(o[e + 1]), "r"(o[e + 2]), "r"(o[e + 3]), "r"(o[e + 4]), "r"(o[e + 5]), "r"(o[e + 6]), "r"(o[e + 7])
+                           : "memory");
           }
         }
       }
       if (write) {
         const bool bad = dead || *reinterpret_cast<volatile uint32_t*>(&bar.bad);
-        *reinterpret_cast<float2*>(p.prefix_ml + 2 * at) = make_float2(base, bad ? kAttentionBad : sum.x + sum.y);
+        *reinterpret_cast<float2*>(p.prefix_ml + 2 * (slot * kPrefixRows + row)) = make_float2(base, bad ? kAttentionBad : sum.x + sum.y);
       }
       tc_fence_before();
     }
