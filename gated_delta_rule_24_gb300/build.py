@@ -23,8 +23,9 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libgdn_gb300.so")
 PYCALL = os.path.join(BUILD, "gdn_pycall.so")
 PYCALL_SOURCE = os.path.join(CSRC, "pycall.c")
-SOURCES = ["prefill.cu", "decode.cu", "decay_prefill.cu", "decay_step.cu", "norm_rope.cu", "attention.cu", "attention_prefix.cu", "api.cpp"]
-HEADERS = [os.path.join(CSRC, f) for f in ("prefill.h", "decode.h", "decay.h", "decay.cuh", "attention.h", "ptx.cuh")] + [os.path.join(INCLUDE, "gdn.h")]
+SOURCES = ["prefill.cu", "decode.cu", "decay_prefill.cu", "decay_step.cu", "norm_rope.cu", "attention.cu", "api.cpp"]
+HEADERS = [os.path.join(CSRC, f) for f in ("prefill.h", "decode.h", "decay.h", "decay.cuh", "attention.h", "attention_common.cuh",
+                                               "attention_own.cuh", "attention_prefix.cuh", "ptx.cuh")] + [os.path.join(INCLUDE, "gdn.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 COMMON = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

@@ -1131,8 +1131,6 @@ gdn_status_t gdn_paged_attention_step(const gdn_tensor_t* q, const gdn_tensor_t*
   if (page_table->shape[1] > 1 && page_table->stride[1] != 1) return fail(GDN_ERR_INVALID_ARGUMENT, "page_table rows must be contiguous");
   constexpr int64_t kMostKeys = (int64_t(1) << 31) - (1 << 25);  // the tiles behind a length are int32, too
   if (page_table->shape[1] > kMostKeys / page_size) return fail(GDN_ERR_UNSUPPORTED, "page_table holds too many keys of a sequence");
-  if (N * Hq * tokens * (page_table->shape[1] * page_size / 64 + 1) >= (int64_t(1) << 38))
-    return fail(GDN_ERR_UNSUPPORTED, "page_table holds too many keys");
   if (prefix_length < 0) return fail(GDN_ERR_INVALID_ARGUMENT, "prefix_length must not be negative");
   if (prefix_length > kMostKeys) return fail(GDN_ERR_UNSUPPORTED, "prefix_length is too large");
   if (prefix_pages) {
@@ -1143,6 +1141,9 @@ gdn_status_t gdn_paged_attention_step(const gdn_tensor_t* q, const gdn_tensor_t*
   if (prefix_length && prefix_pages->shape[0] < (prefix_length + page_size - 1) / page_size)
     return fail(GDN_ERR_INVALID_ARGUMENT, "%lld prefix_pages hold fewer than %lld keys", (long long)prefix_pages->shape[0],
                 (long long)prefix_length);
+  const int64_t own_blocks = (tokens * (Hq / Hk) + 15) / 16, all_blocks = (T * (Hq / Hk) + 15) / 16;   // of 16 rows; tiles of 64 keys are counted in 32 bits
+  if (N * Hk * own_blocks * (page_table->shape[1] * page_size / gdn::kOwnKeys + 1) + Hk * all_blocks * (prefix_length / gdn::kOwnKeys + 1) >= (int64_t(1) << 31))
+    return fail(GDN_ERR_UNSUPPORTED, "page_table and prefix hold too many keys for the rows");
   if (!std::isfinite(scale)) return fail(GDN_ERR_INVALID_ARGUMENT, "scale must be finite");
   if ((st = check_qkv(output, "output")) != GDN_OK) return st;
   if (output->dtype != q->dtype) return fail(GDN_ERR_UNSUPPORTED, "output must have q's dtype");

@@ -7,8 +7,8 @@
 
 namespace gdn {
 
-constexpr int kOwnKeys = 64;                         // keys of a tile of attention.cu
-constexpr int kPrefixKeys = 128, kPrefixRows = 256;  // tiles of attention_prefix.cu
+constexpr int kOwnKeys = 64;                         // keys of a tile of attention_own.cuh
+constexpr int kPrefixKeys = 128, kPrefixRows = 256;  // tiles of attention_prefix.cuh
 constexpr float kAttentionBad = -1.f;                // as a part's sum: it met a bad page, or gave up
 
 struct AttentionParams {
@@ -39,10 +39,12 @@ struct AttentionParams {
   float* part_ml;              // [slots][block_rows][2]: base, sum
   int32_t* first_worker;       // [units], then
   int32_t* last_worker;        // [units]
-  // The prefix by attention_prefix.cu (prefix_blocks is then 0): units of a key head, workers, and their parts.
+  // The prefix by attention_prefix.cuh (prefix_blocks is then 0): units of a key head, workers at most, how many
+  // share the tiles, and their parts.
   CUtensorMap tm_pk;  // as tm_k, boxes of prefix_box places
   CUtensorMap tm_pv;
   int32_t prefix_box, prefix_units, prefix_workers;
+  int32_t* prefix_shares;
   float* prefix_o;   // [slots][16][kPrefixRows][8]: columns by eights
   float* prefix_ml;  // [slots][kPrefixRows][2]
   // Testing aids: the bound of every wait in ns (0: 0.2 s), and the first copy of every warp withheld.
@@ -52,7 +54,6 @@ struct AttentionParams {
 
 // Fills in what follows from the sizes (and the workspace, where it is given); returns the workspace's bytes.
 size_t plan_attention(AttentionParams* p, int sms, void* workspace);
-cudaError_t launch_attention_prefix(const AttentionParams& p, cudaStream_t stream);
 cudaError_t launch_attention(const AttentionParams& p, cudaStream_t stream);
 
 }  // namespace gdn

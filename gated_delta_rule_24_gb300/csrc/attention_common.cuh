@@ -1,0 +1,38 @@
+// What the kernels of the attention over a paged cache share.
+#pragma once
+#include <cuda_runtime.h>
+
+#include "attention.h"
+#include "decay.cuh"
+#include "ptx.cuh"
+
+namespace gdn {
+
+constexpr uint64_t kWaitNs = 200000000ull;
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
+constexpr float kRoom = 8.f;  // how far (powers of two) scores may exceed the base before it moves
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// `total` tiles in equal shares, the first ones a tile larger where that does not come out even.
+struct Shares {
+  uint32_t each, larger;
+  __device__ __forceinline__ Shares(uint32_t total, uint32_t shares) : each(total / shares), larger(total - total / shares * shares) {}
+  __device__ __forceinline__ uint32_t from(uint32_t share) const { return share * each + min(share, larger); }
+  __device__ __forceinline__ uint32_t share_of(uint32_t tile) const {
+    const uint32_t end = larger * (each + 1);
+    return tile < end ? tile / (each + 1) : larger + (tile - end) / each;
+  }
+};
+
+// Keys of sequence n in its own pages, or -1 where its length is none.
+__device__ __forceinline__ int length_of(const AttentionParams& p, int n) {
+  const int64_t x = index_at(p.lengths, p.len_dtype, n);
+  return x < 0 || x > (int64_t)p.max_pages * p.page_size ? -1 : (int)x;
+}
+
+}  // namespace gdn

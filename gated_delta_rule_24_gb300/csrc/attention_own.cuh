@@ -1,0 +1,533 @@
+// The own pages of the sequences in the attention over a paged cache: what a worker does with its share
+// (attention.cu says what workers, units and shares are).
+//
+// Each key and value is read once for up to 16 rows, 2 x 16 flops a byte at most: the kernel is bound by
+// HBM bandwidth as long as copies are always under way.  A warp of its own looks up pages and issues the tensor
+// copies (boxes of up to 64 places of a page) into a ring of three tiles, over the ends of units; with a unit's first
+// tile come its queries.  Four warps take 16 of a tile's keys each: scores (keys x rows) and sums (values x rows) by warp
+// products with eight rows, or two times eight, as the narrow side, so that few rows take few products and registers; weights
+// are passed on in registers.  The warps meet at the end of a unit only, over the memory of its last tile.
+#pragma once
+#include "attention_common.cuh"
+
+namespace gdn {
+namespace own {
+
+constexpr int kWarps = 4;                      // that compute; one more copies
+constexpr int kThreads = 32 * kWarps + 32;
+constexpr int kWarpKeys = 16, kTile = kWarps * kWarpKeys;
+static_assert(kTile == kOwnKeys, "boxes fit a tile");
+constexpr int kRows = 16;                      // rows of a unit
+constexpr int kStages = 3;
+constexpr int kHalfBytes = kTile * 128;        // 64 of a row's 128 values
+constexpr int kTileBytes = 4 * kHalfBytes;     // keys, then values
+constexpr int kQueryBytes = kRows * 256;
+static_assert(kWarps * kRows * kHeadDim * 4 == kTileBytes, "the warps' sums lie over a tile");
+struct Bars {
+  float2 ml[kWarps][kRows];
+  uint64_t full[kStages], empty[kStages];
+  uint32_t found[kWarps];                      // the share's start
+  uint32_t bad[kStages];                       // a page of the stage's tile is none
+};
+constexpr int kBytes = kStages * (kTileBytes + kQueryBytes) + sizeof(Bars);
+constexpr int kPlace = (kBytes + 1023) / 1024 * 1024;   // of a worker beside another
+
+template <bool F16>
+__device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  if constexpr (F16)
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+  else
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// A value that the compiler takes for new here: what is made of it is not kept in registers from before, over loops that need them.
+__device__ __forceinline__ int here(int x) {
+  asm volatile("" : "+r"(x));
+  return x;
+}
+
+__device__ __forceinline__ int tiles_of(int length) { return length > 0 ? (length + kTile - 1) / kTile : 0; }
+
+// A tile of the walk through all units: sequence n (N: the prefix), `sub` = key head * row blocks + row
+// block, tile t.  The lanes of a warp hold the lengths of 32 sequences.
+struct Walk {
+  int n, sub, t, tiles, length, subs;
+  int held, held_from;
+
+  __device__ __forceinline__ void hold(const AttentionParams& p, int lane) {
+    held_from = n;
+    held = n + lane < p.N ? length_of(p, n + lane) : 0;
+  }
+  __device__ __forceinline__ void enter(const AttentionParams& p, int lane) {  // lengths of n, which has keys
+    if (n >= p.N) {
+      length = p.prefix;
+      subs = p.H_k * p.prefix_blocks;
+    } else {
+      if (n - held_from >= 32) hold(p, lane);
+      length = __shfl_sync(0xffffffffu, held, n - held_from);
+      subs = p.H_k * p.blocks;
+    }
+    tiles = tiles_of(length);
+  }
+  __device__ __forceinline__ void next(const AttentionParams& p, int lane) {
+    if (++t < tiles) return;
+    t = 0;
+    if (++sub < subs) return;
+    sub = 0;
+    ++n;
+    while (n < p.N) {  // to the next sequence with keys
+      if (n - held_from >= 32) hold(p, lane);
+      const unsigned some = __ballot_sync(0xffffffffu, held > 0) >> (n - held_from);
+      if (some) {
+        n += __ffs(some) - 1;
+        break;
+      }
+      n = held_from + 32;
+    }
+    if (n > p.N) n = p.N;
+    enter(p, lane);
+  }
+};
+
+// An 8 x 8 matrix of 16-bit elements, a lane's pair (t / 4, 2 (t % 4) + {0, 1}) turned into (2 (t % 4) + {0, 1}, t / 4).
+__device__ __forceinline__ uint32_t transposed(uint32_t x) {
+  uint32_t y;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// 16 bytes to shared memory, zeros where there is nothing to copy.
+__device__ __forceinline__ void copy16(uint32_t to, const void* from, bool some) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to), "l"(from), "r"(some ? 16 : 0) : "memory");
+}
+// Arrives (as one of those that the barrier counts) once this thread's copies so far are there.
+__device__ __forceinline__ void arrive_copied(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// The rows of a unit.
+struct Unit {
+  int tok0, head0, r0, rows;
+  __device__ __forceinline__ Unit(const AttentionParams& p, const Walk& w) {
+    const bool own = w.n < p.N;
+    const int blocks = own ? p.blocks : p.prefix_blocks, head = w.sub / blocks;
+    head0 = head * p.group;
+    r0 = (w.sub - head * blocks) * kRows;
+    tok0 = own ? w.n * p.tokens : 0;
+    rows = min(kRows, (own ? p.tokens : p.N * p.tokens) * p.group - r0);
+  }
+};
+
+// The copying warp.
+__device__ __forceinline__ void copy_tiles(const AttentionParams& p, uint8_t* smem, Bars& bar, Walk walk, int count, uint64_t limit) {
+  const int lane = threadIdx.x & 31, boxes = kTile / p.box_rows;
+  const auto page_of = [&](const Walk& w) -> int64_t {  // of the lane's box: -2 behind the length, -1 outside the cache
+    const int key = w.t * kTile + lane * p.box_rows;
+    if (lane >= boxes || key >= w.length) return -2;
+    const int64_t page = w.n < p.N ? index_at(p.table, p.table_dtype, w.n * p.table_st + key / p.page_size)
+                                   : index_at(p.prefix_pages, p.prefix_dtype, key / p.page_size);
+    return page < 0 || page >= p.pages ? -1 : page;
+  };
+  int64_t page = page_of(walk);
+  int issued = 0;
+  for (int k = 0; k < count; ++k) {
+    const int stage = k % kStages;
+    Walk ahead = walk;
+    int64_t page_ahead = -2;
+    if (k + 1 < count) {
+      ahead.next(p, lane);
+      page_ahead = page_of(ahead);
+    }
+    if (!__all_sync(0xffffffffu, mbar_wait(&bar.empty[stage], (k / kStages + 1) & 1, limit))) {
+      if (lane == 0) atomicOr(p.dev_err, kDevErrTimeout);
+      break;
+    }
+    ++issued;
+    const bool bad = __any_sync(0xffffffffu, page == -1), held = p.hold_copies && k == 0;
+    const unsigned some = __ballot_sync(0xffffffffu, page >= 0);
+    uint8_t* tile = smem + stage * kTileBytes;
+    uint64_t* full = &bar.full[stage];
+    if (lane == 0) {
+      bar.bad[stage] = bad;
+      if (bad) atomicOr(p.dev_err, kDevErrPage);
+      mbar_arrive_expect_tx(full, __popc(some) * p.box_rows * 512);
+    }
+    __syncwarp();
+    if (page >= 0 && !held) {
+      const int row = (walk.t * kTile + lane * p.box_rows) % p.page_size, head = walk.sub / (walk.n < p.N ? p.blocks : p.prefix_blocks);
+      uint8_t* at = tile + lane * p.box_rows * 128;
+      for (int half = 0; half < 2; ++half) {
+        tma_load_4d(at + half * kHalfBytes, &p.tm_k, full, 64 * half, head, row, (int)page);
+        tma_load_4d(at + (2 + half) * kHalfBytes, &p.tm_v, full, 64 * half, head, row, (int)page);
+      }
+    }
+    if (k == 0 || walk.t == 0) {  // the queries: half a warp a row
+      const Unit u(p, walk);
+      const uint32_t to = smem_u32(smem + kStages * kTileBytes + stage * kQueryBytes);
+      const int chunk = lane & 15;
+#pragma unroll
+      for (int j = 0; j < kRows / 2; ++j) {
+        const int i = 2 * j + (lane >> 4), r = u.r0 + i;
+        const bool some_row = i < u.rows;
+        const uint16_t* from = reinterpret_cast<const uint16_t*>(p.q);
+        if (some_row) from += (int64_t)(u.tok0 + r / p.group) * p.q_st + (int64_t)(u.head0 + r % p.group) * p.q_sh + 8 * chunk;
+        copy16(to + i * 256 + ((chunk ^ (i & 7)) << 4), from, some_row);
+      }
+      arrive_copied(full);
+    } else {
+      mbar_arrive(full);
+    }
+    walk = ahead;
+    page = page_ahead;
+  }
+  // every copy ends before the memory is another's
+  for (int k = max(0, issued - kStages); k < issued; ++k)
+    if (!(p.hold_copies && k == 0)) mbar_wait(&bar.full[k % kStages], (k / kStages) & 1, kWaitNs);
+}
+
+// Tiles of all sequences, in the units of one (key head, row block), counted by the first 128 of kThreads threads that
+// meet at barrier `id`; `before`: those of the sequences in front of the thread's own, which are `each` in a row.
+struct Count {
+  uint32_t all = 0, before = 0, mine = 0;
+  int each = 0;
+  __device__ __forceinline__ void make(const AttentionParams& p, uint32_t* room, int tid, int id, bool report) {
+    constexpr int kCounting = 32 * kWarps;
+    each = (p.N + kCounting - 1) / kCounting;
+    bool bad = false;
+    if (tid < kCounting)
+      for (int i = 0, n = tid * each; i < each && n < p.N; ++i, ++n) {
+        const int length = length_of(p, n);
+        bad |= length < 0;
+        mine += tiles_of(length);
+      }
+    if (bad && report) atomicOr(p.dev_err, kDevErrLength);
+    uint32_t upto = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+      const uint32_t x = __shfl_up_sync(0xffffffffu, upto, d);
+      if ((tid & 31) >= d) upto += x;
+    }
+    if (tid < kCounting && (tid & 31) == 31) room[tid >> 5] = upto;
+    named_sync(id, kThreads);
+    before = upto - mine;
+    for (int w = 0; w < kWarps; ++w) {
+      if (w < tid >> 5) before += room[w];
+      all += room[w];
+    }
+  }
+};
+
+// A worker for units of up to 8 kEights rows: `tid` below kThreads, the tiles counted by just these threads, ring and barriers of its own (initialised here), its number and how many share the tiles.  `id`
+// and the one behind it: barriers of its own.
+template <bool F16, int kEights>
+__device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* smem, int tid, const Count& counted, int worker, int workers, int id) {
+  Bars& bar = *reinterpret_cast<Bars*>(smem + kStages * (kTileBytes + kQueryBytes));
+  const int lane = tid & 31, warp = tid >> 5, subs = p.H_k * p.blocks;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&bar.full[i], 33);     // the copying warp's lanes, and one of them for the tensor copies
+      mbar_init(&bar.empty[i], kWarps);
+    }
+    fence_mbar_init();
+  }
+  const uint32_t prefix_tiles = tiles_of(p.prefix), own_tiles = counted.all * subs;
+  const Shares shares(own_tiles + prefix_tiles * p.H_k * p.prefix_blocks, workers);
+  const uint32_t from = shares.from(worker);
+  const int count = (int)(shares.from(worker + 1) - from);
+  if (tid < 32 * kWarps && counted.before * subs <= from && from < (counted.before + counted.mine) * subs) {  // the share begins in one of these
+    uint32_t at = counted.before;
+    for (int n = tid * counted.each;; ++n) {
+      const uint32_t tiles = tiles_of(length_of(p, n));
+      if (from < (at + tiles) * subs) {
+        const uint32_t in = from - at * subs;
+        bar.found[0] = n;
+        bar.found[1] = in / tiles;
+        bar.found[2] = in % tiles;
+        break;
+      }
+      at += tiles;
+    }
+  }
+  if (tid == 0 && from >= own_tiles && prefix_tiles) {
+    bar.found[0] = p.N;
+    bar.found[1] = (from - own_tiles) / prefix_tiles;
+    bar.found[2] = (from - own_tiles) % prefix_tiles;
+  }
+  named_sync(id, kThreads);
+  if (count <= 0) return;
+  Walk take;
+  take.n = (int)bar.found[0];
+  take.sub = (int)bar.found[1];
+  take.t = (int)bar.found[2];
+  take.hold(p, lane);
+  take.enter(p, lane);
+  const uint64_t limit = p.wait_ns ? p.wait_ns : kWaitNs;
+  if (warp == kWarps) {
+    copy_tiles(p, smem, bar, take, count, limit);
+    return;
+  }
+
+  // All four warps walk the same units whatever happens on the way, so that they meet at the same ends.
+  const float c = fabsf(p.scale) * kLog2e;
+  const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
+  constexpr float kBias = F16 ? 6.f : 0.f;  // f16 weights are kept 2^6 above their normal range's end for longer
+  const int mi = lane >> 3, mj = lane & 7;
+  bool dead = false;
+  int k = 0, stage = 0;
+  uint32_t phase = 0;
+  while (k < count) {  // the share's piece of a unit
+    const bool own = take.n < p.N, starts = take.t == 0;
+    const int tiles = min(take.tiles - take.t, count - k);
+    bool unit_bad = false;
+    uint32_t q[kEights][8][2];
+    float base[kEights][2], sum[kEights][2], o[kEights][8][4] = {};   // rows 8 g + 2 (t % 4) + {0, 1}; o: values 16 j + t / 4 (+ 8)
+#pragma unroll
+    for (int g = 0; g < kEights; ++g)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) { base[g][e] = -INFINITY; sum[g][e] = 0.f; }
+#pragma unroll 1
+    for (int i = 0;; ++i) {
+      const uint32_t tile = smem_u32(smem) + stage * kTileBytes;
+      if (!dead && !__all_sync(0xffffffffu, mbar_wait(&bar.full[stage], phase, limit))) {
+        dead = true;
+        if (lane == 0) atomicOr(p.dev_err, kDevErrTimeout);
+      }
+      if (i == 0) {
+#pragma unroll
+        for (int g = 0; g < kEights; ++g) {
+          const uint32_t at = smem_u32(smem) + kStages * kTileBytes + stage * kQueryBytes + (8 * g + mj) * 256;
+#pragma unroll
+          for (int kk = 0; kk < 8; kk += 2) {
+            uint32_t x[4];
+            ldmatrix_x4(at + (((2 * kk + mi) ^ mj) << 4), x);
+            q[g][kk][0] = x[0] ^ flip;
+            q[g][kk][1] = x[1] ^ flip;
+            q[g][kk + 1][0] = x[2] ^ flip;
+            q[g][kk + 1][1] = x[3] ^ flip;
+          }
+        }
+      }
+      unit_bad |= dead || bar.bad[stage];
+      const int key0 = take.t * kTile + warp * kWarpKeys, valid = min(kWarpKeys, take.length - key0);
+      if (valid > 0 && !unit_bad) {
+        const uint32_t kb = tile + warp * kWarpKeys * 128, vb = kb + 2 * kHalfBytes;
+        // Fragments are loaded ahead of the products that take them, the first of the values' before the weights are made.
+        // (A row's chunk c of 16 bytes lies at c ^ row % 8: only these bits of an address change from step to step.)
+        const uint32_t keys_at = kb + ((mi & 1) * 8 + mj) * 128 + (((mi >> 1) ^ mj) << 4), values_at = vb + ((mi >> 1) * 8 + mj) * 128 + (((mi & 1) ^ mj) << 4);
+        const auto load_keys = [&](int kk, uint32_t (&to)[4]) { ldmatrix_x4((keys_at ^ ((kk & 3) << 5)) + (kk >> 2) * kHalfBytes, to); };
+        const auto load_values = [&](int j, uint32_t (&to)[4]) { ldmatrix_x4_trans((values_at ^ ((j & 3) << 5)) + (j >> 2) * kHalfBytes, to); };
+        float acc[kEights][2][4] = {};  // even and odd steps; (key t / 4, both rows), (key t / 4 + 8, both rows)
+        uint32_t f[3][4];
+        load_keys(0, f[0]);
+        load_keys(1, f[1]);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk) {
+          if (kk < 6) load_keys(kk + 2, f[(kk + 2) % 3]);
+#pragma unroll
+          for (int g = 0; g < kEights; ++g) mma16<F16>(acc[g][kk & 1], f[kk % 3], q[g][kk][0], q[g][kk][1]);
+        }
+        load_values(0, f[0]);
+        load_values(1, f[1]);
+        float w[kEights][4];
+        const int tail = own && p.tokens > 1 ? max(0, take.length - p.tokens + 1) : take.length;  // keys from here on are not for all rows
+#pragma unroll
+        for (int g = 0; g < kEights; ++g)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[g][e] = (acc[g][0][e] + acc[g][1][e]) * c;
+        if (key0 + kWarpKeys > tail) {
+          const Unit u(p, take);
+          const int at_lane = here(lane);
+#pragma unroll
+          for (int g = 0; g < kEights; ++g)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int key = key0 + at_lane / 4 + 8 * (e >> 1), r = u.r0 + 8 * g + 2 * (at_lane & 3) + (e & 1);
+              const int seen = own ? take.length - p.tokens + 1 + r / p.group : take.length;
+              if (key >= min(seen, take.length)) w[g][e] = -INFINITY;
+            }
+        }
+        bool moves = false;
+#pragma unroll
+        for (int g = 0; g < kEights; ++g)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) moves |= fmaxf(w[g][e], w[g][e + 2]) > base[g][e] + (kRoom + kBias);
+        if (__any_sync(0xffffffffu, moves)) {
+#pragma unroll
+          for (int g = 0; g < kEights; ++g)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              float top = fmaxf(w[g][e], w[g][e + 2]);
+#pragma unroll
+              for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+              const float now = fmaxf(base[g][e], top - kBias);
+              const float keep = now == -INFINITY || now == base[g][e] ? 1.f : exp2_fast(base[g][e] - now);
+              base[g][e] = now;
+              sum[g][e] *= keep;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) { o[g][j][e] *= keep; o[g][j][e + 2] *= keep; }
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < kEights; ++g)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float from_base = base[g][e] == -INFINITY ? 0.f : base[g][e];
+            w[g][e] = exp2_fast(w[g][e] - from_base);
+            w[g][e + 2] = exp2_fast(w[g][e + 2] - from_base);
+            sum[g][e] += w[g][e] + w[g][e + 2];
+          }
+        const int clean = min(valid, max(0, tail - key0));  // keys that all rows see
+        if (clean < kWarpKeys) {
+          // What lies behind must not meet the products, be its weight zero: an infinity would leave a NaN.
+          // Keys that some rows see are added by hand, the places are cleared.
+          const Unit u(p, take);
+          const int at_lane = here(lane);
+#pragma unroll 1
+          for (int j = clean; j < valid; ++j) {
+            const int from = ((j & 7) << 2) | (at_lane & 3);
+#pragma unroll
+            for (int g = 0; g < kEights; ++g)
+#pragma unroll
+              for (int e = 0; e < 2; ++e) {
+                const float pj = __shfl_sync(0xffffffffu, j < 8 ? w[g][e] : w[g][e + 2], from);
+                const int r = u.r0 + 8 * g + 2 * (at_lane & 3) + e;
+                if (key0 + j >= take.length - p.tokens + 1 + r / p.group) continue;  // not seen
+#pragma unroll
+                for (int n = 0; n < 16; ++n) {
+                  const int value = 8 * n + at_lane / 4;
+                  uint16_t x;
+                  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(vb + (n >> 3) * kHalfBytes + j * 128 + (((n & 7) ^ (j & 7)) << 4) + 2 * (value & 7)));
+                  float& to = o[g][n >> 1][e + 2 * (n & 1)];
+                  to = fmaf(pj, unpack16<F16>((uint32_t)x).x, to);
+                }
+              }
+          }
+          __syncwarp();
+          for (int n = lane; n < (kWarpKeys - clean) * 16; n += 32) {
+            const int j = clean + n / 16, chunk = n % 16;
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + (chunk >> 3) * kHalfBytes + j * 128 + ((chunk & 7) << 4)), "r"(0) : "memory");
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+#pragma unroll
+          for (int g = 0; g < kEights; ++g)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (at_lane / 4 + 8 * (e >> 1) >= clean) w[g][e] = 0.f;
+          load_values(0, f[0]);
+          load_values(1, f[1]);
+        }
+        uint32_t b[kEights][2];
+#pragma unroll
+        for (int g = 0; g < kEights; ++g) {
+          b[g][0] = transposed(pack16x2<F16>(w[g][0], w[g][1]));
+          b[g][1] = transposed(pack16x2<F16>(w[g][2], w[g][3]));
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          if (j < 6) load_values(j + 2, f[(j + 2) % 3]);
+#pragma unroll
+          for (int g = 0; g < kEights; ++g) mma16<F16>(o[g][j], f[j % 3], b[g][0], b[g][1]);
+        }
+      }
+      if (i + 1 == tiles) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&bar.empty[stage]);
+      ++take.t;
+      if (++stage == kStages) { stage = 0; phase ^= 1; }
+    }
+    // the warps' parts of the piece come together, over its last tile
+    const bool ends = take.t + 1 == take.tiles, whole = starts && ends;
+    const int at_lane = here(lane), at_tid = here(tid);
+    const Unit u(p, take);
+#pragma unroll
+    for (int g = 0; g < kEights; ++g)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+#pragma unroll
+        for (int d = 4; d < 32; d <<= 1) sum[g][e] += __shfl_xor_sync(0xffffffffu, sum[g][e], d);
+        if (at_lane < 4) bar.ml[warp][8 * g + 2 * at_lane + e] = make_float2(base[g][e], unit_bad ? kAttentionBad : sum[g][e]);
+      }
+    float* join = reinterpret_cast<float*>(smem + stage * kTileBytes);   // [warp][rows][128], columns by eights turned by the row
+    named_sync(id + 1, 32 * kWarps);
+#pragma unroll
+    for (int g = 0; g < kEights; ++g)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+#pragma unroll
+        for (int n = 0; n < 16; ++n)
+          join[(warp * 8 * kEights + 8 * g + 2 * (at_lane & 3) + e) * kHeadDim + (n ^ (at_lane & 3)) * 8 + at_lane / 4] = o[g][n >> 1][e + 2 * (n & 1)];
+    named_sync(id + 1, 32 * kWarps);
+    const int unit = take.n * subs + take.sub;
+    if (tid == 0) {
+      if (starts) p.first_worker[unit] = worker;
+      if (ends) p.last_worker[unit] = worker;
+    }
+    const int64_t slot = whole ? 2 * p.workers + (int64_t)unit : 2 * worker + (starts ? 1 : 0);
+    const int cg = at_tid & 15;
+    float x[kEights][8], top[kEights], l[kEights];
+    bool bad = false;
+#pragma unroll
+    for (int g = 0; g < kEights; ++g) {
+      const int row = at_tid / 16 + 8 * g;
+      float2 ml[kWarps];
+      top[g] = -INFINITY;
+      l[g] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        ml[w] = bar.ml[w][row];
+        top[g] = fmaxf(top[g], ml[w].x);
+        bad |= ml[w].y == kAttentionBad;
+      }
+      const float from_base = top[g] == -INFINITY ? 0.f : top[g];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[g][e] = 0.f;
+#pragma unroll
+      for (int w = 0; w < kWarps; ++w) {
+        const float f = exp2_fast(ml[w].x - from_base);
+        const float4* y = reinterpret_cast<const float4*>(join + (w * 8 * kEights + row) * kHeadDim + (cg ^ (row >> 1 & 3)) * 8);
+        const float4 y0 = y[0], y1 = y[1];
+        l[g] = fmaf(f, ml[w].y, l[g]);
+        x[g][0] = fmaf(f, y0.x, x[g][0]); x[g][1] = fmaf(f, y0.y, x[g][1]); x[g][2] = fmaf(f, y0.z, x[g][2]); x[g][3] = fmaf(f, y0.w, x[g][3]);
+        x[g][4] = fmaf(f, y1.x, x[g][4]); x[g][5] = fmaf(f, y1.y, x[g][5]); x[g][6] = fmaf(f, y1.z, x[g][6]); x[g][7] = fmaf(f, y1.w, x[g][7]);
+      }
+    }
+    // the tile is given back, and the warps go on, before what they have is on its way to memory
+    fence_proxy_async_smem();
+    named_sync(id + 1, 32 * kWarps);
+    if (lane == 0) mbar_arrive(&bar.empty[stage]);
+#pragma unroll
+    for (int g = 0; g < kEights; ++g) {
+      const int row = at_tid / 16 + 8 * g, r = u.r0 + row;
+      if (row >= u.rows) break;
+      if (whole && !p.prefix) {
+        if (!bad) {
+          const bool none = top[g] == -INFINITY && l[g] == 0.f;
+          const float inv = none ? 0.f : 1.f / l[g];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) x[g][e] *= inv;
+          const int64_t token = u.tok0 + r / p.group;
+          const int head = u.head0 + r % p.group;
+          *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + token * p.o_st + head * p.o_sh + 8 * cg) = pack16x8<F16>(x[g]);
+          if (p.lse && cg == 0)
+            p.lse[token * p.lse_st + head] = none ? -INFINITY : ((top[g] == -INFINITY ? 0.f : top[g]) + log2f(l[g])) * kLn2;
+        }
+      } else {
+        float4* y = reinterpret_cast<float4*>(p.part_o + (slot * p.block_rows + row) * kHeadDim + 8 * cg);
+        y[0] = make_float4(x[g][0], x[g][1], x[g][2], x[g][3]);
+        y[1] = make_float4(x[g][4], x[g][5], x[g][6], x[g][7]);
+        if (cg == 0) *reinterpret_cast<float2*>(p.part_ml + (slot * p.block_rows + row) * 2) = make_float2(top[g], bad ? kAttentionBad : l[g]);
+      }
+    }
+    k += tiles;
+    if (++stage == kStages) { stage = 0; phase ^= 1; }
+    if (k < count) take.next(p, lane);
+  }
+}
+
+}  // namespace own
+}  // namespace gdn

@@ -1,5 +1,5 @@
 // Softmax attention of many rows over the prefix that they share, for sm_103a: the part of the paged
-// attention (attention.cu) that reads keys and values once for the whole batch.
+// attention (attention.cu) that reads keys and values once for the whole batch, as one CTA does its share of it.
 //
 //   s_j = scale q . k_j,   (base, sum_j 2^(s_j log2(e) - base), sum_j 2^(s_j log2(e) - base) v_j)
 //
@@ -22,31 +22,20 @@
 //
 // Units are (key head, 256 rows), a unit's tiles of 128 keys come one behind the other, and all units'
 // tiles are cut into equal shares for the SMs; the parts are joined by attention.cu's second kernel.
-#include <cuda_runtime.h>
-
-#include "attention.h"
-#include "decay.cuh"
-#include "ptx.cuh"
+#pragma once
+#include "attention_common.cuh"
 
 namespace gdn {
-namespace {
+namespace prefix {
 
 constexpr int kThreads = 384;                 // two groups of four warps for the weights, one with the copies and the products
 constexpr int kHalf = 16384;                  // 128 rows of 64 values
 constexpr int kTileBytes = 2 * kHalf;
 constexpr int kStages = 2;                    // of keys, and of values
 constexpr int kQ = 0, kK = 2 * kTileBytes, kV = kK + kStages * kTileBytes, kBars = kV + kStages * kTileBytes;
-constexpr int kSmemBytes = kBars + 256;
-constexpr uint32_t kS = 0, kO = 256;          // TMEM columns: S of A and B (and P over it), O of A and B
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kRoom = 8.f;
-constexpr uint64_t kWaitNs = 200000000ull;
+constexpr int kBytes = kBars + 256;
 
-__device__ __forceinline__ float exp2_fast(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
+constexpr uint32_t kS = 0, kO = 256;          // TMEM columns: S of A and B (and P over it), O of A and B
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
   float2 r;
   asm("{\n.reg .b64 x, y;\nmov.b64 x, {%2, %3};\nmov.b64 y, {%4, %5};\nadd.rn.f32x2 x, x, y;\nmov.b64 {%0, %1}, x;\n}"
@@ -70,32 +59,30 @@ struct Bars {
   uint32_t tmem, bad;
 };
 
-// The shares: steps (tiles of keys) of this CTA, and the pieces of units that they make.
+// The share of a worker: steps (tiles of keys), and the pieces of units that they make.
 struct Share {
-  int64_t at, end;
-  int tiles;
-  __device__ __forceinline__ explicit Share(const AttentionParams& p) {
+  uint32_t at, end, tiles;
+  __device__ __forceinline__ Share(const AttentionParams& p, int worker, int workers) {
     tiles = (p.prefix + kPrefixKeys - 1) / kPrefixKeys;
-    const int64_t total = (int64_t)p.H_k * p.prefix_units * tiles;
-    at = total * blockIdx.x / gridDim.x;
-    end = total * (blockIdx.x + 1) / gridDim.x;
+    const Shares s(p.H_k * p.prefix_units * tiles, workers);
+    at = s.from(worker);
+    end = s.from(worker + 1);
   }
   int unit, t0, n;  // the piece: tiles t0 .. t0 + n - 1 of the unit
   __device__ __forceinline__ bool next() {
     if (at >= end) return false;
     unit = (int)(at / tiles);
     t0 = (int)(at % tiles);
-    n = (int)min((int64_t)(tiles - t0), end - at);
+    n = (int)min(tiles - t0, end - at);
     at += n;
     return true;
   }
 };
 
+// All kThreads threads of a CTA.
 template <bool F16>
-__global__ void __launch_bounds__(kThreads, 1) gdn_attention_prefix_kernel(const __grid_constant__ AttentionParams p) {
-  extern __shared__ __align__(1024) uint8_t smem[];
+__device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* smem, int worker, int workers) {
   Bars& bar = *reinterpret_cast<Bars*>(smem + kBars);
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");  // what comes next does not wait for this kernel to begin with
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, group = warp >> 2;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
@@ -112,8 +99,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_attention_prefix_kernel(const
     }
     mbar_init(&bar.done, 1);
     fence_mbar_init();
-    bar.bad = smem_u32(smem) & 1023 ? 1 : 0;  // the swizzled tiles have to be where their bits say
-    if (bar.bad) atomicOr(p.dev_err, kDevErrTimeout);
+    bar.bad = 0;
   }
   if (warp == 9) {
     tmem_alloc(&bar.tmem, 512);
@@ -125,7 +111,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_attention_prefix_kernel(const
   const uint32_t tmem = bar.tmem;
   const uint64_t limit = p.wait_ns ? p.wait_ns : kWaitNs;
   const int rows_all = p.N * p.tokens * p.group;
-  Share share(p);
+  Share share(p, worker, workers);
   const auto turns = [&] { return rows_all - share.unit % p.prefix_units * kPrefixRows <= 128; };  // A and B take turns at the tiles
 
   if (group == 2) {
@@ -175,42 +161,43 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_attention_prefix_kernel(const
         for (int i = max(0, issued[kv] - kStages); i < issued[kv]; ++i)
           if (!(p.hold_copies && i == 0)) mbar_wait(kv ? &bar.v_full[i % kStages] : &bar.k_full[i % kStages], (i / kStages) & 1, kWaitNs);
     } else if (warp == 9) {  // products
-      const bool one = elect_one();
       bool dead = false;
       uint32_t step = 0, steps[2] = {0, 0}, pieces[2] = {0, 0};
       const uint32_t id_s = p.scale < 0.f ? idesc_16_f32(F16, 128, 128, 0, 0, 1) : idesc_16_f32(F16, 128, 128, 0, 0, 0);
       constexpr uint32_t id_o = idesc_16_f32(F16, 128, 128, 0, 1, 0);
-      const uint32_t q_at = smem_u32(smem + kQ), k_at = smem_u32(smem + kK), v_at = smem_u32(smem + kV);
+      const uint64_t d_q = sdesc_sw128(smem_u32(smem + kQ), 16, 1024), d_k = sdesc_sw128(smem_u32(smem + kK), 16, 1024),
+                     d_v = sdesc_sw128(smem_u32(smem + kV), kHalf, 1024);   // shared addresses count by 16 bytes in them
       auto wait = [&](uint64_t* b, uint32_t parity) {
         if (!dead && !__all_sync(0xffffffffu, mbar_wait(b, parity & 1, limit))) dead = true;
         tc_fence_after();
       };
       auto commit = [&](uint64_t* b) {
-        if (one && !dead) mma_commit(b);
+        if (!dead && elect_one()) mma_commit(b);
         __syncwarp();
       };
       auto scores = [&](int x, int rows, uint32_t st) {  // S of A or B, with the rows of tile `rows`
-        if (one && !dead) {
-          const uint32_t a = q_at + rows * kTileBytes, b = k_at + st * kTileBytes;
+        const uint64_t a = d_q + rows * (kTileBytes >> 4), b = d_k + st * (kTileBytes >> 4);
+        if (!dead && elect_one()) {
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
-            const uint32_t off = (kk >> 2) * kHalf + (kk & 3) * 32;
-            mma_ss(tmem + kS + 128 * x, sdesc_sw128(a + off, 16, 1024), sdesc_sw128(b + off, 16, 1024), id_s, kk > 0);
+            const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
+            mma_ss(tmem + kS + 128 * x, a + off, b + off, id_s, kk > 0);
           }
           mma_commit(&bar.s_full[x]);
         }
         __syncwarp();
       };
       auto values = [&](int x, uint32_t at, bool more) {  // O of A or B, of the values of step `at`
-        const uint32_t st = at % kStages, b = v_at + st * kTileBytes;
+        const uint32_t st = at % kStages;
+        const uint64_t b = d_v + st * (kTileBytes >> 4);
         for (int h = 0; h < 2; ++h) {
           wait(&bar.p_full[x][h], steps[x]);
           if (h == 0) wait(&bar.v_full[st], at / kStages);
-          if (one && !dead) {
+          if (!dead && elect_one()) {
 #pragma unroll
             for (int k4 = 0; k4 < 4; ++k4) {
               const int kk = 4 * h + k4;
-              mma_ts(tmem + kO + 128 * x, tmem + kS + 128 * x + 8 * kk, sdesc_sw128(b + kk * 2048, kHalf, 1024), id_o, more || kk > 0);
+              mma_ts(tmem + kO + 128 * x, tmem + kS + 128 * x + 8 * kk, b + kk * (2048 >> 4), id_o, more || kk > 0);
             }
           }
           __syncwarp();
@@ -264,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_attention_prefix_kernel(const
       }
       if (dead && lane == 0) atomicOr(p.dev_err, kDevErrTimeout);
       // nothing is on its way to or from TMEM any more
-      if (one) mma_commit(&bar.done);
+      if (elect_one()) mma_commit(&bar.done);
       __syncwarp();
       mbar_wait(&bar.done, 0, kWaitNs);
     }
@@ -400,8 +387,8 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_attention_prefix_kernel(const
       const bool some = !turn || x < share.n;  // tiles for this group
       if (some) wait(&bar.o_full[x], pieces++);
       tc_fence_after();
-      const bool whole = share.t0 == 0 && share.n == share.tiles, write = r < rows_all;
-      const int64_t slot = whole ? 2 * (int64_t)gridDim.x + share.unit : 2 * (int64_t)blockIdx.x + (share.t0 == 0 ? 1 : 0);
+      const bool whole = share.t0 == 0 && share.n == (int)share.tiles, write = r < rows_all;
+      const int64_t slot = whole ? 2 * (int64_t)p.prefix_workers + share.unit : 2 * (int64_t)worker + (share.t0 == 0 ? 1 : 0);
       const int row = 128 * x + i128;
       if (some && !dead) {
         float* y = p.prefix_o + slot * kPrefixRows * kHeadDim + row * 8;   // by eights of columns: a warp writes 1 KB in a row
@@ -432,26 +419,5 @@ __global__ void __launch_bounds__(kThreads, 1) gdn_attention_prefix_kernel(const
   if (warp == 9) tmem_dealloc(tmem, 512);
 }
 
-template <bool F16>
-cudaError_t launch(const AttentionParams& p, cudaStream_t stream) {
-  static thread_local int generation = -1, device = -1;  // the attribute is one of a device
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  if (generation != launch_config_generation() || device != dev) {
-    e = cudaFuncSetAttribute(gdn_attention_prefix_kernel<F16>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
-    if (e != cudaSuccess) return e;
-    generation = launch_config_generation();
-    device = dev;
-  }
-  gdn_attention_prefix_kernel<F16><<<(unsigned)p.prefix_workers, kThreads, kSmemBytes, stream>>>(p);
-  return cudaGetLastError();
-}
-
-}  // namespace
-
-cudaError_t launch_attention_prefix(const AttentionParams& p, cudaStream_t stream) {
-  return p.op_f16 ? launch<true>(p, stream) : launch<false>(p, stream);
-}
-
+}  // namespace prefix
 }  // namespace gdn
