@@ -321,17 +321,18 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
         const auto load_keys = [&](int kk, uint32_t (&to)[4]) { ldmatrix_x4((keys_at ^ ((kk & 3) << 5)) + (kk >> 2) * kHalfBytes, to); };
         const auto load_values = [&](int j, uint32_t (&to)[4]) { ldmatrix_x4_trans((values_at ^ ((j & 3) << 5)) + (j >> 2) * kHalfBytes, to); };
         float acc[kEights][2][4] = {};  // even and odd steps; (key t / 4, both rows), (key t / 4 + 8, both rows)
-        uint32_t f[3][4];
-        load_keys(0, f[0]);
-        load_keys(1, f[1]);
+        constexpr int kAhead = kEights == 1 ? 2 : 1;   // as registers allow
+        uint32_t f[kAhead + 1][4];
+#pragma unroll
+        for (int kk = 0; kk < kAhead; ++kk) load_keys(kk, f[kk]);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk) {
-          if (kk < 6) load_keys(kk + 2, f[(kk + 2) % 3]);
+          if (kk + kAhead < 8) load_keys(kk + kAhead, f[(kk + kAhead) % (kAhead + 1)]);
 #pragma unroll
-          for (int g = 0; g < kEights; ++g) mma16<F16>(acc[g][kk & 1], f[kk % 3], q[g][kk][0], q[g][kk][1]);
+          for (int g = 0; g < kEights; ++g) mma16<F16>(acc[g][kk & 1], f[kk % (kAhead + 1)], q[g][kk][0], q[g][kk][1]);
         }
-        load_values(0, f[0]);
-        load_values(1, f[1]);
+#pragma unroll
+        for (int j = 0; j < kAhead; ++j) load_values(j, f[j]);
         float w[kEights][4];
         const int tail = own && p.tokens > 1 ? max(0, take.length - p.tokens + 1) : take.length;  // keys from here on are not for all rows
 #pragma unroll
@@ -380,10 +381,24 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
             w[g][e + 2] = exp2_fast(w[g][e + 2] - from_base);
             sum[g][e] += w[g][e] + w[g][e + 2];
           }
-        const int clean = min(valid, max(0, tail - key0));  // keys that all rows see
+        // What must not be seen must not meet the products, be its weight zero: an infinity would leave a NaN.  Places behind the
+        // last key are cleared.  Keys that only some rows see seldom hold anything but numbers; where they do, they are
+        // added by hand and cleared, too.
+        int clean = valid;
+        if (key0 + kWarpKeys > tail) {
+          const int some = min(valid, max(0, tail - key0));  // keys that all rows see
+          bool odd = false;
+          for (int n = lane; n < (valid - some) * 16; n += 32) {
+            const int j = some + n / 16, chunk = n % 16;
+            uint32_t x[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(vb + (chunk >> 3) * kHalfBytes + j * 128 + ((chunk & 7) << 4)));
+            constexpr uint32_t kTop = F16 ? 0x7c00u : 0x7f80u;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) odd |= (x[e] & kTop) == kTop || (x[e] >> 16 & kTop) == kTop;
+          }
+          if (__any_sync(0xffffffffu, odd)) clean = some;
+        }
         if (clean < kWarpKeys) {
-          // What lies behind must not meet the products, be its weight zero: an infinity would leave a NaN.
-          // Keys that some rows see are added by hand, the places are cleared.
           const Unit u(p, take);
           const int at_lane = here(lane);
 #pragma unroll 1
@@ -418,8 +433,8 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               if (at_lane / 4 + 8 * (e >> 1) >= clean) w[g][e] = 0.f;
-          load_values(0, f[0]);
-          load_values(1, f[1]);
+#pragma unroll
+          for (int j = 0; j < kAhead; ++j) load_values(j, f[j]);
         }
         uint32_t b[kEights][2];
 #pragma unroll
@@ -429,9 +444,9 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
-          if (j < 6) load_values(j + 2, f[(j + 2) % 3]);
+          if (j + kAhead < 8) load_values(j + kAhead, f[(j + kAhead) % (kAhead + 1)]);
 #pragma unroll
-          for (int g = 0; g < kEights; ++g) mma16<F16>(o[g][j], f[j % 3], b[g][0], b[g][1]);
+          for (int g = 0; g < kEights; ++g) mma16<F16>(o[g][j], f[j % (kAhead + 1)], b[g][0], b[g][1]);
         }
       }
       if (i + 1 == tiles) break;
