@@ -136,26 +136,26 @@ def describe(t: Optional[torch.Tensor]):
 class _PyCall:
     """The operators whose smallest calls take a few microseconds on the GPU, with the arguments of the C
     functions (``decay_prefill`` and ``decay_step`` also with whether the gate may be ``[H]``, one decay for
-    each head; ``pair_axes`` without its length), tensors described on the way.  At the
-    first use they are taken from the extension ``csrc/pycall.c``, with ``fill``, the addresses of
+    each head; ``pair_axes`` without its length), tensors described on the way; those called ``new_`` allocate their results.
+    At the first use they are taken from the extension ``csrc/pycall.cpp``, with ``fill``, the addresses of
     descriptors alone; where it was not built or does not load, they go by ctypes as all others do."""
 
-    _names = ("qk_norm_rope", "decay_prefill", "decay_step", "qk_norm_rope_axes", "norm_rope_append", "paged_attention_step")
+    _bound = ("qk_norm_rope", "decay_prefill", "decay_step", "qk_norm_rope_axes", "norm_rope_append", "paged_attention_step")
+    _names = (*_bound, "new_qk_norm_rope", "new_norm_rope_append", "new_paged_attention_step", "fill")
 
     def __getattr__(self, name):
-        if name not in self._names and name != "fill":
+        if name not in self._names:
             raise AttributeError(name)
         lib = load_library()
         try:
             loader = importlib.machinery.ExtensionFileLoader("gdn_pycall", _PYCALL_PATH)
             module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("gdn_pycall", _PYCALL_PATH, loader=loader))
             loader.exec_module(module)
-            module.bind(_DTYPES, _on_host if torch.cuda.is_available() else None,
-                        *(ctypes.cast(getattr(lib, "gdn_" + each), ctypes.c_void_p).value
-                          for each in self._names))
+            module.bind(_not_here if torch.cuda.is_available() else None,
+                        *(ctypes.cast(getattr(lib, "gdn_" + each), ctypes.c_void_p).value for each in self._bound))
         except (ImportError, OSError):
             module = _ByCtypes(lib)
-        for each in (*self._names, "fill"):
+        for each in self._names:
             setattr(self, each, getattr(module, each))
         return self.__dict__[name]
 
@@ -197,6 +197,29 @@ class _ByCtypes:
         return self._lib.gdn_paged_attention_step(*_described(q, k_cache, v_cache, page_table, lengths), scale + 0.0,
                                                   *_described(prefix_pages), prefix_length, *_described(output, lse), stream)
 
+    def new_qk_norm_rope(self, q, k, q_weight, k_weight, weight_offset, eps, cos_sin, positions, pair_axes, interleaved):
+        made = torch.empty_like(q), None if k is None else torch.empty_like(k)
+        if pair_axes is None:
+            status = self.qk_norm_rope(q, k, q_weight, k_weight, weight_offset, eps, cos_sin, positions, interleaved, *made, _stream_handle(None))
+        else:
+            status = self.qk_norm_rope_axes(q, k, q_weight, k_weight, weight_offset, eps, cos_sin, positions, pair_axes, interleaved, *made,
+                                            _stream_handle(None))
+        return status or made
+
+    def new_norm_rope_append(self, q, k, v, q_weight, k_weight, weight_offset, eps, norm, cos_sin, positions, pair_axes, interleaved,
+                             slots, k_cache, v_cache):
+        made = torch.empty_like(q)
+        status = self.norm_rope_append(q, k, v, q_weight, k_weight, weight_offset, eps, norm, cos_sin, positions, pair_axes, interleaved,
+                                       slots, made, k_cache, v_cache, _stream_handle(None))
+        return status or made
+
+    def new_paged_attention_step(self, q, k_cache, v_cache, page_table, lengths, scale, prefix_pages, prefix_length, with_lse):
+        made = torch.empty_like(q, memory_format=torch.contiguous_format)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device) if with_lse else None
+        status = self.paged_attention_step(q, k_cache, v_cache, page_table, lengths, scale, prefix_pages, prefix_length, made, lse,
+                                           _stream_handle(None))
+        return status or ((made, lse) if with_lse else made)
+
 
 def _axes(pair_axes):
     if pair_axes is None:
@@ -207,9 +230,11 @@ def _axes(pair_axes):
     return (ctypes.c_int32 * max(1, len(pair_axes)))(*(x if -1 <= x <= 127 else -1 for x in pair_axes)), len(pair_axes)
 
 
-def _on_host(t):
-    """Kernels run after the call has returned, so host memory that they were given could be gone by then;
-    pinned tensors are the caller's to keep."""
+def _not_here(t):
+    """A tensor that the current device may not read.  Kernels run after the call has returned, so host memory that they
+    were given could be gone by then; pinned tensors are the caller's to keep."""
+    if t.is_cuda:
+        raise GdnError(1, f"a tensor is on {t.device}, not on the current device")
     if not t.is_pinned():
         raise GdnError(1, "a tensor is on the host")
 
@@ -217,9 +242,10 @@ def _on_host(t):
 def _described(*tensors):
     described = [_ref(describe(t)) for t in tensors]
     if torch.cuda.is_available():
+        here = _current_device()
         for t in tensors:
-            if t is not None and not t.is_cuda:
-                _on_host(t)
+            if t is not None and not (t.is_cuda and t.device.index == here):
+                _not_here(t)
     return described
 
 
@@ -525,6 +551,11 @@ def qk_norm_rope(q, k=None, cos_sin=None, positions=None, q_weight=None, k_weigh
     With ``pair_axes``, the axis of each of the R / 2 pairs, ``positions`` is ``[axes, T]``, a place on each of up
     to four axes (gdn_qk_norm_rope_axes).
     """
+    if stream is None and q_out is None and k_out is None:
+        made = _calls.new_qk_norm_rope(q, k, q_weight, k_weight, weight_offset, eps, cos_sin, positions, pair_axes, interleaved)
+        if made.__class__ is int:
+            _check(made)
+        return made
     if q_out is None:
         q_out = torch.empty_like(q) if stream is None else _empty(q.shape, q, stream)
     if k is not None and k_out is None:
@@ -546,6 +577,12 @@ def norm_rope_append(q, k, v, k_cache, v_cache, slots, cos_sin=None, positions=N
 
     Returns ``q_out``; pass ``q_out=q`` to work in place.  A result that the call allocates belongs to ``stream``.
     """
+    if stream is None and q_out is None:
+        q_out = _calls.new_norm_rope_append(q, k, v, q_weight, k_weight, weight_offset, eps, norm, cos_sin, positions, pair_axes,
+                                            interleaved, slots, k_cache, v_cache)
+        if q_out.__class__ is int:
+            _check(q_out)
+        return q_out
     if q_out is None:
         q_out = torch.empty_like(q) if stream is None else _empty(q.shape, q, stream)
     status = _calls.norm_rope_append(q, k, v, q_weight, k_weight, weight_offset, eps, norm, cos_sin, positions, pair_axes, interleaved,
@@ -567,12 +604,18 @@ def paged_attention_step(q, k_cache, v_cache, page_table, lengths, scale: Option
     Such calls run one after the other even on different streams; replays of a graph that holds one must not run
     concurrently with others.
     """
+    if stream is None and output is None and lse is None:
+        made = _calls.new_paged_attention_step(q, k_cache, v_cache, page_table, lengths, 0.0 if scale is None else scale, prefix_pages,
+                                               prefix_length, return_lse)
+        if made.__class__ is int:
+            _check(made)
+        return made
     if output is None or (return_lse and lse is None):
         with _allocating_on(stream) if stream is not None else _no_context:
             if output is None:
                 output = torch.empty_like(q, memory_format=torch.contiguous_format)
             if return_lse and lse is None:
-                lse = q.new_empty(q.shape[:2], dtype=torch.float32)
+                lse = torch.empty(q.shape[:2], dtype=torch.float32, device=q.device)
     status = _calls.paged_attention_step(q, k_cache, v_cache, page_table, lengths, 0.0 if scale is None else scale, prefix_pages,
                                          prefix_length, output, lse, _stream_handle(stream))
     if status:

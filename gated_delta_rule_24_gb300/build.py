@@ -3,12 +3,13 @@ binding's extension ``_build/gdn_pycall.so`` beside it.
 
 Each translation unit is compiled by nvcc in parallel, then linked; a rebuild
 happens only when a source or header is newer than what is made of it.  The extension makes calls
-lighter for the host and nothing else: where it cannot be built (no Python headers), the binding does
+lighter for the host and nothing else: where it cannot be built (no headers of Python or torch), the binding does
 without.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import subprocess
 import sys
@@ -22,7 +23,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libgdn_gb300.so")
 PYCALL = os.path.join(BUILD, "gdn_pycall.so")
-PYCALL_SOURCE = os.path.join(CSRC, "pycall.c")
+PYCALL_SOURCE = os.path.join(CSRC, "pycall.cpp")
 SOURCES = ["prefill.cu", "decode.cu", "decay_prefill.cu", "decay_step.cu", "norm_rope.cu", "attention.cu", "api.cpp"]
 HEADERS = [os.path.join(CSRC, f) for f in ("prefill.h", "decode.h", "decay.h", "decay.cuh", "attention.h", "attention_common.cuh",
                                                "attention_own.cuh", "attention_prefix.cuh", "ptx.cuh")] + [os.path.join(INCLUDE, "gdn.h")]
@@ -44,9 +45,13 @@ def _build_pycall() -> None:
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     tmp = PYCALL + f".tmp{os.getpid()}"
     try:
-        r = subprocess.run(["gcc", "-O2", "-std=c11", "-shared", "-fPIC", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
-                            "-I", os.path.join(cuda, "include"), PYCALL_SOURCE, "-o", tmp], capture_output=True, text=True)
-        failed = r.returncode and f"gcc failed on {PYCALL_SOURCE}:\n{r.stdout}\n{r.stderr}"
+        spec = importlib.util.find_spec("torch")
+        torch = os.path.dirname(spec.origin) if spec and spec.origin else "torch"
+        r = subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
+                            "-isystem", os.path.join(torch, "include"), "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+                            "-I", os.path.join(cuda, "include"), PYCALL_SOURCE, "-o", tmp, "-L", os.path.join(torch, "lib"),
+                            "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"], capture_output=True, text=True)
+        failed = r.returncode and f"g++ failed on {PYCALL_SOURCE}:\n{r.stdout}\n{r.stderr}"
     except OSError as e:
         failed = str(e)
     if not failed:
@@ -54,7 +59,7 @@ def _build_pycall() -> None:
         return
     if os.path.exists(PYCALL):  # of an older source
         os.remove(PYCALL)
-    warnings.warn(f"calls of the decay operators will take the host longer: no {PYCALL}: {failed}")
+    warnings.warn(f"small calls will take the host longer: no {PYCALL}: {failed}")
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
