@@ -48,20 +48,19 @@ __global__ void __launch_bounds__(own::kThreads, kResident) gdn_attention_kernel
   }
   own::Count count;
   count.make(p, reinterpret_cast<uint32_t*>(smem), threadIdx.x, 1, blockIdx.x == 0);
-  const uint32_t total = count.all * p.H_k * p.blocks + own::tiles_of(p.prefix) * p.H_k * p.prefix_blocks;
-  // no more workers than tiles: one without any between two parts of a unit would leave a gap
-  const uint32_t workers = min(total, gridDim.x);
+  // no more workers than there is to share: one without anything between two parts of a unit would leave a gap
+  const uint32_t workers = min(own::whole_cost(p, count), gridDim.x);
   if (blockIdx.x >= workers) return;
   own::run_worker<F16, kEights>(p, smem, threadIdx.x, count, blockIdx.x, workers, 1);
 }
 
-// SMs out of `sms` for the own pages beside a prefix of many rows, by what their tiles take an SM: 0.36 us for 64 keys of two
-// workers side by side and 0.5 us for the end of a unit, 1.5 us for 128 keys of 256 rows.
-__device__ __forceinline__ int sms_for_own(const AttentionParams& p, uint32_t own_tiles, uint32_t prefix_steps, int sms) {
-  if (own_tiles == 0) return 0;
-  const float own = 0.36f * own_tiles + 0.5f * min(own_tiles, (uint32_t)(p.N * p.H_k * p.blocks)), prefix = 1.5f * prefix_steps;
-  const int x = (int)(sms * (own / (own + prefix)) + 0.5f);
-  return max(1, min(x, sms - 1));
+// SMs out of `sms` for the own pages beside a prefix of many rows, by what the two take an SM: 0.42 us for a tile's cost (two
+// workers side by side), 1.55 us for 128 keys of 256 rows.  A prefix of up to 128 rows is held by HBM, too, and loses little by an SM
+// less, while the own pages get on more slowly beside it.
+__device__ __forceinline__ int sms_for_own(uint32_t own_cost, uint32_t prefix_cost, bool few_rows, int sms) {
+  if (own_cost == 0) return 0;
+  const float own = (few_rows ? 1.f : 0.42f) * own_cost, prefix = 1.55f * prefix_cost;
+  return max(1, min((int)(sms * (own / (own + prefix)) + 0.5f), sms - 1));
 }
 
 // The own pages and a prefix of many rows side by side: a CTA is one worker of the prefix, or two of the own pages.
@@ -81,28 +80,28 @@ __global__ void __launch_bounds__(prefix::kThreads, 1) gdn_attention_both_kernel
   const int half = threadIdx.x / own::kThreads, tid = threadIdx.x - half * own::kThreads;
   own::Count count;
   if (half < 2) count.make(p, room + 8 * half, tid, 1 + 2 * half, blockIdx.x == 0 && half == 0);
-  if (threadIdx.x == 0) room[16] = count.all;
+  if (threadIdx.x == 0) { room[16] = count.all.tiles; room[17] = count.all.cost; }
   __syncthreads();
-  count.all = room[16];
+  count.all = {room[16], room[17]};
   __syncthreads();
-  const uint32_t steps = p.H_k * p.prefix_units * ((p.prefix + kPrefixKeys - 1) / kPrefixKeys);
-  const uint32_t own_tiles = count.all * p.H_k * p.blocks;
-  const int own_sms = sms_for_own(p, own_tiles, steps, gridDim.x), prefix_workers = min(steps, gridDim.x - own_sms);
+  const uint32_t tiles = (p.prefix + kPrefixKeys - 1) / kPrefixKeys, steps = p.H_k * p.prefix_units * (tiles + prefix::kUnitCost);
+  const uint32_t own_cost = own::whole_cost(p, count);
+  const int own_sms = sms_for_own(own_cost, steps, p.N * p.tokens * p.group <= kPrefixRows / 2, gridDim.x), prefix_workers = min(steps, gridDim.x - own_sms);
   if (blockIdx.x == 0 && threadIdx.x == 0) *p.prefix_shares = prefix_workers;
   if (blockIdx.x < prefix_workers) {
     prefix::run_worker<F16>(p, smem, blockIdx.x, prefix_workers);
   } else if (blockIdx.x >= gridDim.x - own_sms) {
-    const uint32_t worker = 2 * (blockIdx.x - (gridDim.x - own_sms)) + half, workers = min(own_tiles, 2 * own_sms);
+    const uint32_t worker = 2 * (blockIdx.x - (gridDim.x - own_sms)) + half, workers = min(own_cost, 2 * own_sms);
     if (half < 2 && worker < workers)
       own::run_worker<F16, kEights>(p, smem + half * own::kPlace, tid, count, worker, workers, 1 + 2 * half);
   }
 }
 
 // The parts of the units that were cut, and those of the prefix: `kPer` warps for each row take turns at its
-// parts, four on their way at a time, lanes four columns each.
+// parts, four or eight on their way at a time, lanes four columns each.
 template <bool F16, int kPer>
 __global__ void __launch_bounds__(kPer > 4 ? 32 * kPer : 128) gdn_attention_join_kernel(const __grid_constant__ AttentionParams p) {
-  constexpr int kRowsHere = kPer >= 4 ? 1 : 4 / kPer;
+  constexpr int kRowsHere = kPer >= 4 ? 1 : 4 / kPer, kBatch = kPer > 4 ? 8 : 4;
   __shared__ float s_o[kPer][kHeadDim];
   __shared__ float2 s_ml[kPer];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5 & (kPer - 1);
@@ -124,11 +123,10 @@ __global__ void __launch_bounds__(kPer > 4 ? 32 * kPer : 128) gdn_attention_join
   int turns = 1;  // sums of the row that a worker of the prefix kernel has
   if (many) {
     prefix_unit = hk * p.prefix_units + pr / kPrefixRows;
-    const uint32_t tiles = (p.prefix + kPrefixKeys - 1) / kPrefixKeys;
     const int workers = *p.prefix_shares;
-    const Shares s(tiles * p.H_k * p.prefix_units, max(1, min(workers, p.prefix_workers)));
-    prefix_first = (int)s.share_of(prefix_unit * tiles);
-    shared = (int)s.share_of(prefix_unit * tiles + tiles - 1) - prefix_first + 1;
+    const prefix::Steps steps(p, max(1, min(workers, p.prefix_workers)));
+    prefix_first = steps.worker_of(prefix_unit, 0);
+    shared = steps.worker_of(prefix_unit, steps.tiles - 1) - prefix_first + 1;
     turns = p.N * p.tokens * p.group - pr / kPrefixRows * kPrefixRows <= 128 ? 2 : 1;
   } else if (p.prefix) {
     prefix_unit = p.N * subs + hk * p.prefix_blocks + pr / own::kRows;
@@ -143,11 +141,11 @@ __global__ void __launch_bounds__(kPer > 4 ? 32 * kPer : 128) gdn_attention_join
   const int parts_all = own + shared * turns;
   float top = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = warp; i0 < parts_all; i0 += 4 * kPer) {
-    float2 ml[4];
-    float4 x[4];
+  for (int i0 = warp; i0 < parts_all; i0 += kBatch * kPer) {
+    float2 ml[kBatch];
+    float4 x[kBatch];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < kBatch; ++e) {
       const int i = i0 + e * kPer;
       const bool of_prefix = i >= own, of_many = of_prefix && many;
       const int j2 = of_prefix ? i - own : i, j = of_prefix && turns == 2 ? j2 >> 1 : j2, turn = of_prefix && turns == 2 ? j2 & 1 : 0;
@@ -167,7 +165,7 @@ __global__ void __launch_bounds__(kPer > 4 ? 32 * kPer : 128) gdn_attention_join
     }
     float now = top;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < kBatch; ++e) {
       now = fmaxf(now, ml[e].x);
       bad |= ml[e].y == kAttentionBad;
     }
@@ -176,7 +174,7 @@ __global__ void __launch_bounds__(kPer > 4 ? 32 * kPer : 128) gdn_attention_join
     l *= keep;
     o = make_float4(o.x * keep, o.y * keep, o.z * keep, o.w * keep);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
+    for (int e = 0; e < kBatch; ++e) {
       const float f = exp2_fast(ml[e].x - from_base);
       l = fmaf(f, ml[e].y, l);
       o = make_float4(fmaf(f, x[e].x, o.x), fmaf(f, x[e].y, o.y), fmaf(f, x[e].z, o.z), fmaf(f, x[e].w, o.w));

@@ -23,10 +23,12 @@ constexpr int kHalfBytes = kTile * 128;        // 64 of a row's 128 values
 constexpr int kTileBytes = 4 * kHalfBytes;     // keys, then values
 constexpr int kQueryBytes = kRows * 256;
 static_assert(kWarps * kRows * kHeadDim * 4 == kTileBytes, "the warps' sums lie over a tile");
+// Where a share begins: tile t of `sub` of sequence n, after `index` tiles in all.
+struct Place { uint32_t n, sub, t, index; };
 struct Bars {
   float2 ml[kWarps][kRows];
   uint64_t full[kStages], empty[kStages];
-  uint32_t found[kWarps];                      // the share's start
+  Place found[2];                              // the share's ends
   uint32_t bad[kStages];                       // a page of the stage's tile is none
 };
 constexpr int kBytes = kStages * (kTileBytes + kQueryBytes) + sizeof(Bars);
@@ -189,10 +191,15 @@ __device__ __forceinline__ void copy_tiles(const AttentionParams& p, uint8_t* sm
     if (!(p.hold_copies && k == 0)) mbar_wait(&bar.full[k % kStages], (k / kStages) & 1, kWaitNs);
 }
 
-// Tiles of all sequences, in the units of one (key head, row block), counted by the first 128 of kThreads threads that
+// What a unit costs a worker beside its tiles (its queries, its end), in tiles: shares that count it come out even for short sequences, too.
+constexpr int kUnitCost = 1;
+__device__ __forceinline__ uint32_t cost_of(int length) { return length > 0 ? tiles_of(length) + kUnitCost : 0; }
+
+// Tiles and cost of all sequences, in the units of one (key head, row block), counted by the first 128 of kThreads threads that
 // meet at barrier `id`; `before`: those of the sequences in front of the thread's own, which are `each` in a row.
 struct Count {
-  uint32_t all = 0, before = 0, mine = 0;
+  struct Sums { uint32_t tiles, cost; };
+  Sums all = {0, 0}, before = {0, 0}, mine = {0, 0};
   int each = 0;
   __device__ __forceinline__ void make(const AttentionParams& p, uint32_t* room, int tid, int id, bool report) {
     constexpr int kCounting = 32 * kWarps;
@@ -202,24 +209,37 @@ struct Count {
       for (int i = 0, n = tid * each; i < each && n < p.N; ++i, ++n) {
         const int length = length_of(p, n);
         bad |= length < 0;
-        mine += tiles_of(length);
+        mine.tiles += tiles_of(length);
+        mine.cost += cost_of(length);
       }
     if (bad && report) atomicOr(p.dev_err, kDevErrLength);
-    uint32_t upto = mine;
+    Sums upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
-      const uint32_t x = __shfl_up_sync(0xffffffffu, upto, d);
-      if ((tid & 31) >= d) upto += x;
+      const uint32_t x = __shfl_up_sync(0xffffffffu, upto.tiles, d), y = __shfl_up_sync(0xffffffffu, upto.cost, d);
+      if ((tid & 31) >= d) { upto.tiles += x; upto.cost += y; }
     }
-    if (tid < kCounting && (tid & 31) == 31) room[tid >> 5] = upto;
+    Sums* sums = reinterpret_cast<Sums*>(room);
+    if (tid < kCounting && (tid & 31) == 31) sums[tid >> 5] = upto;
     named_sync(id, kThreads);
-    before = upto - mine;
+    before = {upto.tiles - mine.tiles, upto.cost - mine.cost};
     for (int w = 0; w < kWarps; ++w) {
-      if (w < tid >> 5) before += room[w];
-      all += room[w];
+      if (w < tid >> 5) { before.tiles += sums[w].tiles; before.cost += sums[w].cost; }
+      all.tiles += sums[w].tiles;
+      all.cost += sums[w].cost;
     }
   }
 };
+// The cost of everything that workers of the own pages walk, the prefix of few rows behind the sequences.
+__device__ __forceinline__ uint32_t whole_cost(const AttentionParams& p, const Count& counted) {
+  return counted.all.cost * p.H_k * p.blocks + (p.prefix ? cost_of(p.prefix) * p.H_k * p.prefix_blocks : 0);
+}
+
+// Of the cost's point `at` in a sequence whose units begin at `from`, each of `tiles` tiles, after `index` tiles.
+__device__ __forceinline__ Place place_in(uint32_t n, uint32_t at, uint32_t tiles, uint32_t index) {
+  const uint32_t cost = tiles + kUnitCost, sub = at / cost, in = at - sub * cost, t = in > kUnitCost ? in - kUnitCost : 0;
+  return {n, sub, t, index + sub * tiles + t};
+}
 
 // A worker for units of up to 8 kEights rows: `tid` below kThreads, the tiles counted by just these threads, ring and barriers of its own (initialised here), its number and how many share the tiles.  `id`
 // and the one behind it: barriers of its own.
@@ -234,35 +254,38 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
     }
     fence_mbar_init();
   }
-  const uint32_t prefix_tiles = tiles_of(p.prefix), own_tiles = counted.all * subs;
-  const Shares shares(own_tiles + prefix_tiles * p.H_k * p.prefix_blocks, workers);
-  const uint32_t from = shares.from(worker);
-  const int count = (int)(shares.from(worker + 1) - from);
-  if (tid < 32 * kWarps && counted.before * subs <= from && from < (counted.before + counted.mine) * subs) {  // the share begins in one of these
-    uint32_t at = counted.before;
-    for (int n = tid * counted.each;; ++n) {
-      const uint32_t tiles = tiles_of(length_of(p, n));
-      if (from < (at + tiles) * subs) {
-        const uint32_t in = from - at * subs;
-        bar.found[0] = n;
-        bar.found[1] = in / tiles;
-        bar.found[2] = in % tiles;
-        break;
+  // The share's two ends are looked up by the threads that counted the sequences where they lie.  (An end of everything lies nowhere: all
+  // tiles are before it.)
+  const Shares shares(whole_cost(p, counted), workers);
+  const uint32_t prefix_tiles = tiles_of(p.prefix), own_cost = counted.all.cost * subs, own_tiles = counted.all.tiles * subs;
+#pragma unroll
+  for (int end = 0; end < 2; ++end) {
+    const uint32_t at = shares.from(worker + end);
+    if (tid < 32 * kWarps && counted.before.cost * subs <= at && at < (counted.before.cost + counted.mine.cost) * subs) {
+      uint32_t cost = counted.before.cost * subs, tiles_before = counted.before.tiles * subs;
+      for (int n = tid * counted.each;; ++n) {
+        const int length = length_of(p, n);
+        const uint32_t next = cost + cost_of(length) * subs;
+        if (at < next) {
+          bar.found[end] = place_in(n, at - cost, tiles_of(length), tiles_before);
+          break;
+        }
+        cost = next;
+        tiles_before += tiles_of(length) * subs;
       }
-      at += tiles;
+    }
+    if (tid == 0 && at >= own_cost) {
+      if (prefix_tiles && p.prefix_blocks && at < own_cost + (prefix_tiles + kUnitCost) * p.H_k * p.prefix_blocks) bar.found[end] = place_in(p.N, at - own_cost, prefix_tiles, own_tiles);
+      else bar.found[end] = {0, 0, 0, own_tiles + (p.prefix_blocks ? prefix_tiles * p.H_k * p.prefix_blocks : 0)};
     }
   }
-  if (tid == 0 && from >= own_tiles && prefix_tiles) {
-    bar.found[0] = p.N;
-    bar.found[1] = (from - own_tiles) / prefix_tiles;
-    bar.found[2] = (from - own_tiles) % prefix_tiles;
-  }
   named_sync(id, kThreads);
-  if (count <= 0) return;
+  const int count = (int)(bar.found[1].index - bar.found[0].index);
+  if (count <= 0) return;   // a share that is nothing but a unit's cost
   Walk take;
-  take.n = (int)bar.found[0];
-  take.sub = (int)bar.found[1];
-  take.t = (int)bar.found[2];
+  take.n = (int)bar.found[0].n;
+  take.sub = (int)bar.found[0].sub;
+  take.t = (int)bar.found[0].t;
   take.hold(p, lane);
   take.enter(p, lane);
   const uint64_t limit = p.wait_ns ? p.wait_ns : kWaitNs;
