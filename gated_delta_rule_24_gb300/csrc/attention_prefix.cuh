@@ -59,8 +59,8 @@ struct Bars {
   uint32_t tmem, bad;
 };
 
-// A unit's tiles, and what it costs a worker beside them (rows of Q in, sums out: some 8 us against 1.55 us for a tile).
-constexpr uint32_t kUnitCost = 5;
+// A unit's tiles, and what it costs a worker beside them (rows of Q in, sums out: some 6 us against 1.55 us for a tile).
+constexpr uint32_t kUnitCost = 4;
 struct Steps {
   uint32_t tiles, cost;   // of a unit
   Shares shares;

@@ -224,15 +224,16 @@ cudaError_t launch_norm_rope(const RopeParams& p, cudaStream_t stream) {
   if (rows <= 0) return cudaSuccess;
   const int sms = device_sm_count();
   if (sms <= 0) return cudaErrorInvalidDevice;
-  // Heads a group, up to 16, so that two rounds of groups are left on all SMs, and the loads of up to
-  // four under way: 65536 tokens x 48 heads take 249 us with 16 heads a group, 290 with 4, 428 with 1
-  // (6.6, 5.7 and 3.8 TB/s); 2000 tokens 14.6 us with 3 and two under way, 16.7 with 1, 27 with the
-  // loop that has four.
-  constexpr int kResident = 80, kRounds = 2;  // groups on an SM
-  const int64_t most = rows / ((int64_t)sms * kResident * kRounds);
-  const int per = (int)(most < 1 ? 1 : most > 16 ? 16 : most);
-  if (per < 2) return launch<1>(p, 1, stream);
-  if (per < 4) return launch<2>(p, per, stream);
+  // Heads a group, a power of two up to 16 (heads come in such numbers, and a group with fewer waits for the others), so that one
+  // round of groups is on the SMs; the loads of one, two or four heads under way.  2000 tokens x 32 heads take 6.8 us by eights, 8.2 by
+  // fours, 10.2 by ones (plain; on three axes 8.3, 9.9 and 15.5); 8000 x 16 10.8 to 13.4 us by sixteens, 13.0 to 14.3 by eights;
+  // 65536 x 48 249 us by sixteens, 290 by fours, 428 by ones; 1000 x 10 the same by ones and twos.
+  constexpr int kResident = 80;  // groups on an SM
+  const int64_t places = (int64_t)sms * kResident;
+  int per = 1;
+  while (per < 16 && per * places < rows) per *= 2;
+  if (per < 2) return launch<1>(p, per, stream);
+  if (per < 16) return launch<2>(p, per, stream);
   return launch<4>(p, per, stream);
 }
 
