@@ -1158,6 +1158,7 @@ gdn_status_t gdn_paged_attention_step(const gdn_tensor_t* q, const gdn_tensor_t*
       return fail(GDN_ERR_INVALID_ARGUMENT, "lse must be [T=%lld, H_q=%lld]", (long long)T, (long long)Hq);
     if ((Hq > 1 && lse->stride[1] != 1) || (T > 1 && lse->stride[0] < Hq))
       return fail(GDN_ERR_INVALID_ARGUMENT, "lse rows must be contiguous");
+    if (reinterpret_cast<uintptr_t>(lse->data) % 4) return fail(GDN_ERR_INVALID_ARGUMENT, "lse must be 4-byte aligned");
   }
   for (const gdn_tensor_t* y : {output, lse})
     for (const gdn_tensor_t* in : {q, k_cache, v_cache, page_table, lengths, prefix_pages})

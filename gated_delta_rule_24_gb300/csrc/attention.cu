@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(own::kThreads, kResident) gdn_attention_kernel
   extern __shared__ __align__(1024) uint8_t smem[];
   if (misplaced(p, smem)) return;
   go_ahead();
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 0 && p.pages > 0) {
     tma_prefetch_desc(&p.tm_k);
     tma_prefetch_desc(&p.tm_v);
   }
@@ -69,7 +69,7 @@ __global__ void __launch_bounds__(prefix::kThreads, 1) gdn_attention_both_kernel
   extern __shared__ __align__(1024) uint8_t smem[];
   if (misplaced(p, smem)) return;
   go_ahead();
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 0 && p.pages > 0) {
     tma_prefetch_desc(&p.tm_k);
     tma_prefetch_desc(&p.tm_v);
     tma_prefetch_desc(&p.tm_pk);
