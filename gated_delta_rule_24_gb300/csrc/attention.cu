@@ -87,7 +87,6 @@ __global__ void __launch_bounds__(prefix::kThreads, 1) gdn_attention_both_kernel
   const uint32_t tiles = (p.prefix + kPrefixKeys - 1) / kPrefixKeys, steps = p.H_k * p.prefix_units * (tiles + prefix::kUnitCost);
   const uint32_t own_cost = own::whole_cost(p, count);
   const int own_sms = sms_for_own(own_cost, steps, p.N * p.tokens * p.group <= kPrefixRows / 2, gridDim.x), prefix_workers = min(steps, gridDim.x - own_sms);
-  if (blockIdx.x == 0 && threadIdx.x == 0) *p.prefix_shares = prefix_workers;
   if (blockIdx.x < prefix_workers) {
     prefix::run_worker<F16>(p, smem, blockIdx.x, prefix_workers);
   } else if (blockIdx.x >= gridDim.x - own_sms) {
@@ -98,69 +97,63 @@ __global__ void __launch_bounds__(prefix::kThreads, 1) gdn_attention_both_kernel
 }
 
 // The parts of the units that were cut, and those of the prefix: `kPer` warps for each row take turns at its
-// parts, four or eight on their way at a time, lanes four columns each.
-template <bool F16, int kPer>
-__global__ void __launch_bounds__(kPer > 4 ? 32 * kPer : 128) gdn_attention_join_kernel(const __grid_constant__ AttentionParams p) {
-  constexpr int kRowsHere = kPer >= 4 ? 1 : 4 / kPer, kBatch = kPer > 4 ? 8 : 4;
+// parts, kBatch on their way at a time, lanes four columns each.
+template <int kPer> constexpr int kJoinThreads = 32 * (kPer > 4 ? kPer : 4);
+template <bool F16, int kPer, int kBatch>
+__global__ void __launch_bounds__(kJoinThreads<kPer>) gdn_attention_join_kernel(const __grid_constant__ AttentionParams p) {
+  constexpr int kRowsHere = kJoinThreads<kPer> / 32 / kPer;
   __shared__ float s_o[kPer][kHeadDim];
   __shared__ float2 s_ml[kPer];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5 & (kPer - 1);
-  const int64_t id = (int64_t)blockIdx.x * kRowsHere + (kPer >= 4 ? 0 : threadIdx.x >> 5);
-  grid_wait();
-  if (id >= (int64_t)p.N * p.H_k * p.blocks * p.block_rows) return;
-  const int unit = (int)(id / p.block_rows), row = (int)(id - (int64_t)unit * p.block_rows);
-  const int subs = p.H_k * p.blocks, n = unit / subs, sub = unit - n * subs, hk = sub / p.blocks;
+  const uint32_t id = blockIdx.x * kRowsHere + threadIdx.x / (32 * kPer), subs = p.H_k * p.blocks;
+  const uint32_t unit = id / p.block_rows, row = id - unit * p.block_rows, n = unit / subs, sub = unit - n * subs, hk = sub / p.blocks;
   const int r = (sub - hk * p.blocks) * own::kRows + row;
-  if (r >= p.tokens * p.group) return;
-  const int length = length_of(p, n);
-  // the sequence's own parts: of worker `first` and those behind it, or one of a whole unit
-  int first = p.first_worker[unit], own = p.last_worker[unit] - first + 1;
-  if (length <= 0) first = own = 0;
-  // the prefix' parts of the row, of this kind's workers or of those of the prefix kernel
-  int prefix_first = 0, shared = 0, prefix_unit = 0;
-  const int pr = n * p.tokens * p.group + r;
+  const bool some = n < (uint32_t)p.N && r < p.tokens * p.group;
+  const int length = some ? length_of(p, n) : -1;
+  // the row of the prefix, and its unit of the prefix kernel's or of the walk's
+  const uint32_t pr = n * p.tokens * p.group + r;
   const bool many = p.prefix_units > 0;
-  int turns = 1;  // sums of the row that a worker of the prefix kernel has
-  if (many) {
-    prefix_unit = hk * p.prefix_units + pr / kPrefixRows;
-    const int workers = *p.prefix_shares;
-    const prefix::Steps steps(p, max(1, min(workers, p.prefix_workers)));
-    prefix_first = steps.worker_of(prefix_unit, 0);
-    shared = steps.worker_of(prefix_unit, steps.tiles - 1) - prefix_first + 1;
-    turns = p.N * p.tokens * p.group - pr / kPrefixRows * kPrefixRows <= 128 ? 2 : 1;
-  } else if (p.prefix) {
-    prefix_unit = p.N * subs + hk * p.prefix_blocks + pr / own::kRows;
-    prefix_first = p.first_worker[prefix_unit];
-    shared = p.last_worker[prefix_unit] - prefix_first + 1;
+  const uint32_t prefix_unit = many ? hk * p.prefix_units + pr / kPrefixRows : p.N * subs + hk * p.prefix_blocks + pr / own::kRows;
+  grid_wait();
+  if (length < 0) return;
+  // the sequence's own parts: of worker `first` and those behind it, or one of a whole unit; then the prefix'
+  int first = 0, own = 0, prefix_first = 0, shared = 0;
+  if (p.prefix) {
+    prefix_first = (many ? p.prefix_first : p.first_worker)[prefix_unit];
+    shared = (many ? p.prefix_last : p.last_worker)[prefix_unit] - prefix_first + 1;
   }
-  if (length < 0 || (own == 1 && !p.prefix)) return;  // none, or it is in the output
+  if (length > 0) {
+    first = p.first_worker[unit];
+    own = p.last_worker[unit] - first + 1;
+  }
+  if (own == 1 && !p.prefix) return;  // it is in the output
   // parts of no worker: the kernel before this one gave up, and said so
   bool bad = first < 0 || own < 0 || first + own > p.workers || prefix_first < 0 || shared < 0 ||
              prefix_first + shared > (many ? p.prefix_workers : p.workers);
   if (bad) own = shared = 0;
-  const int parts_all = own + shared * turns;
   float top = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int i0 = warp; i0 < parts_all; i0 += kBatch * kPer) {
+  for (int i0 = warp; i0 < own + shared; i0 += kBatch * kPer) {
     float2 ml[kBatch];
     float4 x[kBatch];
 #pragma unroll
     for (int e = 0; e < kBatch; ++e) {
       const int i = i0 + e * kPer;
-      const bool of_prefix = i >= own, of_many = of_prefix && many;
-      const int j2 = of_prefix ? i - own : i, j = of_prefix && turns == 2 ? j2 >> 1 : j2, turn = of_prefix && turns == 2 ? j2 & 1 : 0;
-      const int parts = of_prefix ? shared : own, w = (of_prefix ? prefix_first : first) + j;
-      const int workers = of_many ? p.prefix_workers : p.workers;
-      const int64_t slot = parts == 1 ? 2 * (int64_t)workers + (of_prefix ? prefix_unit : unit) : 2 * w + (j == 0 ? 1 : 0);
-      const int64_t at = of_many ? slot * kPrefixRows + pr % kPrefixRows + 128 * turn : slot * p.block_rows + (of_prefix ? pr % own::kRows : row);
       ml[e] = make_float2(-INFINITY, 0.f);
       x[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (i < parts_all) {
-        ml[e] = *reinterpret_cast<const float2*>((of_many ? p.prefix_ml : p.part_ml) + 2 * at);
-        const float* y = of_many ? p.prefix_o + (slot * kHeadDim + lane / 2 * 8) * kPrefixRows + (pr % kPrefixRows + 128 * turn) * 8 + (lane & 1) * 4
-                                 : p.part_o + at * kHeadDim + 4 * lane;
-        x[e] = *reinterpret_cast<const float4*>(y);
-        if (ml[e].y == 0.f) x[e] = make_float4(0.f, 0.f, 0.f, 0.f);  // no key: nothing was written
+      if (i >= own + shared) continue;
+      if (i >= own && many) {
+        const int w = prefix_first + i - own;
+        const int64_t slot = shared == 1 ? 2 * (int64_t)p.prefix_workers + prefix_unit : 2 * w + (i == own ? 1 : 0);
+        ml[e] = *reinterpret_cast<const float2*>(p.prefix_ml + 2 * (slot * kPrefixRows + pr % kPrefixRows));
+        x[e] = *reinterpret_cast<const float4*>(p.prefix_o + (slot * kHeadDim + lane / 2 * 8) * kPrefixRows + pr % kPrefixRows * 8 + (lane & 1) * 4);
+      } else {
+        const bool of_prefix = i >= own;
+        const int w = of_prefix ? prefix_first + i - own : first + i;
+        const int64_t slot = (of_prefix ? shared : own) == 1 ? 2 * (int64_t)p.workers + (of_prefix ? prefix_unit : unit) : 2 * w + (i == 0 || i == own ? 1 : 0);
+        const int64_t at = slot * p.block_rows + (of_prefix ? pr % own::kRows : row);
+        ml[e] = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
+        x[e] = *reinterpret_cast<const float4*>(p.part_o + at * kHeadDim + 4 * lane);
       }
     }
     float now = top;
@@ -185,19 +178,23 @@ __global__ void __launch_bounds__(kPer > 4 ? 32 * kPer : 128) gdn_attention_join
     if (lane == 0) s_ml[warp] = make_float2(top, l);
     bad = __syncthreads_or(bad);
     if (warp > 0) return;
-    top = -INFINITY;
+    const float2 ml = lane < kPer ? s_ml[lane] : make_float2(-INFINITY, 0.f);
+    top = ml.x;
 #pragma unroll
-    for (int w = 0; w < kPer; ++w) top = fmaxf(top, s_ml[w].x);
-    const float from_base = top == -INFINITY ? 0.f : top;
-    l = 0.f;
+    for (int d = kPer / 2; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
+    const float f = exp2_fast(ml.x - (top == -INFINITY ? 0.f : top));
+    l = f * ml.y;
+#pragma unroll
+    for (int d = kPer / 2; d > 0; d >>= 1) l += __shfl_xor_sync(0xffffffffu, l, d);
     o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
+#pragma unroll 8
     for (int w = 0; w < kPer; ++w) {
-      const float f = exp2_fast(s_ml[w].x - from_base);
+      const float fw = __shfl_sync(0xffffffffu, f, w);
       const float4 x = reinterpret_cast<const float4*>(s_o[w])[lane];
-      l = fmaf(f, s_ml[w].y, l);
-      o = make_float4(fmaf(f, x.x, o.x), fmaf(f, x.y, o.y), fmaf(f, x.z, o.z), fmaf(f, x.w, o.w));
+      o = make_float4(fmaf(fw, x.x, o.x), fmaf(fw, x.y, o.y), fmaf(fw, x.z, o.z), fmaf(fw, x.w, o.w));
     }
+    top = __shfl_sync(0xffffffffu, top, 0);
+    l = __shfl_sync(0xffffffffu, l, 0);
   }
   if (bad) return;
   const float from_base = top == -INFINITY ? 0.f : top;
@@ -249,13 +246,14 @@ cudaError_t launch(const AttentionParams& p, cudaStream_t stream) {
   if (many) e = launch_behind(gdn_attention_both_kernel<F16, kEights>, p.prefix_workers, prefix::kThreads, kBothBytes, false, p, stream);
   else if (most) e = launch_behind(gdn_attention_kernel<F16, kEights>, std::min<int64_t>(p.workers, most), own::kThreads, own::kBytes, false, p, stream);
   if (e != cudaSuccess) return e;
-  // Warps a row by the parts that a row has about: 16 rows of 152 parts each take 5 us with sixteen, 26 with four.
+  // Warps a row by the parts that a row has about.
   int64_t parts = 1 + p.workers / (own_units + p.H_k * p.prefix_blocks);
   if (many) parts += 1 + p.prefix_workers / ((int64_t)p.H_k * p.prefix_units);
   const int64_t rows = own_units * p.block_rows;
-  if (parts <= 8) return launch_behind(gdn_attention_join_kernel<F16, 1>, (rows + 3) / 4, 128, 0, true, p, stream);
-  if (parts <= 32) return launch_behind(gdn_attention_join_kernel<F16, 4>, rows, 128, 0, true, p, stream);
-  return launch_behind(gdn_attention_join_kernel<F16, 16>, rows, 512, 0, true, p, stream);
+  const bool behind = many || most;   // a kernel of this call: what went before that has ended
+  if (parts <= 8) return launch_behind(gdn_attention_join_kernel<F16, 1, 8>, (rows + 3) / 4, kJoinThreads<1>, 0, behind, p, stream);
+  if (parts <= 64) return launch_behind(gdn_attention_join_kernel<F16, 8, 8>, rows, kJoinThreads<8>, 0, behind, p, stream);
+  return launch_behind(gdn_attention_join_kernel<F16, 32, 5>, rows, kJoinThreads<32>, 0, behind, p, stream);
 }
 
 }  // namespace
@@ -284,12 +282,12 @@ size_t plan_attention(AttentionParams* p, int sms, void* workspace) {
   float* prefix_o = reinterpret_cast<float*>(take((size_t)many_slots * kHeadDim * 4));
   float* part_ml = reinterpret_cast<float*>(take((size_t)slots * 8));
   float* prefix_ml = reinterpret_cast<float*>(take((size_t)many_slots * 8));
-  int32_t* first_worker = reinterpret_cast<int32_t*>(take((size_t)units * 8 + 4));
+  int32_t* first_worker = reinterpret_cast<int32_t*>(take((size_t)(units + many_units) * 8));
   if (workspace) {
     p->part_o = part_o; p->part_ml = part_ml;
     p->prefix_o = prefix_o; p->prefix_ml = prefix_ml;
     p->first_worker = first_worker; p->last_worker = first_worker + units;
-    p->prefix_shares = first_worker + 2 * units;
+    p->prefix_first = first_worker + 2 * units; p->prefix_last = p->prefix_first + many_units;
   }
   return end;
 }

@@ -39,12 +39,12 @@ struct AttentionParams {
   float* part_ml;              // [slots][block_rows][2]: base, sum
   int32_t* first_worker;       // [units], then
   int32_t* last_worker;        // [units]
-  // The prefix by attention_prefix.cuh (prefix_blocks is then 0): units of a key head, workers at most, how many
-  // share the tiles, and their parts.
+  // The prefix by attention_prefix.cuh (prefix_blocks is then 0): units of a key head, workers at most, their parts, and the first and
+  // the last worker of a unit.
   CUtensorMap tm_pk;  // as tm_k, boxes of prefix_box places
   CUtensorMap tm_pv;
   int32_t prefix_box, prefix_units, prefix_workers;
-  int32_t* prefix_shares;
+  int32_t *prefix_first, *prefix_last;  // [units]
   float* prefix_o;   // [slots][16][kPrefixRows][8]: columns by eights
   float* prefix_ml;  // [slots][kPrefixRows][2]
   // Testing aids: the bound of every wait in ns (0: 0.2 s), and the first copy of every warp withheld.

@@ -23,10 +23,6 @@ struct Shares {
   uint32_t each, larger;
   __device__ __forceinline__ Shares(uint32_t total, uint32_t shares) : each(total / shares), larger(total - total / shares * shares) {}
   __device__ __forceinline__ uint32_t from(uint32_t share) const { return share * each + min(share, larger); }
-  __device__ __forceinline__ uint32_t share_of(uint32_t tile) const {
-    const uint32_t end = larger * (each + 1);
-    return tile < end ? tile / (each + 1) : larger + (tile - end) / each;
-  }
 };
 
 // Keys of sequence n in its own pages, or -1 where its length is none.

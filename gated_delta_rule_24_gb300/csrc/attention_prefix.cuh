@@ -18,7 +18,7 @@
 // grow to 2^8 at most, which changes no rounding.  When S of a tile is there, all products issued before it
 // are done, so a row's thread may scale O then without a hand-off of its own.
 //
-// Where a unit has no more than 128 rows, A and B are the same rows and take every other tile of keys, each with sums of its own.
+// Where a unit has no more than 128 rows, A and B are the same rows and take every other tile of keys, and their sums come together at the end of a piece.
 //
 // Units are (key head, 256 rows), a unit's tiles of 128 keys come one behind the other, and all units'
 // tiles are cut into equal shares for the SMs; the parts are joined by attention.cu's second kernel.
@@ -33,7 +33,7 @@ constexpr int kHalf = 16384;                  // 128 rows of 64 values
 constexpr int kTileBytes = 2 * kHalf;
 constexpr int kStages = 2;                    // of keys, and of values
 constexpr int kQ = 0, kK = 2 * kTileBytes, kV = kK + kStages * kTileBytes, kBars = kV + kStages * kTileBytes;
-constexpr int kBytes = kBars + 256;
+constexpr int kBytes = kBars + 4096;
 
 constexpr uint32_t kS = 0, kO = 256;          // TMEM columns: S of A and B (and P over it), O of A and B
 __device__ __forceinline__ float2 add2(float2 a, float2 b) {
@@ -57,7 +57,10 @@ struct Bars {
   uint64_t k_full[kStages], k_empty[kStages], v_full[kStages], v_empty[kStages];
   uint64_t q_full[2], s_full[2], p_full[2][2], o_full[2], done;
   uint32_t tmem, bad;
+  float2 ml[2][128];   // base and sum of A's and B's rows where they are the same
 };
+
+static_assert(sizeof(Bars) <= kBytes - kBars, "room for them");
 
 // A unit's tiles, and what it costs a worker beside them (rows of Q in, sums out: some 6 us against 1.55 us for a tile).
 constexpr uint32_t kUnitCost = 4;
@@ -66,7 +69,6 @@ struct Steps {
   Shares shares;
   __device__ __forceinline__ Steps(const AttentionParams& p, int workers)
       : tiles((p.prefix + kPrefixKeys - 1) / kPrefixKeys), cost(tiles + kUnitCost), shares(p.H_k * p.prefix_units * cost, workers) {}
-  __device__ __forceinline__ int worker_of(uint32_t unit, uint32_t tile) const { return (int)shares.share_of(unit * cost + kUnitCost + tile); }
 };
 
 // The share of a worker, and the pieces of units that it makes.
@@ -394,29 +396,66 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
       const bool some = !turn || x < share.n;  // tiles for this group
       if (some) wait(&bar.o_full[x], pieces++);
       tc_fence_after();
-      const bool whole = share.t0 == 0 && share.n == (int)share.tiles, write = r < rows_all;
-      const int64_t slot = whole ? 2 * (int64_t)p.prefix_workers + share.unit : 2 * (int64_t)worker + (share.t0 == 0 ? 1 : 0);
-      const int row = 128 * x + i128;
-      if (some && !dead) {
-        float* y = p.prefix_o + slot * kPrefixRows * kHeadDim + row * 8;   // by eights of columns: a warp writes 1 KB in a row
-#pragma unroll 1
-        for (int h = 0; h < 4; ++h) {
-          uint32_t o[32];
-          tmem_ld32(o_at + 32 * h, o);
-          loaded(o);
-          if (write) {
+      const bool ends = share.t0 + share.n == (int)share.tiles, write = r < rows_all;
+      if (tid == 0) {
+        if (share.t0 == 0) p.prefix_first[share.unit] = worker;
+        if (ends) p.prefix_last[share.unit] = worker;
+      }
+      const int64_t slot = share.t0 == 0 && ends ? 2 * (int64_t)p.prefix_workers + share.unit : 2 * (int64_t)worker + (share.t0 == 0 ? 1 : 0);
+      const int row = turn ? i128 : 128 * x + i128;
+      float* y = p.prefix_o + slot * kPrefixRows * kHeadDim + row * 8;   // by eights of columns: a warp writes 1 KB in a row
+      const auto store = [&](int h, const uint32_t (&o)[32]) {
+        if (!write) return;
 #pragma unroll
-            for (int e = 0; e < 32; e += 8)
-              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(y + (4 * h + e / 8) * kPrefixRows * 8),
-                           "r"(o[e]), "r"(o[e + 1]), "r"(o[e + 2]), "r"(o[e + 3]), "r"(o[e + 4]), "r"(o[e + 5]), "r"(o[e + 6]), "r"(o[e + 7])
-                           : "memory");
+        for (int e = 0; e < 32; e += 8)
+          asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(y + (4 * h + e / 8) * kPrefixRows * 8),
+                       "r"(o[e]), "r"(o[e + 1]), "r"(o[e + 2]), "r"(o[e + 3]), "r"(o[e + 4]), "r"(o[e + 5]), "r"(o[e + 6]), "r"(o[e + 7])
+                       : "memory");
+      };
+      float total = sum.x + sum.y;
+      if (dead || *reinterpret_cast<volatile uint32_t*>(&bar.bad)) total = kAttentionBad;
+      if (!turn) {
+        if (!dead) {
+#pragma unroll 1
+          for (int h = 0; h < 4; ++h) {
+            uint32_t o[32];
+            tmem_ld32(o_at + 32 * h, o);
+            loaded(o);
+            store(h, o);
           }
         }
+      } else {  // the sums of A and B come together, half the columns in each group
+        bar.ml[x][i128] = make_float2(base, total);
+        tc_fence_before();
+        named_sync(1, 256);
+        tc_fence_after();
+        const float2 other = bar.ml[x ^ 1][i128];
+        const bool any_bad = total == kAttentionBad || other.y == kAttentionBad;
+        const float now = fmaxf(base, other.x), from_base = now == -INFINITY ? 0.f : now;
+        const float mine = exp2_fast(base - from_base), theirs = exp2_fast(other.x - from_base);
+        if (!any_bad) {
+          const uint32_t o_theirs = tmem + kO + 128 * (x ^ 1) + lanes;
+          const bool have_mine = some, have_theirs = (x ^ 1) < share.n;   // O of a group without tiles holds anything
+#pragma unroll 1
+          for (int h = 2 * x; h < 2 * x + 2; ++h) {
+            uint32_t o[32], o2[32];
+            tmem_ld32(o_at + 32 * h, o);
+            tmem_ld32(o_theirs + 32 * h, o2);
+            loaded(o);
+            loaded(o2);
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              o[e] = __float_as_uint((have_mine ? mine * __uint_as_float(o[e]) : 0.f) + (have_theirs ? theirs * __uint_as_float(o2[e]) : 0.f));
+            store(h, o);
+          }
+        }
+        base = now;
+        total = any_bad ? kAttentionBad : mine * total + theirs * other.y;
+        tc_fence_before();
+        named_sync(1, 256);   // before either O is another's
+        tc_fence_after();
       }
-      if (write) {
-        const bool bad = dead || *reinterpret_cast<volatile uint32_t*>(&bar.bad);
-        *reinterpret_cast<float2*>(p.prefix_ml + 2 * (slot * kPrefixRows + row)) = make_float2(base, bad ? kAttentionBad : sum.x + sum.y);
-      }
+      if (write && (!turn || x == 0)) *reinterpret_cast<float2*>(p.prefix_ml + 2 * (slot * kPrefixRows + row)) = make_float2(base, total);
       tc_fence_before();
     }
   }
