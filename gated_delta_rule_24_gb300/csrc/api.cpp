@@ -891,19 +891,19 @@ bool caches_apart(const gdn_tensor_t* a, const gdn_tensor_t* b) {
   return !rows_meet(a, bytes / 2, order, 3);
 }
 
-// A paged cache in boxes of (64 values, 1 head, `rows` places, 1 page), 128B swizzle.
-gdn_status_t encode_cache(CUtensorMap* m, const gdn_tensor_t* t, const char* name, uint32_t rows) {
+// A paged cache in boxes of `rows` places of a page and one head, 128B swizzle: of 64 values each, or (`both`) of the
+// two halves of a row one behind the other.
+gdn_status_t encode_cache(CUtensorMap* m, const gdn_tensor_t* t, const char* name, uint32_t rows, bool both) {
   memset(m, 0, sizeof(*m));
   if (t->shape[0] == 0) return GDN_OK;  // no page will ever be loaded
-  cuuint64_t dims[4] = {128, (cuuint64_t)t->shape[2], (cuuint64_t)t->shape[1], (cuuint64_t)t->shape[0]};
-  cuuint64_t strides[3];
-  for (int d = 0; d < 3; ++d)  // that of a single head, place or page can be anything
-    strides[d] = t->shape[2 - d] > 1 ? (cuuint64_t)t->stride[2 - d] * 2 : 256;
-  cuuint32_t box[4] = {64, 1, rows, 1};
-  cuuint32_t estr[4] = {1, 1, 1, 1};
-  CUresult r = g_encode(m, t->dtype == GDN_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4, t->data, dims,
-                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  auto stride = [&](int d) { return t->shape[d] > 1 ? (cuuint64_t)t->stride[d] * 2 : 256; };  // that of a single head, place or page can be anything
+  const cuuint64_t heads = t->shape[2], places = t->shape[1], pages = t->shape[0];
+  const cuuint64_t dims4[4] = {128, heads, places, pages}, strides4[3] = {stride(2), stride(1), stride(0)};
+  const cuuint64_t dims5[5] = {64, places, 2, heads, pages}, strides5[4] = {stride(1), 128, stride(2), stride(0)};
+  const cuuint32_t box4[4] = {64, 1, rows, 1}, box5[5] = {64, rows, 2, 1, 1}, estr[5] = {1, 1, 1, 1, 1};
+  CUresult r = g_encode(m, t->dtype == GDN_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, both ? 5 : 4, t->data,
+                        both ? dims5 : dims4, both ? strides5 : strides4, both ? box5 : box4, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   if (r != CUDA_SUCCESS) return fail(GDN_ERR_INVALID_ARGUMENT, "TMA descriptor for %s rejected (CUresult %d)", name, (int)r);
   return GDN_OK;
 }
@@ -1174,8 +1174,8 @@ gdn_status_t gdn_paged_attention_step(const gdn_tensor_t* q, const gdn_tensor_t*
   p.prefix_box = 8;
   while (p.prefix_box < gdn::kPrefixKeys && page_size % (2 * p.prefix_box) == 0) p.prefix_box *= 2;
   p.box_rows = std::min(p.prefix_box, gdn::kOwnKeys);
-  if ((st = encode_cache(&p.tm_k, k_cache, "k_cache", p.box_rows)) != GDN_OK) return st;
-  if ((st = encode_cache(&p.tm_v, v_cache, "v_cache", p.box_rows)) != GDN_OK) return st;
+  if ((st = encode_cache(&p.tm_k, k_cache, "k_cache", p.box_rows, true)) != GDN_OK) return st;
+  if ((st = encode_cache(&p.tm_v, v_cache, "v_cache", p.box_rows, true)) != GDN_OK) return st;
   p.table = page_table->data; p.table_st = page_table->stride[0]; p.table_dtype = page_table->dtype;
   p.max_pages = (int32_t)page_table->shape[1];
   p.lengths = lengths->data; p.len_dtype = lengths->dtype;
@@ -1184,8 +1184,8 @@ gdn_status_t gdn_paged_attention_step(const gdn_tensor_t* q, const gdn_tensor_t*
   if (lse) { p.lse = static_cast<float*>(lse->data); p.lse_st = lse->stride[0]; }
   p.dev_err = g_dev[dev].dev_err;
   if (prefix_length) {
-    if ((st = encode_cache(&p.tm_pk, k_cache, "k_cache", p.prefix_box)) != GDN_OK) return st;
-    if ((st = encode_cache(&p.tm_pv, v_cache, "v_cache", p.prefix_box)) != GDN_OK) return st;
+    if ((st = encode_cache(&p.tm_pk, k_cache, "k_cache", p.prefix_box, false)) != GDN_OK) return st;
+    if ((st = encode_cache(&p.tm_pv, v_cache, "v_cache", p.prefix_box, false)) != GDN_OK) return st;
   }
   p.pages = k_cache->shape[0];
   p.N = (int32_t)N; p.tokens = (int32_t)tokens; p.H_q = (int32_t)Hq; p.H_k = (int32_t)Hk; p.page_size = (int32_t)page_size;

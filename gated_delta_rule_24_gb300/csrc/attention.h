@@ -12,7 +12,7 @@ constexpr int kPrefixKeys = 128, kPrefixRows = 256;  // tiles of attention_prefi
 constexpr float kAttentionBad = -1.f;                // as a part's sum: it met a bad page, or gave up
 
 struct AttentionParams {
-  CUtensorMap tm_k;  // [pages, page_size, H_k, 128], box (64 values, 1 head, box_rows places, 1 page), 128B swizzle
+  CUtensorMap tm_k;  // [pages, H_k, 2 halves, page_size, 64], box (64 values, box_rows places, 2 halves, 1 head, 1 page), 128B swizzle
   CUtensorMap tm_v;
   const void* q;  // [N * tokens, H_q, 128], strides in elements
   int64_t q_st, q_sh;
@@ -41,7 +41,7 @@ struct AttentionParams {
   int32_t* last_worker;        // [units]
   // The prefix by attention_prefix.cuh (prefix_blocks is then 0): units of a key head, workers at most, their parts, and the first and
   // the last worker of a unit.
-  CUtensorMap tm_pk;  // as tm_k, boxes of prefix_box places
+  CUtensorMap tm_pk;  // [pages, page_size, H_k, 128], box (64 values, 1 head, prefix_box places, 1 page), 128B swizzle
   CUtensorMap tm_pv;
   int32_t prefix_box, prefix_units, prefix_workers;
   int32_t *prefix_first, *prefix_last;  // [units]

@@ -19,8 +19,8 @@ constexpr int kWarpKeys = 16, kTile = kWarps * kWarpKeys;
 static_assert(kTile == kOwnKeys, "boxes fit a tile");
 constexpr int kRows = 16;                      // rows of a unit
 constexpr int kStages = 3;
-constexpr int kHalfBytes = kTile * 128;        // 64 of a row's 128 values
-constexpr int kTileBytes = 4 * kHalfBytes;     // keys, then values
+constexpr int kKeysBytes = kTile * 256;
+constexpr int kTileBytes = 2 * kKeysBytes;     // keys, then values; either box by box, a box' rows by halves of 64 values
 constexpr int kQueryBytes = kRows * 256;
 static_assert(kWarps * kRows * kHeadDim * 4 == kTileBytes, "the warps' sums lie over a tile");
 // Where a share begins: tile t of `sub` of sequence n, after `index` tiles in all.
@@ -161,11 +161,9 @@ __device__ __forceinline__ void copy_tiles(const AttentionParams& p, uint8_t* sm
     __syncwarp();
     if (page >= 0 && !held) {
       const int row = (walk.t * kTile + lane * p.box_rows) % p.page_size, head = walk.sub / (walk.n < p.N ? p.blocks : p.prefix_blocks);
-      uint8_t* at = tile + lane * p.box_rows * 128;
-      for (int half = 0; half < 2; ++half) {
-        tma_load_4d(at + half * kHalfBytes, &p.tm_k, full, 64 * half, head, row, (int)page);
-        tma_load_4d(at + (2 + half) * kHalfBytes, &p.tm_v, full, 64 * half, head, row, (int)page);
-      }
+      uint8_t* at = tile + lane * p.box_rows * 256;
+      tma_load_5d(at, &p.tm_k, full, 0, row, 0, head, (int)page);
+      tma_load_5d(at + kKeysBytes, &p.tm_v, full, 0, row, 0, head, (int)page);
     }
     if (k == 0 || walk.t == 0) {  // the queries: half a warp a row
       const Unit u(p, walk);
@@ -299,6 +297,8 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
   const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
   constexpr float kBias = F16 ? 6.f : 0.f;  // f16 weights are kept 2^6 above their normal range's end for longer
   const int mi = lane >> 3, mj = lane & 7;
+  // the warp's 16 rows in a tile: where they begin, how far the second eight and the second half of a row are
+  const int box = p.box_rows, mine = warp * kWarpKeys / box * box * 256 + warp * kWarpKeys % box * 128, eights = box > 8 ? 1024 : 2048, halves = box * 128;
   bool dead = false;
   int k = 0, stage = 0;
   uint32_t phase = 0;
@@ -337,12 +337,12 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
       unit_bad |= dead || bar.bad[stage];
       const int key0 = take.t * kTile + warp * kWarpKeys, valid = min(kWarpKeys, take.length - key0);
       if (valid > 0 && !unit_bad) {
-        const uint32_t kb = tile + warp * kWarpKeys * 128, vb = kb + 2 * kHalfBytes;
+        const uint32_t kb = tile + mine, vb = kb + kKeysBytes;
         // Fragments are loaded ahead of the products that take them, the first of the values' before the weights are made.
         // (A row's chunk c of 16 bytes lies at c ^ row % 8: only these bits of an address change from step to step.)
-        const uint32_t keys_at = kb + ((mi & 1) * 8 + mj) * 128 + (((mi >> 1) ^ mj) << 4), values_at = vb + ((mi >> 1) * 8 + mj) * 128 + (((mi & 1) ^ mj) << 4);
-        const auto load_keys = [&](int kk, uint32_t (&to)[4]) { ldmatrix_x4((keys_at ^ ((kk & 3) << 5)) + (kk >> 2) * kHalfBytes, to); };
-        const auto load_values = [&](int j, uint32_t (&to)[4]) { ldmatrix_x4_trans((values_at ^ ((j & 3) << 5)) + (j >> 2) * kHalfBytes, to); };
+        const uint32_t keys_at = kb + (mi & 1) * eights + mj * 128 + (((mi >> 1) ^ mj) << 4), values_at = vb + (mi >> 1) * eights + mj * 128 + (((mi & 1) ^ mj) << 4);
+        const auto load_keys = [&](int kk, uint32_t (&to)[4]) { ldmatrix_x4((keys_at ^ ((kk & 3) << 5)) + (kk >> 2) * halves, to); };
+        const auto load_values = [&](int j, uint32_t (&to)[4]) { ldmatrix_x4_trans((values_at ^ ((j & 3) << 5)) + (j >> 2) * halves, to); };
         float acc[kEights][2][4] = {};  // even and odd steps; (key t / 4, both rows), (key t / 4 + 8, both rows)
         constexpr int kAhead = kEights == 1 ? 2 : 1;   // as registers allow
         uint32_t f[kAhead + 1][4];
@@ -414,7 +414,7 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
           for (int n = lane; n < (valid - some) * 16; n += 32) {
             const int j = some + n / 16, chunk = n % 16;
             uint32_t x[4];
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(vb + (chunk >> 3) * kHalfBytes + j * 128 + ((chunk & 7) << 4)));
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(vb + (chunk >> 3) * halves + (j >> 3) * eights + (j & 7) * 128 + ((chunk & 7) << 4)));
             constexpr uint32_t kTop = F16 ? 0x7c00u : 0x7f80u;
 #pragma unroll
             for (int e = 0; e < 4; ++e) odd |= (x[e] & kTop) == kTop || (x[e] >> 16 & kTop) == kTop;
@@ -438,7 +438,7 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
                 for (int n = 0; n < 16; ++n) {
                   const int value = 8 * n + at_lane / 4;
                   uint16_t x;
-                  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(vb + (n >> 3) * kHalfBytes + j * 128 + (((n & 7) ^ (j & 7)) << 4) + 2 * (value & 7)));
+                  asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(vb + (n >> 3) * halves + (j >> 3) * eights + (j & 7) * 128 + (((n & 7) ^ (j & 7)) << 4) + 2 * (value & 7)));
                   float& to = o[g][n >> 1][e + 2 * (n & 1)];
                   to = fmaf(pj, unpack16<F16>((uint32_t)x).x, to);
                 }
@@ -447,7 +447,7 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
           __syncwarp();
           for (int n = lane; n < (kWarpKeys - clean) * 16; n += 32) {
             const int j = clean + n / 16, chunk = n % 16;
-            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + (chunk >> 3) * kHalfBytes + j * 128 + ((chunk & 7) << 4)), "r"(0) : "memory");
+            asm volatile("st.shared.v4.b32 [%0], {%1, %1, %1, %1};" ::"r"(vb + (chunk >> 3) * halves + (j >> 3) * eights + (j & 7) * 128 + ((chunk & 7) << 4)), "r"(0) : "memory");
           }
           fence_proxy_async_smem();
           __syncwarp();

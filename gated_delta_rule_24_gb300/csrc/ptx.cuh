@@ -121,6 +121,14 @@ GDN_DEV void tma_load_4d(void* dst, const void* tmap, uint64_t* bar, int c0, int
       "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
       : "memory");
 }
+// 5-D tiled load; coordinates innermost first, in elements.
+GDN_DEV void tma_load_5d(void* dst, const void* tmap, uint64_t* bar, int c0, int c1, int c2, int c3, int c4) {
+  asm volatile(
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
+      "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar))
+      : "memory");
+}
 // Takes over a CTA of this grid that has not been launched yet, if there is one: 16 bytes of response
 // to shared memory.  Not to be asked again after a "none".
 GDN_DEV void clc_ask(void* response, uint64_t* bar) {
