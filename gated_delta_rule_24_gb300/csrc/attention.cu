@@ -54,12 +54,12 @@ __global__ void __launch_bounds__(own::kThreads, kResident) gdn_attention_kernel
   own::run_worker<F16, kEights>(p, smem, threadIdx.x, count, blockIdx.x, workers, 1);
 }
 
-// SMs out of `sms` for the own pages beside a prefix of many rows, by what the two take an SM: 0.42 us for a tile's cost (two
+// SMs out of `sms` for the own pages beside a prefix of many rows, by what the two take an SM: 0.38 us for a tile's cost (two
 // workers side by side), 1.55 us for 128 keys of 256 rows.  A prefix of up to 128 rows is held by HBM, too, and loses little by an SM
 // less, while the own pages get on more slowly beside it.
 __device__ __forceinline__ int sms_for_own(uint32_t own_cost, uint32_t prefix_cost, bool few_rows, int sms) {
   if (own_cost == 0) return 0;
-  const float own = (few_rows ? 1.f : 0.42f) * own_cost, prefix = 1.55f * prefix_cost;
+  const float own = (few_rows ? 1.f : 0.38f) * own_cost, prefix = 1.55f * prefix_cost;
   return max(1, min((int)(sms * (own / (own + prefix)) + 0.5f), sms - 1));
 }
 
@@ -246,14 +246,16 @@ cudaError_t launch(const AttentionParams& p, cudaStream_t stream) {
   if (many) e = launch_behind(gdn_attention_both_kernel<F16, kEights>, p.prefix_workers, prefix::kThreads, kBothBytes, false, p, stream);
   else if (most) e = launch_behind(gdn_attention_kernel<F16, kEights>, std::min<int64_t>(p.workers, most), own::kThreads, own::kBytes, false, p, stream);
   if (e != cudaSuccess) return e;
-  // Warps a row by the parts that a row has about.
+  // Warps a row by the parts that a row has about, as long as the rows' CTAs find a place all at once (three of eight warps or one of 32
+  // an SM); after that rows keep the SMs busy with a warp each.
+  const int64_t prefix_tiles = ((int64_t)p.prefix + kPrefixKeys - 1) / kPrefixKeys, sms = p.workers / kResident;
   int64_t parts = 1 + p.workers / (own_units + p.H_k * p.prefix_blocks);
-  if (many) parts += 1 + p.prefix_workers / ((int64_t)p.H_k * p.prefix_units);
+  if (many) parts += 1 + std::min<int64_t>(prefix_tiles - 1, p.prefix_workers / ((int64_t)p.H_k * p.prefix_units));
   const int64_t rows = own_units * p.block_rows;
   const bool behind = many || most;   // a kernel of this call: what went before that has ended
-  if (parts <= 8) return launch_behind(gdn_attention_join_kernel<F16, 1, 8>, (rows + 3) / 4, kJoinThreads<1>, 0, behind, p, stream);
-  if (parts <= 64) return launch_behind(gdn_attention_join_kernel<F16, 8, 8>, rows, kJoinThreads<8>, 0, behind, p, stream);
-  return launch_behind(gdn_attention_join_kernel<F16, 32, 5>, rows, kJoinThreads<32>, 0, behind, p, stream);
+  if (parts > 64 && rows <= sms) return launch_behind(gdn_attention_join_kernel<F16, 32, 5>, rows, kJoinThreads<32>, 0, behind, p, stream);
+  if (parts > 8 && rows <= 3 * sms) return launch_behind(gdn_attention_join_kernel<F16, 8, 8>, rows, kJoinThreads<8>, 0, behind, p, stream);
+  return launch_behind(gdn_attention_join_kernel<F16, 1, 8>, (rows + 3) / 4, kJoinThreads<1>, 0, behind, p, stream);
 }
 
 }  // namespace
@@ -261,6 +263,9 @@ cudaError_t launch(const AttentionParams& p, cudaStream_t stream) {
 size_t plan_attention(AttentionParams* p, int sms, void* workspace) {
   p->group = p->H_q / p->H_k;
   const int64_t rows = (int64_t)p->tokens * p->group, all = p->N * rows;
+  // More than a block's rows a key head go to the tensor cores, whatever the prefix' length.  8 rows of 2 key heads and 30000 keys take
+  // 14.4 us there and 12.8 us in the walk, 16 rows of 8 heads 32.6 and 34.8 us, 256 rows of 4 heads and 64 keys 14.4 and 14.3 us,
+  // 8192 keys 23 and 40 us (with 300 keys of its own a sequence).
   const bool many = p->prefix && all > own::kRows;
   p->workers = kResident * sms;
   p->blocks = (int32_t)((rows + own::kRows - 1) / own::kRows);

@@ -190,7 +190,7 @@ __device__ __forceinline__ void copy_tiles(const AttentionParams& p, uint8_t* sm
 }
 
 // What a unit costs a worker beside its tiles (its queries, its end), in tiles: shares that count it come out even for short sequences, too.
-constexpr int kUnitCost = 1;
+constexpr int kUnitCost = 2;
 __device__ __forceinline__ uint32_t cost_of(int length) { return length > 0 ? tiles_of(length) + kUnitCost : 0; }
 
 // Tiles and cost of all sequences, in the units of one (key head, row block), counted by the first 128 of kThreads threads that
