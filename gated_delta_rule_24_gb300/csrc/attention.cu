@@ -48,19 +48,19 @@ __global__ void __launch_bounds__(own::kThreads, kResident) gdn_attention_kernel
   }
   own::Count count;
   count.make(p, reinterpret_cast<uint32_t*>(smem), threadIdx.x, 1, blockIdx.x == 0);
-  // no more workers than there is to share: one without anything between two parts of a unit would leave a gap
-  const uint32_t workers = min(own::whole_cost(p, count), gridDim.x);
-  if (blockIdx.x >= workers) return;
-  own::run_worker<F16, kEights>(p, smem, threadIdx.x, count, blockIdx.x, workers, 1);
+  // no more shares than there is to share: one without anything between two parts of a unit would leave a gap
+  const uint32_t shares = min(own::whole_cost(p, count), gridDim.x / p.blocks_aside);
+  if (blockIdx.x >= shares * p.blocks_aside) return;
+  own::run_worker<F16, kEights>(p, smem, threadIdx.x, count, blockIdx.x, shares, 1);
 }
 
 // SMs out of `sms` for the own pages beside a prefix of many rows, by what the two take an SM: 0.38 us for a tile's cost (two
 // workers side by side), 1.55 us for 128 keys of 256 rows.  A prefix of up to 128 rows is held by HBM, too, and loses little by an SM
 // less, while the own pages get on more slowly beside it.
-__device__ __forceinline__ int sms_for_own(uint32_t own_cost, uint32_t prefix_cost, bool few_rows, int sms) {
+__device__ __forceinline__ int sms_for_own(uint32_t own_cost, int aside, uint32_t prefix_cost, bool few_rows, int sms) {
   if (own_cost == 0) return 0;
-  const float own = (few_rows ? 1.f : 0.38f) * own_cost, prefix = 1.55f * prefix_cost;
-  return max(1, min((int)(sms * (own / (own + prefix)) + 0.5f), sms - 1));
+  const float own = (few_rows ? 1.f : 0.38f) * own_cost * aside, prefix = 1.55f * prefix_cost;
+  return max((aside + 1) / 2, min((int)(sms * (own / (own + prefix)) + 0.5f), sms - 1));
 }
 
 // The own pages and a prefix of many rows side by side: a CTA is one worker of the prefix, or two of the own pages.
@@ -86,13 +86,13 @@ __global__ void __launch_bounds__(prefix::kThreads, 1) gdn_attention_both_kernel
   __syncthreads();
   const uint32_t tiles = (p.prefix + kPrefixKeys - 1) / kPrefixKeys, steps = p.H_k * p.prefix_units * (tiles + prefix::kUnitCost);
   const uint32_t own_cost = own::whole_cost(p, count);
-  const int own_sms = sms_for_own(own_cost, steps, p.N * p.tokens * p.group <= kPrefixRows / 2, gridDim.x), prefix_workers = min(steps, gridDim.x - own_sms);
+  const int own_sms = sms_for_own(own_cost, p.blocks_aside, steps, p.N * p.tokens * p.group <= kPrefixRows / 2, gridDim.x), prefix_workers = min(steps, gridDim.x - own_sms);
   if (blockIdx.x < prefix_workers) {
     prefix::run_worker<F16>(p, smem, blockIdx.x, prefix_workers);
   } else if (blockIdx.x >= gridDim.x - own_sms) {
-    const uint32_t worker = 2 * (blockIdx.x - (gridDim.x - own_sms)) + half, workers = min(own_cost, 2 * own_sms);
-    if (half < 2 && worker < workers)
-      own::run_worker<F16, kEights>(p, smem + half * own::kPlace, tid, count, worker, workers, 1 + 2 * half);
+    const uint32_t worker = 2 * (blockIdx.x - (gridDim.x - own_sms)) + half, shares = min(own_cost, (uint32_t)(2 * own_sms / p.blocks_aside));
+    if (half < 2 && worker < shares * p.blocks_aside)
+      own::run_worker<F16, kEights>(p, smem + half * own::kPlace, tid, count, worker, shares, 1 + 2 * half);
   }
 }
 
@@ -124,11 +124,11 @@ __global__ void __launch_bounds__(kJoinThreads<kPer>) gdn_attention_join_kernel(
   }
   if (length > 0) {
     first = p.first_worker[unit];
-    own = p.last_worker[unit] - first + 1;
+    own = (p.last_worker[unit] - first) / p.blocks_aside + 1;   // the workers of one side of the shares
   }
   if (own == 1 && !p.prefix) return;  // it is in the output
   // parts of no worker: the kernel before this one gave up, and said so
-  bool bad = first < 0 || own < 0 || first + own > p.workers || prefix_first < 0 || shared < 0 ||
+  bool bad = first < 0 || own < 0 || first + (own - 1) * p.blocks_aside >= p.workers || prefix_first < 0 || shared < 0 ||
              prefix_first + shared > (many ? p.prefix_workers : p.workers);
   if (bad) own = shared = 0;
   float top = -INFINITY, l = 0.f;
@@ -149,7 +149,7 @@ __global__ void __launch_bounds__(kJoinThreads<kPer>) gdn_attention_join_kernel(
         x[e] = *reinterpret_cast<const float4*>(p.prefix_o + (slot * kHeadDim + lane / 2 * 8) * kPrefixRows + pr % kPrefixRows * 8 + (lane & 1) * 4);
       } else {
         const bool of_prefix = i >= own;
-        const int w = of_prefix ? prefix_first + i - own : first + i;
+        const int w = of_prefix ? prefix_first + i - own : first + i * p.blocks_aside;
         const int64_t slot = (of_prefix ? shared : own) == 1 ? 2 * (int64_t)p.workers + (of_prefix ? prefix_unit : unit) : 2 * w + (i == 0 || i == own ? 1 : 0);
         const int64_t at = slot * p.block_rows + (of_prefix ? pr % own::kRows : row);
         ml[e] = *reinterpret_cast<const float2*>(p.part_ml + 2 * at);
@@ -269,6 +269,8 @@ size_t plan_attention(AttentionParams* p, int sms, void* workspace) {
   const bool many = p->prefix && all > own::kRows;
   p->workers = kResident * sms;
   p->blocks = (int32_t)((rows + own::kRows - 1) / own::kRows);
+  p->block_groups = (p->blocks + 3) / 4;   // L2 feeds some two to three times what HBM does, so more side by side gain nothing
+  p->blocks_aside = (p->blocks + p->block_groups - 1) / p->block_groups;
   p->prefix_blocks = p->prefix && !many ? 1 : 0;
   p->block_rows = (int32_t)std::min<int64_t>(own::kRows, p->prefix_blocks ? all : rows);
   p->prefix_units = many ? (int32_t)((all + kPrefixRows - 1) / kPrefixRows) : 0;

@@ -33,7 +33,8 @@ struct AttentionParams {
   int32_t op_f16;
   // Workers, units and where their partial results go (attention.cu says what these are).
   int32_t workers;
-  int32_t blocks, block_rows;  // row blocks of a (sequence, key head) and the rows of one
+  int32_t blocks, block_rows;          // row blocks of a (sequence, key head) and the rows of one
+  int32_t block_groups, blocks_aside;  // groups of blocks, and the blocks of one (the last group may have fewer)
   int32_t prefix_blocks;       // row blocks of a key head for the prefix
   float* part_o;               // [slots][block_rows][128]
   float* part_ml;              // [slots][block_rows][2]: base, sum

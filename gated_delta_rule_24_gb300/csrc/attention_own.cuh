@@ -54,8 +54,9 @@ __device__ __forceinline__ int here(int x) {
 
 __device__ __forceinline__ int tiles_of(int length) { return length > 0 ? (length + kTile - 1) / kTile : 0; }
 
-// A tile of the walk through all units: sequence n (N: the prefix), `sub` = key head * row blocks + row
-// block, tile t.  The lanes of a warp hold the lengths of 32 sequences.
+// A tile of the walk through all units: sequence n (N: the prefix), `sub` = key head * groups of row blocks + group, tile t.  The
+// blocks of a group are walked by as many workers side by side, so that a key that one reads is in L2 for the others.
+// The lanes of a warp hold the lengths of 32 sequences.
 struct Walk {
   int n, sub, t, tiles, length, subs;
   int held, held_from;
@@ -71,7 +72,7 @@ struct Walk {
     } else {
       if (n - held_from >= 32) hold(p, lane);
       length = __shfl_sync(0xffffffffu, held, n - held_from);
-      subs = p.H_k * p.blocks;
+      subs = p.H_k * p.block_groups;
     }
     tiles = tiles_of(length);
   }
@@ -111,21 +112,22 @@ __device__ __forceinline__ void arrive_copied(uint64_t* bar) {
   asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 
-// The rows of a unit.
+// The rows of a unit, for the worker of its group's block `side` (none behind the last block).
 struct Unit {
-  int tok0, head0, r0, rows;
-  __device__ __forceinline__ Unit(const AttentionParams& p, const Walk& w) {
+  int tok0, head0, r0, rows, index;
+  __device__ __forceinline__ Unit(const AttentionParams& p, const Walk& w, int side) {
     const bool own = w.n < p.N;
-    const int blocks = own ? p.blocks : p.prefix_blocks, head = w.sub / blocks;
+    const int groups = own ? p.block_groups : p.prefix_blocks, head = w.sub / groups, block = (w.sub - head * groups) * p.blocks_aside + side;
     head0 = head * p.group;
-    r0 = (w.sub - head * blocks) * kRows;
+    r0 = block * kRows;
     tok0 = own ? w.n * p.tokens : 0;
     rows = min(kRows, (own ? p.tokens : p.N * p.tokens) * p.group - r0);
+    index = own ? (w.n * p.H_k + head) * p.blocks + block : p.N * p.H_k * p.blocks + head;
   }
 };
 
 // The copying warp.
-__device__ __forceinline__ void copy_tiles(const AttentionParams& p, uint8_t* smem, Bars& bar, Walk walk, int count, uint64_t limit) {
+__device__ __forceinline__ void copy_tiles(const AttentionParams& p, uint8_t* smem, Bars& bar, Walk walk, int count, int side, uint64_t limit) {
   const int lane = threadIdx.x & 31, boxes = kTile / p.box_rows;
   const auto page_of = [&](const Walk& w) -> int64_t {  // of the lane's box: -2 behind the length, -1 outside the cache
     const int key = w.t * kTile + lane * p.box_rows;
@@ -160,13 +162,13 @@ __device__ __forceinline__ void copy_tiles(const AttentionParams& p, uint8_t* sm
     }
     __syncwarp();
     if (page >= 0 && !held) {
-      const int row = (walk.t * kTile + lane * p.box_rows) % p.page_size, head = walk.sub / (walk.n < p.N ? p.blocks : p.prefix_blocks);
+      const int row = (walk.t * kTile + lane * p.box_rows) % p.page_size, head = walk.sub / (walk.n < p.N ? p.block_groups : p.prefix_blocks);
       uint8_t* at = tile + lane * p.box_rows * 256;
       tma_load_5d(at, &p.tm_k, full, 0, row, 0, head, (int)page);
       tma_load_5d(at + kKeysBytes, &p.tm_v, full, 0, row, 0, head, (int)page);
     }
     if (k == 0 || walk.t == 0) {  // the queries: half a warp a row
-      const Unit u(p, walk);
+      const Unit u(p, walk, side);
       const uint32_t to = smem_u32(smem + kStages * kTileBytes + stage * kQueryBytes);
       const int chunk = lane & 15;
 #pragma unroll
@@ -230,7 +232,7 @@ struct Count {
 };
 // The cost of everything that workers of the own pages walk, the prefix of few rows behind the sequences.
 __device__ __forceinline__ uint32_t whole_cost(const AttentionParams& p, const Count& counted) {
-  return counted.all.cost * p.H_k * p.blocks + (p.prefix ? cost_of(p.prefix) * p.H_k * p.prefix_blocks : 0);
+  return counted.all.cost * p.H_k * p.block_groups + (p.prefix ? cost_of(p.prefix) * p.H_k * p.prefix_blocks : 0);
 }
 
 // Of the cost's point `at` in a sequence whose units begin at `from`, each of `tiles` tiles, after `index` tiles.
@@ -239,12 +241,14 @@ __device__ __forceinline__ Place place_in(uint32_t n, uint32_t at, uint32_t tile
   return {n, sub, t, index + sub * tiles + t};
 }
 
-// A worker for units of up to 8 kEights rows: `tid` below kThreads, the tiles counted by just these threads, ring and barriers of its own (initialised here), its number and how many share the tiles.  `id`
-// and the one behind it: barriers of its own.
+// A worker for units of up to 8 kEights rows: `tid` below kThreads, the tiles counted by just these threads, ring and barriers of its own
+// (initialised here), its number (blocks_aside in a row have the same share), how many shares there are.  `id` and the one behind
+// it: barriers of its own.
 template <bool F16, int kEights>
-__device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* smem, int tid, const Count& counted, int worker, int workers, int id) {
+__device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* smem, int tid, const Count& counted, int worker, int share_count, int id) {
   Bars& bar = *reinterpret_cast<Bars*>(smem + kStages * (kTileBytes + kQueryBytes));
-  const int lane = tid & 31, warp = tid >> 5, subs = p.H_k * p.blocks;
+  const int lane = tid & 31, warp = tid >> 5, subs = p.H_k * p.block_groups;
+  const int share = worker / p.blocks_aside, side = worker - share * p.blocks_aside;
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&bar.full[i], 33);     // the copying warp's lanes, and one of them for the tensor copies
@@ -254,11 +258,11 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
   }
   // The share's two ends are looked up by the threads that counted the sequences where they lie.  (An end of everything lies nowhere: all
   // tiles are before it.)
-  const Shares shares(whole_cost(p, counted), workers);
+  const Shares shares(whole_cost(p, counted), share_count);
   const uint32_t prefix_tiles = tiles_of(p.prefix), own_cost = counted.all.cost * subs, own_tiles = counted.all.tiles * subs;
 #pragma unroll
   for (int end = 0; end < 2; ++end) {
-    const uint32_t at = shares.from(worker + end);
+    const uint32_t at = shares.from(share + end);
     if (tid < 32 * kWarps && counted.before.cost * subs <= at && at < (counted.before.cost + counted.mine.cost) * subs) {
       uint32_t cost = counted.before.cost * subs, tiles_before = counted.before.tiles * subs;
       for (int n = tid * counted.each;; ++n) {
@@ -288,7 +292,7 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
   take.enter(p, lane);
   const uint64_t limit = p.wait_ns ? p.wait_ns : kWaitNs;
   if (warp == kWarps) {
-    copy_tiles(p, smem, bar, take, count, limit);
+    copy_tiles(p, smem, bar, take, count, side, limit);
     return;
   }
 
@@ -363,7 +367,7 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
 #pragma unroll
           for (int e = 0; e < 4; ++e) w[g][e] = (acc[g][0][e] + acc[g][1][e]) * c;
         if (key0 + kWarpKeys > tail) {
-          const Unit u(p, take);
+          const Unit u(p, take, side);
           const int at_lane = here(lane);
 #pragma unroll
           for (int g = 0; g < kEights; ++g)
@@ -422,7 +426,7 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
           if (__any_sync(0xffffffffu, odd)) clean = some;
         }
         if (clean < kWarpKeys) {
-          const Unit u(p, take);
+          const Unit u(p, take, side);
           const int at_lane = here(lane);
 #pragma unroll 1
           for (int j = clean; j < valid; ++j) {
@@ -481,7 +485,7 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
     // the warps' parts of the piece come together, over its last tile
     const bool ends = take.t + 1 == take.tiles, whole = starts && ends;
     const int at_lane = here(lane), at_tid = here(tid);
-    const Unit u(p, take);
+    const Unit u(p, take, side);
 #pragma unroll
     for (int g = 0; g < kEights; ++g)
 #pragma unroll
@@ -500,12 +504,11 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
         for (int n = 0; n < 16; ++n)
           join[(warp * 8 * kEights + 8 * g + 2 * (at_lane & 3) + e) * kHeadDim + (n ^ (at_lane & 3)) * 8 + at_lane / 4] = o[g][n >> 1][e + 2 * (n & 1)];
     named_sync(id + 1, 32 * kWarps);
-    const int unit = take.n * subs + take.sub;
-    if (tid == 0) {
-      if (starts) p.first_worker[unit] = worker;
-      if (ends) p.last_worker[unit] = worker;
+    if (tid == 0 && u.rows > 0) {
+      if (starts) p.first_worker[u.index] = worker;
+      if (ends) p.last_worker[u.index] = worker;
     }
-    const int64_t slot = whole ? 2 * p.workers + (int64_t)unit : 2 * worker + (starts ? 1 : 0);
+    const int64_t slot = whole ? 2 * p.workers + (int64_t)u.index : 2 * worker + (starts ? 1 : 0);
     const int cg = at_tid & 15;
     float x[kEights][8], top[kEights], l[kEights];
     bool bad = false;

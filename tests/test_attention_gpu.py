@@ -38,6 +38,9 @@ SHAPES = {
     "side_by_side": dict(lengths=[140, 222], h_q=8, h_k=2, layout="side", dtype=HF),
     "two_tokens": dict(lengths=[2, 1, 0, 3, 100], tokens=2, h_q=4, h_k=2),
     "sixteen_tokens": dict(lengths=[16, 15, 40, 300], tokens=16, h_q=4, h_k=2, dtype=HF),
+    "eighty_rows": dict(lengths=[300, 17, 5, 129], tokens=16, h_q=10, h_k=2, page=24),
+    "heads_128": dict(lengths=[700, 0, 33], h_q=128, h_k=1, page=32, dtype=HF),
+    "many_rows_long": dict(lengths=[9000, 64], tokens=3, h_q=24, h_k=1, page=64),
     "many": dict(lengths=[(37 * i) % 211 for i in range(300)], h_q=4, h_k=2),
     "long": dict(lengths=[20011], h_q=8, h_k=2, page=64),
     "long_and_short": dict(lengths=[1, 12000, 3, 0, 7000, 8], h_q=8, h_k=1, page=16),
@@ -49,6 +52,7 @@ SHAPES = {
     "prefix_rows_257": dict(lengths=[(i * 29) % 90 for i in range(257)], prefix=1000, h_q=2, h_k=2, page=16),
     "prefix_rows_many": dict(lengths=[(i * 29) % 90 for i in range(100)], prefix=1511, h_q=14, h_k=2, page=64, idx=I64),
     "prefix_rows_f16": dict(lengths=[5 + i for i in range(70)], prefix=640, h_q=16, h_k=2, page=128, dtype=HF, layout="heads"),
+    "prefix_of_blocks": dict(lengths=[40, 2, 0, 300], tokens=8, h_q=16, h_k=1, prefix=100, page=8),
     "prefix_rows_short": dict(lengths=[(i * 29) % 90 for i in range(60)], prefix=3, h_q=16, h_k=2, page=8),
     "prefix_rows_tokens": dict(lengths=[(i * 31) % 140 for i in range(40)], tokens=4, prefix=257, h_q=8, h_k=1, layout="woven"),
     "prefix_long": dict(lengths=[40, 60], prefix=20007, h_q=8, h_k=2, page=64),
