@@ -121,12 +121,23 @@ GDN_DEV void tma_load_4d(void* dst, const void* tmap, uint64_t* bar, int c0, int
       "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar))
       : "memory");
 }
-// 5-D tiled load; coordinates innermost first, in elements.
-GDN_DEV void tma_load_5d(void* dst, const void* tmap, uint64_t* bar, int c0, int c1, int c2, int c3, int c4) {
+// How L2 keeps what a load brings: not for long, or as anything else.
+GDN_DEV uint64_t l2_evict_first() {
+  uint64_t x;
+  asm("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(x));
+  return x;
+}
+GDN_DEV uint64_t l2_evict_normal() {
+  uint64_t x;
+  asm("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(x));
+  return x;
+}
+// 5-D tiled load with such a policy; coordinates innermost first, in elements.
+GDN_DEV void tma_load_5d(void* dst, const void* tmap, uint64_t* bar, int c0, int c1, int c2, int c3, int c4, uint64_t policy) {
   asm volatile(
-      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
-      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7];" ::"r"(smem_u32(dst)),
-      "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar))
+      "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%2, %3, %4, %5, %6}], [%7], %8;" ::"r"(smem_u32(dst)),
+      "l"(tmap), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(c4), "r"(smem_u32(bar)), "l"(policy)
       : "memory");
 }
 // Takes over a CTA of this grid that has not been launched yet, if there is one: 16 bytes of response
