@@ -24,11 +24,6 @@ namespace {
 
 constexpr int kResident = 2;  // workers of the own pages on an SM
 
-// The join is launched without a gap: the kernel before it lets it start (go_ahead), and it waits for that one's end (grid_wait)
-// before it reads anything.
-__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void go_ahead() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 // Where the swizzled tiles have to be; there is no room to spare for it.
 __device__ __forceinline__ bool misplaced(const AttentionParams& p, const uint8_t* smem) {
   if (!(smem_u32(smem) & 1023)) return false;
@@ -40,6 +35,7 @@ __device__ __forceinline__ bool misplaced(const AttentionParams& p, const uint8_
 template <bool F16, int kEights>
 __global__ void __launch_bounds__(own::kThreads, kResident) gdn_attention_kernel(const __grid_constant__ AttentionParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
+  grid_wait();
   if (misplaced(p, smem)) return;
   go_ahead();
   if (threadIdx.x == 0 && p.pages > 0) {
@@ -67,6 +63,7 @@ __device__ __forceinline__ int sms_for_own(uint32_t own_cost, int aside, uint32_
 template <bool F16, int kEights>
 __global__ void __launch_bounds__(prefix::kThreads, 1) gdn_attention_both_kernel(const __grid_constant__ AttentionParams p) {
   extern __shared__ __align__(1024) uint8_t smem[];
+  grid_wait();
   if (misplaced(p, smem)) return;
   go_ahead();
   if (threadIdx.x == 0 && p.pages > 0) {
@@ -109,12 +106,12 @@ __global__ void __launch_bounds__(kJoinThreads<kPer>) gdn_attention_join_kernel(
   const uint32_t unit = id / p.block_rows, row = id - unit * p.block_rows, n = unit / subs, sub = unit - n * subs, hk = sub / p.blocks;
   const int r = (sub - hk * p.blocks) * own::kRows + row;
   const bool some = n < (uint32_t)p.N && r < p.tokens * p.group;
-  const int length = some ? length_of(p, n) : -1;
   // the row of the prefix, and its unit of the prefix kernel's or of the walk's
   const uint32_t pr = n * p.tokens * p.group + r;
   const bool many = p.prefix_units > 0;
   const uint32_t prefix_unit = many ? hk * p.prefix_units + pr / kPrefixRows : p.N * subs + hk * p.prefix_blocks + pr / own::kRows;
   grid_wait();
+  const int length = some ? length_of(p, n) : -1;
   if (length < 0) return;
   // the sequence's own parts: of worker `first` and those behind it, or one of a whole unit; then the prefix'
   int first = 0, own = 0, prefix_first = 0, shared = 0;
@@ -210,22 +207,6 @@ __global__ void __launch_bounds__(kJoinThreads<kPer>) gdn_attention_join_kernel(
 constexpr int kBothBytes = std::max(2 * own::kPlace, prefix::kBytes);
 static_assert(kBothBytes <= 227 * 1024 && kResident * (own::kBytes + 1024) <= 228 * 1024, "what an SM has");
 
-// A kernel that may start before the one in front of it has ended (it waits for it itself).
-template <typename Kernel>
-cudaError_t launch_behind(Kernel kernel, int64_t grid, int threads, int smem, bool behind, const AttentionParams& p, cudaStream_t stream) {
-  cudaLaunchConfig_t c = {};
-  c.gridDim = dim3((unsigned)grid);
-  c.blockDim = dim3(threads);
-  c.dynamicSmemBytes = smem;
-  c.stream = stream;
-  cudaLaunchAttribute a;
-  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  a.val.programmaticStreamSerializationAllowed = 1;
-  c.attrs = &a;
-  c.numAttrs = behind ? 1 : 0;
-  return cudaLaunchKernelEx(&c, kernel, p);
-}
-
 template <bool F16, int kEights>
 cudaError_t launch(const AttentionParams& p, cudaStream_t stream) {
   static thread_local int generation = -1, device = -1;  // the attribute is one of a device
@@ -243,8 +224,8 @@ cudaError_t launch(const AttentionParams& p, cudaStream_t stream) {
   const int64_t most = ((int64_t)p.max_pages * p.page_size + kOwnKeys - 1) / kOwnKeys * own_units +
                        ((int64_t)p.prefix + kOwnKeys - 1) / kOwnKeys * p.H_k * p.prefix_blocks;
   const bool many = p.prefix_units > 0;
-  if (many) e = launch_behind(gdn_attention_both_kernel<F16, kEights>, p.prefix_workers, prefix::kThreads, kBothBytes, false, p, stream);
-  else if (most) e = launch_behind(gdn_attention_kernel<F16, kEights>, std::min<int64_t>(p.workers, most), own::kThreads, own::kBytes, false, p, stream);
+  if (many) e = launch_behind(gdn_attention_both_kernel<F16, kEights>, p.prefix_workers, prefix::kThreads, kBothBytes, stream, p);
+  else if (most) e = launch_behind(gdn_attention_kernel<F16, kEights>, std::min<int64_t>(p.workers, most), own::kThreads, own::kBytes, stream, p);
   if (e != cudaSuccess) return e;
   // Warps a row by the parts that a row has about, as long as the rows' CTAs find a place all at once (three of eight warps or one of 32
   // an SM); after that rows keep the SMs busy with a warp each.
@@ -252,10 +233,9 @@ cudaError_t launch(const AttentionParams& p, cudaStream_t stream) {
   int64_t parts = 1 + p.workers / (own_units + p.H_k * p.prefix_blocks);
   if (many) parts += 1 + std::min<int64_t>(prefix_tiles - 1, p.prefix_workers / ((int64_t)p.H_k * p.prefix_units));
   const int64_t rows = own_units * p.block_rows;
-  const bool behind = many || most;   // a kernel of this call: what went before that has ended
-  if (parts > 64 && rows <= sms) return launch_behind(gdn_attention_join_kernel<F16, 32, 5>, rows, kJoinThreads<32>, 0, behind, p, stream);
-  if (parts > 8 && rows <= 3 * sms) return launch_behind(gdn_attention_join_kernel<F16, 8, 8>, rows, kJoinThreads<8>, 0, behind, p, stream);
-  return launch_behind(gdn_attention_join_kernel<F16, 1, 8>, (rows + 3) / 4, kJoinThreads<1>, 0, behind, p, stream);
+  if (parts > 64 && rows <= sms) return launch_behind(gdn_attention_join_kernel<F16, 32, 5>, rows, kJoinThreads<32>, 0, stream, p);
+  if (parts > 8 && rows <= 3 * sms) return launch_behind(gdn_attention_join_kernel<F16, 8, 8>, rows, kJoinThreads<8>, 0, stream, p);
+  return launch_behind(gdn_attention_join_kernel<F16, 1, 8>, (rows + 3) / 4, kJoinThreads<1>, 0, stream, p);
 }
 
 }  // namespace

@@ -3,6 +3,7 @@
 #pragma once
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
+#include <cuda_runtime.h>
 #include <float.h>
 #include <stdint.h>
 
@@ -99,5 +100,22 @@ struct StateType {
       return pack16x8<SDT == 2>(x);
   }
 };
+
+// Launches a kernel that waits by itself (grid_wait) for the one in front of it on the stream: its set-up is out of the way when that
+// one ends, which saves some 2 us of a call among others.
+template <typename... Params, typename... Args>
+cudaError_t launch_behind(void (*kernel)(Params...), int64_t grid, int threads, int smem, cudaStream_t stream, const Args&... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = dim3((unsigned)grid);
+  c.blockDim = dim3((unsigned)threads);
+  c.dynamicSmemBytes = (size_t)smem;
+  c.stream = stream;
+  cudaLaunchAttribute a;
+  a.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  a.val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = &a;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, args...);
+}
 
 }  // namespace gdn

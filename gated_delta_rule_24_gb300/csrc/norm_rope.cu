@@ -21,6 +21,7 @@
 #include <cuda_runtime.h>
 
 #include "decay.cuh"
+#include "ptx.cuh"
 
 namespace gdn {
 namespace {
@@ -73,6 +74,7 @@ __device__ __forceinline__ void load_axes8(const RopeParams& p, const int64_t (&
 template <bool F16, bool kInterleaved, int kAhead, bool kGeneral>
 __global__ void __launch_bounds__(kRopeThreads) gdn_norm_rope_kernel(const __grid_constant__ RopeParams p, unsigned q_ctas,
                                                                      unsigned qk_ctas, int per) {
+  grid_wait();
   const int l = threadIdx.x % kRopeLanes;
   const bool is_k = blockIdx.x >= q_ctas, is_v = kGeneral && blockIdx.x >= qk_ctas;
   const RopeTensor& t = p.t[is_v ? 2 : is_k ? 1 : 0];
@@ -206,10 +208,8 @@ template <bool F16, int kAhead, bool kGeneral>
 cudaError_t launch(const RopeParams& p, int per, cudaStream_t stream) {
   auto ctas = [&](int heads) { return (p.T * ((heads + per - 1) / per) + kRopeGroups - 1) / kRopeGroups; };
   const int64_t q = ctas(p.t[0].heads), qk = q + ctas(p.t[1].heads);
-  const unsigned grid = (unsigned)(qk + ctas(p.t[2].heads));
-  if (p.interleaved) gdn_norm_rope_kernel<F16, true, kAhead, kGeneral><<<grid, kRopeThreads, 0, stream>>>(p, (unsigned)q, (unsigned)qk, per);
-  else gdn_norm_rope_kernel<F16, false, kAhead, kGeneral><<<grid, kRopeThreads, 0, stream>>>(p, (unsigned)q, (unsigned)qk, per);
-  return cudaGetLastError();
+  return launch_behind(p.interleaved ? gdn_norm_rope_kernel<F16, true, kAhead, kGeneral> : gdn_norm_rope_kernel<F16, false, kAhead, kGeneral>,
+                       qk + ctas(p.t[2].heads), kRopeThreads, 0, stream, p, (unsigned)q, (unsigned)qk, per);
 }
 template <int kAhead>
 cudaError_t launch(const RopeParams& p, int per, cudaStream_t stream) {

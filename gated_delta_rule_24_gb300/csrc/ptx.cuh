@@ -173,6 +173,12 @@ GDN_DEV void bulk_wait_read_all() { asm volatile("cp.async.bulk.wait_group.read 
 // Wait until every committed bulk store but the newest group has read its source.
 GDN_DEV void bulk_wait_read_but_newest() { asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory"); }
 
+// ---------------------------------------------------------------- kernels one behind the other
+// A kernel launched with launch_behind may be set up while the one in front of it still runs: grid_wait waits for that one's end
+// (and for what it has written) and comes before anything is read or written.  go_ahead lets the next one be set up early.
+GDN_DEV void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+GDN_DEV void go_ahead() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // ---------------------------------------------------------------- fences
 GDN_DEV void fence_proxy_async_smem() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 GDN_DEV void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
