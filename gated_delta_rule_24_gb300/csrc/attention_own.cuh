@@ -121,7 +121,7 @@ struct Unit {
     head0 = head * p.group;
     r0 = block * kRows;
     tok0 = own ? w.n * p.tokens : 0;
-    rows = min(kRows, (own ? p.tokens : p.N * p.tokens) * p.group - r0);
+    rows = w.length > 0 ? min(kRows, (own ? p.tokens : p.N * p.tokens) * p.group - r0) : 0;
     index = own ? (w.n * p.H_k + head) * p.blocks + block : p.N * p.H_k * p.blocks + head;
   }
 };
@@ -267,17 +267,19 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
   for (int end = 0; end < 2; ++end) {
     const uint32_t at = shares.from(share + end);
     if (tid < 32 * kWarps && counted.before.cost * subs <= at && at < (counted.before.cost + counted.mine.cost) * subs) {
-      uint32_t cost = counted.before.cost * subs, tiles_before = counted.before.tiles * subs;
-      for (int n = tid * counted.each;; ++n) {
+      uint32_t cost = counted.before.cost * subs;
+      Place place = {(uint32_t)p.N, 0, 0, counted.before.tiles * subs};
+      for (int n = tid * counted.each; n < p.N; ++n) {
         const int length = length_of(p, n);
         const uint32_t next = cost + cost_of(length) * subs;
         if (at < next) {
-          bar.found[end] = place_in(n, at - cost, tiles_of(length), tiles_before);
+          place = place_in(n, at - cost, tiles_of(length), place.index);
           break;
         }
         cost = next;
-        tiles_before += tiles_of(length) * subs;
+        place.index += tiles_of(length) * subs;
       }
+      bar.found[end] = place;
     }
     if (tid == 0 && at >= own_cost) {
       if (prefix_tiles && p.prefix_blocks && at < own_cost + (prefix_tiles + kUnitCost) * p.H_k * p.prefix_blocks) bar.found[end] = place_in(p.N, at - own_cost, prefix_tiles, own_tiles);
@@ -311,7 +313,7 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
   uint32_t phase = 0;
   while (k < count) {  // the share's piece of a unit
     const bool own = take.n < p.N, starts = take.t == 0;
-    const int tiles = min(take.tiles - take.t, count - k);
+    const int tiles = max(1, min(take.tiles - take.t, count - k));   // lengths that change meanwhile do not keep it here
     bool unit_bad = false;
     uint32_t q[kEights][8][2];
     float base[kEights][2], sum[kEights][2], o[kEights][8][4] = {};   // rows 8 g + 2 (t % 4) + {0, 1}; o: values 16 j + t / 4 (+ 8)
