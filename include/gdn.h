@@ -363,8 +363,8 @@ gdn_status_t gdn_norm_rope_append(const gdn_tensor_t* q, const gdn_tensor_t* k, 
  *     s_j = scale q . k_j,     out = sum_j exp(s_j) v_j / sum_j exp(s_j),     lse = log sum_j exp(s_j)
  *
  * over all keys j of the prefix and the first lengths[n] - tokens + i + 1 keys of the sequence's own
- * pages (the new tokens' keys are there already).  A row without any key gives zeros and an lse
- * of -infinity.
+ * pages (the new tokens' keys are there already).  A row without any key, or whose scores are all -infinity,
+ * gives zeros and an lse of -infinity.  An infinity or NaN in a key or value reaches the rows that see it, no others.
  *
  *  q              [T, H_q, 128] bf16 or f16 (stride rules of gdn_chunk_prefill's q), T = N * tokens,
  *                 tokens from 1 to 16.
