@@ -327,7 +327,7 @@ gdn_status_t gdn_qk_norm_rope_axes(const gdn_tensor_t* q, const gdn_tensor_t* k,
  *
  *  q              [T, H_q, 128], k, v [T, H_k, 128], of one dtype (rules of gdn_qk_norm_rope).
  *  norm           zero: no norm, the values are only turned (and those that do not turn are
- *                 what they were, bit for bit unless NaN); q_weight and k_weight then have to be NULL.
+ *                 what they were, bit for bit); q_weight and k_weight then have to be NULL.
  *  q_weight, k_weight, weight_offset, eps, cos_sin, interleaved
  *                 as in gdn_qk_norm_rope.
  *  positions,

@@ -162,6 +162,21 @@ def test_values_keep_their_bits():
     assert torch.equal(t.v_cache.view(torch.int16)[at], t.v.view(torch.int16))
 
 
+@pytest.mark.parametrize("rotary", [0, 16, 64, 112])
+@pytest.mark.parametrize("interleaved", [False, True])
+def test_without_norm_what_does_not_turn_keeps_its_bits(rotary, interleaved):
+    """Zeros of either sign, NaN of any kind and all else."""
+    t = Tokens(64, 2, 2, rotary=rotary, seed=32, weights=False)
+    random = torch.randint(-32768, 32768, (2, 64, 2, 128), generator=torch.Generator().manual_seed(2)).to(torch.int16)
+    random[:, ::3, :, 1::2], random[:, 1::3, :, ::2] = -32768, 0
+    for x, bits in zip((t.q, t.k), random.cuda()):
+        x[..., rotary:].view(torch.int16).copy_(bits[..., rotary:])
+    q = gdn.norm_rope_append(t.q, t.k, t.v, t.k_cache, t.v_cache, t.slots, t.cs, t.pos, norm=False, interleaved=interleaved)
+    at = t.slots.long() // t.page, t.slots.long() % t.page
+    for got, x in ((q, t.q), (t.k_cache[at], t.k)):
+        assert torch.equal(got[..., rotary:].contiguous().view(torch.int16), x[..., rotary:].contiguous().view(torch.int16))
+
+
 def test_padded_and_bad_slots():
     t = Tokens(40, 4, 2, seed=27, idx=torch.int64)
     t.slots[7], t.slots[30:] = -5, -1
