@@ -212,13 +212,19 @@ gdn_status_t check_state(const gdn_tensor_t* t, const char* name, int64_t H) {
   return GDN_OK;
 }
 
+// Whether a kernel may read the elements one by one.
+gdn_status_t check_aligned(const gdn_tensor_t* t, const char* name) {
+  if (reinterpret_cast<uintptr_t>(t->data) % elem_size(t->dtype)) return fail(GDN_ERR_INVALID_ARGUMENT, "%s must be aligned to its elements", name);
+  return GDN_OK;
+}
+
 gdn_status_t check_index_vec(const gdn_tensor_t* t, const char* name, int64_t n) {
   gdn_status_t st = check_basic(t, name, 1);
   if (st != GDN_OK) return st;
   if (t->dtype != GDN_I32 && t->dtype != GDN_I64) return fail(GDN_ERR_UNSUPPORTED, "%s must be i32 or i64", name);
   if (n >= 0 && t->shape[0] != n) return fail(GDN_ERR_INVALID_ARGUMENT, "%s must have %lld entries", name, (long long)n);
   if (t->shape[0] > 1 && t->stride[0] != 1) return fail(GDN_ERR_INVALID_ARGUMENT, "%s must be contiguous", name);
-  return GDN_OK;
+  return check_aligned(t, name);
 }
 
 // The device must be an sm_103 part with enough opt-in shared memory per block.
@@ -778,6 +784,7 @@ gdn_status_t rope_places(const gdn_tensor_t* cos_sin, const gdn_tensor_t* positi
     if (!positions) return fail(GDN_ERR_INVALID_ARGUMENT, "pair_axes without positions");
     if ((st = check_basic(positions, "positions", 2)) != GDN_OK) return st;
     if (positions->dtype != GDN_I32 && positions->dtype != GDN_I64) return fail(GDN_ERR_UNSUPPORTED, "positions must be i32 or i64");
+    if ((st = check_aligned(positions, "positions")) != GDN_OK) return st;
     const int64_t A = positions->shape[0];
     if (A < 1 || A > 4) return fail(GDN_ERR_UNSUPPORTED, "positions must have 1 to 4 axes, got %lld", (long long)A);
     if (positions->shape[1] != T) return fail(GDN_ERR_INVALID_ARGUMENT, "positions must be [axes, T=%lld]", (long long)T);
@@ -847,6 +854,20 @@ gdn_status_t norm_rope(const gdn_tensor_t* q, const gdn_tensor_t* k, const gdn_t
   return GDN_OK;
 }
 
+// Whether no two of a tensor's rows of 128 lie over each other: every stride steps over all that the smaller ones span.
+bool each_apart(const gdn_tensor_t* t) {
+  int order[3] = {0, 1, 2};
+  std::sort(order, order + t->ndim - 1, [&](int a, int b) { return t->stride[a] < t->stride[b]; });
+  int64_t extent = 128;
+  for (int i = 0; i < t->ndim - 1; ++i) {
+    const int d = order[i];
+    if (t->shape[d] <= 1) continue;
+    if (t->stride[d] < extent) return false;
+    extent += (t->shape[d] - 1) * t->stride[d];
+  }
+  return true;
+}
+
 // A paged cache [pages, page_size, heads, 128]: rows of 128 at 16-byte steps, no two in one place.
 gdn_status_t check_cache(const gdn_tensor_t* t, const char* name, int32_t dtype) {
   gdn_status_t st = check_basic(t, name, 4);
@@ -858,15 +879,9 @@ gdn_status_t check_cache(const gdn_tensor_t* t, const char* name, int32_t dtype)
     return fail(GDN_ERR_UNSUPPORTED, "%s has too many pages, places or heads", name);
   if (t->stride[3] != 1) return fail(GDN_ERR_INVALID_ARGUMENT, "%s innermost dim must be contiguous", name);
   if (reinterpret_cast<uintptr_t>(t->data) % 16) return fail(GDN_ERR_INVALID_ARGUMENT, "%s must be 16-byte aligned", name);
-  int order[3] = {0, 1, 2};
-  std::sort(order, order + 3, [&](int a, int b) { return t->stride[a] < t->stride[b]; });
-  int64_t extent = 128;
-  for (int d : order) {
-    if (t->shape[d] <= 1) continue;
-    if (t->stride[d] % 8) return fail(GDN_ERR_INVALID_ARGUMENT, "%s strides must be multiples of 8 elements", name);
-    if (t->stride[d] < extent) return fail(GDN_ERR_INVALID_ARGUMENT, "%s has two places in one", name);
-    extent += (t->shape[d] - 1) * t->stride[d];
-  }
+  for (int d = 0; d < 3; ++d)
+    if (t->shape[d] > 1 && t->stride[d] % 8) return fail(GDN_ERR_INVALID_ARGUMENT, "%s strides must be multiples of 8 elements", name);
+  if (!each_apart(t)) return fail(GDN_ERR_INVALID_ARGUMENT, "%s has two places in one", name);
   return GDN_OK;
 }
 
@@ -1127,6 +1142,7 @@ gdn_status_t gdn_paged_attention_step(const gdn_tensor_t* q, const gdn_tensor_t*
   if (T * Hq >= (int64_t(1) << 28)) return fail(GDN_ERR_UNSUPPORTED, "too many (row, head) pairs");
   if ((st = check_basic(page_table, "page_table", 2)) != GDN_OK) return st;
   if (page_table->dtype != GDN_I32 && page_table->dtype != GDN_I64) return fail(GDN_ERR_UNSUPPORTED, "page_table must be i32 or i64");
+  if ((st = check_aligned(page_table, "page_table")) != GDN_OK) return st;
   if (page_table->shape[0] != N) return fail(GDN_ERR_INVALID_ARGUMENT, "page_table must have %lld rows", (long long)N);
   if (page_table->shape[1] > 1 && page_table->stride[1] != 1) return fail(GDN_ERR_INVALID_ARGUMENT, "page_table rows must be contiguous");
   constexpr int64_t kMostKeys = (int64_t(1) << 31) - (1 << 25);  // the tiles behind a length are int32, too
@@ -1149,8 +1165,7 @@ gdn_status_t gdn_paged_attention_step(const gdn_tensor_t* q, const gdn_tensor_t*
   if (output->dtype != q->dtype) return fail(GDN_ERR_UNSUPPORTED, "output must have q's dtype");
   if (output->shape[0] != T || output->shape[1] != Hq)
     return fail(GDN_ERR_INVALID_ARGUMENT, "output must be [T=%lld, H_q=%lld, 128]", (long long)T, (long long)Hq);
-  if (Hq > 1 && output->stride[1] < 128) return fail(GDN_ERR_INVALID_ARGUMENT, "output heads overlap");
-  if (T > 1 && output->stride[0] < 128) return fail(GDN_ERR_INVALID_ARGUMENT, "output rows overlap");
+  if (!each_apart(output)) return fail(GDN_ERR_INVALID_ARGUMENT, "output has two rows in one");
   if (lse) {
     if ((st = check_basic(lse, "lse", 2)) != GDN_OK) return st;
     if (lse->dtype != GDN_F32) return fail(GDN_ERR_UNSUPPORTED, "lse must be f32, got %s", dt_name(lse->dtype));
@@ -1158,7 +1173,7 @@ gdn_status_t gdn_paged_attention_step(const gdn_tensor_t* q, const gdn_tensor_t*
       return fail(GDN_ERR_INVALID_ARGUMENT, "lse must be [T=%lld, H_q=%lld]", (long long)T, (long long)Hq);
     if ((Hq > 1 && lse->stride[1] != 1) || (T > 1 && lse->stride[0] < Hq))
       return fail(GDN_ERR_INVALID_ARGUMENT, "lse rows must be contiguous");
-    if (reinterpret_cast<uintptr_t>(lse->data) % 4) return fail(GDN_ERR_INVALID_ARGUMENT, "lse must be 4-byte aligned");
+    if ((st = check_aligned(lse, "lse")) != GDN_OK) return st;
   }
   for (const gdn_tensor_t* y : {output, lse})
     for (const gdn_tensor_t* in : {q, k_cache, v_cache, page_table, lengths, prefix_pages})

@@ -201,6 +201,8 @@ ATTEND = {
     "output_dtype": (dict(output=z(6, 4, 128, dtype=HF)), UNSUPPORTED),
     "output_heads": (dict(output=z(6, 3, 128)), INVALID),
     "output_expanded": (dict(output=z(6, 1, 128).expand(6, 4, 128)), INVALID),
+    "output_rows_over_heads": (dict(output=z(9 * 128).as_strided((6, 4, 128), (128, 128, 1))), INVALID),
+    "output_heads_over_rows": (dict(output=z(36 * 128).as_strided((6, 4, 128), (128, 3 * 128, 1))), INVALID),
     "lse_f16": (dict(lse=z(6, 4)), UNSUPPORTED),
     "lse_shape": (dict(lse=torch.zeros(4, 6)), INVALID),
     "lse_transposed": (dict(lse=torch.zeros(4, 6).t()), INVALID),
@@ -218,6 +220,24 @@ def test_attention_refuses(way, case):
         changed, want = dict(v_cache=v, output=v.view(-1)[:6 * 512].view(6, 4, 128)), ALIAS
     assert status(gdn.gdn_paged_attention_step, attend_args(), **changed) == want
     assert gdn.load_library().gdn_last_error()
+
+
+def _off(*shape, dtype=I32):
+    """Zeros that begin two bytes behind where an element may begin."""
+    n = torch.zeros(shape, dtype=dtype).numel()
+    return torch.frombuffer(bytearray(8 * n + 32), dtype=dtype, count=n, offset=2).view(shape)
+
+
+@pytest.mark.parametrize("fn,args,name,tensor", [
+    (gdn.gdn_qk_norm_rope_axes, axes_args, "positions", _off(3, 6)), (gdn.gdn_norm_rope_append, append_args, "slots", _off(6)),
+    (gdn.gdn_norm_rope_append, append_args, "positions", _off(6, dtype=torch.int64)),
+    (gdn.gdn_paged_attention_step, attend_args, "page_table", _off(3, 2)), (gdn.gdn_paged_attention_step, attend_args, "lengths", _off(3)),
+    (gdn.gdn_paged_attention_step, attend_args, "prefix_pages", _off(2)), (gdn.gdn_paged_attention_step, attend_args, "lse", _off(6, 4, dtype=torch.float32)),
+], ids=["axes_positions", "slots", "positions", "page_table", "lengths", "prefix_pages", "lse"])
+def test_elements_off_their_places_are_refused(way, fn, args, name, tensor):
+    assert tensor.data_ptr() % 4 == 2
+    assert status(fn, args(), **{name: tensor}) == INVALID
+    assert b"aligned" in gdn.load_library().gdn_last_error()
 
 
 @pytest.mark.parametrize("fn,args", [(gdn.gdn_qk_norm_rope_axes, axes_args), (gdn.gdn_norm_rope_append, append_args),
