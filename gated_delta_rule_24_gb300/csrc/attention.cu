@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kJoinThreads<kPer>) gdn_attention_join_kernel(
   __shared__ float2 s_ml[kPer];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5 & (kPer - 1);
   const uint32_t id = blockIdx.x * kRowsHere + threadIdx.x / (32 * kPer), subs = p.H_k * p.blocks;
-  const uint32_t unit = id / p.block_rows, row = id - unit * p.block_rows, n = unit / subs, sub = unit - n * subs, hk = sub / p.blocks;
+  const uint32_t unit = over(id, p.by_rows), row = id - unit * p.block_rows, n = over(unit, p.by_subs), sub = unit - n * subs, hk = over(sub, p.by_blocks);
   const int r = (sub - hk * p.blocks) * own::kRows + row;
   const bool some = n < (uint32_t)p.N && r < p.tokens * p.group;
   // the row of the prefix, and its unit of the prefix kernel's or of the walk's
@@ -199,9 +199,9 @@ __global__ void __launch_bounds__(kJoinThreads<kPer>) gdn_attention_join_kernel(
   if (bad) return;
   const float from_base = top == -INFINITY ? 0.f : top;
   const bool none = top == -INFINITY && l == 0.f;
-  const float inv = none ? 0.f : 1.f / l;
-  const int64_t token = n * (int64_t)p.tokens + r / p.group;
-  const int head = hk * p.group + r % p.group;
+  const float inv = none ? 0.f : inverse(l);
+  const int of_unit = over(r, p.by_group), head = hk * p.group + r - of_unit * p.group;
+  const int64_t token = n * (int64_t)p.tokens + of_unit;
   *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(p.out) + token * p.o_st + head * p.o_sh + 4 * lane) =
       make_uint2(pack16x2<F16>(o.x * inv, o.y * inv), pack16x2<F16>(o.z * inv, o.w * inv));
   if (p.lse && lane == 0) p.lse[token * p.lse_st + head] = none ? -INFINITY : (from_base + log2f(l)) * kLn2;
@@ -259,6 +259,13 @@ size_t plan_attention(AttentionParams* p, int sms, void* workspace) {
   p->prefix_units = many ? (int32_t)((all + kPrefixRows - 1) / kPrefixRows) : 0;
   const int64_t many_units = (int64_t)p->H_k * p->prefix_units;
   p->prefix_workers = many ? sms : 0;   // or fewer: the device shares the SMs out
+  p->by_group = divisor(p->group);
+  p->by_page = divisor(p->page_size);
+  p->by_groups = divisor(p->block_groups);
+  p->by_rows = divisor(p->block_rows);
+  p->by_blocks = divisor(p->blocks);
+  p->by_subs = divisor(p->H_k * p->blocks);
+  p->by_units = divisor(p->prefix_units);
   const int64_t units = (int64_t)p->N * p->H_k * p->blocks + (int64_t)p->H_k * p->prefix_blocks;
   const int64_t slots = (2 * (int64_t)p->workers + (p->prefix ? units : 0)) * p->block_rows;
   const int64_t many_slots = many ? (2 * (int64_t)sms + many_units) * kPrefixRows : 0;

@@ -11,6 +11,18 @@ constexpr int kOwnKeys = 64;                         // keys of a tile of attent
 constexpr int kPrefixKeys = 128, kPrefixRows = 256;  // tiles of attention_prefix.cuh
 constexpr float kAttentionBad = -1.f;                // as a part's sum: it met a bad page, or gave up
 
+// Division by a number that a whole call keeps: n / by = (n + the upper half of n mul) >> shift for n < 2^31 (Granlund and Montgomery,
+// Division by invariant integers using multiplication, 1994).
+struct Divisor {
+  uint32_t by, mul, shift;
+};
+inline Divisor divisor(uint32_t by) {
+  Divisor d = {by ? by : 1, 0, 0};
+  while ((uint64_t(1) << d.shift) < d.by) ++d.shift;
+  d.mul = (uint32_t)((((uint64_t(1) << d.shift) - d.by) << 32) / d.by + 1);
+  return d;
+}
+
 struct AttentionParams {
   CUtensorMap tm_k;  // [pages, H_k, 2 halves, page_size, 64], box (64 values, box_rows places, 2 halves, 1 head, 1 page), 128B swizzle
   CUtensorMap tm_v;
@@ -27,6 +39,7 @@ struct AttentionParams {
   int32_t* dev_err;
   int64_t pages;
   int32_t N, tokens, H_q, H_k, group, page_size, max_pages, prefix;
+  Divisor by_group, by_page;  // the two above
   int32_t box_rows;  // places of a box
   int32_t table_dtype, len_dtype, prefix_dtype;
   float scale;
@@ -35,7 +48,8 @@ struct AttentionParams {
   int32_t workers;
   int32_t blocks, block_rows;          // row blocks of a (sequence, key head) and the rows of one
   int32_t block_groups, blocks_aside;  // groups of blocks, and the blocks of one (the last group may have fewer)
-  int32_t prefix_blocks;       // row blocks of a key head for the prefix
+  Divisor by_groups, by_rows, by_blocks, by_subs;  // block_groups, block_rows, blocks, H_k * blocks
+  int32_t prefix_blocks;       // 1 where the prefix is walked like the own pages, by one block of rows a key head, else 0
   float* part_o;               // [slots][block_rows][128]
   float* part_ml;              // [slots][block_rows][2]: base, sum
   int32_t* first_worker;       // [units], then
@@ -45,6 +59,7 @@ struct AttentionParams {
   CUtensorMap tm_pk;  // [pages, page_size, H_k, 128], box (64 values, 1 head, prefix_box places, 1 page), 128B swizzle
   CUtensorMap tm_pv;
   int32_t prefix_box, prefix_units, prefix_workers;
+  Divisor by_units;  // prefix_units
   int32_t *prefix_first, *prefix_last;  // [units]
   float* prefix_o;   // [slots][16][kPrefixRows][8]: columns by eights
   float* prefix_ml;  // [slots][kPrefixRows][2]

@@ -18,6 +18,16 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return y;
 }
 
+// 1 / x for sums of weights, to an ulp or so.
+__device__ __forceinline__ float inverse(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// n / d.by for 0 <= n < 2^31, in a fifth of the time that a division takes: a unit's end with six of those is some 1500 clocks.
+__device__ __forceinline__ int over(int n, const Divisor& d) { return (int)((__umulhi((uint32_t)n, d.mul) + (uint32_t)n) >> d.shift); }
+
 // `total` tiles in equal shares, the first ones a tile larger where that does not come out even.
 struct Shares {
   uint32_t each, larger;

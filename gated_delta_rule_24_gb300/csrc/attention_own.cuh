@@ -120,7 +120,7 @@ struct Unit {
   int tok0, head0, r0, rows, index;
   __device__ __forceinline__ Unit(const AttentionParams& p, const Walk& w, int side) {
     const bool own = w.n < p.N;
-    const int groups = own ? p.block_groups : p.prefix_blocks, head = w.sub / groups, block = (w.sub - head * groups) * p.blocks_aside + side;
+    const int head = own ? over(w.sub, p.by_groups) : w.sub, block = (own ? (w.sub - head * p.block_groups) * p.blocks_aside : 0) + side;
     head0 = head * p.group;
     r0 = block * kRows;
     tok0 = own ? w.n * p.tokens : 0;
@@ -130,14 +130,15 @@ struct Unit {
 };
 
 // The copying warp.
+template <int kEights>
 __device__ __forceinline__ void copy_tiles(const AttentionParams& p, uint8_t* smem, Bars& bar, Walk walk, int count, int side, uint64_t limit) {
   const int lane = threadIdx.x & 31, boxes = kTile / p.box_rows;
-  const auto page_of = [&](const Walk& w) -> int64_t {  // of the lane's box: -2 behind the length, -1 outside the cache
-    const int key = w.t * kTile + lane * p.box_rows;
-    if (lane >= boxes || key >= w.length) return -2;
-    const int64_t page = w.n < p.N ? index_at(p.table, p.table_dtype, w.n * p.table_st + key / p.page_size)
-                                   : index_at(p.prefix_pages, p.prefix_dtype, key / p.page_size);
-    return page < 0 || page >= p.pages ? -1 : page;
+  const auto key_of = [&](const Walk& w) { return lane < boxes ? w.t * kTile + lane * p.box_rows : INT32_MAX; };  // the lane's box' first
+  const auto page_of = [&](const Walk& w) -> int64_t {  // looked at only when its turn comes: it is on its way until then
+    const int key = key_of(w);
+    if (key >= w.length) return 0;
+    const int at = over(key, p.by_page);
+    return w.n < p.N ? index_at(p.table, p.table_dtype, w.n * p.table_st + at) : index_at(p.prefix_pages, p.prefix_dtype, at);
   };
   // What one worker alone reads is not seen again, and leaves its place in L2 to a prefix that others read many times: 256 sequences behind
   // 32768 shared keys read 428 MB of HBM, 640 without (335 is the least).
@@ -147,7 +148,7 @@ __device__ __forceinline__ void copy_tiles(const AttentionParams& p, uint8_t* sm
   for (int k = 0; k < count; ++k) {
     const int stage = k % kStages;
     Walk ahead = walk;
-    int64_t page_ahead = -2;
+    int64_t page_ahead = 0;
     if (k + 1 < count) {
       ahead.next(p, lane);
       page_ahead = page_of(ahead);
@@ -157,8 +158,10 @@ __device__ __forceinline__ void copy_tiles(const AttentionParams& p, uint8_t* sm
       break;
     }
     ++issued;
-    const bool bad = __any_sync(0xffffffffu, page == -1), held = p.hold_copies && k == 0;
-    const unsigned some = __ballot_sync(0xffffffffu, page >= 0);
+    const int key = key_of(walk);
+    const bool has = key < walk.length, good = has && page >= 0 && page < p.pages, held = p.hold_copies && k == 0;
+    const bool bad = __any_sync(0xffffffffu, has && !good);
+    const unsigned some = __ballot_sync(0xffffffffu, good);
     uint8_t* tile = smem + stage * kTileBytes;
     uint64_t* full = &bar.full[stage];
     if (lane == 0) {
@@ -167,23 +170,22 @@ __device__ __forceinline__ void copy_tiles(const AttentionParams& p, uint8_t* sm
       mbar_arrive_expect_tx(full, __popc(some) * p.box_rows * 512);
     }
     __syncwarp();
-    if (page >= 0 && !held) {
-      const int row = (walk.t * kTile + lane * p.box_rows) % p.page_size, head = walk.sub / (walk.n < p.N ? p.block_groups : p.prefix_blocks);
+    if (good && !held) {
+      const int row = key - over(key, p.by_page) * p.page_size, head = walk.n < p.N ? over(walk.sub, p.by_groups) : walk.sub;
       uint8_t* at = tile + lane * p.box_rows * 256;
       tma_load_5d(at, &p.tm_k, full, 0, row, 0, head, (int)page, policy);
       tma_load_5d(at + kKeysBytes, &p.tm_v, full, 0, row, 0, head, (int)page, policy);
     }
-    if (k == 0 || walk.t == 0) {  // the queries: half a warp a row
+    if (k == 0 || walk.t == 0) {  // the queries: half a warp a row, whose place a lane of each half finds for all
       const Unit u(p, walk, side);
       const uint32_t to = smem_u32(smem + kStages * kTileBytes + stage * kQueryBytes);
-      const int chunk = lane & 15;
+      const int chunk = lane & 15, r = u.r0 + chunk, token = over(r, p.by_group);
+      const int64_t place = chunk < u.rows ? (int64_t)(u.tok0 + token) * p.q_st + (int64_t)(u.head0 + r - token * p.group) * p.q_sh : 0;
 #pragma unroll
-      for (int j = 0; j < kRows / 2; ++j) {
-        const int i = 2 * j + (lane >> 4), r = u.r0 + i;
-        const bool some_row = i < u.rows;
-        const uint16_t* from = reinterpret_cast<const uint16_t*>(p.q);
-        if (some_row) from += (int64_t)(u.tok0 + r / p.group) * p.q_st + (int64_t)(u.head0 + r % p.group) * p.q_sh + 8 * chunk;
-        copy16(to + i * 256 + ((chunk ^ (i & 7)) << 4), from, some_row);
+      for (int j = 0; j < 4 * kEights; ++j) {
+        const int i = 2 * j + (lane >> 4);
+        const uint16_t* from = reinterpret_cast<const uint16_t*>(p.q) + __shfl_sync(0xffffffffu, place, i) + 8 * chunk;
+        copy16(to + i * 256 + ((chunk ^ (i & 7)) << 4), from, i < u.rows);
       }
       arrive_copied(full);
     } else {
@@ -300,7 +302,7 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
   take.enter(p, lane);
   const uint64_t limit = p.wait_ns ? p.wait_ns : kWaitNs;
   if (warp == kWarps) {
-    copy_tiles(p, smem, bar, take, count, side, limit);
+    copy_tiles<kEights>(p, smem, bar, take, count, side, limit);
     return;
   }
 
@@ -382,7 +384,7 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int key = key0 + at_lane / 4 + 8 * (e >> 1), r = u.r0 + 8 * g + 2 * (at_lane & 3) + (e & 1);
-              const int seen = own ? take.length - p.tokens + 1 + r / p.group : take.length;
+              const int seen = own ? take.length - p.tokens + 1 + over(r, p.by_group) : take.length;
               if (key >= min(seen, take.length)) w[g][e] = -INFINITY;
             }
         }
@@ -403,6 +405,7 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
               const float keep = now == -INFINITY || now == base[g][e] ? 1.f : exp2_fast(base[g][e] - now);
               base[g][e] = now;
               sum[g][e] *= keep;
+              if (i == 0) continue;   // all zeros
 #pragma unroll
               for (int j = 0; j < 8; ++j) { o[g][j][e] *= keep; o[g][j][e + 2] *= keep; }
             }
@@ -445,7 +448,7 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
               for (int e = 0; e < 2; ++e) {
                 const float pj = __shfl_sync(0xffffffffu, j < 8 ? w[g][e] : w[g][e + 2], from);
                 const int r = u.r0 + 8 * g + 2 * (at_lane & 3) + e;
-                if (key0 + j >= take.length - p.tokens + 1 + r / p.group) continue;  // not seen
+                if (key0 + j >= take.length - p.tokens + 1 + over(r, p.by_group)) continue;  // not seen
 #pragma unroll
                 for (int n = 0; n < 16; ++n) {
                   const int value = 8 * n + at_lane / 4;
@@ -556,11 +559,11 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
       if (whole && !p.prefix) {
         if (!bad) {
           const bool none = top[g] == -INFINITY && l[g] == 0.f;
-          const float inv = none ? 0.f : 1.f / l[g];
+          const float inv = none ? 0.f : inverse(l[g]);
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[g][e] *= inv;
-          const int64_t token = u.tok0 + r / p.group;
-          const int head = u.head0 + r % p.group;
+          const int of_unit = over(r, p.by_group), head = u.head0 + r - of_unit * p.group;
+          const int64_t token = u.tok0 + of_unit;
           *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + token * p.o_st + head * p.o_sh + 8 * cg) = pack16x8<F16>(x[g]);
           if (p.lse && cg == 0)
             p.lse[token * p.lse_st + head] = none ? -INFINITY : ((top[g] == -INFINITY ? 0.f : top[g]) + log2f(l[g])) * kLn2;

@@ -126,7 +126,7 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
   const uint64_t limit = p.wait_ns ? p.wait_ns : kWaitNs;
   const int rows_all = p.N * p.tokens * p.group;
   Share share(Steps(p, workers), worker);
-  const auto turns = [&] { return rows_all - share.unit % p.prefix_units * kPrefixRows <= 128; };  // A and B take turns at the tiles
+  const auto turns = [&] { return rows_all - (share.unit - over(share.unit, p.by_units) * p.prefix_units) * kPrefixRows <= 128; };  // A and B take turns at the tiles
 
   if (group == 2) {
     if (warp == 8) {  // copies
@@ -136,11 +136,11 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
       auto page_of = [&](int t) -> int64_t {
         const int key = t * kPrefixKeys + lane * box;
         if (lane >= boxes || key >= p.prefix) return -2;
-        const int64_t page = index_at(p.prefix_pages, p.prefix_dtype, key / p.page_size);
+        const int64_t page = index_at(p.prefix_pages, p.prefix_dtype, over(key, p.by_page));
         return page < 0 || page >= p.pages ? -1 : page;
       };
       while (!dead && share.next()) {
-        const int head = share.unit / p.prefix_units;
+        const int head = over(share.unit, p.by_units);
         int64_t page = page_of(share.t0);
         for (int i = 0; i < share.n && !dead; ++i, ++step) {
           const int t = share.t0 + i, st = step % kStages;
@@ -151,7 +151,7 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
             atomicOr(&bar.bad, 1u);
           }
           const uint32_t bytes = __popc(some) * box * 256;
-          const int row = (t * kPrefixKeys + lane * box) % p.page_size;
+          const int key = t * kPrefixKeys + lane * box, row = key - over(key, p.by_page) * p.page_size;
           for (int kv = 0; kv < 2; ++kv) {
             uint64_t* full = kv ? &bar.v_full[st] : &bar.k_full[st];
             dead = dead || !__all_sync(0xffffffffu, mbar_wait(kv ? &bar.v_empty[st] : &bar.k_empty[st], (step / kStages + 1) & 1, limit));
@@ -285,14 +285,14 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
     };
     for (; share.next(); first += share.n) {
       const bool turn = turns();
-      const int unit_row = share.unit % p.prefix_units * kPrefixRows, row0 = unit_row + (turn ? 0 : 128 * x), r = row0 + i128;
+      const int unit_head = over(share.unit, p.by_units), unit_row = (share.unit - unit_head * p.prefix_units) * kPrefixRows, row0 = unit_row + (turn ? 0 : 128 * x), r = row0 + i128;
       if (!turn || x == 0) {  // the rows of Q, half a warp a row, all on their way at once
-        const int head = share.unit / p.prefix_units * p.group, chunk = lane & 15;
+        const int head = unit_head * p.group, chunk = lane & 15;
         const uint16_t* q = reinterpret_cast<const uint16_t*>(p.q) + 8 * chunk;
         const uint32_t to = smem_u32(smem + kQ + x * kTileBytes + (chunk >> 3) * kHalf);
 #pragma unroll 4
         for (int j = 0; j < 16; ++j) {
-          const int rr = (warp & 3) * 32 + 2 * j + (lane >> 4), row = row0 + rr, token = row / p.group;
+          const int rr = (warp & 3) * 32 + 2 * j + (lane >> 4), row = row0 + rr, token = over(row, p.by_group);
           const bool some = row < rows_all;
           const uint16_t* from = some ? q + (int64_t)token * p.q_st + (int64_t)(head + row - token * p.group) * p.q_sh : q;
           asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(to + sw128_chunk(rr, chunk & 7)), "l"(from), "r"(some ? 16 : 0) : "memory");
