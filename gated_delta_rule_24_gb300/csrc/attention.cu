@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(prefix::kThreads, 1) gdn_attention_both_kernel
   uint32_t* room = reinterpret_cast<uint32_t*>(smem);
   const int half = threadIdx.x / own::kThreads, tid = threadIdx.x - half * own::kThreads;
   own::Count count;
-  if (half < 2) count.make(p, room + 8 * half, tid, 1 + 2 * half, blockIdx.x == 0 && half == 0);
+  if (half < 2) count.make(p, room + 8 * half, tid, 1 + half, blockIdx.x == 0 && half == 0);
   if (threadIdx.x == 0) { room[16] = count.all.tiles; room[17] = count.all.cost; }
   __syncthreads();
   count.all = {room[16], room[17]};
@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(prefix::kThreads, 1) gdn_attention_both_kernel
   } else if (blockIdx.x >= gridDim.x - own_sms) {
     const uint32_t worker = 2 * (blockIdx.x - (gridDim.x - own_sms)) + half, shares = min(own_cost, (uint32_t)(2 * own_sms / p.blocks_aside));
     if (half < 2 && worker < shares * p.blocks_aside)
-      own::run_worker<F16, kEights>(p, smem + half * own::kPlace, tid, count, worker, shares, 1 + 2 * half);
+      own::run_worker<F16, kEights>(p, smem + half * own::kPlace, tid, count, worker, shares, 1 + half);
   }
 }
 

@@ -25,12 +25,12 @@ constexpr int kStages = 3;
 constexpr int kKeysBytes = kTile * 256;
 constexpr int kTileBytes = 2 * kKeysBytes;     // keys, then values; either box by box, a box' rows by halves of 64 values
 constexpr int kQueryBytes = kRows * 256;
-static_assert(kWarps * kRows * kHeadDim * 4 == kTileBytes, "the warps' sums lie over a tile");
+static_assert(kRows * kHeadDim * 4 == kWarpKeys * 512 && kRows * 256 == kWarpKeys * 256, "a warp's sums lie over its own keys and values");
 // Where a share begins: tile t of `sub` of sequence n, after `index` tiles in all.
 struct Place { uint32_t n, sub, t, index; };
 struct Bars {
-  float2 ml[kWarps][kRows];
-  uint64_t full[kStages], empty[kStages];
+  float2 ml[2][kWarps][kRows];                 // of one piece, and of the next
+  uint64_t full[kStages], empty[kStages], joined;
   Place found[2];                              // the share's ends
   uint32_t bad[kStages];                       // a page of the stage's tile is none
 };
@@ -250,8 +250,8 @@ __device__ __forceinline__ Place place_in(uint32_t n, uint32_t at, uint32_t tile
 }
 
 // A worker for units of up to 8 kEights rows: `tid` below kThreads, the tiles counted by just these threads, ring and barriers of its own
-// (initialised here), its number (blocks_aside in a row have the same share), how many shares there are.  `id` and the one behind
-// it: barriers of its own.
+// (initialised here), its number (blocks_aside in a row have the same share), how many shares there are.  `id`: a
+// barrier of its own.
 template <bool F16, int kEights>
 __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* smem, int tid, const Count& counted, int worker, int share_count, int id) {
   Bars& bar = *reinterpret_cast<Bars*>(smem + kStages * (kTileBytes + kQueryBytes));
@@ -262,6 +262,7 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
       mbar_init(&bar.full[i], 33);     // the copying warp's lanes, and one of them for the tensor copies
       mbar_init(&bar.empty[i], kWarps);
     }
+    mbar_init(&bar.joined, kWarps);
     fence_mbar_init();
   }
   // The share's two ends are looked up by the threads that counted the sequences where they lie.  (An end of everything lies nowhere: all
@@ -306,16 +307,19 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
     return;
   }
 
-  // All four warps walk the same units whatever happens on the way, so that they meet at the same ends.
+  // All four warps walk the same units whatever happens on the way, so that they meet at the same ends.  (Lengths that someone changes
+  // meanwhile could part them; the wait at an end has its limit, too.)
   const float c = fabsf(p.scale) * kLog2e;
   const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
   constexpr float kBias = F16 ? 6.f : 0.f;  // f16 weights are kept 2^6 above their normal range's end for longer
   const int mi = lane >> 3, mj = lane & 7;
   // the warp's 16 rows in a tile: where they begin, how far the second eight and the second half of a row are
-  const int box = p.box_rows, mine = warp * kWarpKeys / box * box * 256 + warp * kWarpKeys % box * 128, eights = box > 8 ? 1024 : 2048, halves = box * 128;
+  const int box = p.box_rows, eights = box > 8 ? 1024 : 2048, halves = box * 128;
+  const auto rows_of = [&](int w) { return (w * kWarpKeys & -box) * 256 + (w * kWarpKeys & (box - 1)) * 128; };
+  const int mine = rows_of(warp);
   bool dead = false;
   int k = 0, stage = 0;
-  uint32_t phase = 0;
+  uint32_t phase = 0, piece = 0;
   while (k < count) {  // the share's piece of a unit
     const bool own = take.n < p.N, starts = take.t == 0;
     const int tiles = max(1, min(take.tiles - take.t, count - k));   // lengths that change meanwhile do not keep it here
@@ -493,82 +497,93 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
       ++take.t;
       if (++stage == kStages) { stage = 0; phase ^= 1; }
     }
-    // the warps' parts of the piece come together, over its last tile
+    // The warps' parts of the piece come together over its last tile: a row of sums takes half of one of the eight kilobytes that the warp's
+    // keys and values were in, the columns by eights turned by the row.
     const bool ends = take.t + 1 == take.tiles, whole = starts && ends;
     const int at_lane = here(lane), at_tid = here(tid);
-    const Unit u(p, take, side);
+    float2(&ml)[kWarps][kRows] = bar.ml[piece & 1];
+    uint8_t* const tile = smem + stage * kTileBytes;
 #pragma unroll
     for (int g = 0; g < kEights; ++g)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
 #pragma unroll
         for (int d = 4; d < 32; d <<= 1) sum[g][e] += __shfl_xor_sync(0xffffffffu, sum[g][e], d);
-        if (at_lane < 4) bar.ml[warp][8 * g + 2 * at_lane + e] = make_float2(base[g][e], unit_bad ? kAttentionBad : sum[g][e]);
+        if (at_lane < 4) ml[warp][8 * g + 2 * at_lane + e] = make_float2(base[g][e], unit_bad ? kAttentionBad : sum[g][e]);
       }
-    float* join = reinterpret_cast<float*>(smem + stage * kTileBytes);   // [warp][rows][128], columns by eights turned by the row
-    named_sync(id + 1, 32 * kWarps);
+    __syncwarp();
+    float* const to = reinterpret_cast<float*>(tile + mine + (at_lane >> 1 & 1) * halves + (at_lane & 1) * eights) + at_lane / 4;
 #pragma unroll
     for (int g = 0; g < kEights; ++g)
 #pragma unroll
       for (int e = 0; e < 2; ++e)
 #pragma unroll
         for (int n = 0; n < 16; ++n)
-          join[(warp * 8 * kEights + 8 * g + 2 * (at_lane & 3) + e) * kHeadDim + (n ^ (at_lane & 3)) * 8 + at_lane / 4] = o[g][n >> 1][e + 2 * (n & 1)];
-    named_sync(id + 1, 32 * kWarps);
+          to[g * (kKeysBytes / 4) + e * kHeadDim + (n ^ (at_lane & 3)) * 8] = o[g][n >> 1][e + 2 * (n & 1)];
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bar.joined);
+    if (!dead && !__all_sync(0xffffffffu, mbar_wait(&bar.joined, piece & 1, limit))) {
+      dead = true;
+      if (lane == 0) atomicOr(p.dev_err, kDevErrTimeout);
+    }
+    ++piece;
+    const Unit u(p, take, side);
     if (tid == 0 && u.rows > 0) {
       if (starts) p.first_worker[u.index] = worker;
       if (ends) p.last_worker[u.index] = worker;
     }
     const int64_t slot = whole ? 2 * p.workers + (int64_t)u.index : 2 * worker + (starts ? 1 : 0);
-    const int cg = at_tid & 15;
+    const int cg = at_tid & 15, row0 = at_tid / 16;
+    const bool turned = cg & 4;  // these take their second four columns first, so that eight lanes meet in no bank
+    const float* const from = reinterpret_cast<const float*>(tile + (row0 >> 2 & 1) * halves + (row0 >> 1 & 1) * eights + (row0 & 1) * 512) + (cg ^ (row0 >> 1 & 3)) * 8;
     float x[kEights][8], top[kEights], l[kEights];
-    bool bad = false;
+    bool bad = dead;
 #pragma unroll
     for (int g = 0; g < kEights; ++g) {
-      const int row = at_tid / 16 + 8 * g;
-      float2 ml[kWarps];
+      const int row = row0 + 8 * g;
+      float2 of[kWarps];
       top[g] = -INFINITY;
       l[g] = 0.f;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        ml[w] = bar.ml[w][row];
-        top[g] = fmaxf(top[g], ml[w].x);
-        bad |= ml[w].y == kAttentionBad;
+        of[w] = ml[w][row];
+        top[g] = fmaxf(top[g], of[w].x);
+        bad |= of[w].y == kAttentionBad;
       }
       const float from_base = top[g] == -INFINITY ? 0.f : top[g];
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[g][e] = 0.f;
+      float4 a = make_float4(0.f, 0.f, 0.f, 0.f), b = a;
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
-        const float f = exp2_fast(ml[w].x - from_base);
-        const float4* y = reinterpret_cast<const float4*>(join + (w * 8 * kEights + row) * kHeadDim + (cg ^ (row >> 1 & 3)) * 8);
-        const float4 y0 = y[0], y1 = y[1];
-        l[g] = fmaf(f, ml[w].y, l[g]);
-        x[g][0] = fmaf(f, y0.x, x[g][0]); x[g][1] = fmaf(f, y0.y, x[g][1]); x[g][2] = fmaf(f, y0.z, x[g][2]); x[g][3] = fmaf(f, y0.w, x[g][3]);
-        x[g][4] = fmaf(f, y1.x, x[g][4]); x[g][5] = fmaf(f, y1.y, x[g][5]); x[g][6] = fmaf(f, y1.z, x[g][6]); x[g][7] = fmaf(f, y1.w, x[g][7]);
+        const float f = exp2_fast(of[w].x - from_base);
+        const float4* y = reinterpret_cast<const float4*>(from + (g * kKeysBytes + rows_of(w)) / 4);
+        const float4 y0 = y[turned], y1 = y[!turned];
+        l[g] = fmaf(f, of[w].y, l[g]);
+        a = make_float4(fmaf(f, y0.x, a.x), fmaf(f, y0.y, a.y), fmaf(f, y0.z, a.z), fmaf(f, y0.w, a.w));
+        b = make_float4(fmaf(f, y1.x, b.x), fmaf(f, y1.y, b.y), fmaf(f, y1.z, b.z), fmaf(f, y1.w, b.w));
       }
+      x[g][0] = turned ? b.x : a.x; x[g][1] = turned ? b.y : a.y; x[g][2] = turned ? b.z : a.z; x[g][3] = turned ? b.w : a.w;
+      x[g][4] = turned ? a.x : b.x; x[g][5] = turned ? a.y : b.y; x[g][6] = turned ? a.z : b.z; x[g][7] = turned ? a.w : b.w;
     }
     // the tile is given back, and the warps go on, before what they have is on its way to memory
     fence_proxy_async_smem();
-    named_sync(id + 1, 32 * kWarps);
+    __syncwarp();
     if (lane == 0) mbar_arrive(&bar.empty[stage]);
 #pragma unroll
     for (int g = 0; g < kEights; ++g) {
-      const int row = at_tid / 16 + 8 * g, r = u.r0 + row;
-      if (row >= u.rows) break;
+      const int row = row0 + 8 * g, r = u.r0 + row;
+      const bool some = row < u.rows;
       if (whole && !p.prefix) {
-        if (!bad) {
-          const bool none = top[g] == -INFINITY && l[g] == 0.f;
-          const float inv = none ? 0.f : inverse(l[g]);
+        const bool none = top[g] == -INFINITY && l[g] == 0.f;
+        const float inv = none ? 0.f : inverse(l[g]);
 #pragma unroll
-          for (int e = 0; e < 8; ++e) x[g][e] *= inv;
-          const int of_unit = over(r, p.by_group), head = u.head0 + r - of_unit * p.group;
-          const int64_t token = u.tok0 + of_unit;
-          *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + token * p.o_st + head * p.o_sh + 8 * cg) = pack16x8<F16>(x[g]);
-          if (p.lse && cg == 0)
-            p.lse[token * p.lse_st + head] = none ? -INFINITY : ((top[g] == -INFINITY ? 0.f : top[g]) + log2f(l[g])) * kLn2;
-        }
-      } else {
+        for (int e = 0; e < 8; ++e) x[g][e] *= inv;
+        const int of_unit = over(r, p.by_group), head = u.head0 + r - of_unit * p.group;
+        const int64_t token = u.tok0 + of_unit;
+        const uint4 y = pack16x8<F16>(x[g]);
+        if (some && !bad) *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(p.out) + token * p.o_st + head * p.o_sh + 8 * cg) = y;
+        if (some && !bad && p.lse && cg == 0)
+          p.lse[token * p.lse_st + head] = none ? -INFINITY : ((top[g] == -INFINITY ? 0.f : top[g]) + log2f(l[g])) * kLn2;
+      } else if (some) {
         float4* y = reinterpret_cast<float4*>(p.part_o + (slot * p.block_rows + row) * kHeadDim + 8 * cg);
         y[0] = make_float4(x[g][0], x[g][1], x[g][2], x[g][3]);
         y[1] = make_float4(x[g][4], x[g][5], x[g][6], x[g][7]);
