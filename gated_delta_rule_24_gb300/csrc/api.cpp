@@ -1206,7 +1206,7 @@ gdn_status_t gdn_paged_attention_step(const gdn_tensor_t* q, const gdn_tensor_t*
   p.N = (int32_t)N; p.tokens = (int32_t)tokens; p.H_q = (int32_t)Hq; p.H_k = (int32_t)Hk; p.page_size = (int32_t)page_size;
   p.scale = (scale == 0.0f) ? 1.0f / std::sqrt(128.0f) : scale;
   p.op_f16 = q->dtype == GDN_F16 ? 1 : 0;
-  p.wait_ns = t_wait_ns;
+  p.wait_ns = t_wait_ns ? t_wait_ns : gdn::kAttentionWaitNs;
   p.hold_copies = t_hold_local_ready;
   const int sms = gdn::device_sm_count();
   Workspace workspace;

@@ -9,6 +9,7 @@ namespace gdn {
 
 constexpr int kOwnKeys = 64;                         // keys of a tile of attention_own.cuh
 constexpr int kPrefixKeys = 128, kPrefixRows = 256;  // tiles of attention_prefix.cuh
+constexpr uint64_t kAttentionWaitNs = 200000000;      // the bound of every wait, unless a test sets another
 constexpr float kAttentionBad = -1.f;                // as a part's sum: it met a bad page, or gave up
 
 // Division by a number that a whole call keeps: n / by = (n + the upper half of n mul) >> shift for n < 2^31 (Granlund and Montgomery,
@@ -63,7 +64,7 @@ struct AttentionParams {
   int32_t *prefix_first, *prefix_last;  // [units]
   float* prefix_o;   // [slots][16][kPrefixRows][8]: columns by eights
   float* prefix_ml;  // [slots][kPrefixRows][2]
-  // Testing aids: the bound of every wait in ns (0: 0.2 s), and the first copy of every warp withheld.
+  // The bound of every wait in ns, and a testing aid: the first copy of every warp withheld.
   int32_t hold_copies;
   uint64_t wait_ns;
 };

@@ -8,7 +8,6 @@
 
 namespace gdn {
 
-constexpr uint64_t kWaitNs = 200000000ull;
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 constexpr float kRoom = 8.f;  // how far (powers of two) scores may exceed the base before it moves
 

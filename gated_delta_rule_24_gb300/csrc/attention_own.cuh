@@ -131,7 +131,7 @@ struct Unit {
 
 // The copying warp.
 template <int kEights>
-__device__ __forceinline__ void copy_tiles(const AttentionParams& p, uint8_t* smem, Bars& bar, Walk walk, int count, int side, uint64_t limit) {
+__device__ __forceinline__ void copy_tiles(const AttentionParams& p, uint8_t* smem, Bars& bar, Walk walk, int count, int side) {
   const int lane = threadIdx.x & 31, boxes = kTile / p.box_rows;
   const auto key_of = [&](const Walk& w) { return lane < boxes ? w.t * kTile + lane * p.box_rows : INT32_MAX; };  // the lane's box' first
   const auto page_of = [&](const Walk& w) -> int64_t {  // looked at only when its turn comes: it is on its way until then
@@ -153,7 +153,7 @@ __device__ __forceinline__ void copy_tiles(const AttentionParams& p, uint8_t* sm
       ahead.next(p, lane);
       page_ahead = page_of(ahead);
     }
-    if (!__all_sync(0xffffffffu, mbar_wait(&bar.empty[stage], (k / kStages + 1) & 1, limit))) {
+    if (!__all_sync(0xffffffffu, mbar_wait(&bar.empty[stage], (k / kStages + 1) & 1, p.wait_ns))) {
       if (lane == 0) atomicOr(p.dev_err, kDevErrTimeout);
       break;
     }
@@ -196,7 +196,7 @@ __device__ __forceinline__ void copy_tiles(const AttentionParams& p, uint8_t* sm
   }
   // every copy ends before the memory is another's
   for (int k = max(0, issued - kStages); k < issued; ++k)
-    if (!(p.hold_copies && k == 0)) mbar_wait(&bar.full[k % kStages], (k / kStages) & 1, kWaitNs);
+    if (!(p.hold_copies && k == 0)) mbar_wait(&bar.full[k % kStages], (k / kStages) & 1, kAttentionWaitNs);
 }
 
 // What a unit costs a worker beside its tiles (its queries, its end), in tiles: shares that count it come out even for short sequences, too.
@@ -301,22 +301,18 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
   take.t = (int)bar.found[0].t;
   take.hold(p, lane);
   take.enter(p, lane);
-  const uint64_t limit = p.wait_ns ? p.wait_ns : kWaitNs;
   if (warp == kWarps) {
-    copy_tiles<kEights>(p, smem, bar, take, count, side, limit);
+    copy_tiles<kEights>(p, smem, bar, take, count, side);
     return;
   }
 
   // All four warps walk the same units whatever happens on the way, so that they meet at the same ends.  (Lengths that someone changes
   // meanwhile could part them; the wait at an end has its limit, too.)
-  const float c = fabsf(p.scale) * kLog2e;
-  const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
   constexpr float kBias = F16 ? 6.f : 0.f;  // f16 weights are kept 2^6 above their normal range's end for longer
   const int mi = lane >> 3, mj = lane & 7;
-  // the warp's 16 rows in a tile: where they begin, how far the second eight and the second half of a row are
-  const int box = p.box_rows, eights = box > 8 ? 1024 : 2048, halves = box * 128;
-  const auto rows_of = [&](int w) { return (w * kWarpKeys & -box) * 256 + (w * kWarpKeys & (box - 1)) * 128; };
-  const int mine = rows_of(warp);
+  // a warp's 16 rows in a tile of boxes: where they begin, how far the second eight and the second half of a row are
+  const auto rows_of = [](int w, int box) { return (w * kWarpKeys & -box) * 256 + (w * kWarpKeys & (box - 1)) * 128; };
+  const auto eights_of = [](int box) { return box > 8 ? 1024 : 2048; };
   bool dead = false;
   int k = 0, stage = 0;
   uint32_t phase = 0, piece = 0;
@@ -333,11 +329,12 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
 #pragma unroll 1
     for (int i = 0;; ++i) {
       const uint32_t tile = smem_u32(smem) + stage * kTileBytes;
-      if (!dead && !__all_sync(0xffffffffu, mbar_wait(&bar.full[stage], phase, limit))) {
+      if (!dead && !__all_sync(0xffffffffu, mbar_wait(&bar.full[stage], phase, p.wait_ns))) {
         dead = true;
         if (lane == 0) atomicOr(p.dev_err, kDevErrTimeout);
       }
       if (i == 0) {
+        const uint32_t flip = p.scale < 0.f ? 0x80008000u : 0u;
 #pragma unroll
         for (int g = 0; g < kEights; ++g) {
           const uint32_t at = smem_u32(smem) + kStages * kTileBytes + stage * kQueryBytes + (8 * g + mj) * 256;
@@ -355,7 +352,8 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
       unit_bad |= dead || bar.bad[stage];
       const int key0 = take.t * kTile + warp * kWarpKeys, valid = min(kWarpKeys, take.length - key0);
       if (valid > 0 && !unit_bad) {
-        const uint32_t kb = tile + mine, vb = kb + kKeysBytes;
+        const int box = here(p.box_rows), eights = eights_of(box), halves = box * 128;
+        const uint32_t kb = tile + rows_of(warp, box), vb = kb + kKeysBytes;
         // Fragments are loaded ahead of the products that take them, the first of the values' before the weights are made.
         // (A row's chunk c of 16 bytes lies at c ^ row % 8: only these bits of an address change from step to step.)
         const uint32_t keys_at = kb + (mi & 1) * eights + mj * 128 + (((mi >> 1) ^ mj) << 4), values_at = vb + (mi >> 1) * eights + mj * 128 + (((mi & 1) ^ mj) << 4);
@@ -379,7 +377,7 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
 #pragma unroll
         for (int g = 0; g < kEights; ++g)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) w[g][e] = (acc[g][0][e] + acc[g][1][e]) * c;
+          for (int e = 0; e < 4; ++e) w[g][e] = (acc[g][0][e] + acc[g][1][e]) * (fabsf(p.scale) * kLog2e);
         if (key0 + kWarpKeys > tail) {
           const Unit u(p, take, side);
           const int at_lane = here(lane);
@@ -503,6 +501,7 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
     const int at_lane = here(lane), at_tid = here(tid);
     float2(&ml)[kWarps][kRows] = bar.ml[piece & 1];
     uint8_t* const tile = smem + stage * kTileBytes;
+    const int box = here(p.box_rows), eights = eights_of(box), halves = box * 128;
 #pragma unroll
     for (int g = 0; g < kEights; ++g)
 #pragma unroll
@@ -512,7 +511,7 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
         if (at_lane < 4) ml[warp][8 * g + 2 * at_lane + e] = make_float2(base[g][e], unit_bad ? kAttentionBad : sum[g][e]);
       }
     __syncwarp();
-    float* const to = reinterpret_cast<float*>(tile + mine + (at_lane >> 1 & 1) * halves + (at_lane & 1) * eights) + at_lane / 4;
+    float* const to = reinterpret_cast<float*>(tile + rows_of(warp, box) + (at_lane >> 1 & 1) * halves + (at_lane & 1) * eights) + at_lane / 4;
 #pragma unroll
     for (int g = 0; g < kEights; ++g)
 #pragma unroll
@@ -522,7 +521,7 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
           to[g * (kKeysBytes / 4) + e * kHeadDim + (n ^ (at_lane & 3)) * 8] = o[g][n >> 1][e + 2 * (n & 1)];
     __syncwarp();
     if (lane == 0) mbar_arrive(&bar.joined);
-    if (!dead && !__all_sync(0xffffffffu, mbar_wait(&bar.joined, piece & 1, limit))) {
+    if (!dead && !__all_sync(0xffffffffu, mbar_wait(&bar.joined, piece & 1, p.wait_ns))) {
       dead = true;
       if (lane == 0) atomicOr(p.dev_err, kDevErrTimeout);
     }
@@ -555,7 +554,7 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
 #pragma unroll
       for (int w = 0; w < kWarps; ++w) {
         const float f = exp2_fast(of[w].x - from_base);
-        const float4* y = reinterpret_cast<const float4*>(from + (g * kKeysBytes + rows_of(w)) / 4);
+        const float4* y = reinterpret_cast<const float4*>(from + (g * kKeysBytes + rows_of(w, box)) / 4);
         const float4 y0 = y[turned], y1 = y[!turned];
         l[g] = fmaf(f, of[w].y, l[g]);
         a = make_float4(fmaf(f, y0.x, a.x), fmaf(f, y0.y, a.y), fmaf(f, y0.z, a.z), fmaf(f, y0.w, a.w));

@@ -123,7 +123,7 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = bar.tmem;
-  const uint64_t limit = p.wait_ns ? p.wait_ns : kWaitNs;
+  const uint64_t limit = p.wait_ns;
   const int rows_all = p.N * p.tokens * p.group;
   Share share(Steps(p, workers), worker);
   const auto turns = [&] { return rows_all - (share.unit - over(share.unit, p.by_units) * p.prefix_units) * kPrefixRows <= 128; };  // A and B take turns at the tiles
@@ -173,7 +173,7 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
       // every copy ends before the memory is another's
       for (int kv = 0; kv < 2; ++kv)
         for (int i = max(0, issued[kv] - kStages); i < issued[kv]; ++i)
-          if (!(p.hold_copies && i == 0)) mbar_wait(kv ? &bar.v_full[i % kStages] : &bar.k_full[i % kStages], (i / kStages) & 1, kWaitNs);
+          if (!(p.hold_copies && i == 0)) mbar_wait(kv ? &bar.v_full[i % kStages] : &bar.k_full[i % kStages], (i / kStages) & 1, kAttentionWaitNs);
     } else if (warp == 9) {  // products
       bool dead = false;
       uint32_t step = 0, steps[2] = {0, 0}, pieces[2] = {0, 0};
@@ -267,7 +267,7 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
       // nothing is on its way to or from TMEM any more
       if (elect_one()) mma_commit(&bar.done);
       __syncwarp();
-      mbar_wait(&bar.done, 0, kWaitNs);
+      mbar_wait(&bar.done, 0, kAttentionWaitNs);
     }
   } else {
     const int x = group, i128 = tid & 127;  // tile A or B, the thread's row of it
