@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(own::kThreads, kResident) gdn_attention_kernel
     tma_prefetch_desc(&p.tm_v);
   }
   own::Count count;
-  count.make(p, reinterpret_cast<uint32_t*>(smem), threadIdx.x, 1, blockIdx.x == 0);
+  count.make(p, own::bars_of(smem), reinterpret_cast<uint32_t*>(smem), threadIdx.x, 1, blockIdx.x == 0);
   // no more shares than there is to share: one without anything between two parts of a unit would leave a gap
   const uint32_t shares = min(own::whole_cost(p, count), gridDim.x / p.blocks_aside);
   if (blockIdx.x >= shares * p.blocks_aside) return;
@@ -79,7 +79,7 @@ __global__ void __launch_bounds__(prefix::kThreads, 1) gdn_attention_both_kernel
   uint32_t* room = reinterpret_cast<uint32_t*>(smem);
   const int half = threadIdx.x / own::kThreads, tid = threadIdx.x - half * own::kThreads;
   own::Count count;
-  if (half < 2) count.make(p, room + 8 * half, tid, 1 + half, blockIdx.x == 0 && half == 0);
+  if (half < 2) count.make(p, own::bars_of(smem + half * own::kPlace), room + 8 * half, tid, 1 + half, blockIdx.x == 0 && half == 0);
   if (threadIdx.x == 0) { room[16] = count.all.tiles; room[17] = count.all.cost; }
   __syncthreads();
   count.all = {room[16], room[17]};
@@ -114,23 +114,24 @@ __global__ void __launch_bounds__(kJoinThreads<kPer>) gdn_attention_join_kernel(
   const bool many = p.prefix_units > 0;
   const uint32_t prefix_unit = many ? hk * p.prefix_units + pr / kPrefixRows : p.N * subs + hk * p.prefix_blocks + pr / own::kRows;
   grid_wait();
-  const int length = some ? length_of(p, n) : -1;
-  if (length < 0) return;
-  // the sequence's own parts: of worker `first` and those behind it, or one of a whole unit; then the prefix'
-  int first = 0, own = 0, prefix_first = 0, shared = 0;
-  if (p.prefix) {
-    prefix_first = (many ? p.prefix_first : p.first_worker)[prefix_unit];
-    shared = (many ? p.prefix_last : p.last_worker)[prefix_unit] - prefix_first + 1;
-  }
-  if (length > 0) {
+  // The length, and the sequence's own parts: of the workers from the first to the last (one side of the shares), or one of a whole unit;
+  // then the prefix'.  All are asked for at once, and where there are no keys an earlier call's are not looked at.
+  int length = -1, first = 0, last = 0, prefix_first = 0, prefix_last = -1;
+  if (some) {
+    length = length_of(p, n);
     first = p.first_worker[unit];
-    own = (p.last_worker[unit] - first) / p.blocks_aside + 1;   // the workers of one side of the shares
+    last = p.last_worker[unit];
+    if (p.prefix) {
+      prefix_first = (many ? p.prefix_first : p.first_worker)[prefix_unit];
+      prefix_last = (many ? p.prefix_last : p.last_worker)[prefix_unit];
+    }
   }
-  if (own == 1 && !p.prefix) return;  // it is in the output
+  if (length < 0) return;
   // parts of no worker: the kernel before this one gave up, and said so
-  bool bad = first < 0 || own < 0 || first + (own - 1) * p.blocks_aside >= p.workers || prefix_first < 0 || shared < 0 ||
-             prefix_first + shared > (many ? p.prefix_workers : p.workers);
-  if (bad) own = shared = 0;
+  bool bad = (length > 0 && (first < 0 || last < first || last >= p.workers)) ||
+             (p.prefix && (prefix_first < 0 || prefix_last < prefix_first || prefix_last >= (many ? p.prefix_workers : p.workers)));
+  int own = length > 0 && !bad ? over(last - first, p.by_aside) + 1 : 0, shared = bad ? 0 : prefix_last - prefix_first + 1;
+  if (own == 1 && !p.prefix) return;  // it is in the output
   float top = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
   for (int i0 = warp; i0 < own + shared; i0 += kBatch * kPer) {
@@ -264,6 +265,7 @@ size_t plan_attention(AttentionParams* p, int sms, void* workspace) {
   p->by_groups = divisor(p->block_groups);
   p->by_rows = divisor(p->block_rows);
   p->by_blocks = divisor(p->blocks);
+  p->by_aside = divisor(p->blocks_aside);
   p->by_subs = divisor(p->H_k * p->blocks);
   p->by_units = divisor(p->prefix_units);
   const int64_t units = (int64_t)p->N * p->H_k * p->blocks + (int64_t)p->H_k * p->prefix_blocks;

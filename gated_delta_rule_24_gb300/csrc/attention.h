@@ -49,7 +49,7 @@ struct AttentionParams {
   int32_t workers;
   int32_t blocks, block_rows;          // row blocks of a (sequence, key head) and the rows of one
   int32_t block_groups, blocks_aside;  // groups of blocks, and the blocks of one (the last group may have fewer)
-  Divisor by_groups, by_rows, by_blocks, by_subs;  // block_groups, block_rows, blocks, H_k * blocks
+  Divisor by_groups, by_aside, by_rows, by_blocks, by_subs;  // block_groups, blocks_aside, block_rows, blocks, H_k * blocks
   int32_t prefix_blocks;       // 1 where the prefix is walked like the own pages, by one block of rows a key head, else 0
   float* part_o;               // [slots][block_rows][128]
   float* part_ml;              // [slots][block_rows][2]: base, sum

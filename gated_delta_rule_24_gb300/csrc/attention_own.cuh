@@ -22,6 +22,7 @@ constexpr int kWarpKeys = 16, kTile = kWarps * kWarpKeys;
 static_assert(kTile == kOwnKeys, "boxes fit a tile");
 constexpr int kRows = 16;                      // rows of a unit
 constexpr int kStages = 3;
+constexpr int kHeld = 512;                     // so many sequences' lengths are read once, when they are counted
 constexpr int kKeysBytes = kTile * 256;
 constexpr int kTileBytes = 2 * kKeysBytes;     // keys, then values; either box by box, a box' rows by halves of 64 values
 constexpr int kQueryBytes = kRows * 256;
@@ -33,9 +34,12 @@ struct Bars {
   uint64_t full[kStages], empty[kStages], joined;
   Place found[2];                              // the share's ends
   uint32_t bad[kStages];                       // a page of the stage's tile is none
+  int lengths[kHeld];
 };
 constexpr int kBytes = kStages * (kTileBytes + kQueryBytes) + sizeof(Bars);
 constexpr int kPlace = (kBytes + 1023) / 1024 * 1024;   // of a worker beside another
+__device__ __forceinline__ Bars& bars_of(uint8_t* smem) { return *reinterpret_cast<Bars*>(smem + kStages * (kTileBytes + kQueryBytes)); }
+__device__ __forceinline__ int length_at(const AttentionParams& p, const Bars& bar, int n) { return n < kHeld ? bar.lengths[n] : length_of(p, n); }
 
 template <bool F16>
 __device__ __forceinline__ void mma16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -64,29 +68,29 @@ struct Walk {
   int n, sub, t, tiles, length, subs;
   int held, held_from;
 
-  __device__ __forceinline__ void hold(const AttentionParams& p, int lane) {
+  __device__ __forceinline__ void hold(const AttentionParams& p, const Bars& bar, int lane) {
     held_from = n;
-    held = n + lane < p.N ? length_of(p, n + lane) : 0;
+    held = n + lane < p.N ? length_at(p, bar, n + lane) : 0;
   }
-  __device__ __forceinline__ void enter(const AttentionParams& p, int lane) {  // lengths of n, which has keys
+  __device__ __forceinline__ void enter(const AttentionParams& p, const Bars& bar, int lane) {  // lengths of n, which has keys
     if (n >= p.N) {
       length = p.prefix;
       subs = p.H_k * p.prefix_blocks;
     } else {
-      if (n - held_from >= 32) hold(p, lane);
+      if (n - held_from >= 32) hold(p, bar, lane);
       length = __shfl_sync(0xffffffffu, held, n - held_from);
       subs = p.H_k * p.block_groups;
     }
     tiles = tiles_of(length);
   }
-  __device__ __forceinline__ void next(const AttentionParams& p, int lane) {
+  __device__ __forceinline__ void next(const AttentionParams& p, const Bars& bar, int lane) {
     if (++t < tiles) return;
     t = 0;
     if (++sub < subs) return;
     sub = 0;
     ++n;
     while (n < p.N) {  // to the next sequence with keys
-      if (n - held_from >= 32) hold(p, lane);
+      if (n - held_from >= 32) hold(p, bar, lane);
       const unsigned some = __ballot_sync(0xffffffffu, held > 0) >> (n - held_from);
       if (some) {
         n += __ffs(some) - 1;
@@ -95,7 +99,7 @@ struct Walk {
       n = held_from + 32;
     }
     if (n > p.N) n = p.N;
-    enter(p, lane);
+    enter(p, bar, lane);
   }
 };
 
@@ -150,7 +154,7 @@ __device__ __forceinline__ void copy_tiles(const AttentionParams& p, uint8_t* sm
     Walk ahead = walk;
     int64_t page_ahead = 0;
     if (k + 1 < count) {
-      ahead.next(p, lane);
+      ahead.next(p, bar, lane);
       page_ahead = page_of(ahead);
     }
     if (!__all_sync(0xffffffffu, mbar_wait(&bar.empty[stage], (k / kStages + 1) & 1, p.wait_ns))) {
@@ -203,19 +207,20 @@ __device__ __forceinline__ void copy_tiles(const AttentionParams& p, uint8_t* sm
 constexpr int kUnitCost = 2;
 __device__ __forceinline__ uint32_t cost_of(int length) { return length > 0 ? tiles_of(length) + kUnitCost : 0; }
 
-// Tiles and cost of all sequences, in the units of one (key head, row block), counted by the first 128 of kThreads threads that
+// Keeps the first lengths in `bar`.  Tiles and cost of all sequences, in the units of one (key head, row block), counted by the first 128 of kThreads threads that
 // meet at barrier `id`; `before`: those of the sequences in front of the thread's own, which are `each` in a row.
 struct Count {
   struct Sums { uint32_t tiles, cost; };
   Sums all = {0, 0}, before = {0, 0}, mine = {0, 0};
   int each = 0;
-  __device__ __forceinline__ void make(const AttentionParams& p, uint32_t* room, int tid, int id, bool report) {
+  __device__ __forceinline__ void make(const AttentionParams& p, Bars& bar, uint32_t* room, int tid, int id, bool report) {
     constexpr int kCounting = 32 * kWarps;
     each = (p.N + kCounting - 1) / kCounting;
     bool bad = false;
     if (tid < kCounting)
       for (int i = 0, n = tid * each; i < each && n < p.N; ++i, ++n) {
         const int length = length_of(p, n);
+        if (n < kHeld) bar.lengths[n] = length;
         bad |= length < 0;
         mine.tiles += tiles_of(length);
         mine.cost += cost_of(length);
@@ -254,7 +259,7 @@ __device__ __forceinline__ Place place_in(uint32_t n, uint32_t at, uint32_t tile
 // barrier of its own.
 template <bool F16, int kEights>
 __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* smem, int tid, const Count& counted, int worker, int share_count, int id) {
-  Bars& bar = *reinterpret_cast<Bars*>(smem + kStages * (kTileBytes + kQueryBytes));
+  Bars& bar = bars_of(smem);
   const int lane = tid & 31, warp = tid >> 5, subs = p.H_k * p.block_groups;
   const int share = worker / p.blocks_aside, side = worker - share * p.blocks_aside;
   if (tid == 0) {
@@ -276,7 +281,7 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
       uint32_t cost = counted.before.cost * subs;
       Place place = {(uint32_t)p.N, 0, 0, counted.before.tiles * subs};
       for (int n = tid * counted.each; n < p.N; ++n) {
-        const int length = length_of(p, n);
+        const int length = length_at(p, bar, n);
         const uint32_t next = cost + cost_of(length) * subs;
         if (at < next) {
           place = place_in(n, at - cost, tiles_of(length), place.index);
@@ -299,8 +304,8 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
   take.n = (int)bar.found[0].n;
   take.sub = (int)bar.found[0].sub;
   take.t = (int)bar.found[0].t;
-  take.hold(p, lane);
-  take.enter(p, lane);
+  take.hold(p, bar, lane);
+  take.enter(p, bar, lane);
   if (warp == kWarps) {
     copy_tiles<kEights>(p, smem, bar, take, count, side);
     return;
@@ -591,7 +596,7 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
     }
     k += tiles;
     if (++stage == kStages) { stage = 0; phase ^= 1; }
-    if (k < count) take.next(p, lane);
+    if (k < count) take.next(p, bar, lane);
   }
 }
 
