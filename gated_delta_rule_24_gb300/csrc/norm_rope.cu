@@ -20,6 +20,8 @@
 // 64.6 us, 6.2 TB/s; one token 2.7 us, a kernel's start.
 #include <cuda_runtime.h>
 
+#include <algorithm>
+
 #include "decay.cuh"
 #include "ptx.cuh"
 
@@ -232,8 +234,20 @@ cudaError_t launch_norm_rope(const RopeParams& p, cudaStream_t stream) {
   const int64_t places = (int64_t)sms * kResident;
   int per = 1;
   while (per < 16 && per * places < rows) per *= 2;
-  if (per < 2) return launch<1>(p, per, stream);
-  if (per < 16) return launch<2>(p, per, stream);
+  int ahead = per < 2 ? 1 : per < 16 ? 2 : 4;
+  // The general kernel has few registers left beside four heads, and more groups on an SM are worth more than heads under way where a
+  // group has less than that, in the mean: 178283 tokens x 4 + 1 heads 111 us with one, 118 with two, 141 with four; 100000 x 8 + 2 106, 100
+  // and 107; 60000 x 12 + 4 94, 87 and 83.
+  if (p.general) {
+    int heads = 0, tensors = 0;
+    for (const RopeTensor& t : p.t) {
+      heads += t.heads < per ? t.heads : per;
+      tensors += t.heads > 0;
+    }
+    ahead = std::min(ahead, heads < 4 * tensors ? 1 : heads < 8 * tensors ? 2 : 4);
+  }
+  if (ahead == 1) return launch<1>(p, per, stream);
+  if (ahead == 2) return launch<2>(p, per, stream);
   return launch<4>(p, per, stream);
 }
 
