@@ -8,8 +8,9 @@
 // products with eight rows, or two times eight, as the narrow side, so that few rows take few products and registers; weights
 // are passed on in registers.  The warps meet at the end of a unit only, over the memory of its last tile.
 //
-// Measured: 256 sequences of up to 8192 keys, 4.3 GB of pages in 640 us, 6.7 TB/s and as much as a copy; one sequence of
-// 131072 keys, where no worker has more than some twenty tiles and the start and the join count, 28.5 us.
+// Measured: 256 sequences of up to 8192 keys, 4.3 GB of pages in 634 us, 6.8 TB/s and as much as a copy; one sequence of
+// 131072 keys, where no worker has more than some twenty tiles and the start and the join count, 27.6 us.
+// A unit of 16 rows and one tile takes a worker 4.2 us, of 8 rows 3.0: four warps at a third of their issue slots, two workers an SM.
 #pragma once
 #include "attention_common.cuh"
 

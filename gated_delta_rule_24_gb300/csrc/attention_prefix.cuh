@@ -24,9 +24,9 @@
 // Units are (key head, 256 rows), a unit's tiles of 128 keys come one behind the other, and all units'
 // tiles are cut into equal shares for the SMs; the parts are joined by attention.cu's second kernel.
 //
-// Measured: 128 keys of 256 rows take an SM 2930 to 3150 clocks (1.55 us) of the 2048 that the products alone need; what is left is
-// the way from a product over TMEM, exponentials and TMEM to the next.  256 sequences of 8 rows over 32768 shared keys on 4 key heads,
-// each with some own pages: 138 us in all.
+// Measured: 128 keys of 256 rows take an SM 2930 to 3150 clocks (1.55 us) of the 2048 that the products alone need: the scores' ones get both
+// operands from shared memory and keep it busy, and the weights' threads wait for them half of the time.  256 sequences of 8 rows over 32768 shared keys on 4 key heads,
+// each with some own pages: 133 us in all.
 #pragma once
 #include "attention_common.cuh"
 
