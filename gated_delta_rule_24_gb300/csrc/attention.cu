@@ -53,14 +53,14 @@ __global__ void __launch_bounds__(own::kThreads, kResident) gdn_attention_kernel
   own::run_worker<F16, kEights>(p, smem, threadIdx.x, count, blockIdx.x, shares, 1);
 }
 
-// SMs out of `sms` for the own pages beside a prefix of many rows, by what the two take an SM: 0.38 us for a tile's cost of 16 rows (two
-// workers side by side), 0.32 of 8, 1.55 us for 128 keys of 256 rows.  (256 sequences of 8 rows and 512 keys behind 32768: 135 us with 0.32,
-// 137 with 0.38, 142 with 0.26; 64 of 16 rows and 1500 keys behind 30000: 154 with 0.38, 160 with 0.34, 163 with 0.43.)  A prefix of up to 128 rows is held by HBM, too, and loses little by an SM
+// SMs out of `sms` for the own pages beside a prefix of many rows, by what the two take an SM: 0.34 us for a tile's cost of 16 rows (two
+// workers side by side), 0.32 of 8, 1.4 us for 128 keys of 256 rows.  (256 sequences of 8 rows and 512 keys behind 32768: 125 us, 128 to
+// 129 with 0.35 to 0.37, 136 with 0.29; 64 of 16 rows and 1500 keys behind 30000: 153 us, 157 to 162 with 0.38 to 0.41, 160 with 0.31.)  A prefix of up to 128 rows is held by HBM, too, and loses little by an SM
 // less, while the own pages get on more slowly beside it.
 template <int kEights>
 __device__ __forceinline__ int sms_for_own(uint32_t own_cost, int aside, uint32_t prefix_cost, bool few_rows, int sms) {
   if (own_cost == 0) return 0;
-  const float own = (few_rows ? 1.f : kEights == 1 ? 0.32f : 0.38f) * own_cost * aside, prefix = 1.55f * prefix_cost;
+  const float own = (few_rows ? 0.9f : kEights == 1 ? 0.32f : 0.34f) * own_cost * aside, prefix = 1.4f * prefix_cost;
   return max((aside + 1) / 2, min((int)(sms * (own / (own + prefix)) + 0.5f), sms - 1));
 }
 

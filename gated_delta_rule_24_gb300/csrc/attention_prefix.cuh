@@ -24,10 +24,12 @@
 // Units are (key head, 256 rows), a unit's tiles of 128 keys come one behind the other, and all units'
 // tiles are cut into equal shares for the SMs; the parts are joined by attention.cu's second kernel.
 //
-// Measured: 128 keys of 256 rows take an SM 2930 to 3150 clocks (1.55 us) of the 2048 that the products alone need: the scores' ones get both
-// operands from shared memory and keep it busy, and the weights' threads wait for them half of the time.  256 sequences of 8 rows over 32768 shared keys on 4 key heads,
-// each with some own pages: 133 us in all.
+// Measured: 128 keys of 256 rows take an SM 2700 to 2870 clocks (1.4 us) of the 2048 that the products alone need: a row's weights take 1570
+// from its scores, and the products of a tile 1310 then, 1030 where nothing else uses TMEM and shared memory.  256 sequences of 8 rows over 32768 shared keys on 4 key heads,
+// each with some own pages: 125 us in all.
 #pragma once
+#include <type_traits>
+
 #include "attention_common.cuh"
 
 namespace gdn {
@@ -67,7 +69,7 @@ struct Bars {
 
 static_assert(sizeof(Bars) <= kBytes - kBars, "room for them");
 
-// A unit's tiles, and what it costs a worker beside them (rows of Q in, sums out: some 6 us against 1.55 us for a tile).
+// A unit's tiles, and what it costs a worker beside them (rows of Q in, sums out: some 6 us against 1.4 us for a tile).
 constexpr uint32_t kUnitCost = 4;
 struct Steps {
   uint32_t tiles, cost;   // of a unit
@@ -174,100 +176,109 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
       for (int kv = 0; kv < 2; ++kv)
         for (int i = max(0, issued[kv] - kStages); i < issued[kv]; ++i)
           if (!(p.hold_copies && i == 0)) mbar_wait(kv ? &bar.v_full[i % kStages] : &bar.k_full[i % kStages], (i / kStages) & 1, kAttentionWaitNs);
-    } else if (warp == 9) {  // products
-      bool dead = false;
-      uint32_t step = 0, steps[2] = {0, 0}, pieces[2] = {0, 0};
-      const uint32_t id_s = p.scale < 0.f ? idesc_16_f32(F16, 128, 128, 0, 0, 1) : idesc_16_f32(F16, 128, 128, 0, 0, 0);
-      constexpr uint32_t id_o = idesc_16_f32(F16, 128, 128, 0, 1, 0);
-      const uint64_t d_q = sdesc_sw128(smem_u32(smem + kQ), 16, 1024), d_k = sdesc_sw128(smem_u32(smem + kK), 16, 1024),
-                     d_v = sdesc_sw128(smem_u32(smem + kV), kHalf, 1024);   // shared addresses count by 16 bytes in them
-      auto wait = [&](uint64_t* b, uint32_t parity) {
-        if (!dead && !__all_sync(0xffffffffu, mbar_wait(b, parity & 1, limit))) dead = true;
-        tc_fence_after();
-      };
-      auto commit = [&](uint64_t* b) {
-        if (!dead && elect_one()) mma_commit(b);
-        __syncwarp();
-      };
-      auto scores = [&](int x, int rows, uint32_t st) {  // S of A or B, with the rows of tile `rows`
-        const uint64_t a = d_q + rows * (kTileBytes >> 4), b = d_k + st * (kTileBytes >> 4);
-        if (!dead && elect_one()) {
+    } else if (warp == 9) {  // products, by one thread from end to end: each elects, votes and branches of a warp would cost what a product does
+      if (elect_one()) {
+        bool dead = false;
+        uint32_t step = 0, steps[2] = {0, 0}, pieces[2] = {0, 0};
+        const uint32_t id_s = idesc_16_f32(F16, 128, 128, 0, 0, p.scale < 0.f);
+        constexpr uint32_t id_o = idesc_16_f32(F16, 128, 128, 0, 1, 0);
+        const uint64_t d_q = sdesc_sw128(smem_u32(smem + kQ), 16, 1024), d_k = sdesc_sw128(smem_u32(smem + kK), 16, 1024),
+                       d_v = sdesc_sw128(smem_u32(smem + kV), kHalf, 1024);   // shared addresses count by 16 bytes in them
+        using std::integral_constant;
+        constexpr integral_constant<int, 0> kA{};
+        constexpr integral_constant<int, 1> kB{};
+        const auto wait = [&](uint64_t* b, uint32_t parity) {
+          dead = dead || !mbar_wait(b, parity & 1, limit);
+          tc_fence_after();
+        };
+        const auto commit = [&](uint64_t* b) {
+          if (!dead) mma_commit(b);
+        };
+        const auto scores = [&](auto which, auto rows, uint32_t at) {  // S of A or B, with the rows of tile `rows`, of the keys of step `at`
+          constexpr int x = decltype(which)::value, tile = decltype(rows)::value;
+          const uint64_t a = d_q + tile * (kTileBytes >> 4), b = d_k + at % kStages * (kTileBytes >> 4);
+          if (dead) return;
 #pragma unroll
           for (int kk = 0; kk < 8; ++kk) {
             const uint32_t off = ((kk >> 2) * kHalf + (kk & 3) * 32) >> 4;
             mma_ss(tmem + kS + 128 * x, a + off, b + off, id_s, kk > 0);
           }
           mma_commit(&bar.s_full[x]);
-        }
-        __syncwarp();
-      };
-      auto values = [&](int x, uint32_t at, bool more) {  // O of A or B, of the values of step `at`
-        const uint32_t st = at % kStages;
-        const uint64_t b = d_v + st * (kTileBytes >> 4);
-        for (int h = 0; h < 2; ++h) {
-          wait(&bar.p_full[x][h], steps[x]);
-          if (h == 0) wait(&bar.v_full[st], at / kStages);
-          if (!dead && elect_one()) {
+        };
+        const auto values = [&](auto which, uint32_t at, bool more) {  // O of A or B, of the values of step `at`
+          constexpr int x = decltype(which)::value;
+          const uint32_t st = at % kStages;
+          const uint64_t b = d_v + st * (kTileBytes >> 4);
 #pragma unroll
-            for (int k4 = 0; k4 < 4; ++k4) {
-              const int kk = 4 * h + k4;
-              mma_ts(tmem + kO + 128 * x, tmem + kS + 128 * x + 8 * kk, b + kk * (2048 >> 4), id_o, more || kk > 0);
+          for (int h = 0; h < 2; ++h) {
+            wait(&bar.p_full[x][h], steps[x]);
+            if (h == 0) wait(&bar.v_full[st], at / kStages);
+            if (dead) return;
+#pragma unroll
+            for (int kk = 4 * h; kk < 4 * h + 4; ++kk)
+              mma_ts(tmem + kO + 128 * x, tmem + kS + 128 * x + 8 * kk, b + kk * (2048 >> 4), id_o, kk > 0 || more);
+          }
+          ++steps[x];
+        };
+        while (!dead && share.next()) {
+          const uint32_t n = share.n;
+          if (turns()) {
+            wait(&bar.q_full[0], pieces[0]++);
+            const auto start = [&](auto which, uint32_t at) {
+              wait(&bar.k_full[at % kStages], at / kStages);
+              scores(which, kA, at);
+              commit(&bar.k_empty[at % kStages]);
+            };
+            const auto tile = [&](auto which, uint32_t i) {
+              const uint32_t at = step + i;
+              values(which, at, i > 1);
+              commit(&bar.v_empty[at % kStages]);
+              if (i + 2 < n) start(which, at + 2);
+              else commit(&bar.o_full[decltype(which)::value]);
+            };
+            start(kA, step);
+            if (n > 1) start(kB, step + 1);
+#pragma unroll 1
+            for (uint32_t i = 0; i < n && !dead; i += 2) {
+              tile(kA, i);
+              if (i + 1 < n) tile(kB, i + 1);
             }
+            step += n;
+            continue;
           }
-          __syncwarp();
-        }
-        ++steps[x];
-      };
-      while (!dead && share.next()) {
-        const uint32_t n = share.n;
-        if (turns()) {
           wait(&bar.q_full[0], pieces[0]++);
-          for (uint32_t i = 0; i < min(n, 2u); ++i) {
-            wait(&bar.k_full[(step + i) % kStages], (step + i) / kStages);
-            scores(i, 0, (step + i) % kStages);
-            commit(&bar.k_empty[(step + i) % kStages]);
-          }
-          for (uint32_t i = 0; i < n && !dead; ++i) {
-            const uint32_t x = i & 1, at = step + i, ahead = at + 2;
-            values(x, at, i > 1);
-            commit(&bar.v_empty[at % kStages]);
-            if (i + 2 < n) {
+          wait(&bar.k_full[step % kStages], step / kStages);
+          scores(kA, kA, step);
+          wait(&bar.q_full[1], pieces[1]++);
+          scores(kB, kB, step);
+          commit(&bar.k_empty[step % kStages]);
+#pragma unroll 1
+          for (uint32_t i = 0; i < n && !dead; ++i, ++step) {
+            const uint32_t ahead = step + 1;
+            const bool last = i + 1 == n;
+            values(kA, step, i > 0);
+            if (!last) {
               wait(&bar.k_full[ahead % kStages], ahead / kStages);
-              scores(x, 0, ahead % kStages);
+              scores(kA, kA, ahead);
+            } else {
+              commit(&bar.o_full[0]);
+            }
+            values(kB, step, i > 0);
+            commit(&bar.v_empty[step % kStages]);
+            if (!last) {
+              scores(kB, kB, ahead);
               commit(&bar.k_empty[ahead % kStages]);
             } else {
-              commit(&bar.o_full[x]);
-            }
-          }
-          step += n;
-          continue;
-        }
-        for (int x = 0; x < 2; ++x) {
-          wait(&bar.q_full[x], pieces[x]++);
-          if (x == 0) wait(&bar.k_full[step % kStages], step / kStages);
-          scores(x, x, step % kStages);
-        }
-        commit(&bar.k_empty[step % kStages]);
-        for (uint32_t i = 0; i < n && !dead; ++i, ++step) {
-          const uint32_t ahead = step + 1;
-          for (int x = 0; x < 2; ++x) {
-            values(x, step, i > 0);
-            if (x == 1) commit(&bar.v_empty[step % kStages]);
-            if (i + 1 < n) {
-              if (x == 0) wait(&bar.k_full[ahead % kStages], ahead / kStages);
-              scores(x, x, ahead % kStages);
-              if (x == 1) commit(&bar.k_empty[ahead % kStages]);
-            } else {
-              commit(&bar.o_full[x]);
+              commit(&bar.o_full[1]);
             }
           }
         }
+        if (dead) atomicOr(p.dev_err, kDevErrTimeout);
+        // nothing is on its way to or from TMEM any more
+        mma_commit(&bar.done);
+        mbar_wait(&bar.done, 0, kAttentionWaitNs);
       }
-      if (dead && lane == 0) atomicOr(p.dev_err, kDevErrTimeout);
-      // nothing is on its way to or from TMEM any more
-      if (elect_one()) mma_commit(&bar.done);
       __syncwarp();
-      mbar_wait(&bar.done, 0, kAttentionWaitNs);
     }
   } else {
     const int x = group, i128 = tid & 127;  // tile A or B, the thread's row of it
