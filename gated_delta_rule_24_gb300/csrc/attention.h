@@ -5,24 +5,14 @@
 #include <cuda_runtime_api.h>
 #include <stdint.h>
 
+#include "decay.h"
+
 namespace gdn {
 
 constexpr int kOwnKeys = 64;                         // keys of a tile of attention_own.cuh
 constexpr int kPrefixKeys = 128, kPrefixRows = 256;  // tiles of attention_prefix.cuh
 constexpr uint64_t kAttentionWaitNs = 200000000;      // the bound of every wait, unless a test sets another
 constexpr float kAttentionBad = -1.f;                // as a part's sum: it met a bad page, or gave up
-
-// Division by a number that a whole call keeps: n / by = (n + the upper half of n mul) >> shift for n < 2^31 (Granlund and Montgomery,
-// Division by invariant integers using multiplication, 1994).
-struct Divisor {
-  uint32_t by, mul, shift;
-};
-inline Divisor divisor(uint32_t by) {
-  Divisor d = {by ? by : 1, 0, 0};
-  while ((uint64_t(1) << d.shift) < d.by) ++d.shift;
-  d.mul = (uint32_t)((((uint64_t(1) << d.shift) - d.by) << 32) / d.by + 1);
-  return d;
-}
 
 struct AttentionParams {
   CUtensorMap tm_k;  // [pages, H_k, 2 halves, page_size, 64], box (64 values, box_rows places, 2 halves, 1 head, 1 page), 128B swizzle

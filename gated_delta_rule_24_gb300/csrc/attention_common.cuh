@@ -24,9 +24,6 @@ __device__ __forceinline__ float inverse(float x) {
   return y;
 }
 
-// n / d.by for 0 <= n < 2^31, in a fifth of the time that a division takes: a unit's end with six of those is some 1500 clocks.
-__device__ __forceinline__ int over(int n, const Divisor& d) { return (int)((__umulhi((uint32_t)n, d.mul) + (uint32_t)n) >> d.shift); }
-
 // `total` tiles in equal shares, the first ones a tile larger where that does not come out even.
 struct Shares {
   uint32_t each, larger;

@@ -8,6 +8,18 @@
 
 namespace gdn {
 
+// Division by a number that a whole call keeps: n / by = (n + the upper half of n mul) >> shift for n < 2^31 (Granlund and Montgomery,
+// Division by invariant integers using multiplication, 1994).
+struct Divisor {
+  uint32_t by, mul, shift;
+};
+inline Divisor divisor(uint32_t by) {
+  Divisor d = {by ? by : 1, 0, 0};
+  while ((uint64_t(1) << d.shift) < d.by) ++d.shift;
+  d.mul = (uint32_t)((((uint64_t(1) << d.shift) - d.by) << 32) / d.by + 1);
+  return d;
+}
+
 // One head tensor of the norm-and-rotation kernel: [T, heads, 128], strides in elements.
 struct RopeTensor {
   const void* x;
@@ -17,6 +29,7 @@ struct RopeTensor {
   int64_t y_sp;   // of a paged cache: from page to page (y_st is then from place to place in a page)
   const void* w;  // [128] or null
   int32_t heads, w_dtype;
+  Divisor by_parts;  // parts of `heads` that a group takes (launch_norm_rope)
 };
 struct RopeParams {
   RopeTensor t[3];        // q, then k (heads = 0: absent), then v of an append
