@@ -42,6 +42,8 @@ SHAPES = {
     "heads_128": dict(lengths=[700, 0, 33], h_q=128, h_k=1, page=32, dtype=HF),
     "many_rows_long": dict(lengths=[9000, 64], tokens=3, h_q=24, h_k=1, page=64),
     "many": dict(lengths=[(37 * i) % 211 for i in range(300)], h_q=4, h_k=2),
+    "hundreds": dict(lengths=[0 if 480 < i < 620 else (41 * i) % 83 for i in range(700)], h_q=3, h_k=1, page=8),
+    "hundreds_behind_a_prefix": dict(lengths=[0 if 500 < i < 520 else (41 * i) % 83 for i in range(600)], tokens=2, h_q=2, h_k=1, prefix=90, page=8),
     "long": dict(lengths=[20011], h_q=8, h_k=2, page=64),
     "long_and_short": dict(lengths=[1, 12000, 3, 0, 7000, 8], h_q=8, h_k=1, page=16),
     "prefix_1": dict(lengths=[3, 0, 20], prefix=1),
