@@ -85,6 +85,7 @@ __global__ void __launch_bounds__(prefix::kThreads, 1) gdn_attention_both_kernel
   if (threadIdx.x == 0) { room[16] = count.all.tiles; room[17] = count.all.cost; }
   __syncthreads();
   count.all = {room[16], room[17]};
+  fence_proxy_async_smem();
   __syncthreads();
   const uint32_t tiles = (p.prefix + kPrefixKeys - 1) / kPrefixKeys, steps = p.H_k * p.prefix_units * (tiles + prefix::kUnitCost);
   const uint32_t own_cost = own::whole_cost(p, count);

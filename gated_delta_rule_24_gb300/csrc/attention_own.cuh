@@ -242,6 +242,7 @@ struct Count {
       all.tiles += sums[w].tiles;
       all.cost += sums[w].cost;
     }
+    fence_proxy_async_smem();   // tensor copies come over the room, behind the next barrier
   }
 };
 // The cost of everything that workers of the own pages walk, the prefix of few rows behind the sequences.
