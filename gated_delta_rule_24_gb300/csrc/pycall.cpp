@@ -20,7 +20,7 @@ decltype(&gdn_decay_step) f_step;
 decltype(&gdn_qk_norm_rope_axes) f_axes;
 decltype(&gdn_norm_rope_append) f_append;
 decltype(&gdn_paged_attention_step) f_attend;
-PyObject* not_here;  // called with a tensor that the current GPU may not read: raises where that is an error (or None: never asked)
+PyObject* not_here;  // called with a tensor that the current GPU may not read or write: raises where that is an error (or None: never asked)
 
 constexpr int kMost = 12;
 struct Descriptors {
@@ -64,6 +64,19 @@ void describe(const at::Tensor& t, gdn_tensor_t* d) {
   d->data = t.data_ptr();
 }
 
+// Asks about a tensor, an argument or a new result, that the current GPU may not read or write.
+void ask(Descriptors& d, const at::Tensor& x) {
+  if (not_here == Py_None) return;
+  if (x.is_cuda()) {
+    if (d.device == -2) d.device = c10::cuda::current_device();
+    if (x.get_device() == d.device) return;
+  }
+  PyObject* o = THPVariable_Wrap(x);
+  PyObject* r = o ? PyObject_CallOneArg(not_here, o) : nullptr;
+  Py_XDECREF(o);
+  if (!r) throw Raised();
+  Py_DECREF(r);
+}
 // Descriptors first .. first + n - 1 of the tensors t[0 .. n - 1], none for None.
 void describe_all(Descriptors& d, PyObject* const* t, int first, int n) {
   for (int i = first; i < first + n; ++i) {
@@ -72,14 +85,7 @@ void describe_all(Descriptors& d, PyObject* const* t, int first, int n) {
     const at::Tensor& x = tensor_of(t[i - first]);
     describe(x, &d.room[i]);
     d.at[i] = &d.room[i];
-    if (not_here == Py_None) continue;
-    if (x.is_cuda()) {
-      if (d.device == -2) d.device = c10::cuda::current_device();
-      if (x.get_device() == d.device) continue;
-    }
-    PyObject* r = PyObject_CallOneArg(not_here, t[i - first]);
-    if (!r) throw Raised();
-    Py_DECREF(r);
+    ask(d, x);
   }
 }
 // A gate of one dimension is one decay for each head: the rows of q with a stride of 0.
@@ -169,9 +175,11 @@ PyObject* two(PyObject* a, PyObject* b) {
 at::Tensor like(const at::Tensor& q, bool rows = false) {  // rows: contiguous whatever the order of q in memory
   return rows ? at::empty(q.sizes(), q.options().requires_grad(false)) : at::empty_like(q, q.options().requires_grad(false));
 }
+// A result made after an argument that is allowed in pinned memory would lie in ordinary host memory.
 void describe_new(Descriptors& d, int i, const at::Tensor& t) {
   describe(t, &d.room[i]);
   d.at[i] = &d.room[i];
+  ask(d, t);
 }
 
 // A function of the module: what it throws becomes a Python exception.
