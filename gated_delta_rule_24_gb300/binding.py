@@ -16,7 +16,7 @@ from typing import Optional
 
 import torch
 
-from .build import LIB as _LIB_PATH, PYCALL as _PYCALL_PATH
+from .build import LIB as _LIB_PATH, MADE_FOR as _MADE_FOR, PYCALL as _PYCALL_PATH
 
 GDN_OK = 0
 STATUS_NAMES = {0: "GDN_OK", 1: "GDN_ERR_INVALID_ARGUMENT", 2: "GDN_ERR_UNSUPPORTED",
@@ -138,7 +138,7 @@ class _PyCall:
     functions (``decay_prefill`` and ``decay_step`` also with whether the gate may be ``[H]``, one decay for
     each head; ``pair_axes`` without its length), tensors described on the way; those called ``new_`` allocate their results.
     At the first use they are taken from the extension ``csrc/pycall.cpp``, with ``fill``, the addresses of
-    descriptors alone; where it was not built or does not load, they go by ctypes as all others do."""
+    descriptors alone; where it was not built, does not load or was made for another torch or Python, they go by ctypes as all others do."""
 
     _bound = ("qk_norm_rope", "decay_prefill", "decay_step", "qk_norm_rope_axes", "norm_rope_append", "paged_attention_step")
     _names = (*_bound, "new_qk_norm_rope", "new_norm_rope_append", "new_paged_attention_step", "fill")
@@ -151,6 +151,9 @@ class _PyCall:
             loader = importlib.machinery.ExtensionFileLoader("gdn_pycall", _PYCALL_PATH)
             module = importlib.util.module_from_spec(importlib.util.spec_from_file_location("gdn_pycall", _PYCALL_PATH, loader=loader))
             loader.exec_module(module)
+            made_for = getattr(module, "made_for", None)
+            if made_for != _MADE_FOR:
+                raise ImportError(f"{_PYCALL_PATH} was made for {made_for}, not for {_MADE_FOR}")
             module.bind(_not_here if torch.cuda.is_available() else None,
                         *(ctypes.cast(getattr(lib, "gdn_" + each), ctypes.c_void_p).value for each in self._bound))
         except (ImportError, OSError):

@@ -1,20 +1,22 @@
 """Build the sm_103a C-ABI library ``_build/libgdn_gb300.so`` in the package tree, and the
-binding's extension ``_build/gdn_pycall.so`` beside it.
+binding's extension ``_build/gdn_pycall-<torch>-<Python>.so`` beside it.
 
 Each translation unit is compiled by nvcc in parallel, then linked; a rebuild
 happens only when a source or header is newer than what is made of it.  The extension makes calls
 lighter for the host and nothing else: where it cannot be built (no headers of Python or torch), the binding does
-without.
+without.  It reads torch's objects at their places in memory, which are other ones in another torch: it is made for one torch and
+one Python, and its name and the module itself say for which.
 """
 from __future__ import annotations
 
 import concurrent.futures as cf
-import importlib.util
 import os
 import subprocess
 import sys
 import sysconfig
 import warnings
+
+import torch
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -22,12 +24,20 @@ CSRC = os.path.join(PKG, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(BUILD, "libgdn_gb300.so")
-PYCALL = os.path.join(BUILD, "gdn_pycall.so")
 PYCALL_SOURCE = os.path.join(CSRC, "pycall.cpp")
 SOURCES = ["prefill.cu", "decode.cu", "decay_prefill.cu", "decay_step.cu", "norm_rope.cu", "attention.cu", "api.cpp"]
 HEADERS = [os.path.join(CSRC, f) for f in ("prefill.h", "decode.h", "decay.h", "decay.cuh", "attention.h", "attention_common.cuh",
                                                "attention_own.cuh", "attention_prefix.cuh", "ptx.cuh")] + [os.path.join(INCLUDE, "gdn.h")]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
+
+
+def made_for() -> str:
+    """The torch and the Python that an extension made now goes with."""
+    return f"torch{torch.__version__}-{(torch.version.git_version or 'none')[:10]}-{sysconfig.get_config_var('SOABI')}"
+
+
+MADE_FOR = made_for()
+PYCALL = os.path.join(BUILD, f"gdn_pycall-{MADE_FOR}.so")
 COMMON = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 
 
@@ -45,11 +55,11 @@ def _build_pycall() -> None:
     cuda = os.environ.get("CUDA_HOME", "/usr/local/cuda")
     tmp = PYCALL + f".tmp{os.getpid()}"
     try:
-        spec = importlib.util.find_spec("torch")
-        torch = os.path.dirname(spec.origin) if spec and spec.origin else "torch"
-        r = subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
-                            "-isystem", os.path.join(torch, "include"), "-isystem", os.path.join(torch, "include", "torch", "csrc", "api", "include"),
-                            "-I", os.path.join(cuda, "include"), PYCALL_SOURCE, "-o", tmp, "-L", os.path.join(torch, "lib"),
+        folder = os.path.dirname(torch.__file__)
+        r = subprocess.run(["g++", "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden", f'-DGDN_MADE_FOR="{MADE_FOR}"',
+                            "-I", sysconfig.get_paths()["include"], "-I", INCLUDE,
+                            "-isystem", os.path.join(folder, "include"), "-isystem", os.path.join(folder, "include", "torch", "csrc", "api", "include"),
+                            "-I", os.path.join(cuda, "include"), PYCALL_SOURCE, "-o", tmp, "-L", os.path.join(folder, "lib"),
                             "-ltorch_python", "-ltorch", "-ltorch_cpu", "-lc10", "-lc10_cuda"], capture_output=True, text=True)
         failed = r.returncode and f"g++ failed on {PYCALL_SOURCE}:\n{r.stdout}\n{r.stderr}"
     except OSError as e:

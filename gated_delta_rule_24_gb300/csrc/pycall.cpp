@@ -399,5 +399,8 @@ PyModuleDef module = {PyModuleDef_HEAD_INIT, "gdn_pycall", nullptr, -1, methods,
 
 PyMODINIT_FUNC PyInit_gdn_pycall(void) {
   not_here = Py_NewRef(Py_None);
-  return PyModule_Create(&module);
+  PyObject* m = PyModule_Create(&module);
+  // the torch and the Python whose objects are read here, for the binding to compare before it makes a call
+  if (m && PyModule_AddStringConstant(m, "made_for", GDN_MADE_FOR) < 0) Py_CLEAR(m);
+  return m;
 }
