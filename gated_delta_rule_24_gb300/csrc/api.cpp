@@ -31,6 +31,8 @@ gdn_status_t fail(gdn_status_t st, const char* fmt, ...) {
   va_start(ap, fmt);
   vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap);
   va_end(ap);
+  // What CUDA refused is reported by this status.  Left in the runtime, it would be taken for an error of the caller's next launch.
+  if (st == GDN_ERR_CUDA) cudaGetLastError();
   return st;
 }
 
