@@ -46,7 +46,7 @@ __global__ void __launch_bounds__(own::kThreads, kResident) gdn_attention_kernel
     tma_prefetch_desc(&p.tm_v);
   }
   own::Count count;
-  count.make(p, own::bars_of(smem), reinterpret_cast<uint32_t*>(smem), threadIdx.x, 1, blockIdx.x == 0);
+  count.make(p, own::bars_of(smem), reinterpret_cast<uint32_t*>(smem), threadIdx.x, 1);
   // no more shares than there is to share: one without anything between two parts of a unit would leave a gap
   const uint32_t shares = min(own::whole_cost(p, count), gridDim.x / p.blocks_aside);
   if (blockIdx.x >= shares * p.blocks_aside) return;
@@ -81,7 +81,7 @@ __global__ void __launch_bounds__(prefix::kThreads, 1) gdn_attention_both_kernel
   uint32_t* room = reinterpret_cast<uint32_t*>(smem);
   const int half = threadIdx.x / own::kThreads, tid = threadIdx.x - half * own::kThreads;
   own::Count count;
-  if (half < 2) count.make(p, own::bars_of(smem + half * own::kPlace), room + 8 * half, tid, 1 + half, blockIdx.x == 0 && half == 0);
+  if (half < 2) count.make(p, own::bars_of(smem + half * own::kPlace), room + 8 * half, tid, 1 + half);
   if (threadIdx.x == 0) { room[16] = count.all.tiles; room[17] = count.all.cost; }
   __syncthreads();
   count.all = {room[16], room[17]};
@@ -129,7 +129,10 @@ __global__ void __launch_bounds__(kJoinThreads<kPer>) gdn_attention_join_kernel(
       prefix_last = (many ? p.prefix_last : p.last_worker)[prefix_unit];
     }
   }
-  if (length < 0) return;
+  if (length < 0) {  // reported here, as there may be nothing for the kernel before this one to do, and it is not launched then
+    if (some && sub == 0 && row == 0 && (threadIdx.x & (32 * kPer - 1)) == 0) atomicOr(p.dev_err, kDevErrLength);
+    return;
+  }
   // parts of no worker: the kernel before this one gave up, and said so
   bool bad = (length > 0 && (first < 0 || last < first || last >= p.workers)) ||
              (p.prefix && (prefix_first < 0 || prefix_last < prefix_first || prefix_last >= (many ? p.prefix_workers : p.workers)));

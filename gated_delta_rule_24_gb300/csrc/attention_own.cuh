@@ -214,19 +214,16 @@ struct Count {
   struct Sums { uint32_t tiles, cost; };
   Sums all = {0, 0}, before = {0, 0}, mine = {0, 0};
   int each = 0;
-  __device__ __forceinline__ void make(const AttentionParams& p, Bars& bar, uint32_t* room, int tid, int id, bool report) {
+  __device__ __forceinline__ void make(const AttentionParams& p, Bars& bar, uint32_t* room, int tid, int id) {
     constexpr int kCounting = 32 * kWarps;
     each = (p.N + kCounting - 1) / kCounting;
-    bool bad = false;
     if (tid < kCounting)
       for (int i = 0, n = tid * each; i < each && n < p.N; ++i, ++n) {
         const int length = length_of(p, n);
         if (n < kHeld) bar.lengths[n] = length;
-        bad |= length < 0;
         mine.tiles += tiles_of(length);
         mine.cost += cost_of(length);
       }
-    if (bad && report) atomicOr(p.dev_err, kDevErrLength);
     Sums upto = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
