@@ -27,10 +27,13 @@ namespace {
 
 constexpr int kResident = 2;  // workers of the own pages on an SM
 
-// Where the swizzled tiles have to be; there is no room to spare for it.
+// Whether the swizzled tiles would not be where they have to be; there is no room to spare for it.  It is so for all CTAs then: none has a
+// share, and no unit has a worker, so that the join does not take the workspace's for an earlier call's.
 __device__ __forceinline__ bool misplaced(const AttentionParams& p, const uint8_t* smem) {
   if (!(smem_u32(smem) & 1023)) return false;
   if (threadIdx.x == 0) atomicOr(p.dev_err, kDevErrTimeout);
+  const int64_t places = 2 * ((p.last_worker - p.first_worker) + (p.prefix_last - p.prefix_first));   // one array
+  for (int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x; i < places; i += (int64_t)gridDim.x * blockDim.x) p.first_worker[i] = -1;
   return true;
 }
 
