@@ -53,7 +53,7 @@ __global__ void __launch_bounds__(own::kThreads, kResident) gdn_attention_kernel
   // no more shares than there is to share: one without anything between two parts of a unit would leave a gap
   const uint32_t shares = min(own::whole_cost(p, count), gridDim.x / p.blocks_aside);
   if (blockIdx.x >= shares * p.blocks_aside) return;
-  own::run_worker<F16, kEights>(p, smem, threadIdx.x, count, blockIdx.x, shares, 1);
+  own::run_worker<F16, kEights, false>(p, smem, threadIdx.x, count, blockIdx.x, shares, 1);
 }
 
 // SMs out of `sms` for the own pages beside a prefix of many rows, by what the two take an SM: 0.34 us for a tile's cost of 16 rows (two
@@ -98,7 +98,7 @@ __global__ void __launch_bounds__(prefix::kThreads, 1) gdn_attention_both_kernel
   } else if (blockIdx.x >= gridDim.x - own_sms) {
     const uint32_t worker = 2 * (blockIdx.x - (gridDim.x - own_sms)) + half, shares = min(own_cost, (uint32_t)(2 * own_sms / p.blocks_aside));
     if (half < 2 && worker < shares * p.blocks_aside)
-      own::run_worker<F16, kEights>(p, smem + half * own::kPlace, tid, count, worker, shares, 1 + half);
+      own::run_worker<F16, kEights, true>(p, smem + half * own::kPlace, tid, count, worker, shares, 1 + half);
   }
 }
 

@@ -12,6 +12,8 @@
 // 131072 keys, where no worker has more than some twenty tiles and the start and the join count, 27.6 us.
 // A unit of 16 rows and one tile takes a worker 4.2 us, of 8 rows 3.0: four warps at a third of their issue slots, two workers an SM.
 #pragma once
+#include <type_traits>
+
 #include "attention_common.cuh"
 
 namespace gdn {
@@ -109,6 +111,22 @@ __device__ __forceinline__ uint32_t transposed(uint32_t x) {
   uint32_t y;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
   return y;
+}
+
+// Two weights as two pairs of the values' type whose sums they are, to 2^-15 (bf16) or 2^-21 (f16) of each: rounded once, they lose up to
+// 2^-8 or 2^-11, as much as the output's own rounding.  A first part lies below its weight, so that the second is above zero, and an infinite
+// value that meets both stays what it is.
+template <bool F16>
+__device__ __forceinline__ void split2(float a, float b, uint32_t& first, uint32_t& second) {
+  const uint32_t below_a = max(__float_as_uint(a), 1u) - 1u, below_b = max(__float_as_uint(b), 1u) - 1u;   // (0 stays 0)
+  if constexpr (F16) {
+    asm("cvt.rz.f16x2.f32 %0, %1, %2;" : "=r"(first) : "f"(__uint_as_float(below_b)), "f"(__uint_as_float(below_a)));
+    const float2 x = unpack16<true>(first);
+    second = pack16x2<true>(fmaxf(a - x.x, fminf(a, 0x1p-24f)), fmaxf(b - x.y, fminf(b, 0x1p-24f)));   // f16's smallest
+  } else {
+    first = __byte_perm(below_a, below_b, 0x7632);   // the upper halves
+    second = pack16x2<false>(a - __uint_as_float(below_a & 0xffff0000u), b - __uint_as_float(below_b & 0xffff0000u));
+  }
 }
 
 // 16 bytes to shared memory, zeros where there is nothing to copy.
@@ -255,8 +273,8 @@ __device__ __forceinline__ Place place_in(uint32_t n, uint32_t at, uint32_t tile
 
 // A worker for units of up to 8 kEights rows: `tid` below kThreads, the tiles counted by just these threads, ring and barriers of its own
 // (initialised here), its number (blocks_aside in a row have the same share), how many shares there are.  `id`: a
-// barrier of its own.
-template <bool F16, int kEights>
+// barrier of its own.  kBeside: a prefix on the tensor cores adds to the same outputs.
+template <bool F16, int kEights, bool kBeside>
 __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* smem, int tid, const Count& counted, int worker, int share_count, int id) {
   Bars& bar = bars_of(smem);
   const int lane = tid & 31, warp = tid >> 5, subs = p.H_k * p.block_groups;
@@ -480,18 +498,35 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
 #pragma unroll
           for (int j = 0; j < kAhead; ++j) load_values(j, f[j]);
         }
-        uint32_t b[kEights][2];
+        // Weights go into the sums as two parts (split2) where one block of rows reads the keys: HBM bounds that, and it costs
+        // little (256 sequences of 8192 keys and 8 rows 638 us with and without, 128 of 4096 keys and 16 rows 173 us instead of 172, one tile 8.4
+        // instead of 8.3).  Where several blocks read them, the products bound the kernel, and weights are rounded once: 64 sequences of 1500 keys and 64
+        // rows take 84 us instead of 97, and outputs are 1.35 times as far off as with a rounding of the output alone.  So they are beside a
+        // prefix on the tensor cores, whose weights are rounded once, too (48 sequences of 16 rows and 2000 keys behind 16384: 50 us instead of 54).
+        const auto add = [&](auto of) {
+          constexpr int kParts = decltype(of)::value;
+          uint32_t b[kEights][2][2];
 #pragma unroll
-        for (int g = 0; g < kEights; ++g) {
-          b[g][0] = transposed(pack16x2<F16>(w[g][0], w[g][1]));
-          b[g][1] = transposed(pack16x2<F16>(w[g][2], w[g][3]));
-        }
+          for (int g = 0; g < kEights; ++g)
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          if (j + kAhead < 8) load_values(j + kAhead, f[(j + kAhead) % (kAhead + 1)]);
+            for (int e = 0; e < 2; ++e) {
+              uint32_t part[2];
+              if constexpr (kParts == 2) split2<F16>(w[g][2 * e], w[g][2 * e + 1], part[0], part[1]);
+              else part[0] = pack16x2<F16>(w[g][2 * e], w[g][2 * e + 1]);
 #pragma unroll
-          for (int g = 0; g < kEights; ++g) mma16<F16>(o[g][j], f[j % (kAhead + 1)], b[g][0], b[g][1]);
-        }
+              for (int n = 0; n < kParts; ++n) b[g][n][e] = transposed(part[n]);
+            }
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            if (j + kAhead < 8) load_values(j + kAhead, f[(j + kAhead) % (kAhead + 1)]);
+#pragma unroll
+            for (int g = 0; g < kEights; ++g)
+#pragma unroll
+              for (int n = 0; n < kParts; ++n) mma16<F16>(o[g][j], f[j % (kAhead + 1)], b[g][n][0], b[g][n][1]);
+          }
+        };
+        if (!kBeside && (kEights == 1 || p.blocks == 1)) add(std::integral_constant<int, 2>{});
+        else add(std::integral_constant<int, 1>{});
       }
       if (i + 1 == tiles) break;
       __syncwarp();
