@@ -57,9 +57,18 @@ __global__ void __launch_bounds__(own::kThreads, kResident) gdn_attention_kernel
 }
 
 // SMs out of `sms` for the own pages beside a prefix of many rows, by what the two take an SM: 0.34 us for a tile's cost of 16 rows (two
-// workers side by side), 0.32 of 8, 1.4 us for 128 keys of 256 rows.  (256 sequences of 8 rows and 512 keys behind 32768: 125 us, 128 to
-// 129 with 0.35 to 0.37, 136 with 0.29; 64 of 16 rows and 1500 keys behind 30000: 153 us, 157 to 162 with 0.38 to 0.41, 160 with 0.31.)  A prefix of up to 128 rows is held by HBM, too, and loses little by an SM
-// less, while the own pages get on more slowly beside it.
+// workers side by side), 0.32 of 8, 1.4 us for 128 keys of 256 rows.  us with 0.25, 0.29, 0.32, 0.34, 0.37 and 0.42:
+//   256 sequences of 8 rows a key head and 512 keys behind 32768    129 134 123 125 125 132
+//   100 of 7 rows, 300 keys, behind 20000                           42 41 40 40 40 42
+//   300 of 8 rows, 100 keys, one key head, behind 50000             60 58 55 55 56 57
+//   200 of 2 rows, 1000 keys, 8 key heads, behind 10000             148 147 150 151 151 154
+//   64 of 16 rows, 1500 keys, behind 30000                          87 80 76 76 71 71
+// A prefix of up to 128 rows is held by HBM, too, and loses little by an SM less, while the own pages get on more slowly beside it: 0.9 there.
+// us with 0.34, 0.5, 0.7, 0.9, 1.2 and 1.6:
+//   64 rows, 300 own keys, behind 100000     48 46 46 46 46 46       64 rows, 3000 own keys     54 51 52 52 53 54
+//   128 rows, 500, behind 65536              45 43 43 43 43 43       128 rows on two key heads  28 24 23 23 23 23
+//   160 rows, 500, behind 65536              45 45 45 45 46 46       256 rows                   48 49 49 49 51 53
+//   512 rows, 500, behind 32768              42 46 48 50 55 62
 template <int kEights>
 __device__ __forceinline__ int sms_for_own(uint32_t own_cost, int aside, uint32_t prefix_cost, bool few_rows, int sms) {
   if (own_cost == 0) return 0;
@@ -241,7 +250,11 @@ cudaError_t launch(const AttentionParams& p, cudaStream_t stream) {
   else if (most) e = launch_behind(gdn_attention_kernel<F16, kEights>, std::min<int64_t>(p.workers, most), own::kThreads, own::kBytes, stream, p);
   if (e != cudaSuccess) return e;
   // Warps a row by the parts that a row has about, as long as the rows' CTAs find a place all at once (three of eight warps or one of 32
-  // an SM); after that rows keep the SMs busy with a warp each.
+  // an SM); after that rows keep the SMs busy with a warp each.  us of a call with 32 warps, 8 warps, a warp by sixes and by eights:
+  //   153 parts, 16 rows      27 28 46 47      184 parts, 160 rows     27 29 90 64      31 parts, 160 rows      19 17 24 23
+  //   77 parts, 64 rows       26 27 37 36      49 parts, 256 rows      48 47 58 52      10 parts, 512 rows      109.5 105.4 106.3 105.6
+  //   192 parts, 128 rows     20 26 87 57      45 parts, 448 rows      53 48 59 54      5 parts, 512 rows       51 47 45 46
+  //   39 parts, 32 rows       86 87 91 90      43 parts, 640 rows      61 53 62 56      3 parts, 1332 rows      37 26 24 23
   const int64_t prefix_tiles = ((int64_t)p.prefix + kPrefixKeys - 1) / kPrefixKeys, sms = p.workers / kResident;
   int64_t parts = 1 + p.workers / (own_units + p.H_k * p.prefix_blocks);
   if (many) parts += 1 + std::min<int64_t>(prefix_tiles - 1, p.prefix_workers / ((int64_t)p.H_k * p.prefix_units));

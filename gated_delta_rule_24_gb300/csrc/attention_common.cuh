@@ -9,7 +9,12 @@
 namespace gdn {
 
 constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
-constexpr float kRoom = 8.f;  // how far (powers of two) scores may exceed the base before it moves
+// A base moves when a score exceeds the one that it was set by, the largest then, by more than kRoom powers of two.  Bases of f16 weights
+// are set kBias below that score, so that weights down to 2^-20 of the largest stay in f16's normal range: a weight is
+// 2^8 at most in bf16 and 2^14 in f16, whose numbers end below 2^16.
+constexpr float kRoom = 8.f;
+template <bool F16> constexpr float kBias = F16 ? 6.f : 0.f;
+static_assert(kRoom + kBias<true> < 15.f, "weights stay finite in f16");
 
 __device__ __forceinline__ float exp2_fast(float x) {
   float y;

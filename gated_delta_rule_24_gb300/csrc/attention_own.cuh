@@ -1,12 +1,12 @@
 // The own pages of the sequences in the attention over a paged cache: what a worker does with its share
 // (attention.cu says what workers, units and shares are).
 //
-// Each key and value is read once for up to 16 rows, 2 x 16 flops a byte at most: the kernel is bound by
+// Each key and value is read once for up to 16 rows, 16 flops a byte at most (4 x 128 a row for 512 bytes): the kernel is bound by
 // HBM bandwidth as long as copies are always under way.  A warp of its own looks up pages and issues the tensor
 // copies (boxes of up to 64 places of a page) into a ring of three tiles, over the ends of units; with a unit's first
 // tile come its queries.  Four warps take 16 of a tile's keys each: scores (keys x rows) and sums (values x rows) by warp
 // products with eight rows, or two times eight, as the narrow side, so that few rows take few products and registers; weights
-// are passed on in registers.  The warps meet at the end of a unit only, over the memory of its last tile.
+// are passed on in registers, in two parts of the values' type where that costs nothing.  The warps meet at the end of a unit only, over the memory of its last tile.
 //
 // Measured: 256 sequences of up to 8192 keys, 4.3 GB of pages in 634 us, 6.8 TB/s and as much as a copy; one sequence of
 // 131072 keys, where no worker has more than some twenty tiles and the start and the join count, 27.6 us.
@@ -330,7 +330,6 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
 
   // All four warps walk the same units whatever happens on the way, so that they meet at the same ends.  (Lengths that someone changes
   // meanwhile could part them; the wait at an end has its limit, too.)
-  constexpr float kBias = F16 ? 6.f : 0.f;  // f16 weights are kept 2^6 above their normal range's end for longer
   const int mi = lane >> 3, mj = lane & 7;
   // a warp's 16 rows in a tile of boxes: where they begin, how far the second eight and the second half of a row are
   const auto rows_of = [](int w, int box) { return (w * kWarpKeys & -box) * 256 + (w * kWarpKeys & (box - 1)) * 128; };
@@ -416,7 +415,7 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
 #pragma unroll
         for (int g = 0; g < kEights; ++g)
 #pragma unroll
-          for (int e = 0; e < 2; ++e) moves |= fmaxf(w[g][e], w[g][e + 2]) > base[g][e] + (kRoom + kBias);
+          for (int e = 0; e < 2; ++e) moves |= fmaxf(w[g][e], w[g][e + 2]) > base[g][e] + (kRoom + kBias<F16>);
         if (__any_sync(0xffffffffu, moves)) {
 #pragma unroll
           for (int g = 0; g < kEights; ++g)
@@ -425,7 +424,7 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
               float top = fmaxf(w[g][e], w[g][e + 2]);
 #pragma unroll
               for (int d = 4; d < 32; d <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, d));
-              const float now = fmaxf(base[g][e], top - kBias);
+              const float now = fmaxf(base[g][e], top - kBias<F16>);
               const float keep = now == -INFINITY || now == base[g][e] ? 1.f : exp2_fast(base[g][e] - now);
               base[g][e] = now;
               sum[g][e] *= keep;

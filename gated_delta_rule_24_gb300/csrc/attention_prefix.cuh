@@ -14,9 +14,13 @@
 //
 // and while four warps make A's weights, the tensor cores are at B's products, and the other way round.
 // (P comes in two halves, and the first goes into the product while the second is made.)  A
-// base moves only when a score exceeds it by 2^8, so that O is seldom read back to be scaled: the weights
-// grow to 2^8 at most, which changes no rounding.  When S of a tile is there, all products issued before it
+// base moves only when a score exceeds the largest before it by 2^8, so that O is seldom read back to be scaled: the weights
+// grow to 2^8 at most (2^14 in f16, attention_common.cuh), which changes no rounding.  When S of a tile is there, all products issued before it
 // are done, so a row's thread may scale O then without a hand-off of its own.
+//
+// P is rounded once to the values' type, as the product wants both operands of one type; the sum of weights is of what they were before, in
+// f32.  That costs outputs up to u sum w |v| (2.2e-3 of the output instead of 1.65e-3 in bf16, its own rounding included).  A second
+// product with the rest would take the tensor cores 1030 clocks more for each 128 keys of 256 rows, beside the 2048 of the others.
 //
 // Where a unit has no more than 128 rows, A and B are the same rows and take every other tile of keys, and their sums come
 // together at the end of a piece.
@@ -26,7 +30,7 @@
 //
 // Measured: 128 keys of 256 rows take an SM 2700 to 2870 clocks (1.4 us) of the 2048 that the products alone need: a row's weights take 1570
 // from its scores, and the products of a tile 1310 then, 1030 where nothing else uses TMEM and shared memory.  256 sequences of 8 rows over 32768 shared keys on 4 key heads,
-// each with some own pages: 125 us in all.
+// each with some own pages: 123 us in all in a graph, up to 133 as a call among others.
 #pragma once
 #include <type_traits>
 
@@ -285,7 +289,6 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
     const uint32_t lanes = (uint32_t)(warp & 3) << 21;
     const uint32_t s_at = tmem + kS + 128 * x + lanes, o_at = tmem + kO + 128 * x + lanes;
     const float c = fabsf(p.scale) * kLog2e;
-    constexpr float kBias = F16 ? 6.f : 0.f;
     bool dead = false;
     uint32_t steps = 0, pieces = 0, first = 0;   // `first`: the piece's first step
     auto wait = [&](uint64_t* b, uint32_t parity) {
@@ -359,8 +362,8 @@ __device__ __forceinline__ void run_worker(const AttentionParams& p, uint8_t* sm
           if (dead) continue;
         }
         const float high = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3])) * c;
-        if (__any_sync(0xffffffffu, high > base + (kRoom + kBias))) {
-          const float now = fmaxf(base, high - kBias);
+        if (__any_sync(0xffffffffu, high > base + (kRoom + kBias<F16>))) {
+          const float now = fmaxf(base, high - kBias<F16>);
           const float keep = now == -INFINITY || now == base ? 1.f : exp2_fast(base - now);
           base = now;
           sum = mul2(sum, pair(keep));
