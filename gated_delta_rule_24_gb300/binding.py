@@ -11,6 +11,7 @@ import contextlib
 import ctypes
 import importlib.machinery
 import importlib.util
+import operator
 import os
 from typing import Optional
 
@@ -198,7 +199,7 @@ class _ByCtypes:
 
     def paged_attention_step(self, q, k_cache, v_cache, page_table, lengths, scale, prefix_pages, prefix_length, output, lse, stream):
         return self._lib.gdn_paged_attention_step(*_described(q, k_cache, v_cache, page_table, lengths), scale + 0.0,
-                                                  *_described(prefix_pages), prefix_length, *_described(output, lse), stream)
+                                                  *_described(prefix_pages), _int64(prefix_length), *_described(output, lse), stream)
 
     def new_qk_norm_rope(self, q, k, q_weight, k_weight, weight_offset, eps, cos_sin, positions, pair_axes, interleaved):
         made = torch.empty_like(q), None if k is None else torch.empty_like(k)
@@ -222,6 +223,14 @@ class _ByCtypes:
         status = self.paged_attention_step(q, k_cache, v_cache, page_table, lengths, scale, prefix_pages, prefix_length, made, lse,
                                            _stream_handle(None))
         return status or ((made, lse) if with_lse else made)
+
+
+def _int64(x):
+    """``x`` as C takes it: ctypes by itself drops the bits that do not fit."""
+    x = operator.index(x)
+    if not -1 << 63 <= x < 1 << 63:
+        raise OverflowError(f"{x} is no integer of 64 bits")
+    return x
 
 
 def _axes(pair_axes):
