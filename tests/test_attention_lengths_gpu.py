@@ -57,3 +57,32 @@ def test_only_the_bad_ones(kw, prefix):
         A.check(got, ref, rows=[i for i in range(600 * t) if i // t != at])
         rows = slice(at * t, at * t + t)
         assert bool((got[0][rows] == 9.0).all()) and bool((got[1][rows] == 9.0).all())
+
+
+@pytest.mark.parametrize("rows,prefix", [(3, 0), (3, 40), (40, 40)], ids=["own", "walk", "tensor_cores"])
+def test_a_cache_without_pages(rows, prefix):
+    """Every page index is none then: reported, and the rows that need one are left."""
+    b = A.Batch([5] * rows, prefix=prefix, h_q=16, h_k=2, seed=72)
+    b.k_cache, b.v_cache = b.k_cache[:0], b.v_cache[:0]
+    lengths = b.lengths.clone()
+    lengths[0] = 0
+    out, lse = run(b, b.table, lengths, prefix)
+    assert gdn.device_status() == 0x20
+    assert bool((out[1:] == 9.0).all()) and bool((lse[1:] == 9.0).all())
+    assert bool((out[0] == (9.0 if prefix else 0.0)).all())
+
+
+def test_a_hundred_thousand_sequences():
+    """More than a thread counts at once, most of them empty."""
+    n = 100_000
+    lengths = torch.zeros(n, dtype=torch.int32, device="cuda")
+    at = torch.randperm(n, generator=torch.Generator().manual_seed(73))[:3000].cuda()
+    lengths[at] = torch.randint(1, 17, (3000,), generator=torch.Generator().manual_seed(74)).to(torch.int32).cuda()
+    b = A.Batch([16] * 50, h_q=2, h_k=1, page=8, seed=75)
+    table = b.table[torch.arange(n, device="cuda") % 50].contiguous()
+    q = A.normal(n, 2, 128, seed=76)
+    out, lse = gdn.paged_attention_step(q, b.k_cache, b.v_cache, table, lengths, return_lse=True)
+    empty = lengths == 0
+    assert not bool(out[empty].any()) and bool((lse[empty] == -float("inf")).all())
+    keys = [tuple(x[:int(lengths[i])] for x in b.keys[int(i) % 50]) for i in at]
+    A.check((out[at], lse[at]), A.attend(q[at], keys, tuple(x[:0] for x in b.shared), 1))
