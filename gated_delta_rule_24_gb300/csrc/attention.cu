@@ -15,7 +15,7 @@
 // HBM busy: one kernel then shares the SMs out between the two kinds of workers, as the lengths on the
 // device ask for.
 //
-// Measured as one call in a graph: 511 keys of one sequence 8.3 us, which is two kernels' start and the way of one tile; the rest
+// Measured as one call in a graph: 511 keys of one sequence 8.4 us, which is two kernels' start and the way of one tile; the rest
 // stands with the two kinds of workers.
 #include "attention_own.cuh"
 #include "attention_prefix.cuh"

@@ -27,11 +27,13 @@
  *  - Errors: every entry point returns a gdn_status_t.  On any error detected on
  *    the host nothing is launched and nothing is written.  gdn_last_error()
  *    returns a message describing the most recent error of the calling thread.
- *  - Inputs the host cannot see (the contents of cu_seqlens and state_indices)
- *    are checked on the device: a sequence with a negative, decreasing or
- *    out-of-range bound, or a state index outside the pool, is skipped (its
- *    output rows and state slot are not written) and a device error word is
- *    set; read it with gdn_get_device_status().  No kernel traps.
+ *  - Inputs the host cannot see (the contents of cu_seqlens, state_indices,
+ *    positions, slots, page tables and lengths) are checked on the device: a
+ *    sequence with a negative, decreasing or out-of-range bound, or a state index
+ *    outside the pool, is skipped (its output rows and state slot are not written)
+ *    and a device error word is set; read it with gdn_get_device_status().  What a
+ *    bad position, slot, page or length leaves unwritten stands with its entry
+ *    point.  No kernel traps.
  */
 #ifndef GDN_H
 #define GDN_H
@@ -310,7 +312,8 @@ gdn_status_t gdn_qk_norm_rope(const gdn_tensor_t* q, const gdn_tensor_t* k, cons
  * Arguments, layouts, defaults and errors are those of gdn_qk_norm_rope, but
  *  cos_sin        required.
  *  positions      required.  [A, T] i32 or i64, A from 1 to 4, each row contiguous.  Every
- *                 position of a token has to be on the table, or its output rows are left unwritten.
+ *                 position of a token has to be on the table, also on an axis that turns no pair, or its output
+ *                 rows are left unwritten.
  *  pair_axes      required, in HOST memory, read during the call: num_pairs = R / 2 entries, the axis (0 to A - 1) that
  *                 turns pair i.
  */
@@ -343,7 +346,8 @@ gdn_status_t gdn_qk_norm_rope_axes(const gdn_tensor_t* q, const gdn_tensor_t* k,
  *  v_cache        [pages, page_size, H_k, 128] of q's dtype, innermost contiguous, 16-byte
  *                 aligned, the other strides multiples of 8 elements in any order (heads of a page
  *                 one behind the other, both caches in one buffer); written in place.  Neither
- *                 overlaps another argument.
+ *                 overlaps another argument.  Any page_size; gdn_paged_attention_step reads caches whose
+ *                 page_size is a multiple of 8.
  * A token with a position outside the table sets GDN_DEVERR_POSITION; its row of q_out and its
  * places in the caches are left unwritten.  Asynchronous on `stream`; no workspace.
  */
@@ -364,7 +368,10 @@ gdn_status_t gdn_norm_rope_append(const gdn_tensor_t* q, const gdn_tensor_t* k, 
  *
  * over all keys j of the prefix and the first lengths[n] - tokens + i + 1 keys of the sequence's own
  * pages (the new tokens' keys are there already).  A row without any key, or whose scores are all -infinity,
- * gives zeros and an lse of -infinity.  An infinity or NaN in a key or value reaches the rows that see it, no others.
+ * gives zeros and an lse of -infinity.  An infinity or NaN in a key or value reaches the rows that see it, no others (a score of
+ * +infinity or NaN makes the row and its lse NaN, one of -infinity has a weight of zero).  Weights are made and summed in f32; for the products with
+ * the values they keep some 15 (bf16) or 21 (f16) bits where tokens * H_q / H_k <= 16 and there is no prefix, or one that
+ * T * H_q / H_k <= 16 rows share; else they are rounded to q's dtype.
  *
  *  q              [T, H_q, 128] bf16 or f16 (stride rules of gdn_chunk_prefill's q), T = N * tokens,
  *                 tokens from 1 to 16.
